@@ -19,10 +19,21 @@ Entry points (same names as the C ABI):
   fa_decode_splitkv_gqa(q, k, v, splits, scale=None, workspace=None, merge_order=None, with_lse=False)
   fa_bwd(q, k, v, o, dout, lse, scale=None, causal=False, workspace=None) -> (dq, dk, dv)
   fa_bwd_workspace_bytes(B, H, Nq, d)
+  fa_rope_freqs(rot, theta=10000.0) -> float64 frequencies
+  fa_rope(q, k, positions, freqs, axes=None, interleaved=False) -> (q_out, k_out)
+  fa_rope_bwd(dq, dk, positions, freqs, axes=None, interleaved=False) -> (dq_in, dk_in)
+  fa_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, freqs=None, axes=None,
+                  interleaved=False) -> q_out or None
+  fa_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale=None, workspace=None, with_lse=False)
+      -> (o, lse)
+  fa_decode_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None,
+                         workspace=None, with_lse=False) -> (o, lse)
+  fa_decode_paged_workspace_bytes(B, H, Hkv, d, prefix_len=0)
   fa_check_device_error()
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -83,6 +94,18 @@ def lib() -> ctypes.CDLL:
             L.fa_bwd.restype = i
             L.fa_bwd_workspace_bytes.argtypes = [i, i, i, i]
             L.fa_bwd_workspace_bytes.restype = sz
+            ll = ctypes.c_longlong
+            L.fa_rope.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, i, vp, vp, i, i, i, i, vp]
+            L.fa_rope.restype = i
+            L.fa_paged_append.argtypes = [vp] * 9 + [i] * 6 + [vp, vp, vp, i, i, i, vp]
+            L.fa_paged_append.restype = i
+            L.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, ll, vp, i, i, i, i, i, i, i, vp, f, vp, sz, vp, vp]
+            L.fa_decode_paged.restype = i
+            L.fa_decode_paged_prefix.argtypes = [vp, vp, vp, vp, vp, i, vp, ll, vp, i, i, i, i, i, i, i, vp, f, vp, sz,
+                                                 vp, vp]
+            L.fa_decode_paged_prefix.restype = i
+            L.fa_decode_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+            L.fa_decode_paged_workspace_bytes.restype = sz
             L.fa_check_device_error.argtypes = []
             L.fa_check_device_error.restype = i
             L.fa_status_string.argtypes = [i]
@@ -398,6 +421,265 @@ def fa_decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             _stream_handle(stream))
     _check(st, "fa_decode_splitkv_noalloc")
     return o
+
+
+def _need_cuda(**tensors) -> None:
+    dev = None
+    for n, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{n} is on {t.device}, not on the current device cuda:{dev}")
+
+
+def _strides(t: torch.Tensor) -> list[int]:
+    """The strides of all dimensions but the last; 0 for those of one entry, whose stride says nothing."""
+    return [s if n != 1 else 0 for s, n in zip(t.stride()[:-1], t.shape)]
+
+
+def _on_stream(stream, *tensors):
+    """A context in which outputs and workspaces are allocated for `stream`.  Tensors used on a stream other than
+    the current one are recorded there, so that the allocator does not hand their memory on while it is read."""
+    if stream is None or stream == torch.cuda.current_stream():
+        return contextlib.nullcontext()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _last_contig(name: str, t: torch.Tensor) -> None:
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def fa_rope_freqs(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The usual frequencies theta^(-2i/rot), i < rot/2, as the float64 tensor that fa_rope and fa_paged_append take."""
+    return theta ** (torch.arange(0, rot, 2, dtype=torch.float64, device=device) / -rot)
+
+
+def _rotation(positions, freqs, axes):
+    _need_cuda(positions=positions, freqs=freqs, axes=axes)
+    if positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32")
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 vector (radians per position)")
+    if axes is not None and (axes.dtype != torch.int32 or axes.shape != freqs.shape or not axes.is_contiguous()):
+        raise ValueError("axes must be contiguous int32, one entry a frequency")
+
+
+def _rope(q, k, positions, freqs, axes, interleaved, q_out, k_out, inverse, stream, where):
+    _need_cuda(q=q, k=k, q_out=q_out, k_out=k_out)
+    _rotation(positions, freqs, axes)
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
+        raise ValueError("q [B,H,N,d], k [B,Hkv,N,d] expected")
+    if k is not None and k.dtype != q.dtype:
+        raise TypeError("q and k must share a dtype")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    B, H, N, d = q.shape
+    if positions.dim() == 1:  # [N]: one axis, the same for every batch entry
+        want, n_axes, shared = (N,), 1, 1
+    elif positions.dim() == 2:  # [B, N]: one axis
+        want, n_axes, shared = (B, N), 1, 0
+    else:  # [axes, B, N] or, the same for every batch entry, [axes, 1, N]
+        n_axes = positions.shape[0]
+        shared = int(positions.dim() == 3 and positions.shape[1] == 1 and B > 1)
+        want = (n_axes, 1 if shared else B, N)
+    if tuple(positions.shape) != want:
+        raise ValueError("positions [N], [B,N], [axes,B,N] or [axes,1,N] expected")
+    code = _dtype_code(q)
+    with _on_stream(stream, q, k, q_out, k_out, positions, freqs, axes):
+        if q_out is None:
+            q_out = torch.empty((B, H, N, d), device=q.device, dtype=q.dtype)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, device=k.device, dtype=k.dtype)
+    strides = []
+    for n, t, like in (("q", q, q), ("k", k, k), ("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is None:
+            strides += [0, 0, 0]
+            continue
+        _last_contig(n, t)
+        if t.shape != like.shape or t.dtype != like.dtype:
+            raise ValueError(f"{n} must match its input")
+        strides += _strides(t)
+    st = lib().fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), (ctypes.c_longlong * 12)(*strides), B, H,
+                       0 if k is None else k.shape[1], N, d, code, positions.data_ptr(), shared, freqs.data_ptr(),
+                       _ptr(axes), n_axes, 2 * freqs.shape[0], int(bool(interleaved)), inverse, _stream_handle(stream))
+    _check(st, where)
+    return q_out, k_out
+
+
+def fa_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freqs: torch.Tensor,
+            axes: torch.Tensor | None = None, interleaved: bool = False, q_out: torch.Tensor | None = None,
+            k_out: torch.Tensor | None = None, stream=None):
+    """Rotary positions on q [B, H, N, d] and k [B, Hkv, N, d] (or None), bf16 or fp32; returns (q_out, k_out).
+
+    positions: int32 [N], [B, N], or with several axes [axes, B, N] / [axes, 1, N].  freqs: float64 [rot/2], radians
+    per position (fa_rope_freqs); the first rot elements of a head are rotated.  axes: int32 [rot/2], the position
+    axis of each pair.  q and k may be strided views (heads of a projection's output); new outputs are contiguous.
+    An output may be its input itself; otherwise it must overlap no input.
+    """
+    return _rope(q, k, positions, freqs, axes, interleaved, q_out, k_out, 0, stream, "fa_rope")
+
+
+def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor, freqs: torch.Tensor,
+                axes: torch.Tensor | None = None, interleaved: bool = False, dq_in: torch.Tensor | None = None,
+                dk_in: torch.Tensor | None = None, stream=None):
+    """The backward pass of fa_rope: gradients of its outputs in, gradients (dq_in, dk_in) of its q and k out."""
+    return _rope(dq, dk, positions, freqs, axes, interleaved, dq_in, dk_in, 1, stream, "fa_rope (backward)")
+
+
+def _cache_shape(k_cache, v_cache):
+    _need_cuda(k_cache=k_cache, v_cache=v_cache)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache/v_cache [num_pages,Hkv,page_size,d] expected")
+    if not (k_cache.dtype == v_cache.dtype == torch.bfloat16):
+        raise TypeError("the cache is bf16")
+    strides = _strides(k_cache)
+    if strides != _strides(v_cache):
+        raise ValueError("k_cache and v_cache must have the same strides")
+    _last_contig("k_cache", k_cache)
+    _last_contig("v_cache", v_cache)
+    return (*k_cache.shape, (ctypes.c_longlong * 3)(*strides))
+
+
+def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    slots: torch.Tensor, q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                    freqs: torch.Tensor | None = None, axes: torch.Tensor | None = None, interleaved: bool = False,
+                    q_out: torch.Tensor | None = None, stream=None):
+    """Writes new tokens' k, v [T, Hkv, d] to their slots of a paged cache; returns the tokens' queries (or None).
+
+    k_cache, v_cache: bf16 [num_pages, Hkv, page_size, d] (strided views with d contiguous allowed, the same strides
+    for both).  slots: int64 [T], page * page_size + row; a negative slot stores nothing.  positions (int32 [T] or
+    [axes, T]) with freqs rotate k and q as fa_rope does; without them both are copied.  q [T, H, d] may be strided.
+    """
+    _need_cuda(k=k, v=v, q=q, q_out=q_out, slots=slots)
+    P, Hkv, ps, d, cs = _cache_shape(k_cache, v_cache)
+    if k.dim() != 3 or k.shape != v.shape or tuple(k.shape[1:]) != (Hkv, d):
+        raise ValueError("k/v [T,Hkv,d] of the cache's Hkv and d expected")
+    T = k.shape[0]
+    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d):
+        raise ValueError("q [T,H,d] expected")
+    if not (k.dtype == v.dtype == torch.bfloat16) or (q is not None and q.dtype != torch.bfloat16):
+        raise TypeError("k, v and q are bf16")
+    if slots.dtype != torch.int64 or tuple(slots.shape) != (T,) or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int64 [T]")
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs go together")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    n_axes, rot = 1, 0
+    if positions is not None:
+        _rotation(positions, freqs, axes)
+        n_axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if tuple(positions.shape) not in ((T,), (n_axes, T)):
+            raise ValueError("positions [T] or [axes,T] expected")
+        rot = 2 * freqs.shape[0]
+    for n, t in (("k", k), ("v", v), ("q", q)):
+        if t is not None:
+            _last_contig(n, t)
+    with _on_stream(stream, k, v, q, q_out, slots, positions, freqs, axes, k_cache, v_cache):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, device=q.device, dtype=q.dtype)
+    if q is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous()):
+        raise ValueError("q_out must be contiguous and match q")
+    strides = _strides(k) + _strides(v) + (_strides(q) if q is not None else [0, 0])
+    if T == 0:
+        return q_out
+    st = lib().fa_paged_append(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(),
+                               v_cache.data_ptr(), (ctypes.c_longlong * 6)(*strides), cs, slots.data_ptr(), T,
+                               0 if q is None else q.shape[1], Hkv, d, P, ps, _ptr(positions), _ptr(freqs), _ptr(axes),
+                               n_axes, rot, int(bool(interleaved)), _stream_handle(stream))
+    _check(st, "fa_paged_append")
+    return q_out
+
+
+def fa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int, prefix_len: int = 0) -> int:
+    return int(lib().fa_decode_paged_workspace_bytes(B, H, Hkv, d, int(prefix_len)))
+
+
+def _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale, workspace, with_lse, o,
+                  stream, where):
+    _need_cuda(q=q, o=o, prefix_pages=prefix_pages, page_table=page_table, seq_lens=seq_lens,
+               workspace=workspace)
+    P, Hkv, ps, d, cs = _cache_shape(k_cache, v_cache)
+    if q.dim() not in (3, 4) or q.shape[-1] != d or (q.dim() == 4 and q.shape[2] != 1) or not q.is_contiguous():
+        raise ValueError("contiguous q [B,H,d] or [B,H,1,d] expected")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("decode takes bf16 q, k, v")
+    B, H = q.shape[:2]
+    if H % Hkv != 0:
+        raise ValueError("query heads must be a multiple of key/value heads")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    max_pages = page_table.shape[1]
+    if max_pages < 1:
+        raise ValueError("page_table must have a column")
+    if page_table.stride(1) != 1 and max_pages > 1:
+        raise ValueError("page_table's rows must be contiguous")
+    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32 [B]")
+    if prefix_len:
+        if prefix_pages is None or prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1 \
+                or not prefix_pages.is_contiguous() or prefix_pages.shape[0] * ps < prefix_len:
+            raise ValueError("prefix_pages must be contiguous int32 and hold the prefix")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    L = lib()
+    with _on_stream(stream, q, k_cache, v_cache, prefix_pages, page_table, seq_lens, o, workspace):
+        if o is None:
+            o = torch.empty((B, H, d), device=q.device, dtype=torch.bfloat16)
+        lse = torch.empty((B, H), device=q.device, dtype=torch.float32) if with_lse else None
+        if workspace is None:
+            need = L.fa_decode_paged_workspace_bytes(B, H, Hkv, d, prefix_len)
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    if o.dtype != torch.bfloat16 or o.numel() != B * H * d or not o.is_contiguous():
+        raise ValueError("o must be contiguous bf16 [B,H,d]")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = L.fa_decode_paged_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                                  _ptr(prefix_pages) if prefix_len else None, prefix_len, page_table.data_ptr(),
+                                  max(page_table.stride(0), max_pages) if B == 1 else page_table.stride(0),
+                                  seq_lens.data_ptr(), B, H, Hkv, d, P, ps, max_pages, cs, float(scale),
+                                  _ptr(workspace), ws_bytes, _ptr(lse), _stream_handle(stream))
+    _check(st, where)
+    return o, lse
+
+
+def fa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    seq_lens: torch.Tensor, scale: float | None = None, workspace: torch.Tensor | None = None,
+                    with_lse: bool = False, o: torch.Tensor | None = None, stream=None):
+    """One query per head over a paged cache; returns (o [B, H, d], lse [B, H] or None).
+
+    q: bf16 [B, H, d].  k_cache, v_cache as in fa_paged_append.  page_table: int32 [B, max_pages]; sequence b sees its
+    first seq_lens[b] (int32, on the device) rows.  A sequence without keys gets o = 0, lse = -inf; one with a bad
+    page or length gets NaN and makes fa_check_device_error return FA_ERR_INVALID_ARG.
+    """
+    return _decode_paged(q, k_cache, v_cache, None, 0, page_table, seq_lens, scale, workspace, with_lse, o, stream,
+                         "fa_decode_paged")
+
+
+def fa_decode_paged_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           prefix_pages: torch.Tensor | None, prefix_len: int, page_table: torch.Tensor,
+                           seq_lens: torch.Tensor, scale: float | None = None, workspace: torch.Tensor | None = None,
+                           with_lse: bool = False, o: torch.Tensor | None = None, stream=None):
+    """fa_decode_paged for sequences that all begin with the prefix_len keys in prefix_pages (int32), read once.
+
+    page_table and seq_lens describe each sequence's own rows behind the prefix; a negative length marks an unused
+    place of a padded batch, which sees nothing.
+    """
+    return _decode_paged(q, k_cache, v_cache, prefix_pages, int(prefix_len), page_table, seq_lens, scale, workspace,
+                         with_lse, o, stream, "fa_decode_paged_prefix")
 
 
 def fa_check_device_error() -> int:

@@ -15,7 +15,7 @@
 
 namespace {
 
-__device__ int g_fa_err;  // device error word: 0, or DEV_TIMEOUT | wait site
+__device__ int g_fa_err;  // device error word: 0, DEV_TIMEOUT | wait site, or DEV_BAD_INDEX | site
 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
@@ -78,6 +78,13 @@ int current_device_status() {
   int* err = nullptr;
   return device_setup(&dev, &err);
 }
+
+int current_device_info(int** err, int* sms) {
+  int dev = 0;
+  return device_setup(&dev, err, sms);
+}
+
+int report_cuda_error(cudaError_t e) { return cuda_fail(e); }
 }  // namespace fa
 
 namespace {
@@ -839,7 +846,7 @@ int fa_check_device_error(void) {
   if (h != 0) {
     const int zero = 0;
     if ((ce = cudaMemcpyToSymbol(g_fa_err, &zero, sizeof(int))) != cudaSuccess) return cuda_fail(ce);
-    return FA_ERR_TIMEOUT;
+    return (h & 0x200) ? FA_ERR_INVALID_ARG : FA_ERR_TIMEOUT;  // DEV_BAD_INDEX (sm103_ptx.cuh), else a timeout
   }
   return FA_OK;
 }

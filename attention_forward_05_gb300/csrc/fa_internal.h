@@ -43,6 +43,83 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, int thread
 // call fails.  Allocates nothing.
 int current_device_status();
 
+// The same with what the launch code needs: the device's error word and SM count.
+int current_device_info(int** err, int* sms);
+
+// Records a CUDA error for fa_last_cuda_error() and returns FA_ERR_CUDA.
+int report_cuda_error(cudaError_t e);
+
+// Rotation of position pairs shared by fa_rope and fa_paged_append (fa_rope.cu).
+struct Rotary {
+  const double* freqs = nullptr;  // device [rot / 2], radians per position
+  const int* axes = nullptr;      // device [rot / 2], position axis of each pair; nullptr: axis 0
+  const int* pos = nullptr;       // device int32 positions: pos[axis * axis_stride + b * batch_stride + n]
+  long long axis_stride = 0, batch_stride = 0;
+  int n_axes = 1;
+  int rot = 0;                    // elements rotated at the start of a head: a multiple of 16, <= d; 0: none
+  int interleaved = 0;            // pairs (2i, 2i+1) instead of (i, i + rot/2)
+  int inverse = 0;                // rotate by the negative angle (the gradient's rotation)
+};
+
+// Element strides of one [B, heads, N, d] operand (d contiguous).
+struct RowStrides {
+  long long b, h, n;
+};
+
+struct RopeLaunch {
+  const void* q;
+  const void* k;        // nullptr with Hkv = 0
+  void* q_out;
+  void* k_out;
+  RowStrides sq, sk, sqo, sko;
+  int B, H, Hkv, N, d;
+  int bf16;
+  Rotary r;
+  int* err;
+  int sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_rope(const RopeLaunch& a);
+
+struct AppendLaunch {
+  const void* q;        // nullptr with H = 0
+  const void* k;
+  const void* v;
+  void* q_out;          // [T, H, d] contiguous
+  void* k_cache;
+  void* v_cache;
+  long long q_tok, q_head, k_tok, k_head, v_tok, v_head;  // element strides of the new tokens
+  long long c_page, c_head, c_row;                        // element strides of both caches
+  const long long* slots;                                 // device [T]
+  int T, H, Hkv, d, page_size;
+  long long n_slots;    // num_pages * page_size
+  Rotary r;
+  int* err;
+  int sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_append(const AppendLaunch& a);
+
+struct PagedLaunch {
+  const void* q;            // [B, H, d] bf16
+  const void* k_cache;
+  const void* v_cache;
+  void* o;                  // [B, H, d] bf16
+  float* lse;               // [B, H] or nullptr
+  long long c_page, c_head, c_row;  // element strides of both caches
+  const int* table;         // [B, max_pages], rows table_stride apart
+  const int* lens;          // [B]
+  const int* prefix_pages;  // [ceil(prefix_len / page_size)]
+  int B, H, Hkv, d, num_pages, page_size, max_pages;
+  long long table_stride;
+  int prefix_len;
+  float c;                  // scale * log2(e)
+  int* err;
+  int sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_decode_paged(const PagedLaunch& a);
+
 struct FwdLaunch {
   const CUtensorMap* tm_q;  // 3-D maps over [B*H, N, d] (innermost d), 128-byte swizzle
   const CUtensorMap* tm_k;

@@ -18,7 +18,11 @@ namespace fa {
 #endif
 
 // Device error codes written into the library's error word.
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 0x100 };
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 0x100, DEV_BAD_INDEX = 0x200 };
+
+// Records an index read from device memory (a page, slot, length or axis) that lies outside its range.
+// A timeout already recorded stays.
+__device__ __forceinline__ void record_bad_index(int* err, int where) { atomicCAS(err, 0, DEV_BAD_INDEX | where); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -1,7 +1,9 @@
 /*
  * fa.h -- C ABI of libfa: fused FlashAttention forward (plain, causal,
  * grouped-query, split-KV), its backward, and split-KV decode (per-head and
- * grouped-query) for one NVIDIA GB300 GPU (sm_103a).
+ * grouped-query) for one NVIDIA GB300 GPU (sm_103a); rotary positions, a paged
+ * key/value cache and the decode that reads it, with or without a prefix that
+ * all sequences share.
  *
  * Sources (web pages, cited by title and section):
  *   [T1] "FlashAttention 简化版：Tiling + Online Softmax" (forceinjection.github.io)
@@ -259,10 +261,134 @@ int fa_decode_splitkv_noalloc(const void* q, const void* k, const void* v, void*
                               fa_stream_t stream);
 
 /*
+ * fa_rope -- rotary positions on q and k (or, with inverse = 1, the backward
+ * pass: the same rotation by the negative angle on the gradients of fa_rope's
+ * outputs, as fa_bwd writes them for its q and k).
+ *
+ * The first `rot` elements of a head form rot/2 pairs: elements (i, i + rot/2),
+ * or (2i, 2i + 1) with interleaved = 1.  Pair i turns by the angle
+ * phi = positions[axis(i)][b][n] * freqs[i]:
+ *   (x1, x2) -> (x1 cos phi - x2 sin phi, x1 sin phi + x2 cos phi)
+ * and the elements from `rot` on are copied.  One axis gives text positions;
+ * three (time, height, width) those of images and video.  Angles are exact for
+ * every 32-bit position (the phase is formed in 64-bit integers, not in fp32);
+ * products and sums are fp32, rounded once to dtype.
+ *   q [B, H, N, d], k [B, Hkv, N, d] in dtype (FA_BF16 or FA_FP32), d 64 or 128;
+ *     k = k_out = NULL with Hkv = 0 rotates q alone.
+ *   q_out, k_out  out: the inputs themselves (same pointer, same strides) or
+ *     memory that overlaps no input.
+ *   strides       NULL = all contiguous, or a HOST array of 12: the (batch,
+ *     head, token) strides in elements of q, k, q_out and k_out, so that heads can
+ *     be read out of a projection's [B, N, heads, d] output.  d is contiguous;
+ *     every stride is >= 0 and a multiple of 16 bytes.  Rows of an output must
+ *     not overlap one another.
+ *   positions     device int32 [n_axes, B, N], or [n_axes, N] with pos_shared = 1
+ *     (the same for every batch entry); any value, negative ones too.
+ *   freqs         device float64 [rot/2], radians per position, finite.
+ *   axes          device int32 [rot/2]: axis(i) in 0 .. n_axes - 1, or NULL: axis 0.
+ *     A pair whose entry is out of range becomes NaN, and
+ *     fa_check_device_error reports FA_ERR_INVALID_ARG.
+ *   n_axes 1 .. 8; rot a multiple of 16, 16 <= rot <= d.
+ * No workspace.  Returns FA_OK or an fa_status code.
+ */
+int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+            int B, int H, int Hkv, int N, int d, int dtype, const int* positions, int pos_shared,
+            const double* freqs, const int* axes, int n_axes, int rot, int interleaved, int inverse,
+            fa_stream_t stream);
+
+/*
+ * fa_paged_append -- writes the keys and values of T new tokens into a paged
+ * cache, rotating the keys (and the tokens' queries) on the way.
+ *
+ * The cache is a pool of num_pages pages of page_size rows: k_cache and v_cache
+ * [num_pages, Hkv, page_size, d] bf16, or any layout with d contiguous given by
+ * cache_strides (a HOST array: the page, head and row strides in elements, used
+ * for both caches; NULL = contiguous).  Token t goes to slots[t]:
+ * page slots[t] / page_size, row slots[t] % page_size.
+ *   k, v     [T, Hkv, d] bf16      q [T, H, d] bf16, or NULL with H = 0
+ *   q_out    [T, H, d] bf16 contiguous, out (may be q itself if that is contiguous)
+ *   in_strides  NULL = contiguous, or a HOST array of 6: (token, head) strides in
+ *            elements of k, v and q (slices of one projection's output).
+ *   slots    device int64 [T].  A negative slot stores nothing: a batch padded to a
+ *            fixed size marks its unused places so.  A slot past the cache stores
+ *            nothing and makes fa_check_device_error report FA_ERR_INVALID_ARG.
+ *            Two tokens must not name one slot in a call (that slot would hold
+ *            parts of either); no other slot is touched.
+ *   positions, freqs, axes, n_axes, rot, interleaved  as in fa_rope, with positions
+ *            int32 [n_axes, T]; rot = 0 with positions = freqs = NULL stores the keys
+ *            and copies the queries as they are.  q_out is written for every token,
+ *            those with a negative slot too.
+ * All strides are multiples of 8 elements.  T = 0 is a step without new tokens.
+ * Returns FA_OK or an fa_status code.
+ */
+int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, void* k_cache, void* v_cache,
+                    const long long* in_strides, const long long* cache_strides, const long long* slots,
+                    int T, int H, int Hkv, int d, int num_pages, int page_size,
+                    const int* positions, const double* freqs, const int* axes, int n_axes, int rot,
+                    int interleaved, fa_stream_t stream);
+
+/*
+ * fa_decode_paged -- attention of one bf16 query per head over a paged cache:
+ * sequence b sees its seq_lens[b] rows, row i being row i % page_size of page
+ * page_table[b][i / page_size].  Lengths stay on the device; the work is spread
+ * evenly over the GPU whatever they are.
+ *
+ *   q, o       [B, H, d] bf16 (o is written); query head h reads key/value head
+ *              h / (H / Hkv), any group size H / Hkv.
+ *   k_cache, v_cache, cache_strides, num_pages, page_size   as in fa_paged_append.
+ *   page_table device int32 [B, max_pages], rows table_stride entries apart; entries
+ *              past a sequence's last page are not read.
+ *   seq_lens   device int32 [B].  A sequence without keys (seq_lens[b] <= 0) gets
+ *              o = 0 and lse = -inf.
+ *   scale      finite score scale.
+ *   lse        fp32 [B, H] out (natural log, scaled-score units), or NULL.
+ *   workspace  device buffer of at least fa_decode_paged_workspace_bytes(B, H, Hkv,
+ *              d, 0) bytes, 16-byte aligned, or NULL to allocate it stream-ordered on
+ *              `stream`.  It needs no clearing; calls that may overlap on the GPU must
+ *              not share one.
+ * A sequence with a page outside the cache or more keys than max_pages * page_size
+ * gets NaN in o and lse, and fa_check_device_error reports FA_ERR_INVALID_ARG; the
+ * others are not affected.  Accumulation and softmax statistics are fp32, P is
+ * rounded to bf16 for P V.  No atomics: repeated calls on one GPU give identical
+ * bits.  max_pages * page_size < 2^30.  Returns FA_OK or an fa_status code.
+ */
+int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, const int* page_table,
+                    long long table_stride, const int* seq_lens, int B, int H, int Hkv, int d,
+                    int num_pages, int page_size, int max_pages, const long long* cache_strides, float scale,
+                    void* workspace, size_t workspace_bytes, float* lse, fa_stream_t stream);
+
+/*
+ * fa_decode_paged_prefix -- fa_decode_paged for a batch whose sequences all begin
+ * with the same prefix_len keys, which are read and multiplied once for the whole
+ * batch.  Sequence b sees the prefix, then its own seq_lens[b] rows:
+ * page_table and seq_lens describe the own rows alone.
+ *   prefix_pages  device int32 [ceil(prefix_len / page_size)]: the pages of the
+ *                 prefix, whose last one may be partly used.
+ *   prefix_len    >= 0; 0 is fa_decode_paged (prefix_pages may then be NULL).
+ *   seq_lens      0 = a sequence that sees the prefix alone; negative = an unused place
+ *                 of a padded batch, which sees nothing (o = 0, lse = -inf).
+ *   workspace     fa_decode_paged_workspace_bytes(B, H, Hkv, d, prefix_len) bytes.
+ * A prefix page outside the cache gives NaN in every sequence that sees the prefix.
+ * Other arguments and rules as in fa_decode_paged.
+ */
+int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cache, void* o,
+                           const int* prefix_pages, int prefix_len, const int* page_table,
+                           long long table_stride, const int* seq_lens, int B, int H, int Hkv, int d,
+                           int num_pages, int page_size, int max_pages, const long long* cache_strides,
+                           float scale, void* workspace, size_t workspace_bytes, float* lse,
+                           fa_stream_t stream);
+
+/* Bytes of workspace fa_decode_paged (prefix_len = 0) and fa_decode_paged_prefix need on the current
+ * device; 0 on bad arguments or without an sm_103 GPU. */
+size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int prefix_len);
+
+/*
  * fa_check_device_error -- reads and clears the library's device error word
  * on the current device (synchronises that device).  Returns FA_OK, or
  * FA_ERR_TIMEOUT if a kernel gave up on a wait since the last check (its
- * outputs are then undefined), or FA_ERR_CUDA if the read itself failed.
+ * outputs are then undefined), or FA_ERR_INVALID_ARG if a kernel met an index
+ * outside its range in device memory (a page, slot, length or axis of the entry
+ * points above that say so), or FA_ERR_CUDA if the read itself failed.
  */
 int fa_check_device_error(void);
 
