@@ -114,11 +114,19 @@ struct PagedLaunch {
   long long table_stride;
   int prefix_len;
   float c;                  // scale * log2(e)
+  char* ws;                 // paged_plan(...).total bytes
   int* err;
   int sms;
   cudaStream_t stream;
 };
+// Workspace layout (byte offsets) of a paged decode with G query heads a key/value head.
+struct PagedPlan {
+  int n_cta = 0;
+  size_t part_ml = 0, part_o = 0, total = 0;
+};
+PagedPlan paged_plan(int G, int d, int sms);
 cudaError_t launch_decode_paged(const PagedLaunch& a);
+cudaError_t launch_decode_prefix(const PagedLaunch& a);
 
 struct FwdLaunch {
   const CUtensorMap* tm_q;  // 3-D maps over [B*H, N, d] (innermost d), 128-byte swizzle

@@ -1,11 +1,22 @@
-// fa_paged.cu -- one query per head over a paged key/value cache.
+// fa_paged.cu -- one query per head over a paged key/value cache (split-KV decode of a ragged batch).
 //
-// Sequence b sees the keys of the shared prefix (if any), then its own len_b cache rows through its row
-// of the page table: o = softmax(scale q K^T) V and the natural-log LSE, by the online-softmax
-// recurrence in log2 units.
+// Sequence b sees len_b cache rows through its row of the page table: o = softmax(scale q K^T) V and the
+// natural-log LSE, by the online-softmax recurrence in log2 units.  All G = H / Hkv query heads of a
+// key/value head are the rows of one 16-row (or two 16-row) matrix tile, so each key and value is read from
+// device memory once: the kernel is bound by those bytes.
 //
-// One CTA per (sequence, query head); each warp takes every eighth key, and the warps' partial states
-// (m, l, o) merge at the end.
+// Work split.  A unit is one (sequence, group of query heads); its keys are cut into tiles of PG_TILE.  The
+// tiles of all units, in order, are dealt evenly to the CTAs, one contiguous range each, whatever the
+// lengths are (they stay in device memory; every CTA sums them itself).  A CTA's range covers whole units,
+// which it finishes, and at most two parts of units at its ends, which it leaves as partial states (m, l,
+// unnormalised O) for fa_paged_merge_kernel.
+//
+// Inside a CTA each warp takes its own KW keys of every tile through its own ring of asynchronous 16-byte
+// copies, with no barrier between the warps until a unit ends: S = Q K^T and O += P V by warp-level matrix
+// products (S in registers becomes the A operand of P V), the running maximum moved only when a score passes
+// it by more than 2^PG_TAU.  Rows of any page size and stride: the lanes look up their keys' pages one step
+// ahead and pass the row offsets around by shuffles.  The warps' states merge in shared memory when a unit
+// ends.  A matrix tile of few real rows wastes products, not bytes.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -14,85 +25,597 @@
 namespace fa {
 
 namespace {
-constexpr int PG_WARPS = 8;
+
 enum : int { W_PAGE = 0x30, W_LEN };  // sites recorded with DEV_BAD_INDEX
+constexpr float PG_TAU = 8.f;
+
+template <int D_, int MT_>
+struct PgCfg {
+  static constexpr int D = D_;
+  static constexpr int MT = MT_;             // 16-row tiles of query heads
+  static constexpr int GR = 16 * MT;         // query heads a unit holds
+  static constexpr int NW = 4;
+  static constexpr int KW = D == 128 ? 16 : 32;  // keys of one warp step: 8 KB of K and V
+  static constexpr int TILE = NW * KW;
+  static constexpr int STAGES = 3;
+  static constexpr int CTAS = 2;             // per SM
+  static constexpr int ROW_BYTES = D * 2;
+  static constexpr int K_BYTES = KW * ROW_BYTES;
+  static constexpr int STAGE_BYTES = 2 * K_BYTES;
+  static constexpr int OFF_Q = NW * STAGES * STAGE_BYTES;
+  static constexpr int OFF_ML = OFF_Q + GR * ROW_BYTES;         // float2 [NW][GR]
+  static constexpr int OFF_PLAN = OFF_ML + NW * GR * 8;
+  static constexpr int SMEM = OFF_PLAN + 64;
+  static constexpr bool Q_IN_REGS = MT == 1 || D == 64;
+  static_assert(16 * D * 4 <= STAGE_BYTES, "a warp's O of one row tile fits one of its stages");
+};
+
+struct PgParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kc;
+  const __nv_bfloat16* vc;
+  __nv_bfloat16* o;
+  float* lse;
+  const int* table;
+  const int* lens;
+  long long c_page, c_head, c_row, table_stride;
+  int B, H, Hkv, G, ngrp, U;      // U = Hkv * ngrp units a sequence
+  int num_pages, page_size;
+  int cap;                        // max_pages * page_size
+  int n_cta;
+  float c;
+  int* err;
+  // partial states: [2 * n_cta][GR] of m, then l, then O [GR][D]
+  float* part_ml;                 // float2 [2 * n_cta][GR]
+  float* part_o;                  // [2 * n_cta][GR][D]
+  // shared prefix (0 states: none): every unit's own state goes to unit_ml / unit_o [B * H], and the merge adds
+  // the prefix's states [pre_split][Hkv * B * G]
+  int prefix;
+  float* unit_ml;
+  float* unit_o;
+  const float* pre_ml;
+  const float* pre_o;
+  int pre_split;
+};
+
+// Tiles of sequence b: 0 for a sequence without keys or with a length past its table.
+template <int TILE>
+__device__ __forceinline__ int seq_tiles(const PgParams& p, int b, int* len) {
+  const int n = p.lens[b];
+  *len = n;
+  return n <= 0 || n > p.cap ? 0 : (n + TILE - 1) / TILE;
+}
+
+// CTAs that share `total` tiles, the first tile of CTA c, and the CTA of tile t.
+__device__ __forceinline__ long long cta_count(long long total, int n_cta) { return total < n_cta ? total : n_cta; }
+__device__ __forceinline__ long long cta_first(long long c, long long total, long long n) { return c * total / n; }
+__device__ __forceinline__ long long cta_of(long long t, long long total, long long n) {
+  return ((t + 1) * n - 1) / total;
+}
+
+template <class C>
+struct Cursor {
+  int b, u, tile, nt, len;
+  __device__ __forceinline__ void next(const PgParams& p) {
+    if (++tile < nt) return;
+    tile = 0;
+    if (++u < p.U) return;
+    u = 0;
+    do {
+      if (++b >= p.B) {  // past the last unit: nothing is read through it
+        nt = 0x7fffffff;
+        len = 0;
+        return;
+      }
+      nt = seq_tiles<C::TILE>(p, b, &len);
+    } while (nt == 0);
+  }
+};
+
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(32 * PG_WARPS) fa_decode_paged_simple(const PagedLaunch a) {
-  constexpr int E = D / 32;
-  __shared__ float sm_m[PG_WARPS], sm_l[PG_WARPS], sm_o[PG_WARPS][D];
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+template <class C>
+__global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int D = C::D, MT = C::MT, KW = C::KW, NW = C::NW, S = C::STAGES;
+  constexpr int CPR = D / 8;        // 16-byte pieces of a row
+  constexpr int RPP = 32 / CPR;     // rows one warp-wide copy covers
+  constexpr int NP = KW / RPP;      // copies of K (and of V) a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = h / (a.H / a.Hkv);
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<long long>(b) * a.H + h) * D;
-  float qf[E], o[E];
+  griddep_launch_dependents();
+
+  // ---- plan: total tiles, this CTA's range, the unit it starts in
+  long long* plan = reinterpret_cast<long long*>(smem + C::OFF_PLAN);  // [0..3] warp sums, [4] tiles before, [5] b
+  const int per = (p.B + 32 * NW - 1) / (32 * NW);
+  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+  long long mine = 0;
+  int len_tmp;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles<C::TILE>(p, b, &len_tmp);
+  long long incl = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qf[e] = __bfloat162float(q[lane * E + e]) * a.c;
-    o[e] = 0.f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
   }
-  int len = a.lens[b];
-  const bool idle = len < 0;
-  bool bad = false;
-  if (len > static_cast<long long>(a.max_pages) * a.page_size) bad = true;
-  if (idle || bad) len = 0;
-  const int total = idle ? 0 : a.prefix_len + len;
-  float m = -INFINITY, l = 0.f;
-  for (int j = warp; j < total && !bad; j += PG_WARPS) {
-    const int i = j < a.prefix_len ? j : j - a.prefix_len;
-    const int page = j < a.prefix_len ? a.prefix_pages[i / a.page_size] : a.table[b * a.table_stride + i / a.page_size];
-    if (page < 0 || page >= a.num_pages) {
-      bad = true;
-      break;
-    }
-    const long long off = page * a.c_page + hk * a.c_head + i % a.page_size * a.c_row + lane * E;
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k_cache) + off;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) + off;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qf[e], __bfloat162float(k[e]), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float m_new = fmaxf(m, s);
-    const float ref = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = ex2_approx(m - ref), p = ex2_approx(s - ref);
-    l = l * alpha + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * alpha + p * __bfloat162float(v[e]);
-    m = m_new;
-  }
-  if (bad) l = __int_as_float(0x7fc00000);
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-    if (bad) record_bad_index(a.err, W_PAGE);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
+  if (lane == 31) plan[warp] = incl;
   __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY;
-    for (int w = 0; w < PG_WARPS; ++w) M = fmaxf(M, sm_m[w]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, O = 0.f;
-    for (int w = 0; w < PG_WARPS; ++w) {
-      const float wt = ex2_approx(sm_m[w] - ref);
-      L += sm_l[w] * wt;
-      O += sm_o[w][threadIdx.x] * wt;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) incl += plan[w];
+    total += plan[w];
+  }
+  total *= p.U;
+  const long long n = cta_count(total, p.n_cta);
+  if (static_cast<long long>(blockIdx.x) >= n) return;  // the whole CTA (n = 0 without keys)
+  const long long t0 = cta_first(blockIdx.x, total, n), t1 = cta_first(blockIdx.x + 1, total, n);
+  {
+    long long before = (incl - mine) * p.U;
+    if (t0 >= before && t0 < incl * p.U) {
+      for (int b = b_lo;; ++b) {
+        const long long nt = static_cast<long long>(seq_tiles<C::TILE>(p, b, &len_tmp)) * p.U;
+        if (t0 < before + nt) {
+          plan[4] = before;
+          plan[5] = b;
+          break;
+        }
+        before += nt;
+      }
     }
-    const long long row = static_cast<long long>(b) * a.H + h;
-    const bool nothing = total == 0 && !bad;
-    static_cast<__nv_bfloat16*>(a.o)[row * D + threadIdx.x] = __float2bfloat16_rn(nothing ? 0.f : O / L);
-    if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = nothing ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  Cursor<C> cur;
+  cur.b = static_cast<int>(plan[5]);
+  cur.nt = seq_tiles<C::TILE>(p, cur.b, &cur.len);
+  cur.u = static_cast<int>((t0 - plan[4]) / cur.nt);
+  cur.tile = static_cast<int>((t0 - plan[4]) % cur.nt);
+  const int steps = static_cast<int>(t1 - t0);
+
+  // ---- loads: `ld` is the step whose pages are being looked up; lane r holds the page of key r of its KW
+  const uint32_t ring = smem_u32(smem) + warp * S * C::STAGE_BYTES;
+  Cursor<C> ld = cur;
+  int ld_step = 0, ld_stage = 0;
+  const int r_l = lane % KW;
+  int pid = 0;
+  auto lookup = [&]() {
+    const int key = ld.tile * C::TILE + warp * KW + r_l;
+    if (ld_step < steps && key < ld.len) pid = __ldg(p.table + ld.b * p.table_stride + key / p.page_size);
+  };
+  auto load_step = [&]() {  // copies of step ld_step into ring stage ld_stage, then the next step's lookup
+    if (ld_step < steps) {
+      const int key = ld.tile * C::TILE + warp * KW + r_l;
+      long long off = -1;  // zeros
+      if (key < ld.len) {
+        if (pid >= 0 && pid < p.num_pages) {
+          off = pid * p.c_page + (ld.u / p.ngrp) * p.c_head + key % p.page_size * p.c_row;
+        } else {
+          off = -2;  // a NaN key: the sequence's outputs become NaN
+          record_bad_index(p.err, W_PAGE);
+        }
+      }
+      const int piece = lane % CPR;
+      const uint32_t dst0 = ring + ld_stage * C::STAGE_BYTES;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int row = i * RPP + lane / CPR;
+        const long long ro = __shfl_sync(0xffffffffu, off, row);
+        const uint32_t dst = dst0 + row * C::ROW_BYTES + ((piece ^ (row & 7)) << 4);
+        const long long src = ro < 0 ? 0 : ro + piece * 8;
+        if (ro == -2 && piece == 0)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(0x7fff7fffu) : "memory");
+        else
+          cp_async16(dst, p.kc + src, ro < 0 ? 0 : 16);
+        cp_async16(dst + C::K_BYTES, p.vc + src, ro < 0 ? 0 : 16);
+      }
+    }
+    cp_async_commit();
+    ++ld_step;
+    ld_stage = ld_stage + 1 == S ? 0 : ld_stage + 1;
+    if (ld_step < steps) {
+      ld.next(p);
+      lookup();
+    }
+  };
+  lookup();
+
+  // ---- queries of the first unit
+  uint8_t* sq = smem + C::OFF_Q;
+  constexpr int QN = C::GR * CPR / (32 * NW);  // 16-byte pieces of Q a thread carries
+  static_assert(C::GR * CPR % (32 * NW) == 0, "whole rounds");
+  uint4 qv[QN];
+  auto fetch_q = [&](int b, int u) {
+    const int h0 = u / p.ngrp * p.G + u % p.ngrp * C::GR;
+    const int rows = min(C::GR, p.G - u % p.ngrp * C::GR);
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int e = i * 32 * NW + threadIdx.x, row = e / CPR;
+      qv[i] = row < rows ? *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(b) * p.H + h0 + row) * D +
+                                                           e % CPR * 8)
+                         : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto store_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int e = i * 32 * NW + threadIdx.x, row = e / CPR;
+      *reinterpret_cast<uint4*>(sq + row * C::ROW_BYTES + ((e % CPR ^ (row & 7)) << 4)) = qv[i];
+    }
+  };
+  fetch_q(cur.b, cur.u);
+#pragma unroll
+  for (int i = 0; i < S; ++i) load_step();
+  store_q();
+  __syncthreads();
+
+  // ---- fragments
+  const int l7 = lane & 7, mat = lane >> 3;
+  const uint32_t q_addr = smem_u32(sq) + ((mat & 1) * 8 + l7) * C::ROW_BYTES;   // A: rows (mat&1), k half (mat>>1)
+  const int q_x = (mat >> 1) ^ l7;
+  const uint32_t k_off = ((mat >> 1) * 8 + l7) * C::ROW_BYTES;                   // B: keys (mat>>1), k half (mat&1)
+  const int k_x = (mat & 1) ^ l7;
+  const uint32_t v_off = C::K_BYTES + ((mat & 1) * 8 + l7) * C::ROW_BYTES;       // B of P V: keys (mat&1), dims (mat>>1)
+  const int v_x = (mat >> 1) ^ l7;
+  uint32_t qf[C::Q_IN_REGS ? MT : 1][C::Q_IN_REGS ? D / 16 : 1][4];
+  auto load_qf = [&]() {
+    if constexpr (C::Q_IN_REGS) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          ldmatrix_x4(q_addr + mt * 16 * C::ROW_BYTES + (((2 * ks) ^ q_x) << 4), qf[mt][ks]);
+    }
+  };
+  load_qf();
+  float o[MT][D / 8][4];
+  float m_ref[MT][2], l[MT][2];
+  auto reset = [&]() {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+      m_ref[mt][0] = m_ref[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+  };
+  reset();
+  int seg_tile0 = cur.tile;  // first tile of the unit that this CTA covers
+  bool first_unit = true;
+  int stage = 0;
+
+  for (int step = 0; step < steps; ++step) {
+    cp_async_wait<S - 1>();
+    __syncwarp();
+    const uint32_t st = ring + stage * C::STAGE_BYTES;
+    const int valid = cur.len - (cur.tile * C::TILE + warp * KW);
+    if (valid > 0) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float s[KW / 8][4];
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t a[4];
+          if constexpr (C::Q_IN_REGS) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = qf[mt][ks][e];
+          } else {
+            ldmatrix_x4(q_addr + mt * 16 * C::ROW_BYTES + (((2 * ks) ^ q_x) << 4), a);
+          }
+#pragma unroll
+          for (int kb = 0; kb < KW / 16; ++kb) {
+            uint32_t b[4];
+            ldmatrix_x4(st + k_off + kb * 16 * C::ROW_BYTES + (((2 * ks) ^ k_x) << 4), b);
+            mma_16816(s[2 * kb], a, b[0], b[1]);
+            mma_16816(s[2 * kb + 1], a, b[2], b[3]);
+          }
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float t = s[j][e] * p.c;
+            if (valid < KW && 8 * j + 2 * (lane & 3) + (e & 1) >= valid) t = -INFINITY;
+            s[j][e] = t;
+            mx[e >> 1] = fmaxf(mx[e >> 1], t);
+          }
+        if (__any_sync(0xffffffffu, mx[0] > m_ref[mt][0] + PG_TAU || mx[1] > m_ref[mt][1] + PG_TAU)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            if (mx[r] > m_ref[mt][r] + PG_TAU) {
+              const float alpha = ex2_approx(m_ref[mt][r] - mx[r]);  // 0 on the first keys
+              m_ref[mt][r] = mx[r];
+              l[mt][r] *= alpha;
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j) {
+                o[mt][j][2 * r] *= alpha;
+                o[mt][j][2 * r + 1] *= alpha;
+              }
+            }
+          }
+        }
+        const float m0 = m_ref[mt][0] == -INFINITY ? 0.f : m_ref[mt][0];
+        const float m1 = m_ref[mt][1] == -INFINITY ? 0.f : m_ref[mt][1];
+        uint32_t pf[KW / 16][4];  // P rounded to bf16: the A operand of P V
+#pragma unroll
+        for (int j = 0; j < KW / 8; ++j) {
+          const float p0 = ex2_approx(s[j][0] - m0), p1 = ex2_approx(s[j][1] - m0);
+          const float p2 = ex2_approx(s[j][2] - m1), p3 = ex2_approx(s[j][3] - m1);
+          l[mt][0] += p0 + p1;
+          l[mt][1] += p2 + p3;
+          pf[j / 2][(j & 1) * 2] = pack_bf16x2(p0, p1);
+          pf[j / 2][(j & 1) * 2 + 1] = pack_bf16x2(p2, p3);
+        }
+#pragma unroll
+        for (int kb = 0; kb < KW / 16; ++kb)
+#pragma unroll
+          for (int dp = 0; dp < D / 16; ++dp) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(st + v_off + kb * 16 * C::ROW_BYTES + (((2 * dp) ^ v_x) << 4), b);
+            mma_16816(o[mt][2 * dp], pf[kb], b[0], b[1]);
+            mma_16816(o[mt][2 * dp + 1], pf[kb], b[2], b[3]);
+          }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+
+    const bool unit_ends = cur.tile + 1 == cur.nt;
+    if (unit_ends || step + 1 == steps) {
+      // ---- the unit's part in this CTA ends: merge the warps' states
+      Cursor<C> nx = cur;
+      const bool more = step + 1 < steps;
+      if (more) {
+        nx.next(p);
+        fetch_q(nx.b, nx.u);  // in flight during the merge
+      }
+      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 1);
+          l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 2);
+          if ((lane & 3) == 0) ml[warp * C::GR + mt * 16 + r * 8 + (lane >> 2)] = make_float2(m_ref[mt][r], l[mt][r]);
+        }
+      __syncthreads();
+      const bool whole = unit_ends && seg_tile0 == 0;
+      const int slot = 2 * blockIdx.x + (first_unit ? 0 : 1);
+      const int h0 = cur.u / p.ngrp * p.G + cur.u % p.ngrp * C::GR;
+      const int rows = min(C::GR, p.G - cur.u % p.ngrp * C::GR);
+      float* const mine_o = reinterpret_cast<float*>(smem + (warp * S + stage) * C::STAGE_BYTES);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = mt * 16 + r * 8 + (lane >> 2);
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * C::GR + row].x);
+          const float wt = M == -INFINITY ? 0.f : ex2_approx(m_ref[mt][r] - M);
+          // row r*8 + lane/4 of the tile; 16-byte pieces swapped by the row so that eight rows use all banks
+          float* dst = mine_o + (r * 8 + (lane >> 2)) * D;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            const int col = 8 * j + 2 * (lane & 3);
+            *reinterpret_cast<float2*>(dst + (((col >> 2) ^ (lane >> 2)) << 2) + (col & 3)) =
+                make_float2(o[mt][j][2 * r] * wt, o[mt][j][2 * r + 1] * wt);
+          }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 16 * (D / 4); e += 32 * NW) {
+          const int row = e / (D / 4), pc = e % (D / 4);
+          const int grow = mt * 16 + row;
+          if (grow < rows) {
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * C::GR + grow].x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              const float2 x = ml[w * C::GR + grow];
+              // an empty warp state is (-inf, 0); a NaN l must survive
+              L += x.y * (x.x == -INFINITY ? 1.f : ex2_approx(x.x - M));
+              const float4 y = *reinterpret_cast<const float4*>(
+                  reinterpret_cast<const float*>(smem + (w * S + stage) * C::STAGE_BYTES) + row * D +
+                  ((pc ^ (row & 7)) << 2));
+              acc.x += y.x;
+              acc.y += y.y;
+              acc.z += y.z;
+              acc.w += y.w;
+            }
+            const long long head = static_cast<long long>(cur.b) * p.H + h0 + grow;
+            if (whole && !p.prefix) {
+              const float inv = 1.f / L;
+              *reinterpret_cast<uint2*>(p.o + head * D + pc * 4) =
+                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+              if (p.lse != nullptr && pc == 0) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
+            } else {
+              const long long at = whole ? head : static_cast<long long>(slot) * C::GR + grow;
+              *reinterpret_cast<float4*>((whole ? p.unit_o : p.part_o) + at * D + pc * 4) = acc;
+              if (pc == 0) reinterpret_cast<float2*>(whole ? p.unit_ml : p.part_ml)[at] = make_float2(M, L);
+            }
+          }
+        }
+        __syncthreads();
+      }
+      first_unit = false;
+      if (more) {
+        store_q();
+        __syncthreads();
+        load_qf();
+        reset();
+        seg_tile0 = nx.tile;
+      }
+    }
+    load_step();  // into the stage just read
+    stage = stage + 1 == S ? 0 : stage + 1;
+    if (step + 1 < steps) cur.next(p);
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the parts of units that several CTAs share (and the shared prefix's states), writes the outputs of
+// sequences without keys, and reports bad lengths.  One CTA per unit; M = max m_s, then l and O add up with
+// weights 2^(m_s - M) in key order.
+template <int D, int GR, int TILE>
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgParams p) {
+  __shared__ long long red[2][4];
+  griddep_wait();
+  const int b = blockIdx.x / p.U, u = blockIdx.x % p.U;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long before = 0, total = 0;
+  int len;
+  for (int i = threadIdx.x; i < p.B; i += 128) {
+    const int nt = seq_tiles<TILE>(p, i, &len);
+    total += nt;
+    if (i < b) before += nt;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) {
+    red[0][warp] = before;
+    red[1][warp] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    before += red[0][w];
+    total += red[1][w];
+  }
+  const int nt = seq_tiles<TILE>(p, b, &len);
+  const bool bad = len > p.cap;
+  if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
+  const long long first = before * p.U + static_cast<long long>(u) * nt;
+  long long c0 = 0, c1 = -1, n = 1;
+  total *= p.U;
+  if (nt > 0) {
+    n = cta_count(total, p.n_cta);
+    c0 = cta_of(first, total, n);
+    c1 = cta_of(first + nt - 1, total, n);
+    if (c0 == c1 && !p.prefix) return;  // its CTA wrote the output
+  }
+  const int pre = len < 0 || bad ? 0 : p.pre_split;
+  const bool whole = nt > 0 && c0 == c1;
+  const int own = whole ? 1 : static_cast<int>(c1 - c0 + 1);
+  const int slot0 = nt > 0 && first > cta_first(c0, total, n) ? 1 : 0;  // c0's second slot when its range began earlier
+  const int h0 = u / p.ngrp * p.G + u % p.ngrp * GR;
+  const int rows = min(GR, p.G - u % p.ngrp * GR);
+  const int hk = u / p.ngrp;
+  for (int e = threadIdx.x; e < rows * (D / 4); e += 128) {
+    const int row = e / (D / 4), pc = e % (D / 4);
+    const long long head = static_cast<long long>(b) * p.H + h0 + row;
+    const long long prow = static_cast<long long>(hk) * p.B * p.G + static_cast<long long>(b) * p.G + (h0 + row - hk * p.G);
+    const long long pstep = static_cast<long long>(p.Hkv) * p.B * p.G;
+    auto ml_at = [&](int s) {
+      if (s < pre) return reinterpret_cast<const float2*>(p.pre_ml)[s * pstep + prow];
+      s -= pre;
+      if (whole) return reinterpret_cast<const float2*>(p.unit_ml)[head];
+      return reinterpret_cast<const float2*>(p.part_ml)[(2 * (c0 + s) + (s == 0 ? slot0 : 0)) * GR + row];
+    };
+    auto o_at = [&](int s) {
+      if (s < pre) return p.pre_o + (s * pstep + prow) * D;
+      s -= pre;
+      if (whole) return static_cast<const float*>(p.unit_o) + head * D;
+      return static_cast<const float*>(p.part_o) + ((2 * (c0 + s) + (s == 0 ? slot0 : 0)) * GR + row) * D;
+    };
+    const int parts = pre + own;
+    float M = -INFINITY, L = 0.f;
+    for (int s = 0; s < parts; ++s) M = fmaxf(M, ml_at(s).x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < parts; ++s) {
+      const float2 x = ml_at(s);
+      const float w = x.x == -INFINITY ? 1.f : ex2_approx(x.x - M);  // an empty state is (-inf, 0, 0)
+      const float4 y = *reinterpret_cast<const float4*>(o_at(s) + pc * 4);
+      L = fmaf(x.y, w, L);
+      acc.x = fmaf(y.x, w, acc.x);
+      acc.y = fmaf(y.y, w, acc.y);
+      acc.z = fmaf(y.z, w, acc.z);
+      acc.w = fmaf(y.w, w, acc.w);
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    const float inv = bad ? nan : parts == 0 ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2*>(p.o + head * D + pc * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (p.lse != nullptr && pc == 0)
+      p.lse[head] = bad ? nan : parts == 0 ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
 }
 
+namespace {
+
+constexpr size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+template <class C>
+PagedPlan plan_of(int sms) {
+  PagedPlan pl;
+  pl.n_cta = sms * C::CTAS;
+  pl.part_ml = 0;
+  pl.part_o = round256(static_cast<size_t>(2) * pl.n_cta * C::GR * 8);
+  pl.total = pl.part_o + round256(static_cast<size_t>(2) * pl.n_cta * C::GR * C::D * 4);
+  return pl;
+}
+
+template <class C>
+cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
+  PgParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.kc = static_cast<const __nv_bfloat16*>(a.k_cache);
+  p.vc = static_cast<const __nv_bfloat16*>(a.v_cache);
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.table = a.table;
+  p.lens = a.lens;
+  p.c_page = a.c_page;
+  p.c_head = a.c_head;
+  p.c_row = a.c_row;
+  p.table_stride = a.table_stride;
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.G = a.H / a.Hkv;
+  p.ngrp = (p.G + C::GR - 1) / C::GR;
+  p.U = a.Hkv * p.ngrp;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.cap = a.max_pages * a.page_size;
+  p.n_cta = pl.n_cta;
+  p.c = a.c;
+  p.err = a.err;
+  p.part_ml = reinterpret_cast<float*>(a.ws + pl.part_ml);
+  p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
+  cudaError_t e = cudaFuncSetAttribute(fa_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  fa_paged_kernel<C><<<static_cast<unsigned>(pl.n_cta), 32 * C::NW, C::SMEM, a.stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_dependent(fa_paged_merge_kernel<C::D, C::GR, C::TILE>, static_cast<unsigned>(a.B * p.U), 128, 0,
+                          a.stream, p);
+}
+
+}  // namespace
+
+// Groups of more than 16 query heads take two 16-row tiles a unit (K and V are then read once for 32 heads);
+// larger ones several units of 32.
+PagedPlan paged_plan(int G, int d, int sms) {
+  if (d == 64) return G <= 16 ? plan_of<PgCfg<64, 1>>(sms) : plan_of<PgCfg<64, 2>>(sms);
+  return G <= 16 ? plan_of<PgCfg<128, 1>>(sms) : plan_of<PgCfg<128, 2>>(sms);
+}
+
 cudaError_t launch_decode_paged(const PagedLaunch& a) {
-  const unsigned grid = static_cast<unsigned>(a.B * a.H);
-  if (a.d == 64) fa_decode_paged_simple<64><<<grid, 32 * PG_WARPS, 0, a.stream>>>(a);
-  else fa_decode_paged_simple<128><<<grid, 32 * PG_WARPS, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  const int G = a.H / a.Hkv;
+  const PagedPlan pl = paged_plan(G, a.d, a.sms);
+  if (a.d == 64) return G <= 16 ? launch_paged<PgCfg<64, 1>>(a, pl) : launch_paged<PgCfg<64, 2>>(a, pl);
+  return G <= 16 ? launch_paged<PgCfg<128, 1>>(a, pl) : launch_paged<PgCfg<128, 2>>(a, pl);
 }
 
 }  // namespace fa

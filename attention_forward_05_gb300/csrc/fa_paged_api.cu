@@ -154,8 +154,11 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
 }
 
 size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int prefix_len) {
-  (void)B, (void)H, (void)Hkv, (void)d, (void)prefix_len;
-  return 0;
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || prefix_len < 0 || (d != 64 && d != 128)) return 0;
+  int* err = nullptr;
+  int sms = 0;
+  if (fa::current_device_info(&err, &sms) != FA_OK) return 0;
+  return fa::paged_plan(H / Hkv, d, sms).total;
 }
 
 int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cache, void* o, const int* prefix_pages,
@@ -183,7 +186,15 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   fa::PagedLaunch a;
   const int rc = fa::current_device_info(&a.err, &a.sms);
   if (rc != FA_OK) return rc;
-  (void)workspace_bytes;
+  const size_t need = fa::paged_plan(H / Hkv, d, a.sms).total;
+  if (workspace && workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  void* ws = workspace;
+  if (ws == nullptr) {
+    const cudaError_t ea = cudaMallocAsync(&ws, need, a.stream);
+    if (ea != cudaSuccess) return fa::report_cuda_error(ea);
+  }
+  a.ws = static_cast<char*>(ws);
   a.q = q;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
@@ -205,8 +216,11 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   a.table_stride = table_stride;
   a.prefix_len = prefix_len;
   a.c = scale * 1.4426950408889634f;
-  a.stream = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = fa::launch_decode_paged(a);
+  cudaError_t e = prefix_len > 0 ? fa::launch_decode_prefix(a) : fa::launch_decode_paged(a);
+  if (workspace == nullptr) {
+    const cudaError_t e2 = cudaFreeAsync(ws, a.stream);
+    if (e == cudaSuccess) e = e2;
+  }
   return e == cudaSuccess ? FA_OK : fa::report_cuda_error(e);
 }
 
