@@ -23,10 +23,10 @@ struct NvtxRange {
 // Launch with programmatic stream serialization: the kernel may start before the previous kernel in
 // the stream has completed, once every CTA of that kernel has executed griddepcontrol.launch_dependents.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, int threads, int smem, cudaStream_t stream,
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t stream,
                              Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
@@ -122,7 +122,7 @@ struct PagedLaunch {
 // Workspace layout (byte offsets) of a paged decode with G query heads a key/value head.
 struct PagedPlan {
   int n_cta = 0;
-  size_t part_ml = 0, part_o = 0, total = 0;
+  size_t part_ml = 0, part_o = 0, joins = 0, total = 0;
 };
 PagedPlan paged_plan(int G, int d, int sms);
 cudaError_t launch_decode_paged(const PagedLaunch& a);

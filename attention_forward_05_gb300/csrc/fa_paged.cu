@@ -9,7 +9,7 @@
 // tiles of all units, in order, are dealt evenly to the CTAs, one contiguous range each, whatever the
 // lengths are (they stay in device memory; every CTA sums them itself).  A CTA's range covers whole units,
 // which it finishes, and at most two parts of units at its ends, which it leaves as partial states (m, l,
-// unnormalised O) for fa_paged_merge_kernel.
+// unnormalised O) for fa_paged_join_kernel.
 //
 // Inside a CTA each warp takes its own KW keys of every tile through its own ring of asynchronous 16-byte
 // copies, with no barrier between the warps until a unit ends: S = Q K^T and O += P V by warp-level matrix
@@ -65,17 +65,10 @@ struct PgParams {
   int n_cta;
   float c;
   int* err;
-  // partial states: [2 * n_cta][GR] of m, then l, then O [GR][D]
-  float* part_ml;                 // float2 [2 * n_cta][GR]
-  float* part_o;                  // [2 * n_cta][GR][D]
-  // shared prefix (0 states: none): every unit's own state goes to unit_ml / unit_o [B * H], and the merge adds
-  // the prefix's states [pre_split][Hkv * B * G]
-  int prefix;
-  float* unit_ml;
-  float* unit_o;
-  const float* pre_ml;
-  const float* pre_o;
-  int pre_split;
+  float* part_ml;                 // float2 (m, l) [2 * n_cta][GR] of the CTAs' first (0) and last (1) unfinished units
+  float* part_o;                  // [2 * n_cta][GR][D] unnormalised
+  int4* joins;                    // [n_cta]: the unit (b, u) that starts in this CTA and ends in a later one, the slot of
+                                  // its first part (0 or 1), and its parts (0: there is none)
 };
 
 // Tiles of sequence b: 0 for a sequence without keys or with a length past its table.
@@ -146,7 +139,21 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     total += plan[w];
   }
   total *= p.U;
+  // outputs of sequences without keys, and of those whose length passes their table
+  for (int b = blockIdx.x; b < p.B; b += p.n_cta) {
+    int len;
+    if (seq_tiles<C::TILE>(p, b, &len) > 0) continue;
+    const bool bad = len > 0;
+    if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
+    const long long row0 = static_cast<long long>(b) * p.H;
+    for (int e = threadIdx.x; e < p.H * CPR; e += 32 * NW)
+      reinterpret_cast<uint4*>(p.o + row0 * D)[e] = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
+                                                        : make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr)
+      for (int h = threadIdx.x; h < p.H; h += 32 * NW) p.lse[row0 + h] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
+  }
   const long long n = cta_count(total, p.n_cta);
+  if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (static_cast<long long>(blockIdx.x) >= n) return;  // the whole CTA (n = 0 without keys)
   const long long t0 = cta_first(blockIdx.x, total, n), t1 = cta_first(blockIdx.x + 1, total, n);
   {
@@ -431,19 +438,23 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
               acc.w += y.w;
             }
             const long long head = static_cast<long long>(cur.b) * p.H + h0 + grow;
-            if (whole && !p.prefix) {
+            if (whole) {
               const float inv = 1.f / L;
               *reinterpret_cast<uint2*>(p.o + head * D + pc * 4) =
                   make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
               if (p.lse != nullptr && pc == 0) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
             } else {
-              const long long at = whole ? head : static_cast<long long>(slot) * C::GR + grow;
-              *reinterpret_cast<float4*>((whole ? p.unit_o : p.part_o) + at * D + pc * 4) = acc;
-              if (pc == 0) reinterpret_cast<float2*>(whole ? p.unit_ml : p.part_ml)[at] = make_float2(M, L);
+              const long long at = static_cast<long long>(slot) * C::GR + grow;
+              *reinterpret_cast<float4*>(p.part_o + at * D + pc * 4) = acc;
+              if (pc == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(M, L);
             }
           }
         }
         __syncthreads();
+      }
+      if (!unit_ends && seg_tile0 == 0 && threadIdx.x == 0) {  // begun here, ended by a later CTA
+        const long long last = t1 - (cur.tile + 1) + cur.nt - 1;
+        p.joins[blockIdx.x] = make_int4(cur.b, cur.u, slot & 1, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
       }
       first_unit = false;
       if (more) {
@@ -461,95 +472,77 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   cp_async_wait<0>();
 }
 
-// Joins the parts of units that several CTAs share (and the shared prefix's states), writes the outputs of
-// sequences without keys, and reports bad lengths.  One CTA per unit; M = max m_s, then l and O add up with
-// weights 2^(m_s - M) in key order.
-template <int D, int GR, int TILE>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgParams p) {
-  __shared__ long long red[2][4];
+// Joins the parts of a unit that several CTAs share: M = max m_s, then l and O add up with weights 2^(m_s - M).
+// One CTA per (CTA in which such a unit begins, query head of the unit); its four warps take every fourth
+// part, eight rows in flight, and add up in warp order.
+constexpr int PJ_WARPS = 4;
+template <int D, int GR>
+__global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgParams p) {
+  constexpr int E = D / 32;
+  __shared__ float sm_o[PJ_WARPS][D];
   griddep_wait();
-  const int b = blockIdx.x / p.U, u = blockIdx.x % p.U;
+  const int4 j = p.joins[blockIdx.x];
+  const int parts = j.w;
+  const int row = blockIdx.y;
+  const int g0 = j.y % p.ngrp * GR;
+  if (parts == 0 || g0 + row >= p.G) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long before = 0, total = 0;
-  int len;
-  for (int i = threadIdx.x; i < p.B; i += 128) {
-    const int nt = seq_tiles<TILE>(p, i, &len);
-    total += nt;
-    if (i < b) before += nt;
+  // part s lies in the unit's first CTA's slot j.z, or in slot 0 of the s-th CTA after it
+  auto at = [&](int s) { return static_cast<long long>(2 * (static_cast<int>(blockIdx.x) + s) + (s == 0 ? j.z : 0)) * GR + row; };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float M = -INFINITY;
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, ml[at(s)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  auto weight = [&](float m) { return m == -INFINITY ? 1.f : ex2_approx(m - M); };  // an empty state is (-inf, 0, 0)
+  float L = 0.f;
+  for (int s = lane; s < parts; s += 32) {
+    const float2 x = ml[at(s)];
+    L += x.y * weight(x.x);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) {
-    red[0][warp] = before;
-    red[1][warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float acc[E];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    before += red[0][w];
-    total += red[1][w];
-  }
-  const int nt = seq_tiles<TILE>(p, b, &len);
-  const bool bad = len > p.cap;
-  if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
-  const long long first = before * p.U + static_cast<long long>(u) * nt;
-  long long c0 = 0, c1 = -1, n = 1;
-  total *= p.U;
-  if (nt > 0) {
-    n = cta_count(total, p.n_cta);
-    c0 = cta_of(first, total, n);
-    c1 = cta_of(first + nt - 1, total, n);
-    if (c0 == c1 && !p.prefix) return;  // its CTA wrote the output
-  }
-  const int pre = len < 0 || bad ? 0 : p.pre_split;
-  const bool whole = nt > 0 && c0 == c1;
-  const int own = whole ? 1 : static_cast<int>(c1 - c0 + 1);
-  const int slot0 = nt > 0 && first > cta_first(c0, total, n) ? 1 : 0;  // c0's second slot when its range began earlier
-  const int h0 = u / p.ngrp * p.G + u % p.ngrp * GR;
-  const int rows = min(GR, p.G - u % p.ngrp * GR);
-  const int hk = u / p.ngrp;
-  for (int e = threadIdx.x; e < rows * (D / 4); e += 128) {
-    const int row = e / (D / 4), pc = e % (D / 4);
-    const long long head = static_cast<long long>(b) * p.H + h0 + row;
-    const long long prow = static_cast<long long>(hk) * p.B * p.G + static_cast<long long>(b) * p.G + (h0 + row - hk * p.G);
-    const long long pstep = static_cast<long long>(p.Hkv) * p.B * p.G;
-    auto ml_at = [&](int s) {
-      if (s < pre) return reinterpret_cast<const float2*>(p.pre_ml)[s * pstep + prow];
-      s -= pre;
-      if (whole) return reinterpret_cast<const float2*>(p.unit_ml)[head];
-      return reinterpret_cast<const float2*>(p.part_ml)[(2 * (c0 + s) + (s == 0 ? slot0 : 0)) * GR + row];
-    };
-    auto o_at = [&](int s) {
-      if (s < pre) return p.pre_o + (s * pstep + prow) * D;
-      s -= pre;
-      if (whole) return static_cast<const float*>(p.unit_o) + head * D;
-      return static_cast<const float*>(p.part_o) + ((2 * (c0 + s) + (s == 0 ? slot0 : 0)) * GR + row) * D;
-    };
-    const int parts = pre + own;
-    float M = -INFINITY, L = 0.f;
-    for (int s = 0; s < parts; ++s) M = fmaxf(M, ml_at(s).x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < parts; ++s) {
-      const float2 x = ml_at(s);
-      const float w = x.x == -INFINITY ? 1.f : ex2_approx(x.x - M);  // an empty state is (-inf, 0, 0)
-      const float4 y = *reinterpret_cast<const float4*>(o_at(s) + pc * 4);
-      L = fmaf(x.y, w, L);
-      acc.x = fmaf(y.x, w, acc.x);
-      acc.y = fmaf(y.y, w, acc.y);
-      acc.z = fmaf(y.z, w, acc.z);
-      acc.w = fmaf(y.w, w, acc.w);
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int s0 = warp; s0 < parts; s0 += 8 * PJ_WARPS) {
+    float w[8], v[8][E];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * PJ_WARPS;
+      w[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+      if (s < parts) {
+        w[i] = ml[at(s)].x;
+        const float* src = p.part_o + at(s) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[i][0] = x.x, v[i][1] = x.y;
+        }
+      }
     }
-    const float nan = __int_as_float(0x7fc00000);
-    const float inv = bad ? nan : parts == 0 ? 0.f : 1.f / L;
-    *reinterpret_cast<uint2*>(p.o + head * D + pc * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (p.lse != nullptr && pc == 0)
-      p.lse[head] = bad ? nan : parts == 0 ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float wt = weight(w[i]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], wt, acc[e]);
+    }
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  const long long head = static_cast<long long>(j.x) * p.H + j.y / p.ngrp * p.G + g0 + row;
+  if (threadIdx.x < D) {
+    float O = 0.f;
+#pragma unroll
+    for (int w = 0; w < PJ_WARPS; ++w) O += sm_o[w][threadIdx.x];
+    p.o[head * D + threadIdx.x] = __float2bfloat16_rn(O / L);
+  }
+  if (p.lse != nullptr && threadIdx.x == 0) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 namespace {
@@ -562,7 +555,8 @@ PagedPlan plan_of(int sms) {
   pl.n_cta = sms * C::CTAS;
   pl.part_ml = 0;
   pl.part_o = round256(static_cast<size_t>(2) * pl.n_cta * C::GR * 8);
-  pl.total = pl.part_o + round256(static_cast<size_t>(2) * pl.n_cta * C::GR * C::D * 4);
+  pl.joins = pl.part_o + round256(static_cast<size_t>(2) * pl.n_cta * C::GR * C::D * 4);
+  pl.total = pl.joins + round256(static_cast<size_t>(pl.n_cta) * 16);
   return pl;
 }
 
@@ -594,11 +588,13 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.err = a.err;
   p.part_ml = reinterpret_cast<float*>(a.ws + pl.part_ml);
   p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
+  p.joins = reinterpret_cast<int4*>(a.ws + pl.joins);
   cudaError_t e = cudaFuncSetAttribute(fa_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   fa_paged_kernel<C><<<static_cast<unsigned>(pl.n_cta), 32 * C::NW, C::SMEM, a.stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(fa_paged_merge_kernel<C::D, C::GR, C::TILE>, static_cast<unsigned>(a.B * p.U), 128, 0,
+  // a programmatic dependent: its launch overlaps the first kernel
+  return launch_dependent(fa_paged_join_kernel<C::D, C::GR>, dim3(pl.n_cta, p.G < C::GR ? p.G : C::GR), 32 * PJ_WARPS, 0,
                           a.stream, p);
 }
 
