@@ -28,6 +28,9 @@ namespace {
 
 enum : int { W_PAGE = 0x30, W_LEN };  // sites recorded with DEV_BAD_INDEX
 constexpr float PG_TAU = 8.f;
+// A unit's end (merging the warps' states, fetching the next queries) takes a CTA about as long as PG_END tiles:
+// the ranges are cut as if every unit had that many tiles more.
+constexpr int PG_END = 2;
 
 template <int D_, int MT_>
 struct PgCfg {
@@ -86,18 +89,20 @@ __device__ __forceinline__ long long cta_of(long long t, long long total, long l
   return ((t + 1) * n - 1) / total;
 }
 
+// A place in a CTA's range: tile `tile` of unit (b, u), at position v of the range.
 template <class C>
 struct Cursor {
-  int b, u, tile, nt, len;
+  int b, u, tile, nt, len, v;
   __device__ __forceinline__ void next(const PgParams& p) {
+    ++v;
     if (++tile < nt) return;
+    v += PG_END;
     tile = 0;
     if (++u < p.U) return;
     u = 0;
     do {
-      if (++b >= p.B) {  // past the last unit: nothing is read through it
-        nt = 0x7fffffff;
-        len = 0;
+      if (++b >= p.B) {  // past the last unit, and so past every range
+        v = 0x7fffffff;
         return;
       }
       nt = seq_tiles<C::TILE>(p, b, &len);
@@ -116,6 +121,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   constexpr int NP = KW / RPP;      // copies of K (and of V) a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
+  griddep_wait();
 
   // ---- plan: total tiles, this CTA's range, the unit it starts in
   long long* plan = reinterpret_cast<long long*>(smem + C::OFF_PLAN);  // [0..3] warp sums, [4] tiles before, [5] b
@@ -123,7 +129,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
   long long mine = 0;
   int len_tmp;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles<C::TILE>(p, b, &len_tmp);
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int nt = seq_tiles<C::TILE>(p, b, &len_tmp);
+    if (nt > 0) mine += nt + PG_END;
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -160,7 +169,8 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     long long before = (incl - mine) * p.U;
     if (t0 >= before && t0 < incl * p.U) {
       for (int b = b_lo;; ++b) {
-        const long long nt = static_cast<long long>(seq_tiles<C::TILE>(p, b, &len_tmp)) * p.U;
+        const int tiles = seq_tiles<C::TILE>(p, b, &len_tmp);
+        const long long nt = tiles > 0 ? static_cast<long long>(tiles + PG_END) * p.U : 0;
         if (t0 < before + nt) {
           plan[4] = before;
           plan[5] = b;
@@ -174,22 +184,29 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   Cursor<C> cur;
   cur.b = static_cast<int>(plan[5]);
   cur.nt = seq_tiles<C::TILE>(p, cur.b, &cur.len);
-  cur.u = static_cast<int>((t0 - plan[4]) / cur.nt);
-  cur.tile = static_cast<int>((t0 - plan[4]) % cur.nt);
-  const int steps = static_cast<int>(t1 - t0);
+  cur.u = static_cast<int>((t0 - plan[4]) / (cur.nt + PG_END));
+  cur.tile = static_cast<int>((t0 - plan[4]) % (cur.nt + PG_END));
+  cur.v = 0;
+  const int range = static_cast<int>(t1 - t0);
+  if (cur.tile >= cur.nt) {  // the range begins behind a unit's last tile
+    cur.v = cur.nt - 1 - cur.tile;
+    cur.tile = cur.nt - 1;
+    cur.next(p);
+  }
+  if (cur.v >= range) return;  // no tile of its own (the whole CTA)
 
   // ---- loads: `ld` is the step whose pages are being looked up; lane r holds the page of key r of its KW
   const uint32_t ring = smem_u32(smem) + warp * S * C::STAGE_BYTES;
   Cursor<C> ld = cur;
-  int ld_step = 0, ld_stage = 0;
+  int ld_stage = 0;
   const int r_l = lane % KW;
   int pid = 0;
   auto lookup = [&]() {
     const int key = ld.tile * C::TILE + warp * KW + r_l;
-    if (ld_step < steps && key < ld.len) pid = __ldg(p.table + ld.b * p.table_stride + key / p.page_size);
+    if (ld.v < range && key < ld.len) pid = __ldg(p.table + ld.b * p.table_stride + key / p.page_size);
   };
-  auto load_step = [&]() {  // copies of step ld_step into ring stage ld_stage, then the next step's lookup
-    if (ld_step < steps) {
+  auto load_step = [&]() {  // copies of step ld into ring stage ld_stage, then the next step's lookup
+    if (ld.v < range) {
       const int key = ld.tile * C::TILE + warp * KW + r_l;
       long long off = -1;  // zeros
       if (key < ld.len) {
@@ -216,9 +233,8 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
       }
     }
     cp_async_commit();
-    ++ld_step;
     ld_stage = ld_stage + 1 == S ? 0 : ld_stage + 1;
-    if (ld_step < steps) {
+    if (ld.v < range) {
       ld.next(p);
       lookup();
     }
@@ -291,7 +307,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   bool first_unit = true;
   int stage = 0;
 
-  for (int step = 0; step < steps; ++step) {
+  while (cur.v < range) {
     cp_async_wait<S - 1>();
     __syncwarp();
     const uint32_t st = ring + stage * C::STAGE_BYTES;
@@ -374,14 +390,12 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     __syncwarp();  // every lane has read the stage
 
     const bool unit_ends = cur.tile + 1 == cur.nt;
-    if (unit_ends || step + 1 == steps) {
+    Cursor<C> nx = cur;
+    nx.next(p);
+    if (unit_ends || nx.v >= range) {
       // ---- the unit's part in this CTA ends: merge the warps' states
-      Cursor<C> nx = cur;
-      const bool more = step + 1 < steps;
-      if (more) {
-        nx.next(p);
-        fetch_q(nx.b, nx.u);  // in flight during the merge
-      }
+      const bool more = nx.v < range;
+      if (more) fetch_q(nx.b, nx.u);  // in flight during the merge
       float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -401,6 +415,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          if (mt * 16 + r * 8 >= rows) continue;  // no queries in these eight rows
           const int row = mt * 16 + r * 8 + (lane >> 2);
           float M = -INFINITY;
 #pragma unroll
@@ -453,7 +468,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
         __syncthreads();
       }
       if (!unit_ends && seg_tile0 == 0 && threadIdx.x == 0) {  // begun here, ended by a later CTA
-        const long long last = t1 - (cur.tile + 1) + cur.nt - 1;
+        const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
         p.joins[blockIdx.x] = make_int4(cur.b, cur.u, slot & 1, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
       }
       first_unit = false;
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     }
     load_step();  // into the stage just read
     stage = stage + 1 == S ? 0 : stage + 1;
-    if (step + 1 < steps) cur.next(p);
+    cur = nx;
   }
   cp_async_wait<0>();
 }
@@ -591,9 +606,8 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.joins = reinterpret_cast<int4*>(a.ws + pl.joins);
   cudaError_t e = cudaFuncSetAttribute(fa_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  fa_paged_kernel<C><<<static_cast<unsigned>(pl.n_cta), 32 * C::NW, C::SMEM, a.stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // a programmatic dependent: its launch overlaps the first kernel
+  // programmatic dependents: a launch overlaps the end of the kernel before it
+  if ((e = launch_dependent(fa_paged_kernel<C>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
   return launch_dependent(fa_paged_join_kernel<C::D, C::GR>, dim3(pl.n_cta, p.G < C::GR ? p.G : C::GR), 32 * PJ_WARPS, 0,
                           a.stream, p);
 }
