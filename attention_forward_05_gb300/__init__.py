@@ -28,7 +28,7 @@ Entry points (same names as the C ABI):
       -> (o, lse)
   fa_decode_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None,
                          workspace=None, with_lse=False) -> (o, lse)
-  fa_decode_paged_workspace_bytes(B, H, Hkv, d, prefix_len=0)
+  fa_decode_paged_workspace_bytes(B, H, Hkv, d, page_size, prefix_len=0)
   fa_check_device_error()
 """
 from __future__ import annotations
@@ -104,7 +104,7 @@ def lib() -> ctypes.CDLL:
             L.fa_decode_paged_prefix.argtypes = [vp, vp, vp, vp, vp, i, vp, ll, vp, i, i, i, i, i, i, i, vp, f, vp, sz,
                                                  vp, vp]
             L.fa_decode_paged_prefix.restype = i
-            L.fa_decode_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+            L.fa_decode_paged_workspace_bytes.argtypes = [i, i, i, i, i, i]
             L.fa_decode_paged_workspace_bytes.restype = sz
             L.fa_check_device_error.argtypes = []
             L.fa_check_device_error.restype = i
@@ -603,8 +603,8 @@ def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     return q_out
 
 
-def fa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int, prefix_len: int = 0) -> int:
-    return int(lib().fa_decode_paged_workspace_bytes(B, H, Hkv, d, int(prefix_len)))
+def fa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int, page_size: int, prefix_len: int = 0) -> int:
+    return int(lib().fa_decode_paged_workspace_bytes(B, H, Hkv, d, int(page_size), int(prefix_len)))
 
 
 def _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale, workspace, with_lse, o,
@@ -640,7 +640,7 @@ def _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq
             o = torch.empty((B, H, d), device=q.device, dtype=torch.bfloat16)
         lse = torch.empty((B, H), device=q.device, dtype=torch.float32) if with_lse else None
         if workspace is None:
-            need = L.fa_decode_paged_workspace_bytes(B, H, Hkv, d, prefix_len)
+            need = L.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, prefix_len)
             workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
     if o.dtype != torch.bfloat16 or o.numel() != B * H * d or not o.is_contiguous():
         raise ValueError("o must be contiguous bf16 [B,H,d]")

@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <utility>
 
 #include "fa.h"
 #include "fa_internal.h"
@@ -109,6 +110,39 @@ int encode_map(CUtensorMap* map, const void* base, bool bf16, int BH, int rows, 
   }
   return FA_OK;
 }
+
+}  // namespace
+
+namespace fa {
+
+cudaError_t encode_paged_map(CUtensorMap* map, const void* base, int d, int page_size, int Hkv, int num_pages,
+                             long long c_row, long long c_head, long long c_page, int box_rows, int heads_inner) {
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(Hkv),
+                        static_cast<cuuint64_t>(num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c_row) * 2, static_cast<cuuint64_t>(c_head) * 2,
+                           static_cast<cuuint64_t>(c_page) * 2};
+  for (int i = 0; i < 3; ++i)
+    if (dims[i + 1] == 1) strides[i] = static_cast<cuuint64_t>(d) * 2;  // never stepped over; must not be 0
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  if (heads_inner) {
+    std::swap(dims[1], dims[2]);
+    std::swap(strides[0], strides[1]);
+    std::swap(box[1], box[2]);
+  }
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda = 100000 + static_cast<int>(r);
+    return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace fa
+
+namespace {
 
 constexpr long long kMaxElems = 1LL << 40;
 

@@ -42,7 +42,10 @@
 
 namespace fa {
 
-template <typename T, int D_, int BC_, int NQT_, int STAGES_, int MINB_ = 1, bool PV2_ = false>
+struct FwdParams;
+struct FwdPagedParams;
+
+template <typename T, int D_, int BC_, int NQT_, int STAGES_, int MINB_ = 1, bool PV2_ = false, bool PAGED_ = false>
 struct FwdCfg {
   using Elem = T;
   static constexpr int D = D_;
@@ -53,6 +56,10 @@ struct FwdCfg {
   // PV2: the softmax hands over P in two halves (key columns [0, BC/2) first), and P V of the first
   // half is issued while the second half is still being exponentiated.
   static constexpr bool PV2 = PV2_;
+  // PAGED: keys and values come out of the pages of a cache, the query rows of a key/value head are the
+  // (sequence, head of the group) pairs of a decode batch, and every CTA leaves partial states (FwdPagedParams).
+  static constexpr bool PAGED = PAGED_;
+  using Params = std::conditional_t<PAGED_, FwdPagedParams, FwdParams>;
   static constexpr int BR = 128;
   static constexpr int ESZ = static_cast<int>(sizeof(T));
   static constexpr bool TF32 = (ESZ == 4);
@@ -72,12 +79,13 @@ struct FwdCfg {
   static constexpr int OFF_K = OFF_Q + NQT * Q_BYTES;
   static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
-  // barriers: q_full, k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[NQT], p_full[NQT], o_done[NQT], drain
-  static constexpr int NBAR = 1 + 4 * STAGES + 4 * NQT + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot (4 B) + abort flag (4 B)
+  // barriers: q_full, k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[NQT], p_full[NQT], o_done[NQT], drain,
+  // first half of P [NQT], and (PAGED) the copy of the last, ragged value tile
+  static constexpr int NBAR = 1 + 4 * STAGES + 4 * NQT + 1 + (PAGED ? 1 : 0);
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot (4 B), abort flag (4 B), (PAGED) bad page flag (4 B)
   // Key-split CTAs (FwdParams::ks_half) exist for the two-tile bf16 configuration without the two-half
   // hand-over; their tile slot 1 leaves its rows' (m, l) here for the merge.
-  static constexpr bool KS = NQT == 2 && !TF32 && !PV2;
+  static constexpr bool KS = NQT == 2 && !TF32 && !PV2 && !PAGED;
   static constexpr int OFF_ML = OFF_MISC + 16;
   static constexpr int ML_BYTES = KS ? BR * 8 : 0;
   static constexpr int SMEM_BYTES = OFF_ML + ML_BYTES + 1024;  // + slack to align the base to 1024
@@ -130,8 +138,20 @@ struct FwdParams {
   int n_whole, ks_tile0, ks_half;
 };
 
+// PAGED: head bh of the grid is key/value head bh of the cache, its query rows r = (sequence r / G, head bh * G + r % G)
+// of q [B, H, D] (Nq = B * G), its keys the rows of the listed pages in order (Nk of them).  tm_k and tm_v are 4-D maps
+// (D, page_size, Hkv, num_pages), or (D, Hkv, page_size, num_pages) with heads_inner, so that strides ascend; their boxes
+// have box_rows rows: a power of two >= 8 that divides the page size, so a box lies in one page and starts on a
+// swizzle boundary.
+struct FwdPagedParams : FwdParams {
+  const __nv_bfloat16* q;
+  const int* pages;
+  int G, num_pages, page_size, box_rows, heads_inner;
+};
+
 // wait-site identifiers recorded with a timeout
-enum : int { W_Q = 1, W_KF, W_VF, W_KE, W_VE, W_SF, W_PF, W_OD, W_DRAIN_MMA, W_DRAIN_K, W_DRAIN_V };
+enum : int { W_Q = 1, W_KF, W_VF, W_KE, W_VE, W_SF, W_PF, W_OD, W_DRAIN_MMA, W_DRAIN_K, W_DRAIN_V, W_TAIL };
+enum : int { W_PREFIX_PAGE = 0x38 };  // recorded with DEV_BAD_INDEX
 
 // Row maximum (MAX) or minimum of the BC scores a thread holds: 4 independent
 // chains over groups of 8 elements, two new elements per 3-input max/min.
@@ -210,7 +230,7 @@ __device__ __forceinline__ void tmem_st16_lo(uint32_t taddr, const uint32_t (&r)
 template <class C>
 __global__ void __maxnreg__(C::MAXREG)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+                  const __grid_constant__ CUtensorMap tm_v, const typename C::Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -276,9 +296,15 @@ __global__ void __maxnreg__(C::MAXREG)
   auto bar_ph = [&](int t) { return bar0 + 8u * (2 + 4 * C::STAGES + 3 * C::NQT + t); };  // first half of P
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* bad_page = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);            // PAGED
+  const uint32_t bar_tail = bar0 + 8u * (2 + 4 * C::STAGES + 4 * C::NQT);                        // PAGED
 
   if (threadIdx.x == 0) {
-    mbar_init(bar_q, 1);
+    mbar_init(bar_q, C::PAGED ? 4 * C::NQT : 1);  // PAGED: the softmax warps bring in Q
+    if constexpr (C::PAGED) {
+      mbar_init(bar_tail, 1);
+      *bad_page = 0;
+    }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar_kf(s), 1);
       mbar_init(bar_vf(s), 1);
@@ -298,7 +324,7 @@ __global__ void __maxnreg__(C::MAXREG)
   if (warp == C::LOAD_WARP) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
+      if (!C::PAGED) tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -314,7 +340,76 @@ __global__ void __maxnreg__(C::MAXREG)
   griddep_wait();
   griddep_launch_dependents();
 
-  if (warp == C::LOAD_WARP) {
+  if (C::PAGED && warp == C::LOAD_WARP) {
+    if constexpr (C::PAGED) {
+      // ------------------------------------------------------------ TMA producer, paged
+      // Lane i copies the i-th box of a tile, from the page that it looked up one tile ahead.  Boxes past the last key
+      // and boxes of a bad page are read past the cache's last page: zeros.  The rows of the last page behind the last
+      // key hold anything: as keys they are masked, as values the warp zeroes them in shared memory (0 * NaN would
+      // reach O) and hands the tile over itself.
+      const int boxes = C::BC / p.box_rows;
+      int nk_done = 0, nv_done = 0;
+      bool tail_done = false;
+      auto page_of = [&](int j) {
+        const int key = k_begin + j * C::BC + lane * p.box_rows;
+        if (lane >= boxes || j >= T || key >= k_end) return p.num_pages;
+        const int pg = __ldg(p.pages + key / p.page_size);
+        if (pg >= 0 && pg < p.num_pages) return pg;
+        *bad_page = 1;
+        record_bad_index(p.err, W_PREFIX_PAGE);
+        return p.num_pages;
+      };
+      int page = page_of(0);
+      for (int j = 0; j < T; ++j) {
+        const int s = j % C::STAGES;
+        const uint32_t ph = ((j / C::STAGES) & 1) ^ 1;
+        const int next_page = page_of(j + 1);
+        const int row = (k_begin + j * C::BC + lane * p.box_rows) % p.page_size;
+        const int left = k_end - (k_begin + j * C::BC);  // keys of this tile and later
+        const bool ragged = left < C::BC;
+        auto copy = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar) {
+          if (lane == 0) mbar_expect_tx(bar, C::KV_BYTES);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int c = 0; c < C::NCH; ++c)
+              tma_load_4d(dst + c * C::KV_CH_BYTES + lane * p.box_rows * 128, tm, bar, c * C::CHUNK, p.heads_inner ? kvh : row,
+                          p.heads_inner ? row : kvh, page);
+          }
+        };
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_ke(s), ph, abort_flag, p.err, W_KE))) break;
+        copy(&tm_k, sbase + C::OFF_K + s * C::KV_BYTES, bar_kf(s));
+        nk_done = j + 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_ve(s), ph, abort_flag, p.err, W_VE))) break;
+        const uint32_t dv = sbase + C::OFF_V + s * C::KV_BYTES;
+        copy(&tm_v, dv, ragged ? bar_tail : bar_vf(s));
+        if (ragged) {  // only the CTA's last tile
+          tail_done = true;
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_tail, 0, abort_flag, p.err, W_TAIL))) break;
+          for (int i = lane; i < (C::BC - left) * C::NCH * 8; i += 32) {
+            const int piece = i % 8, c = i / 8 % C::NCH, r = left + i / (8 * C::NCH);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dv + c * C::KV_CH_BYTES + r * 128 + piece * 16),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_vf(s));
+        }
+        nv_done = j + 1;
+        page = next_page;
+      }
+      if (lane == 0) {  // every copy issued must land before the CTA exits
+        if (tail_done) mbar_wait_drain(bar_tail, 0, p.err, W_DRAIN_V);
+        for (int s = 0; s < C::STAGES; ++s) {
+          const int nks = (nk_done > s) ? (nk_done - 1 - s) / C::STAGES + 1 : 0;
+          const int nvs = (nv_done > s) ? (nv_done - 1 - s) / C::STAGES + 1 : 0;
+          if (nks > 0) mbar_wait_drain(bar_kf(s), (nks - 1) & 1, p.err, W_DRAIN_K);
+          if (nvs > 0) mbar_wait_drain(bar_vf(s), (nvs - 1) & 1, p.err, W_DRAIN_V);
+        }
+      }
+    }
+  } else if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && T > 0) {
       int nk_done = 0, nv_done = 0;  // key tiles whose K (resp. V) copy was issued: tiles 0 .. n-1
@@ -560,6 +655,26 @@ __global__ void __maxnreg__(C::MAXREG)
     const int t = warp >> 2;
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
+    if constexpr (C::PAGED) {
+      // This warp's 32 rows of Q into the swizzled tile, 16 bytes a lane; rows past the last query are zeros.
+      constexpr int PIECES = C::D / 8;         // 16-byte pieces of a row
+      constexpr int RP = 32 / PIECES;          // rows at a time
+#pragma unroll
+      for (int i = 0; i < 32 / RP; ++i) {
+        const int r = wq * 32 + i * RP + lane / PIECES, pc = lane % PIECES;
+        const int qrow = q0 + t * C::BR + r;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (qrow < p.Nq) {
+          const long long head = static_cast<long long>(qrow / p.G) * p.Hkv * p.G + bh * p.G + qrow % p.G;
+          w = *reinterpret_cast<const uint4*>(p.q + head * C::D + pc * 8);
+        }
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + t * C::Q_BYTES + pc / 8 * C::Q_CH_BYTES + r * 128 +
+                                  ((pc % 8 ^ (r & 7)) << 4)) = w;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q);
+    }
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_base + t * C::BC;
     const uint32_t tP = tmem + lane_base + t * C::BC;
@@ -916,7 +1031,7 @@ __global__ void __maxnreg__(C::MAXREG)
         for (int c4 = 0; c4 < C::OCOLS / 4; ++c4) reinterpret_cast<uint4*>(wrow)[c4] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<float2*>(p.ws_ml)[srow] = make_float2(-INFINITY, 0.f);
       }
-    } else if (ok && p.n_split > 1) {  // partial state (m, l, unnormalised O) of this key range, for the merge
+    } else if (ok && (C::PAGED || p.n_split > 1)) {  // partial state (m, l, unnormalised O) of this key range, for the merge
       tc_fence_after();
       const int qrow = q0 + t * trow + row;
       const bool in_range = qrow < p.Nq;
@@ -934,6 +1049,7 @@ __global__ void __maxnreg__(C::MAXREG)
           for (int v4 = 0; v4 < 8; ++v4) dst[v4] = make_uint4(orr[4 * v4], orr[4 * v4 + 1], orr[4 * v4 + 2], orr[4 * v4 + 3]);
         }
       }
+      if (C::PAGED && *bad_page) l = __int_as_float(0x7fc00000);  // set before the tile's copy, which o_done follows
       if (in_range) reinterpret_cast<float2*>(p.ws_ml)[srow] = make_float2(m_ref, l);
     } else if (ok) {
       tc_fence_after();
@@ -993,7 +1109,18 @@ cudaError_t launch_fwd(const FwdLaunch& a) {
   cudaError_t e = cudaFuncSetAttribute(fa_fwd_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  FwdParams p;
+  typename C::Params p;
+  if constexpr (C::PAGED) {
+    p.q = static_cast<const __nv_bfloat16*>(a.paged_q);
+    p.pages = a.pages;
+    p.G = a.G;
+    p.num_pages = a.num_pages;
+    p.page_size = a.page_size;
+    p.box_rows = a.box_rows;
+    p.heads_inner = a.heads_inner;
+    if (a.box_rows < 8 || C::BC % a.box_rows != 0 || a.page_size % a.box_rows != 0 || C::BC / a.box_rows > 32)
+      return cudaErrorInvalidValue;
+  }
   p.o = a.o;
   p.lse = a.lse;
   p.err = a.err;

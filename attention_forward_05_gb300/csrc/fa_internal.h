@@ -119,14 +119,19 @@ struct PagedLaunch {
   int sms;
   cudaStream_t stream;
 };
-// Workspace layout (byte offsets) of a paged decode with G query heads a key/value head.
+// Work split and workspace layout (byte offsets) of a paged decode.
 struct PagedPlan {
-  int n_cta = 0;
-  size_t part_ml = 0, part_o = 0, joins = 0, total = 0;
+  int n_cta = 0;                                      // CTAs that share the sequences' own keys
+  size_t part_ml = 0, part_o = 0, joins = 0;          // states of units shared by CTAs (fa_paged.cu)
+  // with a shared prefix:
+  int n_split = 0, kv_per_split = 0, wide = 0;        // the prefix's key splits; wide: two query tiles per CTA
+  size_t pre_ml = 0, pre_o = 0, unit_ml = 0, unit_o = 0, infos = 0;
+  int gather_len = 0, gather_rows = 0;                // pages (of gather_rows rows) the prefix is first copied into; 0: none
+  size_t gather_k = 0, gather_v = 0, gather_pages = 0;
+  size_t total = 0;
 };
-PagedPlan paged_plan(int G, int d, int sms);
-cudaError_t launch_decode_paged(const PagedLaunch& a);
-cudaError_t launch_decode_prefix(const PagedLaunch& a);
+PagedPlan paged_plan(int B, int H, int Hkv, int d, int page_size, int prefix_len, int sms);
+cudaError_t launch_decode_paged(const PagedLaunch& a, const PagedPlan& pl);
 
 struct FwdLaunch {
   const CUtensorMap* tm_q;  // 3-D maps over [B*H, N, d] (innermost d), 128-byte swizzle
@@ -152,6 +157,10 @@ struct FwdLaunch {
   // ks_tile0 .. of the head-major list of 128-row tiles), whose two tile slots take the keys [0, ks_half)
   // and [ks_half, Nk) and merge (fa_fwd_kernel.cuh, FwdParams).
   int ks_whole = 0, ks_tile0 = 0, ks_count = 0, ks_half = 0;
+  // Paged keys and a decode batch's queries (fa_fwd_kernel.cuh, FwdPagedParams); tm_q is not used.
+  const void* paged_q = nullptr;  // [B, Hkv * G, d]
+  const int* pages = nullptr;
+  int G = 0, num_pages = 0, page_size = 0, box_rows = 0, heads_inner = 0;
 };
 
 // Tile geometry the tensor maps must be encoded with, per instantiation.
@@ -185,6 +194,16 @@ cudaError_t launch_fwd_fp32_d128(const FwdLaunch& a);
 // `sms`: the device's SM count (picks the d = 64 configuration whose CTAs start in one wave, if any)
 cudaError_t launch_fwd_decode(const FwdLaunch& a, int d, int sms);
 FwdGeometry fwd_geometry_decode(int d);
+
+// Attention of all a decode batch's queries over the shared prefix's pages (fa_paged_prefix.cu): partial states
+// [n_split][Hkv][B * G] into the workspace.
+void plan_prefix(int B, int G, int Hkv, int d, int page_size, int prefix_len, int sms, PagedPlan* pl);
+cudaError_t launch_prefix(const PagedLaunch& a, const PagedPlan& pl);
+
+// 4-D tensor map over a paged cache: dims (d, page_size, Hkv, num_pages) with boxes of (64, box_rows, 1, 1), or with
+// rows and heads exchanged (heads_inner); 128-byte swizzle.
+cudaError_t encode_paged_map(CUtensorMap* map, const void* base, int d, int page_size, int Hkv, int num_pages,
+                             long long c_row, long long c_head, long long c_page, int box_rows, int heads_inner);
 
 struct BwdLaunch {
   // maps for the dK/dV kernel: K, V boxes (64 cols, kv_keys rows); Q, dO boxes (64 cols, kv_qrows rows)

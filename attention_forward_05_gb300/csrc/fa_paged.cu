@@ -70,6 +70,15 @@ struct PgParams {
   int* err;
   float* part_ml;                 // float2 (m, l) [2 * n_cta][GR] of the CTAs' first (0) and last (1) unfinished units
   float* part_o;                  // [2 * n_cta][GR][D] unnormalised
+  // with a shared prefix every unit's own state stays a state for fa_paged_finish_kernel:
+  int prefix;                     // 1: so
+  float* unit_ml;                 // float2 [B * H]: units that one CTA covers
+  float* unit_o;                  // [B * H][D]
+  int2* infos;                    // [B * U]: slot of the unit's first part (-1: in unit_ml / unit_o), and its parts (0: no own
+                                  // keys; -1: an unused place; -2: a bad length)
+  const float* pre_ml;            // float2 [pre_split][Hkv][B * G] of the prefix
+  const float* pre_o;
+  int pre_split;
   int4* joins;                    // [n_cta]: the unit (b, u) that starts in this CTA and ends in a later one, the slot of
                                   // its first part (0 or 1), and its parts (0: there is none)
 };
@@ -121,7 +130,9 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   constexpr int NP = KW / RPP;      // copies of K (and of V) a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
-  griddep_wait();
+  // After the prefix's kernel, which waited for everything before it and whose states this kernel does not read, it
+  // may run beside that kernel; each CTA then waits at its end, so that this grid's completion implies that one's.
+  if (!p.prefix) griddep_wait();
 
   // ---- plan: total tiles, this CTA's range, the unit it starts in
   long long* plan = reinterpret_cast<long long*>(smem + C::OFF_PLAN);  // [0..3] warp sums, [4] tiles before, [5] b
@@ -154,6 +165,11 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     if (seq_tiles<C::TILE>(p, b, &len) > 0) continue;
     const bool bad = len > 0;
     if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
+    if (p.prefix) {
+      for (int u = threadIdx.x; u < p.U; u += 32 * NW)
+        p.infos[static_cast<long long>(b) * p.U + u] = make_int2(-1, bad ? -2 : len < 0 ? -1 : 0);
+      continue;
+    }
     const long long row0 = static_cast<long long>(b) * p.H;
     for (int e = threadIdx.x; e < p.H * CPR; e += 32 * NW)
       reinterpret_cast<uint4*>(p.o + row0 * D)[e] = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
@@ -163,7 +179,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   }
   const long long n = cta_count(total, p.n_cta);
   if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (static_cast<long long>(blockIdx.x) >= n) return;  // the whole CTA (n = 0 without keys)
+  auto leave = [&]() {
+    if (p.prefix) griddep_wait();
+  };
+  if (static_cast<long long>(blockIdx.x) >= n) return leave();  // the whole CTA (n = 0 without keys)
   const long long t0 = cta_first(blockIdx.x, total, n), t1 = cta_first(blockIdx.x + 1, total, n);
   {
     long long before = (incl - mine) * p.U;
@@ -193,7 +212,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     cur.tile = cur.nt - 1;
     cur.next(p);
   }
-  if (cur.v >= range) return;  // no tile of its own (the whole CTA)
+  if (cur.v >= range) return leave();  // no tile of its own (the whole CTA)
 
   // ---- loads: `ld` is the step whose pages are being looked up; lane r holds the page of key r of its KW
   const uint32_t ring = smem_u32(smem) + warp * S * C::STAGE_BYTES;
@@ -453,7 +472,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
               acc.w += y.w;
             }
             const long long head = static_cast<long long>(cur.b) * p.H + h0 + grow;
-            if (whole) {
+            if (whole && p.prefix) {
+              *reinterpret_cast<float4*>(p.unit_o + head * D + pc * 4) = acc;
+              if (pc == 0) reinterpret_cast<float2*>(p.unit_ml)[head] = make_float2(M, L);
+            } else if (whole) {
               const float inv = 1.f / L;
               *reinterpret_cast<uint2*>(p.o + head * D + pc * 4) =
                   make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -467,9 +489,11 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
         }
         __syncthreads();
       }
-      if (!unit_ends && seg_tile0 == 0 && threadIdx.x == 0) {  // begun here, ended by a later CTA
+      if (seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
         const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
-        p.joins[blockIdx.x] = make_int4(cur.b, cur.u, slot & 1, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
+        const int parts = static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1);
+        if (p.prefix) p.infos[static_cast<long long>(cur.b) * p.U + cur.u] = make_int2(whole ? -1 : slot, parts);
+        else if (!whole) p.joins[blockIdx.x] = make_int4(cur.b, cur.u, slot & 1, parts);
       }
       first_unit = false;
       if (more) {
@@ -485,6 +509,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     cur = nx;
   }
   cp_async_wait<0>();
+  leave();
 }
 
 // Joins the parts of a unit that several CTAs share: M = max m_s, then l and O add up with weights 2^(m_s - M).
@@ -560,18 +585,122 @@ __global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgPa
   if (p.lse != nullptr && threadIdx.x == 0) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// With a shared prefix: joins the prefix's states of a query with its own, and writes the output.  One warp per
+// (sequence, query head), eight states' rows in flight; states add up in key order (prefix splits, then own parts).
+constexpr int PF_WARPS = 4;
+template <int D, int GR>
+__global__ void __launch_bounds__(32 * PF_WARPS) fa_paged_finish_kernel(const PgParams p) {
+  constexpr int E = D / 32;
+  griddep_wait();
+  const long long head = static_cast<long long>(blockIdx.x) * PF_WARPS + (threadIdx.x >> 5);
+  if (head >= static_cast<long long>(p.B) * p.H) return;
+  const int lane = threadIdx.x & 31;
+  const int b = static_cast<int>(head / p.H), h = static_cast<int>(head % p.H);
+  const int hk = h / p.G, g = h % p.G;
+  const int2 info = p.infos[static_cast<long long>(b) * p.U + hk * p.ngrp + g / GR];
+  const int row = g % GR;
+  const long long pstep = static_cast<long long>(p.B) * p.H;
+  const long long prow = (static_cast<long long>(hk) * p.B + b) * p.G + g;
+  const int pre = info.y < 0 ? 0 : p.pre_split;
+  const int parts = info.y < 0 ? 0 : pre + info.y;
+  auto state = [&](int s, const float2** ml, const float** o) {
+    if (s < pre) {
+      *ml = reinterpret_cast<const float2*>(p.pre_ml) + s * pstep + prow;
+      *o = p.pre_o + (s * pstep + prow) * D;
+    } else if (info.x < 0) {
+      *ml = reinterpret_cast<const float2*>(p.unit_ml) + head;
+      *o = p.unit_o + head * D;
+    } else {  // the first part's slot, then slot 0 of the CTAs after that one
+      const long long at = static_cast<long long>(s == pre ? info.x : 2 * (info.x / 2 + s - pre)) * GR + row;
+      *ml = reinterpret_cast<const float2*>(p.part_ml) + at;
+      *o = p.part_o + at * D;
+    }
+  };
+  float M = -INFINITY;
+  for (int s = lane; s < parts; s += 32) {
+    const float2* ml;
+    const float* o;
+    state(s, &ml, &o);
+    M = fmaxf(M, ml->x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += 8) {
+    float2 x[8];
+    float v[8][E];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+      if (s0 + i < parts) {
+        const float2* ml;
+        const float* o;
+        state(s0 + i, &ml, &o);
+        x[i] = *ml;
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(o + lane * E);
+          v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(o + lane * E);
+          v[i][0] = y.x, v[i][1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s0 + i < parts) {
+        const float w = x[i].x == -INFINITY ? 1.f : ex2_approx(x[i].x - M);  // an empty state is (-inf, 0, 0)
+        L = fmaf(x[i].y, w, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
+      }
+    }
+  }
+  const float nan = __int_as_float(0x7fc00000);
+  const float inv = info.y == -2 ? nan : parts == 0 ? 0.f : 1.f / L;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.o + head * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse != nullptr && lane == 0)
+    p.lse[head] = info.y == -2 ? nan : parts == 0 ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
 namespace {
 
 constexpr size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 template <class C>
-PagedPlan plan_of(int sms) {
+PagedPlan plan_of(int B, int H, int Hkv, int page_size, int prefix_len, int sms) {
   PagedPlan pl;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
   pl.n_cta = sms * C::CTAS;
-  pl.part_ml = 0;
-  pl.part_o = round256(static_cast<size_t>(2) * pl.n_cta * C::GR * 8);
-  pl.joins = pl.part_o + round256(static_cast<size_t>(2) * pl.n_cta * C::GR * C::D * 4);
-  pl.total = pl.joins + round256(static_cast<size_t>(pl.n_cta) * 16);
+  const size_t slots = static_cast<size_t>(2) * pl.n_cta, heads = static_cast<size_t>(B) * H;
+  pl.part_ml = take(slots * C::GR * 8);
+  pl.part_o = take(slots * C::GR * C::D * 4);
+  pl.joins = take(static_cast<size_t>(pl.n_cta) * 16);
+  if (prefix_len > 0) {
+    const int G = H / Hkv;
+    plan_prefix(B, G, Hkv, C::D, page_size, prefix_len, sms, &pl);
+    pl.pre_ml = take(heads * pl.n_split * 8);
+    pl.pre_o = take(heads * pl.n_split * C::D * 4);
+    pl.unit_ml = take(heads * 8);
+    pl.unit_o = take(heads * C::D * 4);
+    pl.infos = take(static_cast<size_t>(B) * Hkv * ((G + C::GR - 1) / C::GR) * 8);
+    const size_t rows = static_cast<size_t>(pl.gather_len) * pl.gather_rows * Hkv;
+    pl.gather_k = take(rows * C::D * 2);
+    pl.gather_v = take(rows * C::D * 2);
+    pl.gather_pages = take(static_cast<size_t>(pl.gather_len) * 4);
+  }
+  pl.total = at;
   return pl;
 }
 
@@ -606,26 +735,41 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.joins = reinterpret_cast<int4*>(a.ws + pl.joins);
   cudaError_t e = cudaFuncSetAttribute(fa_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  if (a.prefix_len > 0) {
+    p.prefix = 1;
+    p.unit_ml = reinterpret_cast<float*>(a.ws + pl.unit_ml);
+    p.unit_o = reinterpret_cast<float*>(a.ws + pl.unit_o);
+    p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
+    p.pre_ml = reinterpret_cast<const float*>(a.ws + pl.pre_ml);
+    p.pre_o = reinterpret_cast<const float*>(a.ws + pl.pre_o);
+    p.pre_split = pl.n_split;
+    if ((e = launch_prefix(a, pl)) != cudaSuccess) return e;
+  }
   // programmatic dependents: a launch overlaps the end of the kernel before it
   if ((e = launch_dependent(fa_paged_kernel<C>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
+  if (a.prefix_len > 0)
+    return launch_dependent(fa_paged_finish_kernel<C::D, C::GR>, (a.B * a.H + PF_WARPS - 1) / PF_WARPS, 32 * PF_WARPS, 0,
+                            a.stream, p);
   return launch_dependent(fa_paged_join_kernel<C::D, C::GR>, dim3(pl.n_cta, p.G < C::GR ? p.G : C::GR), 32 * PJ_WARPS, 0,
                           a.stream, p);
 }
 
-}  // namespace
-
 // Groups of more than 16 query heads take two 16-row tiles a unit (K and V are then read once for 32 heads);
 // larger ones several units of 32.
-PagedPlan paged_plan(int G, int d, int sms) {
-  if (d == 64) return G <= 16 ? plan_of<PgCfg<64, 1>>(sms) : plan_of<PgCfg<64, 2>>(sms);
-  return G <= 16 ? plan_of<PgCfg<128, 1>>(sms) : plan_of<PgCfg<128, 2>>(sms);
+template <typename F>
+auto with_config(int G, int d, F&& f) {
+  if (d == 64) return G <= 16 ? f(PgCfg<64, 1>{}) : f(PgCfg<64, 2>{});
+  return G <= 16 ? f(PgCfg<128, 1>{}) : f(PgCfg<128, 2>{});
 }
 
-cudaError_t launch_decode_paged(const PagedLaunch& a) {
-  const int G = a.H / a.Hkv;
-  const PagedPlan pl = paged_plan(G, a.d, a.sms);
-  if (a.d == 64) return G <= 16 ? launch_paged<PgCfg<64, 1>>(a, pl) : launch_paged<PgCfg<64, 2>>(a, pl);
-  return G <= 16 ? launch_paged<PgCfg<128, 1>>(a, pl) : launch_paged<PgCfg<128, 2>>(a, pl);
+}  // namespace
+
+PagedPlan paged_plan(int B, int H, int Hkv, int d, int page_size, int prefix_len, int sms) {
+  return with_config(H / Hkv, d, [&](auto c) { return plan_of<decltype(c)>(B, H, Hkv, page_size, prefix_len, sms); });
+}
+
+cudaError_t launch_decode_paged(const PagedLaunch& a, const PagedPlan& pl) {
+  return with_config(a.H / a.Hkv, a.d, [&](auto c) { return launch_paged<decltype(c)>(a, pl); });
 }
 
 }  // namespace fa

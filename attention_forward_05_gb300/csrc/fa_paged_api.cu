@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr long long kMaxElems = 1LL << 40;
+constexpr long long kMaxElems = 1LL << 38;  // strides in bytes stay below the tensor maps' 2^40
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -20,6 +20,11 @@ bool good_strides(const long long* s, int n, int unit) {
   for (int i = 0; i < n; ++i)
     if (s[i] < 0 || s[i] > kMaxElems || s[i] % unit != 0) return false;
   return true;
+}
+
+// Strides of a cache: good_strides, and no dimension of several entries that stands still.
+bool good_cache(const long long* c, int num_pages, int Hkv, int page_size) {
+  return good_strides(c, 3, 8) && (c[0] > 0 || num_pages == 1) && (c[1] > 0 || Hkv == 1) && (c[2] > 0 || page_size == 1);
 }
 
 // Arguments of a rotation; rot = 0 (no rotation) is the caller's business.
@@ -114,7 +119,7 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
   c[0] = cache_strides ? cache_strides[0] : static_cast<long long>(Hkv) * page_size * d;
   c[1] = cache_strides ? cache_strides[1] : static_cast<long long>(page_size) * d;
   c[2] = cache_strides ? cache_strides[2] : d;
-  if (!good_strides(s, 6, 8) || !good_strides(c, 3, 8)) return FA_ERR_INVALID_ARG;
+  if (!good_strides(s, 6, 8) || !good_cache(c, num_pages, Hkv, page_size)) return FA_ERR_INVALID_ARG;
   fa::AppendLaunch a;
   const int rc = fa::current_device_info(&a.err, &a.sms);
   if (rc != FA_OK) return rc;
@@ -153,12 +158,14 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
   return e == cudaSuccess ? FA_OK : fa::report_cuda_error(e);
 }
 
-size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int prefix_len) {
-  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || prefix_len < 0 || (d != 64 && d != 128)) return 0;
+size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int page_size, int prefix_len) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || page_size < 1 || prefix_len < 0 || prefix_len >= (1 << 30) ||
+      (d != 64 && d != 128) || static_cast<long long>(B) * H > 0x7FFFFFFFLL / d)
+    return 0;
   int* err = nullptr;
   int sms = 0;
   if (fa::current_device_info(&err, &sms) != FA_OK) return 0;
-  return fa::paged_plan(H / Hkv, d, sms).total;
+  return fa::paged_plan(B, H, Hkv, d, page_size, prefix_len, sms).total;
 }
 
 int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cache, void* o, const int* prefix_pages,
@@ -182,16 +189,16 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   c[0] = cache_strides ? cache_strides[0] : static_cast<long long>(Hkv) * page_size * d;
   c[1] = cache_strides ? cache_strides[1] : static_cast<long long>(page_size) * d;
   c[2] = cache_strides ? cache_strides[2] : d;
-  if (!good_strides(c, 3, 8)) return FA_ERR_INVALID_ARG;
+  if (!good_cache(c, num_pages, Hkv, page_size)) return FA_ERR_INVALID_ARG;
   fa::PagedLaunch a;
   const int rc = fa::current_device_info(&a.err, &a.sms);
   if (rc != FA_OK) return rc;
-  const size_t need = fa::paged_plan(H / Hkv, d, a.sms).total;
-  if (workspace && workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  const fa::PagedPlan plan = fa::paged_plan(B, H, Hkv, d, page_size, prefix_len, a.sms);
+  if (workspace && workspace_bytes < plan.total) return FA_ERR_INVALID_ARG;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   void* ws = workspace;
   if (ws == nullptr) {
-    const cudaError_t ea = cudaMallocAsync(&ws, need, a.stream);
+    const cudaError_t ea = cudaMallocAsync(&ws, plan.total, a.stream);
     if (ea != cudaSuccess) return fa::report_cuda_error(ea);
   }
   a.ws = static_cast<char*>(ws);
@@ -216,7 +223,7 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   a.table_stride = table_stride;
   a.prefix_len = prefix_len;
   a.c = scale * 1.4426950408889634f;
-  cudaError_t e = prefix_len > 0 ? fa::launch_decode_prefix(a) : fa::launch_decode_paged(a);
+  cudaError_t e = fa::launch_decode_paged(a, plan);
   if (workspace == nullptr) {
     const cudaError_t e2 = cudaFreeAsync(ws, a.stream);
     if (e == cudaSuccess) e = e2;

@@ -343,7 +343,7 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
  *   scale      finite score scale.
  *   lse        fp32 [B, H] out (natural log, scaled-score units), or NULL.
  *   workspace  device buffer of at least fa_decode_paged_workspace_bytes(B, H, Hkv,
- *              d, 0) bytes, 16-byte aligned, or NULL to allocate it stream-ordered on
+ *              d, page_size, 0) bytes, 16-byte aligned, or NULL to allocate it stream-ordered on
  *              `stream`.  It needs no clearing; calls that may overlap on the GPU must
  *              not share one.
  * A sequence with a page outside the cache or more keys than max_pages * page_size
@@ -367,7 +367,8 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
  *   prefix_len    >= 0; 0 is fa_decode_paged (prefix_pages may then be NULL).
  *   seq_lens      0 = a sequence that sees the prefix alone; negative = an unused place
  *                 of a padded batch, which sees nothing (o = 0, lse = -inf).
- *   workspace     fa_decode_paged_workspace_bytes(B, H, Hkv, d, prefix_len) bytes.
+ *   workspace     fa_decode_paged_workspace_bytes(B, H, Hkv, d, page_size, prefix_len)
+ *                 bytes.
  * A prefix page outside the cache gives NaN in every sequence that sees the prefix.
  * Other arguments and rules as in fa_decode_paged.
  */
@@ -380,7 +381,7 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
 
 /* Bytes of workspace fa_decode_paged (prefix_len = 0) and fa_decode_paged_prefix need on the current
  * device; 0 on bad arguments or without an sm_103 GPU. */
-size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int prefix_len);
+size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int page_size, int prefix_len);
 
 /*
  * fa_check_device_error -- reads and clears the library's device error word

@@ -121,7 +121,8 @@ def check_decode(q, kc, vc, o, lse, tables, lens, scale, name, prefix=(), prefix
 
 def paged_cache(pages: int, Hkv: int, ps: int, d: int, device, seed: int, layout: str = "head"):
     """(k_cache, v_cache) of shape [pages, Hkv, ps, d], N(0,1).  layout: "head" contiguous; "row" [pages, ps, Hkv, d];
-    "one" both interleaved in one buffer [pages, 2, ps, Hkv, d]."""
+    "one" both interleaved in one buffer [pages, 2, ps, Hkv, d]; "odd" padded rows, heads and pages
+    (strides that are not multiples of one another)."""
     g = torch.Generator(device=device)
     g.manual_seed(seed)
 
@@ -132,6 +133,10 @@ def paged_cache(pages: int, Hkv: int, ps: int, d: int, device, seed: int, layout
         return draw(pages, Hkv, ps, d), draw(pages, Hkv, ps, d)
     if layout == "row":
         return draw(pages, ps, Hkv, d).transpose(1, 2), draw(pages, ps, Hkv, d).transpose(1, 2)
+    if layout == "odd":
+        row, head = d + 8, ps * (d + 8) + 24
+        page = Hkv * head + 40
+        return tuple(draw(pages * page + 64)[16:].as_strided((pages, Hkv, ps, d), (page, head, row, 1)) for _ in range(2))
     both = draw(pages, 2, ps, Hkv, d)
     return both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2)
 

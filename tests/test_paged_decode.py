@@ -60,7 +60,7 @@ def test_groups(cuda_device, d, H, Hkv):
     _check(c, o, lse, f"paged d{d} H{H} Hkv{Hkv}")
 
 
-@pytest.mark.parametrize("layout", ["head", "row", "one"])
+@pytest.mark.parametrize("layout", ["head", "row", "one", "odd"])
 @pytest.mark.parametrize("ps", [1, 5, 8, 16, 24, 64, 100, 256, 1024])
 def test_pages_and_layouts(cuda_device, layout, ps):
     """Page sizes that divide a tile, span several or end inside one; contiguous and strided caches; unused rows and
@@ -183,7 +183,7 @@ def test_prefix(cuda_device, d, B, H, Hkv, ps, prefix_len):
     _check(c, o, lse, f"prefix d{d} B{B} H{H}/{Hkv} ps{ps} P{prefix_len}", seqs=seqs)
 
 
-@pytest.mark.parametrize("layout", ["row", "one"])
+@pytest.mark.parametrize("layout", ["row", "one", "odd"])
 def test_prefix_layouts(cuda_device, layout):
     for d, ps in ((64, 16), (128, 64), (64, 100), (128, 12)):
         c = _case(cuda_device, [5, 80, 0], 8, 2, d, ps, 1900 + d, layout, prefix_len=333)
@@ -220,12 +220,23 @@ def test_repeats_are_identical_and_caller_buffers(cuda_device):
     for plen in (0, 700):
         c = _case(cuda_device, [900, 20, 0, 4000, 1], 16, 2, 128, 16, 2100, prefix_len=plen)
         a, la = _run(c)
-        need = fa.fa_decode_paged_workspace_bytes(5, 16, 2, 128, plen)
-        ws = torch.full((need + 16,), 255, dtype=torch.uint8, device=cuda_device)
+        need = fa.fa_decode_paged_workspace_bytes(5, 16, 2, 128, 16, plen)
+        assert need > 0
+        ws = torch.full((need,), 255, dtype=torch.uint8, device=cuda_device)
         o = torch.full((5, 16, 128), math.nan, dtype=torch.bfloat16, device=cuda_device)
         for _ in range(3):
             b, lb = _run(c, workspace=ws, o=o)
             assert b is o and torch.equal(a, b) and torch.equal(la, lb)
+        _ok()
+
+
+def test_workspace_that_is_too_small_is_refused(cuda_device):
+    for plen, ps in ((0, 16), (700, 16), (90, 5)):
+        c = _case(cuda_device, [90, 20], 16, 2, 128, ps, 2150, prefix_len=plen)
+        need = fa.fa_decode_paged_workspace_bytes(2, 16, 2, 128, ps, plen)
+        with pytest.raises(fa.FAError):
+            _run(c, workspace=torch.empty(need - 256, dtype=torch.uint8, device=cuda_device))
+        _run(c, workspace=torch.empty(need, dtype=torch.uint8, device=cuda_device))
         _ok()
 
 

@@ -88,7 +88,7 @@ def _decode(**kw):
     (dict(plen=-1), INVALID), (dict(plen=5), INVALID), (dict(plen=BIG, pp=P3), INVALID),
     (dict(plen=5, pp=P3 + 1), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(B=1 << 20, H=1 << 12), INVALID), (dict(cs=[2048, 1024, 60]), INVALID),
-    (dict(cs=[-2048, 1024, 64]), INVALID),
+    (dict(cs=[-2048, 1024, 64]), INVALID), (dict(cs=[0, 1024, 64]), INVALID), (dict(cs=[2048, 1024, 0]), INVALID),
 ])
 def test_decode_rejects(kw, status):
     assert _decode(**kw) == status
@@ -100,7 +100,8 @@ def test_decode_paged_forwards_its_refusals():
 
 
 def test_workspace_bytes_of_bad_arguments():
-    for bad in ((0, 8, 2, 64, 0), (2, 8, 3, 64, 0), (2, 8, 2, 96, 0), (2, 8, 2, 64, -1), (2, 8, 0, 64, 0)):
+    for bad in ((0, 8, 2, 64, 16, 0), (2, 8, 3, 64, 16, 0), (2, 8, 2, 96, 16, 0), (2, 8, 2, 64, 16, -1), (2, 8, 0, 64, 16, 0),
+                (2, 8, 2, 64, 0, 5)):
         assert fa.fa_decode_paged_workspace_bytes(*bad) == 0
 
 

@@ -191,7 +191,7 @@ def _check_append(kc0, vc0, kc, vc, slots, k, v, rk, tk, ps, name):
     assert torch.equal(kc[free], kc0[free]), name
 
 
-@pytest.mark.parametrize("layout", ["head", "row", "one"])
+@pytest.mark.parametrize("layout", ["head", "row", "one", "odd"])
 @pytest.mark.parametrize("d,rot,inter,ps", [(64, 64, False, 16), (128, 32, True, 1), (128, 128, False, 24), (64, 0, False, 100)])
 @pytest.mark.parametrize("T,H,Hkv", [(1, 8, 2), (37, 0, 3), (300, 5, 5)])
 def test_append(cuda_device, layout, d, rot, inter, ps, T, H, Hkv):
