@@ -373,8 +373,8 @@ __global__ void __maxnreg__(C::MAXREG)
           if (lane < boxes) {
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c)
-              tma_load_4d(dst + c * C::KV_CH_BYTES + lane * p.box_rows * 128, tm, bar, c * C::CHUNK, p.heads_inner ? kvh : row,
-                          p.heads_inner ? row : kvh, page);
+              tma_load_4d(dst + c * C::KV_CH_BYTES + lane * p.box_rows * 128, tm, bar, c * C::CHUNK,
+                          p.heads_inner ? kvh : row, p.heads_inner ? row : kvh, page);
           }
         };
         if (!__all_sync(0xffffffffu, mbar_wait(bar_ke(s), ph, abort_flag, p.err, W_KE))) break;

@@ -122,10 +122,10 @@ struct PagedLaunch {
 // Work split and workspace layout (byte offsets) of a paged decode.
 struct PagedPlan {
   int n_cta = 0;                                      // CTAs that share the sequences' own keys
-  size_t part_ml = 0, part_o = 0, joins = 0;          // states of units shared by CTAs (fa_paged.cu)
+  size_t part_ml = 0, part_o = 0, infos = 0;          // states of units shared by warps (fa_paged.cu)
   // with a shared prefix:
   int n_split = 0, kv_per_split = 0, wide = 0;        // the prefix's key splits; wide: two query tiles per CTA
-  size_t pre_ml = 0, pre_o = 0, unit_ml = 0, unit_o = 0, infos = 0;
+  size_t pre_ml = 0, pre_o = 0, unit_ml = 0, unit_o = 0;
   int gather_len = 0, gather_rows = 0;                // pages (of gather_rows rows) the prefix is first copied into; 0: none
   size_t gather_k = 0, gather_v = 0, gather_pages = 0;
   size_t total = 0;

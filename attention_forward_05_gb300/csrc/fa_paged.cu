@@ -50,7 +50,24 @@ struct PgCfg {
   static constexpr int OFF_PLAN = OFF_ML + NW * GR * 8;
   static constexpr int SMEM = OFF_PLAN + 64;
   static constexpr bool Q_IN_REGS = MT == 1 || D == 64;
+  static constexpr int MT_FIT = MT * 16 * D * 4 <= STAGE_BYTES ? MT : 1;  // row tiles whose O fits a warp's stage at once
   static_assert(16 * D * 4 <= STAGE_BYTES, "a warp's O of one row tile fits one of its stages");
+};
+
+// Division of numbers below 2^31 by a fixed one.
+struct FastDiv {
+  unsigned mul, shift, d;
+  explicit FastDiv(unsigned n) : mul(0), shift(0), d(n) {
+    if (n <= 1) return;
+    unsigned l = 0;
+    while ((1u << l) < n) ++l;
+    mul = static_cast<unsigned>((1ull << (31 + l)) / n + 1);
+    shift = l - 1;
+  }
+  FastDiv() : FastDiv(1) {}
+  __device__ __forceinline__ int div(int x) const {
+    return d <= 1 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), mul) >> shift);
+  }
 };
 
 struct PgParams {
@@ -64,23 +81,22 @@ struct PgParams {
   long long c_page, c_head, c_row, table_stride;
   int B, H, Hkv, G, ngrp, U;      // U = Hkv * ngrp units a sequence
   int num_pages, page_size;
+  FastDiv by_page;
   int cap;                        // max_pages * page_size
   int n_cta;
   float c;
   int* err;
   float* part_ml;                 // float2 (m, l) [2 * n_cta][GR] of the CTAs' first (0) and last (1) unfinished units
   float* part_o;                  // [2 * n_cta][GR][D] unnormalised
-  // with a shared prefix every unit's own state stays a state for fa_paged_finish_kernel:
-  int prefix;                     // 1: so
+  int2* infos;                    // [B * U]: slot of the unit's first part (-1: it has one, in unit_ml / unit_o), and its
+                                  // parts (0: no own keys; -1: an unused place; -2: a bad length)
+  // with a shared prefix every unit's own state stays a state, and the join adds the prefix's:
+  int prefix;
   float* unit_ml;                 // float2 [B * H]: units that one CTA covers
   float* unit_o;                  // [B * H][D]
-  int2* infos;                    // [B * U]: slot of the unit's first part (-1: in unit_ml / unit_o), and its parts (0: no own
-                                  // keys; -1: an unused place; -2: a bad length)
-  const float* pre_ml;            // float2 [pre_split][Hkv][B * G] of the prefix
+  const float* pre_ml;            // float2 [pre_split][Hkv][B * G]
   const float* pre_o;
   int pre_split;
-  int4* joins;                    // [n_cta]: the unit (b, u) that starts in this CTA and ends in a later one, the slot of
-                                  // its first part (0 or 1), and its parts (0: there is none)
 };
 
 // Tiles of sequence b: 0 for a sequence without keys or with a length past its table.
@@ -165,11 +181,9 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     if (seq_tiles<C::TILE>(p, b, &len) > 0) continue;
     const bool bad = len > 0;
     if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
-    if (p.prefix) {
-      for (int u = threadIdx.x; u < p.U; u += 32 * NW)
-        p.infos[static_cast<long long>(b) * p.U + u] = make_int2(-1, bad ? -2 : len < 0 ? -1 : 0);
-      continue;
-    }
+    for (int u = threadIdx.x; u < p.U; u += 32 * NW)
+      p.infos[static_cast<long long>(b) * p.U + u] = make_int2(-1, bad ? -2 : len < 0 ? -1 : 0);
+    if (p.prefix) continue;  // the join writes their outputs
     const long long row0 = static_cast<long long>(b) * p.H;
     for (int e = threadIdx.x; e < p.H * CPR; e += 32 * NW)
       reinterpret_cast<uint4*>(p.o + row0 * D)[e] = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
@@ -178,7 +192,6 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
       for (int h = threadIdx.x; h < p.H; h += 32 * NW) p.lse[row0 + h] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
   }
   const long long n = cta_count(total, p.n_cta);
-  if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   auto leave = [&]() {
     if (p.prefix) griddep_wait();
   };
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   int pid = 0;
   auto lookup = [&]() {
     const int key = ld.tile * C::TILE + warp * KW + r_l;
-    if (ld.v < range && key < ld.len) pid = __ldg(p.table + ld.b * p.table_stride + key / p.page_size);
+    if (ld.v < range && key < ld.len) pid = __ldg(p.table + ld.b * p.table_stride + p.by_page.div(key));
   };
   auto load_step = [&]() {  // copies of step ld into ring stage ld_stage, then the next step's lookup
     if (ld.v < range) {
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
       long long off = -1;  // zeros
       if (key < ld.len) {
         if (pid >= 0 && pid < p.num_pages) {
-          off = pid * p.c_page + (ld.u / p.ngrp) * p.c_head + key % p.page_size * p.c_row;
+          off = pid * p.c_page + (p.ngrp == 1 ? ld.u : ld.u / p.ngrp) * p.c_head + (key - p.by_page.div(key) * p.page_size) * p.c_row;
         } else {
           off = -2;  // a NaN key: the sequence's outputs become NaN
           record_bad_index(p.err, W_PAGE);
@@ -415,94 +428,83 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
       // ---- the unit's part in this CTA ends: merge the warps' states
       const bool more = nx.v < range;
       if (more) fetch_q(nx.b, nx.u);  // in flight during the merge
-      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 1);
-          l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 2);
-          if ((lane & 3) == 0) ml[warp * C::GR + mt * 16 + r * 8 + (lane >> 2)] = make_float2(m_ref[mt][r], l[mt][r]);
-        }
-      __syncthreads();
       const bool whole = unit_ends && seg_tile0 == 0;
       const int slot = 2 * blockIdx.x + (first_unit ? 0 : 1);
-      const int h0 = cur.u / p.ngrp * p.G + cur.u % p.ngrp * C::GR;
-      const int rows = min(C::GR, p.G - cur.u % p.ngrp * C::GR);
-      float* const mine_o = reinterpret_cast<float*>(smem + (warp * S + stage) * C::STAGE_BYTES);
+      const int hk = cur.u / p.ngrp, g0 = cur.u % p.ngrp * C::GR;
+      const int rows = min(C::GR, p.G - g0);
+      const long long head0 = static_cast<long long>(cur.b) * p.H + hk * p.G + g0;
+      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+      auto stage_of = [&](int w) { return reinterpret_cast<float*>(smem + (w * S + stage) * C::STAGE_BYTES); };
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
+        // Every warp leaves (m, l) and its O of the rows in use in its own stage, 16-byte pieces swapped by the row
+        // so that eight rows use all banks; then each thread adds up one piece over the warps.
+        float* const mine_o = stage_of(warp) + mt % C::MT_FIT * 16 * D;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          if (mt * 16 + r * 8 >= rows) continue;  // no queries in these eight rows
-          const int row = mt * 16 + r * 8 + (lane >> 2);
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * C::GR + row].x);
-          const float wt = M == -INFINITY ? 0.f : ex2_approx(m_ref[mt][r] - M);
-          // row r*8 + lane/4 of the tile; 16-byte pieces swapped by the row so that eight rows use all banks
+          if (mt * 16 + r * 8 >= rows) continue;
+          float sum = l[mt][r];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if ((lane & 3) == 0) ml[warp * C::GR + mt * 16 + r * 8 + (lane >> 2)] = make_float2(m_ref[mt][r], sum);
           float* dst = mine_o + (r * 8 + (lane >> 2)) * D;
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
             const int col = 8 * j + 2 * (lane & 3);
             *reinterpret_cast<float2*>(dst + (((col >> 2) ^ (lane >> 2)) << 2) + (col & 3)) =
-                make_float2(o[mt][j][2 * r] * wt, o[mt][j][2 * r + 1] * wt);
+                make_float2(o[mt][j][2 * r], o[mt][j][2 * r + 1]);
           }
         }
+        if (mt % C::MT_FIT != C::MT_FIT - 1) continue;
         __syncthreads();
-        for (int e = threadIdx.x; e < 16 * (D / 4); e += 32 * NW) {
-          const int row = e / (D / 4), pc = e % (D / 4);
-          const int grow = mt * 16 + row;
-          if (grow < rows) {
-            float M = -INFINITY, L = 0.f;
+        const int row_lo = (mt + 1 - C::MT_FIT) * 16, row_hi = min(rows, (mt + 1) * 16);
+        for (int e = threadIdx.x; e < (row_hi - row_lo) * (D / 4); e += 32 * NW) {
+          const int row = e / (D / 4), pc = e % (D / 4), grow = row_lo + row;
+          float2 x[NW];
+          float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * C::GR + grow].x);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-              const float2 x = ml[w * C::GR + grow];
-              // an empty warp state is (-inf, 0); a NaN l must survive
-              L += x.y * (x.x == -INFINITY ? 1.f : ex2_approx(x.x - M));
-              const float4 y = *reinterpret_cast<const float4*>(
-                  reinterpret_cast<const float*>(smem + (w * S + stage) * C::STAGE_BYTES) + row * D +
-                  ((pc ^ (row & 7)) << 2));
-              acc.x += y.x;
-              acc.y += y.y;
-              acc.z += y.z;
-              acc.w += y.w;
-            }
-            const long long head = static_cast<long long>(cur.b) * p.H + h0 + grow;
-            if (whole && p.prefix) {
-              *reinterpret_cast<float4*>(p.unit_o + head * D + pc * 4) = acc;
-              if (pc == 0) reinterpret_cast<float2*>(p.unit_ml)[head] = make_float2(M, L);
-            } else if (whole) {
-              const float inv = 1.f / L;
-              *reinterpret_cast<uint2*>(p.o + head * D + pc * 4) =
-                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-              if (p.lse != nullptr && pc == 0) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
-            } else {
-              const long long at = static_cast<long long>(slot) * C::GR + grow;
-              *reinterpret_cast<float4*>(p.part_o + at * D + pc * 4) = acc;
-              if (pc == 0) reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(M, L);
-            }
+          for (int w = 0; w < NW; ++w) {
+            x[w] = ml[w * C::GR + grow];
+            M = fmaxf(M, x[w].x);
           }
+          const float ref = M == -INFINITY ? 0.f : M;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {  // an empty state is (-inf, 0, 0); a state of NaN keys (-inf, NaN, NaN)
+            const float wt = ex2_approx(x[w].x - ref);
+            L = fmaf(x[w].y, wt, L);
+            const float4 y = *reinterpret_cast<const float4*>(stage_of(w) + row * D + ((pc ^ (row & 7)) << 2));
+            acc.x = fmaf(y.x, wt, acc.x);
+            acc.y = fmaf(y.y, wt, acc.y);
+            acc.z = fmaf(y.z, wt, acc.z);
+            acc.w = fmaf(y.w, wt, acc.w);
+          }
+          if (whole && !p.prefix) {
+            const float inv = 1.f / L;
+            *reinterpret_cast<uint2*>(p.o + (head0 + grow) * D + pc * 4) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            if (p.lse != nullptr && pc == 0) p.lse[head0 + grow] = (M + log2f(L)) * 0.6931471805599453f;
+          } else {
+            const long long at = whole ? head0 + grow : static_cast<long long>(slot) * C::GR + grow;
+            *reinterpret_cast<float4*>((whole ? p.unit_o : p.part_o) + at * D + pc * 4) = acc;
+            if (pc == 0) reinterpret_cast<float2*>(whole ? p.unit_ml : p.part_ml)[at] = make_float2(M, L);
+          }
+        }
+        if (mt == MT - 1) {
+          if (seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
+            const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
+            p.infos[static_cast<long long>(cur.b) * p.U + cur.u] =
+                make_int2(whole ? -1 : slot, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
+          }
+          if (more) store_q();  // every warp is past its products with the unit's queries
         }
         __syncthreads();
       }
-      if (seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
-        const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
-        const int parts = static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1);
-        if (p.prefix) p.infos[static_cast<long long>(cur.b) * p.U + cur.u] = make_int2(whole ? -1 : slot, parts);
-        else if (!whole) p.joins[blockIdx.x] = make_int4(cur.b, cur.u, slot & 1, parts);
-      }
+      if (!more) break;
       first_unit = false;
-      if (more) {
-        store_q();
-        __syncthreads();
-        load_qf();
-        reset();
-        seg_tile0 = nx.tile;
-      }
+      load_qf();
+      reset();
+      seg_tile0 = nx.tile;
     }
     load_step();  // into the stage just read
     stage = stage + 1 == S ? 0 : stage + 1;
@@ -512,161 +514,117 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   leave();
 }
 
-// Joins the parts of a unit that several CTAs share: M = max m_s, then l and O add up with weights 2^(m_s - M).
-// One CTA per (CTA in which such a unit begins, query head of the unit); its four warps take every fourth
-// part, eight rows in flight, and add up in warp order.
+// Joins the parts of units that several CTAs share, and with a shared prefix the prefix's states and every
+// sequence's own, and writes the outputs.  A CTA takes every gridDim.x-th (sequence, query head); its four warps
+// take every fourth state, eight states' rows in flight, with the online-softmax recurrence, and add up in warp
+// order.  Bound by latency: a handful of dependent loads.
 constexpr int PJ_WARPS = 4;
 template <int D, int GR>
 __global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgParams p) {
   constexpr int E = D / 32;
   __shared__ float sm_o[PJ_WARPS][D];
+  __shared__ float2 sm_ml[PJ_WARPS];
   griddep_wait();
-  const int4 j = p.joins[blockIdx.x];
-  const int parts = j.w;
-  const int row = blockIdx.y;
-  const int g0 = j.y % p.ngrp * GR;
-  if (parts == 0 || g0 + row >= p.G) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // part s lies in the unit's first CTA's slot j.z, or in slot 0 of the s-th CTA after it
-  auto at = [&](int s) { return static_cast<long long>(2 * (static_cast<int>(blockIdx.x) + s) + (s == 0 ? j.z : 0)) * GR + row; };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, ml[at(s)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  auto weight = [&](float m) { return m == -INFINITY ? 1.f : ex2_approx(m - M); };  // an empty state is (-inf, 0, 0)
-  float L = 0.f;
-  for (int s = lane; s < parts; s += 32) {
-    const float2 x = ml[at(s)];
-    L += x.y * weight(x.x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s0 = warp; s0 < parts; s0 += 8 * PJ_WARPS) {
-    float w[8], v[8][E];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = s0 + i * PJ_WARPS;
-      w[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-      if (s < parts) {
-        w[i] = ml[at(s)].x;
-        const float* src = p.part_o + at(s) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          v[i][0] = x.x, v[i][1] = x.y;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float wt = weight(w[i]);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], wt, acc[e]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
-  __syncthreads();
-  const long long head = static_cast<long long>(j.x) * p.H + j.y / p.ngrp * p.G + g0 + row;
-  if (threadIdx.x < D) {
-    float O = 0.f;
-#pragma unroll
-    for (int w = 0; w < PJ_WARPS; ++w) O += sm_o[w][threadIdx.x];
-    p.o[head * D + threadIdx.x] = __float2bfloat16_rn(O / L);
-  }
-  if (p.lse != nullptr && threadIdx.x == 0) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
-}
-
-// With a shared prefix: joins the prefix's states of a query with its own, and writes the output.  One warp per
-// (sequence, query head), eight states' rows in flight; states add up in key order (prefix splits, then own parts).
-constexpr int PF_WARPS = 4;
-template <int D, int GR>
-__global__ void __launch_bounds__(32 * PF_WARPS) fa_paged_finish_kernel(const PgParams p) {
-  constexpr int E = D / 32;
-  griddep_wait();
-  const long long head = static_cast<long long>(blockIdx.x) * PF_WARPS + (threadIdx.x >> 5);
-  if (head >= static_cast<long long>(p.B) * p.H) return;
-  const int lane = threadIdx.x & 31;
-  const int b = static_cast<int>(head / p.H), h = static_cast<int>(head % p.H);
-  const int hk = h / p.G, g = h % p.G;
-  const int2 info = p.infos[static_cast<long long>(b) * p.U + hk * p.ngrp + g / GR];
-  const int row = g % GR;
-  const long long pstep = static_cast<long long>(p.B) * p.H;
-  const long long prow = (static_cast<long long>(hk) * p.B + b) * p.G + g;
-  const int pre = info.y < 0 ? 0 : p.pre_split;
-  const int parts = info.y < 0 ? 0 : pre + info.y;
-  auto state = [&](int s, const float2** ml, const float** o) {
-    if (s < pre) {
-      *ml = reinterpret_cast<const float2*>(p.pre_ml) + s * pstep + prow;
-      *o = p.pre_o + (s * pstep + prow) * D;
-    } else if (info.x < 0) {
-      *ml = reinterpret_cast<const float2*>(p.unit_ml) + head;
-      *o = p.unit_o + head * D;
-    } else {  // the first part's slot, then slot 0 of the CTAs after that one
-      const long long at = static_cast<long long>(s == pre ? info.x : 2 * (info.x / 2 + s - pre)) * GR + row;
-      *ml = reinterpret_cast<const float2*>(p.part_ml) + at;
-      *o = p.part_o + at * D;
-    }
-  };
-  float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) {
-    const float2* ml;
-    const float* o;
-    state(s, &ml, &o);
-    M = fmaxf(M, ml->x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s0 = 0; s0 < parts; s0 += 8) {
-    float2 x[8];
-    float v[8][E];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-      if (s0 + i < parts) {
-        const float2* ml;
-        const float* o;
-        state(s0 + i, &ml, &o);
-        x[i] = *ml;
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(o + lane * E);
-          v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(o + lane * E);
-          v[i][0] = y.x, v[i][1] = y.y;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (s0 + i < parts) {
-        const float w = x[i].x == -INFINITY ? 1.f : ex2_approx(x[i].x - M);  // an empty state is (-inf, 0, 0)
-        L = fmaf(x[i].y, w, L);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
-      }
-    }
-  }
+  const long long heads = static_cast<long long>(p.B) * p.H;
   const float nan = __int_as_float(0x7fc00000);
-  const float inv = info.y == -2 ? nan : parts == 0 ? 0.f : 1.f / L;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.o + head * D) + lane * (E / 2);
+  for (long long k0 = blockIdx.x; k0 < heads; k0 += 32LL * gridDim.x) {
+    // this CTA's next 32 rows: what there is to do for each
+    const long long mine = k0 + static_cast<long long>(lane) * gridDim.x;
+    int2 info = make_int2(-1, 1);
+    if (mine < heads) {
+      const int h = static_cast<int>(mine % p.H);
+      info = p.infos[mine / p.H * p.U + h / p.G * p.ngrp + h % p.G / GR];
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, mine < heads && (p.prefix || info.y > 1));
+    while (todo != 0) {
+      const int k = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const long long head = k0 + static_cast<long long>(k) * gridDim.x;
+      const int slot = __shfl_sync(0xffffffffu, info.x, k), own = __shfl_sync(0xffffffffu, info.y, k);
+      const int b = static_cast<int>(head / p.H), h = static_cast<int>(head % p.H);
+      const int hk = h / p.G, g = h % p.G;
+      const long long pstep = static_cast<long long>(p.B) * p.H;
+      const long long prow = (static_cast<long long>(hk) * p.B + b) * p.G + g;
+      const int pre = own < 0 ? 0 : p.pre_split;
+      const int parts = own < 0 ? 0 : pre + own;
+      float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[head] = info.y == -2 ? nan : parts == 0 ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      for (int s0 = warp; s0 < parts; s0 += 8 * PJ_WARPS) {
+        float2 x[8];
+        float v[8][E];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int s = s0 + i * PJ_WARPS;
+          x[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+          if (s >= parts) continue;
+          const float2* ml;
+          const float* o;
+          if (s < pre) {
+            ml = reinterpret_cast<const float2*>(p.pre_ml) + s * pstep + prow;
+            o = p.pre_o + (s * pstep + prow) * D;
+          } else if (slot < 0) {
+            ml = reinterpret_cast<const float2*>(p.unit_ml) + head;
+            o = p.unit_o + head * D;
+          } else {  // the first part's slot, then slot 0 of the CTAs after that one
+            const long long at = static_cast<long long>(s == pre ? slot : 2 * (slot / 2 + s - pre)) * GR + g % GR;
+            ml = reinterpret_cast<const float2*>(p.part_ml) + at;
+            o = p.part_o + at * D;
+          }
+          x[i] = *ml;
+          if constexpr (E == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(o + lane * E);
+            v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(o + lane * E);
+            v[i][0] = y.x, v[i][1] = y.y;
+          }
+        }
+        float m_new = M;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m_new = fmaxf(m_new, x[i].x);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = ex2_approx(M - ref);
+        M = m_new;
+        L *= alpha;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // an empty state is (-inf, 0, 0); a state of NaN keys (-inf, NaN, NaN)
+          const float w = ex2_approx(x[i].x - ref);
+          L = fmaf(x[i].y, w, L);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+      if (lane == 0) sm_ml[warp] = make_float2(M, L);
+      __syncthreads();
+      if (threadIdx.x < D) {
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < PJ_WARPS; ++w) M = fmaxf(M, sm_ml[w].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float O = 0.f;
+        L = 0.f;
+#pragma unroll
+        for (int w = 0; w < PJ_WARPS; ++w) {
+          const float wt = ex2_approx(sm_ml[w].x - ref);
+          L = fmaf(sm_ml[w].y, wt, L);
+          O = fmaf(sm_o[w][threadIdx.x], wt, O);
+        }
+        const float inv = own == -2 ? nan : parts == 0 ? 0.f : 1.f / L;
+        p.o[head * D + threadIdx.x] = __float2bfloat16_rn(O * inv);
+        if (p.lse != nullptr && threadIdx.x == 0)
+          p.lse[head] = own == -2 ? nan : parts == 0 ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      }
+      __syncthreads();
+    }
+  }
 }
 
 namespace {
@@ -686,7 +644,7 @@ PagedPlan plan_of(int B, int H, int Hkv, int page_size, int prefix_len, int sms)
   const size_t slots = static_cast<size_t>(2) * pl.n_cta, heads = static_cast<size_t>(B) * H;
   pl.part_ml = take(slots * C::GR * 8);
   pl.part_o = take(slots * C::GR * C::D * 4);
-  pl.joins = take(static_cast<size_t>(pl.n_cta) * 16);
+  pl.infos = take(static_cast<size_t>(B) * Hkv * ((H / Hkv + C::GR - 1) / C::GR) * 8);
   if (prefix_len > 0) {
     const int G = H / Hkv;
     plan_prefix(B, G, Hkv, C::D, page_size, prefix_len, sms, &pl);
@@ -694,7 +652,6 @@ PagedPlan plan_of(int B, int H, int Hkv, int page_size, int prefix_len, int sms)
     pl.pre_o = take(heads * pl.n_split * C::D * 4);
     pl.unit_ml = take(heads * 8);
     pl.unit_o = take(heads * C::D * 4);
-    pl.infos = take(static_cast<size_t>(B) * Hkv * ((G + C::GR - 1) / C::GR) * 8);
     const size_t rows = static_cast<size_t>(pl.gather_len) * pl.gather_rows * Hkv;
     pl.gather_k = take(rows * C::D * 2);
     pl.gather_v = take(rows * C::D * 2);
@@ -726,20 +683,20 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.U = a.Hkv * p.ngrp;
   p.num_pages = a.num_pages;
   p.page_size = a.page_size;
+  p.by_page = FastDiv(static_cast<unsigned>(a.page_size));
   p.cap = a.max_pages * a.page_size;
   p.n_cta = pl.n_cta;
   p.c = a.c;
   p.err = a.err;
   p.part_ml = reinterpret_cast<float*>(a.ws + pl.part_ml);
   p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
-  p.joins = reinterpret_cast<int4*>(a.ws + pl.joins);
+  p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
   cudaError_t e = cudaFuncSetAttribute(fa_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   if (a.prefix_len > 0) {
     p.prefix = 1;
     p.unit_ml = reinterpret_cast<float*>(a.ws + pl.unit_ml);
     p.unit_o = reinterpret_cast<float*>(a.ws + pl.unit_o);
-    p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
     p.pre_ml = reinterpret_cast<const float*>(a.ws + pl.pre_ml);
     p.pre_o = reinterpret_cast<const float*>(a.ws + pl.pre_o);
     p.pre_split = pl.n_split;
@@ -747,11 +704,9 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   }
   // programmatic dependents: a launch overlaps the end of the kernel before it
   if ((e = launch_dependent(fa_paged_kernel<C>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
-  if (a.prefix_len > 0)
-    return launch_dependent(fa_paged_finish_kernel<C::D, C::GR>, (a.B * a.H + PF_WARPS - 1) / PF_WARPS, 32 * PF_WARPS, 0,
-                            a.stream, p);
-  return launch_dependent(fa_paged_join_kernel<C::D, C::GR>, dim3(pl.n_cta, p.G < C::GR ? p.G : C::GR), 32 * PJ_WARPS, 0,
-                          a.stream, p);
+  const long long heads = static_cast<long long>(a.B) * a.H, most = static_cast<long long>(a.sms) * 16;
+  return launch_dependent(fa_paged_join_kernel<C::D, C::GR>, static_cast<unsigned>(heads < most ? heads : most),
+                          32 * PJ_WARPS, 0, a.stream, p);
 }
 
 // Groups of more than 16 query heads take two 16-row tiles a unit (K and V are then read once for 32 heads);

@@ -5,7 +5,7 @@
 // keys: the forward kernel's tensor-core tiles (fa_fwd_kernel.cuh), with K and V copied out of the cache's pages
 // and partial states (m, l, unnormalised O) as its result.  The prefix is read once a key split instead of once
 // a sequence, and for large batches the work is bound by the matrix rate.  The sequences' own keys follow in
-// fa_paged_kernel, and fa_paged_finish_kernel (fa_paged.cu) joins the states.
+// fa_paged_kernel, and fa_paged_join_kernel (fa_paged.cu) joins the states.
 //
 // Configurations (fa_fwd_bf16.cu and fa_fwd_decode.cu have the same tiles): two 128-row query tiles per CTA, or
 // one where the B * G rows of a head fit in it.
