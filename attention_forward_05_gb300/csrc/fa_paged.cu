@@ -2,21 +2,28 @@
 //
 // Sequence b sees len_b cache rows through its row of the page table: o = softmax(scale q K^T) V and the
 // natural-log LSE, by the online-softmax recurrence in log2 units.  All G = H / Hkv query heads of a
-// key/value head are the rows of one 16-row (or two 16-row) matrix tile, so each key and value is read from
-// device memory once: the kernel is bound by those bytes.
+// key/value head go through one pass over its keys, so each key and value is read from device memory once:
+// the kernel is bound by those bytes.
 //
-// Work split.  A unit is one (sequence, group of query heads); its keys are cut into tiles of PG_TILE.  The
-// tiles of all units, in order, are dealt evenly to the CTAs, one contiguous range each, whatever the
-// lengths are (they stay in device memory; every CTA sums them itself).  A CTA's range covers whole units,
+// Products.  Both are computed transposed, by warp-level matrix instructions: S^T = K Q^T with 16 keys as the
+// rows and 8 heads as the columns, O^T += V^T P^T with 16 dimensions as the rows.  Keys and values then fill the
+// 16-row side, and a group of up to 8 heads wastes no product; S^T turns into the operand P^T by one transposing
+// move a 16-key block.  (With the heads as the 16 rows a tile step took 630 instructions an 8 KB of K and V
+// instead of about 200, and the issue slots, not the bytes, bound short contexts.)  A thread holds two heads'
+// columns, so maxima, sums and rescaling are its own; the running maximum moves only when a score passes it by
+// more than 2^PG_TAU.
+//
+// Work split.  A unit is one (sequence, group of query heads); its keys are cut into tiles of TILE (32 KB of K
+// and V).  The tiles of all units, in order, are dealt evenly to the CTAs, one contiguous range each, whatever
+// the lengths are (they stay in device memory; every CTA sums them itself).  A CTA's range covers whole units,
 // which it finishes, and at most two parts of units at its ends, which it leaves as partial states (m, l,
-// unnormalised O) for fa_paged_join_kernel.
+// unnormalised O) for fa_paged_join_kernel.  (Ranges of single warps left four times as many parts to join:
+// 28 instead of 21 us on one sequence of 32768 keys.)
 //
 // Inside a CTA each warp takes its own KW keys of every tile through its own ring of asynchronous 16-byte
-// copies, with no barrier between the warps until a unit ends: S = Q K^T and O += P V by warp-level matrix
-// products (S in registers becomes the A operand of P V), the running maximum moved only when a score passes
-// it by more than 2^PG_TAU.  Rows of any page size and stride: the lanes look up their keys' pages one step
-// ahead and pass the row offsets around by shuffles.  The warps' states merge in shared memory when a unit
-// ends.  A matrix tile of few real rows wastes products, not bytes.
+// copies, with no barrier between the warps until a unit ends; then their states merge in shared memory.  The
+// lanes look up their keys' pages one step ahead.  Page sizes that are multiples of 16 rows copy 16 rows from
+// one base address; others pass every row's offset around by shuffles.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -32,16 +39,16 @@ constexpr float PG_TAU = 8.f;
 // the ranges are cut as if every unit had that many tiles more.
 constexpr int PG_END = 2;
 
-template <int D_, int MT_>
+template <int D_, int NT_>
 struct PgCfg {
   static constexpr int D = D_;
-  static constexpr int MT = MT_;             // 16-row tiles of query heads
-  static constexpr int GR = 16 * MT;         // query heads a unit holds
+  static constexpr int NT = NT_;                 // 8-column tiles of query heads
+  static constexpr int GR = 8 * NT;              // query heads a unit holds
   static constexpr int NW = 4;
   static constexpr int KW = D == 128 ? 16 : 32;  // keys of one warp step: 8 KB of K and V
   static constexpr int TILE = NW * KW;
-  static constexpr int STAGES = 3;
-  static constexpr int CTAS = 2;             // per SM
+  static constexpr int CTAS = NT == 4 ? 2 : 3;   // per SM
+  static constexpr int STAGES = NT == 4 ? 3 : 2;
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int K_BYTES = KW * ROW_BYTES;
   static constexpr int STAGE_BYTES = 2 * K_BYTES;
@@ -49,9 +56,9 @@ struct PgCfg {
   static constexpr int OFF_ML = OFF_Q + GR * ROW_BYTES;         // float2 [NW][GR]
   static constexpr int OFF_PLAN = OFF_ML + NW * GR * 8;
   static constexpr int SMEM = OFF_PLAN + 64;
-  static constexpr bool Q_IN_REGS = MT == 1 || D == 64;
-  static constexpr int MT_FIT = MT * 16 * D * 4 <= STAGE_BYTES ? MT : 1;  // row tiles whose O fits a warp's stage at once
-  static_assert(16 * D * 4 <= STAGE_BYTES, "a warp's O of one row tile fits one of its stages");
+  static constexpr int FIT = STAGE_BYTES / (GR * D * 4) > 0 ? NT : STAGE_BYTES / (8 * D * 4);  // head tiles whose O fits a stage
+  static_assert(NT % FIT == 0, "whole rounds");
+  static_assert(SMEM * CTAS <= 227 * 1024 - CTAS * 1024, "shared memory");
 };
 
 // Division of numbers below 2^31 by a fixed one.
@@ -82,6 +89,7 @@ struct PgParams {
   int B, H, Hkv, G, ngrp, U;      // U = Hkv * ngrp units a sequence
   int num_pages, page_size;
   FastDiv by_page;
+  int runs16;                     // page_size is a multiple of 16
   int cap;                        // max_pages * page_size
   int n_cta;
   float c;
@@ -140,7 +148,7 @@ struct Cursor {
 template <class C>
 __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int D = C::D, MT = C::MT, KW = C::KW, NW = C::NW, S = C::STAGES;
+  constexpr int D = C::D, KW = C::KW, NW = C::NW, S = C::STAGES;
   constexpr int CPR = D / 8;        // 16-byte pieces of a row
   constexpr int RPP = 32 / CPR;     // rows one warp-wide copy covers
   constexpr int NP = KW / RPP;      // copies of K (and of V) a step
@@ -231,7 +239,11 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   const uint32_t ring = smem_u32(smem) + warp * S * C::STAGE_BYTES;
   Cursor<C> ld = cur;
   int ld_stage = 0;
-  const int r_l = lane % KW;
+  const int r_l = lane % KW, piece = lane % CPR;
+  const long long lane_off = static_cast<long long>(lane / CPR) * p.c_row + piece * 8;
+  const long long pass_off = RPP * p.c_row;
+  // piece `piece` of row r of a stage lies at r * ROW_BYTES + ((piece ^ (r & 7)) << 4); pass i has r = i * RPP + lane / CPR
+  const uint32_t dst_lane = ring + lane / CPR * C::ROW_BYTES + ((piece ^ (lane / CPR)) << 4);
   int pid = 0;
   auto lookup = [&]() {
     const int key = ld.tile * C::TILE + warp * KW + r_l;
@@ -240,275 +252,287 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   auto load_step = [&]() {  // copies of step ld into ring stage ld_stage, then the next step's lookup
     if (ld.v < range) {
       const int key = ld.tile * C::TILE + warp * KW + r_l;
-      long long off = -1;  // zeros
-      if (key < ld.len) {
-        if (pid >= 0 && pid < p.num_pages) {
-          off = pid * p.c_page + (p.ngrp == 1 ? ld.u : ld.u / p.ngrp) * p.c_head + (key - p.by_page.div(key) * p.page_size) * p.c_row;
-        } else {
+      const bool good = pid >= 0 && pid < p.num_pages;
+      long long off = pid * p.c_page + (p.ngrp == 1 ? ld.u : ld.u / p.ngrp) * p.c_head +
+                      (key - p.by_page.div(key) * p.page_size) * p.c_row;
+      const uint32_t dst0 = dst_lane + ld_stage * C::STAGE_BYTES;
+      if (p.runs16 && __all_sync(0xffffffffu, key < ld.len && good)) {
+#pragma unroll
+        for (int h = 0; h < KW / 16; ++h) {
+          const long long base = __shfl_sync(0xffffffffu, off, 16 * h) + lane_off;
+          const __nv_bfloat16 *kp = p.kc + base, *vp = p.vc + base;
+#pragma unroll
+          for (int j = 0; j < 16 / RPP; ++j) {
+            const int i = h * (16 / RPP) + j;
+            const uint32_t dst = (dst0 ^ ((i * RPP & 7) << 4)) + i * RPP * C::ROW_BYTES;
+            cp_async16(dst, kp);
+            cp_async16(dst + C::K_BYTES, vp);
+            kp += pass_off;
+            vp += pass_off;
+          }
+        }
+      } else {
+        if (key >= ld.len) {
+          off = -1;  // zeros
+        } else if (!good) {
           off = -2;  // a NaN key: the sequence's outputs become NaN
           record_bad_index(p.err, W_PAGE);
         }
-      }
-      const int piece = lane % CPR;
-      const uint32_t dst0 = ring + ld_stage * C::STAGE_BYTES;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int row = i * RPP + lane / CPR;
-        const long long ro = __shfl_sync(0xffffffffu, off, row);
-        const uint32_t dst = dst0 + row * C::ROW_BYTES + ((piece ^ (row & 7)) << 4);
-        const long long src = ro < 0 ? 0 : ro + piece * 8;
-        if (ro == -2 && piece == 0)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(0x7fff7fffu) : "memory");
-        else
-          cp_async16(dst, p.kc + src, ro < 0 ? 0 : 16);
-        cp_async16(dst + C::K_BYTES, p.vc + src, ro < 0 ? 0 : 16);
+        for (int i = 0; i < NP; ++i) {
+          const long long ro = __shfl_sync(0xffffffffu, off, i * RPP + lane / CPR);
+          const uint32_t dst = (dst0 ^ ((i * RPP & 7) << 4)) + i * RPP * C::ROW_BYTES;
+          const long long src = ro < 0 ? 0 : ro + piece * 8;
+          if (ro == -2 && piece == 0)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(0x7fff7fffu) : "memory");
+          else
+            cp_async16(dst, p.kc + src, ro < 0 ? 0 : 16);
+          cp_async16(dst + C::K_BYTES, p.vc + src, ro < 0 ? 0 : 16);
+        }
       }
-    }
-    cp_async_commit();
-    ld_stage = ld_stage + 1 == S ? 0 : ld_stage + 1;
-    if (ld.v < range) {
       ld.next(p);
       lookup();
     }
+    cp_async_commit();
+    ld_stage = ld_stage + 1 == S ? 0 : ld_stage + 1;
   };
   lookup();
 
-  // ---- queries of the first unit
+  // ---- queries: fetched into registers, handed over through shared memory (sign flipped for a negative scale, so
+  // that the largest score is the largest product)
   uint8_t* sq = smem + C::OFF_Q;
-  constexpr int QN = C::GR * CPR / (32 * NW);  // 16-byte pieces of Q a thread carries
-  static_assert(C::GR * CPR % (32 * NW) == 0, "whole rounds");
+  constexpr int QN = (C::GR * CPR + 32 * NW - 1) / (32 * NW);  // 16-byte pieces of Q a thread carries
   uint4 qv[QN];
+  const float c = fmaxf(fabsf(p.c), 1e-30f);  // a zero scale: every score 0, without 0 * inf in masked places
+  const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
   auto fetch_q = [&](int b, int u) {
-    const int h0 = u / p.ngrp * p.G + u % p.ngrp * C::GR;
-    const int rows = min(C::GR, p.G - u % p.ngrp * C::GR);
+    const int g0 = u % p.ngrp * C::GR, rows = min(C::GR, p.G - g0);
+    const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.H + u / p.ngrp * p.G + g0) * D;
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
-      const int e = i * 32 * NW + threadIdx.x, row = e / CPR;
-      qv[i] = row < rows ? *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(b) * p.H + h0 + row) * D +
-                                                           e % CPR * 8)
-                         : make_uint4(0, 0, 0, 0);
+      const int e = i * 32 * NW + threadIdx.x;
+      qv[i] = e / CPR < rows ? reinterpret_cast<const uint4*>(src)[e] : make_uint4(flip, flip, flip, flip);
     }
   };
   auto store_q = [&]() {
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
       const int e = i * 32 * NW + threadIdx.x, row = e / CPR;
-      *reinterpret_cast<uint4*>(sq + row * C::ROW_BYTES + ((e % CPR ^ (row & 7)) << 4)) = qv[i];
+      if (row < C::GR)
+        *reinterpret_cast<uint4*>(sq + row * C::ROW_BYTES + ((e % CPR ^ (row & 7)) << 4)) =
+            make_uint4(qv[i].x ^ flip, qv[i].y ^ flip, qv[i].z ^ flip, qv[i].w ^ flip);
     }
   };
   fetch_q(cur.b, cur.u);
 #pragma unroll
-  for (int i = 0; i < S; ++i) load_step();
+  for (int i = 0; i < S - 1; ++i) load_step();
   store_q();
   __syncthreads();
 
-  // ---- fragments
-  const int l7 = lane & 7, mat = lane >> 3;
-  const uint32_t q_addr = smem_u32(sq) + ((mat & 1) * 8 + l7) * C::ROW_BYTES;   // A: rows (mat&1), k half (mat>>1)
-  const int q_x = (mat >> 1) ^ l7;
-  const uint32_t k_off = ((mat >> 1) * 8 + l7) * C::ROW_BYTES;                   // B: keys (mat>>1), k half (mat&1)
-  const int k_x = (mat & 1) ^ l7;
-  const uint32_t v_off = C::K_BYTES + ((mat & 1) * 8 + l7) * C::ROW_BYTES;       // B of P V: keys (mat&1), dims (mat>>1)
-  const int v_x = (mat >> 1) ^ l7;
-  uint32_t qf[C::Q_IN_REGS ? MT : 1][C::Q_IN_REGS ? D / 16 : 1][4];
+  // ---- fragments (mat, l7: the 8x8 matrix and its row whose address a lane gives)
+  const int l7 = lane & 7, mat = lane >> 3, gid = lane >> 2, tig = lane & 3;
+  const uint32_t q_addr = smem_u32(sq) + l7 * C::ROW_BYTES + ((mat ^ l7) << 4);   // B: heads l7, two k steps' halves
+  const uint32_t k_lane = ring + ((mat & 1) * 8 + l7) * C::ROW_BYTES + (((mat >> 1) ^ l7) << 4);                // A: keys, k halves
+  const uint32_t v_lane = ring + C::K_BYTES + ((mat >> 1) * 8 + l7) * C::ROW_BYTES + (((mat & 1) ^ l7) << 4);  // A: dims, keys
+  uint32_t qf[C::NT][D / 32][4];  // [head tile][two k steps]: B fragments (b0, b1) of the one, then of the other
   auto load_qf = [&]() {
-    if constexpr (C::Q_IN_REGS) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          ldmatrix_x4(q_addr + mt * 16 * C::ROW_BYTES + (((2 * ks) ^ q_x) << 4), qf[mt][ks]);
-    }
+      for (int k2 = 0; k2 < D / 32; ++k2) ldmatrix_x4((q_addr ^ (k2 << 6)) + nt * 8 * C::ROW_BYTES, qf[nt][k2]);
   };
   load_qf();
-  float o[MT][D / 8][4];
-  float m_ref[MT][2], l[MT][2];
+  float o[C::NT][D / 16][4];       // O^T: dims 16 dp + gid (+ 8) x heads 2 tig, 2 tig + 1
+  float m_ref[C::NT][2], l[C::NT][2];
   auto reset = [&]() {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
+      for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
-      m_ref[mt][0] = m_ref[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+        for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+      m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
     }
   };
   reset();
-  int seg_tile0 = cur.tile;  // first tile of the unit that this CTA covers
   bool first_unit = true;
   int stage = 0;
 
-  while (cur.v < range) {
-    cp_async_wait<S - 1>();
-    __syncwarp();
-    const uint32_t st = ring + stage * C::STAGE_BYTES;
-    const int valid = cur.len - (cur.tile * C::TILE + warp * KW);
-    if (valid > 0) {
+  while (true) {
+    const int seg_tile0 = cur.tile;  // first tile of the unit that this CTA covers
+    const int tiles = min(cur.nt - cur.tile, range - cur.v);
+    for (int i = 0;; ++i) {
+      load_step();  // into the stage of the step before this one
+      cp_async_wait<S - 1>();
+      __syncwarp();
+      const int valid = cur.len - ((seg_tile0 + i) * C::TILE + warp * KW);
+      const uint32_t ks0 = k_lane + stage * C::STAGE_BYTES, vs0 = v_lane + stage * C::STAGE_BYTES;
+      if (valid > 0) {
+        float s[C::NT][KW / 16][4];  // S^T: keys 16 kb + gid (+ 8) x heads 2 tig, 2 tig + 1
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float s[KW / 8][4];
+        for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < KW / 8; ++j)
+          for (int kb = 0; kb < KW / 16; ++kb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[nt][kb][e] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t a[4];
-          if constexpr (C::Q_IN_REGS) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = qf[mt][ks][e];
-          } else {
-            ldmatrix_x4(q_addr + mt * 16 * C::ROW_BYTES + (((2 * ks) ^ q_x) << 4), a);
-          }
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
           for (int kb = 0; kb < KW / 16; ++kb) {
-            uint32_t b[4];
-            ldmatrix_x4(st + k_off + kb * 16 * C::ROW_BYTES + (((2 * ks) ^ k_x) << 4), b);
-            mma_16816(s[2 * kb], a, b[0], b[1]);
-            mma_16816(s[2 * kb + 1], a, b[2], b[3]);
+            uint32_t a[4];
+            ldmatrix_x4((ks0 ^ (ks << 5)) + kb * 16 * C::ROW_BYTES, a);
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt)
+              mma_16816(s[nt][kb], a, qf[nt][ks / 2][ks % 2 * 2], qf[nt][ks / 2][ks % 2 * 2 + 1]);
           }
+        if (valid < KW) {
+#pragma unroll
+          for (int kb = 0; kb < KW / 16; ++kb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (kb * 16 + r * 8 + gid >= valid)
+#pragma unroll
+                for (int nt = 0; nt < C::NT; ++nt) s[nt][kb][2 * r] = s[nt][kb][2 * r + 1] = -INFINITY;
         }
-        float mx[2] = {-INFINITY, -INFINITY};
+        uint32_t pf[C::NT][KW / 16][2];  // P^T rounded to bf16: the B operand of V^T P^T
 #pragma unroll
-        for (int j = 0; j < KW / 8; ++j)
+        for (int nt = 0; nt < C::NT; ++nt) {
+          float mx[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float t = s[j][e] * p.c;
-            if (valid < KW && 8 * j + 2 * (lane & 3) + (e & 1) >= valid) t = -INFINITY;
-            s[j][e] = t;
-            mx[e >> 1] = fmaxf(mx[e >> 1], t);
+          for (int x = 0; x < 2; ++x) {
+            mx[x] = fmaxf(s[nt][0][x], s[nt][0][2 + x]);
+#pragma unroll
+            for (int kb = 1; kb < KW / 16; ++kb) mx[x] = max3f(mx[x], s[nt][kb][x], s[nt][kb][2 + x]);
+            mx[x] *= c;
           }
-        if (__any_sync(0xffffffffu, mx[0] > m_ref[mt][0] + PG_TAU || mx[1] > m_ref[mt][1] + PG_TAU)) {
+          if (__any_sync(0xffffffffu, mx[0] > m_ref[nt][0] + PG_TAU || mx[1] > m_ref[nt][1] + PG_TAU)) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            if (mx[r] > m_ref[mt][r] + PG_TAU) {
-              const float alpha = ex2_approx(m_ref[mt][r] - mx[r]);  // 0 on the first keys
-              m_ref[mt][r] = mx[r];
-              l[mt][r] *= alpha;
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-              for (int j = 0; j < D / 8; ++j) {
-                o[mt][j][2 * r] *= alpha;
-                o[mt][j][2 * r + 1] *= alpha;
+              for (int off = 4; off < 32; off <<= 1) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], off));
+              if (mx[x] > m_ref[nt][x] + PG_TAU) {
+                const float alpha = ex2_approx(m_ref[nt][x] - mx[x]);  // 0 on the first keys
+                m_ref[nt][x] = mx[x];
+                l[nt][x] *= alpha;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                  o[nt][j][x] *= alpha;
+                  o[nt][j][2 + x] *= alpha;
+                }
               }
             }
           }
-        }
-        const float m0 = m_ref[mt][0] == -INFINITY ? 0.f : m_ref[mt][0];
-        const float m1 = m_ref[mt][1] == -INFINITY ? 0.f : m_ref[mt][1];
-        uint32_t pf[KW / 16][4];  // P rounded to bf16: the A operand of P V
+          const float n0 = m_ref[nt][0] == -INFINITY ? 0.f : -m_ref[nt][0];
+          const float n1 = m_ref[nt][1] == -INFINITY ? 0.f : -m_ref[nt][1];
 #pragma unroll
-        for (int j = 0; j < KW / 8; ++j) {
-          const float p0 = ex2_approx(s[j][0] - m0), p1 = ex2_approx(s[j][1] - m0);
-          const float p2 = ex2_approx(s[j][2] - m1), p3 = ex2_approx(s[j][3] - m1);
-          l[mt][0] += p0 + p1;
-          l[mt][1] += p2 + p3;
-          pf[j / 2][(j & 1) * 2] = pack_bf16x2(p0, p1);
-          pf[j / 2][(j & 1) * 2 + 1] = pack_bf16x2(p2, p3);
+          for (int kb = 0; kb < KW / 16; ++kb) {
+            const float p0 = ex2_approx(fmaf(s[nt][kb][0], c, n0)), p1 = ex2_approx(fmaf(s[nt][kb][1], c, n1));
+            const float p2 = ex2_approx(fmaf(s[nt][kb][2], c, n0)), p3 = ex2_approx(fmaf(s[nt][kb][3], c, n1));
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            pf[nt][kb][0] = movmatrix_trans(pack_bf16x2(p0, p1));
+            pf[nt][kb][1] = movmatrix_trans(pack_bf16x2(p2, p3));
+          }
         }
 #pragma unroll
         for (int kb = 0; kb < KW / 16; ++kb)
 #pragma unroll
           for (int dp = 0; dp < D / 16; ++dp) {
-            uint32_t b[4];
-            ldmatrix_x4_trans(st + v_off + kb * 16 * C::ROW_BYTES + (((2 * dp) ^ v_x) << 4), b);
-            mma_16816(o[mt][2 * dp], pf[kb], b[0], b[1]);
-            mma_16816(o[mt][2 * dp + 1], pf[kb], b[2], b[3]);
+            uint32_t a[4];
+            ldmatrix_x4_trans((vs0 ^ (dp << 5)) + kb * 16 * C::ROW_BYTES, a);
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt) mma_16816(o[nt][dp], a, pf[nt][kb][0], pf[nt][kb][1]);
           }
       }
+      __syncwarp();  // every lane has read the stage
+      if (i + 1 == tiles) break;
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
-    __syncwarp();  // every lane has read the stage
 
-    const bool unit_ends = cur.tile + 1 == cur.nt;
+    // ---- the unit's part in this CTA ends: merge the warps' states
+    cur.tile += tiles - 1;
+    cur.v += tiles - 1;
     Cursor<C> nx = cur;
     nx.next(p);
-    if (unit_ends || nx.v >= range) {
-      // ---- the unit's part in this CTA ends: merge the warps' states
-      const bool more = nx.v < range;
-      if (more) fetch_q(nx.b, nx.u);  // in flight during the merge
-      const bool whole = unit_ends && seg_tile0 == 0;
-      const int slot = 2 * blockIdx.x + (first_unit ? 0 : 1);
-      const int hk = cur.u / p.ngrp, g0 = cur.u % p.ngrp * C::GR;
-      const int rows = min(C::GR, p.G - g0);
-      const long long head0 = static_cast<long long>(cur.b) * p.H + hk * p.G + g0;
-      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-      auto stage_of = [&](int w) { return reinterpret_cast<float*>(smem + (w * S + stage) * C::STAGE_BYTES); };
+    const bool more = nx.v < range;
+    if (more) fetch_q(nx.b, nx.u);  // in flight during the merge
+    const bool whole = seg_tile0 == 0 && cur.tile + 1 == cur.nt;
+    const int slot = 2 * blockIdx.x + (first_unit ? 0 : 1);
+    const int hk = cur.u / p.ngrp, g0 = cur.u % p.ngrp * C::GR;
+    const int rows = min(C::GR, p.G - g0);
+    const long long head0 = static_cast<long long>(cur.b) * p.H + hk * p.G + g0;
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    auto stage_of = [&](int w) { return reinterpret_cast<float*>(smem + (w * S + stage) * C::STAGE_BYTES); };
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        // Every warp leaves (m, l) and its O of the rows in use in its own stage, 16-byte pieces swapped by the row
-        // so that eight rows use all banks; then each thread adds up one piece over the warps.
-        float* const mine_o = stage_of(warp) + mt % C::MT_FIT * 16 * D;
+    for (int nt = 0; nt < C::NT; ++nt) {
+      // Every warp leaves (m, l) and its O in its own stage, row by head, 8-element runs swapped by the head pair so that
+      // a store's 32 elements use all banks; then each thread adds up one 16-byte piece over the warps.
+      float* const mine_o = stage_of(warp) + nt % C::FIT * 8 * D;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (mt * 16 + r * 8 >= rows) continue;
-          float sum = l[mt][r];
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if ((lane & 3) == 0) ml[warp * C::GR + mt * 16 + r * 8 + (lane >> 2)] = make_float2(m_ref[mt][r], sum);
-          float* dst = mine_o + (r * 8 + (lane >> 2)) * D;
+      for (int x = 0; x < 2; ++x) {
+        float sum = l[nt][x];
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            const int col = 8 * j + 2 * (lane & 3);
-            *reinterpret_cast<float2*>(dst + (((col >> 2) ^ (lane >> 2)) << 2) + (col & 3)) =
-                make_float2(o[mt][j][2 * r], o[mt][j][2 * r + 1]);
-          }
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (gid == 0) ml[warp * C::GR + nt * 8 + 2 * tig + x] = make_float2(m_ref[nt][x], sum);
+        float* dst = mine_o + (2 * tig + x) * D + gid;
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+          dst[16 * dp ^ (tig << 3)] = o[nt][dp][x];
+          dst[(16 * dp + 8) ^ (tig << 3)] = o[nt][dp][2 + x];
         }
-        if (mt % C::MT_FIT != C::MT_FIT - 1) continue;
-        __syncthreads();
-        const int row_lo = (mt + 1 - C::MT_FIT) * 16, row_hi = min(rows, (mt + 1) * 16);
-        for (int e = threadIdx.x; e < (row_hi - row_lo) * (D / 4); e += 32 * NW) {
-          const int row = e / (D / 4), pc = e % (D / 4), grow = row_lo + row;
-          float2 x[NW];
-          float M = -INFINITY, L = 0.f;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            x[w] = ml[w * C::GR + grow];
-            M = fmaxf(M, x[w].x);
-          }
-          const float ref = M == -INFINITY ? 0.f : M;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {  // an empty state is (-inf, 0, 0); a state of NaN keys (-inf, NaN, NaN)
-            const float wt = ex2_approx(x[w].x - ref);
-            L = fmaf(x[w].y, wt, L);
-            const float4 y = *reinterpret_cast<const float4*>(stage_of(w) + row * D + ((pc ^ (row & 7)) << 2));
-            acc.x = fmaf(y.x, wt, acc.x);
-            acc.y = fmaf(y.y, wt, acc.y);
-            acc.z = fmaf(y.z, wt, acc.z);
-            acc.w = fmaf(y.w, wt, acc.w);
-          }
-          if (whole && !p.prefix) {
-            const float inv = 1.f / L;
-            *reinterpret_cast<uint2*>(p.o + (head0 + grow) * D + pc * 4) =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-            if (p.lse != nullptr && pc == 0) p.lse[head0 + grow] = (M + log2f(L)) * 0.6931471805599453f;
-          } else {
-            const long long at = whole ? head0 + grow : static_cast<long long>(slot) * C::GR + grow;
-            *reinterpret_cast<float4*>((whole ? p.unit_o : p.part_o) + at * D + pc * 4) = acc;
-            if (pc == 0) reinterpret_cast<float2*>(whole ? p.unit_ml : p.part_ml)[at] = make_float2(M, L);
-          }
-        }
-        if (mt == MT - 1) {
-          if (seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
-            const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
-            p.infos[static_cast<long long>(cur.b) * p.U + cur.u] =
-                make_int2(whole ? -1 : slot, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
-          }
-          if (more) store_q();  // every warp is past its products with the unit's queries
-        }
-        __syncthreads();
       }
-      if (!more) break;
-      first_unit = false;
-      load_qf();
-      reset();
-      seg_tile0 = nx.tile;
+      if (nt % C::FIT != C::FIT - 1) continue;
+      __syncthreads();
+      const int row_lo = (nt + 1 - C::FIT) * 8, row_hi = min(rows, (nt + 1) * 8);
+      for (int e = threadIdx.x; e < (row_hi - row_lo) * (D / 4); e += 32 * NW) {
+        const int row = e / (D / 4), pc = e % (D / 4), grow = row_lo + row;
+        float2 x[NW];
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          x[w] = ml[w * C::GR + grow];
+          M = fmaxf(M, x[w].x);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {  // an empty state is (-inf, 0, 0); a state of NaN keys (-inf, NaN, NaN)
+          const float wt = ex2_approx(x[w].x - ref);
+          L = fmaf(x[w].y, wt, L);
+          const float4 y = *reinterpret_cast<const float4*>(stage_of(w) + row * D + ((4 * pc) ^ ((row >> 1 & 3) << 3)));
+          acc.x = fmaf(y.x, wt, acc.x);
+          acc.y = fmaf(y.y, wt, acc.y);
+          acc.z = fmaf(y.z, wt, acc.z);
+          acc.w = fmaf(y.w, wt, acc.w);
+        }
+        if (whole && !p.prefix) {
+          const float inv = 1.f / L;
+          *reinterpret_cast<uint2*>(p.o + (head0 + grow) * D + pc * 4) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (p.lse != nullptr && pc == 0) p.lse[head0 + grow] = (M + log2f(L)) * 0.6931471805599453f;
+        } else {
+          const long long at = whole ? head0 + grow : static_cast<long long>(slot) * C::GR + grow;
+          *reinterpret_cast<float4*>((whole ? p.unit_o : p.part_o) + at * D + pc * 4) = acc;
+          if (pc == 0) reinterpret_cast<float2*>(whole ? p.unit_ml : p.part_ml)[at] = make_float2(M, L);
+        }
+      }
+      if (nt == C::NT - 1) {
+        if (seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
+          const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
+          p.infos[static_cast<long long>(cur.b) * p.U + cur.u] =
+              make_int2(whole ? -1 : slot, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
+        }
+        if (more) store_q();  // every warp is past its products with the unit's queries
+      }
+      __syncthreads();
     }
-    load_step();  // into the stage just read
-    stage = stage + 1 == S ? 0 : stage + 1;
+    if (!more) break;
+    first_unit = false;
+    load_qf();
+    reset();
     cur = nx;
+    stage = stage + 1 == S ? 0 : stage + 1;
   }
   cp_async_wait<0>();
   leave();
@@ -683,6 +707,7 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.U = a.Hkv * p.ngrp;
   p.num_pages = a.num_pages;
   p.page_size = a.page_size;
+  p.runs16 = a.page_size % 16 == 0;
   p.by_page = FastDiv(static_cast<unsigned>(a.page_size));
   p.cap = a.max_pages * a.page_size;
   p.n_cta = pl.n_cta;
@@ -709,12 +734,12 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
                           32 * PJ_WARPS, 0, a.stream, p);
 }
 
-// Groups of more than 16 query heads take two 16-row tiles a unit (K and V are then read once for 32 heads);
-// larger ones several units of 32.
+// Query heads a unit holds: 8, 16 or 32, whichever the group fits (larger groups take several units of 32, which
+// read K and V again).
 template <typename F>
 auto with_config(int G, int d, F&& f) {
-  if (d == 64) return G <= 16 ? f(PgCfg<64, 1>{}) : f(PgCfg<64, 2>{});
-  return G <= 16 ? f(PgCfg<128, 1>{}) : f(PgCfg<128, 2>{});
+  if (d == 64) return G <= 8 ? f(PgCfg<64, 1>{}) : G <= 16 ? f(PgCfg<64, 2>{}) : f(PgCfg<64, 4>{});
+  return G <= 8 ? f(PgCfg<128, 1>{}) : G <= 16 ? f(PgCfg<128, 2>{}) : f(PgCfg<128, 4>{});
 }
 
 }  // namespace
