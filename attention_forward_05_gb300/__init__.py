@@ -423,28 +423,45 @@ def fa_decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     return o
 
 
-def _need_cuda(**tensors) -> None:
-    dev = None
-    for n, t in tensors.items():
+# The entry points below are called once a generated token or layer, on tensors of a few kilobytes as on large ones, so
+# their host path counts: plain comparisons first, and messages only where one of them fails.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of torch.cuda.current_stream()'s time
+
+
+def _device_of(names: str, *tensors) -> int:
+    """The current device's index; raises unless every tensor given (None: not given) is on it."""
+    dev = -1
+    for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0 or (dev >= 0 and d != dev):
+            break
+        if dev < 0:
+            if d != torch.cuda.current_device():
+                break
+            dev = d
+    else:
+        return dev
+    for n, t in zip(names.split(), tensors):
+        if t is not None and not t.is_cuda:
             raise ValueError(f"{n} must be a CUDA tensor")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{n} is on {t.device}, not on the current device cuda:{dev}")
+        if t is not None and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{n} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    raise ValueError("no tensor given")
 
 
-def _strides(t: torch.Tensor) -> list[int]:
-    """The strides of all dimensions but the last; 0 for those of one entry, whose stride says nothing."""
-    return [s if n != 1 else 0 for s, n in zip(t.stride()[:-1], t.shape)]
+def _stream_of(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream_handle(stream)
 
 
 def _on_stream(stream, *tensors):
     """A context in which outputs and workspaces are allocated for `stream`.  Tensors used on a stream other than
     the current one are recorded there, so that the allocator does not hand their memory on while it is read."""
-    if stream is None or stream == torch.cuda.current_stream():
+    if stream == torch.cuda.current_stream():
         return contextlib.nullcontext()
     for t in tensors:
         if t is not None:
@@ -456,9 +473,13 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _last_contig(name: str, t: torch.Tensor) -> None:
-    if t.stride(-1) != 1:
+def _strides(name: str, t: torch.Tensor) -> list[int]:
+    """The strides of all dimensions but the last, which must be contiguous; 0 for those of one entry, whose stride
+    says nothing."""
+    s = t.stride()
+    if s[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    return [x if n != 1 else 0 for x, n in zip(s[:-1], t.shape)]
 
 
 def fa_rope_freqs(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -467,7 +488,6 @@ def fa_rope_freqs(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tens
 
 
 def _rotation(positions, freqs, axes):
-    _need_cuda(positions=positions, freqs=freqs, axes=axes)
     if positions.dtype != torch.int32 or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int32")
     if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
@@ -477,44 +497,62 @@ def _rotation(positions, freqs, axes):
 
 
 def _rope(q, k, positions, freqs, axes, interleaved, q_out, k_out, inverse, stream, where):
-    _need_cuda(q=q, k=k, q_out=q_out, k_out=k_out)
+    dev = _device_of("q k q_out k_out positions freqs axes", q, k, q_out, k_out, positions, freqs, axes)
     _rotation(positions, freqs, axes)
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4:
         raise ValueError("q [B,H,N,d], k [B,Hkv,N,d] expected")
-    if k is not None and k.dtype != q.dtype:
-        raise TypeError("q and k must share a dtype")
-    if k is None and k_out is not None:
+    B, H, N, d = shape
+    Hkv = 0
+    if k is not None:
+        ks = k.shape
+        if len(ks) != 4 or ks[0] != B or ks[2] != N or ks[3] != d:
+            raise ValueError("q [B,H,N,d], k [B,Hkv,N,d] expected")
+        if k.dtype != dtype:
+            raise TypeError("q and k must share a dtype")
+        Hkv = ks[1]
+    elif k_out is not None:
         raise ValueError("k_out without k")
-    B, H, N, d = q.shape
-    if positions.dim() == 1:  # [N]: one axis, the same for every batch entry
+    ps = tuple(positions.shape)
+    if len(ps) == 1:  # [N]: one axis, the same for every batch entry
         want, n_axes, shared = (N,), 1, 1
-    elif positions.dim() == 2:  # [B, N]: one axis
+    elif len(ps) == 2:  # [B, N]: one axis
         want, n_axes, shared = (B, N), 1, 0
     else:  # [axes, B, N] or, the same for every batch entry, [axes, 1, N]
-        n_axes = positions.shape[0]
-        shared = int(positions.dim() == 3 and positions.shape[1] == 1 and B > 1)
+        n_axes = ps[0]
+        shared = int(len(ps) == 3 and ps[1] == 1 and B > 1)
         want = (n_axes, 1 if shared else B, N)
-    if tuple(positions.shape) != want:
+    if ps != want:
         raise ValueError("positions [N], [B,N], [axes,B,N] or [axes,1,N] expected")
     code = _dtype_code(q)
-    with _on_stream(stream, q, k, q_out, k_out, positions, freqs, axes):
+    given = q_out is not None or k_out is not None
+    ctx = None if stream is None else _on_stream(stream, q, k, q_out, k_out, positions, freqs, axes)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if q_out is None:
-            q_out = torch.empty((B, H, N, d), device=q.device, dtype=q.dtype)
+            q_out = torch.empty(shape, device=q.device, dtype=dtype)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, device=k.device, dtype=k.dtype)
-    strides = []
-    for n, t, like in (("q", q, q), ("k", k, k), ("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is None:
-            strides += [0, 0, 0]
-            continue
-        _last_contig(n, t)
-        if t.shape != like.shape or t.dtype != like.dtype:
-            raise ValueError(f"{n} must match its input")
-        strides += _strides(t)
-    st = lib().fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), (ctypes.c_longlong * 12)(*strides), B, H,
-                       0 if k is None else k.shape[1], N, d, code, positions.data_ptr(), shared, freqs.data_ptr(),
-                       _ptr(axes), n_axes, 2 * freqs.shape[0], int(bool(interleaved)), inverse, _stream_handle(stream))
-    _check(st, where)
+            k_out = torch.empty(ks, device=k.device, dtype=dtype)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    strides = None  # all contiguous
+    if given or not q.is_contiguous() or (k is not None and not k.is_contiguous()):
+        strides = []
+        for n, t, like in (("q", q, q), ("k", k, k), ("q_out", q_out, q), ("k_out", k_out, k)):
+            if t is None:
+                strides += [0, 0, 0]
+                continue
+            if t.shape != like.shape or t.dtype != dtype:
+                raise ValueError(f"{n} must match its input")
+            strides += _strides(n, t)
+        strides = (ctypes.c_longlong * 12)(*strides)
+    st = (_lib or lib()).fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), strides, B, H, Hkv, N, d, code,
+                                 positions.data_ptr(), shared, freqs.data_ptr(), _ptr(axes), n_axes,
+                                 2 * freqs.shape[0], 1 if interleaved else 0, inverse, _stream_of(stream, dev))
+    if st:
+        _check(st, where)
     return q_out, k_out
 
 
@@ -538,18 +576,18 @@ def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tens
     return _rope(dq, dk, positions, freqs, axes, interleaved, dq_in, dk_in, 1, stream, "fa_rope (backward)")
 
 
-def _cache_shape(k_cache, v_cache):
-    _need_cuda(k_cache=k_cache, v_cache=v_cache)
+def _cache_strides(k_cache, v_cache):
+    """The strides of both caches as the C ABI takes them (None: contiguous); checks shape, dtype and layout."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("k_cache/v_cache [num_pages,Hkv,page_size,d] expected")
-    if not (k_cache.dtype == v_cache.dtype == torch.bfloat16):
+    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
         raise TypeError("the cache is bf16")
-    strides = _strides(k_cache)
-    if strides != _strides(v_cache):
+    if k_cache.is_contiguous() and v_cache.is_contiguous():
+        return None
+    strides = _strides("k_cache", k_cache)
+    if strides != _strides("v_cache", v_cache):
         raise ValueError("k_cache and v_cache must have the same strides")
-    _last_contig("k_cache", k_cache)
-    _last_contig("v_cache", v_cache)
-    return (*k_cache.shape, (ctypes.c_longlong * 3)(*strides))
+    return (ctypes.c_longlong * 3)(*strides)
 
 
 def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -562,44 +600,58 @@ def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     for both).  slots: int64 [T], page * page_size + row; a negative slot stores nothing.  positions (int32 [T] or
     [axes, T]) with freqs rotate k and q as fa_rope does; without them both are copied.  q [T, H, d] may be strided.
     """
-    _need_cuda(k=k, v=v, q=q, q_out=q_out, slots=slots)
-    P, Hkv, ps, d, cs = _cache_shape(k_cache, v_cache)
-    if k.dim() != 3 or k.shape != v.shape or tuple(k.shape[1:]) != (Hkv, d):
+    dev = _device_of("k v k_cache v_cache slots q q_out positions freqs axes", k, v, k_cache, v_cache, slots, q, q_out,
+                     positions, freqs, axes)
+    cs = _cache_strides(k_cache, v_cache)
+    P, Hkv, ps, d = k_cache.shape
+    shape = k.shape
+    T = shape[0]
+    if tuple(shape) != (T, Hkv, d) or v.shape != shape:
         raise ValueError("k/v [T,Hkv,d] of the cache's Hkv and d expected")
-    T = k.shape[0]
-    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d):
-        raise ValueError("q [T,H,d] expected")
-    if not (k.dtype == v.dtype == torch.bfloat16) or (q is not None and q.dtype != torch.bfloat16):
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or (q is not None and q.dtype != torch.bfloat16):
         raise TypeError("k, v and q are bf16")
     if slots.dtype != torch.int64 or tuple(slots.shape) != (T,) or not slots.is_contiguous():
         raise ValueError("slots must be contiguous int64 [T]")
     if (positions is None) != (freqs is None):
         raise ValueError("positions and freqs go together")
-    if q is None and q_out is not None:
-        raise ValueError("q_out without q")
     n_axes, rot = 1, 0
     if positions is not None:
         _rotation(positions, freqs, axes)
-        n_axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if tuple(positions.shape) not in ((T,), (n_axes, T)):
+        pshape = tuple(positions.shape)
+        n_axes = 1 if len(pshape) == 1 else pshape[0]
+        if pshape != (T,) and pshape != (n_axes, T):
             raise ValueError("positions [T] or [axes,T] expected")
         rot = 2 * freqs.shape[0]
-    for n, t in (("k", k), ("v", v), ("q", q)):
-        if t is not None:
-            _last_contig(n, t)
-    with _on_stream(stream, k, v, q, q_out, slots, positions, freqs, axes, k_cache, v_cache):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, device=q.device, dtype=q.dtype)
-    if q is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous()):
+    H = 0
+    if q is not None:
+        qs = q.shape
+        if len(qs) != 3 or qs[0] != T or qs[2] != d:
+            raise ValueError("q [T,H,d] expected")
+        H = qs[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    strides = None
+    if not (k.is_contiguous() and v.is_contiguous() and (q is None or q.is_contiguous())):
+        strides = (ctypes.c_longlong * 6)(*_strides("k", k), *_strides("v", v),
+                                          *((0, 0) if q is None else _strides("q", q)))
+    if stream is not None:
+        ctx = _on_stream(stream, k, v, q, q_out, slots, positions, freqs, axes, k_cache, v_cache)
+    if q is not None and q_out is None:
+        if stream is None:
+            q_out = torch.empty(qs, device=q.device, dtype=torch.bfloat16)
+        else:
+            with ctx:
+                q_out = torch.empty(qs, device=q.device, dtype=torch.bfloat16)
+    elif q is not None and (q_out.shape != qs or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous()):
         raise ValueError("q_out must be contiguous and match q")
-    strides = _strides(k) + _strides(v) + (_strides(q) if q is not None else [0, 0])
     if T == 0:
         return q_out
-    st = lib().fa_paged_append(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(),
-                               v_cache.data_ptr(), (ctypes.c_longlong * 6)(*strides), cs, slots.data_ptr(), T,
-                               0 if q is None else q.shape[1], Hkv, d, P, ps, _ptr(positions), _ptr(freqs), _ptr(axes),
-                               n_axes, rot, int(bool(interleaved)), _stream_handle(stream))
-    _check(st, "fa_paged_append")
+    st = (_lib or lib()).fa_paged_append(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(),
+                                         v_cache.data_ptr(), strides, cs, slots.data_ptr(), T, H, Hkv, d, P, ps,
+                                         _ptr(positions), _ptr(freqs), _ptr(axes), n_axes, rot,
+                                         1 if interleaved else 0, _stream_of(stream, dev))
+    if st:
+        _check(st, "fa_paged_append")
     return q_out
 
 
@@ -607,52 +659,73 @@ def fa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int, page_size:
     return int(lib().fa_decode_paged_workspace_bytes(B, H, Hkv, d, int(page_size), int(prefix_len)))
 
 
+_paged_ws_bytes: dict = {}  # workspace sizes by device and shape
+
+
 def _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale, workspace, with_lse, o,
                   stream, where):
-    _need_cuda(q=q, o=o, prefix_pages=prefix_pages, page_table=page_table, seq_lens=seq_lens,
-               workspace=workspace)
-    P, Hkv, ps, d, cs = _cache_shape(k_cache, v_cache)
-    if q.dim() not in (3, 4) or q.shape[-1] != d or (q.dim() == 4 and q.shape[2] != 1) or not q.is_contiguous():
+    dev = _device_of("q k_cache v_cache page_table seq_lens prefix_pages o workspace", q, k_cache, v_cache, page_table,
+                     seq_lens, prefix_pages, o, workspace)
+    cs = _cache_strides(k_cache, v_cache)
+    P, Hkv, ps, d = k_cache.shape
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != d or (len(shape) == 4 and shape[2] != 1) or not q.is_contiguous():
         raise ValueError("contiguous q [B,H,d] or [B,H,1,d] expected")
     if q.dtype != torch.bfloat16:
         raise TypeError("decode takes bf16 q, k, v")
-    B, H = q.shape[:2]
-    if H % Hkv != 0:
+    B, H = shape[0], shape[1]
+    if Hkv < 1 or H % Hkv != 0:
         raise ValueError("query heads must be a multiple of key/value heads")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be int32 [B, max_pages]")
     max_pages = page_table.shape[1]
+    row, col = page_table.stride()
     if max_pages < 1:
         raise ValueError("page_table must have a column")
-    if page_table.stride(1) != 1 and max_pages > 1:
+    if col != 1 and max_pages > 1:
         raise ValueError("page_table's rows must be contiguous")
+    if B == 1:
+        row = max_pages
     if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be contiguous int32 [B]")
-    if prefix_len:
-        if prefix_pages is None or prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1 \
-                or not prefix_pages.is_contiguous() or prefix_pages.shape[0] * ps < prefix_len:
-            raise ValueError("prefix_pages must be contiguous int32 and hold the prefix")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    L = lib()
-    with _on_stream(stream, q, k_cache, v_cache, prefix_pages, page_table, seq_lens, o, workspace):
-        if o is None:
-            o = torch.empty((B, H, d), device=q.device, dtype=torch.bfloat16)
-        lse = torch.empty((B, H), device=q.device, dtype=torch.float32) if with_lse else None
-        if workspace is None:
-            need = L.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, prefix_len)
-            workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
-    if o.dtype != torch.bfloat16 or o.numel() != B * H * d or not o.is_contiguous():
+    if prefix_len and (prefix_pages is None or prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1
+                       or not prefix_pages.is_contiguous() or not 0 < prefix_len <= prefix_pages.shape[0] * ps):
+        raise ValueError("prefix_pages must be contiguous int32 and hold the prefix")
+    if o is not None and (o.dtype != torch.bfloat16 or o.numel() != B * H * d or not o.is_contiguous()):
         raise ValueError("o must be contiguous bf16 [B,H,d]")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    if scale is None:
+        scale = d ** -0.5
+    L = _lib or lib()
+    ctx = None
+    if stream is not None:
+        ctx = _on_stream(stream, q, k_cache, v_cache, prefix_pages, page_table, seq_lens, o, workspace)
+        ctx.__enter__()
+    try:
+        device = q.device
+        if o is None:
+            o = torch.empty((B, H, d), device=device, dtype=torch.bfloat16)
+        lse = torch.empty((B, H), device=device, dtype=torch.float32) if with_lse else None
+        if workspace is None:
+            key = (dev, B, H, Hkv, d, ps, prefix_len)
+            need = _paged_ws_bytes.get(key)
+            if need is None:
+                need = L.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, prefix_len)
+                if len(_paged_ws_bytes) > 4096:
+                    _paged_ws_bytes.clear()
+                _paged_ws_bytes[key] = need
+            workspace = torch.empty(need, device=device, dtype=torch.uint8) if need else None
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = L.fa_decode_paged_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
-                                  _ptr(prefix_pages) if prefix_len else None, prefix_len, page_table.data_ptr(),
-                                  max(page_table.stride(0), max_pages) if B == 1 else page_table.stride(0),
-                                  seq_lens.data_ptr(), B, H, Hkv, d, P, ps, max_pages, cs, float(scale),
-                                  _ptr(workspace), ws_bytes, _ptr(lse), _stream_handle(stream))
-    _check(st, where)
+                                  prefix_pages.data_ptr() if prefix_len else None, prefix_len, page_table.data_ptr(),
+                                  row, seq_lens.data_ptr(), B, H, Hkv, d, P, ps, max_pages, cs, scale,
+                                  _ptr(workspace), ws_bytes, _ptr(lse), _stream_of(stream, dev))
+    if st:
+        _check(st, where)
     return o, lse
 
 
