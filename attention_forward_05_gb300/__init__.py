@@ -33,8 +33,8 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -423,137 +423,45 @@ def fa_decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     return o
 
 
-# The entry points below are called once a generated token or layer, on tensors of a few kilobytes as on large ones, so
-# their host path counts: plain comparisons first, and messages only where one of them fails.
+# The entry points below are called once a generated token or layer, on a few kilobytes as on large tensors, so their
+# host path counts: it is compiled (csrc/fa_binding.cpp; checks, allocations, the call of the C ABI).
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of torch.cuda.current_stream()'s time
-
-
-def _device_of(names: str, *tensors) -> int:
-    """The current device's index; raises unless every tensor given (None: not given) is on it."""
-    dev = -1
-    for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0 or (dev >= 0 and d != dev):
-            break
-        if dev < 0:
-            if d != torch.cuda.current_device():
-                break
-            dev = d
-    else:
-        return dev
-    for n, t in zip(names.split(), tensors):
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{n} must be a CUDA tensor")
-        if t is not None and t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{n} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
-    raise ValueError("no tensor given")
+_binding = None
 
 
-def _stream_of(stream, dev: int) -> int:
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    return _stream_handle(stream)
+def _load_binding():
+    """The compiled part of the binding (built first if stale).  Raises if it cannot be built or loaded."""
+    global _binding
+    lib()  # builds both, and loads the library that the binding links
+    with _lock:
+        if _binding is None:
+            spec = importlib.util.spec_from_file_location("_fa_binding", _build.BINDING)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _binding = module
+    return _binding
 
 
 def _on_stream(stream, *tensors):
-    """A context in which outputs and workspaces are allocated for `stream`.  Tensors used on a stream other than
-    the current one are recorded there, so that the allocator does not hand their memory on while it is read."""
-    if stream == torch.cuda.current_stream():
-        return contextlib.nullcontext()
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+    """Makes `stream` current, so that outputs and workspaces are allocated for it.  Tensors used on a stream other
+    than their own are recorded there, so that the allocator does not hand their memory on while it is read."""
+    if stream != torch.cuda.current_stream():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
-def _ptr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
-
-
-def _strides(name: str, t: torch.Tensor) -> list[int]:
-    """The strides of all dimensions but the last, which must be contiguous; 0 for those of one entry, whose stride
-    says nothing."""
-    s = t.stride()
-    if s[-1] != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return [x if n != 1 else 0 for x, n in zip(s[:-1], t.shape)]
+def _result(r, where: str):
+    """A binding call's tensors; raises for a status code."""
+    if r.__class__ is int:
+        _check(r, where)
+    return r
 
 
 def fa_rope_freqs(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
     """The usual frequencies theta^(-2i/rot), i < rot/2, as the float64 tensor that fa_rope and fa_paged_append take."""
     return theta ** (torch.arange(0, rot, 2, dtype=torch.float64, device=device) / -rot)
-
-
-def _rotation(positions, freqs, axes):
-    if positions.dtype != torch.int32 or not positions.is_contiguous():
-        raise ValueError("positions must be contiguous int32")
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError("freqs must be a contiguous float64 vector (radians per position)")
-    if axes is not None and (axes.dtype != torch.int32 or axes.shape != freqs.shape or not axes.is_contiguous()):
-        raise ValueError("axes must be contiguous int32, one entry a frequency")
-
-
-def _rope(q, k, positions, freqs, axes, interleaved, q_out, k_out, inverse, stream, where):
-    dev = _device_of("q k q_out k_out positions freqs axes", q, k, q_out, k_out, positions, freqs, axes)
-    _rotation(positions, freqs, axes)
-    shape, dtype = q.shape, q.dtype
-    if len(shape) != 4:
-        raise ValueError("q [B,H,N,d], k [B,Hkv,N,d] expected")
-    B, H, N, d = shape
-    Hkv = 0
-    if k is not None:
-        ks = k.shape
-        if len(ks) != 4 or ks[0] != B or ks[2] != N or ks[3] != d:
-            raise ValueError("q [B,H,N,d], k [B,Hkv,N,d] expected")
-        if k.dtype != dtype:
-            raise TypeError("q and k must share a dtype")
-        Hkv = ks[1]
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    ps = tuple(positions.shape)
-    if len(ps) == 1:  # [N]: one axis, the same for every batch entry
-        want, n_axes, shared = (N,), 1, 1
-    elif len(ps) == 2:  # [B, N]: one axis
-        want, n_axes, shared = (B, N), 1, 0
-    else:  # [axes, B, N] or, the same for every batch entry, [axes, 1, N]
-        n_axes = ps[0]
-        shared = int(len(ps) == 3 and ps[1] == 1 and B > 1)
-        want = (n_axes, 1 if shared else B, N)
-    if ps != want:
-        raise ValueError("positions [N], [B,N], [axes,B,N] or [axes,1,N] expected")
-    code = _dtype_code(q)
-    given = q_out is not None or k_out is not None
-    ctx = None if stream is None else _on_stream(stream, q, k, q_out, k_out, positions, freqs, axes)
-    if ctx is not None:
-        ctx.__enter__()
-    try:
-        if q_out is None:
-            q_out = torch.empty(shape, device=q.device, dtype=dtype)
-        if k is not None and k_out is None:
-            k_out = torch.empty(ks, device=k.device, dtype=dtype)
-    finally:
-        if ctx is not None:
-            ctx.__exit__(None, None, None)
-    strides = None  # all contiguous
-    if given or not q.is_contiguous() or (k is not None and not k.is_contiguous()):
-        strides = []
-        for n, t, like in (("q", q, q), ("k", k, k), ("q_out", q_out, q), ("k_out", k_out, k)):
-            if t is None:
-                strides += [0, 0, 0]
-                continue
-            if t.shape != like.shape or t.dtype != dtype:
-                raise ValueError(f"{n} must match its input")
-            strides += _strides(n, t)
-        strides = (ctypes.c_longlong * 12)(*strides)
-    st = (_lib or lib()).fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), strides, B, H, Hkv, N, d, code,
-                                 positions.data_ptr(), shared, freqs.data_ptr(), _ptr(axes), n_axes,
-                                 2 * freqs.shape[0], 1 if interleaved else 0, inverse, _stream_of(stream, dev))
-    if st:
-        _check(st, where)
-    return q_out, k_out
 
 
 def fa_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freqs: torch.Tensor,
@@ -566,28 +474,22 @@ def fa_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fr
     axis of each pair.  q and k may be strided views (heads of a projection's output); new outputs are contiguous.
     An output may be its input itself; otherwise it must overlap no input.
     """
-    return _rope(q, k, positions, freqs, axes, interleaved, q_out, k_out, 0, stream, "fa_rope")
+    if stream is not None:
+        with _on_stream(stream, q, k, positions, freqs, axes, q_out, k_out):
+            return fa_rope(q, k, positions, freqs, axes, interleaved, q_out, k_out)
+    r = (_binding or _load_binding()).rope(q, k, positions, freqs, axes, interleaved, q_out, k_out, False)
+    return r if r.__class__ is tuple else _result(r, "fa_rope")
 
 
 def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor, freqs: torch.Tensor,
                 axes: torch.Tensor | None = None, interleaved: bool = False, dq_in: torch.Tensor | None = None,
                 dk_in: torch.Tensor | None = None, stream=None):
     """The backward pass of fa_rope: gradients of its outputs in, gradients (dq_in, dk_in) of its q and k out."""
-    return _rope(dq, dk, positions, freqs, axes, interleaved, dq_in, dk_in, 1, stream, "fa_rope (backward)")
-
-
-def _cache_strides(k_cache, v_cache):
-    """The strides of both caches as the C ABI takes them (None: contiguous); checks shape, dtype and layout."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache/v_cache [num_pages,Hkv,page_size,d] expected")
-    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
-        raise TypeError("the cache is bf16")
-    if k_cache.is_contiguous() and v_cache.is_contiguous():
-        return None
-    strides = _strides("k_cache", k_cache)
-    if strides != _strides("v_cache", v_cache):
-        raise ValueError("k_cache and v_cache must have the same strides")
-    return (ctypes.c_longlong * 3)(*strides)
+    if stream is not None:
+        with _on_stream(stream, dq, dk, positions, freqs, axes, dq_in, dk_in):
+            return fa_rope_bwd(dq, dk, positions, freqs, axes, interleaved, dq_in, dk_in)
+    r = (_binding or _load_binding()).rope(dq, dk, positions, freqs, axes, interleaved, dq_in, dk_in, True)
+    return r if r.__class__ is tuple else _result(r, "fa_rope (backward)")
 
 
 def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -600,133 +502,27 @@ def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     for both).  slots: int64 [T], page * page_size + row; a negative slot stores nothing.  positions (int32 [T] or
     [axes, T]) with freqs rotate k and q as fa_rope does; without them both are copied.  q [T, H, d] may be strided.
     """
-    dev = _device_of("k v k_cache v_cache slots q q_out positions freqs axes", k, v, k_cache, v_cache, slots, q, q_out,
-                     positions, freqs, axes)
-    cs = _cache_strides(k_cache, v_cache)
-    P, Hkv, ps, d = k_cache.shape
-    shape = k.shape
-    T = shape[0]
-    if tuple(shape) != (T, Hkv, d) or v.shape != shape:
-        raise ValueError("k/v [T,Hkv,d] of the cache's Hkv and d expected")
-    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or (q is not None and q.dtype != torch.bfloat16):
-        raise TypeError("k, v and q are bf16")
-    if slots.dtype != torch.int64 or tuple(slots.shape) != (T,) or not slots.is_contiguous():
-        raise ValueError("slots must be contiguous int64 [T]")
-    if (positions is None) != (freqs is None):
-        raise ValueError("positions and freqs go together")
-    n_axes, rot = 1, 0
-    if positions is not None:
-        _rotation(positions, freqs, axes)
-        pshape = tuple(positions.shape)
-        n_axes = 1 if len(pshape) == 1 else pshape[0]
-        if pshape != (T,) and pshape != (n_axes, T):
-            raise ValueError("positions [T] or [axes,T] expected")
-        rot = 2 * freqs.shape[0]
-    H = 0
-    if q is not None:
-        qs = q.shape
-        if len(qs) != 3 or qs[0] != T or qs[2] != d:
-            raise ValueError("q [T,H,d] expected")
-        H = qs[1]
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    strides = None
-    if not (k.is_contiguous() and v.is_contiguous() and (q is None or q.is_contiguous())):
-        strides = (ctypes.c_longlong * 6)(*_strides("k", k), *_strides("v", v),
-                                          *((0, 0) if q is None else _strides("q", q)))
     if stream is not None:
-        ctx = _on_stream(stream, k, v, q, q_out, slots, positions, freqs, axes, k_cache, v_cache)
-    if q is not None and q_out is None:
-        if stream is None:
-            q_out = torch.empty(qs, device=q.device, dtype=torch.bfloat16)
-        else:
-            with ctx:
-                q_out = torch.empty(qs, device=q.device, dtype=torch.bfloat16)
-    elif q is not None and (q_out.shape != qs or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous()):
-        raise ValueError("q_out must be contiguous and match q")
-    if T == 0:
-        return q_out
-    st = (_lib or lib()).fa_paged_append(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), k_cache.data_ptr(),
-                                         v_cache.data_ptr(), strides, cs, slots.data_ptr(), T, H, Hkv, d, P, ps,
-                                         _ptr(positions), _ptr(freqs), _ptr(axes), n_axes, rot,
-                                         1 if interleaved else 0, _stream_of(stream, dev))
-    if st:
-        _check(st, "fa_paged_append")
-    return q_out
+        with _on_stream(stream, k, v, k_cache, v_cache, slots, q, positions, freqs, axes, q_out):
+            return fa_paged_append(k, v, k_cache, v_cache, slots, q, positions, freqs, axes, interleaved, q_out)
+    r = (_binding or _load_binding()).append(k, v, k_cache, v_cache, slots, q, positions, freqs, axes, interleaved,
+                                             q_out)
+    return _result(r, "fa_paged_append")
 
 
 def fa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int, page_size: int, prefix_len: int = 0) -> int:
     return int(lib().fa_decode_paged_workspace_bytes(B, H, Hkv, d, int(page_size), int(prefix_len)))
 
 
-_paged_ws_bytes: dict = {}  # workspace sizes by device and shape
-
-
 def _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale, workspace, with_lse, o,
                   stream, where):
-    dev = _device_of("q k_cache v_cache page_table seq_lens prefix_pages o workspace", q, k_cache, v_cache, page_table,
-                     seq_lens, prefix_pages, o, workspace)
-    cs = _cache_strides(k_cache, v_cache)
-    P, Hkv, ps, d = k_cache.shape
-    shape = q.shape
-    if len(shape) not in (3, 4) or shape[-1] != d or (len(shape) == 4 and shape[2] != 1) or not q.is_contiguous():
-        raise ValueError("contiguous q [B,H,d] or [B,H,1,d] expected")
-    if q.dtype != torch.bfloat16:
-        raise TypeError("decode takes bf16 q, k, v")
-    B, H = shape[0], shape[1]
-    if Hkv < 1 or H % Hkv != 0:
-        raise ValueError("query heads must be a multiple of key/value heads")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be int32 [B, max_pages]")
-    max_pages = page_table.shape[1]
-    row, col = page_table.stride()
-    if max_pages < 1:
-        raise ValueError("page_table must have a column")
-    if col != 1 and max_pages > 1:
-        raise ValueError("page_table's rows must be contiguous")
-    if B == 1:
-        row = max_pages
-    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be contiguous int32 [B]")
-    if prefix_len and (prefix_pages is None or prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1
-                       or not prefix_pages.is_contiguous() or not 0 < prefix_len <= prefix_pages.shape[0] * ps):
-        raise ValueError("prefix_pages must be contiguous int32 and hold the prefix")
-    if o is not None and (o.dtype != torch.bfloat16 or o.numel() != B * H * d or not o.is_contiguous()):
-        raise ValueError("o must be contiguous bf16 [B,H,d]")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    if scale is None:
-        scale = d ** -0.5
-    L = _lib or lib()
-    ctx = None
     if stream is not None:
-        ctx = _on_stream(stream, q, k_cache, v_cache, prefix_pages, page_table, seq_lens, o, workspace)
-        ctx.__enter__()
-    try:
-        device = q.device
-        if o is None:
-            o = torch.empty((B, H, d), device=device, dtype=torch.bfloat16)
-        lse = torch.empty((B, H), device=device, dtype=torch.float32) if with_lse else None
-        if workspace is None:
-            key = (dev, B, H, Hkv, d, ps, prefix_len)
-            need = _paged_ws_bytes.get(key)
-            if need is None:
-                need = L.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, prefix_len)
-                if len(_paged_ws_bytes) > 4096:
-                    _paged_ws_bytes.clear()
-                _paged_ws_bytes[key] = need
-            workspace = torch.empty(need, device=device, dtype=torch.uint8) if need else None
-    finally:
-        if ctx is not None:
-            ctx.__exit__(None, None, None)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = L.fa_decode_paged_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
-                                  prefix_pages.data_ptr() if prefix_len else None, prefix_len, page_table.data_ptr(),
-                                  row, seq_lens.data_ptr(), B, H, Hkv, d, P, ps, max_pages, cs, scale,
-                                  _ptr(workspace), ws_bytes, _ptr(lse), _stream_of(stream, dev))
-    if st:
-        _check(st, where)
-    return o, lse
+        with _on_stream(stream, q, k_cache, v_cache, prefix_pages, page_table, seq_lens, workspace, o):
+            return _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale, workspace,
+                                 with_lse, o, None, where)
+    r = (_binding or _load_binding()).decode(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale,
+                                             workspace, with_lse, o)
+    return r if r.__class__ is tuple else _result(r, where)
 
 
 def fa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
@@ -751,7 +547,7 @@ def fa_decode_paged_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     page_table and seq_lens describe each sequence's own rows behind the prefix; a negative length marks an unused
     place of a padded batch, which sees nothing.
     """
-    return _decode_paged(q, k_cache, v_cache, prefix_pages, int(prefix_len), page_table, seq_lens, scale, workspace,
+    return _decode_paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale, workspace,
                          with_lse, o, stream, "fa_decode_paged_prefix")
 
 
