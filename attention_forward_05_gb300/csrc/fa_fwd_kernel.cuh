@@ -99,10 +99,16 @@ struct FwdCfg {
   static constexpr int COLS = BC;         // key columns of one softmax thread (one query row)
   static constexpr int PCOLS_W = P_COLS;  // P columns written by one softmax warpgroup
   static constexpr int OCOLS = D;         // O columns rescaled and stored by one softmax warpgroup
-  static constexpr int NWARPS = 4 * NQT + 2;
+  // PAGED with two query tiles and d = 128: a second load warp takes the values.  Small pages need many small copies,
+  // and issuing them (about 45 ns each) for both tiles of a step takes one warp longer than the step's products: with
+  // 16-row pages, 16384 keys and 1024 queries a head, the kernel went from 73 to 59 us.  Its registers are free: 12
+  // warps take as many a thread as 10.
+  static constexpr bool SPLIT_LOADS = PAGED && NQT == 2 && D == 128;
+  static constexpr int NWARPS = 4 * NQT + 2 + (SPLIT_LOADS ? 1 : 0);
   static constexpr int NTHREADS = 32 * NWARPS;
   static constexpr int LOAD_WARP = 4 * NQT;
   static constexpr int MMA_WARP = 4 * NQT + 1;
+  static constexpr int LOADV_WARP = SPLIT_LOADS ? 4 * NQT + 2 : LOAD_WARP;
   // Registers per thread: each of the SM's 4 sub-partitions holds 16384 registers and
   // ceil(warps per SM / 4) warps, in 8-register steps.
   static constexpr int WARPS_PER_SUBPART = (NWARPS * MINB + 3) / 4;
@@ -340,13 +346,14 @@ __global__ void __maxnreg__(C::MAXREG)
   griddep_wait();
   griddep_launch_dependents();
 
-  if (C::PAGED && warp == C::LOAD_WARP) {
+  if (C::PAGED && (warp == C::LOAD_WARP || warp == C::LOADV_WARP)) {
     if constexpr (C::PAGED) {
       // ------------------------------------------------------------ TMA producer, paged
       // Lane i copies the i-th box of a tile, from the page that it looked up one tile ahead.  Boxes past the last key
       // and boxes of a bad page are read past the cache's last page: zeros.  The rows of the last page behind the last
       // key hold anything: as keys they are masked, as values the warp zeroes them in shared memory (0 * NaN would
       // reach O) and hands the tile over itself.
+      const bool do_k = warp == C::LOAD_WARP, do_v = warp == C::LOADV_WARP;
       const int boxes = C::BC / p.box_rows;
       int nk_done = 0, nv_done = 0;
       bool tail_done = false;
@@ -377,9 +384,15 @@ __global__ void __maxnreg__(C::MAXREG)
                           p.heads_inner ? kvh : row, p.heads_inner ? row : kvh, page);
           }
         };
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_ke(s), ph, abort_flag, p.err, W_KE))) break;
-        copy(&tm_k, sbase + C::OFF_K + s * C::KV_BYTES, bar_kf(s));
-        nk_done = j + 1;
+        if (do_k) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_ke(s), ph, abort_flag, p.err, W_KE))) break;
+          copy(&tm_k, sbase + C::OFF_K + s * C::KV_BYTES, bar_kf(s));
+          nk_done = j + 1;
+        }
+        if (!do_v) {
+          page = next_page;
+          continue;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(bar_ve(s), ph, abort_flag, p.err, W_VE))) break;
         const uint32_t dv = sbase + C::OFF_V + s * C::KV_BYTES;
         copy(&tm_v, dv, ragged ? bar_tail : bar_vf(s));

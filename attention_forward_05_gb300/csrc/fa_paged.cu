@@ -539,24 +539,27 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
 }
 
 // Joins the parts of units that several CTAs share, and with a shared prefix the prefix's states and every
-// sequence's own, and writes the outputs.  A CTA takes every gridDim.x-th (sequence, query head); its four warps
-// take every fourth state, eight states' rows in flight, with the online-softmax recurrence, and add up in warp
-// order.  Bound by latency: a handful of dependent loads.  (It does not let the next kernel start early: CTAs of
-// the next call's fa_paged_kernel placed between these were spread unevenly over the SMs, and its time on 32
-// sequences of 32768 keys went from 304 to 325 us.)
+// sequence's own, and writes the outputs.  A team of WPR warps takes every (number of teams)-th (sequence, query
+// head): its warps take every WPR-th state, eight states' rows in flight, with the online-softmax recurrence, and add
+// up in warp order.  Bound by latency, a handful of dependent loads: four warps a row while there are CTAs for all
+// rows, one warp a row beyond.  (It does not let the next kernel start early: CTAs of the next call's fa_paged_kernel
+// placed between these were spread unevenly over the SMs, and its time on 32 sequences of 32768 keys went from 304 to
+// 325 us.)
 constexpr int PJ_WARPS = 4;
-template <int D, int GR>
+template <int D, int GR, int WPR>
 __global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgParams p) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, TEAMS = PJ_WARPS / WPR;
   __shared__ float sm_o[PJ_WARPS][D];
   __shared__ float2 sm_ml[PJ_WARPS];
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WPR;  // the warp's place in its team
   const long long heads = static_cast<long long>(p.B) * p.H;
+  const long long team = static_cast<long long>(blockIdx.x) * TEAMS + (threadIdx.x >> 5) / WPR;
+  const long long teams = static_cast<long long>(gridDim.x) * TEAMS;
   const float nan = __int_as_float(0x7fc00000);
-  for (long long k0 = blockIdx.x; k0 < heads; k0 += 32LL * gridDim.x) {
-    // this CTA's next 32 rows: what there is to do for each
-    const long long mine = k0 + static_cast<long long>(lane) * gridDim.x;
+  for (long long k0 = team; k0 < heads; k0 += 32 * teams) {
+    // this team's next 32 rows: what there is to do for each
+    const long long mine = k0 + lane * teams;
     int2 info = make_int2(-1, 1);
     if (mine < heads) {
       const int h = static_cast<int>(mine % p.H);
@@ -566,23 +569,23 @@ __global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgPa
     while (todo != 0) {
       const int k = __ffs(todo) - 1;
       todo &= todo - 1;
-      const long long head = k0 + static_cast<long long>(k) * gridDim.x;
+      const long long head = k0 + k * teams;
       const int slot = __shfl_sync(0xffffffffu, info.x, k), own = __shfl_sync(0xffffffffu, info.y, k);
-      const int b = static_cast<int>(head / p.H), h = static_cast<int>(head % p.H);
-      const int hk = h / p.G, g = h % p.G;
-      const long long pstep = static_cast<long long>(p.B) * p.H;
+      const int b = static_cast<int>(head / p.H), h = static_cast<int>(head - static_cast<long long>(b) * p.H);
+      const int hk = h / p.G, g = h - hk * p.G;
+      const long long pstep = heads;
       const long long prow = (static_cast<long long>(hk) * p.B + b) * p.G + g;
       const int pre = own < 0 ? 0 : p.pre_split;
       const int parts = own < 0 ? 0 : pre + own;
       float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = 0.f;
-      for (int s0 = warp; s0 < parts; s0 += 8 * PJ_WARPS) {
+      for (int s0 = warp; s0 < parts; s0 += 8 * WPR) {
         float2 x[8];
         float v[8][E];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int s = s0 + i * PJ_WARPS;
+          const int s = s0 + i * WPR;
           x[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[i][e] = 0.f;
@@ -626,29 +629,36 @@ __global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgPa
           for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
         }
       }
+      if constexpr (WPR > 1) {
+        static_assert(WPR == 1 || WPR == PJ_WARPS, "a team is a warp or the CTA");
 #pragma unroll
-      for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
-      if (lane == 0) sm_ml[warp] = make_float2(M, L);
-      __syncthreads();
-      if (threadIdx.x < D) {
+        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+        if (lane == 0) sm_ml[warp] = make_float2(M, L);
+        __syncthreads();
         M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < PJ_WARPS; ++w) M = fmaxf(M, sm_ml[w].x);
+        for (int w = 0; w < WPR; ++w) M = fmaxf(M, sm_ml[w].x);
         const float ref = M == -INFINITY ? 0.f : M;
-        float O = 0.f;
         L = 0.f;
 #pragma unroll
-        for (int w = 0; w < PJ_WARPS; ++w) {
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
           const float wt = ex2_approx(sm_ml[w].x - ref);
           L = fmaf(sm_ml[w].y, wt, L);
-          O = fmaf(sm_o[w][threadIdx.x], wt, O);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(sm_o[w][lane * E + e], wt, acc[e]);
         }
+        __syncthreads();
+      }
+      if (warp == 0) {
         const float inv = own == -2 ? nan : parts == 0 ? 0.f : 1.f / L;
-        p.o[head * D + threadIdx.x] = __float2bfloat16_rn(O * inv);
-        if (p.lse != nullptr && threadIdx.x == 0)
+        uint32_t* out = reinterpret_cast<uint32_t*>(p.o + head * D) + lane * (E / 2);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        if (p.lse != nullptr && lane == 0)
           p.lse[head] = own == -2 ? nan : parts == 0 ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       }
-      __syncthreads();
     }
   }
 }
@@ -732,7 +742,11 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   // programmatic dependents: a launch overlaps the end of the kernel before it
   if ((e = launch_dependent(fa_paged_kernel<C>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
   const long long heads = static_cast<long long>(a.B) * a.H, most = static_cast<long long>(a.sms) * 16;
-  return launch_dependent(fa_paged_join_kernel<C::D, C::GR>, static_cast<unsigned>(heads < most ? heads : most),
+  if (heads <= most)
+    return launch_dependent(fa_paged_join_kernel<C::D, C::GR, PJ_WARPS>, static_cast<unsigned>(heads), 32 * PJ_WARPS, 0,
+                            a.stream, p);
+  const long long ctas = (heads + PJ_WARPS - 1) / PJ_WARPS;
+  return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 1>, static_cast<unsigned>(ctas < most ? ctas : most),
                           32 * PJ_WARPS, 0, a.stream, p);
 }
 
