@@ -672,17 +672,23 @@ __global__ void __maxnreg__(C::MAXREG)
       // This warp's 32 rows of Q into the swizzled tile, 16 bytes a lane; rows past the last query are zeros.
       constexpr int PIECES = C::D / 8;         // 16-byte pieces of a row
       constexpr int RP = 32 / PIECES;          // rows at a time
+      constexpr int FLY = 8;                   // loads in flight (a store to shared memory would hold up the next load)
+      const int pc = lane % PIECES;
 #pragma unroll
-      for (int i = 0; i < 32 / RP; ++i) {
-        const int r = wq * 32 + i * RP + lane / PIECES, pc = lane % PIECES;
-        const int qrow = q0 + t * C::BR + r;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (qrow < p.Nq) {
+      for (int i0 = 0; i0 < 32 / RP; i0 += FLY) {
+        uint4 w[FLY];
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) {
+          const int qrow = q0 + t * C::BR + wq * 32 + (i0 + i) * RP + lane / PIECES;
           const long long head = static_cast<long long>(qrow / p.G) * p.Hkv * p.G + bh * p.G + qrow % p.G;
-          w = *reinterpret_cast<const uint4*>(p.q + head * C::D + pc * 8);
+          w[i] = qrow < p.Nq ? *reinterpret_cast<const uint4*>(p.q + head * C::D + pc * 8) : make_uint4(0, 0, 0, 0);
         }
-        *reinterpret_cast<uint4*>(smem + C::OFF_Q + t * C::Q_BYTES + pc / 8 * C::Q_CH_BYTES + r * 128 +
-                                  ((pc % 8 ^ (r & 7)) << 4)) = w;
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) {
+          const int r = wq * 32 + (i0 + i) * RP + lane / PIECES;
+          *reinterpret_cast<uint4*>(smem + C::OFF_Q + t * C::Q_BYTES + pc / 8 * C::Q_CH_BYTES + r * 128 +
+                                    ((pc % 8 ^ (r & 7)) << 4)) = w[i];
+        }
       }
       fence_proxy_async();
       __syncwarp();
