@@ -58,7 +58,7 @@ def _torch_flags() -> tuple[list[str], list[str]]:
            sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
     lib = os.path.join(root, "lib")
     return ([f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f"-I{d}" for d in inc]],
-            [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"])
+            [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

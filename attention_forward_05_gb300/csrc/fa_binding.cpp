@@ -8,7 +8,9 @@
 // fa_status code of a call that the library refused.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -127,8 +129,9 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
+// A new tensor beside `t`, from PyTorch's allocator on the current stream.
 Tensor empty_like_shape(at::IntArrayRef sizes, const Tensor& t, at::ScalarType type) {
-  return at::empty(sizes, t.options().dtype(type).requires_grad(false).memory_format(std::nullopt));
+  return Tensor(at::detail::empty_cuda(sizes, type, t.device(), std::nullopt));
 }
 
 // Frequencies and axes of a rotation.
@@ -292,7 +295,8 @@ PyObject* decode(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     need_args(n_in, 11);
     const Arg q = arg(in[0], "q"), kc = arg(in[1], "k_cache"), vc = arg(in[2], "v_cache"),
               pre = arg(in[3], "prefix_pages", true), table = arg(in[5], "page_table"), lens = arg(in[6], "seq_lens");
-    Arg ws = arg(in[8], "workspace", true), o = arg(in[10], "o", true);
+    const Arg ws = arg(in[8], "workspace", true);
+    Arg o = arg(in[10], "o", true);
     need_cuda(q, kc, vc, pre, table, lens, ws, o);
     const int dev = same_device(q, kc, vc, pre, table, lens, ws, o);
     long long cs[3];
@@ -324,27 +328,31 @@ PyObject* decode(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     need_contiguous(ws);
     const int Bi = as_int(B, "B"), Hi = as_int(H, "H"), hk = as_int(Hkv, "Hkv"), di = as_int(d, "d"),
               psi = as_int(ps, "page_size"), pages = as_int(kc->size(0), "num_pages"), mp = as_int(max_pages, "max_pages");
-    Tensor o_new, lse, ws_new;
+    Tensor o_new, lse;
     if (!o) {
       o_new = empty_like_shape({B, H, d}, *q, at::kBFloat16);
       o.t = &o_new;
     }
     if (truth(in[9])) lse = empty_like_shape({B, H}, *q, at::kFloat);
+    // The workspace goes back to the allocator when this returns: later work that gets it is behind this call's on the
+    // current stream.
+    c10::DataPtr own_ws;
+    void* ws_ptr = ws.ptr();
+    size_t ws_bytes = ws ? ws->nbytes() : 0;
     if (!ws) {
-      const size_t need = fa_decode_paged_workspace_bytes(Bi, Hi, hk, di, psi, static_cast<int>(plen));
-      if (need > 0) {  // 0: arguments that the call below refuses
-        ws_new = empty_like_shape({static_cast<int64_t>(need)}, *q, at::kByte);
-        ws.t = &ws_new;
+      ws_bytes = fa_decode_paged_workspace_bytes(Bi, Hi, hk, di, psi, static_cast<int>(plen));
+      if (ws_bytes > 0) {  // 0: arguments that the call below refuses
+        own_ws = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
+        ws_ptr = own_ws.get();
       }
     }
-    const size_t ws_bytes = ws ? ws->nbytes() : 0;
     const long long row = B == 1 ? mp : table->stride(0);
     int st;
     Py_BEGIN_ALLOW_THREADS;
     st = fa_decode_paged_prefix(q.ptr(), kc.ptr(), vc.ptr(), o.ptr(), plen ? static_cast<const int*>(pre.ptr()) : nullptr,
                                 static_cast<int>(plen), static_cast<const int*>(table.ptr()), row,
                                 static_cast<const int*>(lens.ptr()), Bi, Hi, hk, di, pages, psi, mp, cs,
-                                static_cast<float>(scale), ws.ptr(), ws_bytes,
+                                static_cast<float>(scale), ws_ptr, ws_bytes,
                                 lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream_of(dev));
     Py_END_ALLOW_THREADS;
     if (st != FA_OK) return PyLong_FromLong(st);

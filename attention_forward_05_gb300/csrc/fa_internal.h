@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <utility>
 
 #include <nvtx3/nvToolsExt.h>
@@ -45,6 +46,18 @@ int current_device_status();
 
 // The same with what the launch code needs: the device's error word and SM count.
 int current_device_info(int** err, int* sms);
+
+// Lets `kernel` have more than 48 KB of dynamic shared memory on the current device: set at its first launch there.
+template <auto kernel>
+cudaError_t allow_shared_memory(int bytes) {
+  static std::atomic<unsigned long long> done{0};  // one bit a device (fa_api.cu takes up to 64)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (done.load(std::memory_order_acquire) >> dev & 1u)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
 
 // Records a CUDA error for fa_last_cuda_error() and returns FA_ERR_CUDA.
 int report_cuda_error(cudaError_t e);

@@ -728,7 +728,7 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.part_ml = reinterpret_cast<float*>(a.ws + pl.part_ml);
   p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
   p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
-  cudaError_t e = cudaFuncSetAttribute(fa_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = allow_shared_memory<fa_paged_kernel<C>>(C::SMEM);
   if (e != cudaSuccess) return e;
   if (a.prefix_len > 0) {
     p.prefix = 1;

@@ -11,6 +11,8 @@
 // one where the B * G rows of a head fit in it.
 #include <cuda_bf16.h>
 
+#include <cmath>
+
 #include "fa_fwd_kernel.cuh"
 
 namespace fa {
@@ -64,20 +66,22 @@ __global__ void __launch_bounds__(256) gather_prefix_kernel(const uint4* __restr
 
 template <class C>
 void plan_cfg(int rows, int Hkv, int prefix_len, int sms, PagedPlan* pl) {
-  const long long tiles = (prefix_len + C::BC - 1) / C::BC;
-  const long long ctas = static_cast<long long>(Hkv) * ((rows + C::BR * C::NQT - 1) / (C::BR * C::NQT));
-  const long long slots = static_cast<long long>(sms) * C::MINB;
+  const int tiles = (prefix_len + C::BC - 1) / C::BC;
+  const double ctas = static_cast<double>(Hkv) * ((rows + C::BR * C::NQT - 1) / (C::BR * C::NQT));
+  const double slots = static_cast<double>(sms) * C::MINB;
   // Key splits: the waves of CTAs times a CTA's key tiles, plus about three tiles' time to start and end a CTA,
   // plus the splits' states written and read (in units of a tile's time, 1.2 us).
   const double merge = static_cast<double>(rows) * Hkv * C::D * 8 / 4e6 / 1.2;
   double best = 0;
-  for (long long n = 1; n <= 64 && n <= tiles; ++n) {
-    const long long per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
-    const double t = static_cast<double>((ctas * used + slots - 1) / slots) * (per + 3) + used * merge;
+  for (int n = 1, last = 0; n <= 64 && n <= tiles; ++n) {
+    const int per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
+    if (used == last) continue;
+    last = used;
+    const double t = std::ceil(ctas * used / slots) * (per + 3) + used * merge;
     if (n == 1 || t < best) {
       best = t;
-      pl->n_split = static_cast<int>(used);
-      pl->kv_per_split = static_cast<int>(per) * C::BC;
+      pl->n_split = used;
+      pl->kv_per_split = per * C::BC;
     }
   }
 }
