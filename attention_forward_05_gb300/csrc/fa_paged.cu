@@ -541,16 +541,14 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
 // Joins the parts of units that several CTAs share, and with a shared prefix the prefix's states and every
 // sequence's own, and writes the outputs.  A team of WPR warps takes every (number of teams)-th (sequence, query
 // head): its warps take every WPR-th state, eight states' rows in flight, with the online-softmax recurrence, and add
-// up in warp order.  Bound by latency, a handful of dependent loads: four warps a row while there are CTAs for all
-// rows, one warp a row beyond.  (It does not let the next kernel start early: CTAs of the next call's fa_paged_kernel
-// placed between these were spread unevenly over the SMs, and its time on 32 sequences of 32768 keys went from 304 to
-// 325 us.)
-constexpr int PJ_WARPS = 4;
+// up in warp order.  Bound by latency, a handful of dependent loads, so WPR goes with the states a row is likely to
+// have (join_warps).  (It does not let the next kernel start early: CTAs of the next call's fa_paged_kernel placed
+// between these were spread unevenly over the SMs, and its time on 32 sequences of 32768 keys went from 304 to 325 us.)
 template <int D, int GR, int WPR>
-__global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgParams p) {
-  constexpr int E = D / 32, TEAMS = PJ_WARPS / WPR;
-  __shared__ float sm_o[PJ_WARPS][D];
-  __shared__ float2 sm_ml[PJ_WARPS];
+__global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR) fa_paged_join_kernel(const PgParams p) {
+  constexpr int E = D / 32, TEAMS = WPR == 1 ? 4 : 1;
+  __shared__ float sm_o[WPR][D];
+  __shared__ float2 sm_ml[WPR];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WPR;  // the warp's place in its team
   const long long heads = static_cast<long long>(p.B) * p.H;
@@ -630,7 +628,6 @@ __global__ void __launch_bounds__(32 * PJ_WARPS) fa_paged_join_kernel(const PgPa
         }
       }
       if constexpr (WPR > 1) {
-        static_assert(WPR == 1 || WPR == PJ_WARPS, "a team is a warp or the CTA");
 #pragma unroll
         for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
         if (lane == 0) sm_ml[warp] = make_float2(M, L);
@@ -697,6 +694,17 @@ PagedPlan plan_of(int B, int H, int Hkv, int page_size, int prefix_len, int sms)
   return pl;
 }
 
+// Warps that join a row's states, at eight states a warp in flight.  A unit has about n_cta / units + 1 own parts and
+// at most one a tile (the lengths, and so the parts, are not known here), and the prefix's splits.  One warp a row where
+// that is at most eight and the rows alone fill the GPU (2048 rows of 64 equal sequences: 28 instead of 32 us with
+// four), four otherwise, because a ragged batch's longest sequence has many more (320 rows: 17 instead of 20 us with
+// one); sixteen for a few rows of very many states (one sequence of 32768 keys: 19 instead of 20 us with four).
+int join_warps(long long units, long long heads, long long tiles, const PagedPlan& pl, int sms) {
+  const long long share = pl.n_cta / units, parts = (share < tiles ? share : tiles) + 1 + pl.n_split;
+  if (parts > 32 && heads <= sms) return 16;
+  return parts > 8 || heads <= 8LL * sms ? 4 : 1;
+}
+
 template <class C>
 cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   PgParams p = {};
@@ -742,12 +750,16 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   // programmatic dependents: a launch overlaps the end of the kernel before it
   if ((e = launch_dependent(fa_paged_kernel<C>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
   const long long heads = static_cast<long long>(a.B) * a.H, most = static_cast<long long>(a.sms) * 16;
-  if (heads <= most)
-    return launch_dependent(fa_paged_join_kernel<C::D, C::GR, PJ_WARPS>, static_cast<unsigned>(heads), 32 * PJ_WARPS, 0,
-                            a.stream, p);
-  const long long ctas = (heads + PJ_WARPS - 1) / PJ_WARPS;
-  return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 1>, static_cast<unsigned>(ctas < most ? ctas : most),
-                          32 * PJ_WARPS, 0, a.stream, p);
+  const unsigned rows = static_cast<unsigned>(heads < most ? heads : most);
+  switch (join_warps(static_cast<long long>(a.B) * p.U, heads, p.cap / C::TILE + 1, pl, a.sms)) {
+    case 16: return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 16>, rows, 512, 0, a.stream, p);
+    case 4: return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 4>, rows, 128, 0, a.stream, p);
+    default: {
+      const long long ctas = (heads + 3) / 4;
+      return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 1>, static_cast<unsigned>(ctas < most ? ctas : most), 128, 0,
+                              a.stream, p);
+    }
+  }
 }
 
 // Query heads a unit holds: 8, 16 or 32, whichever the group fits (larger groups take several units of 32, which
