@@ -168,7 +168,8 @@ def test_bad_prefix_page(cuda_device):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("B,H,Hkv,ps,prefix_len", [
     (1, 4, 4, 16, 1), (2, 8, 2, 16, 63), (3, 6, 2, 64, 64), (5, 16, 2, 16, 1000), (33, 8, 1, 32, 517), (40, 24, 2, 24, 300),
-    (70, 4, 4, 5, 129), (64, 8, 2, 128, 2048), (9, 40, 1, 256, 100), (4, 8, 8, 8, 4000), (3, 4, 1, 1, 70)], ids=str)
+    (70, 4, 4, 5, 129), (64, 8, 2, 128, 2048), (9, 40, 1, 256, 100), (4, 8, 8, 8, 4000), (3, 4, 1, 1, 70),
+    (150, 16, 4, 16, 700), (140, 4, 2, 5, 200), (90, 12, 4, 24, 333), (200, 16, 8, 8, 97)], ids=str)
 def test_prefix(cuda_device, d, B, H, Hkv, ps, prefix_len):
     """Sequences with the prefix alone, with own rows behind it, and unused places; prefixes of one key, ending inside a
     page or a tile; batches below and above one tile of query rows."""
