@@ -4,7 +4,9 @@ This module only marshals arguments: it checks tensors, takes their device
 pointers and the current CUDA stream, and calls the C ABI of ``libfa.so``
 (declared in ``include/fa.h``).  Every step of the computation runs in the
 library's CUDA kernels; there is no fallback.  If the library is missing or
-fails to load, importing the binding's entry points raises.
+fails to load, importing the binding's entry points raises.  The position and
+paged-cache calls (fa_rope and below) marshal in compiled code
+(``csrc/fa_binding.cpp``), the others through ctypes.
 
 Entry points (same names as the C ABI):
   fa_fwd(q, k, v, scale=None, o=None, lse=None, with_lse=True, kv_splits=0, causal=False, workspace=None)

@@ -11,7 +11,8 @@
 // move a 16-key block.  (With the heads as the 16 rows a tile step took 630 instructions an 8 KB of K and V
 // instead of about 200, and the issue slots, not the bytes, bound short contexts.)  A thread holds two heads'
 // columns, so maxima, sums and rescaling are its own; the running maximum moves only when a score passes it by
-// more than 2^PG_TAU.
+// more than 2^PG_TAU.  P is rounded to bf16 (to nearest: at most 2^-8 relative a term) because the instruction takes both
+// operands in one 16-bit type and V is bf16; the row sums add the unrounded P, in fp32 like everything else.
 //
 // Work split.  A unit is one (sequence, group of query heads); its keys are cut into tiles of TILE (32 KB of K
 // and V).  The tiles of all units, in order, are dealt evenly to the CTAs, one contiguous range each, whatever
@@ -24,6 +25,9 @@
 // copies, with no barrier between the warps until a unit ends; then their states merge in shared memory.  The
 // lanes look up their keys' pages one step ahead.  Page sizes that are multiples of 16 rows copy 16 rows from
 // one base address; others pass every row's offset around by shuffles.
+//
+// Measured: 32 sequences of 32768 keys (d = 64, groups of 4) 305 us, 7.0 TB/s (floor 322 us at the copy's rate);
+// 61 sequences of 0 to 32768 keys (d = 128, groups of 8) 70 us, 5.9 TB/s; one of 777 keys 6.6 us with the join.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"

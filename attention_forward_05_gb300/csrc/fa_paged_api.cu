@@ -182,6 +182,8 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   if (num_pages < 1 || page_size < 1 || max_pages < 1 || table_stride < max_pages) return FA_ERR_INVALID_ARG;
   if (prefix_len < 0 || prefix_len >= (1 << 30) || (prefix_len > 0 && !prefix_pages)) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(max_pages) * page_size >= (1LL << 30)) return FA_ERR_INVALID_ARG;
+  // the tiles of a CTA's share are counted in 32 bits
+  if (static_cast<long long>(max_pages) * page_size / 64 + 3 > (1LL << 39) / B / H) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H > 0x7FFFFFFFLL / d) return FA_ERR_INVALID_ARG;

@@ -350,7 +350,9 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
  * gets NaN in o and lse, and fa_check_device_error reports FA_ERR_INVALID_ARG; the
  * others are not affected.  Accumulation and softmax statistics are fp32, P is
  * rounded to bf16 for P V.  No atomics: repeated calls on one GPU give identical
- * bits.  max_pages * page_size < 2^30.  Returns FA_OK or an fa_status code.
+ * bits.  max_pages * page_size < 2^30, B * H * d < 2^31, and B * H *
+ * (max_pages * page_size / 64 + 3) <= 2^39 (FA_ERR_INVALID_ARG otherwise).  Returns
+ * FA_OK or an fa_status code.
  */
 int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, const int* page_table,
                     long long table_stride, const int* seq_lens, int B, int H, int Hkv, int d,

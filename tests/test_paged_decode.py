@@ -353,6 +353,63 @@ def test_long_cache_offsets(cuda_device):
     assert int((kc[pages - 5] != 0).any(-1).sum()) == Hkv
 
 
+def test_optional_results_and_views(cuda_device):
+    """No LSE asked for; q with a token dimension; a table that is a slice of a wider one; prefix pages with
+    more entries than the prefix needs; one sequence on one key/value head (strides of single entries)."""
+    c = _case(cuda_device, [40, 0, 129], 8, 2, 64, 16, 2550, prefix_len=50)
+    o, lse = _run(c)
+    wide = torch.full((3, c["table"].shape[1] + 5), 1 << 29, dtype=torch.int32, device=cuda_device)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    more = torch.cat((c["prefix_t"], torch.full((3,), -1, dtype=torch.int32, device=cuda_device)))
+    o2, none = fa.fa_decode_paged_prefix(c["q"].unsqueeze(2), c["kc"], c["vc"], more, 50, wide[:, :c["table"].shape[1]],
+                                         c["lens_t"])
+    _ok()
+    assert none is None and o2.shape == o.shape and torch.equal(o, o2)
+    one = _case(cuda_device, [100], 4, 1, 128, 16, 2551)  # one sequence, one key/value head: strides of single entries
+    a, _ = _run(one)
+    t1 = one["table"].repeat(3, 1)[1:2]
+    b, _ = fa.fa_decode_paged(one["q"], one["kc"], one["vc"], t1, one["lens_t"], with_lse=True)
+    _ok()
+    assert torch.equal(a, b)
+
+
+def test_c_abi_allocates_its_workspace(cuda_device):
+    """The C entry points with workspace = NULL and lse = NULL (stream-ordered allocation inside the call) give the
+    binding's results, on the default and on another stream."""
+    L = fa.lib()
+    for plen in (0, 300):
+        c = _case(cuda_device, [500, 0, 33, -1], 8, 2, 128, 16, 2560 + plen, prefix_len=plen)
+        want, _ = _run(c)
+        torch.cuda.synchronize()
+        P, Hkv, ps, d = c["kc"].shape
+        side = torch.cuda.Stream()
+        for stream in (torch.cuda.current_stream(), side):
+            o = torch.full((4, 8, 128), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+            torch.cuda.synchronize()
+            args = [c["table"].data_ptr(), c["table"].shape[1], c["lens_t"].data_ptr(), 4, 8, Hkv, d, P, ps,
+                    c["table"].shape[1], None, 128 ** -0.5, None, 0, None, stream.cuda_stream]
+            if plen:
+                st = L.fa_decode_paged_prefix(c["q"].data_ptr(), c["kc"].data_ptr(), c["vc"].data_ptr(), o.data_ptr(),
+                                              c["prefix_t"].data_ptr(), plen, *args)
+            else:
+                st = L.fa_decode_paged(c["q"].data_ptr(), c["kc"].data_ptr(), c["vc"].data_ptr(), o.data_ptr(), *args)
+            assert st == fa.FA_OK
+            _ok()
+            assert torch.equal(o, want)
+
+
+def test_more_sequences_than_ctas_and_threads(cuda_device):
+    """Thousands of sequences (several a thread of the plan), most of them empty or of one key."""
+    rng = np.random.default_rng(2570)
+    lens = rng.choice([0, 1, 1, 2, -1, 17, 40], 3001)
+    c = _case(cuda_device, lens.tolist(), 2, 1, 64, 16, 2571, spoil=False)
+    o, lse = _run(c)
+    _ok()
+    _check(c, o, lse, "3001 sequences", seqs=sorted({0, 1, 2, 3000, *rng.integers(0, 3001, 150).tolist()}))
+    empty = torch.as_tensor(lens <= 0, device=cuda_device)
+    assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all() and torch.isfinite(lse[~empty]).all()
+
+
 def test_refusals(cuda_device):
     c = _case(cuda_device, [30, 4], 8, 2, 64, 16, 2500)
     base = dict(q=c["q"], k_cache=c["kc"], v_cache=c["vc"], page_table=c["table"], seq_lens=c["lens_t"])

@@ -87,7 +87,8 @@ def _decode(**kw):
     (dict(ps=0), INVALID), (dict(mp=0), INVALID), (dict(stride=3), INVALID), (dict(mp=1 << 20, ps=1 << 10), INVALID),
     (dict(plen=-1), INVALID), (dict(plen=5), INVALID), (dict(plen=BIG, pp=P3), INVALID),
     (dict(plen=5, pp=P3 + 1), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
-    (dict(d=96), UNSUPPORTED), (dict(B=1 << 20, H=1 << 12), INVALID), (dict(cs=[2048, 1024, 60]), INVALID),
+    (dict(d=96), UNSUPPORTED), (dict(B=1 << 20, H=1 << 12), INVALID),
+    (dict(B=1 << 16, H=8, mp=1 << 19, ps=1 << 10), INVALID), (dict(cs=[2048, 1024, 60]), INVALID),
     (dict(cs=[-2048, 1024, 64]), INVALID), (dict(cs=[0, 1024, 64]), INVALID), (dict(cs=[2048, 1024, 0]), INVALID),
 ])
 def test_decode_rejects(kw, status):

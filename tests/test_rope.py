@@ -262,6 +262,28 @@ def test_append_slot_past_the_cache_is_reported(cuda_device):
     _check_append(kc0, vc0, kc, vc, slots, k, v, ref.f64(k), np.zeros(k.shape), 16, "append bad slot")
 
 
+def test_side_streams(cuda_device):
+    """Rotation and append on another stream than the current one, from tensors made there and here."""
+    s = torch.cuda.Stream()
+    q, k = _draw((2, 4, 200, 64), 450, cuda_device), _draw((2, 2, 200, 64), 451, cuda_device)
+    freqs, pos = fa.fa_rope_freqs(64, device=cuda_device), torch.arange(200, dtype=torch.int32, device=cuda_device)
+    want = fa.fa_rope(q, k, pos, freqs)
+    kc, vc, slots, xq, xk, xv = _append_case(cuda_device, 200, 4, 2, 64, 16, "head", 452)
+    st = torch.as_tensor(slots, device=cuda_device)
+    kc2, vc2 = kc.clone(), vc.clone()
+    wq = fa.fa_paged_append(xk, xv, kc, vc, st, q=xq, positions=pos, freqs=freqs)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = fa.fa_rope(q, k, pos, freqs, stream=s)
+        back = fa.fa_rope_bwd(*got, pos, freqs, stream=s)
+        gq = fa.fa_paged_append(xk, xv, kc2, vc2, st, q=xq, positions=pos, freqs=freqs, stream=s)
+        del back
+    s.synchronize()
+    _ok()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(gq, wq) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
+
+
 def test_append_refusals(cuda_device):
     kc, vc, slots, q, k, v = _append_case(cuda_device, 9, 2, 2, 64, 16, "head", 500)
     st = torch.as_tensor(slots, device=cuda_device)
