@@ -1050,7 +1050,39 @@ __global__ void __maxnreg__(C::MAXREG)
         for (int c4 = 0; c4 < C::OCOLS / 4; ++c4) reinterpret_cast<uint4*>(wrow)[c4] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<float2*>(p.ws_ml)[srow] = make_float2(-INFINITY, 0.f);
       }
-    } else if (ok && (C::PAGED || p.n_split > 1)) {  // partial state (m, l, unnormalised O) of this key range, for the merge
+    } else if (C::PAGED && ok) {
+      // Partial state (m, l, unnormalised O) for the join.  A thread holds a row, and rows are D * 4 bytes apart: written
+      // straight from the threads, a warp's 16-byte stores touch 32 lines each (4 us for 256 rows of 128).  So 32 columns
+      // at a time go through this tile's Q in shared memory (its last product is done), 4 KB a warp, 16-byte pieces swapped
+      // by the row, and out in whole lines.
+      tc_fence_after();
+      const int row0 = q0 + t * C::BR + wq * 32;  // the warp's first row
+      const size_t srow0 = (static_cast<size_t>(split) * p.BH + bh) * p.Nq + row0;
+      uint8_t* const stage = smem + C::OFF_Q + t * C::Q_BYTES + wq * 4096;
+#pragma unroll 1
+      for (int cc = 0; cc < C::OCOLS / 32; ++cc) {
+        uint32_t orr[32];
+        tmem_ld32(tO + cc * 32, orr);
+        tmem_wait_ld();
+        reg_fence(orr);
+#pragma unroll
+        for (int v4 = 0; v4 < 8; ++v4)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((v4 ^ (lane & 7)) << 4)) =
+              make_uint4(orr[4 * v4], orr[4 * v4 + 1], orr[4 * v4 + 2], orr[4 * v4 + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + lane / 8, pc = lane % 8;
+          if (row0 + r < p.Nq)
+            *reinterpret_cast<uint4*>(p.ws_o + (srow0 + r) * C::D + cc * 32 + pc * 4) =
+                *reinterpret_cast<const uint4*>(stage + r * 128 + ((pc ^ (r & 7)) << 4));
+        }
+        __syncwarp();
+      }
+      if constexpr (C::PAGED)
+        if (*bad_page) l = __int_as_float(0x7fc00000);  // set before the tile's copy, which o_done follows
+      if (row0 + lane < p.Nq) reinterpret_cast<float2*>(p.ws_ml)[srow0 + lane] = make_float2(m_ref, l);
+    } else if (ok && p.n_split > 1) {  // partial state (m, l, unnormalised O) of this key range, for the merge
       tc_fence_after();
       const int qrow = q0 + t * trow + row;
       const bool in_range = qrow < p.Nq;
@@ -1068,7 +1100,6 @@ __global__ void __maxnreg__(C::MAXREG)
           for (int v4 = 0; v4 < 8; ++v4) dst[v4] = make_uint4(orr[4 * v4], orr[4 * v4 + 1], orr[4 * v4 + 2], orr[4 * v4 + 3]);
         }
       }
-      if (C::PAGED && *bad_page) l = __int_as_float(0x7fc00000);  // set before the tile's copy, which o_done follows
       if (in_range) reinterpret_cast<float2*>(p.ws_ml)[srow] = make_float2(m_ref, l);
     } else if (ok) {
       tc_fence_after();
