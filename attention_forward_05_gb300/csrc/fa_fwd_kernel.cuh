@@ -360,7 +360,7 @@ __global__ void __maxnreg__(C::MAXREG)
       auto page_of = [&](int j) {
         const int key = k_begin + j * C::BC + lane * p.box_rows;
         if (lane >= boxes || j >= T || key >= k_end) return p.num_pages;
-        const int pg = __ldg(p.pages + key / p.page_size);
+        const int pg = p.pages[key / p.page_size];
         if (pg >= 0 && pg < p.num_pages) return pg;
         *bad_page = 1;
         record_bad_index(p.err, W_PREFIX_PAGE);

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   int pid = 0;
   auto lookup = [&]() {
     const int key = ld.tile * C::TILE + warp * KW + r_l;
-    if (ld.v < range && key < ld.len) pid = __ldg(p.table + ld.b * p.table_stride + p.by_page.div(key));
+    if (ld.v < range && key < ld.len) pid = p.table[ld.b * p.table_stride + p.by_page.div(key)];
   };
   auto load_step = [&]() {  // copies of step ld into ring stage ld_stage, then the next step's lookup
     if (ld.v < range) {

@@ -39,11 +39,11 @@ int box_rows_of(int page_size, int bc) {
 
 // The prefix's rows copied into whole pages of GATHER_PAGE rows, [pages][Hkv][GATHER_PAGE][d], for page sizes whose
 // rows cannot be copied in boxes.  One thread moves 16 bytes of K and of V; a bad page makes its keys NaN.
-__global__ void __launch_bounds__(256) gather_prefix_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                                                            uint4* __restrict__ gk, uint4* __restrict__ gv,
-                                                            int* __restrict__ ids, const int* __restrict__ pages, int n,
-                                                            int Hkv, int pieces, int num_pages, int page_size,
-                                                            long long c_page, long long c_head, long long c_row, int* err) {
+// (No read-only loads here and in fa_paged_kernel: they are launched while their inputs may still be written.)
+__global__ void __launch_bounds__(256) gather_prefix_kernel(const uint4* k, const uint4* v, uint4* gk, uint4* gv,
+                                                            int* ids, const int* pages, int n, int Hkv, int pieces,
+                                                            int num_pages, int page_size, long long c_page,
+                                                            long long c_head, long long c_row, int* err) {
   griddep_launch_dependents();
   griddep_wait();
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
