@@ -68,7 +68,12 @@ struct Arg {
   const Tensor& operator*() const { return *t; }
   const Tensor* operator->() const { return t; }
   explicit operator bool() const { return t != nullptr; }
-  void* ptr() const { return t ? t->data_ptr() : nullptr; }
+  // Throws for a tensor without memory (a fake one): taken before the GIL is let go.
+  void* ptr() const {
+    void* const p = t ? t->data_ptr() : nullptr;
+    if (p == nullptr && t && t->numel() > 0) throw refusal(PyExc_ValueError, "%s has no memory", name);
+    return p;
+  }
 };
 
 Arg arg(PyObject* o, const char* name, bool optional = false) {
@@ -144,6 +149,14 @@ void check_rotation(const Arg& positions, const Arg& freqs, const Arg& axes) {
     throw ValueError("axes must be contiguous int32, one entry a frequency");
 }
 
+// (a, b); takes both references.  A nullptr is an object that could not be made, with its exception set.
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* out = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return out;
+}
+
 void need_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) throw TypeError("%d arguments expected", static_cast<int>(want));
 }
@@ -200,19 +213,19 @@ PyObject* rope(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     const int Bi = as_int(B, "B"), Ni = as_int(N, "N"), d = as_int(q->size(3), "d"), ax = as_int(n_axes, "axes");
     const int rot = as_int(2 * freqs->size(0), "freqs");
     const bool inter = truth(in[5]), inverse = truth(in[8]);
+    void *const qp = q.ptr(), *const kp = k.ptr(), *const qop = qo.ptr(), *const kop = ko.ptr();
+    const int *const posp = static_cast<const int*>(pos.ptr()), *const axp = static_cast<const int*>(axes.ptr());
+    const double* const fp = static_cast<const double*>(freqs.ptr());
+    const fa_stream_t stream = stream_of(dev);
     int st;
     Py_BEGIN_ALLOW_THREADS;
-    st = fa_rope(q.ptr(), k.ptr(), qo.ptr(), ko.ptr(), strides, Bi, H, Hkv, Ni, d, type == at::kFloat ? FA_FP32 : FA_BF16,
-                 static_cast<const int*>(pos.ptr()), shared, static_cast<const double*>(freqs.ptr()),
-                 static_cast<const int*>(axes.ptr()), ax, rot, inter, inverse, stream_of(dev));
+    st = fa_rope(qp, kp, qop, kop, strides, Bi, H, Hkv, Ni, d, type == at::kFloat ? FA_FP32 : FA_BF16, posp, shared, fp,
+                 axp, ax, rot, inter, inverse, stream);
     Py_END_ALLOW_THREADS;
     if (st != FA_OK) return PyLong_FromLong(st);
     PyObject* a = q_new.defined() ? THPVariable_Wrap(std::move(q_new)) : Py_NewRef(in[6]);
     PyObject* b = k_new.defined() ? THPVariable_Wrap(std::move(k_new)) : Py_NewRef(in[7]);
-    PyObject* out = PyTuple_Pack(2, a, b);
-    Py_DECREF(a);
-    Py_DECREF(b);
-    return out;
+    return pair(a, b);
   });
 }
 
@@ -277,11 +290,15 @@ PyObject* append(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     const bool inter = truth(in[9]);
     int st = FA_OK;
     if (T > 0) {  // an empty tensor has no address; there is nothing to append
+      void *const kp = k.ptr(), *const vp = v.ptr(), *const qp = q.ptr(), *const qop = qo.ptr();
+      void *const kcp = kc.ptr(), *const vcp = vc.ptr();
+      const long long* const sp = static_cast<const long long*>(slots.ptr());
+      const int *const posp = static_cast<const int*>(pos.ptr()), *const axp = static_cast<const int*>(axes.ptr());
+      const double* const fp = static_cast<const double*>(freqs.ptr());
+      const fa_stream_t stream = stream_of(dev);
       Py_BEGIN_ALLOW_THREADS;
-      st = fa_paged_append(k.ptr(), v.ptr(), q.ptr(), qo.ptr(), kc.ptr(), vc.ptr(), s, cs,
-                           static_cast<const long long*>(slots.ptr()), Ti, H, hk, di, pages, ps,
-                           static_cast<const int*>(pos.ptr()), static_cast<const double*>(freqs.ptr()),
-                           static_cast<const int*>(axes.ptr()), ax, r, inter, stream_of(dev));
+      st = fa_paged_append(kp, vp, qp, qop, kcp, vcp, s, cs, sp, Ti, H, hk, di, pages, ps, posp, fp, axp, ax, r, inter,
+                           stream);
       Py_END_ALLOW_THREADS;
     }
     if (st != FA_OK) return PyLong_FromLong(st);
@@ -347,21 +364,20 @@ PyObject* decode(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
       }
     }
     const long long row = B == 1 ? mp : table->stride(0);
+    void *const qp = q.ptr(), *const kcp = kc.ptr(), *const vcp = vc.ptr(), *const op = o.ptr();
+    const int* const prep = plen ? static_cast<const int*>(pre.ptr()) : nullptr;
+    const int *const tp = static_cast<const int*>(table.ptr()), *const lp = static_cast<const int*>(lens.ptr());
+    float* const lsep = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+    const fa_stream_t stream = stream_of(dev);
     int st;
     Py_BEGIN_ALLOW_THREADS;
-    st = fa_decode_paged_prefix(q.ptr(), kc.ptr(), vc.ptr(), o.ptr(), plen ? static_cast<const int*>(pre.ptr()) : nullptr,
-                                static_cast<int>(plen), static_cast<const int*>(table.ptr()), row,
-                                static_cast<const int*>(lens.ptr()), Bi, Hi, hk, di, pages, psi, mp, cs,
-                                static_cast<float>(scale), ws_ptr, ws_bytes,
-                                lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream_of(dev));
+    st = fa_decode_paged_prefix(qp, kcp, vcp, op, prep, static_cast<int>(plen), tp, row, lp, Bi, Hi, hk, di, pages, psi, mp,
+                                cs, static_cast<float>(scale), ws_ptr, ws_bytes, lsep, stream);
     Py_END_ALLOW_THREADS;
     if (st != FA_OK) return PyLong_FromLong(st);
     PyObject* a = o_new.defined() ? THPVariable_Wrap(std::move(o_new)) : Py_NewRef(in[10]);
     PyObject* b = lse.defined() ? THPVariable_Wrap(std::move(lse)) : Py_NewRef(Py_None);
-    PyObject* out = PyTuple_Pack(2, a, b);
-    Py_DECREF(a);
-    Py_DECREF(b);
-    return out;
+    return pair(a, b);
   });
 }
 

@@ -428,6 +428,21 @@ def test_refusals(cuda_device):
     _ok()
 
 
+def test_tensors_without_memory_are_refused(cuda_device):
+    """Fake tensors pass every check of shape and device, and have no address: an exception, raised with the GIL held."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        q, cache = (torch.empty(s, dtype=torch.bfloat16, device=cuda_device) for s in ((2, 4, 64), (8, 2, 16, 64)))
+        x, slots = torch.empty(2, 4, 3, 64, device=cuda_device), torch.empty(2, dtype=torch.int64, device=cuda_device)
+        table, lens, pos = (torch.empty(s, dtype=torch.int32, device=cuda_device) for s in ((2, 4), (2,), (3,)))
+        freqs = torch.empty(32, dtype=torch.float64, device=cuda_device)
+    for call in (lambda: fa.fa_decode_paged(q, cache, cache, table, lens), lambda: fa.fa_rope(x, None, pos, freqs),
+                 lambda: fa.fa_paged_append(q[:, :2], q[:, :2], cache, cache, slots)):
+        with pytest.raises((RuntimeError, ValueError)):
+            call()
+    _ok()
+
+
 # ------------------------------------------------------------------------------------------ together
 
 def test_training_step_with_positions(cuda_device):
