@@ -22,9 +22,13 @@ bool good_strides(const long long* s, int n, int unit) {
   return true;
 }
 
-// Strides of a cache: good_strides, and no dimension of several entries that stands still.
+// No dimension of several entries stands still.
+bool distinct(const long long* s, int n0, int n1, int n2) {
+  return (s[0] > 0 || n0 == 1) && (s[1] > 0 || n1 == 1) && (s[2] > 0 || n2 == 1);
+}
+
 bool good_cache(const long long* c, int num_pages, int Hkv, int page_size) {
-  return good_strides(c, 3, 8) && (c[0] > 0 || num_pages == 1) && (c[1] > 0 || Hkv == 1) && (c[2] > 0 || page_size == 1);
+  return good_strides(c, 3, 8) && distinct(c, num_pages, Hkv, page_size);
 }
 
 // Arguments of a rotation; rot = 0 (no rotation) is the caller's business.
@@ -54,7 +58,7 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long l
   int rc = check_rotation(positions, freqs, axes, n_axes, rot, interleaved, d);
   if (rc != FA_OK) return rc;
   const long long heads = static_cast<long long>(H) + Hkv, tokens = static_cast<long long>(B) * N;
-  if (heads > 0x7FFFFFFFLL || tokens > kMaxElems || tokens > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
+  if (heads > 0x7FFFFFFFLL / d || tokens > kMaxElems || tokens > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
   long long s[12];
   for (int i = 0; i < 4; ++i) {
     const long long h = (i & 1) ? Hkv : H;
@@ -63,6 +67,8 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long l
     s[3 * i + 2] = strides ? strides[3 * i + 2] : d;
   }
   if (!good_strides(s, 12, dtype == FA_BF16 ? 8 : 4)) return FA_ERR_INVALID_ARG;
+  for (int i = 2; i < (k ? 4 : 3); ++i)  // an input may be broadcast, an output may not
+    if (!distinct(s + 3 * i, B, i == 2 ? H : Hkv, N)) return FA_ERR_INVALID_ARG;
   fa::RopeLaunch a;
   if ((rc = fa::current_device_info(&a.err, &a.sms)) != FA_OK) return rc;
   a.q = q;
@@ -110,7 +116,7 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
     if (rc != FA_OK) return rc;
   }
   const long long heads = static_cast<long long>(H) + 2LL * Hkv;
-  if (heads > 0x7FFFFFFFLL || T > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
+  if (heads > 0x7FFFFFFFLL / d || T > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
   long long s[6], c[3];
   for (int i = 0; i < 3; ++i) {
     s[2 * i] = in_strides ? in_strides[2 * i] : static_cast<long long>(i < 2 ? Hkv : H) * d;
@@ -184,7 +190,8 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   if (static_cast<long long>(max_pages) * page_size >= (1LL << 30)) return FA_ERR_INVALID_ARG;
   // the tiles of a CTA's share are counted in 32 bits
   if (static_cast<long long>(max_pages) * page_size / 64 + 3 > (1LL << 39) / B / H) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  const float c2 = scale * 1.4426950408889634f;  // log2 units; the largest scales overflow here
+  if (!std::isfinite(c2)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H > 0x7FFFFFFFLL / d) return FA_ERR_INVALID_ARG;
   long long c[3];
@@ -224,7 +231,7 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   a.max_pages = max_pages;
   a.table_stride = table_stride;
   a.prefix_len = prefix_len;
-  a.c = scale * 1.4426950408889634f;
+  a.c = c2;
   cudaError_t e = fa::launch_decode_paged(a, plan);
   if (workspace == nullptr) {
     const cudaError_t e2 = cudaFreeAsync(ws, a.stream);

@@ -288,7 +288,7 @@ int fa_decode_splitkv_noalloc(const void* q, const void* k, const void* v, void*
  *   axes          device int32 [rot/2]: axis(i) in 0 .. n_axes - 1, or NULL: axis 0.
  *     A pair whose entry is out of range becomes NaN, and
  *     fa_check_device_error reports FA_ERR_INVALID_ARG.
- *   n_axes 1 .. 8; rot a multiple of 16, 16 <= rot <= d.
+ *   n_axes 1 .. 8; rot a multiple of 16, 16 <= rot <= d; (H + Hkv) * d < 2^31.
  * No workspace.  Returns FA_OK or an fa_status code.
  */
 int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
@@ -318,7 +318,7 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long l
  *            int32 [n_axes, T]; rot = 0 with positions = freqs = NULL stores the keys
  *            and copies the queries as they are.  q_out is written for every token,
  *            those with a negative slot too.
- * All strides are multiples of 8 elements.  T = 0 is a step without new tokens.
+ * All strides are multiples of 8 elements; (H + 2 * Hkv) * d < 2^31.  T = 0 is a step without new tokens.
  * Returns FA_OK or an fa_status code.
  */
 int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, void* k_cache, void* v_cache,
@@ -340,7 +340,7 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
  *              past a sequence's last page are not read.
  *   seq_lens   device int32 [B].  A sequence without keys (seq_lens[b] <= 0) gets
  *              o = 0 and lse = -inf.
- *   scale      finite score scale.
+ *   scale      finite score scale (finite in log2 units too: |scale| < 2.3e38).
  *   lse        fp32 [B, H] out (natural log, scaled-score units), or NULL.
  *   workspace  device buffer of at least fa_decode_paged_workspace_bytes(B, H, Hkv,
  *              d, page_size, 0) bytes, 16-byte aligned, or NULL to allocate it stream-ordered on

@@ -106,6 +106,17 @@ def test_scales(cuda_device, scale):
     ref.check_decode(c["q"], c["kc"], c["vc"], o, lse, c["tables"], c["lens"], scale, f"scale {scale}")
 
 
+@pytest.mark.parametrize("d,B", [(64, 3), (64, 40), (128, 3), (128, 40)])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
+def test_prefix_scales(cuda_device, scale, d, B):
+    """Both tile widths of the prefix (B * 4 rows a head), its last tile ragged, infinities and NaN behind its end."""
+    c = _case(cuda_device, [17 + b % 5 for b in range(B)], 8, 2, d, 16, 1430 + B, prefix_len=203)
+    o, lse = _run(c, scale=scale)
+    _ok()
+    ref.check_decode(c["q"], c["kc"], c["vc"], o, lse, c["tables"], c["lens"], scale, f"prefix scale {scale} d{d} B{B}",
+                     c["prefix"], 203)
+
+
 @pytest.mark.parametrize("prefix_len", [0, 150])
 def test_peaked_scores_and_late_maxima(cuda_device, prefix_len):
     """Scores that grow along the sequence by far more than a rescale threshold, and one key that outweighs all."""

@@ -41,6 +41,8 @@ INVALID, UNSUPPORTED = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
     (dict(shared=3), INVALID), (dict(d=96), UNSUPPORTED), (dict(dtype=5), UNSUPPORTED),
     (dict(B=1 << 20, N=1 << 20), INVALID),
     (dict(strides=[512, 64, 64] * 3 + [512, 64, 60]), INVALID), (dict(strides=[512, 64, -64] * 4), INVALID),
+    (dict(strides=[512, 64, 64] * 2 + [0, 64, 64] + [512, 64, 64], B=2), INVALID),
+    (dict(strides=[512, 64, 64] * 3 + [512, 64, 0], N=2), INVALID), (dict(H=1 << 25), INVALID),
 ])
 def test_rope_rejects(kw, status):
     assert _rope(**kw) == status
@@ -62,7 +64,7 @@ def _append(**kw):
     (dict(pages=0), INVALID), (dict(ps=0), INVALID), (dict(kc=P2 + 8), INVALID), (dict(d=32), UNSUPPORTED),
     (dict(rot=0), INVALID), (dict(pos=None), INVALID), (dict(freqs=None), INVALID), (dict(rot=80), INVALID),
     (dict(rot=40), UNSUPPORTED), (dict(ins=[128, 60, 128, 64, 256, 64]), INVALID), (dict(cs=[2048, 1024, 4]), INVALID),
-    (dict(cs=[2048, -1024, 64]), INVALID),
+    (dict(cs=[2048, -1024, 64]), INVALID), (dict(Hkv=1 << 24), INVALID),
 ])
 def test_append_rejects(kw, status):
     assert _append(**kw) == status
@@ -86,7 +88,7 @@ def _decode(**kw):
     (dict(B=0), INVALID), (dict(H=0), INVALID), (dict(Hkv=3), INVALID), (dict(pages=0), INVALID),
     (dict(ps=0), INVALID), (dict(mp=0), INVALID), (dict(stride=3), INVALID), (dict(mp=1 << 20, ps=1 << 10), INVALID),
     (dict(plen=-1), INVALID), (dict(plen=5), INVALID), (dict(plen=BIG, pp=P3), INVALID),
-    (dict(plen=5, pp=P3 + 1), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
+    (dict(plen=5, pp=P3 + 1), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(scale=3e38), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(B=1 << 20, H=1 << 12), INVALID),
     (dict(B=1 << 16, H=8, mp=1 << 19, ps=1 << 10), INVALID), (dict(cs=[2048, 1024, 60]), INVALID),
     (dict(cs=[-2048, 1024, 64]), INVALID), (dict(cs=[0, 1024, 64]), INVALID), (dict(cs=[2048, 1024, 0]), INVALID),
