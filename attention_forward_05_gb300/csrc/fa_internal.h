@@ -39,6 +39,27 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, i
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same in clusters of `cluster` CTAs (a divisor of the grid, at most 8).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), unsigned grid, int cluster, int threads, int smem,
+                                      cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // The C ABI's per-device check for the current device: FA_OK on an sm_103 GPU (after fetching the
 // library's device error word), FA_ERR_UNSUPPORTED on any other device, FA_ERR_CUDA when a runtime
 // call fails.  Allocates nothing.

@@ -21,13 +21,17 @@
 // unnormalised O) for fa_paged_join_kernel.  (Ranges of single warps left four times as many parts to join:
 // 28 instead of 21 us on one sequence of 32768 keys.)
 //
+// Where no sequence can be long (its table says how long), a unit has a cluster of 1 to 8 CTAs of its own instead
+// (CLUSTER, cluster_size): nothing is planned, and the cluster joins its states through its shared memory, with the
+// prefix's, so there is no join kernel behind it.
+//
 // Inside a CTA each warp takes its own KW keys of every tile through its own ring of asynchronous 16-byte
 // copies, with no barrier between the warps until a unit ends; then their states merge in shared memory.  The
 // lanes look up their keys' pages one step ahead.  Page sizes that are multiples of 16 rows copy 16 rows from
 // one base address; others pass every row's offset around by shuffles.
 //
-// Measured: 32 sequences of 32768 keys (d = 64, groups of 4) 305 us, 7.0 TB/s (floor 322 us at the copy's rate);
-// 61 sequences of 0 to 32768 keys (d = 128, groups of 8) 70 us, 5.9 TB/s; one of 777 keys 6.6 us with the join.
+// Measured, device time: 32 sequences of 32768 keys (d = 64, groups of 4) 305 us, 7.0 TB/s (floor 322 us at the copy's rate);
+// 61 sequences of 0 to 32768 keys (d = 128, groups of 8) 69 us, 5.9 TB/s; one of 777 keys 4.9 us (6.6 us by ranges).
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -109,6 +113,7 @@ struct PgParams {
   const float* pre_ml;            // float2 [pre_split][Hkv][B * G]
   const float* pre_o;
   int pre_split;
+  int cl;                         // CTAs of a unit in the form without ranges (CLUSTER); 0: the other one
 };
 
 // Tiles of sequence b: 0 for a sequence without keys or with a length past its table.
@@ -124,6 +129,33 @@ __device__ __forceinline__ long long cta_count(long long total, int n_cta) { ret
 __device__ __forceinline__ long long cta_first(long long c, long long total, long long n) { return c * total / n; }
 __device__ __forceinline__ long long cta_of(long long t, long long total, long long n) {
   return ((t + 1) * n - 1) / total;
+}
+
+// ---- thread-block clusters
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The shared-memory address `addr` of this CTA in CTA `rank` of its cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 load_peer8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_peer16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 // A place in a CTA's range: tile `tile` of unit (b, u), at position v of the range.
@@ -147,9 +179,108 @@ struct Cursor {
   }
 };
 
+// (M, L, acc) += states (x, v), by the online-softmax recurrence.  An empty state is (-inf, 0, 0); a state of NaN keys
+// (-inf, NaN, NaN).
+template <int W>
+__device__ __forceinline__ void add_states(const float2 (&x)[W], const float4 (&v)[W], float& M, float& L, float4& acc) {
+  float m_new = M;
+#pragma unroll
+  for (int i = 0; i < W; ++i) m_new = fmaxf(m_new, x[i].x);
+  const float ref = m_new == -INFINITY ? 0.f : m_new;
+  const float alpha = ex2_approx(M - ref);
+  M = m_new;
+  L *= alpha;
+  acc.x *= alpha, acc.y *= alpha, acc.z *= alpha, acc.w *= alpha;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float w = ex2_approx(x[i].x - ref);
+    L = fmaf(x[i].y, w, L);
+    acc.x = fmaf(v[i].x, w, acc.x);
+    acc.y = fmaf(v[i].y, w, acc.y);
+    acc.z = fmaf(v[i].z, w, acc.z);
+    acc.w = fmaf(v[i].w, w, acc.w);
+  }
+}
+
+// The end of the form in which a unit has a cluster of its own: joins the states of the cluster's CTAs, which lie in their
+// shared memory, and those of the prefix, and writes the unit's outputs.  The output's 16-byte pieces are dealt to the
+// CTAs; inside one, groups of threads take every (number of groups)-th state, eight in flight, and are added up in order.
+template <class C, typename RowOf>
+__device__ __forceinline__ void join_cluster(const PgParams& p, int b, int len, int rows, int hk, int g0, long long head0,
+                                             int rank, uint8_t* smem, RowOf state_row) {
+  constexpr int D = C::D, THREADS = 32 * C::NW, W = 8;
+  if (p.cl > 1) cluster_sync();
+  if (p.prefix) griddep_wait();
+  const bool bad = len > p.cap, none = bad || len < 0 || (len == 0 && !p.prefix);
+  if (bad && rank == 0 && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
+  const int pieces = rows * (D / 4), share = (pieces + p.cl - 1) / p.cl;
+  const int wide = share >= THREADS ? THREADS : 1 << (32 - __clz(share - 1));  // pieces side by side
+  const int groups = THREADS / wide, grp = threadIdx.x / wide, at = threadIdx.x % wide;
+  const int pre = p.prefix ? p.pre_split : 0, parts = none ? 0 : pre + p.cl;
+  const long long pstep = static_cast<long long>(p.B) * p.H;
+  const uint32_t base = smem_u32(smem);
+  float4* const sum_o = reinterpret_cast<float4*>(smem);  // the warps' own states, done with
+  float2* const sum_ml = reinterpret_cast<float2*>(smem + THREADS * 16);
+  for (int e0 = 0; e0 < share; e0 += wide) {
+    const int e = rank * share + e0 + at;
+    const bool mine = e0 + at < share && e < pieces;
+    const int row = e / (D / 4), pc = e % (D / 4);
+    const long long prow = (static_cast<long long>(hk) * p.B + b) * p.G + g0 + row;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = grp; mine && s0 < parts; s0 += W * groups) {
+      float2 x[W];
+      float4 v[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int s = s0 + i * groups;
+        x[i] = make_float2(-INFINITY, 0.f);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < pre) {
+          x[i] = reinterpret_cast<const float2*>(p.pre_ml)[s * pstep + prow];
+          v[i] = reinterpret_cast<const float4*>(p.pre_o + (s * pstep + prow) * D)[pc];
+        } else if (s < parts) {
+          x[i] = load_peer8(peer_addr(base + C::OFF_Q + row * 8, s - pre));
+          v[i] = load_peer16(peer_addr(base + state_row(row) + pc * 16, s - pre));
+        }
+      }
+      add_states(x, v, M, L, acc);
+    }
+    if (groups > 1) {
+      sum_o[threadIdx.x] = acc;
+      sum_ml[threadIdx.x] = make_float2(M, L);
+      __syncthreads();
+      if (grp == 0) {
+        M = -INFINITY;
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < groups; g += 4) {  // a power of two; two groups are padded with empty states
+          float2 x[4];
+          float4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = g + i < groups;
+            x[i] = in ? sum_ml[(g + i) * wide + at] : make_float2(-INFINITY, 0.f);
+            v[i] = in ? sum_o[(g + i) * wide + at] : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          add_states(x, v, M, L, acc);
+        }
+      }
+    }
+    if (mine && grp == 0) {
+      const float nan = __int_as_float(0x7fc00000), inv = bad ? nan : none ? 0.f : 1.f / L;
+      *reinterpret_cast<uint2*>(p.o + (head0 + row) * D + pc * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (p.lse != nullptr && pc == 0)
+        p.lse[head0 + row] = bad ? nan : none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+  }
+  if (p.cl > 1) cluster_sync();  // a CTA's shared memory is there while others read it
+}
+
 }  // namespace
 
-template <class C>
+template <class C, bool CLUSTER>
 __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int D = C::D, KW = C::KW, NW = C::NW, S = C::STAGES;
@@ -162,82 +293,95 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   // may run beside that kernel; each CTA then waits at its end, so that this grid's completion implies that one's.
   if (!p.prefix) griddep_wait();
 
-  // ---- plan: total tiles, this CTA's range, the unit it starts in
-  long long* plan = reinterpret_cast<long long*>(smem + C::OFF_PLAN);  // [0..3] warp sums, [4] tiles before, [5] b
-  const int per = (p.B + 32 * NW - 1) / (32 * NW);
-  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
-  long long mine = 0;
-  int len_tmp;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int nt = seq_tiles<C::TILE>(p, b, &len_tmp);
-    if (nt > 0) mine += nt + PG_END;
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) plan[warp] = incl;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) incl += plan[w];
-    total += plan[w];
-  }
-  total *= p.U;
-  // outputs of sequences without keys, and of those whose length passes their table
-  for (int b = blockIdx.x; b < p.B; b += p.n_cta) {
-    int len;
-    if (seq_tiles<C::TILE>(p, b, &len) > 0) continue;
-    const bool bad = len > 0;
-    if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
-    for (int u = threadIdx.x; u < p.U; u += 32 * NW)
-      p.infos[static_cast<long long>(b) * p.U + u] = make_int2(-1, bad ? -2 : len < 0 ? -1 : 0);
-    if (p.prefix) continue;  // the join writes their outputs
-    const long long row0 = static_cast<long long>(b) * p.H;
-    for (int e = threadIdx.x; e < p.H * CPR; e += 32 * NW)
-      reinterpret_cast<uint4*>(p.o + row0 * D)[e] = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
-                                                        : make_uint4(0, 0, 0, 0);
-    if (p.lse != nullptr)
-      for (int h = threadIdx.x; h < p.H; h += 32 * NW) p.lse[row0 + h] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
-  }
-  const long long n = cta_count(total, p.n_cta);
   auto leave = [&]() {
     if (p.prefix) griddep_wait();
   };
-  if (static_cast<long long>(blockIdx.x) >= n) return leave();  // the whole CTA (n = 0 without keys)
-  const long long t0 = cta_first(blockIdx.x, total, n), t1 = cta_first(blockIdx.x + 1, total, n);
-  {
-    long long before = (incl - mine) * p.U;
-    if (t0 >= before && t0 < incl * p.U) {
-      for (int b = b_lo;; ++b) {
-        const int tiles = seq_tiles<C::TILE>(p, b, &len_tmp);
-        const long long nt = tiles > 0 ? static_cast<long long>(tiles + PG_END) * p.U : 0;
-        if (t0 < before + nt) {
-          plan[4] = before;
-          plan[5] = b;
-          break;
+  Cursor<C> cur;
+  int range;
+  long long t0 = 0, total = 0, n = 0;
+  const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % p.cl : 0;
+  if constexpr (CLUSTER) {  // the unit's CTAs share its tiles evenly; some may have none
+    const int unit = static_cast<int>(blockIdx.x) / p.cl;
+    cur.b = unit / p.U;
+    cur.u = unit - cur.b * p.U;
+    cur.nt = seq_tiles<C::TILE>(p, cur.b, &cur.len);
+    cur.tile = cur.nt * rank / p.cl;
+    cur.v = 0;
+    range = cur.nt * (rank + 1) / p.cl - cur.tile;
+  } else {
+    // ---- plan: total tiles, this CTA's range, the unit it starts in
+    long long* plan = reinterpret_cast<long long*>(smem + C::OFF_PLAN);  // [0..3] warp sums, [4] tiles before, [5] b
+    const int per = (p.B + 32 * NW - 1) / (32 * NW);
+    const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+    long long mine = 0;
+    int len_tmp;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const int nt = seq_tiles<C::TILE>(p, b, &len_tmp);
+      if (nt > 0) mine += nt + PG_END;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) plan[warp] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) incl += plan[w];
+      total += plan[w];
+    }
+    total *= p.U;
+    // outputs of sequences without keys, and of those whose length passes their table
+    for (int b = blockIdx.x; b < p.B; b += p.n_cta) {
+      int len;
+      if (seq_tiles<C::TILE>(p, b, &len) > 0) continue;
+      const bool bad = len > 0;
+      if (bad && threadIdx.x == 0) record_bad_index(p.err, W_LEN);
+      for (int u = threadIdx.x; u < p.U; u += 32 * NW)
+        p.infos[static_cast<long long>(b) * p.U + u] = make_int2(-1, bad ? -2 : len < 0 ? -1 : 0);
+      if (p.prefix) continue;  // the join writes their outputs
+      const long long row0 = static_cast<long long>(b) * p.H;
+      for (int e = threadIdx.x; e < p.H * CPR; e += 32 * NW)
+        reinterpret_cast<uint4*>(p.o + row0 * D)[e] = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
+                                                          : make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr)
+        for (int h = threadIdx.x; h < p.H; h += 32 * NW) p.lse[row0 + h] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
+    }
+    n = cta_count(total, p.n_cta);
+    if (static_cast<long long>(blockIdx.x) >= n) return leave();  // the whole CTA (n = 0 without keys)
+    t0 = cta_first(blockIdx.x, total, n);
+    const long long t1 = cta_first(blockIdx.x + 1, total, n);
+    {
+      long long before = (incl - mine) * p.U;
+      if (t0 >= before && t0 < incl * p.U) {
+        for (int b = b_lo;; ++b) {
+          const int tiles = seq_tiles<C::TILE>(p, b, &len_tmp);
+          const long long nt = tiles > 0 ? static_cast<long long>(tiles + PG_END) * p.U : 0;
+          if (t0 < before + nt) {
+            plan[4] = before;
+            plan[5] = b;
+            break;
+          }
+          before += nt;
         }
-        before += nt;
       }
     }
+    __syncthreads();
+    cur.b = static_cast<int>(plan[5]);
+    cur.nt = seq_tiles<C::TILE>(p, cur.b, &cur.len);
+    cur.u = static_cast<int>((t0 - plan[4]) / (cur.nt + PG_END));
+    cur.tile = static_cast<int>((t0 - plan[4]) % (cur.nt + PG_END));
+    cur.v = 0;
+    range = static_cast<int>(t1 - t0);
+    if (cur.tile >= cur.nt) {  // the range begins behind a unit's last tile
+      cur.v = cur.nt - 1 - cur.tile;
+      cur.tile = cur.nt - 1;
+      cur.next(p);
+    }
+    if (cur.v >= range) return leave();  // no tile of its own (the whole CTA)
   }
-  __syncthreads();
-  Cursor<C> cur;
-  cur.b = static_cast<int>(plan[5]);
-  cur.nt = seq_tiles<C::TILE>(p, cur.b, &cur.len);
-  cur.u = static_cast<int>((t0 - plan[4]) / (cur.nt + PG_END));
-  cur.tile = static_cast<int>((t0 - plan[4]) % (cur.nt + PG_END));
-  cur.v = 0;
-  const int range = static_cast<int>(t1 - t0);
-  if (cur.tile >= cur.nt) {  // the range begins behind a unit's last tile
-    cur.v = cur.nt - 1 - cur.tile;
-    cur.tile = cur.nt - 1;
-    cur.next(p);
-  }
-  if (cur.v >= range) return leave();  // no tile of its own (the whole CTA)
 
   // ---- loads: `ld` is the step whose pages are being looked up; lane r holds the page of key r of its KW
   const uint32_t ring = smem_u32(smem) + warp * S * C::STAGE_BYTES;
@@ -294,7 +438,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
           cp_async16(dst + C::K_BYTES, p.vc + src, ro < 0 ? 0 : 16);
         }
       }
-      ld.next(p);
+      if constexpr (CLUSTER)
+        ++ld.v, ++ld.tile;
+      else
+        ld.next(p);
       lookup();
     }
     cp_async_commit();
@@ -366,7 +513,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
   while (true) {
     const int seg_tile0 = cur.tile;  // first tile of the unit that this CTA covers
     const int tiles = min(cur.nt - cur.tile, range - cur.v);
-    for (int i = 0;; ++i) {
+    for (int i = 0; !CLUSTER || i < tiles; ++i) {
       load_step();  // into the stage of the step before this one
       cp_async_wait<S - 1>();
       __syncwarp();
@@ -455,18 +602,28 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
     }
 
     // ---- the unit's part in this CTA ends: merge the warps' states
-    cur.tile += tiles - 1;
-    cur.v += tiles - 1;
+    if (CLUSTER) stage = 0;  // nothing is in flight; the merged state's place is the same in every CTA
     Cursor<C> nx = cur;
-    nx.next(p);
-    const bool more = nx.v < range;
-    if (more) fetch_q(nx.b, nx.u);  // in flight during the merge
-    const bool whole = seg_tile0 == 0 && cur.tile + 1 == cur.nt;
+    bool more = false, whole = false;
+    if constexpr (!CLUSTER) {
+      cur.tile += tiles - 1;
+      cur.v += tiles - 1;
+      nx = cur;
+      nx.next(p);
+      more = nx.v < range;
+      if (more) fetch_q(nx.b, nx.u);  // in flight during the merge
+      whole = seg_tile0 == 0 && cur.tile + 1 == cur.nt;
+    }
     const int slot = 2 * blockIdx.x + (first_unit ? 0 : 1);
     const int hk = cur.u / p.ngrp, g0 = cur.u % p.ngrp * C::GR;
     const int rows = min(C::GR, p.G - g0);
     const long long head0 = static_cast<long long>(cur.b) * p.H + hk * p.G + g0;
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    // CLUSTER: row r of the merged state is in the second stage of warp r / (rows that fit)
+    auto state_row = [&](int r) {
+      constexpr int FITS = C::STAGE_BYTES / (D * 4);
+      return (r / FITS * S + 1) * C::STAGE_BYTES + r % FITS * (D * 4);
+    };
     auto stage_of = [&](int w) { return reinterpret_cast<float*>(smem + (w * S + stage) * C::STAGE_BYTES); };
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
@@ -510,7 +667,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
           acc.z = fmaf(y.z, wt, acc.z);
           acc.w = fmaf(y.w, wt, acc.w);
         }
-        if (whole && !p.prefix) {
+        if constexpr (CLUSTER) {
+          *reinterpret_cast<float4*>(smem + state_row(grow) + pc * 16) = acc;
+          if (pc == 0) reinterpret_cast<float2*>(smem + C::OFF_Q)[grow] = make_float2(M, L);
+        } else if (whole && !p.prefix) {
           const float inv = 1.f / L;
           *reinterpret_cast<uint2*>(p.o + (head0 + grow) * D + pc * 4) =
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -522,7 +682,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
         }
       }
       if (nt == C::NT - 1) {
-        if (seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
+        if (!CLUSTER && seg_tile0 == 0 && threadIdx.x == 0) {  // begun here: what will be found where
           const long long last = t0 + cur.v - cur.tile + cur.nt - 1;
           p.infos[static_cast<long long>(cur.b) * p.U + cur.u] =
               make_int2(whole ? -1 : slot, static_cast<int>(cta_of(last, total, n) - blockIdx.x + 1));
@@ -530,6 +690,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
         if (more) store_q();  // every warp is past its products with the unit's queries
       }
       __syncthreads();
+    }
+    if constexpr (CLUSTER) {
+      join_cluster<C>(p, cur.b, cur.len, rows, hk, g0, head0, rank, smem, state_row);
+      return;
     }
     if (!more) break;
     first_unit = false;
@@ -709,6 +873,18 @@ int join_warps(long long units, long long heads, long long tiles, const PagedPla
   return parts > 8 || heads <= 8LL * sms ? 4 : 1;
 }
 
+// CTAs of a unit in the form where every unit has a cluster of its own, or 0 for even ranges of tiles.  `tiles`: of the
+// longest sequence that its table can hold.  As many as are resident twice a SM at most, and have a tile or more each.
+// A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to 4 us)
+// are used up, whatever the real lengths are.  Clusters against ranges, device time at 32 heads on 8 of 128:
+// 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000: 12.1 and 10.2; 16 of 300: 6.7 and 8.9; 48 of 400:
+// 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400: 29.7 and 32.4; 47 of 60 to 120 behind a prefix: 15.2 and 20.0.
+int cluster_size(long long units, long long tiles, int sms) {
+  int cl = 1;
+  while (cl < 8 && cl < tiles && tiles > 2 && units * cl * 2 <= 2 * sms) cl *= 2;
+  return tiles <= 8 * cl && units * cl <= 0x7FFFFFFF ? cl : 0;
+}
+
 template <class C>
 cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   PgParams p = {};
@@ -740,7 +916,10 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.part_ml = reinterpret_cast<float*>(a.ws + pl.part_ml);
   p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
   p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
-  cudaError_t e = allow_shared_memory<fa_paged_kernel<C>>(C::SMEM);
+  const long long units = static_cast<long long>(a.B) * p.U;
+  p.cl = cluster_size(units, (p.cap + C::TILE - 1) / C::TILE, a.sms);
+  cudaError_t e = p.cl > 0 ? allow_shared_memory<fa_paged_kernel<C, true>>(C::SMEM)
+                           : allow_shared_memory<fa_paged_kernel<C, false>>(C::SMEM);
   if (e != cudaSuccess) return e;
   if (a.prefix_len > 0) {
     p.prefix = 1;
@@ -752,10 +931,13 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
     if ((e = launch_prefix(a, pl)) != cudaSuccess) return e;
   }
   // programmatic dependents: a launch overlaps the end of the kernel before it
-  if ((e = launch_dependent(fa_paged_kernel<C>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
+  if (p.cl > 0)
+    return launch_dependent_clusters(fa_paged_kernel<C, true>, static_cast<unsigned>(units * p.cl), p.cl, 32 * C::NW, C::SMEM,
+                                     a.stream, p);
+  if ((e = launch_dependent(fa_paged_kernel<C, false>, pl.n_cta, 32 * C::NW, C::SMEM, a.stream, p)) != cudaSuccess) return e;
   const long long heads = static_cast<long long>(a.B) * a.H, most = static_cast<long long>(a.sms) * 16;
   const unsigned rows = static_cast<unsigned>(heads < most ? heads : most);
-  switch (join_warps(static_cast<long long>(a.B) * p.U, heads, p.cap / C::TILE + 1, pl, a.sms)) {
+  switch (join_warps(units, heads, p.cap / C::TILE + 1, pl, a.sms)) {
     case 16: return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 16>, rows, 512, 0, a.stream, p);
     case 4: return launch_dependent(fa_paged_join_kernel<C::D, C::GR, 4>, rows, 128, 0, a.stream, p);
     default: {

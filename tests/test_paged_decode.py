@@ -24,13 +24,24 @@ def _ok():
     assert fa.fa_check_device_error() == fa.FA_OK
 
 
+# Keys that every table has room for.  Short tables are taken by one cluster of CTAs a unit, with no join after it;
+# tables of 40000 keys by CTAs that share all tiles evenly.
+MIN_TABLE = 0
+
+
+@pytest.fixture(params=[0, 40_000], ids=["clusters", "ranges"])
+def table_room(request, monkeypatch):
+    monkeypatch.setitem(globals(), "MIN_TABLE", request.param)
+
+
 def _case(dev, lens, H, Hkv, d, ps, seed, layout="head", prefix_len=0, spoil=True):
     tables, prefix, total = ref.deal_pages(lens, ps, seed, extra=-(-prefix_len // ps))
     kc, vc = ref.paged_cache(total, Hkv, ps, d, dev, seed + 1, layout)
     if spoil:
         ref.spoil_unused(kc, vc, tables, lens, prefix, prefix_len)
     return dict(q=_q(len(lens), H, d, dev, seed + 2), kc=kc, vc=vc, tables=tables, prefix=prefix, plen=prefix_len,
-                table=ref.page_table(tables, dev, junk=1 << 29), lens=lens,
+                table=ref.page_table(tables, dev, max(max(map(len, tables), default=1), -(-MIN_TABLE // ps), 1), 1 << 29),
+                lens=lens,
                 lens_t=torch.as_tensor(np.asarray(lens, np.int32), device=dev),
                 prefix_t=torch.as_tensor(np.asarray(prefix, np.int32), device=dev))
 
@@ -53,7 +64,7 @@ RAGGED = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 130, 300, -1, 511, 700]
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 4), (6, 2), (8, 1), (16, 2), (17, 1), (24, 2), (33, 1), (71, 1)], ids=str)
-def test_groups(cuda_device, d, H, Hkv):
+def test_groups(cuda_device, table_room, d, H, Hkv):
     c = _case(cuda_device, RAGGED, H, Hkv, d, 16, 1000 + H + d)
     o, lse = _run(c)
     _ok()
@@ -62,7 +73,7 @@ def test_groups(cuda_device, d, H, Hkv):
 
 @pytest.mark.parametrize("layout", ["head", "row", "one", "odd"])
 @pytest.mark.parametrize("ps", [1, 5, 8, 16, 24, 64, 100, 256, 1024])
-def test_pages_and_layouts(cuda_device, layout, ps):
+def test_pages_and_layouts(cuda_device, table_room, layout, ps):
     """Page sizes that divide a tile, span several or end inside one; contiguous and strided caches; unused rows and
     pages hold NaN and infinities, unused table entries numbers past the cache."""
     for d, lens in ((64, RAGGED), (128, [ps, ps + 1, max(1, ps - 1), 2 * ps, 333])):
@@ -99,7 +110,7 @@ def test_many_sequences(cuda_device, d, H, Hkv):
 
 
 @pytest.mark.parametrize("scale", [1.0, 0.0, -0.2, 1e-3])
-def test_scales(cuda_device, scale):
+def test_scales(cuda_device, table_room, scale):
     c = _case(cuda_device, [100, 1, 77], 4, 2, 64, 16, 1400)
     o, lse = _run(c, scale=scale)
     _ok()
@@ -108,7 +119,7 @@ def test_scales(cuda_device, scale):
 
 @pytest.mark.parametrize("d,B", [(64, 3), (64, 40), (128, 3), (128, 40)])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
-def test_prefix_scales(cuda_device, scale, d, B):
+def test_prefix_scales(cuda_device, table_room, scale, d, B):
     """Both tile widths of the prefix (B * 4 rows a head), its last tile ragged, infinities and NaN behind its end."""
     c = _case(cuda_device, [17 + b % 5 for b in range(B)], 8, 2, d, 16, 1430 + B, prefix_len=203)
     o, lse = _run(c, scale=scale)
@@ -118,7 +129,7 @@ def test_prefix_scales(cuda_device, scale, d, B):
 
 
 @pytest.mark.parametrize("prefix_len", [0, 150])
-def test_peaked_scores_and_late_maxima(cuda_device, prefix_len):
+def test_peaked_scores_and_late_maxima(cuda_device, table_room, prefix_len):
     """Scores that grow along the sequence by far more than a rescale threshold, and one key that outweighs all."""
     for d in (64, 128):
         c = _case(cuda_device, [900, 33, 257], 8, 2, d, 16, 1500 + d, prefix_len=prefix_len, spoil=False)
@@ -131,7 +142,7 @@ def test_peaked_scores_and_late_maxima(cuda_device, prefix_len):
         _check(c, o, lse, f"peaked d{d} prefix {prefix_len}")
 
 
-def test_infinite_and_nan_keys_stay_in_their_sequence(cuda_device):
+def test_infinite_and_nan_keys_stay_in_their_sequence(cuda_device, table_room):
     """NaN or infinity in a key or value that a sequence does see makes that sequence's heads NaN (or infinite), as the
     formula does, and no other's."""
     c = _case(cuda_device, [70, 70, 70, 70], 4, 2, 64, 16, 1600)
@@ -147,7 +158,7 @@ def test_infinite_and_nan_keys_stay_in_their_sequence(cuda_device):
 
 
 @pytest.mark.parametrize("prefix_len", [0, 40])
-def test_bad_pages_and_lengths(cuda_device, prefix_len):
+def test_bad_pages_and_lengths(cuda_device, table_room, prefix_len):
     """A page outside the cache or a length past the table gives NaN in that sequence alone and is reported; nothing is
     read out of bounds (every index is checked before it is used)."""
     c = _case(cuda_device, [100, 64, 33, 16, 5], 8, 2, 128, 16, 1700, prefix_len=prefix_len)
@@ -166,7 +177,7 @@ def test_bad_pages_and_lengths(cuda_device, prefix_len):
     _check(c, o, lse, "beside bad pages", seqs=[1, 4])
 
 
-def test_bad_prefix_page(cuda_device):
+def test_bad_prefix_page(cuda_device, table_room):
     c = _case(cuda_device, [30, 0, -1, 50], 8, 2, 64, 16, 1750, prefix_len=200)
     c["prefix_t"][5] = 1 << 28
     o, lse = _run(c)
@@ -181,7 +192,7 @@ def test_bad_prefix_page(cuda_device):
     (1, 4, 4, 16, 1), (2, 8, 2, 16, 63), (3, 6, 2, 64, 64), (5, 16, 2, 16, 1000), (33, 8, 1, 32, 517), (40, 24, 2, 24, 300),
     (70, 4, 4, 5, 129), (64, 8, 2, 128, 2048), (9, 40, 1, 256, 100), (4, 8, 8, 8, 4000), (3, 4, 1, 1, 70),
     (150, 16, 4, 16, 700), (140, 4, 2, 5, 200), (90, 12, 4, 24, 333), (200, 16, 8, 8, 97)], ids=str)
-def test_prefix(cuda_device, d, B, H, Hkv, ps, prefix_len):
+def test_prefix(cuda_device, table_room, d, B, H, Hkv, ps, prefix_len):
     """Sequences with the prefix alone, with own rows behind it, and unused places; prefixes of one key, ending inside a
     page or a tile; batches below and above one tile of query rows."""
     rng = np.random.default_rng(1800 + B)
@@ -196,7 +207,7 @@ def test_prefix(cuda_device, d, B, H, Hkv, ps, prefix_len):
 
 
 @pytest.mark.parametrize("layout", ["row", "one", "odd"])
-def test_prefix_layouts(cuda_device, layout):
+def test_prefix_layouts(cuda_device, table_room, layout):
     for d, ps in ((64, 16), (128, 64), (64, 100), (128, 12)):
         c = _case(cuda_device, [5, 80, 0], 8, 2, d, ps, 1900 + d, layout, prefix_len=333)
         o, lse = _run(c)
@@ -227,7 +238,7 @@ def test_prefix_equals_the_same_keys_in_every_table(cuda_device):
     assert (o3.float() - o4.float()).abs().max() <= 4 * 2.0 ** -8 * o3.float().abs().max().clamp(min=1.0)
 
 
-def test_repeats_are_identical_and_caller_buffers(cuda_device):
+def test_repeats_are_identical_and_caller_buffers(cuda_device, table_room):
     """Bit-identical repeats, into a caller's o with a caller's dirty workspace."""
     for plen in (0, 700):
         c = _case(cuda_device, [900, 20, 0, 4000, 1], 16, 2, 128, 16, 2100, prefix_len=plen)
@@ -242,7 +253,7 @@ def test_repeats_are_identical_and_caller_buffers(cuda_device):
         _ok()
 
 
-def test_workspace_that_is_too_small_is_refused(cuda_device):
+def test_workspace_that_is_too_small_is_refused(cuda_device, table_room):
     for plen, ps in ((0, 16), (700, 16), (90, 5)):
         c = _case(cuda_device, [90, 20], 16, 2, 128, ps, 2150, prefix_len=plen)
         need = fa.fa_decode_paged_workspace_bytes(2, 16, 2, 128, ps, plen)
@@ -252,7 +263,7 @@ def test_workspace_that_is_too_small_is_refused(cuda_device):
         _ok()
 
 
-def test_side_stream_and_threads(cuda_device):
+def test_side_stream_and_threads(cuda_device, table_room):
     """Calls on side streams, also from two host threads at once, give the results of the default stream."""
     import threading
     cases = [_case(cuda_device, [3000, 17, 0, 450], 8, 2, 64, 16, 2200 + i, prefix_len=500 * i) for i in range(2)]
@@ -364,7 +375,7 @@ def test_long_cache_offsets(cuda_device):
     assert int((kc[pages - 5] != 0).any(-1).sum()) == Hkv
 
 
-def test_optional_results_and_views(cuda_device):
+def test_optional_results_and_views(cuda_device, table_room):
     """No LSE asked for; q with a token dimension; a table that is a slice of a wider one; prefix pages with
     more entries than the prefix needs; one sequence on one key/value head (strides of single entries)."""
     c = _case(cuda_device, [40, 0, 129], 8, 2, 64, 16, 2550, prefix_len=50)
