@@ -874,17 +874,23 @@ int join_warps(long long units, long long heads, long long tiles, const PagedPla
 }
 
 // CTAs of a unit in the form where every unit has a cluster of its own, or 0 for even ranges of tiles.  `tiles`: of the
-// longest sequence that its table can hold.  As many as are resident twice a SM at most, and have a tile or more each.
-// A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to 4 us)
-// are used up, whatever the real lengths are; behind a prefix, whose states are joined too, at sixteen.  Clusters against
-// ranges, device time at 32 heads on 8 of 128: 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000: 12.1 and
-// 10.2; 16 of 300: 6.7 and 8.9, 1500: 18.8 and 14.0; 48 of 400: 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400: 29.7
-// and 32.4; behind a prefix 48 of 60: 17.3 and 24.6, 64 of 800: 48 and 56, 256 of 1 to 600: 77.7 and 81.6, 64 of 1 to
+// longest sequence that its table can hold; n_cta: CTAs that may run at once.  As many as there is room for, less the
+// places that clusters of this size leave free in each of the GPU's 8 processor clusters (3000 keys in 56 clusters of 8: 16.0 us, of 7:
+// 9.9); behind a prefix, whose CTAs want room too, a power of two and two CTAs a SM (96 units in clusters of 3: 14.0 us, of
+// 2: 11.0).  A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to
+// 4 us) are used up, whatever the real lengths are; behind a prefix, whose states are joined too, at sixteen.  Clusters
+// against ranges, device time at 32 heads on 8 of 128: 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000:
+// 12.1 and 10.2; 16 of 300: 6.1 and 8.9, 1500: 14.4 and 14.1; 48 of 400: 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400:
+// 29.7 and 32.4; behind a prefix 48 of 60: 17.3 and 24.6, 64 of 800: 48 and 56, 256 of 1 to 600: 77.7 and 81.6, 64 of 1 to
 // 1500: 34.1 and 33.6.
-int cluster_size(long long units, long long tiles, int sms, bool prefix) {
-  int cl = 1;
-  while (cl < 8 && cl < tiles && tiles > 2 && units * cl * 2 <= 2 * sms) cl *= 2;
-  return tiles <= (prefix ? 16 : 8) * cl && units * cl <= 0x7FFFFFFF ? cl : 0;
+int cluster_size(long long units, long long tiles, int n_cta, int sms, bool prefix) {
+  const long long most = tiles > 2 ? (tiles < 8 ? tiles : 8) : 1;
+  long long cl = 1;
+  if (prefix)
+    while (cl * 2 <= 8 && cl < most && units * cl <= sms) cl *= 2;
+  else
+    while (cl < most && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
+  return tiles <= (prefix ? 16 : 8) * cl && units * cl <= 0x7FFFFFFF ? static_cast<int>(cl) : 0;
 }
 
 template <class C>
@@ -919,7 +925,7 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
   p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
   const long long units = static_cast<long long>(a.B) * p.U;
-  p.cl = cluster_size(units, (p.cap + C::TILE - 1) / C::TILE, a.sms, a.prefix_len > 0);
+  p.cl = cluster_size(units, (p.cap + C::TILE - 1) / C::TILE, pl.n_cta, a.sms, a.prefix_len > 0);
   cudaError_t e = p.cl > 0 ? allow_shared_memory<fa_paged_kernel<C, true>>(C::SMEM)
                            : allow_shared_memory<fa_paged_kernel<C, false>>(C::SMEM);
   if (e != cudaSuccess) return e;
