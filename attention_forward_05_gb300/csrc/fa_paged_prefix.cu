@@ -5,10 +5,10 @@
 // keys: the forward kernel's tensor-core tiles (fa_fwd_kernel.cuh), with K and V copied out of the cache's pages
 // and partial states (m, l, unnormalised O) as its result.  The prefix is read once a key split instead of once
 // a sequence, and for large batches the work is bound by the matrix rate.  The sequences' own keys follow in
-// fa_paged_kernel, and fa_paged_join_kernel (fa_paged.cu) joins the states.
+// fa_paged_kernel (fa_paged.cu), whose clusters, or fa_paged_join_kernel behind it, join the states.
 //
-// Measured, the whole call: 16384 shared keys, 256 sequences (d = 128, 32 heads on 8) 83 us, 829 TFLOP/s, of which this
-// kernel takes 54; 8192 shared keys, 32 sequences (d = 64) 19 us; 1000 and 5 8.6 us.
+// Measured, the whole call: 16384 shared keys, 256 sequences (d = 128, 32 heads on 8) 78 us, 880 TFLOP/s, of which this
+// kernel takes 54; 8192 shared keys, 32 sequences (d = 64) 13 us; 1000 and 5 6.7 us.
 //
 // Configurations (fa_fwd_bf16.cu and fa_fwd_decode.cu have the same tiles): two 128-row query tiles per CTA, or
 // one where the B * G rows of a head fit in it.
