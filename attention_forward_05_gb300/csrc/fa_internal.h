@@ -83,6 +83,22 @@ cudaError_t allow_shared_memory(int bytes) {
 // Records a CUDA error for fa_last_cuda_error() and returns FA_ERR_CUDA.
 int report_cuda_error(cudaError_t e);
 
+// Division of numbers below 2^31 by a fixed one.
+struct FastDiv {
+  unsigned mul, shift, d;
+  explicit FastDiv(unsigned n) : mul(0), shift(0), d(n) {
+    if (n <= 1) return;
+    unsigned l = 0;
+    while ((1u << l) < n) ++l;
+    mul = static_cast<unsigned>((1ull << (31 + l)) / n + 1);
+    shift = l - 1;
+  }
+  FastDiv() : FastDiv(1) {}
+  __device__ __forceinline__ int div(int x) const {
+    return d <= 1 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), mul) >> shift);
+  }
+};
+
 // Rotation of position pairs shared by fa_rope and fa_paged_append (fa_rope.cu).
 struct Rotary {
   const double* freqs = nullptr;  // device [rot / 2], radians per position

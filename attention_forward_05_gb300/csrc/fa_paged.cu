@@ -30,8 +30,8 @@
 // lanes look up their keys' pages one step ahead.  Page sizes that are multiples of 16 rows copy 16 rows from
 // one base address; others pass every row's offset around by shuffles.
 //
-// Measured, device time: 32 sequences of 32768 keys (d = 64, groups of 4) 305 us, 7.0 TB/s (floor 322 us at the copy's rate);
-// 61 sequences of 0 to 32768 keys (d = 128, groups of 8) 69 us, 5.9 TB/s; one of 777 keys 4.9 us (6.6 us by ranges).
+// Measured, device time: 32 sequences of 32768 keys (d = 64, groups of 4) 305 us, 7.0 TB/s (floor 322 us at the copy's
+// rate); 61 sequences of 0 to 32768 keys (d = 128, groups of 8) 69 us, 5.9 TB/s; one of 777 keys 4.9 us (6.6 by ranges).
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -67,22 +67,6 @@ struct PgCfg {
   static constexpr int FIT = STAGE_BYTES / (GR * D * 4) > 0 ? NT : STAGE_BYTES / (8 * D * 4);  // head tiles whose O fits a stage
   static_assert(NT % FIT == 0, "whole rounds");
   static_assert(SMEM * CTAS <= 227 * 1024 - CTAS * 1024, "shared memory");
-};
-
-// Division of numbers below 2^31 by a fixed one.
-struct FastDiv {
-  unsigned mul, shift, d;
-  explicit FastDiv(unsigned n) : mul(0), shift(0), d(n) {
-    if (n <= 1) return;
-    unsigned l = 0;
-    while ((1u << l) < n) ++l;
-    mul = static_cast<unsigned>((1ull << (31 + l)) / n + 1);
-    shift = l - 1;
-  }
-  FastDiv() : FastDiv(1) {}
-  __device__ __forceinline__ int div(int x) const {
-    return d <= 1 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), mul) >> shift);
-  }
 };
 
 struct PgParams {
@@ -875,9 +859,9 @@ int join_warps(long long units, long long heads, long long tiles, const PagedPla
 
 // CTAs of a unit in the form where every unit has a cluster of its own, or 0 for even ranges of tiles.  `tiles`: of the
 // longest sequence that its table can hold; n_cta: CTAs that may run at once.  As many as there is room for, less the
-// places that clusters of this size leave free in each of the GPU's 8 processor clusters (3000 keys in 56 clusters of 8: 16.0 us, of 7:
-// 9.9); behind a prefix, whose CTAs want room too, a power of two and two CTAs a SM (96 units in clusters of 3: 14.0 us, of
-// 2: 11.0).  A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to
+// places that clusters of this size leave free in each of the GPU's 8 processor clusters (3000 keys in 56 clusters of 8:
+// 16.0 us, of 7: 9.9); behind a prefix, whose CTAs want room too, a power of two and two CTAs a SM (96 units in clusters
+// of 3: 14.0 us, of 2: 11.0).  A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to
 // 4 us) are used up, whatever the real lengths are; behind a prefix, whose states are joined too, at sixteen.  Clusters
 // against ranges, device time at 32 heads on 8 of 128: 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000:
 // 12.1 and 10.2; 16 of 300: 6.1 and 8.9, 1500: 14.4 and 14.1; 48 of 400: 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400:

@@ -13,6 +13,8 @@ namespace {
 
 constexpr long long kMaxElems = 1LL << 38;  // strides in bytes stay below the tensor maps' 2^40
 
+constexpr long long kMaxTokens = (1LL << 31) - 1024;  // token indices of a block stay below 2^31
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Strides in elements whose rows must start on 16-byte boundaries; `unit` elements are 16 bytes.
@@ -58,7 +60,7 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long l
   int rc = check_rotation(positions, freqs, axes, n_axes, rot, interleaved, d);
   if (rc != FA_OK) return rc;
   const long long heads = static_cast<long long>(H) + Hkv, tokens = static_cast<long long>(B) * N;
-  if (heads > 0x7FFFFFFFLL / d || tokens > kMaxElems || tokens > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
+  if (tokens > kMaxTokens || heads > 0x7FFFFFFFLL / d || tokens > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
   long long s[12];
   for (int i = 0; i < 4; ++i) {
     const long long h = (i & 1) ? Hkv : H;
@@ -116,7 +118,7 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
     if (rc != FA_OK) return rc;
   }
   const long long heads = static_cast<long long>(H) + 2LL * Hkv;
-  if (heads > 0x7FFFFFFFLL / d || T > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
+  if (T > kMaxTokens || heads > 0x7FFFFFFFLL / d || T > kMaxElems / (heads * d)) return FA_ERR_INVALID_ARG;
   long long s[6], c[3];
   for (int i = 0; i < 3; ++i) {
     s[2 * i] = in_strides ? in_strides[2 * i] : static_cast<long long>(i < 2 ? Hkv : H) * d;

@@ -16,16 +16,20 @@
 // operations each and are formed once per block in shared memory (double precision runs at about two
 // operations a clock and SM here).
 //
-// Work split.  A thread owns one 16-element unit (eight pairs) of one token; its eight sines and cosines serve
-// all the heads it takes, and the loads of four heads are in flight together.  Copies are
-// 16 bytes wide.  Items (a block of tokens, up to four heads) are dealt to the resident blocks in even,
-// contiguous ranges, a token's heads next to each other: a block keeps the sines and cosines while the tokens
-// stay the same, reads a projection's [heads, d] row at about one time, and no block has an item more than
-// another one has.  Both kernels are bound by device memory (each element is read once and written once) as
-// long as the instructions are few: the products go in packed fp32 pairs.  Measured in bf16, bytes read and
-// written over the time with the launch (about 3 us): q and k of 4 x 4096 tokens, 32 heads of 64: 22 us, 6.0 TB/s
-// (with eight heads an item, dealt in turn, and sincospif: 32 us); 2 x 8192 tokens, 20 heads of 128, three axes,
-// adjacent pairs: 31 us, 5.4 TB/s (36); appending 8191 tokens, 48 heads of 128: 38 us, 5.4 TB/s (42).
+// Work split.  A lane owns a unit of a head, eight pairs, in pieces of 16 bytes that lie next to its neighbours' pieces.  A
+// warp's items are a few tokens with up to 16 heads each; their bytes arrive by asynchronous copies in a ring of the
+// warp's own, two items ahead, with the positions (and slots) they need, so nothing waits for a load and no warp
+// waits for another.  Four lanes hold the same unit of four heads and form two of its pairs' sines and cosines each.
+// Consecutive items go to consecutive warps, so the whole GPU reads and writes in few places of device memory.
+//
+// Both kernels are bound by device memory (each element is read once and written once) as long as the instructions
+// are few: the products go in packed fp32 pairs.  Measured, bytes read and written over the time with the launch (about
+// 3 us): q and k of 4 x 4096 tokens, 32 heads of 64, bf16: 24.0 us, 5.6 TB/s; 2 x 8192 tokens, 20 heads of 128, three
+// axes, adjacent pairs: 29.5 us, 5.7 TB/s; appending 8191 tokens, 48 heads of 128: 36.2 us, 5.6 TB/s; 333 tokens, 20 heads
+// of 64, fp32: 2.7 us.  With register loads of the current item, each block on one contiguous range: 26.3, 31.1, 36.3
+// and 3.2 us; with adjacent pairs' 32 bytes a lane in two half-sector copies instead of pieces: 32.0 and 37.6 us for the
+// second and third.  (Past 300 MB at d = 128 lanes that form all eight pairs of their own token, as for few heads below,
+// are up to 10 % faster: 54 against 60 us on 336 MB; below that up to 25 % slower.)
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -88,26 +92,30 @@ __device__ __forceinline__ void turn_sincos(int pos, unsigned long long step, fl
   *sn = __uint_as_float(__float_as_uint(b) ^ (quarter & 2u) << 30);        // sin: + + - -
 }
 
+// Packed cosines and sines of pairs a and b at positions pa and pb.
+__device__ __forceinline__ void two_turns(const PairTurn& a, const PairTurn& b, int pa, int pb, bool inverse, uint64_t* c,
+                                          uint64_t* s) {
+  float ca, sa, cb, sb;
+  turn_sincos(pa, a.step, &ca, &sa);
+  turn_sincos(pb, b.step, &cb, &sb);
+  if (inverse) sa = -sa, sb = -sb;
+  if (a.axis == 255) ca = sa = __int_as_float(0x7fc00000);
+  if (b.axis == 255) cb = sb = __int_as_float(0x7fc00000);
+  *c = f2_pack(ca, cb);
+  *s = f2_pack(sa, sb);
+}
+
 // A thread's eight pairs as packed operands: cos, sin and -sin of pairs 2j and 2j + 1.
 struct Turn {
   uint64_t c[4], s[4], n[4];
 
-  // pairs[0 .. 7] at the positions pos[axis * stride]
-  __device__ __forceinline__ void set(const PairTurn* pairs, const int* pos, long long stride, bool inverse) {
+  // (cs, sn): packed cosines and sines of two pairs, those of pairs 2j and 2j + 1 in lane first + j * step
+  __device__ __forceinline__ void gather(uint64_t cs, uint64_t sn, int first, int step) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float cs[2], sn[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const PairTurn t = pairs[2 * j + i];
-        const bool ok = t.axis != 255;
-        turn_sincos(ok ? pos[t.axis * stride] : 0, t.step, &cs[i], &sn[i]);
-        if (inverse) sn[i] = -sn[i];
-        if (!ok) cs[i] = sn[i] = __int_as_float(0x7fc00000);
-      }
-      c[j] = f2_pack(cs[0], cs[1]);
-      s[j] = f2_pack(sn[0], sn[1]);
-      n[j] = f2_pack(-sn[0], -sn[1]);
+      c[j] = __shfl_sync(0xffffffffu, cs, first + j * step);
+      s[j] = __shfl_sync(0xffffffffu, sn, first + j * step);
+      n[j] = s[j] ^ 0x8000000080000000ull;
     }
   }
   // x1, x2: the first and second elements of pairs 2j and 2j + 1
@@ -118,13 +126,9 @@ struct Turn {
   }
 };
 
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 // A 16-element unit of one head: two runs of eight elements at offsets e0 and e1.
@@ -132,14 +136,20 @@ template <typename T>
 struct Unit;
 template <>
 struct Unit<__nv_bfloat16> {
+  static constexpr int PIECES = 2;  // of 16 bytes
   uint4 a, b;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int e0, int e1) {
-    a = load16(p + e0);
-    b = load16(p + e1);
+  // global -> this lane's places in shared memory, one every 512 bytes
+  static __device__ __forceinline__ void fetch(uint32_t dst, const __nv_bfloat16* p, int e0, int es) {
+    cp_async16(dst, p + e0);
+    cp_async16(dst + 512, p + e0 + es);
   }
-  __device__ __forceinline__ void store(__nv_bfloat16* p, int e0, int e1) const {
+  __device__ __forceinline__ void load(const uint4* p) {
+    a = p[0];
+    b = p[32];
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int e0, int es) const {
     *reinterpret_cast<uint4*>(p + e0) = a;
-    *reinterpret_cast<uint4*>(p + e1) = b;
+    *reinterpret_cast<uint4*>(p + e0 + es) = b;
   }
   // in fp32, one rounding, to nearest even
   template <bool INTER>
@@ -164,18 +174,19 @@ struct Unit<__nv_bfloat16> {
 };
 template <>
 struct Unit<float> {
+  static constexpr int PIECES = 4;
   uint4 v[4];
-  __device__ __forceinline__ void load(const float* p, int e0, int e1) {
-    v[0] = load16(p + e0);
-    v[1] = load16(p + e0 + 4);
-    v[2] = load16(p + e1);
-    v[3] = load16(p + e1 + 4);
+  static __device__ __forceinline__ void fetch(uint32_t dst, const float* p, int e0, int es) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cp_async16(dst + 512 * i, p + e0 + i * es);
   }
-  __device__ __forceinline__ void store(float* p, int e0, int e1) const {
-    *reinterpret_cast<uint4*>(p + e0) = v[0];
-    *reinterpret_cast<uint4*>(p + e0 + 4) = v[1];
-    *reinterpret_cast<uint4*>(p + e1) = v[2];
-    *reinterpret_cast<uint4*>(p + e1 + 4) = v[3];
+  __device__ __forceinline__ void load(const uint4* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = p[32 * i];
+  }
+  __device__ __forceinline__ void store(float* p, int e0, int es) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(p + e0 + i * es) = v[i];
   }
   template <bool INTER>
   __device__ __forceinline__ void turn(const Turn& r) {
@@ -198,180 +209,277 @@ struct Unit<float> {
   }
 };
 
-// Offsets of unit u's two runs, and whether it is rotated.
-template <bool INTER>
-__device__ __forceinline__ bool unit_offsets(int rot, int u, int* e0, int* e1) {
-  if (u < rot / 16 && !INTER) {
-    *e0 = 8 * u;
-    *e1 = rot / 2 + 8 * u;
-    return true;
-  }
-  *e0 = 16 * u;
-  *e1 = 16 * u + 8;
-  return u < rot / 16;
+// Where unit u's pieces of 16 bytes begin: at e0, e0 + es, ... ; returns whether it is rotated.  Neighbouring units' pieces
+// lie next to each other, so that the lanes' 16 bytes fill whole 32-byte sectors.
+template <typename T, int D>
+__device__ __forceinline__ bool unit_pieces(int rot, int u, int* e0, int* es) {
+  constexpr int W = 16 / sizeof(T), NP = 16 / W;  // elements of a piece, pieces of a unit
+  const bool rotated = u < rot / 16;
+  *e0 = rotated ? W * u : rot + W * (u - rot / 16);
+  *es = (rotated ? rot : D - rot) / NP;
+  return rotated;
+}
+// The q-th of its eight pairs: runs of RUN pairs, RUN * 2 elements (adjacent pairs) or RUN elements of either half of `rot`.
+template <typename T, bool INTER>
+__device__ __forceinline__ int unit_pair(int rot, int u, int q) {
+  constexpr int W = 16 / sizeof(T), RUN = INTER ? W / 2 : W;
+  return q / RUN * (rot / 2 * RUN / 8) + RUN * u + q % RUN;
 }
 
-// Items of a kernel: item = token block * slices + slice; the slice is heads slice * per .. slice * per + per - 1,
-// per <= HEADS.  Block i takes items i * count / gridDim.x to (i + 1) * count / gridDim.x - 1.
-constexpr int HEADS = 4;
-struct Items {
-  long long count;
-  int slices, per;
+// A warp's item is a few tokens and one of `slices` parts of the heads.  QUAD: a lane is (token, head lane, unit) and takes
+// heads part * 4 * per + head lane + 4 i, i < per; the four head lanes of a unit form two pairs' sines and cosines each.
+// Without QUAD, for up to three heads, a lane is (token, unit), takes heads part * per + i and forms all eight (65536 tokens
+// of one head of 64: 8.2 us, with QUAD 16.2; of four heads: 4.1 us on 8192 tokens with QUAD, 5.5 without).
+// Warps take every (number of warps)-th item, so that they are near one another in memory.
+struct Tiling {
+  int count, slices, per;
 };
+
+template <int D, bool QUAD>
+struct Lane {
+  static constexpr int UNITS = D / 16, PER_TOKEN = QUAD ? 4 * UNITS : UNITS, TOKS = 32 / PER_TOKEN, STEP = QUAD ? 4 : 1;
+  int lane, u, hl, tok;
+  __device__ __forceinline__ Lane()
+      : lane(threadIdx.x & 31), u(lane % UNITS), hl(QUAD ? lane / UNITS % 4 : 0), tok(lane / PER_TOKEN) {}
+};
+
+// A warp's stage of the ring: 8 pieces of data and a slot a lane, and the tokens' positions on up to 8 axes.
+constexpr int STAGES = 3;
+constexpr int PIECE_SLOTS = 8;
+constexpr int OFF_POS = PIECE_SLOTS * 512, OFF_SLOT = OFF_POS + 256, STAGE_BYTES = OFF_SLOT + 256;
+constexpr int ROPE_SMEM = ROPE_THREADS / 32 * STAGES * STAGE_BYTES;
+
+struct Walk {
+  int item, block, slice;
+  __device__ __forceinline__ Walk(const Tiling& g) {
+    item = blockIdx.x * (ROPE_THREADS / 32) + threadIdx.x / 32;
+    block = item / g.slices;
+    slice = item - block * g.slices;
+  }
+  __device__ __forceinline__ void next(const Tiling& g, int step, int step_block, int step_slice) {
+    item += step;
+    block += step_block;
+    slice += step_slice;
+    if (slice >= g.slices) slice -= g.slices, ++block;
+  }
+};
+
+// Runs a warp's items.  fetch(token, first head, address, address of the slot): starts a lane's copies and returns where the
+// token's position on axis 0 is; finish(token, first head, pieces, slot, turn): rotates and stores them.
+template <typename T, int D, bool INTER, bool QUAD, typename Fetch, typename Finish>
+__device__ __forceinline__ void run_items(const Tiling& g, const Rotary& r, const PairTurn* pairs, bool rotated, int tokens,
+                                          Fetch fetch, Finish finish) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  using L = Lane<D, QUAD>;
+  const L l;
+  uint8_t* const mine = ring + threadIdx.x / 32 * STAGES * STAGE_BYTES;
+  const int step = gridDim.x * (ROPE_THREADS / 32), step_block = step / g.slices, step_slice = step - step_block * g.slices;
+  const auto pair = [&](int q) { return pairs[unit_pair<T, INTER>(r.rot, l.u, q)]; };
+  PairTurn p0{0, 255, 0}, p1{0, 255, 0};
+  if (QUAD && rotated) p0 = pair(2 * l.hl), p1 = pair(2 * l.hl + 1);
+  Walk ld(g);
+  int ld_stage = 0, stage = 0;
+  auto load = [&]() {
+    if (ld.item < g.count) {
+      const int t = ld.block * L::TOKS + l.tok;
+      if (t < tokens) {
+        const uint32_t dst = smem_u32(mine) + ld_stage * STAGE_BYTES;
+        const int* const pos = fetch(t, ld.slice * L::STEP * g.per + l.hl, dst + l.lane * 16, dst + OFF_SLOT + l.lane * 8);
+        if (QUAD) {  // of its two pairs
+          if (p0.axis != 255) cp_async_small<4>(dst + OFF_POS + l.lane * 8, pos + p0.axis * r.axis_stride);
+          if (p1.axis != 255) cp_async_small<4>(dst + OFF_POS + l.lane * 8 + 4, pos + p1.axis * r.axis_stride);
+        } else if (r.rot > 0) {  // the token's, on every axis
+          for (int ax = l.u; ax < r.n_axes; ax += L::PER_TOKEN)
+            cp_async_small<4>(dst + OFF_POS + l.tok * 32 + ax * 4, pos + ax * r.axis_stride);
+        }
+      }
+    }
+    cp_async_commit();
+    ld.next(g, step, step_block, step_slice);
+    ld_stage = ld_stage + 1 == STAGES ? 0 : ld_stage + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) load();
+  for (Walk w(g); w.item < g.count; w.next(g, step, step_block, step_slice)) {
+    __syncwarp();  // the stage of the item before this one has been read
+    load();
+    cp_async_wait<STAGES - 1>();
+    if (!QUAD) __syncwarp();  // the positions that other lanes copied
+    const uint8_t* const st = mine + stage * STAGE_BYTES;
+    Turn turn;
+    if constexpr (QUAD) {  // a lane past the last token turns by whatever its stage holds, and stores nothing
+      const int2 pos = *reinterpret_cast<const int2*>(st + OFF_POS + l.lane * 8);
+      uint64_t c, s;
+      two_turns(p0, p1, pos.x, pos.y, r.inverse != 0, &c, &s);
+      turn.gather(c, s, l.lane - l.hl * L::UNITS, L::UNITS);
+    } else {
+#pragma unroll
+      for (int j = 0; rotated && j < 4; ++j) {
+        const int* const pos = reinterpret_cast<const int*>(st + OFF_POS + l.tok * 32);
+        const PairTurn a = pair(2 * j), b = pair(2 * j + 1);
+        two_turns(a, b, pos[a.axis & 7], pos[b.axis & 7], r.inverse != 0, &turn.c[j], &turn.s[j]);
+        turn.n[j] = turn.s[j] ^ 0x8000000080000000ull;
+      }
+    }
+    const int t = w.block * L::TOKS + l.tok;
+    if (t < tokens)
+      finish(t, w.slice * L::STEP * g.per + l.hl, reinterpret_cast<const uint4*>(st) + l.lane,
+             *reinterpret_cast<const long long*>(st + OFF_SLOT + l.lane * 8), turn);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+  }
+}
 
 }  // namespace
 
-template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_rope_kernel(const RopeLaunch a, const Items items) {
-  constexpr int UNITS = D / 16;
-  constexpr int FLY = sizeof(T) == 2 ? HEADS : HEADS / 2;  // heads loaded together
+template <typename T, int D, bool INTER, bool QUAD>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_rope_kernel(const RopeLaunch a, const Tiling g,
+                                                                            const FastDiv by_n) {
+  constexpr int PER = PIECE_SLOTS / Unit<T>::PIECES, STEP = Lane<D, QUAD>::STEP;
   __shared__ PairTurn pairs[D / 2];
   griddep_wait();
   load_rotation<D>(a.r, pairs, a.err);
   __syncthreads();
-  const int u = threadIdx.x % UNITS;
-  int e0, e1;
-  const bool rotated = unit_offsets<INTER>(a.r.rot, u, &e0, &e1);
-  Turn r;
-  bool known = false;  // r belongs to the item's tokens
-  const long long last = items.count * (blockIdx.x + 1) / gridDim.x;
-  long long item = items.count * blockIdx.x / gridDim.x, block = item / items.slices;
-  int slice = static_cast<int>(item - block * items.slices);
-  for (; item < last; ++item, ++slice) {
-    if (slice == items.slices) {
-      slice = 0;
-      ++block;
-      known = false;
-    }
-    const long long t = block * (ROPE_THREADS / UNITS) + threadIdx.x / UNITS;
-    if (t >= static_cast<long long>(a.B) * a.N) continue;
-    const long long b = t / a.N, n = t - b * a.N;
-    const int h0 = slice * items.per, h1 = min(h0 + items.per, a.H + a.Hkv);
-    const T* const q = static_cast<const T*>(a.q) + b * a.sq.b + n * a.sq.n;
-    const T* const k = static_cast<const T*>(a.k) + b * a.sk.b + n * a.sk.n;
-    T* const qo = static_cast<T*>(a.q_out) + b * a.sqo.b + n * a.sqo.n;
-    T* const ko = static_cast<T*>(a.k_out) + b * a.sko.b + n * a.sko.n;
-    for (int h = h0; h < h1; h += FLY) {
-      Unit<T> x[FLY];
+  const int tokens = a.B * a.N, heads = a.H + a.Hkv;
+  int e0, es;
+  const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, QUAD>().u, &e0, &es);
+  run_items<T, D, INTER, QUAD>(
+      g, a.r, pairs, rotated, tokens,
+      [&](int t, int h0, uint32_t dst, uint32_t) {
+        const int b = by_n.div(t), n = t - b * a.N;
+        const T* const q = static_cast<const T*>(a.q) + b * a.sq.b + n * a.sq.n;
+        const T* const k = static_cast<const T*>(a.k) + b * a.sk.b + n * a.sk.n;
 #pragma unroll
-      for (int i = 0; i < FLY; ++i)
-        if (h + i < h1) x[i].load(h + i < a.H ? q + (h + i) * a.sq.h : k + (h + i - a.H) * a.sk.h, e0, e1);
-      if (!known && rotated)
-        r.set(pairs + 8 * u, a.r.pos + b * a.r.batch_stride + n, a.r.axis_stride, a.r.inverse != 0);
-      known = true;
-#pragma unroll
-      for (int i = 0; i < FLY; ++i)
-        if (h + i < h1) {
-          if (rotated) x[i].template turn<INTER>(r);
-          x[i].store(h + i < a.H ? qo + (h + i) * a.sqo.h : ko + (h + i - a.H) * a.sko.h, e0, e1);
+        for (int i = 0; i < PER; ++i) {
+          const int h = h0 + STEP * i;
+          if (i < g.per && h < heads)
+            Unit<T>::fetch(dst + i * Unit<T>::PIECES * 512, h < a.H ? q + h * a.sq.h : k + (h - a.H) * a.sk.h, e0, es);
         }
-    }
-  }
+        return a.r.pos + (a.r.batch_stride ? t : n);
+      },
+      [&](int t, int h0, const uint4* src, long long, const Turn& turn) {
+        const int b = by_n.div(t), n = t - b * a.N;
+        T* const qo = static_cast<T*>(a.q_out) + b * a.sqo.b + n * a.sqo.n;
+        T* const ko = static_cast<T*>(a.k_out) + b * a.sko.b + n * a.sko.n;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int h = h0 + STEP * i;
+          if (i < g.per && h < heads) {
+            Unit<T> x;
+            x.load(src + i * Unit<T>::PIECES * 32);
+            if (rotated) x.template turn<INTER>(turn);
+            x.store(h < a.H ? qo + h * a.sqo.h : ko + (h - a.H) * a.sko.h, e0, es);
+          }
+        }
+      });
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_paged_append_kernel(const AppendLaunch a, const Items items) {
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_paged_append_kernel(const AppendLaunch a, const Tiling g,
+                                                                                    const FastDiv by_page) {
   using T = __nv_bfloat16;
-  constexpr int UNITS = D / 16;
-  constexpr int FLY = HEADS;
+  constexpr int PER = PIECE_SLOTS / Unit<T>::PIECES, STEP = Lane<D, true>::STEP;
   __shared__ PairTurn pairs[D / 2];
   griddep_wait();
   load_rotation<D>(a.r, pairs, a.err);
   __syncthreads();
-  const int u = threadIdx.x % UNITS;
-  int e0, e1;
-  const bool rotated = unit_offsets<INTER>(a.r.rot, u, &e0, &e1);
-  const int hk = a.H, hv = a.H + a.Hkv;  // first key and first value head of the list of heads
-  Turn r;
-  bool known = false, store = false;  // r, store and row belong to the item's tokens
-  long long row = 0;
-  const long long last = items.count * (blockIdx.x + 1) / gridDim.x;
-  long long item = items.count * blockIdx.x / gridDim.x, block = item / items.slices;
-  int slice = static_cast<int>(item - block * items.slices);
-  for (; item < last; ++item, ++slice) {
-    if (slice == items.slices) {
-      slice = 0;
-      ++block;
-      known = false;
-    }
-    const long long t = block * (ROPE_THREADS / UNITS) + threadIdx.x / UNITS;
-    if (t >= a.T) continue;
-    if (!known) {
-      const long long slot = a.slots[t];
-      if (slot >= a.n_slots) record_bad_index(a.err, W_SLOT);
-      store = slot >= 0 && slot < a.n_slots;
-      const long long page = store ? slot / a.page_size : 0;
-      row = store ? page * a.c_page + (slot - page * a.page_size) * a.c_row : 0;
-    }
-    const int h0 = slice * items.per, h1 = min(h0 + items.per, a.H + 2 * a.Hkv);
-    const T* const q = static_cast<const T*>(a.q) + t * a.q_tok;
-    const T* const k = static_cast<const T*>(a.k) + t * a.k_tok;
-    const T* const v = static_cast<const T*>(a.v) + t * a.v_tok;
-    T* const qo = static_cast<T*>(a.q_out) + t * a.H * D;
-    T* const ko = static_cast<T*>(a.k_cache) + row;
-    T* const vo = static_cast<T*>(a.v_cache) + row;
-    {
-      const int h = h0;
-      Unit<T> x[FLY];
+  const int hk = a.H, hv = a.H + a.Hkv, heads = a.H + 2 * a.Hkv;  // q, k and v heads in a row
+  int e0, es;
+  const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, true>().u, &e0, &es);
+  run_items<T, D, INTER, true>(
+      g, a.r, pairs, rotated, a.T,
+      [&](int t, int h0, uint32_t dst, uint32_t slot_dst) {
+        const T* const q = static_cast<const T*>(a.q) + t * a.q_tok;
+        const T* const k = static_cast<const T*>(a.k) + t * a.k_tok;
+        const T* const v = static_cast<const T*>(a.v) + t * a.v_tok;
+        cp_async_small<8>(slot_dst, a.slots + t);
 #pragma unroll
-      for (int i = 0; i < FLY; ++i) {
-        const int hh = h + i;
-        if (hh < h1 && (hh < hk || store))
-          x[i].load(hh < hk ? q + hh * a.q_head : hh < hv ? k + (hh - hk) * a.k_head : v + (hh - hv) * a.v_head, e0, e1);
-      }
-      if (!known && rotated) r.set(pairs + 8 * u, a.r.pos + t, a.r.axis_stride, false);
-      known = true;
-#pragma unroll
-      for (int i = 0; i < FLY; ++i) {
-        const int hh = h + i;
-        if (hh < h1 && (hh < hk || store)) {
-          if (rotated && hh < hv) x[i].template turn<INTER>(r);
-          x[i].store(hh < hk ? qo + hh * D : hh < hv ? ko + (hh - hk) * a.c_head : vo + (hh - hv) * a.c_head, e0, e1);
+        for (int i = 0; i < PER; ++i) {  // unused places too: their slots are still on the way
+          const int h = h0 + STEP * i;
+          if (i < g.per && h < heads)
+            Unit<T>::fetch(dst + i * Unit<T>::PIECES * 512,
+                           h < hk ? q + h * a.q_head : h < hv ? k + (h - hk) * a.k_head : v + (h - hv) * a.v_head, e0, es);
         }
-      }
-    }
-  }
+        return a.r.pos + t;
+      },
+      [&](int t, int h0, const uint4* src, long long slot, const Turn& turn) {
+        if (slot >= a.n_slots) record_bad_index(a.err, W_SLOT);
+        const bool store = slot >= 0 && slot < a.n_slots;
+        const long long page = !store                     ? 0
+                               : a.n_slots <= 0x7FFFFFFF ? by_page.div(static_cast<int>(slot))
+                                                         : slot / a.page_size;
+        const long long row = store ? page * a.c_page + (slot - page * a.page_size) * a.c_row : 0;
+        T* const qo = static_cast<T*>(a.q_out) + static_cast<long long>(t) * a.H * D;
+        T* const ko = static_cast<T*>(a.k_cache) + row;
+        T* const vo = static_cast<T*>(a.v_cache) + row;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int h = h0 + STEP * i;
+          if (i < g.per && h < heads && (h < hk || store)) {
+            Unit<T> x;
+            x.load(src + i * Unit<T>::PIECES * 32);
+            if (rotated && h < hv) x.template turn<INTER>(turn);
+            x.store(h < hk ? qo + h * D : h < hv ? ko + (h - hk) * a.c_head : vo + (h - hv) * a.c_head, e0, es);
+          }
+        }
+      });
 }
 
-// Splits `tokens` x `heads` into items: one head a thread while that does not fill the GPU, up to HEADS beyond.
-static cudaError_t plan_items(long long tokens, int d, int heads, int sms, Items* items, unsigned* grid) {
-  const int units = d / 16;
-  const long long resident = static_cast<long long>(sms) * ROPE_BLOCKS;
-  const long long per = tokens * units * heads / (resident * ROPE_THREADS);
-  items->per = per < 1 ? 1 : per > HEADS ? HEADS : static_cast<int>(per);
-  items->slices = (heads + items->per - 1) / items->per;
-  const long long block = ROPE_THREADS / units;
-  items->count = (tokens + block - 1) / block * items->slices;
-  if (items->count < 1) return cudaErrorInvalidValue;
-  *grid = static_cast<unsigned>(items->count < resident ? items->count : resident);
+// Cuts `tokens` x `heads`: as many heads a lane, `most` at most, as leave an item for every warp.
+template <int D, bool QUAD>
+static cudaError_t tile(long long tokens, int heads, int most, int sms, Tiling* g, unsigned* grid) {
+  using L = Lane<D, QUAD>;
+  const int warps = ROPE_THREADS / 32;
+  const long long resident = static_cast<long long>(sms) * ROPE_BLOCKS * warps, blocks = (tokens + L::TOKS - 1) / L::TOKS;
+  long long count = 0;
+  for (int per = most;; per /= 2) {
+    g->per = per;
+    g->slices = (heads + L::STEP * per - 1) / (L::STEP * per);
+    count = blocks * g->slices;
+    if (per == 1 || count >= resident) break;
+  }
+  if (count < 1 || count > 0x7FFFFFFF - STAGES * resident) return cudaErrorInvalidValue;
+  g->count = static_cast<int>(count);
+  *grid = static_cast<unsigned>(((count < resident ? count : resident) + warps - 1) / warps);
   return cudaSuccess;
 }
 
-template <typename T, int D>
-static cudaError_t launch_rope_d(const RopeLaunch& a) {
-  Items items;
+template <auto kernel, typename... Args>
+static cudaError_t launch_items(unsigned grid, cudaStream_t stream, Args... args) {
+  const cudaError_t e = allow_shared_memory<kernel>(ROPE_SMEM);
+  return e != cudaSuccess ? e : launch_dependent(kernel, grid, ROPE_THREADS, ROPE_SMEM, stream, args...);
+}
+
+template <typename T, int D, bool QUAD>
+static cudaError_t launch_rope_q(const RopeLaunch& a) {
+  Tiling g;
   unsigned grid = 0;
-  const cudaError_t e = plan_items(static_cast<long long>(a.B) * a.N, D, a.H + a.Hkv, a.sms, &items, &grid);
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  const cudaError_t e = tile<D, QUAD>(tokens, a.H + a.Hkv, PIECE_SLOTS / Unit<T>::PIECES, a.sms, &g, &grid);
   if (e != cudaSuccess) return e;
-  if (a.r.interleaved)
-    return launch_dependent(fa_rope_kernel<T, D, true>, grid, ROPE_THREADS, 0, a.stream, a, items);
-  return launch_dependent(fa_rope_kernel<T, D, false>, grid, ROPE_THREADS, 0, a.stream, a, items);
+  const FastDiv by_n(static_cast<unsigned>(a.N));
+  return a.r.interleaved ? launch_items<fa_rope_kernel<T, D, true, QUAD>>(grid, a.stream, a, g, by_n)
+                         : launch_items<fa_rope_kernel<T, D, false, QUAD>>(grid, a.stream, a, g, by_n);
+}
+
+template <typename T>
+static cudaError_t launch_rope_t(const RopeLaunch& a) {
+  if (a.H + a.Hkv > 3) return a.d == 64 ? launch_rope_q<T, 64, true>(a) : launch_rope_q<T, 128, true>(a);
+  return a.d == 64 ? launch_rope_q<T, 64, false>(a) : launch_rope_q<T, 128, false>(a);
 }
 
 cudaError_t launch_rope(const RopeLaunch& a) {
-  if (a.bf16) return a.d == 64 ? launch_rope_d<__nv_bfloat16, 64>(a) : launch_rope_d<__nv_bfloat16, 128>(a);
-  return a.d == 64 ? launch_rope_d<float, 64>(a) : launch_rope_d<float, 128>(a);
+  return a.bf16 ? launch_rope_t<__nv_bfloat16>(a) : launch_rope_t<float>(a);
 }
 
 template <int D>
 static cudaError_t launch_append_d(const AppendLaunch& a) {
-  Items items;
+  Tiling g;
   unsigned grid = 0;
-  const cudaError_t e = plan_items(a.T, D, a.H + 2 * a.Hkv, a.sms, &items, &grid);
+  const cudaError_t e = tile<D, true>(a.T, a.H + 2 * a.Hkv, PIECE_SLOTS / Unit<__nv_bfloat16>::PIECES, a.sms, &g, &grid);
   if (e != cudaSuccess) return e;
-  if (a.r.interleaved)
-    return launch_dependent(fa_paged_append_kernel<D, true>, grid, ROPE_THREADS, 0, a.stream, a, items);
-  return launch_dependent(fa_paged_append_kernel<D, false>, grid, ROPE_THREADS, 0, a.stream, a, items);
+  const FastDiv by_page(static_cast<unsigned>(a.page_size));
+  return a.r.interleaved ? launch_items<fa_paged_append_kernel<D, true>>(grid, a.stream, a, g, by_page)
+                         : launch_items<fa_paged_append_kernel<D, false>>(grid, a.stream, a, g, by_page);
 }
 
 cudaError_t launch_append(const AppendLaunch& a) { return a.d == 64 ? launch_append_d<64>(a) : launch_append_d<128>(a); }

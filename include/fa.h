@@ -288,7 +288,7 @@ int fa_decode_splitkv_noalloc(const void* q, const void* k, const void* v, void*
  *   axes          device int32 [rot/2]: axis(i) in 0 .. n_axes - 1, or NULL: axis 0.
  *     A pair whose entry is out of range becomes NaN, and
  *     fa_check_device_error reports FA_ERR_INVALID_ARG.
- *   n_axes 1 .. 8; rot a multiple of 16, 16 <= rot <= d; (H + Hkv) * d < 2^31.
+ *   n_axes 1 .. 8; rot a multiple of 16, 16 <= rot <= d; (H + Hkv) * d < 2^31; B * N < 2^31 - 1024.
  * No workspace.  Returns FA_OK or an fa_status code.
  */
 int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,

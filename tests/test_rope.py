@@ -133,6 +133,25 @@ def test_rope_many_heads_and_tokens(cuda_device):
     _check_rope(q[:, :, idx], k[:, :, idx], qo[:, :, idx], ko[:, :, idx], pos[:, :, at], freqs, axes, False, False, "many")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,Hkv,N,d,rot,inter", [
+    (1, 0, 41_003, 64, 64, False), (2, 0, 21_001, 128, 128, True), (2, 1, 30_001, 64, 32, True), (1, 1, 25_002, 128, 112, False),
+    (4, 0, 33_333, 64, 64, True), (40, 5, 3001, 64, 48, False)], ids=str)
+def test_rope_tokens_in_many_rounds(cuda_device, dtype, H, Hkv, N, d, rot, inter):
+    """Every warp takes several items; few heads and more; outputs in place."""
+    q = _draw((1, H, N, d), 46, cuda_device, DT[dtype])
+    k = _draw((1, Hkv, N, d), 47, cuda_device, DT[dtype]) if Hkv else None
+    freqs, axes_t, axes = _rotation(rot, 8, cuda_device, 48)
+    pos = np.random.default_rng(49).integers(-(1 << 16), 1 << 16, (8, 1, N)).astype(np.int32)
+    qo, ko = q.clone(), None if k is None else k.clone()
+    fa.fa_rope(qo, ko, torch.as_tensor(pos, device=cuda_device), freqs, axes=axes_t, interleaved=inter, q_out=qo, k_out=ko)
+    _ok()
+    at = sorted({0, 1, 7, 8, N - 2, N - 1, *np.random.default_rng(50).integers(0, N, 300).tolist()})
+    idx = torch.as_tensor(at, device=cuda_device)
+    _check_rope(q[:, :, idx], None if k is None else k[:, :, idx], qo[:, :, idx], None if ko is None else ko[:, :, idx],
+                pos[:, :, at], freqs, axes, inter, False, f"rounds {dtype} H{H}/{Hkv} d{d}")
+
+
 def test_rope_bad_axis_is_nan_and_reported(cuda_device):
     q = _draw((1, 2, 5, 64), 51, cuda_device, torch.float32)
     freqs = fa.fa_rope_freqs(64, device=cuda_device)
