@@ -31,6 +31,7 @@ Entry points (same names as the C ABI):
   fa_decode_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None,
                          workspace=None, with_lse=False) -> (o, lse)
   fa_decode_paged_workspace_bytes(B, H, Hkv, d, page_size, prefix_len=0)
+  fa_decode_paged_call_bytes(B, H, Hkv, d, page_size, max_pages, prefix_len=0)
   fa_check_device_error()
 """
 from __future__ import annotations
@@ -108,6 +109,8 @@ def lib() -> ctypes.CDLL:
             L.fa_decode_paged_prefix.restype = i
             L.fa_decode_paged_workspace_bytes.argtypes = [i, i, i, i, i, i]
             L.fa_decode_paged_workspace_bytes.restype = sz
+            L.fa_decode_paged_call_bytes.argtypes = [i, i, i, i, i, i, i]
+            L.fa_decode_paged_call_bytes.restype = sz
             L.fa_check_device_error.argtypes = []
             L.fa_check_device_error.restype = i
             L.fa_status_string.argtypes = [i]
@@ -510,6 +513,11 @@ def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     r = (_binding or _load_binding()).append(k, v, k_cache, v_cache, slots, q, positions, freqs, axes, interleaved,
                                              q_out)
     return _result(r, "fa_paged_append")
+
+
+def fa_decode_paged_call_bytes(B: int, H: int, Hkv: int, d: int, page_size: int, max_pages: int, prefix_len: int = 0) -> int:
+    """What a call with tables of max_pages pages uses of its workspace: all of it, or nothing."""
+    return int(lib().fa_decode_paged_call_bytes(B, H, Hkv, d, int(page_size), int(max_pages), int(prefix_len)))
 
 
 def fa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int, page_size: int, prefix_len: int = 0) -> int:

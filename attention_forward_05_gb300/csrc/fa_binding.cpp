@@ -357,8 +357,8 @@ PyObject* decode(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     void* ws_ptr = ws.ptr();
     size_t ws_bytes = ws ? ws->nbytes() : 0;
     if (!ws) {
-      ws_bytes = fa_decode_paged_workspace_bytes(Bi, Hi, hk, di, psi, static_cast<int>(plen));
-      if (ws_bytes > 0) {  // 0: arguments that the call below refuses
+      ws_bytes = fa_decode_paged_call_bytes(Bi, Hi, hk, di, psi, mp, static_cast<int>(plen));
+      if (ws_bytes > 0) {  // 0: none needed, or arguments that the call below refuses
         own_ws = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
         ws_ptr = own_ws.get();
       }

@@ -172,6 +172,7 @@ struct PagedLaunch {
 // Work split and workspace layout (byte offsets) of a paged decode.
 struct PagedPlan {
   int n_cta = 0;                                      // CTAs that share the sequences' own keys
+  int cl = 0;                                         // or CTAs of each unit; without a prefix those need no workspace
   size_t part_ml = 0, part_o = 0, infos = 0;          // states of units shared by warps (fa_paged.cu)
   // with a shared prefix:
   int n_split = 0, kv_per_split = 0, wide = 0;        // the prefix's key splits; wide: two query tiles per CTA
@@ -180,7 +181,8 @@ struct PagedPlan {
   size_t gather_k = 0, gather_v = 0, gather_pages = 0;
   size_t total = 0;
 };
-PagedPlan paged_plan(int B, int H, int Hkv, int d, int page_size, int prefix_len, int sms);
+// max_pages: of a sequence's table; 0: any.
+PagedPlan paged_plan(int B, int H, int Hkv, int d, int page_size, int max_pages, int prefix_len, int sms);
 cudaError_t launch_decode_paged(const PagedLaunch& a, const PagedPlan& pl);
 
 struct FwdLaunch {

@@ -816,8 +816,28 @@ namespace {
 
 constexpr size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// CTAs of a unit in the form where every unit has a cluster of its own, or 0 for even ranges of tiles.  `tiles`: of the
+// longest sequence that its table can hold; n_cta: CTAs that may run at once.  As many as there is room for, less the
+// places that clusters of this size leave free in each of the GPU's 8 processor clusters (3000 keys in 56 clusters of 8:
+// 16.0 us, of 7: 9.9); behind a prefix, whose CTAs want room too, a power of two and two CTAs a SM (96 units in clusters
+// of 3: 14.0 us, of 2: 11.0).  A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to
+// 4 us) are used up, whatever the real lengths are; behind a prefix, whose states are joined too, at sixteen.  Clusters
+// against ranges, device time at 32 heads on 8 of 128: 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000:
+// 12.1 and 10.2; 16 of 300: 6.1 and 8.9, 1500: 14.4 and 14.1; 48 of 400: 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400:
+// 29.7 and 32.4; behind a prefix 48 of 60: 17.3 and 24.6, 64 of 800: 48 and 56, 256 of 1 to 600: 77.7 and 81.6, 64 of 1 to
+// 1500: 34.1 and 33.6.
+int cluster_size(long long units, long long tiles, int n_cta, int sms, bool prefix) {
+  const long long most = tiles > 2 ? (tiles < 8 ? tiles : 8) : 1;
+  long long cl = 1;
+  if (prefix)
+    while (cl * 2 <= 8 && cl < most && units * cl <= sms) cl *= 2;
+  else
+    while (cl < most && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
+  return tiles <= (prefix ? 16 : 8) * cl && units * cl <= 0x7FFFFFFF ? static_cast<int>(cl) : 0;
+}
+
 template <class C>
-PagedPlan plan_of(int B, int H, int Hkv, int page_size, int prefix_len, int sms) {
+PagedPlan plan_of(int B, int H, int Hkv, int page_size, int max_pages, int prefix_len, int sms) {
   PagedPlan pl;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -826,10 +846,13 @@ PagedPlan plan_of(int B, int H, int Hkv, int page_size, int prefix_len, int sms)
     return here;
   };
   pl.n_cta = sms * C::CTAS;
+  const long long groups = (H / Hkv + C::GR - 1) / C::GR, cap = static_cast<long long>(max_pages) * page_size;
+  if (max_pages > 0)
+    pl.cl = cluster_size(groups * B * Hkv, (cap + C::TILE - 1) / C::TILE, pl.n_cta, sms, prefix_len > 0);
   const size_t slots = static_cast<size_t>(2) * pl.n_cta, heads = static_cast<size_t>(B) * H;
   pl.part_ml = take(slots * C::GR * 8);
   pl.part_o = take(slots * C::GR * C::D * 4);
-  pl.infos = take(static_cast<size_t>(B) * Hkv * ((H / Hkv + C::GR - 1) / C::GR) * 8);
+  pl.infos = take(static_cast<size_t>(B) * Hkv * groups * 8);
   if (prefix_len > 0) {
     const int G = H / Hkv;
     plan_prefix(B, G, Hkv, C::D, page_size, prefix_len, sms, &pl);
@@ -855,26 +878,6 @@ int join_warps(long long units, long long heads, long long tiles, const PagedPla
   const long long share = pl.n_cta / units, parts = (share < tiles ? share : tiles) + 1 + pl.n_split;
   if (parts > 32 && heads <= sms) return 16;
   return parts > 8 || heads <= 8LL * sms ? 4 : 1;
-}
-
-// CTAs of a unit in the form where every unit has a cluster of its own, or 0 for even ranges of tiles.  `tiles`: of the
-// longest sequence that its table can hold; n_cta: CTAs that may run at once.  As many as there is room for, less the
-// places that clusters of this size leave free in each of the GPU's 8 processor clusters (3000 keys in 56 clusters of 8:
-// 16.0 us, of 7: 9.9); behind a prefix, whose CTAs want room too, a power of two and two CTAs a SM (96 units in clusters
-// of 3: 14.0 us, of 2: 11.0).  A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to
-// 4 us) are used up, whatever the real lengths are; behind a prefix, whose states are joined too, at sixteen.  Clusters
-// against ranges, device time at 32 heads on 8 of 128: 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000:
-// 12.1 and 10.2; 16 of 300: 6.1 and 8.9, 1500: 14.4 and 14.1; 48 of 400: 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400:
-// 29.7 and 32.4; behind a prefix 48 of 60: 17.3 and 24.6, 64 of 800: 48 and 56, 256 of 1 to 600: 77.7 and 81.6, 64 of 1 to
-// 1500: 34.1 and 33.6.
-int cluster_size(long long units, long long tiles, int n_cta, int sms, bool prefix) {
-  const long long most = tiles > 2 ? (tiles < 8 ? tiles : 8) : 1;
-  long long cl = 1;
-  if (prefix)
-    while (cl * 2 <= 8 && cl < most && units * cl <= sms) cl *= 2;
-  else
-    while (cl < most && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
-  return tiles <= (prefix ? 16 : 8) * cl && units * cl <= 0x7FFFFFFF ? static_cast<int>(cl) : 0;
 }
 
 template <class C>
@@ -909,7 +912,7 @@ cudaError_t launch_paged(const PagedLaunch& a, const PagedPlan& pl) {
   p.part_o = reinterpret_cast<float*>(a.ws + pl.part_o);
   p.infos = reinterpret_cast<int2*>(a.ws + pl.infos);
   const long long units = static_cast<long long>(a.B) * p.U;
-  p.cl = cluster_size(units, (p.cap + C::TILE - 1) / C::TILE, pl.n_cta, a.sms, a.prefix_len > 0);
+  p.cl = pl.cl;
   cudaError_t e = p.cl > 0 ? allow_shared_memory<fa_paged_kernel<C, true>>(C::SMEM)
                            : allow_shared_memory<fa_paged_kernel<C, false>>(C::SMEM);
   if (e != cudaSuccess) return e;
@@ -950,8 +953,9 @@ auto with_config(int G, int d, F&& f) {
 
 }  // namespace
 
-PagedPlan paged_plan(int B, int H, int Hkv, int d, int page_size, int prefix_len, int sms) {
-  return with_config(H / Hkv, d, [&](auto c) { return plan_of<decltype(c)>(B, H, Hkv, page_size, prefix_len, sms); });
+PagedPlan paged_plan(int B, int H, int Hkv, int d, int page_size, int max_pages, int prefix_len, int sms) {
+  return with_config(H / Hkv, d,
+                     [&](auto c) { return plan_of<decltype(c)>(B, H, Hkv, page_size, max_pages, prefix_len, sms); });
 }
 
 cudaError_t launch_decode_paged(const PagedLaunch& a, const PagedPlan& pl) {

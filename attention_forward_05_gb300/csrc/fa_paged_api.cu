@@ -33,6 +33,8 @@ bool good_cache(const long long* c, int num_pages, int Hkv, int page_size) {
   return good_strides(c, 3, 8) && distinct(c, num_pages, Hkv, page_size);
 }
 
+bool needs_workspace(const fa::PagedPlan& plan, int prefix_len) { return plan.cl == 0 || prefix_len > 0; }
+
 // Arguments of a rotation; rot = 0 (no rotation) is the caller's business.
 int check_rotation(const int* positions, const double* freqs, const int* axes, int n_axes, int rot, int interleaved,
                    int d) {
@@ -166,14 +168,19 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
   return e == cudaSuccess ? FA_OK : fa::report_cuda_error(e);
 }
 
-size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int page_size, int prefix_len) {
-  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || page_size < 1 || prefix_len < 0 || prefix_len >= (1 << 30) ||
-      (d != 64 && d != 128) || static_cast<long long>(B) * H > 0x7FFFFFFFLL / d)
+size_t fa_decode_paged_call_bytes(int B, int H, int Hkv, int d, int page_size, int max_pages, int prefix_len) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || page_size < 1 || max_pages < 0 || prefix_len < 0 ||
+      prefix_len >= (1 << 30) || (d != 64 && d != 128) || static_cast<long long>(B) * H > 0x7FFFFFFFLL / d)
     return 0;
   int* err = nullptr;
   int sms = 0;
   if (fa::current_device_info(&err, &sms) != FA_OK) return 0;
-  return fa::paged_plan(B, H, Hkv, d, page_size, prefix_len, sms).total;
+  const fa::PagedPlan plan = fa::paged_plan(B, H, Hkv, d, page_size, max_pages, prefix_len, sms);
+  return needs_workspace(plan, prefix_len) ? plan.total : 0;
+}
+
+size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int page_size, int prefix_len) {
+  return fa_decode_paged_call_bytes(B, H, Hkv, d, page_size, 0, prefix_len);
 }
 
 int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cache, void* o, const int* prefix_pages,
@@ -204,11 +211,12 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   fa::PagedLaunch a;
   const int rc = fa::current_device_info(&a.err, &a.sms);
   if (rc != FA_OK) return rc;
-  const fa::PagedPlan plan = fa::paged_plan(B, H, Hkv, d, page_size, prefix_len, a.sms);
+  const fa::PagedPlan plan = fa::paged_plan(B, H, Hkv, d, page_size, max_pages, prefix_len, a.sms);
   if (workspace && workspace_bytes < plan.total) return FA_ERR_INVALID_ARG;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   void* ws = workspace;
-  if (ws == nullptr) {
+  const bool own_ws = ws == nullptr && needs_workspace(plan, prefix_len);
+  if (own_ws) {
     const cudaError_t ea = cudaMallocAsync(&ws, plan.total, a.stream);
     if (ea != cudaSuccess) return fa::report_cuda_error(ea);
   }
@@ -235,7 +243,7 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
   a.prefix_len = prefix_len;
   a.c = c2;
   cudaError_t e = fa::launch_decode_paged(a, plan);
-  if (workspace == nullptr) {
+  if (own_ws) {
     const cudaError_t e2 = cudaFreeAsync(ws, a.stream);
     if (e == cudaSuccess) e = e2;
   }

@@ -385,6 +385,10 @@ int fa_decode_paged_prefix(const void* q, const void* k_cache, const void* v_cac
  * device; 0 on bad arguments or without an sm_103 GPU. */
 size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int page_size, int prefix_len);
 
+/* Bytes of workspace that a call with tables of max_pages pages uses: those, or 0 where it uses none (no prefix and
+ * tables of a few thousand keys at most), so that its workspace can be NULL without an allocation. */
+size_t fa_decode_paged_call_bytes(int B, int H, int Hkv, int d, int page_size, int max_pages, int prefix_len);
+
 /*
  * fa_check_device_error -- reads and clears the library's device error word
  * on the current device (synchronises that device).  Returns FA_OK, or

@@ -263,6 +263,34 @@ def test_workspace_that_is_too_small_is_refused(cuda_device, table_room):
         _ok()
 
 
+def test_short_tables_need_no_workspace(cuda_device):
+    """fa_decode_paged_call_bytes: nothing for short tables, the whole workspace for long ones and behind a prefix; the C
+    entry point takes a NULL workspace either way, also while a stream is being captured."""
+    whole = fa.fa_decode_paged_workspace_bytes(3, 8, 2, 64, 16)
+    assert whole > 0 and fa.fa_decode_paged_call_bytes(3, 8, 2, 64, 16, 0) == whole
+    assert fa.fa_decode_paged_call_bytes(3, 8, 2, 64, 16, 8) == 0
+    assert fa.fa_decode_paged_call_bytes(3, 8, 2, 64, 16, 4000) == whole
+    behind = fa.fa_decode_paged_workspace_bytes(3, 8, 2, 64, 16, 100)
+    assert fa.fa_decode_paged_call_bytes(3, 8, 2, 64, 16, 8, 100) == behind > whole
+    c = _case(cuda_device, [90, 0, 33], 8, 2, 64, 16, 2170)
+    want, want_l = _run(c)
+    o, lse = torch.empty_like(want), torch.empty_like(want_l)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        st = fa.lib().fa_decode_paged(c["q"].data_ptr(), c["kc"].data_ptr(), c["vc"].data_ptr(), o.data_ptr(),
+                                      c["table"].data_ptr(), c["table"].shape[1], c["lens_t"].data_ptr(), 3, 8, 2, 64,
+                                      c["kc"].shape[0], 16, c["table"].shape[1], None, 0.125, None, 0, lse.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream)
+    assert st == fa.FA_OK
+    for _ in range(2):
+        o.fill_(math.nan)
+        g.replay()
+        assert torch.equal(o, want) and torch.equal(lse, want_l)
+    _ok()
+
+
 def test_side_stream_and_threads(cuda_device, table_room):
     """Calls on side streams, also from two host threads at once, give the results of the default stream."""
     import threading

@@ -106,6 +106,8 @@ def test_workspace_bytes_of_bad_arguments():
     for bad in ((0, 8, 2, 64, 16, 0), (2, 8, 3, 64, 16, 0), (2, 8, 2, 96, 16, 0), (2, 8, 2, 64, 16, -1), (2, 8, 0, 64, 16, 0),
                 (2, 8, 2, 64, 0, 5)):
         assert fa.fa_decode_paged_workspace_bytes(*bad) == 0
+        assert fa.fa_decode_paged_call_bytes(*bad[:5], 4, *bad[5:]) == 0
+    assert fa.fa_decode_paged_call_bytes(2, 8, 2, 64, 16, -1) == 0
 
 
 def test_binding_refuses_cpu_tensors():
