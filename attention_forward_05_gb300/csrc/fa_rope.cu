@@ -18,18 +18,17 @@
 //
 // Work split.  A lane owns a unit of a head, eight pairs, in pieces of 16 bytes that lie next to its neighbours' pieces.  A
 // warp's items are a few tokens with up to 16 heads each; their bytes arrive by asynchronous copies in a ring of the
-// warp's own, two items ahead, with the positions (and slots) they need, so nothing waits for a load and no warp
+// warp's own, an item ahead, with the positions (and slots) they need, so nothing waits for a load and no warp
 // waits for another.  Four lanes hold the same unit of four heads and form two of its pairs' sines and cosines each.
 // Consecutive items go to consecutive warps, so the whole GPU reads and writes in few places of device memory.
 //
 // Both kernels are bound by device memory (each element is read once and written once) as long as the instructions
 // are few: the products go in packed fp32 pairs.  Measured, bytes read and written over the time with the launch (about
-// 3 us): q and k of 4 x 4096 tokens, 32 heads of 64, bf16: 24.0 us, 5.6 TB/s; 2 x 8192 tokens, 20 heads of 128, three
-// axes, adjacent pairs: 29.5 us, 5.7 TB/s; appending 8191 tokens, 48 heads of 128: 36.2 us, 5.6 TB/s; 333 tokens, 20 heads
+// 3 us): q and k of 4 x 4096 tokens, 32 heads of 64, bf16: 23.8 us, 5.6 TB/s; 2 x 8192 tokens, 20 heads of 128, three
+// axes, adjacent pairs: 29 us, 5.8 TB/s; appending 8191 tokens, 48 heads of 128: 35.7 us, 5.6 TB/s; 333 tokens, 20 heads
 // of 64, fp32: 2.7 us.  With register loads of the current item, each block on one contiguous range: 26.3, 31.1, 36.3
 // and 3.2 us; with adjacent pairs' 32 bytes a lane in two half-sector copies instead of pieces: 32.0 and 37.6 us for the
-// second and third.  (Past 300 MB at d = 128 lanes that form all eight pairs of their own token, as for few heads below,
-// are up to 10 % faster: 54 against 60 us on 336 MB; below that up to 25 % slower.)
+// second and third.  Two items ahead measured the same or up to 5 % more.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -40,7 +39,7 @@ namespace fa {
 namespace {
 
 constexpr int ROPE_THREADS = 128;
-constexpr int ROPE_BLOCKS = 4;  // per SM
+constexpr int ROPE_BLOCKS = 4;  // per SM, at most
 enum : int { W_AXIS = 0x20, W_SLOT };  // sites recorded with DEV_BAD_INDEX
 
 // F_i: radians per position as a 64-bit fraction of a turn.
@@ -244,7 +243,7 @@ struct Lane {
 };
 
 // A warp's stage of the ring: 8 pieces of data and a slot a lane, and the tokens' positions on up to 8 axes.
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
 constexpr int PIECE_SLOTS = 8;
 constexpr int OFF_POS = PIECE_SLOTS * 512, OFF_SLOT = OFF_POS + 256, STAGE_BYTES = OFF_SLOT + 256;
 constexpr int ROPE_SMEM = ROPE_THREADS / 32 * STAGES * STAGE_BYTES;
@@ -259,8 +258,12 @@ struct Walk {
   __device__ __forceinline__ void next(const Tiling& g, int step, int step_block, int step_slice) {
     item += step;
     block += step_block;
-    slice += step_slice;
-    if (slice >= g.slices) slice -= g.slices, ++block;
+    if (step_slice == 0) {  // all warps move on to the next part, so that none has the short one every time
+      if (++slice == g.slices) slice = 0;
+    } else {
+      slice += step_slice;
+      if (slice >= g.slices) slice -= g.slices, ++block;
+    }
   }
 };
 
@@ -424,16 +427,21 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_paged_append_ker
       });
 }
 
-// Cuts `tokens` x `heads`: as many heads a lane, `most` at most, as leave an item for every warp.
-template <int D, bool QUAD>
-static cudaError_t tile(long long tokens, int heads, int most, int sms, Tiling* g, unsigned* grid) {
+// Cuts `tokens` x `heads`: as many heads a lane, up to what its stage holds, as leave an item for every warp.  Large inputs
+// go faster with fewer blocks a SM, and so fewer places of device memory read and written at a time (bf16, 32 heads of
+// 64, 268 MB read and written: 47.2 us with four, 42.3 with two; 80 of 128, 336 MB: 59.0 and 52.6; 168 MB: 29.6 with four,
+// 28.6 with three, 30.2 with two), small ones with more (17 MB, one head: 7.9, 8.7 and 10.0).
+template <typename T, int D, bool QUAD>
+static cudaError_t tile(long long tokens, int heads, int sms, Tiling* g, unsigned* grid) {
   using L = Lane<D, QUAD>;
-  const int warps = ROPE_THREADS / 32;
-  const long long resident = static_cast<long long>(sms) * ROPE_BLOCKS * warps, blocks = (tokens + L::TOKS - 1) / L::TOKS;
+  const int warps = ROPE_THREADS / 32, most = PIECE_SLOTS / Unit<T>::PIECES;
+  const long long bytes = tokens * heads * D * static_cast<long long>(2 * sizeof(T));
+  const int blocks_sm = bytes < 150000000 ? ROPE_BLOCKS : bytes < 256000000 ? 3 : 2;
+  const long long resident = static_cast<long long>(sms) * blocks_sm * warps, blocks = (tokens + L::TOKS - 1) / L::TOKS;
   long long count = 0;
   for (int per = most;; per /= 2) {
-    g->per = per;
     g->slices = (heads + L::STEP * per - 1) / (L::STEP * per);
+    g->per = (heads + L::STEP * g->slices - 1) / (L::STEP * g->slices);  // parts alike
     count = blocks * g->slices;
     if (per == 1 || count >= resident) break;
   }
@@ -454,7 +462,7 @@ static cudaError_t launch_rope_q(const RopeLaunch& a) {
   Tiling g;
   unsigned grid = 0;
   const long long tokens = static_cast<long long>(a.B) * a.N;
-  const cudaError_t e = tile<D, QUAD>(tokens, a.H + a.Hkv, PIECE_SLOTS / Unit<T>::PIECES, a.sms, &g, &grid);
+  const cudaError_t e = tile<T, D, QUAD>(tokens, a.H + a.Hkv, a.sms, &g, &grid);
   if (e != cudaSuccess) return e;
   const FastDiv by_n(static_cast<unsigned>(a.N));
   return a.r.interleaved ? launch_items<fa_rope_kernel<T, D, true, QUAD>>(grid, a.stream, a, g, by_n)
@@ -475,7 +483,7 @@ template <int D>
 static cudaError_t launch_append_d(const AppendLaunch& a) {
   Tiling g;
   unsigned grid = 0;
-  const cudaError_t e = tile<D, true>(a.T, a.H + 2 * a.Hkv, PIECE_SLOTS / Unit<__nv_bfloat16>::PIECES, a.sms, &g, &grid);
+  const cudaError_t e = tile<__nv_bfloat16, D, true>(a.T, a.H + 2 * a.Hkv, a.sms, &g, &grid);
   if (e != cudaSuccess) return e;
   const FastDiv by_page(static_cast<unsigned>(a.page_size));
   return a.r.interleaved ? launch_items<fa_paged_append_kernel<D, true>>(grid, a.stream, a, g, by_page)

@@ -330,8 +330,9 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
 /*
  * fa_decode_paged -- attention of one bf16 query per head over a paged cache:
  * sequence b sees its seq_lens[b] rows, row i being row i % page_size of page
- * page_table[b][i / page_size].  Lengths stay on the device; the work is spread
- * evenly over the GPU whatever they are.
+ * page_table[b][i / page_size].  Lengths stay on the device; long tables' work is
+ * spread evenly over the GPU whatever they are, and short tables' sequences each
+ * have CTAs of their own (the results may differ in the last bit).
  *
  *   q, o       [B, H, d] bf16 (o is written); query head h reads key/value head
  *              h / (H / Hkv), any group size H / Hkv.
