@@ -263,6 +263,47 @@ def test_workspace_that_is_too_small_is_refused(cuda_device, table_room):
         _ok()
 
 
+@pytest.mark.parametrize("B,H,Hkv,d,ps,prefix_len", [
+    (4, 8, 2, 64, 16, 0), (40, 32, 8, 128, 16, 1000), (64, 16, 4, 64, 24, 300), (3, 16, 2, 128, 5, 700)], ids=str)
+def test_kernels_that_start_early_see_what_was_written(cuda_device, table_room, B, H, Hkv, d, ps, prefix_len):
+    """Append, decode and two rotations in place, each on the one before's output, through one workspace: launched without
+    a pause they give the bits that they give with a synchronisation after every call."""
+    steps = 15
+    tables, prefix, total = ref.deal_pages([200 + steps] * B, ps, 2900, extra=-(-prefix_len // ps))
+    kc0, vc0 = ref.paged_cache(total, Hkv, ps, d, cuda_device, 2901)
+    width = max(len(tables[0]), -(-MIN_TABLE // ps))
+    table, pre = ref.page_table(tables, cuda_device, width, 1 << 28), torch.as_tensor(np.asarray(prefix, np.int32),
+                                                                                    device=cuda_device)
+    start = torch.as_tensor(np.random.default_rng(2902).integers(0, 200, B).astype(np.int32), device=cuda_device)
+    freqs, x0 = fa.fa_rope_freqs(d, device=cuda_device), _q(B, H + 2 * Hkv, d, cuda_device, 2903)
+    ws = torch.empty(fa.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, prefix_len), dtype=torch.uint8, device=cuda_device)
+
+    def run(pause):
+        kc, vc, x, lens, out = kc0.clone(), vc0.clone(), x0, start.clone(), []
+        for _ in range(steps):
+            slot = table.gather(1, (lens // ps).long()[:, None])[:, 0].long() * ps + lens % ps
+            q = fa.fa_paged_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, slot, q=x[:, :H], positions=lens + prefix_len,
+                                   freqs=freqs)
+            pause()
+            lens += 1
+            o, _ = fa.fa_decode_paged_prefix(q, kc, vc, pre, prefix_len, table, lens, workspace=ws)
+            pause()
+            o4, pos = o.view(B, H, 1, d), lens[:, None].contiguous()
+            fa.fa_rope(o4, None, pos, freqs, q_out=o4)
+            pause()
+            fa.fa_rope_bwd(o4, None, pos, freqs, dq_in=o4)
+            pause()
+            x = torch.cat((o * 0.9 + x[:, :H] * 0.1, o[:, :2 * Hkv]), 1)
+            out.append(x)
+        _ok()
+        return torch.stack(out)
+
+    want = run(torch.cuda.synchronize)
+    assert torch.isfinite(want.float()).all()
+    for _ in range(3):
+        assert torch.equal(run(lambda: None), want)
+
+
 def test_short_tables_need_no_workspace(cuda_device):
     """fa_decode_paged_call_bytes: nothing for short tables, the whole workspace for long ones and behind a prefix; the C
     entry point takes a NULL workspace either way, also while a stream is being captured."""
