@@ -11,8 +11,10 @@
 // move a 16-key block.  (With the heads as the 16 rows a tile step took 630 instructions an 8 KB of K and V
 // instead of about 200, and the issue slots, not the bytes, bound short contexts.)  A thread holds two heads'
 // columns, so maxima, sums and rescaling are its own; the running maximum moves only when a score passes it by
-// more than 2^PG_TAU.  P is rounded to bf16 (to nearest: at most 2^-8 relative a term) because the instruction takes both
-// operands in one 16-bit type and V is bf16; the row sums add the unrounded P, in fp32 like everything else.
+// more than 2^PG_TAU.  The instruction takes both operands in one 16-bit type and V is bf16, so P goes in as two bf16
+// terms (two_terms: together within 2^-15 of P), each multiplied with the same fragment of V; with P rounded to bf16
+// alone o was up to 40 % further from the formula than its own rounding is.  The row sums add P itself, in fp32 like
+// everything else.
 //
 // Work split.  A unit is one (sequence, group of query heads); its keys are cut into tiles of TILE (32 KB of K
 // and V).  The tiles of all units, in order, are dealt evenly to the CTAs, one contiguous range each, whatever
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
 #pragma unroll
                 for (int nt = 0; nt < C::NT; ++nt) s[nt][kb][2 * r] = s[nt][kb][2 * r + 1] = -INFINITY;
         }
-        uint32_t pf[C::NT][KW / 16][2];  // P^T rounded to bf16: the B operand of V^T P^T
+        uint32_t pf[C::NT][KW / 16][2], pr[C::NT][KW / 16][2];  // P^T's two terms: B operands of V^T P^T
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
           float mx[2];
@@ -566,8 +568,13 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
             const float p2 = ex2_approx(fmaf(s[nt][kb][2], c, n0)), p3 = ex2_approx(fmaf(s[nt][kb][3], c, n1));
             l[nt][0] += p0 + p2;
             l[nt][1] += p1 + p3;
-            pf[nt][kb][0] = movmatrix_trans(pack_bf16x2(p0, p1));
-            pf[nt][kb][1] = movmatrix_trans(pack_bf16x2(p2, p3));
+            uint32_t h0, h1, r0, r1;
+            two_terms(p0, p1, h0, r0);
+            two_terms(p2, p3, h1, r1);
+            pf[nt][kb][0] = movmatrix_trans(h0);
+            pf[nt][kb][1] = movmatrix_trans(h1);
+            pr[nt][kb][0] = movmatrix_trans(r0);
+            pr[nt][kb][1] = movmatrix_trans(r1);
           }
         }
 #pragma unroll
@@ -577,7 +584,10 @@ __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgP
             uint32_t a[4];
             ldmatrix_x4_trans((vs0 ^ (dp << 5)) + kb * 16 * C::ROW_BYTES, a);
 #pragma unroll
-            for (int nt = 0; nt < C::NT; ++nt) mma_16816(o[nt][dp], a, pf[nt][kb][0], pf[nt][kb][1]);
+            for (int nt = 0; nt < C::NT; ++nt) {
+              mma_16816(o[nt][dp], a, pf[nt][kb][0], pf[nt][kb][1]);
+              mma_16816(o[nt][dp], a, pr[nt][kb][0], pr[nt][kb][1]);
+            }
           }
       }
       __syncwarp();  // every lane has read the stage
