@@ -97,7 +97,13 @@ struct FwdCfg {
   static constexpr int P_COLS = BC * ESZ / 4;  // 32-bit TMEM columns of one P row
   static constexpr int P_COLS_PER_K = MMA_K * ESZ / 4;
   static constexpr int COLS = BC;         // key columns of one softmax thread (one query row)
-  static constexpr int PCOLS_W = P_COLS;  // P columns written by one softmax warpgroup
+  // PAGED: P goes into P V as two bf16 terms (two_terms) instead of rounded once, because the paged decode of the sequences'
+  // own keys, whose states are joined with these, and the split-KV decode lose nothing of P either.  Every 32 columns of S
+  // become 16 columns of first terms and 16 of second ones, so a chunk of S is read before it is written over and P takes no
+  // more room than S.  P V takes two products a step for one: on 16384 keys and 1024 queries a head (d = 128) the
+  // kernel takes 74 us, with P rounded once 56 (ncu).
+  static constexpr bool TWO = PAGED;
+  static constexpr int PCOLS_W = TWO ? BC : P_COLS;  // P columns written by one softmax warpgroup
   static constexpr int OCOLS = D;         // O columns rescaled and stored by one softmax warpgroup
   // PAGED with two query tiles and d = 128: a second load warp takes the values.  Small pages need many small copies,
   // and issuing them (about 45 ns each) for both tiles of a step takes one warp longer than the step's products: with
@@ -118,6 +124,7 @@ struct FwdCfg {
   static_assert(BC % 32 == 0 && BC >= 32 && BC <= 256, "key tile");
   static_assert(COLS % 32 == 0 && PCOLS_W % 32 == 0 && OCOLS % 32 == 0, "whole 32-column chunks");
   static_assert(!PV2 || (!TF32 && BC >= 128 && (BC / 2) % 64 == 0), "P handed over in two halves of whole packed chunks");
+  static_assert(!TWO || (!TF32 && (PV2 || BC == 64)), "the paths below that write two terms");
   static_assert(TMEM_NEED <= 512 / MINB, "tensor memory");
   static_assert(SMEM_BYTES * MINB <= 227 * 1024, "shared memory");
 };
@@ -199,6 +206,37 @@ __device__ __forceinline__ void softmax_p_bf16(const uint32_t (&sr)[NCOL / 32][3
     }
     rs2[qc & 1] = f2_add(rs2[qc & 1], f2_pack(p0, p1));
     pk[qc / 32][qc % 32] = pack_bf16x2(p0, p1);
+  }
+}
+
+// P of 32 columns as two terms (FwdCfg::TWO): pk[0..15] the first ones, packed as above, pk[16..31] the second ones.
+template <bool TAIL>
+__device__ __forceinline__ void softmax_p_two(const uint32_t (&sr)[32], uint32_t (&pk)[32], uint64_t c2, uint64_t negm2,
+                                              int valid, uint64_t (&rs2)[2]) {
+#pragma unroll
+  for (int qc = 0; qc < 16; ++qc) {
+    const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[2 * qc]), __uint_as_float(sr[2 * qc + 1])), c2, negm2);
+    float x0, x1;
+    f2_unpack_f(x, x0, x1);
+    float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    if (TAIL) {
+      if (2 * qc >= valid) p0 = 0.f;
+      if (2 * qc + 1 >= valid) p1 = 0.f;
+    }
+    rs2[qc & 1] = f2_add(rs2[qc & 1], f2_pack(p0, p1));
+    two_terms(p0, p1, pk[qc], pk[16 + qc]);
+  }
+}
+
+// P of NCOL columns for P V: rounded to bf16, or in two terms.
+template <int NCOL, bool TAIL, bool TWO, int NPK>
+__device__ __forceinline__ void softmax_p(const uint32_t (&sr)[NCOL / 32][32], uint32_t (&pk)[NPK][32], uint64_t c2,
+                                          uint64_t negm2, int valid, uint64_t (&rs2)[2]) {
+  if constexpr (TWO) {
+#pragma unroll
+    for (int i = 0; i < NCOL / 32; ++i) softmax_p_two<TAIL>(sr[i], pk[i], c2, negm2, valid - 32 * i, rs2);
+  } else {
+    softmax_p_bf16<NCOL, TAIL>(sr, pk, c2, negm2, valid, rs2);
   }
 }
 
@@ -545,7 +583,13 @@ __global__ void __maxnreg__(C::MAXREG)
           } else {  // [Bc keys][D]: MN-major, 8-key groups 1024 B apart, 64-column segments LBO apart
             ov = (kk * C::MMA_K * 128) >> 4;
           }
-          mma_ts<C::TF32>(d_tmem, a_tmem + kk * C::P_COLS_PER_K, vb + ov, idesc_pv, (acc || kk > 0) ? 1u : 0u);
+          if constexpr (C::TWO) {  // 16 keys' first terms are 8 columns, their second ones the 8 that lie 16 further
+            const uint32_t a = a_tmem + kk / 2 * 32 + kk % 2 * 8;
+            mma_ts<false>(d_tmem, a, vb + ov, idesc_pv, (acc || kk > 0) ? 1u : 0u);
+            mma_ts<false>(d_tmem, a + 16, vb + ov, idesc_pv, 1u);
+          } else {
+            mma_ts<C::TF32>(d_tmem, a_tmem + kk * C::P_COLS_PER_K, vb + ov, idesc_pv, (acc || kk > 0) ? 1u : 0u);
+          }
         }
       };
       auto commit = [&](uint32_t bar) {
@@ -712,7 +756,7 @@ __global__ void __maxnreg__(C::MAXREG)
       bool okw = mbar_wait(bar_sf(t), j & 1, abort_flag, p.err, W_SF);
       okw = __all_sync(0xffffffffu, okw);
       const int valid = row_lim - kb - j * C::BC;  // valid key columns here (may be <= 0)
-      if constexpr (!C::TF32 && C::COLS <= 64) {
+      if constexpr (!C::TF32 && C::COLS <= 64 && (!C::TWO || C::MAXREG >= 128)) {
         // Fast path once every row of the warp has a reference maximum: P is computed against m_ref
         // while the scores are still arriving, 32 columns at a time (the load of the next chunk
         // overlaps the work on this one).  No row maximum is formed: the row sum bounds every P of
@@ -722,7 +766,9 @@ __global__ void __maxnreg__(C::MAXREG)
         // needed.  A tile with masked columns (causal diagonal, ragged last tile) takes the masked
         // copy of the path, whose P is 0 past each row's `valid` columns.
         // Only for 64-column tiles: with 128 columns the extra live registers spill and the
-        // d = 128 kernel measured 25% slower.
+        // d = 128 kernel measured 25% slower.  Nor with P in two terms, which take as many registers as S, where a thread has
+        // 96 (they spill: 256 sequences behind 16384 keys, d = 64, 158 us instead of 68; with 128 registers this path takes 51 us
+        // on 8 sequences behind 65536 keys, d = 128, the general one 60).
         auto fast = [&](auto masked) -> bool {
           constexpr bool TAIL = decltype(masked)::value;
           tc_fence_after();
@@ -737,20 +783,24 @@ __global__ void __maxnreg__(C::MAXREG)
           for (int cc = 0; cc < C::COLS / 32; ++cc) {
             if (cc + 1 < C::COLS / 32) tmem_ld32(tS + (cc + 1) * 32, sc[(cc + 1) & 1]);
             const uint32_t(&cur)[32] = sc[cc & 1];
+            if constexpr (C::TWO) {
+              softmax_p_two<TAIL>(cur, pk[cc], c2, negm2, valid - cc * 32, rs2);
+            } else {
 #pragma unroll
-            for (int qc = 0; qc < 16; ++qc) {
-              const uint64_t x = f2_fma(f2_pack(__uint_as_float(cur[2 * qc]), __uint_as_float(cur[2 * qc + 1])), c2,
-                                        negm2);
-              float x0, x1;
-              f2_unpack_f(x, x0, x1);
-              float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              if constexpr (TAIL) {
-                if (cc * 32 + 2 * qc >= valid) p0 = 0.f;
-                if (cc * 32 + 2 * qc + 1 >= valid) p1 = 0.f;
+              for (int qc = 0; qc < 16; ++qc) {
+                const uint64_t x = f2_fma(f2_pack(__uint_as_float(cur[2 * qc]), __uint_as_float(cur[2 * qc + 1])), c2,
+                                          negm2);
+                float x0, x1;
+                f2_unpack_f(x, x0, x1);
+                float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                if constexpr (TAIL) {
+                  if (cc * 32 + 2 * qc >= valid) p0 = 0.f;
+                  if (cc * 32 + 2 * qc + 1 >= valid) p1 = 0.f;
+                }
+                rs2[qc & 1] = f2_add(rs2[qc & 1], f2_pack(p0, p1));
+                const int w = cc * 16 + qc;  // packed column of this pair
+                pk[w / 32][w % 32] = pack_bf16x2(p0, p1);
               }
-              rs2[qc & 1] = f2_add(rs2[qc & 1], f2_pack(p0, p1));
-              const int w = cc * 16 + qc;  // packed column of this pair
-              pk[w / 32][w % 32] = pack_bf16x2(p0, p1);
             }
             if (cc + 1 < C::COLS / 32) {
               tmem_wait_ld();
@@ -804,11 +854,12 @@ __global__ void __maxnreg__(C::MAXREG)
           auto& sv_a = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sv[0]);
           auto& sv_b = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sv[HC / 32]);
           const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+          constexpr int HP = C::PCOLS_W / 64;  // 32-column chunks of half of P
           uint32_t pk[C::PCOLS_W / 32][32];
-          auto& pk_a = reinterpret_cast<uint32_t(&)[HC / 64][32]>(pk[0]);
-          auto& pk_b = reinterpret_cast<uint32_t(&)[HC / 64][32]>(pk[HC / 64]);
+          auto& pk_a = reinterpret_cast<uint32_t(&)[HP][32]>(pk[0]);
+          auto& pk_b = reinterpret_cast<uint32_t(&)[HP][32]>(pk[HP]);
           uint64_t rs_a[2] = {0ull, 0ull};
-          softmax_p_bf16<HC, false>(sv_a, pk_a, c2, negm2, HC, rs_a);
+          softmax_p<HC, false, C::TWO>(sv_a, pk_a, c2, negm2, HC, rs_a);
           const float m_b = (c >= 0.f ? row_extreme<HC, true>(sv_b) : row_extreme<HC, false>(sv_b)) * c;
           float r0, r1, r2, r3;
           f2_unpack_f(rs_a[0], r0, r1);
@@ -816,15 +867,15 @@ __global__ void __maxnreg__(C::MAXREG)
           const float l_a = (r0 + r1) + (r2 + r3);
           if (__all_sync(0xffffffffu, l_a <= p_lim && m_b <= m_ref + p.tau)) {
 #pragma unroll
-            for (int i = 0; i < HC / 64; ++i) tmem_st32(tP + i * 32, pk_a[i]);
+            for (int i = 0; i < HP; ++i) tmem_st32(tP + i * 32, pk_a[i]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_ph(t));
             uint64_t rs_b[2] = {0ull, 0ull};
-            softmax_p_bf16<HC, false>(sv_b, pk_b, c2, negm2, HC, rs_b);
+            softmax_p<HC, false, C::TWO>(sv_b, pk_b, c2, negm2, HC, rs_b);
 #pragma unroll
-            for (int i = 0; i < HC / 64; ++i) tmem_st32(tP + (HC / 64 + i) * 32, pk_b[i]);
+            for (int i = 0; i < HP; ++i) tmem_st32(tP + (HP + i) * 32, pk_b[i]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -902,15 +953,16 @@ __global__ void __maxnreg__(C::MAXREG)
         // First half of P, then the O correction (P V of this step accumulates into the corrected
         // O), then the signal for the first half of P V; the second half of P follows.
         constexpr int HC = C::COLS / 2;
+        constexpr int HP = C::PCOLS_W / 64;
         uint32_t pk[C::PCOLS_W / 32][32];
         auto& sr_a = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[0]);
         auto& sr_b = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[HC / 32]);
-        auto& pk_a = reinterpret_cast<uint32_t(&)[HC / 64][32]>(pk[0]);
-        auto& pk_b = reinterpret_cast<uint32_t(&)[HC / 64][32]>(pk[HC / 64]);
-        if (valid >= HC) softmax_p_bf16<HC, false>(sr_a, pk_a, c2, negm2, valid, rs2);
-        else softmax_p_bf16<HC, true>(sr_a, pk_a, c2, negm2, valid, rs2);
+        auto& pk_a = reinterpret_cast<uint32_t(&)[HP][32]>(pk[0]);
+        auto& pk_b = reinterpret_cast<uint32_t(&)[HP][32]>(pk[HP]);
+        if (valid >= HC) softmax_p<HC, false, C::TWO>(sr_a, pk_a, c2, negm2, valid, rs2);
+        else softmax_p<HC, true, C::TWO>(sr_a, pk_a, c2, negm2, valid, rs2);
 #pragma unroll
-        for (int i = 0; i < HC / 64; ++i) tmem_st32(tP + i * 32, pk_a[i]);
+        for (int i = 0; i < HP; ++i) tmem_st32(tP + i * 32, pk_a[i]);
         if (j > 0 && __any_sync(0xffffffffu, need)) {
           const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll
@@ -931,10 +983,10 @@ __global__ void __maxnreg__(C::MAXREG)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_ph(t));
-        if (valid >= C::COLS) softmax_p_bf16<HC, false>(sr_b, pk_b, c2, negm2, valid - HC, rs2);
-        else softmax_p_bf16<HC, true>(sr_b, pk_b, c2, negm2, valid - HC, rs2);
+        if (valid >= C::COLS) softmax_p<HC, false, C::TWO>(sr_b, pk_b, c2, negm2, valid - HC, rs2);
+        else softmax_p<HC, true, C::TWO>(sr_b, pk_b, c2, negm2, valid - HC, rs2);
 #pragma unroll
-        for (int i = 0; i < HC / 64; ++i) tmem_st32(tP + (HC / 64 + i) * 32, pk_b[i]);
+        for (int i = 0; i < HP; ++i) tmem_st32(tP + (HP + i) * 32, pk_b[i]);
       } else if constexpr (CHUNKED) {
         // chunk cc's 16 packed P columns go over S columns 16cc .. 16cc+15, which hold chunk 0 (already read)
 #pragma unroll
@@ -944,6 +996,12 @@ __global__ void __maxnreg__(C::MAXREG)
           reg_fence(sr[0]);
           const int vc = valid - cc * 32;
           uint32_t pk[32];
+          if constexpr (C::TWO) {  // over the chunk's own columns
+            if (vc >= 32) softmax_p_two<false>(sr[0], pk, c2, negm2, vc, rs2);
+            else softmax_p_two<true>(sr[0], pk, c2, negm2, vc, rs2);
+            tmem_st32(tP + cc * 32, pk);
+            continue;
+          }
 #pragma unroll
           for (int qc = 0; qc < 16; ++qc) {
             const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[0][2 * qc]), __uint_as_float(sr[0][2 * qc + 1])), c2,

@@ -407,20 +407,17 @@ __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w <
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Numbers a, b >= 0 as two bf16 terms each (packed as by pack_bf16x2): hi cut off after eight bits, lo the nearest bf16 to what
-// that left, so that hi + lo is within 2^-15 of the number (hi leaves less than 2^-7 of it, lo is off by 2^-8 of that).  lo is
-// kept above 2^-20 of the number: neither term of a number above 2^-106 is zero or negative, and either one times an
-// infinity is that infinity.
+// that left plus 2^-20 hi, so that hi + lo is within 2^-15 of the number (hi leaves less than 2^-7 of it, lo is off by 2^-8 of
+// that).  Without the 2^-20 hi a term could be zero; with it, either term of a number above 2^-106, times an infinity, is
+// that infinity.
 __device__ __forceinline__ void two_terms(float a, float b, uint32_t& hi, uint32_t& lo) {
   const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
   hi = __byte_perm(ua, ub, 0x7632);
-  const uint64_t x = f2_pack(a, b);
-  const uint64_t rest = f2_add(x, f2_pack(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
-                                          __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)));
-  const uint64_t least = f2_mul(x, f2_pack(0x1p-20f, 0x1p-20f));
-  float ra, rb, la, lb;
-  f2_unpack_f(rest, ra, rb);
-  f2_unpack_f(least, la, lb);
-  lo = pack_bf16x2(fmaxf(ra, la), fmaxf(rb, lb));
+  const uint64_t h = f2_pack(__uint_as_float(ua & 0xFFFF0000u), __uint_as_float(ub & 0xFFFF0000u));
+  const uint64_t c = f2_pack(0x1p-20f - 1.f, 0x1p-20f - 1.f);
+  float ra, rb;
+  f2_unpack_f(f2_fma(h, c, f2_pack(a, b)), ra, rb);
+  lo = pack_bf16x2(ra, rb);
 }
 
 }  // namespace fa

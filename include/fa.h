@@ -350,8 +350,7 @@ int fa_paged_append(const void* k, const void* v, const void* q, void* q_out, vo
  * A sequence with a page outside the cache or more keys than max_pages * page_size
  * gets NaN in o and lse, and fa_check_device_error reports FA_ERR_INVALID_ARG; the
  * others are not affected.  Accumulation and softmax statistics are fp32; P goes into
- * P V as two bf16 terms, together within 2^-15 of it (over a shared prefix, below,
- * rounded to bf16).  No atomics: repeated calls on one GPU give identical
+ * P V as two bf16 terms, together within 2^-15 of it.  No atomics: repeated calls on one GPU give identical
  * bits.  max_pages * page_size < 2^30, B * H * d < 2^31, and B * H *
  * (max_pages * page_size / 64 + 3) <= 2^39 (FA_ERR_INVALID_ARG otherwise).  Returns
  * FA_OK or an fa_status code.

@@ -70,6 +70,14 @@ def test_paged_decode_keeps_p(cuda_device, room, d, H, Hkv):
 
 @pytest.mark.parametrize("room", [0, 40_000], ids=["clusters", "ranges"])
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,ps,prefix_len", [(3, 16, 5), (3, 5, 150), (70, 16, 333), (70, 64, 1024), (70, 24, 128)], ids=str)
+def test_shared_prefix_keeps_p(cuda_device, room, d, B, ps, prefix_len):
+    """Both widths of the prefix's query tiles (B * 4 rows a head), whole and ragged tiles, gathered pages, several splits."""
+    _check(cuda_device, [b % 7 for b in range(B)], 8, 2, d, ps, room, 4100 + d + B, prefix_len)
+
+
+@pytest.mark.parametrize("room", [0, 40_000], ids=["clusters", "ranges"])
+@pytest.mark.parametrize("d", [64, 128])
 def test_infinite_values_stay_infinite(cuda_device, room, d):
     """An infinite value that a row sees gives that infinity in its dimension, as the formula does, in the key of largest P
     (P = 1: a term of it that were zero would give NaN) as in the others; the other dimensions are as they were."""
