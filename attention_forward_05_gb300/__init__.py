@@ -437,10 +437,10 @@ _binding = None
 def _load_binding():
     """The compiled part of the binding (built first if stale).  Raises if it cannot be built or loaded."""
     global _binding
-    lib()  # builds both, and loads the library that the binding links
+    lib()  # the library that the binding links
     with _lock:
         if _binding is None:
-            spec = importlib.util.spec_from_file_location("_fa_binding", _build.BINDING)
+            spec = importlib.util.spec_from_file_location("_fa_binding", _build.build_binding())
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             _binding = module

@@ -1,15 +1,20 @@
 """Builds libfa.so in-tree with nvcc for sm_103a (no CMake, no torch extension machinery), and the
-Python binding's compiled part, _fa_binding.so, with g++ against the installed PyTorch's headers.
+Python binding's compiled part with g++ against the installed PyTorch's headers.
 
 The translation units compile in parallel; libfa.so links the CUDA runtime
-statically, so it depends only on the driver.  The binding links libfa.so and
-PyTorch.
+statically, so it depends only on the driver, and nvcc with its host compiler is
+all it takes to build.
+The binding links libfa.so and PyTorch, whose internal C++ interfaces it uses:
+its file's name carries the Python ABI and the PyTorch version it was built
+for, so another one of either builds its own.
 """
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libfa.so")
-BINDING = os.path.join(OUT, "_fa_binding.so")
 BINDING_SRC = os.path.join(CSRC, "fa_binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd_bf16.cu", "fa_fwd_fp32.cu", "fa_fwd_merge.cu", "fa_decode.cu",
            "fa_decode_noalloc.cu", "fa_bwd.cu", "fa_bwd_fp32.cu",
@@ -32,23 +36,35 @@ def _nvcc() -> str:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
+    """Sources of libfa.so."""
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "fa.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
+def _older(target: str, files: list[str]) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in files)
+
+
 def is_stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return _older(LIB, _deps())
+
+
+def binding_path() -> str:
+    """The binding for the running Python and its PyTorch."""
+    import torch
+
+    version = re.sub(r"[^0-9A-Za-z.]", "_", torch.__version__)
+    return os.path.join(OUT, f"_fa_binding.torch{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def binding_is_stale() -> bool:
+    return _older(binding_path(), [BINDING_SRC, os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)])
 
 
 def _torch_flags() -> tuple[list[str], list[str]]:
     """g++ compile and link flags for an extension of the installed Python and PyTorch."""
-    import sysconfig
-
     import torch
 
     root = os.path.dirname(torch.__file__)
@@ -62,7 +78,7 @@ def _torch_flags() -> tuple[list[str], list[str]]:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale or forced) libfa.so and the binding; returns the path of libfa.so.
+    """Compile libfa.so if it is stale or forced; returns its path.
 
     FA_PTXAS_VERBOSE=1 in the environment adds ``-Xptxas -v`` and keeps its
     register / spill report in _build/ptxas.log.
@@ -83,23 +99,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    torch_cflags, torch_ldflags = _torch_flags()
-    binding_obj = os.path.join(OUT, "fa_binding.o")
-
-    def compile_binding():
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *torch_cflags, "-c", BINDING_SRC, "-o", binding_obj]
-        return "fa_binding.cpp", binding_obj, subprocess.run(cmd, capture_output=True, text=True)
-
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(compile_binding)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        bound = binding.result()
     log = []
-    for src, _, r in [*results, bound]:
+    for src, _, r in results:
         log.append(f"== {src}\n{r.stdout}{r.stderr}")
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError(f"compiling {src} failed")
+            raise RuntimeError(f"nvcc failed on {src}")
     if ptxas_v or verbose:
         with open(os.path.join(OUT, "ptxas.log"), "w") as f:
             f.write("\n".join(log))
@@ -110,15 +117,51 @@ def build(force: bool = False, verbose: bool = False) -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, binding_obj, f"-L{OUT}", "-l:libfa.so", "-Wl,-rpath,$ORIGIN", *torch_ldflags]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    return LIB
+
+
+def _compile_binding() -> str:
+    """The binding's object file.  Raises if it does not compile."""
+    os.makedirs(OUT, exist_ok=True)
+    obj = binding_path() + f".{os.getpid()}.o"
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", *_torch_flags()[0], "-c", BINDING_SRC, "-o", obj],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on fa_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> str:
+    path = binding_path()
+    tmp = path + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{OUT}", "-l:libfa.so", "-Wl,-rpath,$ORIGIN", *_torch_flags()[1]],
+                       capture_output=True, text=True)
+    os.remove(obj)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking the binding failed")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, path)
+    return path
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the binding if it is stale or forced; returns its path.  libfa.so must be there (build)."""
+    if not force and not binding_is_stale():
+        return binding_path()
+    return _link_binding(_compile_binding())
+
+
+def build_all(force: bool = False, verbose: bool = False) -> str:
+    """libfa.so and the binding, compiled side by side; returns the path of libfa.so, which is there although the
+    binding may have failed (then this raises)."""
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_binding) if force or binding_is_stale() else None
+        build(force, verbose)
+        if obj is not None:
+            _link_binding(obj.result())
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True))
+    print(build_all(force="--force" in sys.argv, verbose=True))
