@@ -477,7 +477,7 @@ def fa_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fr
     positions: int32 [N], [B, N], or with several axes [axes, B, N] / [axes, 1, N].  freqs: float64 [rot/2], radians
     per position (fa_rope_freqs); the first rot elements of a head are rotated.  axes: int32 [rot/2], the position
     axis of each pair.  q and k may be strided views (heads of a projection's output); new outputs are contiguous.
-    An output may be its input itself; otherwise it must overlap no input.
+    An output may be its input itself; otherwise it must overlap no input.  B = 0 or N = 0 gives empty outputs.
     """
     if stream is not None:
         with _on_stream(stream, q, k, positions, freqs, axes, q_out, k_out):
@@ -542,7 +542,7 @@ def fa_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
     q: bf16 [B, H, d].  k_cache, v_cache as in fa_paged_append.  page_table: int32 [B, max_pages]; sequence b sees its
     first seq_lens[b] (int32, on the device) rows.  A sequence without keys gets o = 0, lse = -inf; one with a bad
-    page or length gets NaN and makes fa_check_device_error return FA_ERR_INVALID_ARG.
+    page or length gets NaN and makes fa_check_device_error return FA_ERR_INVALID_ARG.  B = 0 gives empty outputs.
     """
     return _decode_paged(q, k_cache, v_cache, None, 0, page_table, seq_lens, scale, workspace, with_lse, o, stream,
                          "fa_decode_paged")

@@ -217,11 +217,13 @@ PyObject* rope(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     const int *const posp = static_cast<const int*>(pos.ptr()), *const axp = static_cast<const int*>(axes.ptr());
     const double* const fp = static_cast<const double*>(freqs.ptr());
     const fa_stream_t stream = stream_of(dev);
-    int st;
-    Py_BEGIN_ALLOW_THREADS;
-    st = fa_rope(qp, kp, qop, kop, strides, Bi, H, Hkv, Ni, d, type == at::kFloat ? FA_FP32 : FA_BF16, posp, shared, fp,
-                 axp, ax, rot, inter, inverse, stream);
-    Py_END_ALLOW_THREADS;
+    int st = FA_OK;
+    if (B > 0 && N > 0) {  // an empty tensor has no address; there is nothing to rotate
+      Py_BEGIN_ALLOW_THREADS;
+      st = fa_rope(qp, kp, qop, kop, strides, Bi, H, Hkv, Ni, d, type == at::kFloat ? FA_FP32 : FA_BF16, posp, shared, fp,
+                   axp, ax, rot, inter, inverse, stream);
+      Py_END_ALLOW_THREADS;
+    }
     if (st != FA_OK) return PyLong_FromLong(st);
     PyObject* a = q_new.defined() ? THPVariable_Wrap(std::move(q_new)) : Py_NewRef(in[6]);
     PyObject* b = k_new.defined() ? THPVariable_Wrap(std::move(k_new)) : Py_NewRef(in[7]);
@@ -356,7 +358,7 @@ PyObject* decode(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     c10::DataPtr own_ws;
     void* ws_ptr = ws.ptr();
     size_t ws_bytes = ws ? ws->nbytes() : 0;
-    if (!ws) {
+    if (!ws && B > 0) {
       ws_bytes = fa_decode_paged_call_bytes(Bi, Hi, hk, di, psi, mp, static_cast<int>(plen));
       if (ws_bytes > 0) {  // 0: none needed, or arguments that the call below refuses
         own_ws = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
@@ -369,11 +371,13 @@ PyObject* decode(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     const int *const tp = static_cast<const int*>(table.ptr()), *const lp = static_cast<const int*>(lens.ptr());
     float* const lsep = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
     const fa_stream_t stream = stream_of(dev);
-    int st;
-    Py_BEGIN_ALLOW_THREADS;
-    st = fa_decode_paged_prefix(qp, kcp, vcp, op, prep, static_cast<int>(plen), tp, row, lp, Bi, Hi, hk, di, pages, psi, mp,
-                                cs, static_cast<float>(scale), ws_ptr, ws_bytes, lsep, stream);
-    Py_END_ALLOW_THREADS;
+    int st = FA_OK;
+    if (B > 0) {  // a step without sequences: empty results
+      Py_BEGIN_ALLOW_THREADS;
+      st = fa_decode_paged_prefix(qp, kcp, vcp, op, prep, static_cast<int>(plen), tp, row, lp, Bi, Hi, hk, di, pages, psi,
+                                  mp, cs, static_cast<float>(scale), ws_ptr, ws_bytes, lsep, stream);
+      Py_END_ALLOW_THREADS;
+    }
     if (st != FA_OK) return PyLong_FromLong(st);
     PyObject* a = o_new.defined() ? THPVariable_Wrap(std::move(o_new)) : Py_NewRef(in[10]);
     PyObject* b = lse.defined() ? THPVariable_Wrap(std::move(lse)) : Py_NewRef(Py_None);
