@@ -1,5 +1,6 @@
 """The paged decode over wide tables, which are taken by CTAs that share all tiles (ranges) and joined by a second kernel:
-many sequences, batches without a key, captured steps and the C entry points' own workspaces.
+many sequences, batches without a key, captured steps and the C entry points' own workspaces.  And kernels that directly
+follow one another, with nothing between them that would wait: append, decode and decode through one workspace.
 
 Which form a call takes shows in fa_decode_paged_call_bytes: without a prefix, ranges need a workspace, clusters none."""
 import math
@@ -167,3 +168,93 @@ def test_c_abi_allocates_its_workspace(cuda_device, plen):
         g.replay()
         assert torch.equal(o, want) and torch.equal(lse, want_l)
     _ok()
+
+
+# ------------------------------------------------------------------------------------------ nothing in between
+
+def _same_without_pauses(reset, run, out):
+    """run's calls, launched one behind the other and as one graph, give the bits that they give with a synchronisation
+    after every call."""
+    reset()
+    run(torch.cuda.synchronize)
+    _ok()
+    want = out.clone()
+    assert torch.isfinite(want.float()).all()
+    for _ in range(4):
+        reset()
+        torch.cuda.synchronize()
+        run(lambda: None)
+        assert torch.equal(out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(lambda: None)
+    for _ in range(4):
+        reset()
+        g.replay()
+        assert torch.equal(out, want)
+    _ok()
+
+
+SHAPES = [(4, 8, 2, 64, 16, 0), (1, 16, 4, 128, 64, 0), (40, 32, 8, 128, 16, 1000), (64, 16, 4, 64, 24, 300),
+          (3, 16, 2, 128, 5, 700)]
+
+
+@pytest.mark.parametrize("room", [0, WIDE], ids=["clusters", "ranges"])
+@pytest.mark.parametrize("B,H,Hkv,d,ps,prefix_len", SHAPES, ids=str)
+def test_decode_directly_behind_append(cuda_device, room, B, H, Hkv, d, ps, prefix_len):
+    """Steps of append and decode whose inputs are all made in advance: the decode (or the gather or prefix kernel in front
+    of it) is launched as the append's programmatic dependent, the next append as the decode's."""
+    steps = 30
+    rng = np.random.default_rng(5400)
+    start = rng.integers(0, 200, B)
+    c = _case(cuda_device, (start + steps).tolist(), H, Hkv, d, ps, 5401, prefix_len, room)
+    xs = _randn((steps, B, H + 2 * Hkv, d), cuda_device, 5402)
+    lens = [_int32(start + i + 1, cuda_device) for i in range(steps)]
+    pos = [_int32(start + i + prefix_len, cuda_device) for i in range(steps)]
+    slots = [torch.as_tensor([int(t[n // ps]) * ps + n % ps for t, n in zip(c["tables"], start + i)], device=cuda_device)
+             for i in range(steps)]
+    freqs = fa.fa_rope_freqs(d, device=cuda_device)
+    ws = torch.empty(fa.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, prefix_len), dtype=torch.uint8, device=cuda_device)
+
+    kc, vc = c["kc"].clone(), c["vc"].clone()
+    q, out = torch.empty_like(xs[:, :, :H]).contiguous(), torch.empty((steps, B, H, d), dtype=xs.dtype, device=cuda_device)
+
+    def reset():
+        kc.copy_(c["kc"]), vc.copy_(c["vc"]), q.fill_(math.nan), out.fill_(math.nan)
+
+    def run(pause):
+        for i in range(steps):
+            x = xs[i]
+            fa.fa_paged_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, slots[i], q=x[:, :H], positions=pos[i], freqs=freqs,
+                               q_out=q[i])
+            pause()
+            fa.fa_decode_paged_prefix(q[i], kc, vc, c["prefix_t"], prefix_len, c["table"], lens[i], workspace=ws, o=out[i])
+            pause()
+
+    _same_without_pauses(reset, run, out)
+
+
+@pytest.mark.parametrize("room", [0, WIDE], ids=["clusters", "ranges"])
+@pytest.mark.parametrize("B,H,Hkv,d,ps,prefix_len", SHAPES, ids=str)
+def test_decodes_back_to_back_through_one_workspace(cuda_device, room, B, H, Hkv, d, ps, prefix_len):
+    """Decodes of other queries and lengths directly one behind the other, with and without the prefix in turn, all through
+    one workspace that each finds full of the last one's states."""
+    steps = 24
+    rng = np.random.default_rng(5500)
+    longest = rng.integers(100, 700, B)
+    c = _case(cuda_device, longest.tolist(), H, Hkv, d, ps, 5501, prefix_len, room)
+    qs = _randn((steps, B, H, d), cuda_device, 5502, 1.5)
+    lens = [_int32(rng.integers(-1, longest + 1), cuda_device) for _ in range(steps)]
+    bytes_ = max(fa.fa_decode_paged_workspace_bytes(B, H, Hkv, d, ps, p) for p in (0, prefix_len))
+    ws = torch.empty(bytes_, dtype=torch.uint8, device=cuda_device)
+
+    out = torch.empty((steps, B, H, d), dtype=qs.dtype, device=cuda_device)
+
+    def run(pause):
+        for i in range(steps):
+            plen = prefix_len if i % 3 else 0
+            fa.fa_decode_paged_prefix(qs[i], c["kc"], c["vc"], c["prefix_t"], plen, c["table"], lens[i], workspace=ws,
+                                      o=out[i])
+            pause()
+
+    _same_without_pauses(lambda: out.fill_(math.nan), run, out)
