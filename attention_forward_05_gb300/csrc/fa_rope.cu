@@ -9,10 +9,11 @@
 // Angles.  pos * f_i in fp32 is off by pos * f_i * 2^-24 rad: 0.06 rad at position 10^6.  Only the angle's
 // fraction of a turn matters, and that is exact in integers: f_i / (2 pi) modulo 1 is held as a 64-bit
 // fraction F_i (units of 2^-64 turns), and pos * F_i modulo 2^64 is the phase of any 32-bit position, of
-// either sign, with no range reduction.  F_i carries double precision's rounding of f_i / (2 pi)
-// (2^-54 turns for f_i <= 1), so the phase at position p is off by at most p * 2^-54 turns.  Its upper
-// 32 bits split into the nearest quarter turn and a rest of at most an eighth, whose sine and cosine are
-// Taylor polynomials (to x^9 and x^10: 2e-9 and 1e-10 off at pi/4).  The F_i take four double-precision
+// either sign, with no range reduction.  F_i carries double precision's roundings of 1 / (2 pi) and of f_i / (2 pi)
+// (2^-52 f_i rad together; a negative f_i's fraction is rounded once more, by 2^-54 turns), so the angle at position p is
+// off by at most |p f_i| 2^-52 rad.  Its upper 32 bits split into the nearest quarter turn and a rest of at most an
+// eighth, whose sine and cosine are Taylor polynomials (to x^9 and x^10: 2e-9 and 1e-10 off at pi/4); with the rest's
+// and their own roundings in fp32 they are within 1.9e-7.  The F_i take four double-precision
 // operations each and are formed once per block in shared memory (double precision runs at about two
 // operations a clock and SM here).
 //

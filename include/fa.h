@@ -270,9 +270,12 @@ int fa_decode_splitkv_noalloc(const void* q, const void* k, const void* v, void*
  * phi = positions[axis(i)][b][n] * freqs[i]:
  *   (x1, x2) -> (x1 cos phi - x2 sin phi, x1 sin phi + x2 cos phi)
  * and the elements from `rot` on are copied.  One axis gives text positions;
- * three (time, height, width) those of images and video.  Angles are exact for
- * every 32-bit position (the phase is formed in 64-bit integers, not in fp32);
- * products and sums are fp32, rounded once to dtype.
+ * three (time, height, width) those of images and video.  Angles are formed in
+ * 64-bit integers, not in fp32: position times frequency is exact modulo a turn,
+ * and off by what double precision leaves of the frequency, at most
+ * |pos| (|f| 2^-52 + (f < 0) 2^-51) radians (2.2e-10 at position 10^6, f = 1);
+ * sine and cosine are within 1.9e-7 of that angle's.  Products and sums are fp32,
+ * rounded once to dtype.
  *   q [B, H, N, d], k [B, Hkv, N, d] in dtype (FA_BF16 or FA_FP32), d 64 or 128;
  *     k = k_out = NULL with Hkv = 0 rotates q alone.
  *   q_out, k_out  out: the inputs themselves (same pointer, same strides) or
