@@ -833,10 +833,16 @@ constexpr size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(25
 // of 3: 14.0 us, of 2: 11.0).  A CTA takes about 0.45 us a tile, so at eight tiles a CTA the launch and the join that the clusters save (2 to
 // 4 us) are used up, whatever the real lengths are; behind a prefix, whose states are joined too, at sixteen.  Clusters
 // against ranges, device time at 32 heads on 8 of 128: 1 sequence of 2000 keys 6.1 and 8.1 us, 4000: 8.2 and 9.2, 8000:
-// 12.1 and 10.2; 16 of 300: 6.1 and 8.9, 1500: 14.4 and 14.1; 48 of 400: 9.3 and 13.1; 64 of 400: 18.1 and 16.9; 100 of 400:
-// 29.7 and 32.4; behind a prefix 48 of 60: 17.3 and 24.6, 64 of 800: 48 and 56, 256 of 1 to 600: 77.7 and 81.6, 64 of 1 to
-// 1500: 34.1 and 33.6.
+// 12.1 and 10.2; 16 of 300: 6.1 and 8.9, 1500: 14.4 and 14.1; 48 of 400: 9.3 and 13.1; 100 of 400: 29.7 and 32.4; behind a
+// prefix 48 of 60: 17.3 and 24.6, 64 of 800: 48 and 56, 64 of 1 to 1500: 34.1 and 33.6.  Where the units are a little more than
+// the CTAs that may run at once, sequences that fill their tables leave the second wave nearly empty, others do not (512
+// units of 384 keys: 16.9 and 15.1; of 1 to 384: 11.5 and 13.2); the lengths are not known here.
+// Many units of one or two tiles, without a prefix, are left to the ranges: a unit's start and end are most of its time, and
+// a CTA of a range fetches the next unit's keys meanwhile.  Clusters and ranges: 32 heads on 8 of 128, 456 sequences of 64
+// keys 36 and 30 us, of 128 46 and 49, of 1 to 128 38 and 34, of 192 61 and 66, of 1 to 192 43 and 41; 300 of 64 20.2 and
+// 20.0, of 128 32 and 35; 32 on 8 of 64, 600 of 128 45 and 35, of 256 60 and 57.
 int cluster_size(long long units, long long tiles, int n_cta, int sms, bool prefix) {
+  if (!prefix && tiles <= 2 && units > 6LL * n_cta) return 0;
   const long long most = tiles > 2 ? (tiles < 8 ? tiles : 8) : 1;
   long long cl = 1;
   if (prefix)
