@@ -268,7 +268,7 @@ __device__ __forceinline__ void join_cluster(const PgParams& p, int b, int len, 
 
 template <class C, bool CLUSTER>
 __global__ void __launch_bounds__(32 * C::NW, C::CTAS) fa_paged_kernel(const PgParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(256) uint8_t smem[];  // pieces are found by xor on address bits 4 to 7
   constexpr int D = C::D, KW = C::KW, NW = C::NW, S = C::STAGES;
   constexpr int CPR = D / 8;        // 16-byte pieces of a row
   constexpr int RPP = 32 / CPR;     // rows one warp-wide copy covers
