@@ -9,7 +9,7 @@
 //
 // Measured, the whole call: 16384 shared keys, 256 sequences (d = 128, 32 heads on 8) 96 us, 720 TFLOP/s of the formula's
 // products (P V is done twice, FwdCfg::TWO), of which this kernel takes 74; 8192 shared keys, 32 sequences (d = 64) 15 us;
-// 1000 and 5 7.3 us.  With P rounded to bf16 once: 78, 14 and 7.2 us, and o up to 40 % further from the formula.
+// 1000 and 5 7.5 us.  With P rounded to bf16 once: 78, 14 and 7.5 us, and o up to 40 % further from the formula.
 //
 // Configurations (fa_fwd_bf16.cu and fa_fwd_decode.cu have the same tiles): two 128-row query tiles per CTA, or
 // one where the B * G rows of a head fit in it.

@@ -26,8 +26,8 @@
 // Both kernels are bound by device memory (each element is read once and written once) as long as the instructions
 // are few: the products go in packed fp32 pairs.  Measured, bytes read and written over the time with the launch (about
 // 3 us): q and k of 4 x 4096 tokens, 32 heads of 64, bf16: 23.8 us, 5.6 TB/s; 2 x 8192 tokens, 20 heads of 128, three
-// axes, adjacent pairs: 29 us, 5.8 TB/s; appending 8191 tokens, 48 heads of 128: 35.7 us, 5.6 TB/s; 333 tokens, 20 heads
-// of 64, fp32: 2.7 us.  With register loads of the current item, each block on one contiguous range: 26.3, 31.1, 36.3
+// axes, adjacent pairs: 29 us, 5.8 TB/s; appending 8191 tokens, 48 heads of 128: 34.7 us, 5.8 TB/s; 333 tokens, 20 heads
+// of 64, fp32: 2.9 us.  With register loads of the current item, each block on one contiguous range: 26.3, 31.1, 36.3
 // and 3.2 us; with adjacent pairs' 32 bytes a lane in two half-sector copies instead of pieces: 32.0 and 37.6 us for the
 // second and third.  Two items ahead measured the same or up to 5 % more.
 #include <cuda_bf16.h>
