@@ -431,10 +431,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_paged_append_ker
 // Cuts `tokens` x `heads`: as many heads a lane, up to what its stage holds, as leave an item for every warp.  Large inputs
 // go faster with fewer blocks a SM, and so fewer places of device memory read and written at a time, as long as two full
 // stages a warp are on their way for each of two blocks: heads that fill only part of the lanes' stages need more blocks.
-// Times with 2 / 3 / 4 blocks: bf16, 16 heads of 128 (stages full), 290 MB read and written: 47.6 / 51.5 / 51.4 us; 20 heads
-// (5/8): 53.7 / 47.2 / 50.3; 8 (half): 58.5 / 50.3 / 46.7; one of 64 (a quarter): 136 / 112 / 103; fp32, 8 heads of 128
-// (full): 48.2 / 49.6 / 50.3; 5 (5/8): 51.7 / 46.2 / 50.3.  At 140 MB four are as good or better for nearly all (24.9 / 21.8 /
-// 21.3, 28.0 / 24.8 / 23.1, 30.2 / 26.5 / 24.9 for the bf16 ones of 128); at 170 MB either rule is within 7 % of the best.
+// One launch behind another, times with 2 / 3 / 4 blocks at 290 MB read and written: bf16, 16 heads of 128 (stages full) 47.6 /
+// 51.5 / 51.4 us; 20 heads (5/8) 53.7 / 47.2 / 50.3; 8 (half) 58.5 / 50.3 / 46.7; one of 64 (a quarter) 136 / 112 / 103; fp32, 8
+// heads of 128 (full) 48.2 / 49.6 / 50.3; 5 (5/8) 51.7 / 46.2 / 50.3.  From 256 MB on that decides.  Smaller inputs depend on
+// what the L2 cache holds: 200 MB of 32 heads of 64, 34.0 / 35.5 / 35.7 behind another launch, 39.6 / 41.6 / 41.6 with the
+// cache full of unwritten lines, 35.5 / 31.4 / 31.4 with none; 48 heads of 128 appended, 34.7 / 34.5 / 35.4, 39.6 / 41.6 / 40.6 and
+// 37.5 / 33.4 / 31.4.  So three at least there, and four below 165 MB, where they are as good or better in every state (140 MB
+// of 20 heads of 128: 27.7 / 24.5 / 22.8 behind another launch).
 template <typename T, int D, bool QUAD>
 static cudaError_t tile(long long tokens, int heads, int sms, Tiling* g, unsigned* grid) {
   using L = Lane<D, QUAD>;
@@ -442,7 +445,8 @@ static cudaError_t tile(long long tokens, int heads, int sms, Tiling* g, unsigne
   const long long bytes = tokens * heads * D * static_cast<long long>(2 * sizeof(T));
   const long long room = (heads + L::STEP * most - 1) / (L::STEP * most) * static_cast<long long>(L::STEP * most);  // heads the stages hold
   const int full = static_cast<int>((4 * room + heads) / (2 * heads));  // 2 * room / heads, to the nearest
-  const int blocks_sm = bytes < 165000000 || full > ROPE_BLOCKS ? ROPE_BLOCKS : full;
+  const int least = bytes < 165000000 ? ROPE_BLOCKS : bytes < 256000000 ? 3 : 2;
+  const int blocks_sm = full > ROPE_BLOCKS ? ROPE_BLOCKS : full > least ? full : least;
   const long long resident = static_cast<long long>(sms) * blocks_sm * warps, blocks = (tokens + L::TOKS - 1) / L::TOKS;
   long long count = 0;
   for (int per = most;; per /= 2) {
