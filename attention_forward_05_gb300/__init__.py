@@ -24,8 +24,18 @@ Entry points (same names as the C ABI):
   fa_rope_freqs(rot, theta=10000.0) -> float64 frequencies
   fa_rope(q, k, positions, freqs, axes=None, interleaved=False) -> (q_out, k_out)
   fa_rope_bwd(dq, dk, positions, freqs, axes=None, interleaved=False) -> (dq_in, dk_in)
+  fa_norm_rope(q, k, q_weight, k_weight, positions, freqs, axes=None, interleaved=False, eps=1e-6)
+      -> (q_out, k_out)
+  fa_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, freqs, axes=None, interleaved=False, eps=1e-6)
+      -> (dq_in, dk_in, dq_weight, dk_weight)
+  fa_norm_rope_bwd_workspace_bytes(d)
   fa_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, freqs=None, axes=None,
-                  interleaved=False) -> q_out or None
+                  interleaved=False, q_weight=None, k_weight=None, eps=1e-6) -> q_out or None
+  fa_paged_slots(ctx_lens, new_lens, page_table, free_pages, free_count, page_size, tokens)
+      -> (cu_seqlens, positions, slots, seq_lens, free_left)
+  fa_fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, scale=None, window=0, sinks=0,
+               workspace=None, with_lse=False) -> (o, lse)
+  fa_fwd_paged_workspace_bytes(T, B, H, Hkv, d)
   fa_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale=None, workspace=None, with_lse=False)
       -> (o, lse)
   fa_decode_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None,
@@ -111,6 +121,21 @@ def lib() -> ctypes.CDLL:
             L.fa_decode_paged_workspace_bytes.restype = sz
             L.fa_decode_paged_call_bytes.argtypes = [i, i, i, i, i, i, i]
             L.fa_decode_paged_call_bytes.restype = sz
+            L.fa_norm_rope.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, i, f, vp, i, vp, vp, i, i, i, vp]
+            L.fa_norm_rope.restype = i
+            L.fa_norm_rope_bwd.argtypes = [vp] * 9 + [i] * 6 + [vp, vp, i, f, vp, i, vp, vp, i, i, i, vp, sz, vp]
+            L.fa_norm_rope_bwd.restype = i
+            L.fa_norm_rope_bwd_workspace_bytes.argtypes = [i]
+            L.fa_norm_rope_bwd_workspace_bytes.restype = sz
+            L.fa_paged_append_norm.argtypes = [vp] * 9 + [i] * 6 + [vp, vp, i, f, vp, vp, vp, i, i, i, vp]
+            L.fa_paged_append_norm.restype = i
+            L.fa_paged_slots.argtypes = [vp, vp, vp, ll, vp, i, vp, i, i, i, i, vp, vp, vp, vp, vp, vp]
+            L.fa_paged_slots.restype = i
+            L.fa_fwd_paged.argtypes = [vp, vp, vp, vp, vp, ll, vp, vp, i, i, i, i, i, i, i, i, vp, vp, f, i, i, vp, sz,
+                                       vp, vp]
+            L.fa_fwd_paged.restype = i
+            L.fa_fwd_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+            L.fa_fwd_paged_workspace_bytes.restype = sz
             L.fa_check_device_error.argtypes = []
             L.fa_check_device_error.restype = i
             L.fa_status_string.argtypes = [i]
@@ -497,22 +522,109 @@ def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tens
     return r if r.__class__ is tuple else _result(r, "fa_rope (backward)")
 
 
+def fa_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor, k_weight: torch.Tensor | None,
+                 positions: torch.Tensor | None, freqs: torch.Tensor | None, axes: torch.Tensor | None = None,
+                 interleaved: bool = False, eps: float = 1e-6, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None, stream=None):
+    """fa_rope on heads that are first divided by their root mean square and multiplied by weights; returns (q_out, k_out).
+
+    y = R(w x / sqrt(mean(x^2) + eps)) in fp32, rounded once.  q_weight, k_weight: [d], bf16 or fp32 both; positions and
+    freqs None: norms without a rotation.  Other arguments as in fa_rope.
+    """
+    if stream is not None:
+        with _on_stream(stream, q, k, q_weight, k_weight, positions, freqs, axes, q_out, k_out):
+            return fa_norm_rope(q, k, q_weight, k_weight, positions, freqs, axes, interleaved, eps, q_out, k_out)
+    r = (_binding or _load_binding()).norm_rope(q, k, q_weight, k_weight, positions, freqs, axes, interleaved, eps, q_out,
+                                                k_out)
+    return r if r.__class__ is tuple else _result(r, "fa_norm_rope")
+
+
+def fa_norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                     q_weight: torch.Tensor, k_weight: torch.Tensor | None, positions: torch.Tensor | None,
+                     freqs: torch.Tensor | None, axes: torch.Tensor | None = None, interleaved: bool = False,
+                     eps: float = 1e-6, dq_in: torch.Tensor | None = None, dk_in: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """The backward pass of fa_norm_rope: gradients dq, dk of its outputs and its inputs q, k in; gradients (dq_in, dk_in,
+    dq_weight, dk_weight) of its inputs and weights out, the weights' in fp32, summed over tokens and heads."""
+    if stream is not None:
+        with _on_stream(stream, dq, dk, q, k, q_weight, k_weight, positions, freqs, axes, dq_in, dk_in, workspace):
+            return fa_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, freqs, axes, interleaved, eps, dq_in,
+                                    dk_in, workspace)
+    r = (_binding or _load_binding()).norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, freqs, axes, interleaved,
+                                                    eps, dq_in, dk_in, workspace)
+    return r if r.__class__ is tuple else _result(r, "fa_norm_rope_bwd")
+
+
+def fa_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    return int(lib().fa_norm_rope_bwd_workspace_bytes(int(d)))
+
+
 def fa_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     slots: torch.Tensor, q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
                     freqs: torch.Tensor | None = None, axes: torch.Tensor | None = None, interleaved: bool = False,
-                    q_out: torch.Tensor | None = None, stream=None):
+                    q_out: torch.Tensor | None = None, stream=None, q_weight: torch.Tensor | None = None,
+                    k_weight: torch.Tensor | None = None, eps: float = 1e-6):
     """Writes new tokens' k, v [T, Hkv, d] to their slots of a paged cache; returns the tokens' queries (or None).
 
     k_cache, v_cache: bf16 [num_pages, Hkv, page_size, d] (strided views with d contiguous allowed, the same strides
     for both).  slots: int64 [T], page * page_size + row; a negative slot stores nothing.  positions (int32 [T] or
     [axes, T]) with freqs rotate k and q as fa_rope does; without them both are copied.  q [T, H, d] may be strided.
+    k_weight (and q_weight, with q) norm the heads first, as fa_norm_rope does.
     """
     if stream is not None:
-        with _on_stream(stream, k, v, k_cache, v_cache, slots, q, positions, freqs, axes, q_out):
-            return fa_paged_append(k, v, k_cache, v_cache, slots, q, positions, freqs, axes, interleaved, q_out)
+        with _on_stream(stream, k, v, k_cache, v_cache, slots, q, positions, freqs, axes, q_out, q_weight, k_weight):
+            return fa_paged_append(k, v, k_cache, v_cache, slots, q, positions, freqs, axes, interleaved, q_out, None,
+                                   q_weight, k_weight, eps)
     r = (_binding or _load_binding()).append(k, v, k_cache, v_cache, slots, q, positions, freqs, axes, interleaved,
-                                             q_out)
+                                             q_out, q_weight, k_weight, eps)
     return _result(r, "fa_paged_append")
+
+
+def fa_paged_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
+                   free_count: torch.Tensor, page_size: int, tokens: int, cu_seqlens: torch.Tensor | None = None,
+                   positions: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                   seq_lens: torch.Tensor | None = None, free_left: torch.Tensor | None = None, stream=None):
+    """A step's bookkeeping on the GPU; returns (cu_seqlens, positions, slots, seq_lens, free_left).
+
+    Sequence b has ctx_lens[b] tokens in the cache and gets new_lens[b] more (both int32 [B]).  Its new pages come from the
+    top of the stack free_pages (int32, its first free_count[0] entries are free) and go into its row of page_table (int32
+    [B, max_pages], changed in place).  cu_seqlens [B + 1], positions [tokens], slots [tokens] (int64), seq_lens [B] and
+    free_left [1] are new tensors or the given ones; seq_lens may be ctx_lens and free_left free_count, so that a captured
+    step counts on by itself.  Places behind the last token get slot -1; a sequence that does not fit gets -1 as its length
+    and slots, and makes fa_check_device_error return FA_ERR_INVALID_ARG.
+    """
+    if stream is not None:
+        with _on_stream(stream, ctx_lens, new_lens, page_table, free_pages, free_count, cu_seqlens, positions, slots,
+                        seq_lens, free_left):
+            return fa_paged_slots(ctx_lens, new_lens, page_table, free_pages, free_count, page_size, tokens, cu_seqlens,
+                                  positions, slots, seq_lens, free_left)
+    r = (_binding or _load_binding()).slots(ctx_lens, new_lens, page_table, free_pages, free_count, page_size, tokens,
+                                            cu_seqlens, positions, slots, seq_lens, free_left)
+    return r if r.__class__ is tuple else _result(r, "fa_paged_slots")
+
+
+def fa_fwd_paged_workspace_bytes(T: int, B: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib().fa_fwd_paged_workspace_bytes(int(T), int(B), int(H), int(Hkv), int(d)))
+
+
+def fa_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                 cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, scale: float | None = None, window: int = 0,
+                 sinks: int = 0, workspace: torch.Tensor | None = None, with_lse: bool = False,
+                 o: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Causal attention of a ragged batch's new tokens over a paged cache that holds their keys and values already;
+    returns (o [T, H, d], lse [T, H] or None).
+
+    q: bf16 [T, H, d], may be a strided view; sequence b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1])
+    and the last of its seq_lens[b] (int32 [B]) keys.  window > 0: a token sees the last `window` keys up to its own and the
+    first `sinks` keys.  page_table as in fa_decode_paged.  Rows behind cu_seqlens[B] stay unwritten.
+    """
+    if stream is not None:
+        with _on_stream(stream, q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, workspace, o, lse):
+            return fa_fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, scale, window, sinks, workspace,
+                                with_lse, o, lse)
+    r = (_binding or _load_binding()).fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, scale, window,
+                                                sinks, workspace, with_lse, o, lse)
+    return r if r.__class__ is tuple else _result(r, "fa_fwd_paged")
 
 
 def fa_decode_paged_call_bytes(B: int, H: int, Hkv: int, d: int, page_size: int, max_pages: int, prefix_len: int = 0) -> int:

@@ -26,7 +26,8 @@ LIB = os.path.join(OUT, "libfa.so")
 BINDING_SRC = os.path.join(CSRC, "fa_binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd_bf16.cu", "fa_fwd_fp32.cu", "fa_fwd_merge.cu", "fa_decode.cu",
            "fa_decode_noalloc.cu", "fa_bwd.cu", "fa_bwd_fp32.cu",
-           "fa_decode_gqa.cu", "fa_fwd_decode.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_prefix.cu", "fa_paged_api.cu"]
+           "fa_decode_gqa.cu", "fa_fwd_decode.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_prefix.cu", "fa_paged_api.cu",
+           "fa_norm_rope.cu", "fa_slots.cu", "fa_fwd_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

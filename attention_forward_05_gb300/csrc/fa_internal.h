@@ -150,6 +150,74 @@ struct AppendLaunch {
 };
 cudaError_t launch_append(const AppendLaunch& a);
 
+// Norms of query and key heads ahead of the rotation (fa_norm_rope.cu).
+struct HeadNorm {
+  const void* wq;  // [d]
+  const void* wk;  // [d]; nullptr without key heads
+  int fp32;        // the weights' type: fp32, or bf16
+  float eps;
+};
+cudaError_t launch_norm_rope(const RopeLaunch& a, const HeadNorm& nm);
+cudaError_t launch_norm_append(const AppendLaunch& a, const HeadNorm& nm);
+
+// The backward pass: q, k of the RopeLaunch are the outputs' gradients, q_out, k_out the inputs' ones.
+struct NormBwd {
+  const void* q;        // the forward pass's inputs
+  const void* k;
+  RowStrides sq, sk;
+  float* dwq;           // [d]
+  float* dwk;
+  float* parts;         // workspace: [norm_bwd_parts(sms)][2][d]
+};
+int norm_bwd_parts(int sms);
+cudaError_t launch_norm_rope_bwd(const RopeLaunch& a, const NormBwd& b, const HeadNorm& nm);
+
+// Step bookkeeping (fa_slots.cu).
+constexpr int SLOTS_MAX_B = 16384;  // sequences whose tables fit a CTA's shared memory
+struct SlotsLaunch {
+  const int* ctx_lens;      // [B]
+  const int* new_lens;      // [B]
+  int* page_table;          // [B, max_pages], rows table_stride apart
+  const int* free_pages;    // [n_free]
+  const int* free_count;    // [1]
+  int* cu_seqlens;          // [B + 1]
+  int* positions;           // [T]
+  long long* slots;         // [T]
+  int* seq_lens;            // [B]
+  int* free_left;           // [1]
+  long long table_stride;
+  int B, T, n_free, page_size, max_pages;
+  int* err;
+  cudaStream_t stream;
+};
+cudaError_t launch_slots(const SlotsLaunch& a);
+
+// Attention of a ragged batch's new tokens over the paged cache (fa_fwd_paged.cu).
+constexpr int FWD_PAGED_MAX_B = 16384;  // sequences whose block counts fit the tile ring's shared memory
+constexpr int FWD_PAGED_MAX_G = 128;    // query heads of a key/value head: rows of a query tile
+struct FwdPagedLaunch {
+  const void* q;            // [T, H, d] bf16, strides q_tok, q_head
+  const void* k_cache;
+  const void* v_cache;
+  void* o;                  // [T, H, d] bf16
+  float* lse;               // [T, H] or nullptr
+  long long q_tok, q_head;
+  long long c_page, c_head, c_row;  // element strides of both caches
+  const int* table;         // [B, max_pages], rows table_stride apart
+  const int* cu;            // [B + 1]
+  const int* lens;          // [B]
+  int T, B, H, Hkv, d, num_pages, page_size, max_pages;
+  long long table_stride;
+  int window, sinks;        // window 0: every key up to the token's own
+  float c;                  // scale * log2(e)
+  char* ws;                 // fwd_paged_workspace(...) bytes
+  int* err;
+  int sms;
+  cudaStream_t stream;
+};
+size_t fwd_paged_workspace(int T, int B, int H, int Hkv, int d, int sms);
+cudaError_t launch_fwd_paged(const FwdPagedLaunch& a);
+
 struct PagedLaunch {
   const void* q;            // [B, H, d] bf16
   const void* k_cache;

@@ -1,9 +1,10 @@
 /*
  * fa.h -- C ABI of libfa: fused FlashAttention forward (plain, causal,
  * grouped-query, split-KV), its backward, and split-KV decode (per-head and
- * grouped-query) for one NVIDIA GB300 GPU (sm_103a); rotary positions, a paged
- * key/value cache and the decode that reads it, with or without a prefix that
- * all sequences share.
+ * grouped-query) for one NVIDIA GB300 GPU (sm_103a); rotary positions, with
+ * norms of the heads in the same pass or without, a paged key/value cache, its
+ * bookkeeping, the decode that reads it, with or without a prefix that all
+ * sequences share, and the attention of chunks of new tokens over it.
  *
  * Sources (web pages, cited by title and section):
  *   [T1] "FlashAttention 简化版：Tiling + Online Softmax" (forceinjection.github.io)
@@ -300,6 +301,47 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long l
             fa_stream_t stream);
 
 /*
+ * fa_norm_rope -- fa_rope on heads that are normed first, in the same pass: for a head x of d elements with
+ * the weights w (q_weight for every query head, k_weight for every key head),
+ *   y = R(w x / sqrt(mean(x^2) + eps)),  R fa_rope's rotation,
+ * in fp32, rounded once to dtype.
+ *   q_weight, k_weight  device [d] in weight_dtype (FA_BF16 or FA_FP32, whatever dtype is); k_weight
+ *                       NULL with Hkv = 0.  eps finite, >= 0.
+ *   positions, freqs    NULL with rot = 0: norms alone.
+ * Other arguments and rules as in fa_rope.
+ */
+int fa_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                 int B, int H, int Hkv, int N, int d, int dtype, const void* q_weight, const void* k_weight,
+                 int weight_dtype, float eps, const int* positions, int pos_shared, const double* freqs,
+                 const int* axes, int n_axes, int rot, int interleaved, fa_stream_t stream);
+
+/*
+ * fa_norm_rope_bwd -- the backward pass of fa_norm_rope: from the gradients dq, dk of its outputs and its
+ * inputs q, k the gradients of those inputs and of the weights,
+ *   g = R^-1 dy, u = x / sqrt(mean(x^2) + eps):  dx = (w g - u mean(w g u)) / sqrt(mean(x^2) + eps),
+ *   dw = sum of g u over all tokens and heads.
+ *   dq_in, dk_in          out, in dtype: dq, dk or q, k themselves (same pointer, same strides) or memory that
+ *                         overlaps no input
+ *   dq_weight, dk_weight  out, device fp32 [d] (dk_weight NULL with Hkv = 0)
+ *   strides               NULL = all contiguous, or a HOST array of 18: the (batch, head, token) strides of
+ *                         dq, dk, dq_in, dk_in, q and k
+ *   workspace             device buffer of at least fa_norm_rope_bwd_workspace_bytes(d) bytes, 16-byte aligned,
+ *                         or NULL to allocate it stream-ordered on `stream`; calls that may overlap on the GPU
+ *                         must not share one
+ * Sums are fp32 in a fixed order, without atomics: repeated calls on one GPU give identical bits.  Other
+ * arguments as in fa_norm_rope.
+ */
+int fa_norm_rope_bwd(const void* dq, const void* dk, const void* q, const void* k, void* dq_in, void* dk_in,
+                     float* dq_weight, float* dk_weight, const long long* strides, int B, int H, int Hkv,
+                     int N, int d, int dtype, const void* q_weight, const void* k_weight, int weight_dtype,
+                     float eps, const int* positions, int pos_shared, const double* freqs, const int* axes,
+                     int n_axes, int rot, int interleaved, void* workspace, size_t workspace_bytes,
+                     fa_stream_t stream);
+
+/* Bytes of workspace fa_norm_rope_bwd needs on the current device; 0 on bad arguments or without an sm_103 GPU. */
+size_t fa_norm_rope_bwd_workspace_bytes(int d);
+
+/*
  * fa_paged_append -- writes the keys and values of T new tokens into a paged
  * cache, rotating the keys (and the tokens' queries) on the way.
  *
@@ -392,6 +434,79 @@ size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d, int page_si
 /* Bytes of workspace that a call with tables of max_pages pages uses: those, or 0 where it uses none (no prefix and
  * tables of a few thousand keys at most), so that its workspace can be NULL without an allocation. */
 size_t fa_decode_paged_call_bytes(int B, int H, int Hkv, int d, int page_size, int max_pages, int prefix_len);
+
+/*
+ * fa_paged_append_norm -- fa_paged_append with the norms of fa_norm_rope: keys (and queries) are normed, rotated
+ * and rounded once on their way; values are copied.  q_weight is NULL with H = 0.
+ */
+int fa_paged_append_norm(const void* k, const void* v, const void* q, void* q_out, void* k_cache, void* v_cache,
+                         const long long* in_strides, const long long* cache_strides, const long long* slots,
+                         int T, int H, int Hkv, int d, int num_pages, int page_size, const void* q_weight,
+                         const void* k_weight, int weight_dtype, float eps, const int* positions,
+                         const double* freqs, const int* axes, int n_axes, int rot, int interleaved,
+                         fa_stream_t stream);
+
+/*
+ * fa_paged_slots -- a step's bookkeeping from its request lengths, on the GPU: what fa_paged_append, fa_fwd_paged
+ * and fa_decode_paged take.  Sequence b has ctx_lens[b] tokens in the cache and gets new_lens[b] more, which follow
+ * one another in the step's tokens, sequence by sequence.
+ *   ctx_lens, new_lens  device int32 [B]; new_lens[b] <= 0: no new tokens (a place that is unused may have
+ *                       a negative ctx_lens[b] too)
+ *   page_table          device int32 [B, max_pages], rows table_stride entries apart: a sequence's new pages are
+ *                       added behind the ceil(ctx_lens[b] / page_size) that it has
+ *   free_pages          device int32 [n_free], free_count device int32 [1]: a stack of free pages, of which the top
+ *                       ones are dealt, to the sequences in order: first free_pages[free_count - 1]
+ *   T                   places for new tokens
+ *   cu_seqlens          out, device int32 [B + 1]: sequence b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+ *   positions, slots    out, device int32 and int64 [T]: position and page * page_size + row of each token; 0 and -1
+ *                       in places behind the last token
+ *   seq_lens            out, device int32 [B]: ctx_lens[b] plus the new tokens; may be ctx_lens itself
+ *   free_left           out, device int32 [1]: the free pages that are left; may be free_count itself
+ * A sequence fails where ctx_lens[b] is negative, its tokens pass max_pages * page_size or the T places, or the free pages
+ * do not reach for it and those before it: it gets no page, seq_lens[b] = -1 and slots of -1 (positions of 0), and
+ * fa_check_device_error reports FA_ERR_INVALID_ARG.  The others are not affected.  (fa_fwd_paged gives a failed
+ * sequence's tokens NaN.)  No other output may overlap an input.  max_pages * page_size < 2^30; B <= 16384
+ * (FA_ERR_UNSUPPORTED above); B = 0 and T = 0 are steps without sequences or tokens.
+ */
+int fa_paged_slots(const int* ctx_lens, const int* new_lens, int* page_table, long long table_stride,
+                   const int* free_pages, int n_free, const int* free_count, int B, int T, int page_size,
+                   int max_pages, int* cu_seqlens, int* positions, long long* slots, int* seq_lens,
+                   int* free_left, fa_stream_t stream);
+
+/*
+ * fa_fwd_paged -- attention of a ragged batch's new tokens (prompts, parts of prompts, drafts, single tokens) over a
+ * paged cache that holds their keys and values already.  Sequence b has the tokens cu_seqlens[b] .. cu_seqlens[b + 1]
+ * - 1 of q, n_b of them, the last of its seq_lens[b] keys: token i stands at position p = seq_lens[b] - n_b + i and
+ * sees the keys 0 .. p (causal), or with window > 0 those of them with j > p - window or j < sinks.
+ *
+ *   q, o       [T, H, d] bf16 (o is written, contiguous); query head h reads key/value head h / (H / Hkv).
+ *   q_strides  NULL = contiguous, or a HOST array of 2: the token and head strides of q in elements,
+ *              multiples of 8; heads lie within a token (d <= head stride <= token stride).
+ *   k_cache, v_cache, cache_strides, num_pages, page_size, page_table, table_stride   as in fa_decode_paged.  Pages
+ *              that no token sees, behind a window, are not read: their entries may hold anything.
+ *   cu_seqlens device int32 [B + 1], ascending, cu_seqlens[B] <= T.  Rows of o and lse behind cu_seqlens[B] are left
+ *              as they were.
+ *   seq_lens   device int32 [B], the new tokens included.
+ *   window     0: none.       sinks  first keys that stay visible behind the window.
+ *   scale, lse as in fa_decode_paged; lse [T, H].
+ *   workspace  device buffer of at least fa_fwd_paged_workspace_bytes(T, B, H, Hkv, d) bytes, 16-byte aligned, or
+ *              NULL to allocate it stream-ordered on `stream`.  It needs no clearing; calls that may overlap on the
+ *              GPU must not share one.
+ * A sequence with seq_lens[b] below its new tokens or above max_pages * page_size gets NaN in o and lse, one
+ * with a page outside the cache NaN in the tokens that the page reaches (and others near them); offsets that do
+ * not ascend make their sequence's tokens stay unwritten.  fa_check_device_error then reports FA_ERR_INVALID_ARG.
+ * Accumulation and softmax statistics are fp32.  No atomics on results: repeated calls on one GPU give identical bits.
+ * H / Hkv <= 128, B <= 16384 (FA_ERR_UNSUPPORTED otherwise); max_pages * page_size < 2^30, T * (H / Hkv) <= 2^30.
+ */
+int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, const int* page_table,
+                 long long table_stride, const int* cu_seqlens, const int* seq_lens, int T, int B, int H,
+                 int Hkv, int d, int num_pages, int page_size, int max_pages, const long long* q_strides,
+                 const long long* cache_strides, float scale, int window, int sinks, void* workspace,
+                 size_t workspace_bytes, float* lse, fa_stream_t stream);
+
+/* Bytes of workspace fa_fwd_paged needs on the current device; 0 when none is needed, on bad arguments or without an
+ * sm_103 GPU. */
+size_t fa_fwd_paged_workspace_bytes(int T, int B, int H, int Hkv, int d);
 
 /*
  * fa_check_device_error -- reads and clears the library's device error word
