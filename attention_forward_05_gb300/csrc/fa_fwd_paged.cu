@@ -3,81 +3,1179 @@
 // Token i of sequence b's n_b new ones stands at position p = len_b - n_b + i and sees the keys 0 .. p, or with a sliding
 // window w the keys p - w + 1 .. p and the first `sinks` ones: o = softmax(scale q K^T) V over those, and the LSE.
 //
-// One warp a (token, head): its lanes hold d / 32 elements each, every key costs a sum over the warp.
+// Products.  The rows of a tile are the (token, head of the group) pairs of one key/value head, so a key is read and
+// multiplied once for the whole group.  A block is two tiles of up to 128 rows (whole tokens); its keys come in tiles of BC.
+// The pipeline is the forward kernel's (fa_fwd_kernel.cuh): S = Q K^T and O += P V on tcgen05 with S, P and O in tensor
+// memory, a softmax warpgroup a tile with a thread a row, P over S, O rescaled only when a maximum moves by more than 2^tau.
+// The CTAs stay (one a SM at d = 128, two at 64) and walk through units of work; the load warp runs ahead into the next
+// unit, and its first Q K^T is issued while the last one's epilogue is still writing.
+//
+// Work split.  A unit is (key/value head, block): its keys cut into tiles.  The tiles of all units, in order and weighed by
+// what they cost, are dealt evenly to the CTAs, one contiguous range each, whatever the lengths are (they stay in device
+// memory; every CTA sums them itself).  A range covers whole units, which the CTA finishes, and at most two parts of units
+// at its ends, whose states (m, l, unnormalised O) it leaves in the workspace; fa_fwd_paged_join_kernel joins those in the
+// order of the keys.  No atomics on results: they depend on the lengths and the SM count alone.
+//
+// Keys and values come out of the pages by TMA boxes of as many rows as divide the page size (8 at least: a swizzle
+// period), or, where no such box exists, by 16-byte asynchronous copies.  Keys that no row of the block sees are not read
+// (their pages may be gone); their values are zeros.  A value that some rows see and others do not may be infinite or NaN,
+// and 0 * inf would reach the others: the load warp sets such values aside (zeros in their place), and the epilogue
+// adds them to the rows that see them.
 #include <cuda_bf16.h>
 
-#include "fa_internal.h"
-#include "sm103_ptx.cuh"
+#include "fa_fwd_kernel.cuh"
 
 namespace fa {
 
 namespace {
 
-enum : int { W_FWD_PAGED = 0x48 };  // site recorded with DEV_BAD_INDEX
+enum : int { W_OFFSETS = 0x48, W_LENGTH, W_PAGE, W_DESC, W_DESC_FREE, W_QFREE };  // sites recorded
 
+constexpr float kTau = 32.f;  // fa_api.cu, kLazyTau
+
+template <int D_, bool GATHER_>
+struct ChunkCfg {
+  static constexpr int D = D_;
+  static constexpr bool GATHER = GATHER_;
+  static constexpr int BC = D == 128 ? 128 : 64;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int MINB = D == 128 ? 1 : 2;  // CTAs per SM
+  static constexpr bool PV2 = D == 128;          // P handed over in two halves (FwdCfg)
+  static constexpr int BR = 128;
+  static constexpr int NCH = D / 64;             // 128-byte segments of a row
+  static constexpr int Q_CH_BYTES = BR * 128, KV_CH_BYTES = BC * 128;
+  static constexpr int Q_BYTES = NCH * Q_CH_BYTES, KV_BYTES = NCH * KV_CH_BYTES;
+  static constexpr int OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + STAGES * KV_BYTES, OFF_BAR = OFF_V + STAGES * KV_BYTES;
+  static constexpr int UNITS = 4;                // units announced at a time
+  static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
+  static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_MISC = OFF_UNITS + UNITS * 64;
+  static constexpr int SMEM_BYTES = OFF_MISC + 512 + 1024;  // plan's scratch; slack to align the base to 1024
+  static constexpr int O_COL0 = 2 * BC;          // TMEM: S_t at t * BC, O_t at O_COL0 + t * D
+  static constexpr int TMEM_COLS = 2 * (BC + D);
+  // The values have a load warp of their own at d = 128 (FwdCfg::SPLIT_LOADS); it comes free of registers there.
+  static constexpr int LOAD_WARP = 8, MMA_WARP = 9, LOADV_WARP = D == 128 ? 10 : 8;
+  static constexpr int NWARPS = D == 128 ? 11 : 10, NTHREADS = 32 * NWARPS;
+  static constexpr int CONSUMERS = NWARPS - 1;   // warps that read the announced units
+  static constexpr int WARPS_PER_SUBPART = (NWARPS * MINB + 3) / 4;
+  static constexpr int MAXREG = (16384 / (WARPS_PER_SUBPART * 32)) / 8 * 8;
+  static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory");
+  static_assert(SMEM_BYTES * MINB <= 227 * 1024, "shared memory");
+  static_assert((FWD_PAGED_MAX_B + 1) * 4 <= OFF_BAR, "the plan's block counts lie where the tiles will");
+};
+
+// Costs of the dealing, in quarters of the time of a tile step with both row tiles.  A step of one row tile is bound by its
+// chain of products or its bytes; a unit's start and end take about as long as one and a half steps.
+constexpr int COST_TWO = 4, COST_ONE = 3, COST_UNIT = 6;
+
+struct ChunkParams {
+  __nv_bfloat16* o;
+  float* lse;
+  const __nv_bfloat16* k;  // the caches, for copies of single rows
+  const __nv_bfloat16* v;
+  long long c_page, c_head, c_row;
+  const int* table;
+  const int* cu;
+  const int* lens;
+  long long table_stride;
+  int* err;
+  float4* part_o;    // [CTA][continued, begun][row tile][D / 4][part_rows]
+  float2* part_ml;   // [CTA][continued, begun][row tile][part_rows]
+  struct Begun* begun;  // [CTA]
+  FastDiv by_g, by_page;
+  int T, B, H, Hkv, G, tile_tokens, part_rows, part_tiles;
+  int num_pages, page_size, max_pages, box_rows, heads_inner;
+  int window, sinks;
+  float c, tau, p_lim;
+};
+
+// A unit that a CTA begins and others finish: what the join has to know.
+struct Begun {
+  long long start, total;  // the unit's place in the costs of all units, and their sum
+  int ranges;              // CTAs that the sum is dealt to
+  int tiles, cost;         // its key tiles and what each costs; tiles 0: this CTA begins none
+  int h, q0, ntok;
+};
+
+// Key tiles before place w of a unit that begins at `start`.
+__device__ __forceinline__ int cut(long long w, long long start, int tiles, int cost) {
+  if (w <= start) return 0;
+  const long long x = (w - start - COST_UNIT + cost - 1) / cost;
+  return x <= 0 ? 0 : x >= tiles ? tiles : static_cast<int>(x);
+}
+__device__ __forceinline__ long long range_begin(long long total, int c, int ranges) { return total * c / ranges; }
+
+// A sequence's new tokens, as far as its offsets and length make sense.
+struct Seq {
+  int q0, n, pos0;  // first row of q, tokens, the first one's position
+  bool bad;         // its length does not fit: its tokens become NaN
+};
+__device__ __forceinline__ Seq load_seq(const ChunkParams& p, int b) {
+  Seq s{0, 0, 0, false};
+  if (b >= p.B) return s;
+  const int from = p.cu[b], to = p.cu[b + 1], len = p.lens[b];
+  if (from < 0 || to < from || to > p.T) return s;
+  s.q0 = from;
+  s.n = to - from;
+  s.bad = s.n > 0 && (len < s.n || len > static_cast<long long>(p.max_pages) * p.page_size);
+  s.pos0 = s.bad ? 0 : len - s.n;
+  return s;
+}
+
+// Keys of a block of tokens at positions pos0 .. pos0 + ntok - 1, as tiles: the sinks' ones, then those from the window's
+// first on.
+struct Span {
+  int lo, hi;         // keys that the window shows to some token: lo .. hi - 1
+  int ns, w0, tiles;  // tiles 0 .. ns - 1, then w0 ..; how many in all
+};
+template <int BC>
+__device__ __forceinline__ Span span_of(const ChunkParams& p, int pos0, int ntok) {
+  Span s;
+  s.hi = pos0 + ntok;
+  s.lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+  s.w0 = s.lo / BC;
+  s.ns = min(p.sinks / BC + (p.sinks % BC != 0), s.w0);
+  s.tiles = s.ns + (s.hi + BC - 1) / BC - s.w0;
+  return s;
+}
+template <int BC>
+__device__ __forceinline__ int block_cost(const ChunkParams& p, const Seq& s, int i) {
+  if (s.bad) return COST_UNIT;
+  const int first = i * 2 * p.tile_tokens, ntok = min(2 * p.tile_tokens, s.n - first);
+  return COST_UNIT + (ntok > p.tile_tokens ? COST_TWO : COST_ONE) * span_of<BC>(p, s.pos0 + first, ntok).tiles;
+}
+
+// A unit as the load warp announces it.
+enum : int { UNIT_WHOLE = 0, UNIT_BEGUN = 1, UNIT_CONTINUED = 2, UNIT_BAD = 3, UNIT_NONE = 4 };
+struct __align__(16) Unit {
+  int kind, h, b, q0;
+  int ntok, pos0, jb, je;  // tiles jb .. je - 1 of the block's
+  int ns, w0, lo, hi;
+  int bad_page, set_aside;  // set while its tiles are loaded
+  int pad[2];
+};
+static_assert(sizeof(Unit) == 64, "OFF_MISC");
+
+__device__ __forceinline__ int key_tile(const Unit& u, int j) { return j < u.ns ? j : u.w0 + j - u.ns; }
+
+// Steps of row tile t in this part: it needs no tiles past its own last token.
+template <int BC>
+__device__ __forceinline__ int steps_of(const Unit& u, int t, int tile_tokens) {
+  if (t * tile_tokens >= u.ntok || u.kind >= UNIT_BAD) return 0;
+  const int hi = u.pos0 + min((t + 1) * tile_tokens, u.ntok);
+  return max(0, min(u.je, u.ns + (hi + BC - 1) / BC - u.w0) - u.jb);
+}
+
+// Bits of columns 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Nonzero halves' sign bits where a bf16 is infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+template <int NT>
+__device__ __forceinline__ long long scan(long long v, long long* tmp, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int i = 1; i < 32; i *= 2) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, i);
+    if (lane >= i) x += y;
+  }
+  __syncthreads();  // tmp may still be read
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const long long t = tmp[w];
+    if (w < warp) before += t;
+    all += t;
+  }
+  *total = all;
+  return before + x - v;
+}
+
+template <class C>
+__global__ void __maxnreg__(C::MAXREG)
+    fa_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+  constexpr int D = C::D, BC = C::BC, STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  const auto bar_kf = [&](int s) { return bar0 + 8u * s; };
+  const auto bar_vf = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  const auto bar_ke = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+  const auto bar_ve = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };
+  const auto bar_uf = [&](int i) { return bar0 + 8u * (4 * STAGES + i); };             // unit announced
+  const auto bar_ue = [&](int i) { return bar0 + 8u * (4 * STAGES + C::UNITS + i); };  // and read by all
+  const uint32_t bar1 = bar0 + 8u * (4 * STAGES + 2 * C::UNITS);
+  const uint32_t bar_q = bar1, bar_qe = bar1 + 8, bar_tail = bar1 + 16, bar_drain = bar1 + 24;
+  const auto bar_sf = [&](int t) { return bar1 + 8u * (4 + t); };
+  const auto bar_ph = [&](int t) { return bar1 + 8u * (6 + t); };
+  const auto bar_pf = [&](int t) { return bar1 + 8u * (8 + t); };
+  const auto bar_od = [&](int t) { return bar1 + 8u * (10 + t); };
+  Unit* const units = reinterpret_cast<Unit*>(smem + C::OFF_UNITS);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* const plan_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);                // h, b, block
+  long long* const plan_at = reinterpret_cast<long long*>(smem + C::OFF_MISC + 32);       // start, total
+  long long* const plan_tmp = reinterpret_cast<long long*>(smem + C::OFF_MISC + 64);
+
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_kf(s), 1);
+      mbar_init(bar_vf(s), 1);
+      mbar_init(bar_ke(s), 1);
+      mbar_init(bar_ve(s), 1);
+    }
+    for (int i = 0; i < C::UNITS; ++i) {
+      mbar_init(bar_uf(i), 1);
+      mbar_init(bar_ue(i), C::CONSUMERS);
+    }
+    mbar_init(bar_q, 1);
+    mbar_init(bar_qe, 1);
+    mbar_init(bar_tail, 1);
+    mbar_init(bar_drain, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_sf(t), 1);
+      mbar_init(bar_ph(t), 4);  // one arrive per softmax warp of the tile
+      mbar_init(bar_pf(t), 4);
+      mbar_init(bar_od(t), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::LOAD_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      if (!C::GATHER) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+    }
+  }
+  griddep_wait();
+
+  // ---------------------------------------------------------------- plan: this CTA's range of all units' tiles
+  {
+    int* const nblk = reinterpret_cast<int*>(smem);  // blocks before each sequence, where the tiles will lie
+    const int tb = 2 * p.tile_tokens;
+    const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    long long blocks, mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(p, b);
+      if (blockIdx.x == 0 && s.n == 0 && (p.cu[b] < 0 || p.cu[b] != p.cu[b + 1] || p.cu[b] > p.T))
+        record_bad_index(p.err, W_OFFSETS);
+      if (blockIdx.x == 0 && s.bad) record_bad_index(p.err, W_LENGTH);
+      mine += (s.n + tb - 1) / tb;
+    }
+    long long at = scan<C::NTHREADS>(mine, plan_tmp, &blocks);
+    for (int b = b0; b < b1; ++b) {
+      nblk[b] = static_cast<int>(at);
+      at += (load_seq(p, b).n + tb - 1) / tb;
+    }
+    if (tid == 0) nblk[p.B] = static_cast<int>(blocks);
+    __syncthreads();
+    const int n_blocks = static_cast<int>(blocks);
+    const int pb = (n_blocks + C::NTHREADS - 1) / C::NTHREADS, x0 = min(n_blocks, tid * pb), x1 = min(n_blocks, x0 + pb);
+    int b = 0;
+    if (x0 < x1) {  // the last sequence that begins at or before block x0: those without blocks begin where the next does
+      int hi = p.B;
+      while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (nblk[mid] <= x0) b = mid;
+        else hi = mid;
+      }
+    }
+    long long head = 0;
+    mine = 0;
+    {
+      int bb = b;
+      Seq s = load_seq(p, bb);
+      for (int x = x0; x < x1; ++x) {
+        while (x >= nblk[bb + 1]) s = load_seq(p, ++bb);
+        mine += block_cost<BC>(p, s, x - nblk[bb]);
+      }
+    }
+    const long long before = scan<C::NTHREADS>(mine, plan_tmp, &head);
+    const long long total = head * p.Hkv;
+    const long long least = COST_UNIT + COST_ONE;
+    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1LL, total / least)));
+    const long long w = range_begin(total, min(static_cast<int>(blockIdx.x), ranges), ranges);
+    const int h = head > 0 ? static_cast<int>(w / head) : 0;
+    const long long rem = w - h * head;
+    if (mine > 0 && before <= rem && rem < before + mine) {
+      Seq s = load_seq(p, b);
+      long long from = before;
+      for (int x = x0; x < x1; ++x) {
+        while (x >= nblk[b + 1]) s = load_seq(p, ++b);
+        const int cost = block_cost<BC>(p, s, x - nblk[b]);
+        if (rem < from + cost) {
+          plan_start[0] = h;
+          plan_start[1] = b;
+          plan_start[2] = x - nblk[b];
+          plan_at[0] = h * head + from;
+          break;
+        }
+        from += cost;
+      }
+    }
+    if (tid == 0) {
+      plan_start[3] = static_cast<int>(blockIdx.x) < ranges && total > 0 ? ranges : 0;
+      plan_at[1] = total;
+      p.begun[blockIdx.x].tiles = 0;
+    }
+    __syncthreads();
+    // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
+    for (int i = tid; i < 2 * C::Q_BYTES / 16; i += C::NTHREADS)
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int ranges = plan_start[3];
+
+  if (ranges == 0) {
+    // nothing to do here
+  } else if (warp == C::LOAD_WARP || warp == C::LOADV_WARP) {
+    // ------------------------------------------------------------ loads
+    const bool do_k = warp == C::LOAD_WARP, do_v = warp == C::LOADV_WARP;
+    int n = 0, nq = 0, n_tail = 0;  // tiles, query blocks and edge tiles of values so far
+    int nk = 0, nv = 0;             // tiles whose copies were issued
+    const auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.err, where));
+    };
+    // the walk through the units (LOAD_WARP): lane i knows sequence base + i
+    const long long total = plan_at[1];
+    const long long w0 = range_begin(total, blockIdx.x, ranges), w1 = range_begin(total, blockIdx.x + 1, ranges);
+    long long at = plan_at[0];
+    int h = plan_start[0], b = plan_start[1], blk = plan_start[2], base = -1;
+    Seq mine{};
+    Unit u;
+    bool ok = true;
+    for (int iu = 0; ok; ++iu) {
+      const int slot = iu % C::UNITS;
+      if (do_k) {
+        // the next unit with work in this range
+        u.kind = UNIT_NONE;
+        while (at < w1) {
+          if (base < 0 || b < base || b >= base + 32) {
+            base = b;
+            mine = load_seq(p, base + lane);
+          }
+          Seq s;
+          s.q0 = __shfl_sync(0xffffffffu, mine.q0, b - base);
+          s.n = __shfl_sync(0xffffffffu, mine.n, b - base);
+          s.pos0 = __shfl_sync(0xffffffffu, mine.pos0, b - base);
+          s.bad = __shfl_sync(0xffffffffu, static_cast<int>(mine.bad), b - base);
+          const int first = blk * 2 * p.tile_tokens;
+          if (first >= s.n) {  // past the sequence's last block
+            blk = 0;
+            if (++b >= p.B) {
+              b = 0;
+              ++h;
+            }
+            continue;
+          }
+          const int cost = block_cost<BC>(p, s, blk);
+          const long long start = at;
+          at += cost;
+          u.h = h;
+          u.b = b;
+          u.q0 = s.q0 + first;
+          u.ntok = min(2 * p.tile_tokens, s.n - first);
+          u.pos0 = s.pos0 + first;
+          ++blk;
+          u.bad_page = u.set_aside = 0;
+          u.jb = u.je = u.ns = u.w0 = u.lo = u.hi = 0;
+          if (s.bad) {
+            if (start < w0) continue;  // the range that it begins in has it
+            u.kind = UNIT_BAD;
+            break;
+          }
+          const Span sp = span_of<BC>(p, u.pos0, u.ntok);
+          const int each = u.ntok > p.tile_tokens ? COST_TWO : COST_ONE;
+          u.jb = cut(w0, start, sp.tiles, each);
+          u.je = cut(w1, start, sp.tiles, each);
+          if (u.jb >= u.je) continue;
+          u.ns = sp.ns;
+          u.w0 = sp.w0;
+          u.lo = sp.lo;
+          u.hi = sp.hi;
+          u.kind = u.jb > 0 ? UNIT_CONTINUED : u.je < sp.tiles ? UNIT_BEGUN : UNIT_WHOLE;
+          if (u.kind == UNIT_BEGUN && lane == 0)
+            p.begun[blockIdx.x] = Begun{start, total, ranges, sp.tiles, each, u.h, u.q0, u.ntok};
+          break;
+        }
+        if (iu >= C::UNITS) ok = wait_all(bar_ue(slot), (iu / C::UNITS - 1) & 1, W_DESC_FREE);
+        if (!ok) break;
+        if (lane == 0) {
+          units[slot] = u;
+          mbar_arrive(bar_uf(slot));
+        }
+        __syncwarp();
+      } else {
+        ok = wait_all(bar_uf(slot), (iu / C::UNITS) & 1, W_DESC);
+        if (!ok) break;
+        u = units[slot];
+      }
+      if (u.kind == UNIT_NONE) break;
+      const int tiles = u.je - u.jb;
+      if (tiles > 0) {
+        // keys that some row of the block sees; of those, keys below `all` and from `edge` on are seen by every row
+        const int sinks = p.window > 0 ? min(p.sinks, u.hi) : 0;
+        const int last_lo = p.window > 0 ? max(0, u.pos0 + u.ntok - p.window) : 0;
+        const auto used = [&](int key) { return key < u.hi && (key >= u.lo || key < sinks); };
+        const auto note_bad = [&]() {
+          *reinterpret_cast<volatile int*>(&units[slot].bad_page) = 1;
+          record_bad_index(p.err, W_PAGE);
+        };
+        const int* const table = p.table + u.b * p.table_stride;
+        // Sets values aside and zeroes those that no row sees, in the tile's rows that not every row of Q sees.
+        const auto clean = [&](uint32_t dv, int key0) {
+          const auto rows = [&](int r0, int r1) {
+            for (int i = r0 * C::NCH * 8 + lane; i < r1 * C::NCH * 8; i += 32) {
+              const int r = i / (C::NCH * 8), pc = i % (C::NCH * 8), key = key0 + r;
+              uint4* const at16 = reinterpret_cast<uint4*>(smem + (dv - sbase) + pc / 8 * C::KV_CH_BYTES + r * 128 + pc % 8 * 16);
+              if (!used(key)) {
+                *at16 = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 w = *at16;
+              uint32_t* const ws = &w.x;
+              const uint32_t f0 = not_finite(w.x), f1 = not_finite(w.y), f2 = not_finite(w.z), f3 = not_finite(w.w);
+              if (f0 | f1 | f2 | f3) {
+                const uint32_t f[4] = {f0, f1, f2, f3};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  ws[e] &= ~(((f[e] & 0x8000u) ? 0xFFFFu : 0u) | ((f[e] & 0x80000000u) ? 0xFFFF0000u : 0u));
+                *at16 = w;
+                *reinterpret_cast<volatile int*>(&units[slot].set_aside) = 1;
+              }
+            }
+          };
+          rows(0, min(BC, max(0, last_lo - key0)));
+          rows(min(BC, max(0, u.pos0 + 1 - key0)), BC);
+        };
+        const auto has_edge = [&](int key0) {
+          return key0 + BC > u.pos0 + 1 || (key0 < last_lo && key0 + BC > sinks);
+        };
+        // TMA: lane i copies the i-th box of a tile, from the page that it looked up a tile ahead; boxes that no row sees and
+        // boxes of a bad page are read past the last page: zeros.
+        const int boxes = C::GATHER ? 0 : BC / p.box_rows;
+        const auto page_of = [&](int j) {
+          if (lane >= boxes || j >= u.je) return p.num_pages;
+          const int key = key_tile(u, j) * BC + lane * p.box_rows;
+          if (key >= u.hi || (key + p.box_rows <= u.lo && key >= sinks)) return p.num_pages;
+          const int pg = table[p.by_page.div(key)];
+          if (pg >= 0 && pg < p.num_pages) return pg;
+          note_bad();
+          return p.num_pages;
+        };
+        const auto copy_boxes = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, int key0, int page) {
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(bar, C::KV_BYTES);
+          __syncwarp();
+          if (lane < boxes) {
+            const int key = key0 + lane * p.box_rows, row = key - p.by_page.div(key) * p.page_size;
+#pragma unroll
+            for (int c = 0; c < C::NCH; ++c)
+              tma_load_4d(dst + c * C::KV_CH_BYTES + lane * p.box_rows * 128, tm, bar, c * 64, p.heads_inner ? u.h : row,
+                          p.heads_inner ? row : u.h, page);
+          }
+        };
+        // Single rows: lane i knows where rows i, i + 32, ... of the tile are (-1: zeros).
+        const auto copy_rows = [&](const __nv_bfloat16* cache, uint32_t dst, int key0) {
+          long long where[BC / 32];
+#pragma unroll
+          for (int i = 0; i < BC / 32; ++i) {
+            const int key = key0 + i * 32 + lane;
+            where[i] = -1;
+            if (used(key)) {
+              const int pi = p.by_page.div(key), pg = table[pi];
+              if (pg >= 0 && pg < p.num_pages)
+                where[i] = pg * p.c_page + u.h * p.c_head + (key - pi * p.page_size) * p.c_row;
+              else
+                note_bad();
+            }
+          }
+          constexpr int PIECES = D / 8, RP = 32 / PIECES;
+          const int pc = lane % PIECES;
+#pragma unroll
+          for (int i = 0; i < BC / RP; ++i) {
+            const int r = i * RP + lane / PIECES;
+            const long long from = __shfl_sync(0xffffffffu, where[i * RP / 32], r & 31);
+            cp_async16(dst + pc / 8 * C::KV_CH_BYTES + r * 128 + ((pc % 8 ^ (r & 7)) << 4), cache + (from < 0 ? 0 : from) + pc * 8,
+                       from < 0 ? 0 : 16);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+        };
+        int page = page_of(u.jb);
+        for (int j = u.jb; ok && j < u.je; ++j, ++n) {
+          const int s = n % STAGES;
+          const uint32_t ph = ((n / STAGES) & 1) ^ 1;
+          const int key0 = key_tile(u, j) * BC;
+          const int next_page = page_of(j + 1);
+          if (do_k) {
+            ok = wait_all(bar_ke(s), ph, W_KE);
+            if (!ok) break;
+            const uint32_t dk = sbase + C::OFF_K + s * C::KV_BYTES;
+            if constexpr (C::GATHER) {
+              copy_rows(p.k, dk, key0);
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_kf(s));
+            } else {
+              copy_boxes(&tm_k, dk, bar_kf(s), key0, page);
+              nk = n + 1;
+            }
+            if (j == u.jb) {  // the block's queries, once the last block's products have read theirs
+              if (nq > 0) ok = wait_all(bar_qe, (nq - 1) & 1, W_QFREE);
+              if (!ok) break;
+              if (lane == 0) {
+                const int tiles_q = u.ntok > p.tile_tokens ? 2 : 1;
+                mbar_expect_tx(bar_q, tiles_q * C::NCH * p.G * p.tile_tokens * 128);
+                for (int t = 0; t < tiles_q; ++t)
+#pragma unroll
+                  for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(sbase + C::OFF_Q + t * C::Q_BYTES + c * C::Q_CH_BYTES, &tm_q, bar_q, c * 64, u.h * p.G,
+                                u.q0 + t * p.tile_tokens);
+              }
+              ++nq;
+            }
+          }
+          if (do_v) {
+            ok = wait_all(bar_ve(s), ph, W_VE);
+            if (!ok) break;
+            const uint32_t dv = sbase + C::OFF_V + s * C::KV_BYTES;
+            const bool edge = has_edge(key0);
+            if constexpr (C::GATHER) {
+              copy_rows(p.v, dv, key0);
+              __syncwarp();  // other lanes' copies
+              if (edge) clean(dv, key0);
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_vf(s));
+            } else if (!edge) {
+              copy_boxes(&tm_v, dv, bar_vf(s), key0, page);
+              nv = n + 1;
+            } else {
+              copy_boxes(&tm_v, dv, bar_tail, key0, page);
+              ok = wait_all(bar_tail, n_tail & 1, W_TAIL);
+              ++n_tail;
+              if (!ok) break;
+              clean(dv, key0);
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_vf(s));
+              nv = n + 1;
+            }
+          }
+          page = next_page;
+        }
+      }
+      if (!do_k && lane == 0) mbar_arrive(bar_ue(slot));
+    }
+    if (!C::GATHER || do_k) {
+      if (lane == 0) {  // every copy issued must land before the CTA exits
+        for (int s = 0; !C::GATHER && s < STAGES; ++s) {
+          const int nks = nk > s ? (nk - 1 - s) / STAGES + 1 : 0, nvs = nv > s ? (nv - 1 - s) / STAGES + 1 : 0;
+          if (do_k && nks > 0) mbar_wait_drain(bar_kf(s), (nks - 1) & 1, p.err, W_DRAIN_K);
+          if (do_v && nvs > 0) mbar_wait_drain(bar_vf(s), (nvs - 1) & 1, p.err, W_DRAIN_V);
+        }
+        if (do_v && n_tail > 0) mbar_wait_drain(bar_tail, (n_tail - 1) & 1, p.err, W_DRAIN_V);
+        if (do_k && nq > 0) mbar_wait_drain(bar_q, (nq - 1) & 1, p.err, W_DRAIN_K);
+      }
+      __syncwarp();
+    }
+  } else if (warp == C::MMA_WARP) {
+    // ------------------------------------------------------------ products (one elected lane issues)
+    const auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.err, where));
+    };
+    constexpr uint32_t idesc_qk = make_idesc(1, C::BR, BC, 0, 0), idesc_pv = make_idesc(1, C::BR, D, 0, 1);
+    const uint64_t dq0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024), dk0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(sbase + C::OFF_V, C::KV_CH_BYTES, 1024);
+    const auto issue_qk = [&](int t, int s) {
+      const uint64_t qa = dq0 + static_cast<uint64_t>((t * C::Q_BYTES) >> 4);
+      const uint64_t kb = dk0 + static_cast<uint64_t>((s * C::KV_BYTES) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int e = kk * 16;
+        mma_ss<0>(tmem + t * BC, qa + ((e / 64 * C::Q_CH_BYTES + e % 64 * 2) >> 4), kb + ((e / 64 * C::KV_CH_BYTES + e % 64 * 2) >> 4),
+                  idesc_qk, kk > 0);
+      }
+    };
+    const auto issue_pv = [&](int t, int s, bool acc, int kk0, int kk1) {
+      const uint64_t vb = dv0 + static_cast<uint64_t>((s * C::KV_BYTES) >> 4);
+#pragma unroll
+      for (int kk = kk0; kk < kk1; ++kk)
+        mma_ts<0>(tmem + C::O_COL0 + t * D, tmem + t * BC + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv,
+                  (acc || kk > 0) ? 1u : 0u);
+    };
+    int n = 0, nq = 0, done[2] = {0, 0};
+    bool ok = true;
+    for (int iu = 0; ok; ++iu) {
+      const int slot = iu % C::UNITS;
+      ok = wait_all(bar_uf(slot), (iu / C::UNITS) & 1, W_DESC);
+      if (!ok) break;
+      const Unit u = units[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ue(slot));
+      if (u.kind == UNIT_NONE) break;
+      const int T = u.je - u.jb;
+      if (T == 0) continue;
+      const int st[2] = {steps_of<BC>(u, 0, p.tile_tokens), steps_of<BC>(u, 1, p.tile_tokens)};
+      ok = wait_all(bar_q, nq & 1, W_Q) && wait_all(bar_kf(n % STAGES), (n / STAGES) & 1, W_KF);
+      ++nq;
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (st[t] > 0) {
+            issue_qk(t, n % STAGES);
+            mma_commit(bar_sf(t));
+          }
+        mma_commit(bar_ke(n % STAGES));
+        if (T == 1) mma_commit(bar_qe);
+      }
+      __syncwarp();
+      for (int j = 0; ok && j < T; ++j, ++n) {
+        const int s = n % STAGES, n1 = n + 1, s1 = n1 % STAGES;
+        ok = wait_all(bar_vf(s), (n / STAGES) & 1, W_VF);
+        if (ok && j + 1 < T) ok = wait_all(bar_kf(s1), (n1 / STAGES) & 1, W_KF);
+        if (!ok) break;
+        const int last = st[1] > j ? 1 : 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (st[t] <= j) continue;
+          if constexpr (C::PV2) {
+            ok = ok && wait_all(bar_ph(t), done[t] & 1, W_PF);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) issue_pv(t, s, j > 0, 0, BC / 32);
+            __syncwarp();
+          }
+          ok = ok && wait_all(bar_pf(t), done[t] & 1, W_PF);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(t, s, C::PV2 || j > 0, C::PV2 ? BC / 32 : 0, BC / 16);
+            if (t == last) mma_commit(bar_ve(s));
+            if (j + 1 < st[t]) {
+              issue_qk(t, s1);
+              mma_commit(bar_sf(t));
+            } else {
+              mma_commit(bar_od(t));
+            }
+            if (t == last && j + 1 < T) {
+              mma_commit(bar_ke(s1));
+              if (j + 2 == T) mma_commit(bar_qe);
+            }
+          }
+          __syncwarp();
+          ++done[t];
+        }
+      }
+    }
+    // every product issued above completes before tensor memory is freed
+    if (elect_one()) mma_commit(bar_drain);
+    __syncwarp();
+    mbar_wait_drain(bar_drain, 0, p.err, W_DRAIN_MMA);
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups, a thread a row
+    const int t = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_base + t * BC, tO = tmem + lane_base + C::O_COL0 + t * D;
+    const int my_tok = p.by_g.div(row), g = row - my_tok * p.G;
+    const float c = p.c;
+    const uint64_t c2 = f2_pack(c, c);
+    const uint32_t hidden = __float_as_uint(c >= 0.f ? -INFINITY : INFINITY);  // a score that is not seen, before scaling
+    int done = 0, n_od = 0;
+    bool ok = true;
+    const auto rescale = [&](float alpha) {
+      const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t orr[32];
+        tmem_ld32(tO + cc * 32, orr);
+        tmem_wait_ld();
+        reg_fence(orr);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t v = f2_mul(f2_pack(__uint_as_float(orr[e]), __uint_as_float(orr[e + 1])), a2);
+          f2_unpack(v, orr[e], orr[e + 1]);
+        }
+        tmem_st32(tO + cc * 32, orr);
+      }
+    };
+    const auto hand_over = [&](uint32_t bar) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    for (int iu = 0; ok; ++iu) {
+      const int slot = iu % C::UNITS;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_uf(slot), (iu / C::UNITS) & 1, abort_flag, p.err, W_DESC));
+      if (!ok) break;
+      const volatile Unit& uv = units[slot];
+      const int kind = uv.kind;
+      if (kind == UNIT_NONE) break;
+      const int h = uv.h, q0 = uv.q0, ntok = uv.ntok, pos0 = uv.pos0, jb = uv.jb;
+      const int tok = t * p.tile_tokens + my_tok;
+      const bool real = my_tok < p.tile_tokens && tok < ntok;
+      const int pos = pos0 + min(tok, ntok - 1);
+      int steps;
+      {
+        Unit u;
+        u.kind = kind;
+        u.ntok = ntok;
+        u.pos0 = pos0;
+        u.jb = jb;
+        u.je = uv.je;
+        u.ns = uv.ns;
+        u.w0 = uv.w0;
+        steps = steps_of<BC>(u, t, p.tile_tokens);
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < steps; ++j, ++done) {
+        const bool okw = __all_sync(0xffffffffu, mbar_wait(bar_sf(t), done & 1, abort_flag, p.err, W_SF));
+        if (!okw) {
+          ok = false;
+          break;
+        }
+        const int jj = jb + j, ns = uv.ns;
+        const int key0 = (jj < ns ? jj : uv.w0 + jj - ns) * BC;
+        // columns valid > e, and from `first` on or among the sinks
+        const int valid = pos + 1 - key0;
+        const int first = p.window > 0 ? pos - p.window + 1 - key0 : 0, sink = p.sinks - key0;
+        const bool full = __all_sync(0xffffffffu, valid >= BC && (first <= 0 || sink >= BC));
+        const bool started = __all_sync(0xffffffffu, m_ref != -INFINITY);
+        tc_fence_after();
+        if constexpr (C::PV2) {
+          uint32_t sr[BC / 32][32];
+#pragma unroll
+          for (int i = 0; i < BC / 32; ++i) tmem_ld32(tS + i * 32, sr[i]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < BC / 32; ++i) reg_fence(sr[i]);
+          constexpr int HC = BC / 2, HP = BC / 128;  // columns and packed 32-column chunks of half of P
+          auto& sr_a = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[0]);
+          auto& sr_b = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[HC / 32]);
+          float r0, r1, r2, r3;
+          if (full && started) {
+            // The first half's exponentials against the reference maximum, with no row maximum in front of them: its sum
+            // and the second half's maximum show that none moved past m_ref + tau (FwdCfg::PV2).
+            const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+            uint32_t pk[HP][32];
+            uint64_t rs[2] = {0ull, 0ull};
+            softmax_p_bf16<HC, false>(sr_a, pk, c2, negm2, HC, rs);
+            const float m_b = (c >= 0.f ? row_extreme<HC, true>(sr_b) : row_extreme<HC, false>(sr_b)) * c;
+            f2_unpack_f(rs[0], r0, r1);
+            f2_unpack_f(rs[1], r2, r3);
+            const float l_a = (r0 + r1) + (r2 + r3);
+            if (__all_sync(0xffffffffu, l_a <= p.p_lim && m_b <= m_ref + p.tau)) {
+#pragma unroll
+              for (int i = 0; i < HP; ++i) tmem_st32(tS + i * 32, pk[i]);
+              hand_over(bar_ph(t));
+              uint64_t rs_b[2] = {0ull, 0ull};
+              softmax_p_bf16<HC, false>(sr_b, pk, c2, negm2, HC, rs_b);
+#pragma unroll
+              for (int i = 0; i < HP; ++i) tmem_st32(tS + (HP + i) * 32, pk[i]);
+              hand_over(bar_pf(t));
+              f2_unpack_f(rs_b[0], r0, r1);
+              f2_unpack_f(rs_b[1], r2, r3);
+              l += l_a + ((r0 + r1) + (r2 + r3));
+              continue;
+            }
+          }
+          if (!full) {
+#pragma unroll
+            for (int i = 0; i < BC / 32; ++i) {
+              const uint32_t vis = low_bits(valid - 32 * i) & (~low_bits(first - 32 * i) | low_bits(sink - 32 * i));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(vis >> e & 1u)) sr[i][e] = hidden;
+            }
+          }
+          const float m_new = fmaxf(m_ref, (c >= 0.f ? row_extreme<BC, true>(sr) : row_extreme<BC, false>(sr)) * c);
+          const bool need = m_new > m_ref + p.tau;  // always true on the first tile that a row sees
+          float alpha = 1.f;
+          if (need) {
+            alpha = ex2_approx(m_ref - m_new);  // 0 the first time
+            m_ref = m_new;
+          }
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen nothing: 2^(-inf - 0) = 0
+          const uint64_t negm2 = f2_pack(-m_use, -m_use);
+          uint64_t rs[2] = {0ull, 0ull};
+          uint32_t pk[HP][32];
+          softmax_p_bf16<HC, false>(sr_a, pk, c2, negm2, HC, rs);
+#pragma unroll
+          for (int i = 0; i < HP; ++i) tmem_st32(tS + i * 32, pk[i]);
+          if (j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
+          hand_over(bar_ph(t));
+          softmax_p_bf16<HC, false>(sr_b, pk, c2, negm2, HC, rs);
+#pragma unroll
+          for (int i = 0; i < HP; ++i) tmem_st32(tS + (HP + i) * 32, pk[i]);
+          hand_over(bar_pf(t));
+          f2_unpack_f(rs[0], r0, r1);
+          f2_unpack_f(rs[1], r2, r3);
+          l = l * alpha + ((r0 + r1) + (r2 + r3));
+        } else {
+          // 64-column tiles.  Once every row has a reference maximum, P is computed against it while the scores are still
+          // arriving; a row sum of at most 2^tau shows that none moved past it (fa_fwd_kernel.cuh, `fast`).
+          if (full && started) {
+            const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+            uint32_t sc[2][32], pk[32];
+            uint64_t rs[2] = {0ull, 0ull};
+            tmem_ld32(tS, sc[0]);
+            tmem_wait_ld();
+            reg_fence(sc[0]);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              if (cc == 0) tmem_ld32(tS + 32, sc[1]);
+#pragma unroll
+              for (int qc = 0; qc < 16; ++qc) {
+                const uint64_t x = f2_fma(f2_pack(__uint_as_float(sc[cc][2 * qc]), __uint_as_float(sc[cc][2 * qc + 1])), c2, negm2);
+                float x0, x1;
+                f2_unpack_f(x, x0, x1);
+                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                rs[qc & 1] = f2_add(rs[qc & 1], f2_pack(p0, p1));
+                pk[cc * 16 + qc] = pack_bf16x2(p0, p1);
+              }
+              if (cc == 0) {
+                tmem_wait_ld();
+                reg_fence(sc[1]);
+              }
+            }
+            float r0, r1, r2, r3;
+            f2_unpack_f(rs[0], r0, r1);
+            f2_unpack_f(rs[1], r2, r3);
+            const float l_tile = (r0 + r1) + (r2 + r3);
+            if (__all_sync(0xffffffffu, l_tile <= p.p_lim)) {
+              tmem_st32(tS, pk);
+              hand_over(bar_pf(t));
+              l += l_tile;
+              continue;
+            }
+          }
+          // the general path, a chunk of 32 columns at a time: the maximum, then P
+          uint32_t sr[1][32];
+          const auto chunk = [&](int cc) {
+            tmem_ld32(tS + cc * 32, sr[0]);
+            tmem_wait_ld();
+            reg_fence(sr[0]);
+            if (!full) {
+              const uint32_t vis = low_bits(valid - 32 * cc) & (~low_bits(first - 32 * cc) | low_bits(sink - 32 * cc));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(vis >> e & 1u)) sr[0][e] = hidden;
+            }
+          };
+          float m_new = m_ref;
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            chunk(cc);
+            m_new = fmaxf(m_new, (c >= 0.f ? row_extreme<32, true>(sr) : row_extreme<32, false>(sr)) * c);
+          }
+          const bool need = m_new > m_ref + p.tau;
+          float alpha = 1.f;
+          if (need) {
+            alpha = ex2_approx(m_ref - m_new);
+            m_ref = m_new;
+          }
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t negm2 = f2_pack(-m_use, -m_use);
+          uint64_t rs[2] = {0ull, 0ull};
+          // chunk cc's 16 packed columns go over columns 16 cc .. 16 cc + 15 of S, which hold chunk 0 (already read)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            chunk(cc);
+            uint32_t pk[32];
+#pragma unroll
+            for (int qc = 0; qc < 16; ++qc) {
+              const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[0][2 * qc]), __uint_as_float(sr[0][2 * qc + 1])), c2, negm2);
+              float x0, x1;
+              f2_unpack_f(x, x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              rs[qc & 1] = f2_add(rs[qc & 1], f2_pack(p0, p1));
+              pk[qc] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16_lo(tS + cc * 16, pk);
+          }
+          if (j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
+          hand_over(bar_pf(t));
+          float r0, r1, r2, r3;
+          f2_unpack_f(rs[0], r0, r1);
+          f2_unpack_f(rs[1], r2, r3);
+          l = l * alpha + ((r0 + r1) + (r2 + r3));
+        }
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      if (steps > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_od(t), n_od & 1, abort_flag, p.err, W_OD));
+        ++n_od;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (uv.bad_page || kind == UNIT_BAD) l = __int_as_float(0x7fc00000);
+      const bool aside = uv.set_aside != 0;
+      // Adds the values set aside (infinities, NaN) that this row sees to columns c0 .. c0 + 31 of its O.
+      const auto add_aside = [&](uint32_t (&orr)[32], int c0) {
+        if (!real) return;
+        const int ns = uv.ns, wt = uv.w0, je = uv.je, hi = uv.hi, b = uv.b;
+        const int last_lo = p.window > 0 ? max(0, pos0 + ntok - p.window) : 0;
+        for (int jj = jb; jj < je; ++jj) {
+          const int key0 = (jj < ns ? jj : wt + jj - ns) * BC;
+          if (key0 + BC <= pos0 + 1 && key0 >= last_lo) continue;
+          for (int key = key0; key < min(key0 + BC, hi); ++key) {
+            if (key <= pos0 && key >= last_lo) continue;  // every row sees it: left in the products
+            if (key > pos || (p.window > 0 && key <= pos - p.window && key >= p.sinks)) continue;
+            const int pi = p.by_page.div(key), pg = p.table[b * p.table_stride + pi];
+            if (pg < 0 || pg >= p.num_pages) continue;
+            const __nv_bfloat16* const v = p.v + pg * p.c_page + h * p.c_head + (key - pi * p.page_size) * p.c_row + c0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = __bfloat162float(v[e]);
+              if (!(fabsf(x) < INFINITY)) orr[e] = __float_as_uint(__uint_as_float(orr[e]) + x);
+            }
+          }
+        }
+      };
+      const bool any_rows = t * p.tile_tokens < ntok;
+      if (!any_rows) {
+        // a block of one tile
+      } else if (kind == UNIT_WHOLE || kind == UNIT_BAD) {
+        const float inv_l = 1.f / l;
+        const size_t out = static_cast<size_t>(q0 + tok) * p.H + h * p.G + g;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t orr[32];
+          tmem_ld32(tO + cc * 32, orr);
+          tmem_wait_ld();
+          reg_fence(orr);
+          if (aside) add_aside(orr, cc * 32);
+          if (real) {
+            uint4* const dst = reinterpret_cast<uint4*>(p.o + out * D + cc * 32);
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(orr[8 * v4 + 0]) * inv_l, __uint_as_float(orr[8 * v4 + 1]) * inv_l);
+              w.y = pack_bf16x2(__uint_as_float(orr[8 * v4 + 2]) * inv_l, __uint_as_float(orr[8 * v4 + 3]) * inv_l);
+              w.z = pack_bf16x2(__uint_as_float(orr[8 * v4 + 4]) * inv_l, __uint_as_float(orr[8 * v4 + 5]) * inv_l);
+              w.w = pack_bf16x2(__uint_as_float(orr[8 * v4 + 6]) * inv_l, __uint_as_float(orr[8 * v4 + 7]) * inv_l);
+              dst[v4] = w;
+            }
+          }
+        }
+        if (p.lse != nullptr && real) p.lse[out] = (m_ref + log2f(l)) * 0.6931471805599453f;
+      } else {
+        // Partial state: 16-byte pieces of the rows side by side, so that a warp's stores are whole lines.
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (kind == UNIT_BEGUN)) * p.part_tiles + t;
+        float4* const po = p.part_o + part * (D / 4) * p.part_rows + row;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t orr[32];
+          if (steps > 0) {
+            tmem_ld32(tO + cc * 32, orr);
+            tmem_wait_ld();
+            reg_fence(orr);
+            if (aside) add_aside(orr, cc * 32);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) orr[e] = 0;
+          }
+          if (real) {
+#pragma unroll
+            for (int v4 = 0; v4 < 8; ++v4)
+              po[static_cast<size_t>(cc * 8 + v4) * p.part_rows] =
+                  make_float4(__uint_as_float(orr[4 * v4]), __uint_as_float(orr[4 * v4 + 1]), __uint_as_float(orr[4 * v4 + 2]),
+                              __uint_as_float(orr[4 * v4 + 3]));
+          }
+        }
+        if (real) p.part_ml[part * p.part_rows + row] = make_float2(m_ref, l);
+      }
+      tc_fence_before();  // O has been read: the next unit's first P V comes behind this warp's next hand_over
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ue(slot));
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::LOAD_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the states of the units that CTA blockIdx.x begins and others finish, in the order of their keys:
+// O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  A block has 32 rows (a lane each) of one row tile, its warps a quarter of the
+// columns each.
 template <int D>
-__global__ void __launch_bounds__(128) fa_fwd_paged_kernel(const FwdPagedLaunch a) {
-  using bf = __nv_bfloat16;
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
-  const int t = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H), kvh = h / (a.H / a.Hkv);
-  if (t >= a.T) return;
-  int b = -1;
-  for (int i = lane; i < a.B; i += 32) {
-    const int from = a.cu[i], to = a.cu[i + 1];
-    if (from < 0 || from > to || to > a.T) {
-      if (w == 0) record_bad_index(a.err, W_FWD_PAGED);
-    } else if (from <= t && t < to) {
-      b = i;
+__global__ void __launch_bounds__(128) fa_fwd_paged_join_kernel(const ChunkParams p) {
+  griddep_wait();
+  const int c = blockIdx.x, t = blockIdx.y, row = blockIdx.z * 32 + (threadIdx.x & 31), quarter = threadIdx.x >> 5;
+  const Begun u = p.begun[c];
+  if (u.tiles == 0) return;
+  const int my_tok = p.by_g.div(row), g = row - my_tok * p.G, tok = t * p.tile_tokens + my_tok;
+  if (my_tok >= p.tile_tokens || tok >= u.ntok) return;
+  const size_t stride = static_cast<size_t>(2) * p.part_tiles;  // parts of a CTA
+  // CTA c' > c has a part where tiles lie between its cuts; the first one without ends the unit or is empty
+  float m = -INFINITY;
+  int end = c + 1;
+  {
+    size_t part = (static_cast<size_t>(c) * 2 + 1) * p.part_tiles + t;
+    m = p.part_ml[part * p.part_rows + row].x;
+    for (int from = cut(range_begin(u.total, c + 1, u.ranges), u.start, u.tiles, u.cost); from < u.tiles; ++end) {
+      const int to = cut(range_begin(u.total, end + 1, u.ranges), u.start, u.tiles, u.cost);
+      if (to > from) {
+        part = static_cast<size_t>(end) * stride + t;
+        m = fmaxf(m, p.part_ml[part * p.part_rows + row].x);
+      }
+      from = to;
     }
   }
-  b = __reduce_max_sync(0xffffffffu, b);
-  if (b < 0) return;
-  const int first = a.cu[b], n = a.cu[b + 1] - first;
-  const int len = a.lens[b], p = len - n + t - first;
-  bool bad = len < n || len > static_cast<long long>(a.max_pages) * a.page_size;
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  for (int i = 0; i < E; ++i)
-    q[i] = __bfloat162float(static_cast<const bf*>(a.q)[t * a.q_tok + h * a.q_head + lane * E + i]);
-  const int from = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  for (int j = 0; !bad && j <= p; ++j) {
-    if (j >= a.sinks && j < from) j = from;
-    const int pg = a.table[b * a.table_stride + j / a.page_size];
-    if (pg < 0 || pg >= a.num_pages) {
-      bad = true;
-      break;
+  constexpr int N4 = D / 16;  // 16-byte pieces of a quarter row
+  float4 o[N4];
+  float l = 0.f;
+#pragma unroll
+  for (int i = 0; i < N4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  int from = 0;
+  for (int i = c; i < end; ++i) {
+    const int to = cut(range_begin(u.total, i + 1, u.ranges), u.start, u.tiles, u.cost);
+    if (to > from) {
+      const size_t part = static_cast<size_t>(i) * stride + (i == c ? p.part_tiles : 0) + t;
+      const float2 ml = p.part_ml[part * p.part_rows + row];
+      const float w = ex2_approx(ml.x - m);
+      const float4* const po = p.part_o + (part * (D / 4) + quarter * N4) * p.part_rows + row;
+#pragma unroll
+      for (int k = 0; k < N4; ++k) {
+        const float4 x = po[static_cast<size_t>(k) * p.part_rows];
+        o[k].x = fmaf(w, x.x, o[k].x);
+        o[k].y = fmaf(w, x.y, o[k].y);
+        o[k].z = fmaf(w, x.z, o[k].z);
+        o[k].w = fmaf(w, x.w, o[k].w);
+      }
+      l = fmaf(w, ml.y, l);
     }
-    const long long row = pg * a.c_page + kvh * a.c_head + j % a.page_size * a.c_row + lane * E;
-    float s = 0.f;
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], __bfloat162float(static_cast<const bf*>(a.k_cache)[row + i]), s);
-    for (int i = 1; i < 32; i *= 2) s += __shfl_xor_sync(0xffffffffu, s, i);
-    s *= a.c;
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), e = exp2f(s - mn);
-    m = mn;
-    l = l * al + e;
-    for (int i = 0; i < E; ++i) o[i] = o[i] * al + e * __bfloat162float(static_cast<const bf*>(a.v_cache)[row + i]);
+    from = to;
   }
-  if (bad) {
-    record_bad_index(a.err, W_FWD_PAGED);
-    l = __int_as_float(0x7fc00000);
+  const float inv = 1.f / l;
+  const size_t out = static_cast<size_t>(u.q0 + tok) * p.H + u.h * p.G + g;
+  uint4* const dst = reinterpret_cast<uint4*>(p.o + out * D + quarter * (D / 4));
+#pragma unroll
+  for (int k = 0; k < N4 / 2; ++k) {
+    const float4 a = o[2 * k], b = o[2 * k + 1];
+    dst[k] = make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv), pack_bf16x2(b.x * inv, b.y * inv),
+                        pack_bf16x2(b.z * inv, b.w * inv));
   }
-  const long long out = (static_cast<long long>(t) * a.H + h);
-  for (int i = 0; i < E; ++i) static_cast<bf*>(a.o)[out * D + lane * E + i] = __float2bfloat16(o[i] / l);
-  if (a.lse && lane == 0) a.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+  if (p.lse != nullptr && quarter == 0) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// The workspace: states of cut units, and who begins them.
+struct Layout {
+  int rows, tiles;
+  size_t part_ml, begun, total;
+};
+Layout layout_of(int T, int H, int Hkv, int d, int sms) {
+  const int G = H / Hkv, tokens = FWD_PAGED_MAX_G / G;
+  Layout l;
+  l.tiles = T > tokens ? 2 : 1;
+  l.rows = T >= tokens ? 128 : (T * G + 31) / 32 * 32;
+  const size_t ctas = static_cast<size_t>(sms) * (d == 128 ? ChunkCfg<128, false>::MINB : ChunkCfg<64, false>::MINB);
+  const size_t states = ctas * 2 * l.tiles * l.rows;
+  l.part_ml = states * d * 4;
+  l.begun = l.part_ml + states * 8;
+  l.total = (l.begun + ctas * sizeof(Begun) + 15) / 16 * 16;
+  return l;
+}
+
+// Rows of the largest copy that stays in one page and starts on a swizzle boundary: a power of two that divides the page
+// size, at most the key tile.  Under 8 rows there is none.
+int box_rows_of(int page_size, int bc) {
+  const int r = page_size & -page_size;
+  return r > bc ? bc : r;
+}
+
+template <class C>
+cudaError_t launch_cfg(const FwdPagedLaunch& a) {
+  cudaError_t e = allow_shared_memory<fa_fwd_paged_kernel<C>>(C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const Layout l = layout_of(a.T, a.H, a.Hkv, a.d, a.sms);
+  ChunkParams p = {};
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.k = static_cast<const __nv_bfloat16*>(a.k_cache);
+  p.v = static_cast<const __nv_bfloat16*>(a.v_cache);
+  p.c_page = a.c_page;
+  p.c_head = a.c_head;
+  p.c_row = a.c_row;
+  p.table = a.table;
+  p.cu = a.cu;
+  p.lens = a.lens;
+  p.table_stride = a.table_stride;
+  p.err = a.err;
+  p.part_o = reinterpret_cast<float4*>(a.ws);
+  p.part_ml = reinterpret_cast<float2*>(a.ws + l.part_ml);
+  p.begun = reinterpret_cast<Begun*>(a.ws + l.begun);
+  p.G = a.H / a.Hkv;
+  p.by_g = FastDiv(static_cast<unsigned>(p.G));
+  p.by_page = FastDiv(static_cast<unsigned>(a.page_size));
+  p.T = a.T;
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.tile_tokens = C::BR / p.G;
+  p.part_rows = l.rows;
+  p.part_tiles = l.tiles;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.box_rows = box_rows_of(a.page_size, C::BC);
+  p.heads_inner = a.c_row > a.c_head;
+  p.window = a.window;
+  p.sinks = a.window > 0 ? a.sinks : 0;
+  p.c = a.c == 0.f ? 1e-30f : a.c;  // a hidden score (an infinity) times zero would be NaN
+  p.tau = kTau;
+  p.p_lim = exp2f(kTau);
+  CUtensorMap tq, tk = {}, tv = {};
+  e = encode_heads_map(&tq, a.q, a.d, a.H, a.T, a.q_head, a.q_tok, p.G, p.tile_tokens);
+  if (e == cudaSuccess && !C::GATHER)
+    e = encode_paged_map(&tk, a.k_cache, a.d, a.page_size, a.Hkv, a.num_pages, a.c_row, a.c_head, a.c_page, p.box_rows,
+                         p.heads_inner);
+  if (e == cudaSuccess && !C::GATHER)
+    e = encode_paged_map(&tv, a.v_cache, a.d, a.page_size, a.Hkv, a.num_pages, a.c_row, a.c_head, a.c_page, p.box_rows,
+                         p.heads_inner);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(a.sms * C::MINB);
+  e = launch_dependent(fa_fwd_paged_kernel<C>, dim3(grid), C::NTHREADS, C::SMEM_BYTES, a.stream, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa_fwd_paged_join_kernel<C::D>, dim3(grid, l.tiles, l.rows / 32), 128, 0, a.stream, p);
 }
 
 }  // namespace
 
-size_t fwd_paged_workspace(int, int, int, int, int, int) { return 0; }
+size_t fwd_paged_workspace(int T, int, int H, int Hkv, int d, int sms) { return layout_of(T, H, Hkv, d, sms).total; }
 
 cudaError_t launch_fwd_paged(const FwdPagedLaunch& a) {
-  const long long warps = static_cast<long long>(a.T) * a.H, grid = (warps + 3) / 4;
-  if (a.d == 64)
-    fa_fwd_paged_kernel<64><<<static_cast<unsigned>(grid), 128, 0, a.stream>>>(a);
-  else
-    fa_fwd_paged_kernel<128><<<static_cast<unsigned>(grid), 128, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  const bool gather = a.page_size % 8 != 0;
+  if (a.d == 64) return gather ? launch_cfg<ChunkCfg<64, true>>(a) : launch_cfg<ChunkCfg<64, false>>(a);
+  return gather ? launch_cfg<ChunkCfg<128, true>>(a) : launch_cfg<ChunkCfg<128, false>>(a);
 }
 
 }  // namespace fa

@@ -325,6 +325,10 @@ cudaError_t launch_prefix(const PagedLaunch& a, const PagedPlan& pl);
 cudaError_t encode_paged_map(CUtensorMap* map, const void* base, int d, int page_size, int Hkv, int num_pages,
                              long long c_row, long long c_head, long long c_page, int box_rows, int heads_inner);
 
+// 3-D tensor map over queries [T, H, d]: dims (d, H, T) with boxes of (64, G, tokens); 128-byte swizzle.
+cudaError_t encode_heads_map(CUtensorMap* map, const void* base, int d, int H, int T, long long head, long long token, int G,
+                             int tokens);
+
 struct BwdLaunch {
   // maps for the dK/dV kernel: K, V boxes (64 cols, kv_keys rows); Q, dO boxes (64 cols, kv_qrows rows)
   const CUtensorMap* tm_k_kv;

@@ -151,7 +151,6 @@ def test_bad_sequences_get_nan_and_others_nothing(cuda_device):
     for d in (64, 128):
         chunks = [(40, 6), (0, 5), (300, 20), (17, 1), (64, 3)]
         b = Batch(cuda_device, 4, 2, d, 16, chunks, width=25)
-        o0, l0 = b.run()
         b.len_t[1] = 3  # fewer keys than new tokens
         b.len_t[3] = 25 * 16 + 1  # more than the table holds
         b.table[2, 1] = b.kc.shape[0]
@@ -163,8 +162,7 @@ def test_bad_sequences_get_nan_and_others_nothing(cuda_device):
             rows = slice(first[i], first[i + 1])
             if i in (1, 2, 3):
                 assert torch.isnan(o[rows]).all() and torch.isnan(lse[rows]).all(), i
-            else:
-                assert torch.equal(o[rows], o0[rows]) and torch.equal(lse[rows], l0[rows]), i
+        b.check(o, lse, "beside bad ones", seqs={0, 4})  # the split of the work, and so the last bit, depends on all lengths
 
 
 @pytest.mark.parametrize("cu,good", [([0, 6, 40, 31], [0]), ([0, 6, 11, 32], [0, 1]), ([-1, 6, 11, 31], [1, 2]),
@@ -172,14 +170,15 @@ def test_bad_sequences_get_nan_and_others_nothing(cuda_device):
 def test_bad_offsets_write_nothing_of_their_sequence(cuda_device, cu, good):
     for d in (64, 128):
         b = Batch(cuda_device, 4, 2, d, 16, [(40, 6), (0, 5), (30, 20)])
-        want, _ = b.run()
         b.cu.copy_(torch.tensor(cu, dtype=torch.int32))
         o = torch.full((31, 4, d), 7.0, dtype=BF, device=cuda_device)
         b.run(o=o)
         torch.cuda.synchronize()
         assert fa.fa_check_device_error() == fa.FA_ERR_INVALID_ARG
         for i, rows in enumerate((slice(0, 6), slice(6, 11), slice(11, 31))):
-            assert torch.equal(o[rows], want[rows]) if i in good else (o[rows] == 7).all(), i
+            if i not in good:
+                assert (o[rows] == 7).all(), i
+        b.check(o, None, "beside bad ones", seqs=set(good))
 
 
 def test_no_tokens_and_no_sequences(cuda_device):
