@@ -50,7 +50,7 @@ struct ChunkCfg {
   static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
   static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_UNITS + UNITS * 64;
-  static constexpr int SMEM_BYTES = OFF_MISC + 512 + 1024;  // plan's scratch; slack to align the base to 1024
+  static constexpr int SMEM_BYTES = OFF_MISC + 144 + (32 * 11 + 2) * 8 + 1024;  // plan's scratch; slack to align the base to 1024
   static constexpr int O_COL0 = 2 * BC;          // TMEM: S_t at t * BC, O_t at O_COL0 + t * D
   static constexpr int TMEM_COLS = 2 * (BC + D);
   // The values have a load warp of their own at d = 128 (FwdCfg::SPLIT_LOADS); it comes free of registers there.
@@ -64,9 +64,12 @@ struct ChunkCfg {
   static_assert((FWD_PAGED_MAX_B + 1) * 4 <= OFF_BAR, "the plan's block counts lie where the tiles will");
 };
 
-// Costs of the dealing, in quarters of the time of a tile step with both row tiles.  A step of one row tile is bound by its
-// chain of products or its bytes; a unit's start and end take about as long as one and a half steps.
-constexpr int COST_TWO = 4, COST_ONE = 3, COST_UNIT = 6;
+// The dealing counts key tiles.  A unit's start and end take about as long as COST_UNIT of them, whether it has one row tile
+// or two (a step of one is bound by its chain of products and exponentials, or by the tile's bytes).
+constexpr int COST_UNIT = 4;
+// Cutting units costs their states, written and read again, and a start and an end more: so no unit is cut where the
+// longest range of whole units is at most this much longer than an even share.
+constexpr int COST_CUT = 6;
 
 struct ChunkParams {
   __nv_bfloat16* o;
@@ -82,7 +85,7 @@ struct ChunkParams {
   float4* part_o;    // [CTA][continued, begun][row tile][D / 4][part_rows]
   float2* part_ml;   // [CTA][continued, begun][row tile][part_rows]
   struct Begun* begun;  // [CTA]
-  FastDiv by_g, by_page;
+  FastDiv by_g, by_page, by_block;
   int T, B, H, Hkv, G, tile_tokens, part_rows, part_tiles;
   int num_pages, page_size, max_pages, box_rows, heads_inner;
   int window, sinks;
@@ -90,20 +93,23 @@ struct ChunkParams {
 };
 
 // A unit that a CTA begins and others finish: what the join has to know.
-struct Begun {
-  long long start, total;  // the unit's place in the costs of all units, and their sum
-  int ranges;              // CTAs that the sum is dealt to
-  int tiles, cost;         // its key tiles and what each costs; tiles 0: this CTA begins none
+struct __align__(16) Begun {
+  int parts;  // CTAs that have a part of it, this one and those behind it; 0: this CTA begins none
   int h, q0, ntok;
 };
 
-// Key tiles before place w of a unit that begins at `start`.
-__device__ __forceinline__ int cut(long long w, long long start, int tiles, int cost) {
-  if (w <= start) return 0;
-  const long long x = (w - start - COST_UNIT + cost - 1) / cost;
+// Key tiles before place w of a unit that begins at `start` and takes `extra` tiles' time besides its tiles.
+__device__ __forceinline__ int cut(long long w, long long start, int tiles, int extra) {
+  const long long x = w - start - extra;
   return x <= 0 ? 0 : x >= tiles ? tiles : static_cast<int>(x);
 }
-__device__ __forceinline__ long long range_begin(long long total, int c, int ranges) { return total * c / ranges; }
+__device__ __forceinline__ long long range_begin(long long total, int c, int ranges) { return static_cast<long long>(static_cast<unsigned long long>(total * c) / static_cast<unsigned>(ranges)); }
+// The last range that has tiles of it: the largest i with range_begin(i) before its last tile's place.  Every range between
+// has some: a range is a tile long at least.
+__device__ __forceinline__ int last_range(long long total, int ranges, long long start, int tiles, int extra) {
+  const long long w = start + extra + tiles - 1;
+  return static_cast<int>(min(ranges - 1LL, ((w + 1) * ranges - 1) / total));
+}
 
 // A sequence's new tokens, as far as its offsets and length make sense.
 struct Seq {
@@ -138,11 +144,12 @@ __device__ __forceinline__ Span span_of(const ChunkParams& p, int pos0, int ntok
   s.tiles = s.ns + (s.hi + BC - 1) / BC - s.w0;
   return s;
 }
+// Key tiles of a sequence's i-th block; a bad sequence's block counts as one.
 template <int BC>
-__device__ __forceinline__ int block_cost(const ChunkParams& p, const Seq& s, int i) {
-  if (s.bad) return COST_UNIT;
-  const int first = i * 2 * p.tile_tokens, ntok = min(2 * p.tile_tokens, s.n - first);
-  return COST_UNIT + (ntok > p.tile_tokens ? COST_TWO : COST_ONE) * span_of<BC>(p, s.pos0 + first, ntok).tiles;
+__device__ __forceinline__ int block_tiles(const ChunkParams& p, const Seq& s, int i) {
+  if (s.bad) return 1;
+  const int first = i * 2 * p.tile_tokens;
+  return span_of<BC>(p, s.pos0 + first, min(2 * p.tile_tokens, s.n - first)).tiles;
 }
 
 // A unit as the load warp announces it.
@@ -160,7 +167,7 @@ __device__ __forceinline__ int key_tile(const Unit& u, int j) { return j < u.ns 
 
 // Steps of row tile t in this part: it needs no tiles past its own last token.
 template <int BC>
-__device__ __forceinline__ int steps_of(const Unit& u, int t, int tile_tokens) {
+__device__ __forceinline__ int steps_of(const volatile Unit& u, int t, int tile_tokens) {
   if (t * tile_tokens >= u.ntok || u.kind >= UNIT_BAD) return 0;
   const int hi = u.pos0 + min((t + 1) * tile_tokens, u.ntok);
   return max(0, min(u.je, u.ns + (hi + BC - 1) / BC - u.w0) - u.jb);
@@ -172,27 +179,66 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 // Nonzero halves' sign bits where a bf16 is infinite or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
-template <int NT>
-__device__ __forceinline__ long long scan(long long v, long long* tmp, long long* total) {
+__device__ __forceinline__ int blocks_of(const ChunkParams& p, int n) { return n > 0 ? p.by_block.div(n - 1) + 1 : 0; }
+
+// The last sequence that begins at or before block x: those without blocks begin where the next one does.
+__device__ __forceinline__ int seq_of_block(const int* nblk, int B, int x) {
+  int b = 0, hi = B;
+  while (hi - b > 1) {
+    const int mid = (b + hi) >> 1;
+    if (nblk[mid] <= x) b = mid;
+    else hi = mid;
+  }
+  return b;
+}
+
+// Exclusive prefix sums of the threads' values, and their total.
+template <int NT, typename T>
+__device__ __forceinline__ T scan(T v, T* tmp, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  T x = v;
 #pragma unroll
   for (int i = 1; i < 32; i *= 2) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, i);
+    const T y = __shfl_up_sync(0xffffffffu, x, i);
     if (lane >= i) x += y;
   }
   __syncthreads();  // tmp may still be read
   if (lane == 31) tmp[warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
+  T before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    const long long t = tmp[w];
+    const T t = tmp[w];
     if (w < warp) before += t;
     all += t;
   }
   *total = all;
   return before + x - v;
+}
+
+// Adds the values set aside (infinities, NaN) of the keys that the token at `pos` sees to its row of O, whose element e lies at
+// o + e / run * stride + e % run: rare, so it reads back what the epilogue has just written.
+template <class C, typename T>
+__device__ __noinline__ void add_aside(const ChunkParams& p, const volatile Unit& u, int pos, T* o, int run, long long stride) {
+  const int last_lo = p.window > 0 ? max(0, u.pos0 + u.ntok - p.window) : 0;
+  for (int j = u.jb; j < u.je; ++j) {
+    const int key0 = (j < u.ns ? j : u.w0 + j - u.ns) * C::BC;
+    if (key0 + C::BC <= u.pos0 + 1 && key0 >= last_lo) continue;
+    for (int key = key0; key < min(key0 + C::BC, u.hi); ++key) {
+      if (key <= u.pos0 && key >= last_lo) continue;  // every row sees it: left in the products
+      if (key > pos || (p.window > 0 && key <= pos - p.window && key >= p.sinks)) continue;
+      const int pi = p.by_page.div(key), pg = p.table[u.b * p.table_stride + pi];
+      if (pg < 0 || pg >= p.num_pages) continue;
+      const __nv_bfloat16* const v = p.v + pg * p.c_page + u.h * p.c_head + (key - pi * p.page_size) * p.c_row;
+      for (int e = 0; e < C::D; ++e) {
+        const float x = __bfloat162float(v[e]);
+        if (!(fabsf(x) < INFINITY)) {
+          T& y = o[e / run * stride + e % run];
+          y = static_cast<T>(static_cast<float>(y) + x);
+        }
+      }
+    }
+  }
 }
 
 template <class C>
@@ -222,9 +268,10 @@ __global__ void __maxnreg__(C::MAXREG)
   Unit* const units = reinterpret_cast<Unit*>(smem + C::OFF_UNITS);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  int* const plan_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);                // h, b, block
-  long long* const plan_at = reinterpret_cast<long long*>(smem + C::OFF_MISC + 32);       // start, total
-  long long* const plan_tmp = reinterpret_cast<long long*>(smem + C::OFF_MISC + 64);
+  int* const plan_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);             // head, block, ranges, extra, whole, sequence
+  long long* const plan_at = reinterpret_cast<long long*>(smem + C::OFF_MISC + 32);   // start, total
+  int* const plan_tmp = reinterpret_cast<int*>(smem + C::OFF_MISC + 48);              // 12 64-bit numbers
+  long long* const plan_place = reinterpret_cast<long long*>(smem + C::OFF_MISC + 144);
 
   griddep_launch_dependents();
   if (tid == 0) {
@@ -265,84 +312,108 @@ __global__ void __maxnreg__(C::MAXREG)
 
   // ---------------------------------------------------------------- plan: this CTA's range of all units' tiles
   {
-    int* const nblk = reinterpret_cast<int*>(smem);  // blocks before each sequence, where the tiles will lie
-    const int tb = 2 * p.tile_tokens;
-    const int per = (p.B + C::NTHREADS - 1) / C::NTHREADS, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    long long blocks, mine = 0;
+    constexpr int NT = C::NTHREADS;
+    int* const nblk = reinterpret_cast<int*>(smem);          // blocks before each sequence, where the tiles will lie
+    const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int blocks, mine = 0;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(p, b);
       if (blockIdx.x == 0 && s.n == 0 && (p.cu[b] < 0 || p.cu[b] != p.cu[b + 1] || p.cu[b] > p.T))
         record_bad_index(p.err, W_OFFSETS);
       if (blockIdx.x == 0 && s.bad) record_bad_index(p.err, W_LENGTH);
-      mine += (s.n + tb - 1) / tb;
+      const int nb = blocks_of(p, s.n);
+      if (per > 1) nblk[b] = nb;
+      mine += nb;
     }
-    long long at = scan<C::NTHREADS>(mine, plan_tmp, &blocks);
-    for (int b = b0; b < b1; ++b) {
-      nblk[b] = static_cast<int>(at);
-      at += (load_seq(p, b).n + tb - 1) / tb;
+    int at = scan<NT>(mine, plan_tmp, &blocks);
+    if (per == 1) {
+      if (b0 < b1) nblk[b0] = at;
+    } else {
+      for (int b = b0; b < b1; ++b) {
+        const int nb = nblk[b];
+        nblk[b] = at;
+        at += nb;
+      }
     }
-    if (tid == 0) nblk[p.B] = static_cast<int>(blocks);
+    if (tid == 0) nblk[p.B] = blocks;
     __syncthreads();
-    const int n_blocks = static_cast<int>(blocks);
-    const int pb = (n_blocks + C::NTHREADS - 1) / C::NTHREADS, x0 = min(n_blocks, tid * pb), x1 = min(n_blocks, x0 + pb);
-    int b = 0;
-    if (x0 < x1) {  // the last sequence that begins at or before block x0: those without blocks begin where the next does
-      int hi = p.B;
-      while (hi - b > 1) {
-        const int mid = (b + hi) >> 1;
-        if (nblk[mid] <= x0) b = mid;
-        else hi = mid;
-      }
-    }
-    long long head = 0;
-    mine = 0;
-    {
-      int bb = b;
-      Seq s = load_seq(p, bb);
-      for (int x = x0; x < x1; ++x) {
-        while (x >= nblk[bb + 1]) s = load_seq(p, ++bb);
-        mine += block_cost<BC>(p, s, x - nblk[bb]);
-      }
-    }
-    const long long before = scan<C::NTHREADS>(mine, plan_tmp, &head);
-    const long long total = head * p.Hkv;
-    const long long least = COST_UNIT + COST_ONE;
-    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1LL, total / least)));
-    const long long w = range_begin(total, min(static_cast<int>(blockIdx.x), ranges), ranges);
-    const int h = head > 0 ? static_cast<int>(w / head) : 0;
-    const long long rem = w - h * head;
-    if (mine > 0 && before <= rem && rem < before + mine) {
+    // A thread's blocks x0 .. x1 - 1 (of each key/value head), their tiles, and the tiles before them
+    const int pb = (blocks + NT - 1) / NT, x0 = min(blocks, tid * pb), x1 = min(blocks, x0 + pb);
+    long long head;  // tiles of all blocks
+    long long tiles = 0;
+    if (x0 < x1) {
+      int b = seq_of_block(nblk, p.B, x0);
       Seq s = load_seq(p, b);
-      long long from = before;
       for (int x = x0; x < x1; ++x) {
         while (x >= nblk[b + 1]) s = load_seq(p, ++b);
-        const int cost = block_cost<BC>(p, s, x - nblk[b]);
-        if (rem < from + cost) {
-          plan_start[0] = h;
-          plan_start[1] = b;
-          plan_start[2] = x - nblk[b];
-          plan_at[0] = h * head + from;
-          break;
-        }
-        from += cost;
+        tiles += block_tiles<BC>(p, s, x - nblk[b]);
       }
     }
+    const long long before = scan<NT>(tiles, reinterpret_cast<long long*>(plan_tmp), &head);
+    // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
+    // each takes one, and starts and ends do not count.
+    const int extra = head * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : COST_UNIT;
+    long long* const place = plan_place;  // of each thread's first block in its head, and the head's end
+    place[tid] = before + static_cast<long long>(extra) * x0;
+    head += static_cast<long long>(extra) * blocks;
+    if (tid == 0) place[NT] = head;
+    const long long total = head * p.Hkv;
+    const int ranges = static_cast<int>(min(static_cast<long long>(min(static_cast<int>(gridDim.x), NT - 1)), total));
+    __syncthreads();
+    // Thread i looks up where range i begins: the unit that its first place lies in (or, with several blocks a thread, the
+    // first one of that thread's).  Where a thread has one block at most, it also knows how long the ranges are that take
+    // the units beginning in them, whole.
+    const int my_range = tid;
+    const bool whole_known = pb <= 1;
+    long long from = 0, w = 0;
+    int h = 0, lo = 0;
+    if (ranges > 0 && my_range <= ranges) {
+      w = range_begin(total, my_range, ranges);
+      h = static_cast<int>(static_cast<unsigned long long>(w) / static_cast<unsigned long long>(head));
+      const long long rem = w - h * head;
+      int hi = pb > 1 ? (blocks + pb - 1) / pb : blocks;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (place[mid] <= rem) lo = mid;
+        else hi = mid;
+      }
+      from = h * head + place[lo];
+    }
+    bool whole = false;
+    if (whole_known) {
+      const long long next = my_range < ranges ? (lo + 1 < blocks ? h * head + place[lo + 1] : (h + 1LL) * head) : 0;
+      const long long begin = w == from ? w : next;  // of the first unit that begins in the range or behind it
+      __syncthreads();
+      if (my_range <= ranges) place[my_range] = my_range == ranges ? total : begin;
+      __syncthreads();
+      const bool fits = my_range >= ranges || place[my_range + 1] - place[my_range] <= total / max(ranges, 1) + COST_CUT;
+      whole = __syncthreads_and(fits);
+    }
+    if (my_range == static_cast<int>(blockIdx.x) && my_range < ranges) {
+      plan_start[0] = h;
+      plan_start[1] = lo * max(pb, 1);  // block
+      plan_at[0] = from;
+    }
     if (tid == 0) {
-      plan_start[3] = static_cast<int>(blockIdx.x) < ranges && total > 0 ? ranges : 0;
+      plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
+      plan_start[3] = extra;
+      plan_start[4] = whole;
       plan_at[1] = total;
-      p.begun[blockIdx.x].tiles = 0;
+      p.begun[blockIdx.x].parts = 0;
     }
     __syncthreads();
-    // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
-    for (int i = tid; i < 2 * C::Q_BYTES / 16; i += C::NTHREADS)
-      *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);
+    if (warp == C::LOAD_WARP && lane == 0) plan_start[1] -= nblk[plan_start[5] = seq_of_block(nblk, p.B, plan_start[1])];
+    __syncthreads();
+    if (p.G * p.tile_tokens < C::BR) {  // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
+      for (int i = tid; i < 2 * C::Q_BYTES / 16; i += NT) *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);
+    }
     fence_proxy_async();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int ranges = plan_start[3];
+  const int ranges = plan_start[2];
 
   if (ranges == 0) {
     // nothing to do here
@@ -358,9 +429,13 @@ __global__ void __maxnreg__(C::MAXREG)
     const long long total = plan_at[1];
     const long long w0 = range_begin(total, blockIdx.x, ranges), w1 = range_begin(total, blockIdx.x + 1, ranges);
     long long at = plan_at[0];
-    int h = plan_start[0], b = plan_start[1], blk = plan_start[2], base = -1;
+    int h = plan_start[0], b = plan_start[5], blk = plan_start[1], base = -1;
+    const int extra = plan_start[3];
+    const bool whole = plan_start[4] != 0;
     Seq mine{};
     Unit u;
+    long long begun_at = 0;
+    int begun_tiles = 0;
     bool ok = true;
     for (int iu = 0; ok; ++iu) {
       const int slot = iu % C::UNITS;
@@ -386,9 +461,8 @@ __global__ void __maxnreg__(C::MAXREG)
             }
             continue;
           }
-          const int cost = block_cost<BC>(p, s, blk);
           const long long start = at;
-          at += cost;
+          at += block_tiles<BC>(p, s, blk) + extra;
           u.h = h;
           u.b = b;
           u.q0 = s.q0 + first;
@@ -397,23 +471,21 @@ __global__ void __maxnreg__(C::MAXREG)
           ++blk;
           u.bad_page = u.set_aside = 0;
           u.jb = u.je = u.ns = u.w0 = u.lo = u.hi = 0;
+          if ((whole || s.bad) && start < w0) continue;  // the range that it begins in has it
           if (s.bad) {
-            if (start < w0) continue;  // the range that it begins in has it
             u.kind = UNIT_BAD;
             break;
           }
           const Span sp = span_of<BC>(p, u.pos0, u.ntok);
-          const int each = u.ntok > p.tile_tokens ? COST_TWO : COST_ONE;
-          u.jb = cut(w0, start, sp.tiles, each);
-          u.je = cut(w1, start, sp.tiles, each);
-          if (u.jb >= u.je) continue;
+          u.jb = whole ? 0 : cut(w0, start, sp.tiles, extra);
+          u.je = whole ? sp.tiles : cut(w1, start, sp.tiles, extra);
+          if (u.jb >= u.je) continue;  // it lies before the range, or its first tile behind it
           u.ns = sp.ns;
           u.w0 = sp.w0;
           u.lo = sp.lo;
           u.hi = sp.hi;
           u.kind = u.jb > 0 ? UNIT_CONTINUED : u.je < sp.tiles ? UNIT_BEGUN : UNIT_WHOLE;
-          if (u.kind == UNIT_BEGUN && lane == 0)
-            p.begun[blockIdx.x] = Begun{start, total, ranges, sp.tiles, each, u.h, u.q0, u.ntok};
+          if (u.kind == UNIT_BEGUN) begun_at = start, begun_tiles = sp.tiles;
           break;
         }
         if (iu >= C::UNITS) ok = wait_all(bar_ue(slot), (iu / C::UNITS - 1) & 1, W_DESC_FREE);
@@ -585,6 +657,9 @@ __global__ void __maxnreg__(C::MAXREG)
         }
       }
       if (!do_k && lane == 0) mbar_arrive(bar_ue(slot));
+      if (do_k && u.kind == UNIT_BEGUN && lane == 0)
+        p.begun[blockIdx.x] = Begun{last_range(total, ranges, begun_at, begun_tiles, extra) - static_cast<int>(blockIdx.x) + 1, u.h,
+                                    u.q0, u.ntok};
     }
     if (!C::GATHER || do_k) {
       if (lane == 0) {  // every copy issued must land before the CTA exits
@@ -731,24 +806,10 @@ __global__ void __maxnreg__(C::MAXREG)
       ok = __all_sync(0xffffffffu, mbar_wait(bar_uf(slot), (iu / C::UNITS) & 1, abort_flag, p.err, W_DESC));
       if (!ok) break;
       const volatile Unit& uv = units[slot];
-      const int kind = uv.kind;
-      if (kind == UNIT_NONE) break;
-      const int h = uv.h, q0 = uv.q0, ntok = uv.ntok, pos0 = uv.pos0, jb = uv.jb;
-      const int tok = t * p.tile_tokens + my_tok;
-      const bool real = my_tok < p.tile_tokens && tok < ntok;
-      const int pos = pos0 + min(tok, ntok - 1);
-      int steps;
-      {
-        Unit u;
-        u.kind = kind;
-        u.ntok = ntok;
-        u.pos0 = pos0;
-        u.jb = jb;
-        u.je = uv.je;
-        u.ns = uv.ns;
-        u.w0 = uv.w0;
-        steps = steps_of<BC>(u, t, p.tile_tokens);
-      }
+      if (uv.kind == UNIT_NONE) break;
+      // What the steps below do not need is read again where it is used: they have no registers to spare.
+      const int pos = uv.pos0 + min(t * p.tile_tokens + my_tok, uv.ntok - 1);
+      const int steps = steps_of<BC>(uv, t, p.tile_tokens);
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++done) {
         const bool okw = __all_sync(0xffffffffu, mbar_wait(bar_sf(t), done & 1, abort_flag, p.err, W_SF));
@@ -756,7 +817,7 @@ __global__ void __maxnreg__(C::MAXREG)
           ok = false;
           break;
         }
-        const int jj = jb + j, ns = uv.ns;
+        const int jj = uv.jb + j, ns = uv.ns;
         const int key0 = (jj < ns ? jj : uv.w0 + jj - ns) * BC;
         // columns valid > e, and from `first` on or among the sinks
         const int valid = pos + 1 - key0;
@@ -764,21 +825,24 @@ __global__ void __maxnreg__(C::MAXREG)
         const bool full = __all_sync(0xffffffffu, valid >= BC && (first <= 0 || sink >= BC));
         const bool started = __all_sync(0xffffffffu, m_ref != -INFINITY);
         tc_fence_after();
-        if constexpr (C::PV2) {
-          uint32_t sr[BC / 32][32];
-#pragma unroll
-          for (int i = 0; i < BC / 32; ++i) tmem_ld32(tS + i * 32, sr[i]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < BC / 32; ++i) reg_fence(sr[i]);
-          constexpr int HC = BC / 2, HP = BC / 128;  // columns and packed 32-column chunks of half of P
-          auto& sr_a = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[0]);
-          auto& sr_b = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[HC / 32]);
+        // Once every row of the warp has a reference maximum and sees all columns, P is computed against it with no row maximum in front of it;
+        // row sums of at most 2^tau (and at d = 128 the second half's maximum) show that no score moved past m_ref + tau.
+        // Otherwise nothing has been stored yet, and the general path reads S again (fa_fwd_kernel.cuh, `fast`, PV2).
+        // (A masked copy of it costs more in registers and code than it saves: 375 us on a prompt of 8191 tokens, d = 128, without
+        // it 371; a mixed batch, d = 64, 89 and 86.)
+        const auto fast = [&]() -> bool {
+          const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
           float r0, r1, r2, r3;
-          if (full && started) {
-            // The first half's exponentials against the reference maximum, with no row maximum in front of them: its sum
-            // and the second half's maximum show that none moved past m_ref + tau (FwdCfg::PV2).
-            const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+          if constexpr (C::PV2) {
+            uint32_t sr[BC / 32][32];
+#pragma unroll
+            for (int i = 0; i < BC / 32; ++i) tmem_ld32(tS + i * 32, sr[i]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < BC / 32; ++i) reg_fence(sr[i]);
+            constexpr int HC = BC / 2, HP = BC / 128;  // columns and packed 32-column chunks of half of P
+            auto& sr_a = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[0]);
+            auto& sr_b = reinterpret_cast<uint32_t(&)[HC / 32][32]>(sr[HC / 32]);
             uint32_t pk[HP][32];
             uint64_t rs[2] = {0ull, 0ull};
             softmax_p_bf16<HC, false>(sr_a, pk, c2, negm2, HC, rs);
@@ -786,58 +850,19 @@ __global__ void __maxnreg__(C::MAXREG)
             f2_unpack_f(rs[0], r0, r1);
             f2_unpack_f(rs[1], r2, r3);
             const float l_a = (r0 + r1) + (r2 + r3);
-            if (__all_sync(0xffffffffu, l_a <= p.p_lim && m_b <= m_ref + p.tau)) {
+            if (!__all_sync(0xffffffffu, l_a <= p.p_lim && m_b <= m_ref + p.tau)) return false;
 #pragma unroll
-              for (int i = 0; i < HP; ++i) tmem_st32(tS + i * 32, pk[i]);
-              hand_over(bar_ph(t));
-              uint64_t rs_b[2] = {0ull, 0ull};
-              softmax_p_bf16<HC, false>(sr_b, pk, c2, negm2, HC, rs_b);
+            for (int i = 0; i < HP; ++i) tmem_st32(tS + i * 32, pk[i]);
+            hand_over(bar_ph(t));
+            uint64_t rs_b[2] = {0ull, 0ull};
+            softmax_p_bf16<HC, false>(sr_b, pk, c2, negm2, HC, rs_b);
 #pragma unroll
-              for (int i = 0; i < HP; ++i) tmem_st32(tS + (HP + i) * 32, pk[i]);
-              hand_over(bar_pf(t));
-              f2_unpack_f(rs_b[0], r0, r1);
-              f2_unpack_f(rs_b[1], r2, r3);
-              l += l_a + ((r0 + r1) + (r2 + r3));
-              continue;
-            }
-          }
-          if (!full) {
-#pragma unroll
-            for (int i = 0; i < BC / 32; ++i) {
-              const uint32_t vis = low_bits(valid - 32 * i) & (~low_bits(first - 32 * i) | low_bits(sink - 32 * i));
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(vis >> e & 1u)) sr[i][e] = hidden;
-            }
-          }
-          const float m_new = fmaxf(m_ref, (c >= 0.f ? row_extreme<BC, true>(sr) : row_extreme<BC, false>(sr)) * c);
-          const bool need = m_new > m_ref + p.tau;  // always true on the first tile that a row sees
-          float alpha = 1.f;
-          if (need) {
-            alpha = ex2_approx(m_ref - m_new);  // 0 the first time
-            m_ref = m_new;
-          }
-          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen nothing: 2^(-inf - 0) = 0
-          const uint64_t negm2 = f2_pack(-m_use, -m_use);
-          uint64_t rs[2] = {0ull, 0ull};
-          uint32_t pk[HP][32];
-          softmax_p_bf16<HC, false>(sr_a, pk, c2, negm2, HC, rs);
-#pragma unroll
-          for (int i = 0; i < HP; ++i) tmem_st32(tS + i * 32, pk[i]);
-          if (j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
-          hand_over(bar_ph(t));
-          softmax_p_bf16<HC, false>(sr_b, pk, c2, negm2, HC, rs);
-#pragma unroll
-          for (int i = 0; i < HP; ++i) tmem_st32(tS + (HP + i) * 32, pk[i]);
-          hand_over(bar_pf(t));
-          f2_unpack_f(rs[0], r0, r1);
-          f2_unpack_f(rs[1], r2, r3);
-          l = l * alpha + ((r0 + r1) + (r2 + r3));
-        } else {
-          // 64-column tiles.  Once every row has a reference maximum, P is computed against it while the scores are still
-          // arriving; a row sum of at most 2^tau shows that none moved past it (fa_fwd_kernel.cuh, `fast`).
-          if (full && started) {
-            const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+            for (int i = 0; i < HP; ++i) tmem_st32(tS + (HP + i) * 32, pk[i]);
+            hand_over(bar_pf(t));
+            f2_unpack_f(rs_b[0], r0, r1);
+            f2_unpack_f(rs_b[1], r2, r3);
+            l += l_a + ((r0 + r1) + (r2 + r3));
+          } else {  // the scores of 32 columns arrive while those before them are worked on
             uint32_t sc[2][32], pk[32];
             uint64_t rs[2] = {0ull, 0ull};
             tmem_ld32(tS, sc[0]);
@@ -860,68 +885,68 @@ __global__ void __maxnreg__(C::MAXREG)
                 reg_fence(sc[1]);
               }
             }
-            float r0, r1, r2, r3;
             f2_unpack_f(rs[0], r0, r1);
             f2_unpack_f(rs[1], r2, r3);
             const float l_tile = (r0 + r1) + (r2 + r3);
-            if (__all_sync(0xffffffffu, l_tile <= p.p_lim)) {
-              tmem_st32(tS, pk);
-              hand_over(bar_pf(t));
-              l += l_tile;
-              continue;
-            }
+            if (!__all_sync(0xffffffffu, l_tile <= p.p_lim)) return false;
+            tmem_st32(tS, pk);
+            hand_over(bar_pf(t));
+            l += l_tile;
           }
-          // the general path, a chunk of 32 columns at a time: the maximum, then P
-          uint32_t sr[1][32];
-          const auto chunk = [&](int cc) {
-            tmem_ld32(tS + cc * 32, sr[0]);
-            tmem_wait_ld();
-            reg_fence(sr[0]);
-            if (!full) {
-              const uint32_t vis = low_bits(valid - 32 * cc) & (~low_bits(first - 32 * cc) | low_bits(sink - 32 * cc));
+          return true;
+        };
+        if (started && full && fast()) continue;
+        // The general path, a chunk of 32 columns at a time: the maximum, then P.
+        uint32_t sr[1][32];
+        const auto chunk = [&](int cc) {
+          tmem_ld32(tS + cc * 32, sr[0]);
+          tmem_wait_ld();
+          reg_fence(sr[0]);
+          if (!full) {
+            const uint32_t vis = low_bits(valid - 32 * cc) & (~low_bits(first - 32 * cc) | low_bits(sink - 32 * cc));
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(vis >> e & 1u)) sr[0][e] = hidden;
-            }
-          };
-          float m_new = m_ref;
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            chunk(cc);
-            m_new = fmaxf(m_new, (c >= 0.f ? row_extreme<32, true>(sr) : row_extreme<32, false>(sr)) * c);
+            for (int e = 0; e < 32; ++e)
+              if (!(vis >> e & 1u)) sr[0][e] = hidden;
           }
-          const bool need = m_new > m_ref + p.tau;
-          float alpha = 1.f;
-          if (need) {
-            alpha = ex2_approx(m_ref - m_new);
-            m_ref = m_new;
-          }
-          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t negm2 = f2_pack(-m_use, -m_use);
-          uint64_t rs[2] = {0ull, 0ull};
-          // chunk cc's 16 packed columns go over columns 16 cc .. 16 cc + 15 of S, which hold chunk 0 (already read)
+        };
+        float m_new = m_ref;
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            chunk(cc);
-            uint32_t pk[32];
-#pragma unroll
-            for (int qc = 0; qc < 16; ++qc) {
-              const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[0][2 * qc]), __uint_as_float(sr[0][2 * qc + 1])), c2, negm2);
-              float x0, x1;
-              f2_unpack_f(x, x0, x1);
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              rs[qc & 1] = f2_add(rs[qc & 1], f2_pack(p0, p1));
-              pk[qc] = pack_bf16x2(p0, p1);
-            }
-            tmem_st16_lo(tS + cc * 16, pk);
-          }
-          if (j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
-          hand_over(bar_pf(t));
-          float r0, r1, r2, r3;
-          f2_unpack_f(rs[0], r0, r1);
-          f2_unpack_f(rs[1], r2, r3);
-          l = l * alpha + ((r0 + r1) + (r2 + r3));
+        for (int cc = 0; cc < BC / 32; ++cc) {
+          chunk(cc);
+          m_new = fmaxf(m_new, (c >= 0.f ? row_extreme<32, true>(sr) : row_extreme<32, false>(sr)) * c);
         }
+        const bool need = m_new > m_ref + p.tau;  // always true on the first tile that a row sees
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx(m_ref - m_new);  // 0 the first time
+          m_ref = m_new;
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen nothing: 2^(-inf - 0) = 0
+        const uint64_t negm2 = f2_pack(-m_use, -m_use);
+        uint64_t rs[2] = {0ull, 0ull};
+        if (j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
+        // chunk cc's 16 packed columns go over columns 16 cc .. 16 cc + 15 of S, which hold chunk cc / 2 (already read)
+#pragma unroll
+        for (int cc = 0; cc < BC / 32; ++cc) {
+          chunk(cc);
+          uint32_t pk[32];
+#pragma unroll
+          for (int qc = 0; qc < 16; ++qc) {
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[0][2 * qc]), __uint_as_float(sr[0][2 * qc + 1])), c2, negm2);
+            float x0, x1;
+            f2_unpack_f(x, x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            rs[qc & 1] = f2_add(rs[qc & 1], f2_pack(p0, p1));
+            pk[qc] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16_lo(tS + cc * 16, pk);
+          if (C::PV2 && cc == BC / 64 - 1) hand_over(bar_ph(t));
+        }
+        hand_over(bar_pf(t));
+        float r0, r1, r2, r3;
+        f2_unpack_f(rs[0], r0, r1);
+        f2_unpack_f(rs[1], r2, r3);
+        l = l * alpha + ((r0 + r1) + (r2 + r3));
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
@@ -931,43 +956,21 @@ __global__ void __maxnreg__(C::MAXREG)
         if (!ok) break;
         tc_fence_after();
       }
+      const int kind = uv.kind, ntok = uv.ntok, tok = t * p.tile_tokens + my_tok;
+      const bool real = my_tok < p.tile_tokens && tok < ntok, aside = uv.set_aside != 0;
       if (uv.bad_page || kind == UNIT_BAD) l = __int_as_float(0x7fc00000);
-      const bool aside = uv.set_aside != 0;
-      // Adds the values set aside (infinities, NaN) that this row sees to columns c0 .. c0 + 31 of its O.
-      const auto add_aside = [&](uint32_t (&orr)[32], int c0) {
-        if (!real) return;
-        const int ns = uv.ns, wt = uv.w0, je = uv.je, hi = uv.hi, b = uv.b;
-        const int last_lo = p.window > 0 ? max(0, pos0 + ntok - p.window) : 0;
-        for (int jj = jb; jj < je; ++jj) {
-          const int key0 = (jj < ns ? jj : wt + jj - ns) * BC;
-          if (key0 + BC <= pos0 + 1 && key0 >= last_lo) continue;
-          for (int key = key0; key < min(key0 + BC, hi); ++key) {
-            if (key <= pos0 && key >= last_lo) continue;  // every row sees it: left in the products
-            if (key > pos || (p.window > 0 && key <= pos - p.window && key >= p.sinks)) continue;
-            const int pi = p.by_page.div(key), pg = p.table[b * p.table_stride + pi];
-            if (pg < 0 || pg >= p.num_pages) continue;
-            const __nv_bfloat16* const v = p.v + pg * p.c_page + h * p.c_head + (key - pi * p.page_size) * p.c_row + c0;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float x = __bfloat162float(v[e]);
-              if (!(fabsf(x) < INFINITY)) orr[e] = __float_as_uint(__uint_as_float(orr[e]) + x);
-            }
-          }
-        }
-      };
       const bool any_rows = t * p.tile_tokens < ntok;
       if (!any_rows) {
         // a block of one tile
       } else if (kind == UNIT_WHOLE || kind == UNIT_BAD) {
         const float inv_l = 1.f / l;
-        const size_t out = static_cast<size_t>(q0 + tok) * p.H + h * p.G + g;
+        const size_t out = static_cast<size_t>(uv.q0 + tok) * p.H + uv.h * p.G + g;
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t orr[32];
           tmem_ld32(tO + cc * 32, orr);
           tmem_wait_ld();
           reg_fence(orr);
-          if (aside) add_aside(orr, cc * 32);
           if (real) {
             uint4* const dst = reinterpret_cast<uint4*>(p.o + out * D + cc * 32);
 #pragma unroll
@@ -982,6 +985,7 @@ __global__ void __maxnreg__(C::MAXREG)
           }
         }
         if (p.lse != nullptr && real) p.lse[out] = (m_ref + log2f(l)) * 0.6931471805599453f;
+        if (aside && real) add_aside<C>(p, uv, pos, p.o + out * D, D, 0);
       } else {
         // Partial state: 16-byte pieces of the rows side by side, so that a warp's stores are whole lines.
         const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (kind == UNIT_BEGUN)) * p.part_tiles + t;
@@ -993,8 +997,7 @@ __global__ void __maxnreg__(C::MAXREG)
             tmem_ld32(tO + cc * 32, orr);
             tmem_wait_ld();
             reg_fence(orr);
-            if (aside) add_aside(orr, cc * 32);
-          } else {
+            } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) orr[e] = 0;
           }
@@ -1007,6 +1010,7 @@ __global__ void __maxnreg__(C::MAXREG)
           }
         }
         if (real) p.part_ml[part * p.part_rows + row] = make_float2(m_ref, l);
+        if (aside && real) add_aside<C>(p, uv, pos, reinterpret_cast<float*>(po), 4, 4LL * p.part_rows);
       }
       tc_fence_before();  // O has been read: the next unit's first P V comes behind this warp's next hand_over
       __syncwarp();
@@ -1024,67 +1028,44 @@ __global__ void __maxnreg__(C::MAXREG)
 }
 
 // Joins the states of the units that CTA blockIdx.x begins and others finish, in the order of their keys:
-// O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  A block has 32 rows (a lane each) of one row tile, its warps a quarter of the
-// columns each.
+// O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  A block has 32 rows (a lane each) of one row tile, each warp 8 columns.
 template <int D>
-__global__ void __launch_bounds__(128) fa_fwd_paged_join_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(D * 4) fa_fwd_paged_join_kernel(const ChunkParams p) {
   griddep_wait();
-  const int c = blockIdx.x, t = blockIdx.y, row = blockIdx.z * 32 + (threadIdx.x & 31), quarter = threadIdx.x >> 5;
+  const int c = blockIdx.x, t = blockIdx.y, row = blockIdx.z * 32 + (threadIdx.x & 31), col8 = threadIdx.x >> 5;
   const Begun u = p.begun[c];
-  if (u.tiles == 0) return;
   const int my_tok = p.by_g.div(row), g = row - my_tok * p.G, tok = t * p.tile_tokens + my_tok;
-  if (my_tok >= p.tile_tokens || tok >= u.ntok) return;
-  const size_t stride = static_cast<size_t>(2) * p.part_tiles;  // parts of a CTA
-  // CTA c' > c has a part where tiles lie between its cuts; the first one without ends the unit or is empty
+  if (u.parts == 0 || my_tok >= p.tile_tokens || tok >= u.ntok) return;
+  // CTA c's state of a unit that it begins, then those of the CTAs behind it of a unit that they continue
+  const auto part = [&](int i) {
+    return static_cast<size_t>(c + i) * 2 * p.part_tiles + (i == 0 ? p.part_tiles : 0) + t;
+  };
   float m = -INFINITY;
-  int end = c + 1;
-  {
-    size_t part = (static_cast<size_t>(c) * 2 + 1) * p.part_tiles + t;
-    m = p.part_ml[part * p.part_rows + row].x;
-    for (int from = cut(range_begin(u.total, c + 1, u.ranges), u.start, u.tiles, u.cost); from < u.tiles; ++end) {
-      const int to = cut(range_begin(u.total, end + 1, u.ranges), u.start, u.tiles, u.cost);
-      if (to > from) {
-        part = static_cast<size_t>(end) * stride + t;
-        m = fmaxf(m, p.part_ml[part * p.part_rows + row].x);
-      }
-      from = to;
-    }
-  }
-  constexpr int N4 = D / 16;  // 16-byte pieces of a quarter row
-  float4 o[N4];
-  float l = 0.f;
-#pragma unroll
-  for (int i = 0; i < N4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  int from = 0;
-  for (int i = c; i < end; ++i) {
-    const int to = cut(range_begin(u.total, i + 1, u.ranges), u.start, u.tiles, u.cost);
-    if (to > from) {
-      const size_t part = static_cast<size_t>(i) * stride + (i == c ? p.part_tiles : 0) + t;
-      const float2 ml = p.part_ml[part * p.part_rows + row];
-      const float w = ex2_approx(ml.x - m);
-      const float4* const po = p.part_o + (part * (D / 4) + quarter * N4) * p.part_rows + row;
-#pragma unroll
-      for (int k = 0; k < N4; ++k) {
-        const float4 x = po[static_cast<size_t>(k) * p.part_rows];
-        o[k].x = fmaf(w, x.x, o[k].x);
-        o[k].y = fmaf(w, x.y, o[k].y);
-        o[k].z = fmaf(w, x.z, o[k].z);
-        o[k].w = fmaf(w, x.w, o[k].w);
-      }
-      l = fmaf(w, ml.y, l);
-    }
-    from = to;
+#pragma unroll 8
+  for (int i = 0; i < u.parts; ++i) m = fmaxf(m, p.part_ml[part(i) * p.part_rows + row].x);
+  float o[8] = {}, l = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < u.parts; ++i) {
+    const float2 ml = p.part_ml[part(i) * p.part_rows + row];
+    const float4* const po = p.part_o + (part(i) * (D / 4) + col8 * 2) * p.part_rows + row;
+    const float4 x = po[0], y = po[p.part_rows];
+    const float w = ex2_approx(ml.x - m);
+    o[0] = fmaf(w, x.x, o[0]);
+    o[1] = fmaf(w, x.y, o[1]);
+    o[2] = fmaf(w, x.z, o[2]);
+    o[3] = fmaf(w, x.w, o[3]);
+    o[4] = fmaf(w, y.x, o[4]);
+    o[5] = fmaf(w, y.y, o[5]);
+    o[6] = fmaf(w, y.z, o[6]);
+    o[7] = fmaf(w, y.w, o[7]);
+    l = fmaf(w, ml.y, l);
   }
   const float inv = 1.f / l;
   const size_t out = static_cast<size_t>(u.q0 + tok) * p.H + u.h * p.G + g;
-  uint4* const dst = reinterpret_cast<uint4*>(p.o + out * D + quarter * (D / 4));
-#pragma unroll
-  for (int k = 0; k < N4 / 2; ++k) {
-    const float4 a = o[2 * k], b = o[2 * k + 1];
-    dst[k] = make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv), pack_bf16x2(b.x * inv, b.y * inv),
-                        pack_bf16x2(b.z * inv, b.w * inv));
-  }
-  if (p.lse != nullptr && quarter == 0) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+  *reinterpret_cast<uint4*>(p.o + out * D + col8 * 8) =
+      make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv), pack_bf16x2(o[4] * inv, o[5] * inv),
+                 pack_bf16x2(o[6] * inv, o[7] * inv));
+  if (p.lse != nullptr && col8 == 0) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // The workspace: states of cut units, and who begins them.
@@ -1136,6 +1117,7 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
   p.G = a.H / a.Hkv;
   p.by_g = FastDiv(static_cast<unsigned>(p.G));
   p.by_page = FastDiv(static_cast<unsigned>(a.page_size));
+  p.by_block = FastDiv(static_cast<unsigned>(2 * (C::BR / p.G)));
   p.T = a.T;
   p.B = a.B;
   p.H = a.H;
@@ -1165,7 +1147,7 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
   const unsigned grid = static_cast<unsigned>(a.sms * C::MINB);
   e = launch_dependent(fa_fwd_paged_kernel<C>, dim3(grid), C::NTHREADS, C::SMEM_BYTES, a.stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(fa_fwd_paged_join_kernel<C::D>, dim3(grid, l.tiles, l.rows / 32), 128, 0, a.stream, p);
+  return launch_dependent(fa_fwd_paged_join_kernel<C::D>, dim3(grid, l.tiles, l.rows / 32), C::D * 4, 0, a.stream, p);
 }
 
 }  // namespace
