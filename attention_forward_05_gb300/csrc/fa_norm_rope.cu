@@ -8,10 +8,10 @@
 // The backward pass forms r again from x: reading a stored one would save nothing, x is needed anyway.
 //
 // Work split.  That of fa_rope_items.cuh: a lane holds 16 elements of a head, so a head's sums are d / 16 lanes' sums and
-// two or three shuffles; everything between the load and the store stays in registers, in fp32, rounded once.  The
-// weights of a lane's elements stay in its registers.  The backward pass copies dy and x of half as many heads an item;
-// a lane adds up its elements' share of dw over all its items, a block joins its lanes' shares in a fixed order and
-// leaves them in the workspace, and fa_norm_rope_join_kernel adds the blocks' (no atomics: the same bits every time).
+// two or three shuffles; everything between the ring and the store stays in registers, in fp32, rounded once.  Every block has its part of the query heads, then of the key heads, so a lane's registers hold one set
+// of weights.  The backward pass copies dy and x of half as many heads an item; a lane adds up its
+// elements' share of dw over all its items, a block joins its lanes' shares in a fixed order and leaves them in the
+// workspace, and fa_norm_rope_join_kernel adds the blocks' (no atomics: the same bits every time).
 #include "fa_rope_items.cuh"
 
 namespace fa {
@@ -137,14 +137,7 @@ __device__ __forceinline__ void scale16(Head16& a, float f) {
   }
 }
 
-// Sum over the UNITS lanes of a head, which are neighbours; `mask` is theirs (other heads' lanes may be elsewhere).
-template <int UNITS>
-__device__ __forceinline__ float head_sum(float x, unsigned mask) {
-#pragma unroll
-  for (int i = 1; i < UNITS; i *= 2) x += __shfl_xor_sync(mask, x, i);
-  return x;
-}
-
+// The UNITS lanes of a head, which are neighbours (other heads' lanes may be elsewhere).
 template <int UNITS>
 __device__ __forceinline__ unsigned head_mask() {
   return ((1u << UNITS) - 1u) << ((threadIdx.x & 31) & ~(UNITS - 1));
@@ -152,72 +145,248 @@ __device__ __forceinline__ unsigned head_mask() {
 
 __device__ __forceinline__ float inv_rms(float squares, int d, float eps) { return rsqrtf(squares * (1.f / d) + eps); }
 
-// Norms, rotates and rounds a head's 16 elements.
-template <typename T, int D, bool INTER>
-__device__ __forceinline__ void norm_turn(Unit<T>* x, const Head16& w, float eps, bool rotated, const Turn& turn,
-                                          unsigned mask) {
-  Head16 h = unpack<INTER>(*x);
-  const float r = inv_rms(head_sum<D / 16>(dot16(h, h), mask), D, eps);
-  scale16(h, r);
-  h = mul16(h, w);
-  if (rotated) {
+// Sums over a head's lanes, side by side.
+template <int UNITS, int N>
+__device__ __forceinline__ void head_sums(float (&x)[N], unsigned mask) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) turn.apply(j, h.x1[j], h.x2[j]);
+  for (int i = 1; i < UNITS; i *= 2)
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] += __shfl_xor_sync(mask, x[k], i);
+}
+
+template <int UNITS>
+__device__ __forceinline__ float head_sum(float x, unsigned mask) {
+  float v[1] = {x};
+  head_sums<UNITS>(v, mask);
+  return v[0];
+}
+
+template <bool INTER, typename T>
+__device__ __forceinline__ Head16 read16(const uint4* src) {
+  Unit<T> x;
+  x.load(src);
+  return unpack<INTER>(x);
+}
+
+// The weights times a token's turn: y1 = x1 a - x2 b, y2 = x1 c + x2 d (b with its sign), the same for all of its heads.
+struct Fold {
+  uint64_t a[4], b[4], c[4], d[4];
+  __device__ __forceinline__ Fold(const Head16& w, const Turn& t, bool rotated) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = rotated ? f2_mul(w.x1[j], t.c[j]) : w.x1[j];
+      b[j] = rotated ? f2_mul(w.x2[j], t.n[j]) : 0ull;
+      c[j] = rotated ? f2_mul(w.x1[j], t.s[j]) : 0ull;
+      d[j] = rotated ? f2_mul(w.x2[j], t.c[j]) : w.x2[j];
+    }
   }
-  pack<INTER>(h, x);
+  __device__ __forceinline__ void apply(Head16& x) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t y = f2_fma(x.x1[j], a[j], f2_mul(x.x2[j], b[j]));
+      x.x2[j] = f2_fma(x.x1[j], c[j], f2_mul(x.x2[j], d[j]));
+      x.x1[j] = y;
+    }
+  }
+};
+
+// The heads of one kind, of B * N tokens, and how they are cut.
+struct Heads {
+  const void* x;    // inputs
+  const void* dy;   // backward: gradients of the outputs
+  void* out;
+  const void* w;
+  RowStrides sx, sdy, so;
+  int n;
+  int first_block;  // that takes the first item
+  int quad;         // up to three heads take the lanes without quads (fa_rope_items.cuh)
+  Tiling g;
+};
+__device__ __forceinline__ int block_of(const Heads& hs) { return (blockIdx.x + gridDim.x - hs.first_block) % gridDim.x; }
+__device__ __forceinline__ bool has_items(const Heads& hs) { return block_of(hs) * (ROPE_THREADS / 32) < hs.g.count; }
+
+struct NormParams {
+  Heads heads[2];   // query and key heads
+  Rotary r;
+  FastDiv by_n;
+  float eps;
+  int w_fp32, N, tokens;
+  int* err;
+  float* parts;     // backward
+};
+
+constexpr int FWD_SLOTS = 8, FWD_BLOCKS = 3;
+
+// A block's items, forward.
+template <typename T, int D, bool INTER, bool QUAD>
+__device__ __forceinline__ void norm_items(const NormParams& p, const Heads& hs, const PairTurn* pairs) {
+  constexpr int P = Unit<T>::PIECES, PER = FWD_SLOTS / P, STEP = Lane<D, QUAD>::STEP, UNITS = D / 16;
+  int e0, es;
+  const bool rotated = unit_pieces<T, D>(p.r.rot, Lane<D, QUAD>().u, &e0, &es);
+  const Head16 w = load_weight<T, INTER>(hs.w, p.w_fp32, e0, es);
+  const unsigned mask = head_mask<UNITS>();
+  run_items<T, D, INTER, QUAD, FWD_SLOTS>(
+      hs.g, p.r, pairs, rotated, p.tokens, block_of(hs), gridDim.x,
+      [&](int t, int h0, uint32_t dst, uint32_t) {
+        const int b = p.by_n.div(t), n = t - b * p.N;
+        const T* const x = static_cast<const T*>(hs.x) + b * hs.sx.b + n * hs.sx.n;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int h = h0 + STEP * i;
+          if (i < hs.g.per && h < hs.n) Unit<T>::fetch(dst + i * P * 512, x + h * hs.sx.h, e0, es);
+        }
+        return p.r.pos + (p.r.batch_stride ? t : n);
+      },
+      [&](int t, int h0, const uint4* src, long long, const Turn& turn) {
+        const int b = p.by_n.div(t), n = t - b * p.N;
+        T* const out = static_cast<T*>(hs.out) + b * hs.so.b + n * hs.so.n;
+        const Fold fold(w, turn, rotated);
+#pragma unroll 1
+        for (int i = 0; i < hs.g.per; ++i) {  // one head at a time: several in registers spill
+          const int h = h0 + STEP * i;
+          if (h >= hs.n) break;
+          Head16 x = read16<INTER, T>(src + i * P * 32);
+          scale16(x, inv_rms(head_sum<UNITS>(dot16(x, x), mask), D, p.eps));
+          fold.apply(x);
+          Unit<T> y;
+          pack<INTER>(x, &y);
+          y.store(out + h * hs.so.h, e0, es);
+        }
+      });
+}
+
+// The backward pass has as many heads an item as the forward one, from two tensors, and dw's sums in registers: fewer blocks a
+// SM, with more of the ring each.
+constexpr int BWD_SLOTS = 16, BWD_BLOCKS = 3;
+
+// A block's items, backward; leaves the block's share of dw in `parts`.
+template <typename T, int D, bool INTER, bool QUAD>
+__device__ __forceinline__ void norm_items_bwd(const NormParams& p, const Heads& hs, const PairTurn* pairs, float (*share)[D],
+                                               float* parts) {
+  constexpr int P = Unit<T>::PIECES, PER = BWD_SLOTS / (2 * P), STEP = Lane<D, QUAD>::STEP, UNITS = D / 16;
+  int e0, es;
+  const bool rotated = unit_pieces<T, D>(p.r.rot, Lane<D, QUAD>().u, &e0, &es);
+  const Head16 w = load_weight<T, INTER>(hs.w, p.w_fp32, e0, es);
+  const unsigned mask = head_mask<UNITS>();
+  Head16 sum{};
+  run_items<T, D, INTER, QUAD, BWD_SLOTS>(
+      hs.g, p.r, pairs, rotated, p.tokens, block_of(hs), gridDim.x,
+      [&](int t, int h0, uint32_t dst, uint32_t) {
+        const int b = p.by_n.div(t), n = t - b * p.N;
+        const T* const x = static_cast<const T*>(hs.x) + b * hs.sx.b + n * hs.sx.n;
+        const T* const dy = static_cast<const T*>(hs.dy) + b * hs.sdy.b + n * hs.sdy.n;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int h = h0 + STEP * i;
+          if (i < hs.g.per && h < hs.n) {
+            Unit<T>::fetch(dst + 2 * i * P * 512, dy + h * hs.sdy.h, e0, es);
+            Unit<T>::fetch(dst + (2 * i + 1) * P * 512, x + h * hs.sx.h, e0, es);
+          }
+        }
+        return p.r.pos + (p.r.batch_stride ? t : n);
+      },
+      [&](int t, int h0, const uint4* src, long long, const Turn& turn) {
+        const int b = p.by_n.div(t), n = t - b * p.N;
+        T* const out = static_cast<T*>(hs.out) + b * hs.so.b + n * hs.so.n;
+#pragma unroll 1
+        for (int i = 0; i < hs.g.per; ++i) {
+          const int h = h0 + STEP * i;
+          if (h >= hs.n) break;
+          Head16 gr = read16<INTER, T>(src + 2 * i * P * 32);
+          if (rotated) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) turn.apply(j, gr.x1[j], gr.x2[j]);
+          }
+          Head16 u = read16<INTER, T>(src + (2 * i + 1) * P * 32);
+          float s[2] = {dot16(u, u), dot16(mul16(gr, w), u)};  // sums of x^2 and of w g x
+          head_sums<UNITS>(s, mask);
+          const float f = inv_rms(s[0], D, p.eps), m = s[1] * (1.f / D) * f;  // mean(w g u)
+          scale16(u, f);
+          const uint64_t f2 = f2_pack(f, f), m2 = f2_pack(-m * f, -m * f);
+          Head16 dx;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dx.x1[j] = f2_fma(u.x1[j], m2, f2_mul(f2_mul(gr.x1[j], w.x1[j]), f2));
+            dx.x2[j] = f2_fma(u.x2[j], m2, f2_mul(f2_mul(gr.x2[j], w.x2[j]), f2));
+            sum.x1[j] = f2_fma(gr.x1[j], u.x1[j], sum.x1[j]);
+            sum.x2[j] = f2_fma(gr.x2[j], u.x2[j], sum.x2[j]);
+          }
+          Unit<T> y;
+          pack<INTER>(dx, &y);
+          y.store(out + h * hs.so.h, e0, es);
+        }
+      });
+  // The block's share: lanes of the same unit, then its warps, in order.
+  __syncwarp();
+  constexpr int W = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float lo, hi, v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (first_of<INTER>(q) == i) f2_unpack_f(sum.x1[q / 2], lo, hi), v = q % 2 ? hi : lo;
+      if (second_of<INTER>(q) == i) f2_unpack_f(sum.x2[q / 2], lo, hi), v = q % 2 ? hi : lo;
+    }
+#pragma unroll
+    for (int step = UNITS; step < 32; step *= 2) v += __shfl_xor_sync(0xffffffffu, v, step);
+    if ((threadIdx.x & 31) < UNITS) share[threadIdx.x / 32][e0 + i / W * es + i % W] = v;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += ROPE_THREADS) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < ROPE_THREADS / 32; ++k) v += share[k][i];
+    parts[i] = v;
+  }
+  __syncthreads();  // `share` has been read
 }
 
 }  // namespace
 
-template <typename T, int D, bool INTER, bool QUAD>
-__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_rope_kernel(const RopeLaunch a, const HeadNorm nm,
-                                                                                 const Tiling g, const FastDiv by_n) {
-  constexpr int PER = PIECE_SLOTS / Unit<T>::PIECES, STEP = Lane<D, QUAD>::STEP;
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(ROPE_THREADS, FWD_BLOCKS) fa_norm_rope_kernel(const __grid_constant__ NormParams p) {
   __shared__ PairTurn pairs[D / 2];
   griddep_wait();
-  load_rotation<D>(a.r, pairs, a.err);
+  load_rotation<D>(p.r, pairs, p.err);
   __syncthreads();
-  const int tokens = a.B * a.N, heads = a.H + a.Hkv;
-  int e0, es;
-  const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, QUAD>().u, &e0, &es);
-  const Head16 wq = load_weight<T, INTER>(nm.wq, nm.fp32, e0, es), wk = load_weight<T, INTER>(nm.wk, nm.fp32, e0, es);
-  const unsigned mask = head_mask<D / 16>();
-  run_items<T, D, INTER, QUAD>(
-      g, a.r, pairs, rotated, tokens,
-      [&](int t, int h0, uint32_t dst, uint32_t) {
-        const int b = by_n.div(t), n = t - b * a.N;
-        const T* const q = static_cast<const T*>(a.q) + b * a.sq.b + n * a.sq.n;
-        const T* const k = static_cast<const T*>(a.k) + b * a.sk.b + n * a.sk.n;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int h = h0 + STEP * i;
-          if (i < g.per && h < heads)
-            Unit<T>::fetch(dst + i * Unit<T>::PIECES * 512, h < a.H ? q + h * a.sq.h : k + (h - a.H) * a.sk.h, e0, es);
-        }
-        return a.r.pos + (a.r.batch_stride ? t : n);
-      },
-      [&](int t, int h0, const uint4* src, long long, const Turn& turn) {
-        const int b = by_n.div(t), n = t - b * a.N;
-        T* const qo = static_cast<T*>(a.q_out) + b * a.sqo.b + n * a.sqo.n;
-        T* const ko = static_cast<T*>(a.k_out) + b * a.sko.b + n * a.sko.n;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int h = h0 + STEP * i;
-          if (i < g.per && h < heads) {
-            Unit<T> x;
-            x.load(src + i * Unit<T>::PIECES * 32);
-            norm_turn<T, D, INTER>(&x, h < a.H ? wq : wk, nm.eps, rotated, turn, mask);
-            x.store(h < a.H ? qo + h * a.sqo.h : ko + (h - a.H) * a.sko.h, e0, es);
-          }
-        }
-      });
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const Heads& hs = p.heads[k];
+    if (!has_items(hs)) continue;
+    if (hs.quad)
+      norm_items<T, D, INTER, true>(p, hs, pairs);
+    else
+      norm_items<T, D, INTER, false>(p, hs, pairs);
+  }
+}
+
+// p.r turns by the negative angle.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(ROPE_THREADS, BWD_BLOCKS) fa_norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
+  __shared__ PairTurn pairs[D / 2];
+  __shared__ float share[ROPE_THREADS / 32][D];
+  griddep_launch_dependents();
+  griddep_wait();
+  load_rotation<D>(p.r, pairs, p.err);
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const Heads& hs = p.heads[k];
+    float* const parts = p.parts + (static_cast<long long>(blockIdx.x) * 2 + k) * D;
+    if (!has_items(hs)) {
+      for (int i = threadIdx.x; i < D; i += ROPE_THREADS) parts[i] = 0.f;
+    } else if (hs.quad)
+      norm_items_bwd<T, D, INTER, true>(p, hs, pairs, share, parts);
+    else
+      norm_items_bwd<T, D, INTER, false>(p, hs, pairs, share, parts);
+  }
 }
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_append_kernel(const AppendLaunch a, const HeadNorm nm,
                                                                                    const Tiling g, const FastDiv by_page) {
   using T = __nv_bfloat16;
-  constexpr int PER = PIECE_SLOTS / Unit<T>::PIECES, STEP = Lane<D, true>::STEP;
+  constexpr int P = Unit<T>::PIECES, PER = PIECE_SLOTS / P, STEP = Lane<D, true>::STEP, UNITS = D / 16;
   __shared__ PairTurn pairs[D / 2];
   griddep_wait();
   load_rotation<D>(a.r, pairs, a.err);
@@ -226,9 +395,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_append_kern
   int e0, es;
   const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, true>().u, &e0, &es);
   const Head16 wq = load_weight<T, INTER>(nm.wq, nm.fp32, e0, es), wk = load_weight<T, INTER>(nm.wk, nm.fp32, e0, es);
-  const unsigned mask = head_mask<D / 16>();
+  const unsigned mask = head_mask<UNITS>();
   run_items<T, D, INTER, true>(
-      g, a.r, pairs, rotated, a.T,
+      g, a.r, pairs, rotated, a.T, blockIdx.x, gridDim.x,
       [&](int t, int h0, uint32_t dst, uint32_t slot_dst) {
         const T* const q = static_cast<const T*>(a.q) + t * a.q_tok;
         const T* const k = static_cast<const T*>(a.k) + t * a.k_tok;
@@ -238,8 +407,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_append_kern
         for (int i = 0; i < PER; ++i) {  // unused places too: their slots are still on the way
           const int h = h0 + STEP * i;
           if (i < g.per && h < heads)
-            Unit<T>::fetch(dst + i * Unit<T>::PIECES * 512,
-                           h < hk ? q + h * a.q_head : h < hv ? k + (h - hk) * a.k_head : v + (h - hv) * a.v_head, e0, es);
+            Unit<T>::fetch(dst + i * P * 512, h < hk ? q + h * a.q_head : h < hv ? k + (h - hk) * a.k_head : v + (h - hv) * a.v_head,
+                           e0, es);
         }
         return a.r.pos + t;
       },
@@ -253,186 +422,118 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_append_kern
         T* const qo = static_cast<T*>(a.q_out) + static_cast<long long>(t) * a.H * D;
         T* const ko = static_cast<T*>(a.k_cache) + row;
         T* const vo = static_cast<T*>(a.v_cache) + row;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < g.per; ++i) {
           const int h = h0 + STEP * i;
-          if (i < g.per && h < heads && (h < hk || store)) {
-            Unit<T> x;
-            x.load(src + i * Unit<T>::PIECES * 32);
-            if (h < hv) norm_turn<T, D, INTER>(&x, h < hk ? wq : wk, nm.eps, rotated, turn, mask);
-            x.store(h < hk ? qo + h * D : h < hv ? ko + (h - hk) * a.c_head : vo + (h - hv) * a.c_head, e0, es);
-          }
-        }
-      });
-}
-
-// a.q, a.k: the outputs' gradients; b: the forward pass's inputs; a.r turns by the negative angle.
-template <typename T, int D, bool INTER, bool QUAD>
-__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS)
-    fa_norm_rope_bwd_kernel(const RopeLaunch a, const NormBwd b, const HeadNorm nm, const Tiling g, const FastDiv by_n) {
-  constexpr int P = Unit<T>::PIECES, PER = PIECE_SLOTS / (2 * P), STEP = Lane<D, QUAD>::STEP, UNITS = D / 16;
-  __shared__ PairTurn pairs[D / 2];
-  __shared__ float share[ROPE_THREADS / 32][2][D];
-  griddep_launch_dependents();
-  griddep_wait();
-  load_rotation<D>(a.r, pairs, a.err);
-  __syncthreads();
-  const int tokens = a.B * a.N, heads = a.H + a.Hkv;
-  int e0, es;
-  const int u = Lane<D, QUAD>().u, lane = threadIdx.x & 31;
-  const bool rotated = unit_pieces<T, D>(a.r.rot, u, &e0, &es);
-  // Weights in shared memory, a unit's 16 bytes beside the next unit's: in registers, with dw's sums there, they spill.
-  __shared__ ulonglong2 weights[2][4][UNITS];
-  if (threadIdx.x < UNITS) {  // lane u of the first warp has unit u
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const Head16 w = load_weight<T, INTER>(which ? nm.wk : nm.wq, nm.fp32, e0, es);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) weights[which][j][u] = make_ulonglong2(w.x1[j], w.x2[j]);
-    }
-  }
-  __syncthreads();
-  const unsigned mask = head_mask<UNITS>();
-  Head16 sq{}, sk{};
-  run_items<T, D, INTER, QUAD>(
-      g, a.r, pairs, rotated, tokens,
-      [&](int t, int h0, uint32_t dst, uint32_t) {
-        const int bi = by_n.div(t), n = t - bi * a.N;
-        const T* const dq = static_cast<const T*>(a.q) + bi * a.sq.b + n * a.sq.n;
-        const T* const dk = static_cast<const T*>(a.k) + bi * a.sk.b + n * a.sk.n;
-        const T* const q = static_cast<const T*>(b.q) + bi * b.sq.b + n * b.sq.n;
-        const T* const k = static_cast<const T*>(b.k) + bi * b.sk.b + n * b.sk.n;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int h = h0 + STEP * i;
-          if (i < g.per && h < heads) {
-            Unit<T>::fetch(dst + 2 * i * P * 512, h < a.H ? dq + h * a.sq.h : dk + (h - a.H) * a.sk.h, e0, es);
-            Unit<T>::fetch(dst + (2 * i + 1) * P * 512, h < a.H ? q + h * b.sq.h : k + (h - a.H) * b.sk.h, e0, es);
-          }
-        }
-        return a.r.pos + (a.r.batch_stride ? t : n);
-      },
-      [&](int t, int h0, const uint4* src, long long, const Turn& turn) {
-        const int bi = by_n.div(t), n = t - bi * a.N;
-        T* const qo = static_cast<T*>(a.q_out) + bi * a.sqo.b + n * a.sqo.n;
-        T* const ko = static_cast<T*>(a.k_out) + bi * a.sko.b + n * a.sko.n;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int h = h0 + STEP * i;
-          if (i < g.per && h < heads) {
-            Unit<T> y, x;
-            y.load(src + 2 * i * P * 32);
-            x.load(src + (2 * i + 1) * P * 32);
-            Head16 dy = unpack<INTER>(y);
-            const Head16 hx = unpack<INTER>(x);
+          if (h >= heads || (h >= hk && !store)) break;
+          Unit<T> x;
+          x.load(src + i * P * 32);
+          if (h < hv) {
+            Head16 y = unpack<INTER>(x);
+            scale16(y, inv_rms(head_sum<UNITS>(dot16(y, y), mask), D, nm.eps));
+            y = mul16(y, h < hk ? wq : wk);
             if (rotated) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) turn.apply(j, dy.x1[j], dy.x2[j]);
+              for (int j = 0; j < 4; ++j) turn.apply(j, y.x1[j], y.x2[j]);
             }
-            Head16 wg;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const ulonglong2 w = weights[h >= a.H][j][u];
-              wg.x1[j] = f2_mul(dy.x1[j], w.x);
-              wg.x2[j] = f2_mul(dy.x2[j], w.y);
-            }
-            const float r = inv_rms(head_sum<UNITS>(dot16(hx, hx), mask), D, nm.eps);
-            const float m = head_sum<UNITS>(dot16(wg, hx), mask) * (1.f / D) * r * r;  // mean(w g u) r
-            const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(-m * r, -m * r);
-            Head16 dx;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              dx.x1[j] = f2_fma(hx.x1[j], m2, f2_mul(wg.x1[j], r2));
-              dx.x2[j] = f2_fma(hx.x2[j], m2, f2_mul(wg.x2[j], r2));
-            }
-            if (h < a.H) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                sq.x1[j] = f2_fma(dy.x1[j], f2_mul(hx.x1[j], r2), sq.x1[j]);
-                sq.x2[j] = f2_fma(dy.x2[j], f2_mul(hx.x2[j], r2), sq.x2[j]);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                sk.x1[j] = f2_fma(dy.x1[j], f2_mul(hx.x1[j], r2), sk.x1[j]);
-                sk.x2[j] = f2_fma(dy.x2[j], f2_mul(hx.x2[j], r2), sk.x2[j]);
-              }
-            }
-            Unit<T> o;
-            pack<INTER>(dx, &o);
-            o.store(h < a.H ? qo + h * a.sqo.h : ko + (h - a.H) * a.sko.h, e0, es);
+            pack<INTER>(y, &x);
           }
+          x.store(h < hk ? qo + h * D : h < hv ? ko + (h - hk) * a.c_head : vo + (h - hv) * a.c_head, e0, es);
         }
       });
-  // The block's share: lanes of the same unit, then its warps, in order.
-  __syncwarp();
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const Head16& s = which ? sk : sq;
-    constexpr int W = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float lo, hi, v = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (first_of<INTER>(q) == i) f2_unpack_f(s.x1[q / 2], lo, hi), v = q % 2 ? hi : lo;
-        if (second_of<INTER>(q) == i) f2_unpack_f(s.x2[q / 2], lo, hi), v = q % 2 ? hi : lo;
-      }
-#pragma unroll
-      for (int step = UNITS; step < 32; step *= 2) v += __shfl_xor_sync(0xffffffffu, v, step);
-      if (lane < UNITS) share[threadIdx.x / 32][which][e0 + i / W * es + i % W] = v;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += ROPE_THREADS) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < ROPE_THREADS / 32; ++w) v += share[w][i / D][i % D];
-    b.parts[static_cast<long long>(blockIdx.x) * 2 * D + i] = v;
-  }
 }
 
 // dw = the blocks' shares, added in a fixed order: a block has 32 elements, each warp every 8th share.
-__global__ void __launch_bounds__(256) fa_norm_rope_join_kernel(const float* parts, int n, int d, float* dwq, float* dwk) {
+__global__ void __launch_bounds__(256) fa_norm_rope_join_kernel(const float* parts, int n, int d, float* dwq,
+                                                                float* dwk) {
   __shared__ float sum[8][32];
   griddep_wait();
   const int i = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
+  const bool k = blockIdx.y > 0;
   float v = 0.f;
 #pragma unroll 8
-  for (int p = w; p < n; p += 8) v += parts[static_cast<long long>(p) * 2 * d + i];
+  for (int p = w; p < n; p += 8) v += parts[(static_cast<long long>(p) * 2 + k) * d + i];
   sum[w][threadIdx.x % 32] = v;
   __syncthreads();
   if (w > 0) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) v += sum[k][threadIdx.x];
-  float* const out = i < d ? dwq : dwk;
-  if (out != nullptr) out[i < d ? i : i - d] = v;
+  for (int j = 1; j < 8; ++j) v += sum[j][threadIdx.x];
+  (k ? dwk : dwq)[i] = v;
 }
 
-template <typename T, int D, bool QUAD>
-static cudaError_t launch_norm_q(const RopeLaunch& a, const HeadNorm& nm) {
-  Tiling g;
-  unsigned grid = 0;
+namespace {
+
+// The parameters of both directions, for items of up to `most` heads a lane and `blocks_sm` blocks a SM.
+template <typename T, int D>
+cudaError_t norm_params(const RopeLaunch& a, const HeadNorm& nm, int most, int blocks_sm, NormParams* p, unsigned* grid) {
   const long long tokens = static_cast<long long>(a.B) * a.N;
-  const cudaError_t e = tile<T, D, QUAD>(tokens, a.H + a.Hkv, a.sms, &g, &grid);
+  const long long warps = static_cast<long long>(a.sms) * blocks_sm * (ROPE_THREADS / 32);
+  long long items = 0;
+  for (int k = 0; k < 2; ++k) {
+    Heads& h = p->heads[k];
+    h.x = k ? a.k : a.q;
+    h.out = k ? a.k_out : a.q_out;
+    h.w = k ? nm.wk : nm.wq;
+    h.sx = k ? a.sk : a.sq;
+    h.so = k ? a.sko : a.sqo;
+    h.n = k ? a.Hkv : a.H;
+    h.quad = h.n > 3;
+    h.first_block = static_cast<int>(items);  // for now
+    if (h.n == 0) continue;
+    unsigned blocks = 0;
+    const long long share = warps * h.n / (a.H + a.Hkv);
+    const cudaError_t e = h.quad ? cut_items(tokens, h.n, most, share, Lane<D, true>::STEP, Lane<D, true>::TOKS, &h.g, &blocks)
+                                 : cut_items(tokens, h.n, most, share, Lane<D, false>::STEP, Lane<D, false>::TOKS, &h.g, &blocks);
+    if (e != cudaSuccess) return e;
+    items += h.g.count;
+  }
+  const int per_block = ROPE_THREADS / 32;
+  *grid = static_cast<unsigned>(((items < warps ? items : warps) + per_block - 1) / per_block);
+  p->heads[1].first_block = static_cast<int>(p->heads[0].g.count / per_block % *grid);  // behind the query heads' last item
+  p->r = a.r;
+  p->by_n = FastDiv(static_cast<unsigned>(a.N));
+  p->eps = nm.eps;
+  p->w_fp32 = nm.fp32;
+  p->N = a.N;
+  p->tokens = static_cast<int>(tokens);
+  p->err = a.err;
+  return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t launch_norm_d(const RopeLaunch& a, const HeadNorm& nm) {
+  NormParams p = {};
+  unsigned grid = 0;
+  const cudaError_t e = norm_params<T, D>(a, nm, FWD_SLOTS / Unit<T>::PIECES, FWD_BLOCKS, &p, &grid);
   if (e != cudaSuccess) return e;
-  const FastDiv by_n(static_cast<unsigned>(a.N));
-  return a.r.interleaved ? launch_items<fa_norm_rope_kernel<T, D, true, QUAD>>(grid, a.stream, a, nm, g, by_n)
-                         : launch_items<fa_norm_rope_kernel<T, D, false, QUAD>>(grid, a.stream, a, nm, g, by_n);
+  return a.r.interleaved ? launch_items<fa_norm_rope_kernel<T, D, true>, FWD_SLOTS>(grid, a.stream, p)
+                         : launch_items<fa_norm_rope_kernel<T, D, false>, FWD_SLOTS>(grid, a.stream, p);
 }
 
-template <typename T>
-static cudaError_t launch_norm_t(const RopeLaunch& a, const HeadNorm& nm) {
-  if (a.H + a.Hkv > 3) return a.d == 64 ? launch_norm_q<T, 64, true>(a, nm) : launch_norm_q<T, 128, true>(a, nm);
-  return a.d == 64 ? launch_norm_q<T, 64, false>(a, nm) : launch_norm_q<T, 128, false>(a, nm);
-}
-
-cudaError_t launch_norm_rope(const RopeLaunch& a, const HeadNorm& nm) {
-  return a.bf16 ? launch_norm_t<__nv_bfloat16>(a, nm) : launch_norm_t<float>(a, nm);
+template <typename T, int D>
+cudaError_t launch_bwd_d(const RopeLaunch& a, const NormBwd& b, const HeadNorm& nm) {
+  NormParams p = {};
+  unsigned grid = 0;
+  cudaError_t e = norm_params<T, D>(a, nm, BWD_SLOTS / (2 * Unit<T>::PIECES), BWD_BLOCKS, &p, &grid);
+  if (e != cudaSuccess) return e;
+  if (static_cast<int>(grid) > norm_bwd_parts(a.sms)) return cudaErrorInvalidValue;  // the workspace's room
+  for (int k = 0; k < 2; ++k) {
+    Heads& h = p.heads[k];
+    h.dy = h.x;
+    h.sdy = h.sx;
+    h.x = k ? b.k : b.q;
+    h.sx = k ? b.sk : b.sq;
+  }
+  p.parts = b.parts;
+  e = a.r.interleaved ? launch_items<fa_norm_rope_bwd_kernel<T, D, true>, BWD_SLOTS>(grid, a.stream, p)
+                      : launch_items<fa_norm_rope_bwd_kernel<T, D, false>, BWD_SLOTS>(grid, a.stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa_norm_rope_join_kernel, dim3(D / 32, a.Hkv > 0 ? 2 : 1), 256, 0, a.stream,
+                          static_cast<const float*>(b.parts), static_cast<int>(grid), D, b.dwq, b.dwk);
 }
 
 template <int D>
-static cudaError_t launch_norm_append_d(const AppendLaunch& a, const HeadNorm& nm) {
+cudaError_t launch_norm_append_d(const AppendLaunch& a, const HeadNorm& nm) {
   Tiling g;
   unsigned grid = 0;
   const cudaError_t e = tile<__nv_bfloat16, D, true>(a.T, a.H + 2 * a.Hkv, a.sms, &g, &grid);
@@ -442,36 +543,24 @@ static cudaError_t launch_norm_append_d(const AppendLaunch& a, const HeadNorm& n
                          : launch_items<fa_norm_append_kernel<D, false>>(grid, a.stream, a, nm, g, by_page);
 }
 
+}  // namespace
+
+cudaError_t launch_norm_rope(const RopeLaunch& a, const HeadNorm& nm) {
+  using bf = __nv_bfloat16;
+  if (a.bf16) return a.d == 64 ? launch_norm_d<bf, 64>(a, nm) : launch_norm_d<bf, 128>(a, nm);
+  return a.d == 64 ? launch_norm_d<float, 64>(a, nm) : launch_norm_d<float, 128>(a, nm);
+}
+
 cudaError_t launch_norm_append(const AppendLaunch& a, const HeadNorm& nm) {
   return a.d == 64 ? launch_norm_append_d<64>(a, nm) : launch_norm_append_d<128>(a, nm);
 }
 
-int norm_bwd_parts(int sms) { return sms * ROPE_BLOCKS; }
-
-template <typename T, int D, bool QUAD>
-static cudaError_t launch_bwd_q(const RopeLaunch& a, const NormBwd& b, const HeadNorm& nm) {
-  Tiling g;
-  unsigned grid = 0;
-  const long long tokens = static_cast<long long>(a.B) * a.N;
-  cudaError_t e = tile<T, D, QUAD, 2>(tokens, a.H + a.Hkv, a.sms, &g, &grid);
-  if (e != cudaSuccess) return e;
-  if (static_cast<int>(grid) > norm_bwd_parts(a.sms)) return cudaErrorInvalidValue;  // the workspace's room
-  const FastDiv by_n(static_cast<unsigned>(a.N));
-  e = a.r.interleaved ? launch_items<fa_norm_rope_bwd_kernel<T, D, true, QUAD>>(grid, a.stream, a, b, nm, g, by_n)
-                      : launch_items<fa_norm_rope_bwd_kernel<T, D, false, QUAD>>(grid, a.stream, a, b, nm, g, by_n);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(fa_norm_rope_join_kernel, dim3(2 * D / 32), 256, 0, a.stream, static_cast<const float*>(b.parts),
-                          static_cast<int>(grid), D, b.dwq, b.dwk);
-}
-
-template <typename T>
-static cudaError_t launch_bwd_t(const RopeLaunch& a, const NormBwd& b, const HeadNorm& nm) {
-  if (a.H + a.Hkv > 3) return a.d == 64 ? launch_bwd_q<T, 64, true>(a, b, nm) : launch_bwd_q<T, 128, true>(a, b, nm);
-  return a.d == 64 ? launch_bwd_q<T, 64, false>(a, b, nm) : launch_bwd_q<T, 128, false>(a, b, nm);
-}
+int norm_bwd_parts(int sms) { return sms * BWD_BLOCKS; }
 
 cudaError_t launch_norm_rope_bwd(const RopeLaunch& a, const NormBwd& b, const HeadNorm& nm) {
-  return a.bf16 ? launch_bwd_t<__nv_bfloat16>(a, b, nm) : launch_bwd_t<float>(a, b, nm);
+  using bf = __nv_bfloat16;
+  if (a.bf16) return a.d == 64 ? launch_bwd_d<bf, 64>(a, b, nm) : launch_bwd_d<bf, 128>(a, b, nm);
+  return a.d == 64 ? launch_bwd_d<float, 64>(a, b, nm) : launch_bwd_d<float, 128>(a, b, nm);
 }
 
 }  // namespace fa

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_rope_kernel(cons
   int e0, es;
   const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, QUAD>().u, &e0, &es);
   run_items<T, D, INTER, QUAD>(
-      g, a.r, pairs, rotated, tokens,
+      g, a.r, pairs, rotated, tokens, blockIdx.x, gridDim.x,
       [&](int t, int h0, uint32_t dst, uint32_t) {
         const int b = by_n.div(t), n = t - b * a.N;
         const T* const q = static_cast<const T*>(a.q) + b * a.sq.b + n * a.sq.n;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_paged_append_ker
   int e0, es;
   const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, true>().u, &e0, &es);
   run_items<T, D, INTER, true>(
-      g, a.r, pairs, rotated, a.T,
+      g, a.r, pairs, rotated, a.T, blockIdx.x, gridDim.x,
       [&](int t, int h0, uint32_t dst, uint32_t slot_dst) {
         const T* const q = static_cast<const T*>(a.q) + t * a.q_tok;
         const T* const k = static_cast<const T*>(a.k) + t * a.k_tok;

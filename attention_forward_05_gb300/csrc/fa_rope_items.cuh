@@ -232,16 +232,17 @@ struct Lane {
       : lane(threadIdx.x & 31), u(lane % UNITS), hl(QUAD ? lane / UNITS % 4 : 0), tok(lane / PER_TOKEN) {}
 };
 
-// A warp's stage of the ring: 8 pieces of data and a slot a lane, and the tokens' positions on up to 8 axes.
+// A warp's stage of the ring: pieces of data (8, or as many as `slots` says) and a slot a lane, and the tokens' positions on up
+// to 8 axes.
 constexpr int STAGES = 2;
 constexpr int PIECE_SLOTS = 8;
-constexpr int OFF_POS = PIECE_SLOTS * 512, OFF_SLOT = OFF_POS + 256, STAGE_BYTES = OFF_SLOT + 256;
-constexpr int ROPE_SMEM = ROPE_THREADS / 32 * STAGES * STAGE_BYTES;
+constexpr int stage_bytes(int slots) { return slots * 512 + 512; }
+constexpr int ring_bytes(int slots) { return ROPE_THREADS / 32 * STAGES * stage_bytes(slots); }
 
 struct Walk {
   int item, block, slice;
-  __device__ __forceinline__ Walk(const Tiling& g) {
-    item = blockIdx.x * (ROPE_THREADS / 32) + threadIdx.x / 32;
+  __device__ __forceinline__ Walk(const Tiling& g, int blk) {
+    item = blk * (ROPE_THREADS / 32) + threadIdx.x / 32;
     block = item / g.slices;
     slice = item - block * g.slices;
   }
@@ -258,19 +259,21 @@ struct Walk {
 };
 
 // Runs a warp's items.  fetch(token, first head, address, address of the slot): starts a lane's copies and returns where the
-// token's position on axis 0 is; finish(token, first head, pieces, slot, turn): rotates and stores them.
-template <typename T, int D, bool INTER, bool QUAD, typename Fetch, typename Finish>
+// token's position on axis 0 is; finish(token, first head, pieces, slot, turn): rotates and stores them.  Block `blk` of the
+// `blks` that share the items.
+template <typename T, int D, bool INTER, bool QUAD, int SLOTS = PIECE_SLOTS, typename Fetch, typename Finish>
 __device__ __forceinline__ void run_items(const Tiling& g, const Rotary& r, const PairTurn* pairs, bool rotated, int tokens,
-                                          Fetch fetch, Finish finish) {
+                                          int blk, int blks, Fetch fetch, Finish finish) {
+  constexpr int OFF_POS = SLOTS * 512, OFF_SLOT = OFF_POS + 256, STAGE_BYTES = stage_bytes(SLOTS);
   extern __shared__ __align__(128) uint8_t ring[];
   using L = Lane<D, QUAD>;
   const L l;
   uint8_t* const mine = ring + threadIdx.x / 32 * STAGES * STAGE_BYTES;
-  const int step = gridDim.x * (ROPE_THREADS / 32), step_block = step / g.slices, step_slice = step - step_block * g.slices;
+  const int step = blks * (ROPE_THREADS / 32), step_block = step / g.slices, step_slice = step - step_block * g.slices;
   const auto pair = [&](int q) { return pairs[unit_pair<T, INTER>(r.rot, l.u, q)]; };
   PairTurn p0{0, 255, 0}, p1{0, 255, 0};
   if (QUAD && rotated) p0 = pair(2 * l.hl), p1 = pair(2 * l.hl + 1);
-  Walk ld(g);
+  Walk ld(g, blk);
   int ld_stage = 0, stage = 0;
   auto load = [&]() {
     if (ld.item < g.count) {
@@ -291,9 +294,10 @@ __device__ __forceinline__ void run_items(const Tiling& g, const Rotary& r, cons
     ld.next(g, step, step_block, step_slice);
     ld_stage = ld_stage + 1 == STAGES ? 0 : ld_stage + 1;
   };
+  __syncwarp();  // the ring may have been read for items of another kind
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) load();
-  for (Walk w(g); w.item < g.count; w.next(g, step, step_block, step_slice)) {
+  for (Walk w(g, blk); w.item < g.count; w.next(g, step, step_block, step_slice)) {
     __syncwarp();  // the stage of the item before this one has been read
     load();
     cp_async_wait<STAGES - 1>();
@@ -322,6 +326,24 @@ __device__ __forceinline__ void run_items(const Tiling& g, const Rotary& r, cons
   }
 }
 
+// The cut itself: items for `resident` warps, of up to `most` heads a lane.
+static cudaError_t cut_items(long long tokens, int heads, int most, long long resident, int step, int toks, Tiling* g,
+                             unsigned* grid) {
+  const int warps = ROPE_THREADS / 32;
+  const long long blocks = (tokens + toks - 1) / toks;
+  long long count = 0;
+  for (int per = most;; per /= 2) {
+    g->slices = (heads + step * per - 1) / (step * per);
+    g->per = (heads + step * g->slices - 1) / (step * g->slices);  // parts alike
+    count = blocks * g->slices;
+    if (per == 1 || count >= resident) break;
+  }
+  if (count < 1 || count > 0x7FFFFFFF - STAGES * resident) return cudaErrorInvalidValue;
+  g->count = static_cast<int>(count);
+  *grid = static_cast<unsigned>(((count < resident ? count : resident) + warps - 1) / warps);
+  return cudaSuccess;
+}
+
 // Cuts `tokens` x `heads`: as many heads a lane, up to what its stage holds, as leave an item for every warp.  Large inputs
 // go faster with fewer blocks a SM, and so fewer places of device memory read and written at a time, as long as two full
 // stages a warp are on their way for each of two blocks: heads that fill only part of the lanes' stages need more blocks.
@@ -332,34 +354,22 @@ __device__ __forceinline__ void run_items(const Tiling& g, const Rotary& r, cons
 // cache full of unwritten lines, 35.5 / 31.4 / 31.4 with none; 48 heads of 128 appended, 34.7 / 34.5 / 35.4, 39.6 / 41.6 / 40.6 and
 // 37.5 / 33.4 / 31.4.  So three at least there, and four below 165 MB, where they are as good or better in every state (140 MB
 // of 20 heads of 128: 27.7 / 24.5 / 22.8 behind another launch).
-// IN: tensors of the heads' shape that are read.
-template <typename T, int D, bool QUAD, int IN = 1>
+template <typename T, int D, bool QUAD>
 static cudaError_t tile(long long tokens, int heads, int sms, Tiling* g, unsigned* grid) {
   using L = Lane<D, QUAD>;
-  const int warps = ROPE_THREADS / 32, most = PIECE_SLOTS / (IN * Unit<T>::PIECES);
-  const long long bytes = tokens * heads * D * static_cast<long long>((IN + 1) * sizeof(T));
+  const int warps = ROPE_THREADS / 32, most = PIECE_SLOTS / Unit<T>::PIECES;
+  const long long bytes = tokens * heads * D * static_cast<long long>(2 * sizeof(T));
   const long long room = (heads + L::STEP * most - 1) / (L::STEP * most) * static_cast<long long>(L::STEP * most);  // heads the stages hold
   const int full = static_cast<int>((4 * room + heads) / (2 * heads));  // 2 * room / heads, to the nearest
   const int least = bytes < 165000000 ? ROPE_BLOCKS : bytes < 256000000 ? 3 : 2;
   const int blocks_sm = full > ROPE_BLOCKS ? ROPE_BLOCKS : full > least ? full : least;
-  const long long resident = static_cast<long long>(sms) * blocks_sm * warps, blocks = (tokens + L::TOKS - 1) / L::TOKS;
-  long long count = 0;
-  for (int per = most;; per /= 2) {
-    g->slices = (heads + L::STEP * per - 1) / (L::STEP * per);
-    g->per = (heads + L::STEP * g->slices - 1) / (L::STEP * g->slices);  // parts alike
-    count = blocks * g->slices;
-    if (per == 1 || count >= resident) break;
-  }
-  if (count < 1 || count > 0x7FFFFFFF - STAGES * resident) return cudaErrorInvalidValue;
-  g->count = static_cast<int>(count);
-  *grid = static_cast<unsigned>(((count < resident ? count : resident) + warps - 1) / warps);
-  return cudaSuccess;
+  return cut_items(tokens, heads, most, static_cast<long long>(sms) * blocks_sm * warps, L::STEP, L::TOKS, g, grid);
 }
 
-template <auto kernel, typename... Args>
+template <auto kernel, int SLOTS = PIECE_SLOTS, typename... Args>
 static cudaError_t launch_items(unsigned grid, cudaStream_t stream, Args... args) {
-  const cudaError_t e = allow_shared_memory<kernel>(ROPE_SMEM);
-  return e != cudaSuccess ? e : launch_dependent(kernel, grid, ROPE_THREADS, ROPE_SMEM, stream, args...);
+  const cudaError_t e = allow_shared_memory<kernel>(ring_bytes(SLOTS));
+  return e != cudaSuccess ? e : launch_dependent(kernel, grid, ROPE_THREADS, ring_bytes(SLOTS), stream, args...);
 }
 
 }  // namespace rope
