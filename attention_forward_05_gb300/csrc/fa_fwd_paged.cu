@@ -50,7 +50,7 @@ struct ChunkCfg {
   static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
   static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_UNITS + UNITS * 64;
-  static constexpr int SMEM_BYTES = OFF_MISC + 144 + (32 * 11 + 2) * 8 + 1024;  // plan's scratch; slack to align the base to 1024
+  static constexpr int SMEM_BYTES = OFF_MISC + 160 + (32 * 11 + 2) * 8 + 1024;  // plan's scratch; slack to align the base to 1024
   static constexpr int O_COL0 = 2 * BC;          // TMEM: S_t at t * BC, O_t at O_COL0 + t * D
   static constexpr int TMEM_COLS = 2 * (BC + D);
   // The values have a load warp of their own at d = 128 (FwdCfg::SPLIT_LOADS); it comes free of registers there.
@@ -269,9 +269,9 @@ __global__ void __maxnreg__(C::MAXREG)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* const plan_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);             // head, block, ranges, extra, whole, sequence
-  long long* const plan_at = reinterpret_cast<long long*>(smem + C::OFF_MISC + 32);   // start, total
-  int* const plan_tmp = reinterpret_cast<int*>(smem + C::OFF_MISC + 48);              // 12 64-bit numbers
-  long long* const plan_place = reinterpret_cast<long long*>(smem + C::OFF_MISC + 144);
+  long long* const plan_at = reinterpret_cast<long long*>(smem + C::OFF_MISC + 32);   // start, total, range
+  int* const plan_tmp = reinterpret_cast<int*>(smem + C::OFF_MISC + 64);              // 12 64-bit numbers
+  long long* const plan_place = reinterpret_cast<long long*>(smem + C::OFF_MISC + 160);
 
   griddep_launch_dependents();
   if (tid == 0) {
@@ -393,7 +393,9 @@ __global__ void __maxnreg__(C::MAXREG)
       plan_start[0] = h;
       plan_start[1] = lo * max(pb, 1);  // block
       plan_at[0] = from;
+      plan_at[2] = w;
     }
+    if (my_range == static_cast<int>(blockIdx.x) + 1 && my_range <= ranges) plan_at[3] = w;
     if (tid == 0) {
       plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
       plan_start[3] = extra;
@@ -427,7 +429,7 @@ __global__ void __maxnreg__(C::MAXREG)
     };
     // the walk through the units (LOAD_WARP): lane i knows sequence base + i
     const long long total = plan_at[1];
-    const long long w0 = range_begin(total, blockIdx.x, ranges), w1 = range_begin(total, blockIdx.x + 1, ranges);
+    const long long w0 = plan_at[2], w1 = plan_at[3];
     long long at = plan_at[0];
     int h = plan_start[0], b = plan_start[5], blk = plan_start[1], base = -1;
     const int extra = plan_start[3];
@@ -514,29 +516,40 @@ __global__ void __maxnreg__(C::MAXREG)
         const int* const table = p.table + u.b * p.table_stride;
         // Sets values aside and zeroes those that no row sees, in the tile's rows that not every row of Q sees.
         const auto clean = [&](uint32_t dv, int key0) {
-          const auto rows = [&](int r0, int r1) {
-            for (int i = r0 * C::NCH * 8 + lane; i < r1 * C::NCH * 8; i += 32) {
-              const int r = i / (C::NCH * 8), pc = i % (C::NCH * 8), key = key0 + r;
-              uint4* const at16 = reinterpret_cast<uint4*>(smem + (dv - sbase) + pc / 8 * C::KV_CH_BYTES + r * 128 + pc % 8 * 16);
-              if (!used(key)) {
-                *at16 = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 w = *at16;
-              uint32_t* const ws = &w.x;
-              const uint32_t f0 = not_finite(w.x), f1 = not_finite(w.y), f2 = not_finite(w.z), f3 = not_finite(w.w);
-              if (f0 | f1 | f2 | f3) {
-                const uint32_t f[4] = {f0, f1, f2, f3};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  ws[e] &= ~(((f[e] & 0x8000u) ? 0xFFFFu : 0u) | ((f[e] & 0x80000000u) ? 0xFFFF0000u : 0u));
-                *at16 = w;
+          constexpr int PIECES = C::NCH * 8;  // 16-byte pieces of a row, which lie in its 128-byte segments in some order
+          uint8_t* const tile = smem + (dv - sbase);
+          const auto at16 = [&](int i) {
+            const int r = i / PIECES, pc = i % PIECES;
+            return reinterpret_cast<uint4*>(tile + pc / 8 * C::KV_CH_BYTES + r * 128 + pc % 8 * 16);
+          };
+          const auto zero = [&](int r0, int r1) {
+#pragma unroll 4
+            for (int i = r0 * PIECES + lane; i < r1 * PIECES; i += 32) *at16(i) = make_uint4(0, 0, 0, 0);
+          };
+          const auto check = [&](int r0, int r1) {
+#pragma unroll 4
+            for (int i = r0 * PIECES + lane; i < r1 * PIECES; i += 32) {
+              uint4 w = *at16(i);
+              const uint32_t f[4] = {not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w)};
+              if (f[0] | f[1] | f[2] | f[3]) {
+                const auto keep = [](uint32_t x, uint32_t f) {
+                  return x & ~(((f & 0x8000u) ? 0xFFFFu : 0u) | ((f & 0x80000000u) ? 0xFFFF0000u : 0u));
+                };
+                w.x = keep(w.x, f[0]);
+                w.y = keep(w.y, f[1]);
+                w.z = keep(w.z, f[2]);
+                w.w = keep(w.w, f[3]);
+                *at16(i) = w;
                 *reinterpret_cast<volatile int*>(&units[slot].set_aside) = 1;
               }
             }
           };
-          rows(0, min(BC, max(0, last_lo - key0)));
-          rows(min(BC, max(0, u.pos0 + 1 - key0)), BC);
+          const auto clip = [&](int key) { return min(BC, max(0, key - key0)); };
+          const int s0 = clip(sinks), l0 = clip(u.lo), l1 = clip(last_lo), p0 = clip(u.pos0 + 1), p1 = clip(u.hi);
+          if (s0 < l0) zero(s0, l0);                          // behind the sinks, before every window
+          if (max(s0, l0) < l1) check(max(s0, l0), l1);       // in some tokens' windows
+          check(p0, p1);                                      // the block's own tokens
+          zero(p1, BC);                                       // behind the last one
         };
         const auto has_edge = [&](int key0) {
           return key0 + BC > u.pos0 + 1 || (key0 < last_lo && key0 + BC > sinks);
