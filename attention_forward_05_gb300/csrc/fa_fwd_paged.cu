@@ -49,7 +49,10 @@ struct ChunkCfg {
   static constexpr int UNITS = 4;                // units announced at a time
   static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
   static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_MISC = OFF_UNITS + UNITS * 64;
+  static constexpr int OUT_COLS = D == 128 ? 32 : 16;  // columns of the outputs that a softmax warp has on their way at a time
+  static constexpr int STAGE_BYTES = 32 * OUT_COLS * 2;
+  static constexpr int OFF_STAGE = OFF_UNITS + UNITS * 64;
+  static constexpr int OFF_MISC = OFF_STAGE + 8 * STAGE_BYTES;
   static constexpr int SMEM_BYTES = OFF_MISC + 160 + (32 * 11 + 2) * 8 + 1024;  // plan's scratch; slack to align the base to 1024
   static constexpr int O_COL0 = 2 * BC;          // TMEM: S_t at t * BC, O_t at O_COL0 + t * D
   static constexpr int TMEM_COLS = 2 * (BC + D);
@@ -976,25 +979,45 @@ __global__ void __maxnreg__(C::MAXREG)
       if (!any_rows) {
         // a block of one tile
       } else if (kind == UNIT_WHOLE || kind == UNIT_BAD) {
+        // A thread holds a row: written straight from there, a warp's 16 bytes a lane would touch 32 half sectors.  So OUT_COLS
+        // columns at a time go through shared memory (16-byte pieces swapped by the row) and out in whole sectors.
+        constexpr int PCS = C::OUT_COLS / 8, RPI = 32 / PCS;  // pieces of a row, rows a store
         const float inv_l = 1.f / l;
         const size_t out = static_cast<size_t>(uv.q0 + tok) * p.H + uv.h * p.G + g;
+        uint8_t* const stage = smem + C::OFF_STAGE + warp * C::STAGE_BYTES;
+        const int piece = lane % PCS;
+        const auto at16 = [&](int r, int pc) { return reinterpret_cast<uint4*>(stage + r * (PCS * 16) + ((pc ^ (r / (8 / PCS) % PCS)) << 4)); };
+        __nv_bfloat16* rows[PCS];  // that this lane writes pieces of
+#pragma unroll
+        for (int i = 0; i < PCS; ++i) {
+          const int r = wq * 32 + i * RPI + lane / PCS, rt = p.by_g.div(r), tk = t * p.tile_tokens + rt;
+          rows[i] = rt < p.tile_tokens && tk < ntok
+                        ? p.o + (static_cast<size_t>(uv.q0 + tk) * p.H + uv.h * p.G + r - rt * p.G) * D + piece * 8
+                        : nullptr;
+        }
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t orr[32];
           tmem_ld32(tO + cc * 32, orr);
           tmem_wait_ld();
           reg_fence(orr);
-          if (real) {
-            uint4* const dst = reinterpret_cast<uint4*>(p.o + out * D + cc * 32);
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(orr[8 * v4 + 0]) * inv_l, __uint_as_float(orr[8 * v4 + 1]) * inv_l);
-              w.y = pack_bf16x2(__uint_as_float(orr[8 * v4 + 2]) * inv_l, __uint_as_float(orr[8 * v4 + 3]) * inv_l);
-              w.z = pack_bf16x2(__uint_as_float(orr[8 * v4 + 4]) * inv_l, __uint_as_float(orr[8 * v4 + 5]) * inv_l);
-              w.w = pack_bf16x2(__uint_as_float(orr[8 * v4 + 6]) * inv_l, __uint_as_float(orr[8 * v4 + 7]) * inv_l);
-              dst[v4] = w;
+          for (int half = 0; half < 32 / C::OUT_COLS; ++half) {
+#pragma unroll
+            for (int v4 = 0; v4 < PCS; ++v4) {
+              const auto two = [&](int e) {
+                const int at = half * C::OUT_COLS + 8 * v4 + e;
+                return pack_bf16x2(__uint_as_float(orr[at]) * inv_l, __uint_as_float(orr[at + 1]) * inv_l);
+              };
+              *at16(lane, v4) = make_uint4(two(0), two(2), two(4), two(6));
             }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PCS; ++i) {
+              const uint4 w = *at16(i * RPI + lane / PCS, piece);
+              if (rows[i] != nullptr) *reinterpret_cast<uint4*>(rows[i] + cc * 32 + half * C::OUT_COLS) = w;
+            }
+            __syncwarp();
           }
         }
         if (p.lse != nullptr && real) p.lse[out] = (m_ref + log2f(l)) * 0.6931471805599453f;
@@ -1053,25 +1076,39 @@ __global__ void __launch_bounds__(D * 4) fa_fwd_paged_join_kernel(const ChunkPar
   const auto part = [&](int i) {
     return static_cast<size_t>(c + i) * 2 * p.part_tiles + (i == 0 ? p.part_tiles : 0) + t;
   };
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < u.parts; ++i) m = fmaxf(m, p.part_ml[part(i) * p.part_rows + row].x);
-  float o[8] = {}, l = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < u.parts; ++i) {
-    const float2 ml = p.part_ml[part(i) * p.part_rows + row];
+  const auto load_ml = [&](int i) { return p.part_ml[part(i) * p.part_rows + row]; };
+  const auto load_o = [&](int i, float4 (&x)[2]) {
     const float4* const po = p.part_o + (part(i) * (D / 4) + col8 * 2) * p.part_rows + row;
-    const float4 x = po[0], y = po[p.part_rows];
+    x[0] = po[0];
+    x[1] = po[p.part_rows];
+  };
+  // the first two parts' loads (there are two at least) all at once
+  const float2 ml0 = load_ml(0), ml1 = load_ml(1);
+  float4 x0[2], x1[2];
+  load_o(0, x0);
+  load_o(1, x1);
+  float m = fmaxf(ml0.x, ml1.x);
+#pragma unroll 8
+  for (int i = 2; i < u.parts; ++i) m = fmaxf(m, load_ml(i).x);
+  float o[8] = {}, l = 0.f;
+  const auto add = [&](const float2& ml, const float4 (&x)[2]) {
     const float w = ex2_approx(ml.x - m);
-    o[0] = fmaf(w, x.x, o[0]);
-    o[1] = fmaf(w, x.y, o[1]);
-    o[2] = fmaf(w, x.z, o[2]);
-    o[3] = fmaf(w, x.w, o[3]);
-    o[4] = fmaf(w, y.x, o[4]);
-    o[5] = fmaf(w, y.y, o[5]);
-    o[6] = fmaf(w, y.z, o[6]);
-    o[7] = fmaf(w, y.w, o[7]);
+    o[0] = fmaf(w, x[0].x, o[0]);
+    o[1] = fmaf(w, x[0].y, o[1]);
+    o[2] = fmaf(w, x[0].z, o[2]);
+    o[3] = fmaf(w, x[0].w, o[3]);
+    o[4] = fmaf(w, x[1].x, o[4]);
+    o[5] = fmaf(w, x[1].y, o[5]);
+    o[6] = fmaf(w, x[1].z, o[6]);
+    o[7] = fmaf(w, x[1].w, o[7]);
     l = fmaf(w, ml.y, l);
+  };
+  add(ml0, x0);
+  add(ml1, x1);
+#pragma unroll 8
+  for (int i = 2; i < u.parts; ++i) {
+    load_o(i, x0);
+    add(load_ml(i), x0);
   }
   const float inv = 1.f / l;
   const size_t out = static_cast<size_t>(u.q0 + tok) * p.H + u.h * p.G + g;
