@@ -106,12 +106,17 @@ __device__ __forceinline__ int cut(long long w, long long start, int tiles, int 
   const long long x = w - start - extra;
   return x <= 0 ? 0 : x >= tiles ? tiles : static_cast<int>(x);
 }
-__device__ __forceinline__ long long range_begin(long long total, int c, int ranges) { return static_cast<long long>(static_cast<unsigned long long>(total * c) / static_cast<unsigned>(ranges)); }
+// a / b of numbers >= 0, which are nearly always short.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return static_cast<long long>(static_cast<unsigned long long>(a) / static_cast<unsigned long long>(b));
+}
+__device__ __forceinline__ long long range_begin(long long total, int c, int ranges) { return divide(total * c, ranges); }
 // The last range that has tiles of it: the largest i with range_begin(i) before its last tile's place.  Every range between
 // has some: a range is a tile long at least.
 __device__ __forceinline__ int last_range(long long total, int ranges, long long start, int tiles, int extra) {
   const long long w = start + extra + tiles - 1;
-  return static_cast<int>(min(ranges - 1LL, ((w + 1) * ranges - 1) / total));
+  return static_cast<int>(min(ranges - 1LL, divide((w + 1) * ranges - 1, total)));
 }
 
 // A sequence's new tokens, as far as its offsets and length make sense.
@@ -372,7 +377,7 @@ __global__ void __maxnreg__(C::MAXREG)
     int h = 0, lo = 0;
     if (ranges > 0 && my_range <= ranges) {
       w = range_begin(total, my_range, ranges);
-      h = static_cast<int>(static_cast<unsigned long long>(w) / static_cast<unsigned long long>(head));
+      h = static_cast<int>(divide(w, head));
       const long long rem = w - h * head;
       int hi = pb > 1 ? (blocks + pb - 1) / pb : blocks;
       while (hi - lo > 1) {
@@ -389,7 +394,7 @@ __global__ void __maxnreg__(C::MAXREG)
       __syncthreads();
       if (my_range <= ranges) place[my_range] = my_range == ranges ? total : begin;
       __syncthreads();
-      const bool fits = my_range >= ranges || place[my_range + 1] - place[my_range] <= total / max(ranges, 1) + COST_CUT;
+      const bool fits = my_range >= ranges || place[my_range + 1] - place[my_range] <= divide(total, max(ranges, 1)) + COST_CUT;
       whole = __syncthreads_and(fits);
     }
     if (my_range == static_cast<int>(blockIdx.x) && my_range < ranges) {
@@ -530,21 +535,23 @@ __global__ void __maxnreg__(C::MAXREG)
             for (int i = r0 * PIECES + lane; i < r1 * PIECES; i += 32) *at16(i) = make_uint4(0, 0, 0, 0);
           };
           const auto check = [&](int r0, int r1) {
-#pragma unroll 4
-            for (int i = r0 * PIECES + lane; i < r1 * PIECES; i += 32) {
-              uint4 w = *at16(i);
-              const uint32_t f[4] = {not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w)};
-              if (f[0] | f[1] | f[2] | f[3]) {
-                const auto keep = [](uint32_t x, uint32_t f) {
-                  return x & ~(((f & 0x8000u) ? 0xFFFFu : 0u) | ((f & 0x80000000u) ? 0xFFFF0000u : 0u));
-                };
-                w.x = keep(w.x, f[0]);
-                w.y = keep(w.y, f[1]);
-                w.z = keep(w.z, f[2]);
-                w.w = keep(w.w, f[3]);
-                *at16(i) = w;
-                *reinterpret_cast<volatile int*>(&units[slot].set_aside) = 1;
-              }
+#pragma unroll 1
+            for (int i0 = r0 * PIECES + lane; i0 < r1 * PIECES; i0 += 128) {  // four loads on their way at a time
+              uint4 w[4];
+              uint32_t any = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = i0 + 32 * k < r1 * PIECES ? *at16(i0 + 32 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) any |= not_finite(w[k].x) | not_finite(w[k].y) | not_finite(w[k].z) | not_finite(w[k].w);
+              if (any == 0) continue;
+              const auto keep = [](uint32_t x) {
+                const uint32_t f = not_finite(x);
+                return x & ~(((f & 0x8000u) ? 0xFFFFu : 0u) | ((f & 0x80000000u) ? 0xFFFF0000u : 0u));
+              };
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (i0 + 32 * k < r1 * PIECES) *at16(i0 + 32 * k) = make_uint4(keep(w[k].x), keep(w[k].y), keep(w[k].z), keep(w[k].w));
+              *reinterpret_cast<volatile int*>(&units[slot].set_aside) = 1;
             }
           };
           const auto clip = [&](int key) { return min(BC, max(0, key - key0)); };
@@ -1088,8 +1095,12 @@ __global__ void __launch_bounds__(D * 4) fa_fwd_paged_join_kernel(const ChunkPar
   load_o(0, x0);
   load_o(1, x1);
   float m = fmaxf(ml0.x, ml1.x);
-#pragma unroll 8
-  for (int i = 2; i < u.parts; ++i) m = fmaxf(m, load_ml(i).x);
+  for (int i = 2; i < u.parts; i += 4) {  // four at a time, the last one again where there are fewer
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = load_ml(min(i + k, u.parts - 1)).x;
+    m = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+  }
   float o[8] = {}, l = 0.f;
   const auto add = [&](const float2& ml, const float4 (&x)[2]) {
     const float w = ex2_approx(ml.x - m);
@@ -1105,10 +1116,17 @@ __global__ void __launch_bounds__(D * 4) fa_fwd_paged_join_kernel(const ChunkPar
   };
   add(ml0, x0);
   add(ml1, x1);
-#pragma unroll 8
-  for (int i = 2; i < u.parts; ++i) {
-    load_o(i, x0);
-    add(load_ml(i), x0);
+  for (int i = 2; i < u.parts; i += 4) {
+    float2 ml[4];
+    float4 x[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ml[k] = load_ml(min(i + k, u.parts - 1));
+      load_o(min(i + k, u.parts - 1), x[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < u.parts) add(ml[k], x[k]);
   }
   const float inv = 1.f / l;
   const size_t out = static_cast<size_t>(u.q0 + tok) * p.H + u.h * p.G + g;
