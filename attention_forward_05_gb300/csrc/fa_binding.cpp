@@ -464,15 +464,27 @@ PyObject* slots(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     if (table->stride(1) != 1 && max_pages > 1 && B > 0) throw ValueError("page_table's rows must be contiguous");
     const int ps = as_int(in[5], "page_size"), T = as_int(in[6], "tokens");
     const int64_t sizes[5] = {B + 1, T, T, B, 1};
-    Tensor made[5];
+    Tensor made[5], whole;
     void* ptr[5];
+    // New outputs lie in one allocation: five of a few bytes would take longer to allocate than to fill.
+    int64_t bytes = 0, offset[5];
+    for (int i = 0; i < 5; ++i) {
+      offset[i] = bytes;
+      if (!out[i]) bytes += (sizes[i] * (i == 2 ? 8 : 4) + 15) / 16 * 16;
+    }
+    if (bytes > 0) whole = empty_like_shape({bytes}, *ctx, at::kByte);
     for (int i = 0; i < 5; ++i) {
       const at::ScalarType type = i == 2 ? at::kLong : at::kInt;
       if (!out[i]) {
-        made[i] = empty_like_shape({sizes[i]}, *ctx, type);
+        made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()),
+                                                           c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                           c10::scalarTypeToTypeMeta(type));
+        made[i].unsafeGetTensorImpl()->set_storage_offset(offset[i] / (i == 2 ? 8 : 4));
+        made[i].unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
         out[i].t = &made[i];
+      } else {
+        vector(out[i], sizes[i], type);
       }
-      vector(out[i], sizes[i], type);
       ptr[i] = out[i].ptr();
     }
     const int Bi = as_int(B, "B"), mp = as_int(max_pages, "max_pages"), n_free = as_int(pages->size(0), "free_pages");

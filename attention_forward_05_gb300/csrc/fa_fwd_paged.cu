@@ -46,6 +46,10 @@ struct ChunkCfg {
   static constexpr int Q_CH_BYTES = BR * 128, KV_CH_BYTES = BC * 128;
   static constexpr int Q_BYTES = NCH * Q_CH_BYTES, KV_BYTES = NCH * KV_CH_BYTES;
   static constexpr int OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + STAGES * KV_BYTES, OFF_BAR = OFF_V + STAGES * KV_BYTES;
+  // The dealing counts key tiles.  A unit's start and end take about as long as this many of them, whether it has one row
+  // tile or two (a step of one is bound by its chain of products and exponentials, or by the tile's bytes).  A prompt of 8191
+  // tokens, d = 128, with 2, 3, 4: 371, 357, 362 us; a mixed batch, d = 64: 88, 83, 79.
+  static constexpr int COST_UNIT = D == 128 ? 3 : 4;
   static constexpr int UNITS = 4;                // units announced at a time
   static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
   static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
@@ -67,9 +71,6 @@ struct ChunkCfg {
   static_assert((FWD_PAGED_MAX_B + 1) * 4 <= OFF_BAR, "the plan's block counts lie where the tiles will");
 };
 
-// The dealing counts key tiles.  A unit's start and end take about as long as COST_UNIT of them, whether it has one row tile
-// or two (a step of one is bound by its chain of products and exponentials, or by the tile's bytes).
-constexpr int COST_UNIT = 4;
 // Cutting units costs their states, written and read again, and a start and an end more: so no unit is cut where the
 // longest range of whole units is at most this much longer than an even share.
 constexpr int COST_CUT = 6;
@@ -360,7 +361,7 @@ __global__ void __maxnreg__(C::MAXREG)
     const long long before = scan<NT>(tiles, reinterpret_cast<long long*>(plan_tmp), &head);
     // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
     // each takes one, and starts and ends do not count.
-    const int extra = head * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : COST_UNIT;
+    const int extra = head * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
     long long* const place = plan_place;  // of each thread's first block in its head, and the head's end
     place[tid] = before + static_cast<long long>(extra) * x0;
     head += static_cast<long long>(extra) * blocks;

@@ -39,7 +39,7 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, i
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// The same in clusters of `cluster` CTAs (a divisor of the grid, at most 8).
+// The same in clusters of `cluster` CTAs (a divisor of the grid; above 8 the kernel has to allow it).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), unsigned grid, int cluster, int threads, int smem,
                                       cudaStream_t stream, Args&&... args) {

@@ -5,8 +5,8 @@
 // (where a sequence's tokens begin) and of the pages it needs, ceil((ctx_b + n_b) / P) - ceil(ctx_b / P) (how far down the
 // stack of free pages its own begin).  A token then finds its sequence by bisection and its slot by itself.
 //
-// One cluster of up to 8 CTAs.  Every CTA forms both sums over all sequences in its shared memory (12 bytes a sequence)
-// and takes every 8th piece of the tokens, so no CTA waits for another's sums; the cluster's barrier stands between the
+// One cluster of up to 16 CTAs (what one SM writes at a time, about 25 GB/s, bounds steps of many tokens).  Every CTA forms both sums over all sequences in its shared memory (12 bytes a sequence)
+// and takes its pieces of the tokens, so no CTA waits for another's sums; the cluster's barrier stands between the
 // last read of the lengths and the free pages' count and the writes of the new ones, which may go to the same memory.
 // A few thousand bytes: bound by the launch and four dependent round trips to memory.
 #include "fa_internal.h"
@@ -17,7 +17,7 @@ namespace fa {
 namespace {
 
 constexpr int THREADS = 1024;
-constexpr int MAX_CTAS = 8;
+constexpr int MAX_CTAS = 16;  // of the cluster (above 8 it has to be asked for)
 enum : int { W_STEP = 0x40 };  // site recorded with DEV_BAD_INDEX
 
 // Exclusive prefix sums of the threads' values, and the total; `tmp` is shared, [THREADS / 32 + 1].
@@ -51,6 +51,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* tmp, lon
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+template <int RUN>
 __global__ void __launch_bounds__(THREADS) fa_slots_kernel(const SlotsLaunch a, const FastDiv by_page, int ctas) {
   extern __shared__ int tables[];
   int* const s_start = tables;             // first token of each sequence (its new length until the first sum)
@@ -124,45 +125,84 @@ __global__ void __launch_bounds__(THREADS) fa_slots_kernel(const SlotsLaunch a, 
       if (s_bad || free_count < 0) record_bad_index(a.err, W_STEP);
     }
   }
-  for (int t = rank * THREADS + tid; t < a.T; t += ctas * THREADS) {
+  // The last sequence that begins at or before token t: those without tokens begin where the next one does.
+  const auto sequence_of = [&](int t) {
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_start[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  // Page pi of sequence b, which has `held` already; a new one also goes into its table where `mine`.
+  const auto page_of = [&](int b, int pi, int held, bool mine) {
+    int* const entry = a.page_table + b * a.table_stride + pi;
+    if (pi < held) return *entry;
+    const int page = a.free_pages[free_count - 1 - (s_base[b] + pi - held)];
+    if (mine) *entry = page;
+    return page;
+  };
+  const auto slot_of = [&](int page, int row) { return page < 0 ? -1LL : static_cast<long long>(page) * a.page_size + row; };
+  const auto one = [&](int t) {
     int pos = 0;
     long long slot = -1;
     if (t < tokens) {
-      int lo = 0, hi = a.B;  // the last sequence that begins at or before t: sequences without tokens begin where the next does
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_start[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      const int ctx = s_ctx[lo], base = s_base[lo];
-      if (base >= 0) {
-        pos = ctx + (t - s_start[lo]);
-        const int pi = by_page.div(pos), held = pages_of(ctx), row = pos - pi * a.page_size;
-        int* const entry = a.page_table + lo * a.table_stride + pi;
-        int page;
-        if (pi < held) {
-          page = *entry;
-        } else {
-          page = a.free_pages[free_count - 1 - (base + pi - held)];
-          if (row == 0) *entry = page;
-        }
-        slot = page < 0 ? -1 : static_cast<long long>(page) * a.page_size + row;
+      const int b = sequence_of(t);
+      if (s_base[b] >= 0) {
+        pos = s_ctx[b] + (t - s_start[b]);
+        const int pi = by_page.div(pos), row = pos - pi * a.page_size;
+        slot = slot_of(page_of(b, pi, pages_of(s_ctx[b]), row == 0), row);  // a page whose first row is a new token's is new
       }
     }
     a.positions[t] = pos;
     a.slots[t] = slot;
+  };
+  if (RUN == 1) {
+    for (int t = rank * THREADS + tid; t < a.T; t += ctas * THREADS) one(t);
+  } else {
+    // RUN neighbouring tokens a thread: of one sequence, they lie in two pages at most.
+    const bool wide = ((reinterpret_cast<unsigned long long>(a.positions) | reinterpret_cast<unsigned long long>(a.slots)) & 15) == 0;
+    for (int t = (rank * THREADS + tid) * RUN; t < a.T; t += ctas * THREADS * RUN) {
+      const int b = t < tokens ? sequence_of(t) : 0;
+      const int end = t >= tokens ? 0 : b + 1 < a.B ? s_start[b + 1] : tokens;
+      if (!wide || t + RUN > end || s_base[b] < 0) {
+        for (int e = 0; e < RUN && t + e < a.T; ++e) one(t + e);
+        continue;
+      }
+      const int pos = s_ctx[b] + (t - s_start[b]), pi = by_page.div(pos), row = pos - pi * a.page_size, held = pages_of(s_ctx[b]);
+      const bool second = row + RUN > a.page_size;
+      const int page0 = page_of(b, pi, held, row == 0), page1 = second ? page_of(b, pi + 1, held, true) : 0;
+      long long slot[RUN];
+#pragma unroll
+      for (int e = 0; e < RUN; ++e)
+        slot[e] = row + e < a.page_size ? slot_of(page0, row + e) : slot_of(page1, row + e - a.page_size);
+#pragma unroll
+      for (int e = 0; e < RUN; e += 4) {
+        *reinterpret_cast<int4*>(a.positions + t + e) = make_int4(pos + e, pos + e + 1, pos + e + 2, pos + e + 3);
+        reinterpret_cast<longlong2*>(a.slots + t + e)[0] = make_longlong2(slot[e], slot[e + 1]);
+        reinterpret_cast<longlong2*>(a.slots + t + e)[1] = make_longlong2(slot[e + 2], slot[e + 3]);
+      }
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_slots(const SlotsLaunch& a) {
-  int ctas = (a.T + 2 * THREADS - 1) / (2 * THREADS);
-  ctas = ctas < 1 ? 1 : ctas > MAX_CTAS ? MAX_CTAS : ctas;
-  const cudaError_t e = allow_shared_memory<fa_slots_kernel>(12 * SLOTS_MAX_B);
+template <int RUN>
+static cudaError_t launch_run(const SlotsLaunch& a) {
+  const int need = (a.T + RUN * THREADS - 1) / (RUN * THREADS), ctas = need < 1 ? 1 : need > MAX_CTAS ? MAX_CTAS : need;
+  cudaError_t e = allow_shared_memory<fa_slots_kernel<RUN>>(12 * SLOTS_MAX_B);
+  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(fa_slots_kernel<RUN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  return launch_dependent_clusters(fa_slots_kernel, static_cast<unsigned>(ctas), ctas, THREADS, 12 * a.B, a.stream, a,
+  return launch_dependent_clusters(fa_slots_kernel<RUN>, static_cast<unsigned>(ctas), ctas, THREADS, 12 * a.B, a.stream, a,
                                    FastDiv(static_cast<unsigned>(a.page_size)), ctas);
+}
+
+// One token a thread as long as the cluster has threads for it; then four, whose pages are looked up once, where four rows lie
+// in two pages at most.
+cudaError_t launch_slots(const SlotsLaunch& a) {
+  return a.T <= MAX_CTAS * THREADS || a.page_size < 4 ? launch_run<1>(a) : launch_run<4>(a);
 }
 
 }  // namespace fa

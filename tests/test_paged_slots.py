@@ -48,6 +48,7 @@ def compare(t, out, err, want):
 @pytest.mark.parametrize("B,ps,ctx_hi,new_hi", [
     (1, 16, 0, 1), (1, 1, 5, 3), (3, 16, 100, 40), (37, 24, 500, 1), (256, 64, 4000, 1), (1000, 16, 50, 9), (2049, 16, 40, 3),
     (16384, 8, 3, 2), (5, 16, 20, 9000), (61, 1, 30, 60), (64, 128, 0, 700),
+    (61, 16, 700, 4000), (700, 8, 90, 60), (3, 7, 11, 9001), (300, 24, 5, 100),
 ])
 def test_equals_the_rules(cuda_device, B, ps, ctx_hi, new_hi):
     ctx, new, table, free, count, T = make(B, ps, -(-(ctx_hi + new_hi) // ps) + 1, ctx_hi, new_hi, B + ps)
