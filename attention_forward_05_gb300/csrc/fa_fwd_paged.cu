@@ -920,24 +920,23 @@ __global__ void __maxnreg__(C::MAXREG)
           return true;
         };
         if (started && full && fast()) continue;
-        // The general path, a chunk of 32 columns at a time: the maximum, then P.
-        uint32_t sr[1][32];
-        const auto chunk = [&](int cc) {
-          tmem_ld32(tS + cc * 32, sr[0]);
-          tmem_wait_ld();
-          reg_fence(sr[0]);
+        // The general path: the maximum of the columns that the row sees, then P.
+        uint32_t sr[BC / 32][32];
+#pragma unroll
+        for (int cc = 0; cc < BC / 32; ++cc) tmem_ld32(tS + cc * 32, sr[cc]);
+        tmem_wait_ld();
+        float m_new = m_ref;
+#pragma unroll
+        for (int cc = 0; cc < BC / 32; ++cc) {
+          reg_fence(sr[cc]);
           if (!full) {
             const uint32_t vis = low_bits(valid - 32 * cc) & (~low_bits(first - 32 * cc) | low_bits(sink - 32 * cc));
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(vis >> e & 1u)) sr[0][e] = hidden;
+              if (!(vis >> e & 1u)) sr[cc][e] = hidden;
           }
-        };
-        float m_new = m_ref;
-#pragma unroll
-        for (int cc = 0; cc < BC / 32; ++cc) {
-          chunk(cc);
-          m_new = fmaxf(m_new, (c >= 0.f ? row_extreme<32, true>(sr) : row_extreme<32, false>(sr)) * c);
+          auto& one = reinterpret_cast<uint32_t(&)[1][32]>(sr[cc]);
+          m_new = fmaxf(m_new, (c >= 0.f ? row_extreme<32, true>(one) : row_extreme<32, false>(one)) * c);
         }
         const bool need = m_new > m_ref + p.tau;  // always true on the first tile that a row sees
         float alpha = 1.f;
@@ -948,15 +947,12 @@ __global__ void __maxnreg__(C::MAXREG)
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen nothing: 2^(-inf - 0) = 0
         const uint64_t negm2 = f2_pack(-m_use, -m_use);
         uint64_t rs[2] = {0ull, 0ull};
-        if (j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
-        // chunk cc's 16 packed columns go over columns 16 cc .. 16 cc + 15 of S, which hold chunk cc / 2 (already read)
 #pragma unroll
         for (int cc = 0; cc < BC / 32; ++cc) {
-          chunk(cc);
           uint32_t pk[32];
 #pragma unroll
           for (int qc = 0; qc < 16; ++qc) {
-            const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[0][2 * qc]), __uint_as_float(sr[0][2 * qc + 1])), c2, negm2);
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[cc][2 * qc]), __uint_as_float(sr[cc][2 * qc + 1])), c2, negm2);
             float x0, x1;
             f2_unpack_f(x, x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -964,7 +960,11 @@ __global__ void __maxnreg__(C::MAXREG)
             pk[qc] = pack_bf16x2(p0, p1);
           }
           tmem_st16_lo(tS + cc * 16, pk);
-          if (C::PV2 && cc == BC / 64 - 1) hand_over(bar_ph(t));
+          if (cc == BC / 64 - 1 || BC == 64) {
+            // the correction of O, before the first product that adds to it
+            if ((C::PV2 || cc == BC / 32 - 1) && j > 0 && __any_sync(0xffffffffu, need)) rescale(alpha);
+            if (C::PV2) hand_over(bar_ph(t));
+          }
         }
         hand_over(bar_pf(t));
         float r0, r1, r2, r3;
