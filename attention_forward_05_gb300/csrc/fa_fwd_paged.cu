@@ -88,7 +88,7 @@ struct ChunkParams {
   int* err;
   float4* part_o;    // [CTA][continued, begun][row tile][D / 4][part_rows]
   float2* part_ml;   // [CTA][continued, begun][row tile][part_rows]
-  struct Begun* begun;  // [CTA]
+  struct Shared* shared;  // [CTA]
   FastDiv by_g, by_page, by_block;
   int T, B, H, Hkv, G, tile_tokens, part_rows, part_tiles;
   int num_pages, page_size, max_pages, box_rows, heads_inner;
@@ -96,9 +96,9 @@ struct ChunkParams {
   float c, tau, p_lim;
 };
 
-// A unit that a CTA begins and others finish: what the join has to know.
-struct __align__(16) Begun {
-  int parts;  // CTAs that have a part of it, this one and those behind it; 0: this CTA begins none
+// What the join has to know of a unit that several CTAs share: the one that this CTA begins, or else the one whose middle it has.
+struct __align__(16) Shared {
+  int first, parts;  // the CTA that begins it, and how many have a part; parts 0: this CTA shares none
   int h, q0, ntok;
 };
 
@@ -113,11 +113,9 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return static_cast<long long>(static_cast<unsigned long long>(a) / static_cast<unsigned long long>(b));
 }
 __device__ __forceinline__ long long range_begin(long long total, int c, int ranges) { return divide(total * c, ranges); }
-// The last range that has tiles of it: the largest i with range_begin(i) before its last tile's place.  Every range between
-// has some: a range is a tile long at least.
-__device__ __forceinline__ int last_range(long long total, int ranges, long long start, int tiles, int extra) {
-  const long long w = start + extra + tiles - 1;
-  return static_cast<int>(min(ranges - 1LL, divide((w + 1) * ranges - 1, total)));
+// The range that place w lies in.
+__device__ __forceinline__ int range_of(long long total, int ranges, long long w) {
+  return static_cast<int>(divide((w + 1) * ranges - 1, total));
 }
 
 // A sequence's new tokens, as far as its offsets and length make sense.
@@ -410,7 +408,7 @@ __global__ void __maxnreg__(C::MAXREG)
       plan_start[3] = extra;
       plan_start[4] = whole;
       plan_at[1] = total;
-      p.begun[blockIdx.x].parts = 0;
+      p.shared[blockIdx.x].parts = 0;
     }
     __syncthreads();
     if (warp == C::LOAD_WARP && lane == 0) plan_start[1] -= nblk[plan_start[5] = seq_of_block(nblk, p.B, plan_start[1])];
@@ -445,8 +443,8 @@ __global__ void __maxnreg__(C::MAXREG)
     const bool whole = plan_start[4] != 0;
     Seq mine{};
     Unit u;
-    long long begun_at = 0;
-    int begun_tiles = 0;
+    long long cut_at = 0;  // place of a shared unit's first tile
+    int cut_tiles = 0;
     bool ok = true;
     for (int iu = 0; ok; ++iu) {
       const int slot = iu % C::UNITS;
@@ -496,7 +494,7 @@ __global__ void __maxnreg__(C::MAXREG)
           u.lo = sp.lo;
           u.hi = sp.hi;
           u.kind = u.jb > 0 ? UNIT_CONTINUED : u.je < sp.tiles ? UNIT_BEGUN : UNIT_WHOLE;
-          if (u.kind == UNIT_BEGUN) begun_at = start, begun_tiles = sp.tiles;
+          if (u.kind != UNIT_WHOLE) cut_at = start + extra, cut_tiles = sp.tiles;
           break;
         }
         if (iu >= C::UNITS) ok = wait_all(bar_ue(slot), (iu / C::UNITS - 1) & 1, W_DESC_FREE);
@@ -681,9 +679,11 @@ __global__ void __maxnreg__(C::MAXREG)
         }
       }
       if (!do_k && lane == 0) mbar_arrive(bar_ue(slot));
-      if (do_k && u.kind == UNIT_BEGUN && lane == 0)
-        p.begun[blockIdx.x] = Begun{last_range(total, ranges, begun_at, begun_tiles, extra) - static_cast<int>(blockIdx.x) + 1, u.h,
-                                    u.q0, u.ntok};
+      // A range is a tile long at least: every CTA between the first and the last one has a part.
+      if (do_k && (u.kind == UNIT_BEGUN || u.kind == UNIT_CONTINUED) && lane == 0) {
+        const int from = range_of(total, ranges, cut_at), to = range_of(total, ranges, cut_at + cut_tiles - 1);
+        p.shared[blockIdx.x] = Shared{from, to - from + 1, u.h, u.q0, u.ntok};
+      }
     }
     if (!C::GATHER || do_k) {
       if (lane == 0) {  // every copy issued must land before the CTA exits
@@ -1071,64 +1071,92 @@ __global__ void __maxnreg__(C::MAXREG)
   }
 }
 
-// Joins the states of the units that CTA blockIdx.x begins and others finish, in the order of their keys:
-// O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  A block has 32 rows (a lane each) of one row tile, each warp 8 columns.
+// Joins the states of shared units in the order of their keys: O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  A block has 32 rows
+// (a lane each) of one row tile, each of its D / 8 warps 8 columns of a unit that two CTAs share.  A unit that n CTAs share has
+// the blocks of the first n - 1 of them, or as many as a power of two and D / 8 allow: each has a share of the columns, and its
+// warps split the parts, whose states they join in shared memory.
 template <int D>
-__global__ void __launch_bounds__(D * 4) fa_fwd_paged_join_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(D * 4, D == 128 ? 3 : 6) fa_fwd_paged_join_kernel(const ChunkParams p) {
+  constexpr int WARPS = D / 8;
+  __shared__ float4 states[WARPS][2][32];
+  __shared__ float2 states_ml[WARPS][32];
   griddep_wait();
-  const int c = blockIdx.x, t = blockIdx.y, row = blockIdx.z * 32 + (threadIdx.x & 31), col8 = threadIdx.x >> 5;
-  const Begun u = p.begun[c];
+  const int t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.z * 32 + lane;
+  const Shared u = p.shared[blockIdx.x];
+  if (u.parts == 0) return;
+  const int mine = blockIdx.x - u.first;  // which of the unit's blocks
+  int blocks = 1;
+  while (2 * blocks <= min(u.parts - 1, WARPS)) blocks *= 2;
+  if (mine >= blocks || t * p.tile_tokens >= u.ntok) return;
+  const int slice = warp % blocks, col8 = mine * (WARPS / blocks) + warp / blocks;
   const int my_tok = p.by_g.div(row), g = row - my_tok * p.G, tok = t * p.tile_tokens + my_tok;
-  if (u.parts == 0 || my_tok >= p.tile_tokens || tok >= u.ntok) return;
-  // CTA c's state of a unit that it begins, then those of the CTAs behind it of a unit that they continue
-  const auto part = [&](int i) {
-    return static_cast<size_t>(c + i) * 2 * p.part_tiles + (i == 0 ? p.part_tiles : 0) + t;
-  };
-  const auto load_ml = [&](int i) { return p.part_ml[part(i) * p.part_rows + row]; };
-  const auto load_o = [&](int i, float4 (&x)[2]) {
-    const float4* const po = p.part_o + (part(i) * (D / 4) + col8 * 2) * p.part_rows + row;
-    x[0] = po[0];
-    x[1] = po[p.part_rows];
-  };
-  // the first two parts' loads (there are two at least) all at once
-  const float2 ml0 = load_ml(0), ml1 = load_ml(1);
-  float4 x0[2], x1[2];
-  load_o(0, x0);
-  load_o(1, x1);
-  float m = fmaxf(ml0.x, ml1.x);
-  for (int i = 2; i < u.parts; i += 4) {  // four at a time, the last one again where there are fewer
-    float x[4];
+  const bool real = my_tok < p.tile_tokens && tok < u.ntok;
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  for (int i0 = slice; real && i0 < u.parts; i0 += 2 * blocks) {  // two parts at a time
+    float2 ml[2];
+    float4 x[2][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = load_ml(min(i + k, u.parts - 1)).x;
-    m = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-  }
-  float o[8] = {}, l = 0.f;
-  const auto add = [&](const float2& ml, const float4 (&x)[2]) {
-    const float w = ex2_approx(ml.x - m);
-    o[0] = fmaf(w, x[0].x, o[0]);
-    o[1] = fmaf(w, x[0].y, o[1]);
-    o[2] = fmaf(w, x[0].z, o[2]);
-    o[3] = fmaf(w, x[0].w, o[3]);
-    o[4] = fmaf(w, x[1].x, o[4]);
-    o[5] = fmaf(w, x[1].y, o[5]);
-    o[6] = fmaf(w, x[1].z, o[6]);
-    o[7] = fmaf(w, x[1].w, o[7]);
-    l = fmaf(w, ml.y, l);
-  };
-  add(ml0, x0);
-  add(ml1, x1);
-  for (int i = 2; i < u.parts; i += 4) {
-    float2 ml[4];
-    float4 x[4][2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      ml[k] = load_ml(min(i + k, u.parts - 1));
-      load_o(min(i + k, u.parts - 1), x[k]);
+    for (int k = 0; k < 2; ++k) {
+      const int i = i0 + k * blocks;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < u.parts) {
+        // the first CTA's state of a unit that it begins, or another one's of a unit that it continues
+        const size_t part = static_cast<size_t>(u.first + i) * 2 * p.part_tiles + (i == 0 ? p.part_tiles : 0) + t;
+        const float4* const po = p.part_o + (part * (D / 4) + col8 * 2) * p.part_rows + row;
+        ml[k] = p.part_ml[part * p.part_rows + row];
+        x[k][0] = po[0];
+        x[k][1] = po[p.part_rows];
+      }
     }
+    const float m_new = fmaxf(m, fmaxf(ml[0].x, ml[1].x));
+    const float m_use = m_new == -INFINITY ? 0.f : m_new;  // no part so far sees a key of this row: weights of 0
+    const float old = ex2_approx(m - m_use);
+    l *= old;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k < u.parts) add(ml[k], x[k]);
+    for (int e = 0; e < 8; ++e) o[e] *= old;
+    m = m_new;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float w = ex2_approx(ml[k].x - m_use);
+      l = fmaf(w, ml[k].y, l);
+      o[0] = fmaf(w, x[k][0].x, o[0]);
+      o[1] = fmaf(w, x[k][0].y, o[1]);
+      o[2] = fmaf(w, x[k][0].z, o[2]);
+      o[3] = fmaf(w, x[k][0].w, o[3]);
+      o[4] = fmaf(w, x[k][1].x, o[4]);
+      o[5] = fmaf(w, x[k][1].y, o[5]);
+      o[6] = fmaf(w, x[k][1].z, o[6]);
+      o[7] = fmaf(w, x[k][1].w, o[7]);
+    }
   }
+  if (blocks > 1) {
+    states_ml[warp][lane] = make_float2(m, l);
+    states[warp][0][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    states[warp][1][lane] = make_float4(o[4], o[5], o[6], o[7]);
+    __syncthreads();
+    if (slice > 0) return;
+    for (int w = 1; w < blocks; ++w) m = fmaxf(m, states_ml[warp + w][lane].x);
+    const float m_use = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    for (int w = 0; w < blocks; ++w) {
+      const float2 ml = states_ml[warp + w][lane];
+      const float4 a = states[warp + w][0][lane], b = states[warp + w][1][lane];
+      const float f = ex2_approx(ml.x - m_use);
+      l = fmaf(f, ml.y, l);
+      o[0] = fmaf(f, a.x, o[0]);
+      o[1] = fmaf(f, a.y, o[1]);
+      o[2] = fmaf(f, a.z, o[2]);
+      o[3] = fmaf(f, a.w, o[3]);
+      o[4] = fmaf(f, b.x, o[4]);
+      o[5] = fmaf(f, b.y, o[5]);
+      o[6] = fmaf(f, b.z, o[6]);
+      o[7] = fmaf(f, b.w, o[7]);
+    }
+  }
+  if (!real) return;
   const float inv = 1.f / l;
   const size_t out = static_cast<size_t>(u.q0 + tok) * p.H + u.h * p.G + g;
   *reinterpret_cast<uint4*>(p.o + out * D + col8 * 8) =
@@ -1137,10 +1165,10 @@ __global__ void __launch_bounds__(D * 4) fa_fwd_paged_join_kernel(const ChunkPar
   if (p.lse != nullptr && col8 == 0) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// The workspace: states of cut units, and who begins them.
+// The workspace: states of shared units, and who shares them.
 struct Layout {
   int rows, tiles;
-  size_t part_ml, begun, total;
+  size_t part_ml, shared, total;
 };
 Layout layout_of(int T, int H, int Hkv, int d, int sms) {
   const int G = H / Hkv, tokens = FWD_PAGED_MAX_G / G;
@@ -1150,8 +1178,8 @@ Layout layout_of(int T, int H, int Hkv, int d, int sms) {
   const size_t ctas = static_cast<size_t>(sms) * (d == 128 ? ChunkCfg<128, false>::MINB : ChunkCfg<64, false>::MINB);
   const size_t states = ctas * 2 * l.tiles * l.rows;
   l.part_ml = states * d * 4;
-  l.begun = l.part_ml + states * 8;
-  l.total = (l.begun + ctas * sizeof(Begun) + 15) / 16 * 16;
+  l.shared = l.part_ml + states * 8;
+  l.total = l.shared + ctas * sizeof(Shared);
   return l;
 }
 
@@ -1182,7 +1210,7 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
   p.err = a.err;
   p.part_o = reinterpret_cast<float4*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(a.ws + l.part_ml);
-  p.begun = reinterpret_cast<Begun*>(a.ws + l.begun);
+  p.shared = reinterpret_cast<Shared*>(a.ws + l.shared);
   p.G = a.H / a.Hkv;
   p.by_g = FastDiv(static_cast<unsigned>(p.G));
   p.by_page = FastDiv(static_cast<unsigned>(a.page_size));
