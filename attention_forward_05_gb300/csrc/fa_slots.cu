@@ -5,10 +5,11 @@
 // (where a sequence's tokens begin) and of the pages it needs, ceil((ctx_b + n_b) / P) - ceil(ctx_b / P) (how far down the
 // stack of free pages its own begin).  A token then finds its sequence by bisection and its slot by itself.
 //
-// One cluster of up to 16 CTAs (what one SM writes at a time, about 25 GB/s, bounds steps of many tokens).  Every CTA forms both sums over all sequences in its shared memory (12 bytes a sequence)
-// and takes its pieces of the tokens, so no CTA waits for another's sums; the cluster's barrier stands between the
-// last read of the lengths and the free pages' count and the writes of the new ones, which may go to the same memory.
-// A few thousand bytes: bound by the launch and four dependent round trips to memory.
+// One cluster of up to 16 CTAs.  Every CTA forms both sums over all sequences in its shared memory (12 bytes a sequence)
+// and takes its pieces of the tokens, so no CTA waits for another's sums; the cluster's barrier stands between the last
+// read of the lengths and the free pages' count and the writes of the new ones, which may go to the same memory.
+// A few thousand bytes: bound by the launch and four dependent round trips to memory (237 sequences of a token: 3.9 us in a
+// graph); with many tokens by the rate at which one SM writes (67961 tokens, 0.8 MB: 7.7 us; by clusters of 8 10.3).
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
 
