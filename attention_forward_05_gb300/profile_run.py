@@ -17,6 +17,12 @@ heads shared by its query heads.
   append               8191 tokens, 32 query and 8 key/value heads of 128, into pages of 64 rows
   decode_paged         32 sequences of 8192 keys, 32 query heads on 4 key/value heads of 128, pages of 16 rows
   decode_paged_prefix  the same heads: 16384 shared keys in pages of 64 rows, 256 sequences of 64 own keys
+  norm_rope            norms and rotation of q and k of 2 x 8192 tokens, 32 + 8 heads of 128, bf16
+  norm_rope_bwd        its gradients, the norms' weights' too
+  slots                page tables, positions and slots of 64 prompts of 1000 tokens behind 500
+  fwd_paged            a prompt of 8191 tokens, 32 query heads on 8 key/value heads of 128, pages of 64 rows
+  fwd_paged_d64        8 chunks of 512 tokens behind 4096 keys, 32 query heads on 4 of 64, pages of 16 rows
+  fwd_paged_window     48 single tokens behind 8192 keys, window of 4096 and 4 sinks, 32 heads on 8 of 128, pages of 16
 """
 from __future__ import annotations
 
@@ -31,7 +37,8 @@ from attention_forward_05_gb300 import accounting
 from attention_forward_05_gb300.inputs import WORKLOADS, make_dout, make_qkv, merge_order, workload_inputs
 
 
-OPS = ("rope", "append", "decode_paged", "decode_paged_prefix")
+OPS = ("rope", "append", "decode_paged", "decode_paged_prefix", "norm_rope", "norm_rope_bwd", "slots", "fwd_paged",
+       "fwd_paged_d64", "fwd_paged_window")
 
 
 def operator(name: str, dev):
@@ -57,6 +64,37 @@ def operator(name: str, dev):
         pos, freqs = at.to(torch.int32), fa.fa_rope_freqs(d, device=dev)
         return (lambda: fa.fa_paged_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, slots, q=x[:, :H], positions=pos,
                                            freqs=freqs)), 4 * x.numel(), 3 * T * (H + Hkv) * d
+    if name.startswith("norm_rope"):
+        B, N, H, Hkv, d = 2, 8192, 32, 8, 128
+        q, k = draw(B, N, H, d).transpose(1, 2), draw(B, N, Hkv, d).transpose(1, 2)
+        wq, wk, pos, freqs = draw(d), draw(d), torch.arange(N, dtype=torch.int32, device=dev), fa.fa_rope_freqs(d, device=dev)
+        n = q.numel() + k.numel()
+        if name == "norm_rope":
+            return (lambda: fa.fa_norm_rope(q, k, wq, wk, pos, freqs)), 4 * n, 8 * n
+        dq, dk = draw(B, H, N, d), draw(B, Hkv, N, d)
+        return (lambda: fa.fa_norm_rope_bwd(dq, dk, q, k, wq, wk, pos, freqs)), 6 * n, 16 * n
+    if name == "slots":
+        B, n, ctx, ps = 64, 1000, 500, 16
+        pages = -(-(ctx + n) // ps)
+        table = torch.zeros(B, pages, dtype=torch.int32, device=dev)
+        free = torch.randperm(B * pages, generator=gen, device=dev).to(torch.int32)
+        ctxs, news, count = (torch.full((m,), v, dtype=torch.int32, device=dev)
+                             for m, v in ((B, ctx), (B, n), (1, B * pages)))
+        return (lambda: fa.fa_paged_slots(ctxs, news, table, free, count, ps, B * n)), 12 * B * n, 0
+    if name.startswith("fwd_paged"):
+        B, n, ctx, H, Hkv, d, ps, window, sinks = {"fwd_paged": (1, 8191, 0, 32, 8, 128, 64, 0, 0),
+                                                   "fwd_paged_d64": (8, 512, 4096, 32, 4, 64, 16, 0, 0),
+                                                   "fwd_paged_window": (48, 1, 8191, 32, 8, 128, 16, 4096, 4)}[name]
+        width = -(-(ctx + n) // ps)
+        kc, vc = draw(B * width, Hkv, ps, d), draw(B * width, Hkv, ps, d)
+        table = torch.randperm(B * width, generator=gen, device=dev).to(torch.int32).view(B, width)
+        lens = torch.full((B,), ctx + n, dtype=torch.int32, device=dev)
+        cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev)
+        q = draw(B * n, H, d)
+        keys = B * (window + sinks if window else ctx + n)
+        pairs = keys if window else B * (n * ctx + n * (n + 1) // 2)
+        return (lambda: fa.fa_fwd_paged(q, kc, vc, table, cu, lens, window=window, sinks=sinks)), \
+            4 * keys * Hkv * d + 4 * q.numel(), 4 * H * d * pairs
     H, Hkv, d = 32, 4, 128
     B, n, ps, prefix = (32, 8192, 16, 0) if name == "decode_paged" else (256, 64, 64, 16384)
     width, shared = n // ps, prefix // ps
