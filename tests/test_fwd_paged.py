@@ -52,6 +52,7 @@ MIXED = [(0, 1), (130, 1), (5, 7), (0, 300), (257, 0), (63, 65), (1000, 23), (12
     (8, 2, 64, 1, MIXED), (8, 2, 128, 1, MIXED), (4, 2, 128, 20, MIXED), (4, 2, 64, 3, MIXED), (2, 1, 64, 100, MIXED),
     (32, 1, 128, 16, [(300, 9), (0, 17)]), (128, 1, 64, 16, [(77, 3), (0, 2)]), (100, 1, 128, 16, [(40, 5)]),
     (8, 8, 128, 16, [(3000, 5)]), (4, 2, 64, 16, [(5000, 3), (0, 1), (4000, 60)]),
+    (64, 1, 128, 16, [(10, 900), (300, 800)]), (128, 2, 64, 32, [(0, 500), (40, 300), (7, 1)]), (2, 1, 64, 128, [(9000, 71), (6000, 1)]),
 ])
 def test_chunks(cuda_device, H, Hkv, d, ps, chunks):
     b = Batch(cuda_device, H, Hkv, d, ps, chunks)
@@ -246,10 +247,22 @@ def test_single_tokens_equal_the_decode(cuda_device):
 
 def test_many_short_sequences(cuda_device):
     rng = np.random.default_rng(3)
-    for d, B in ((64, 700), (128, 300)):
+    for d, B in ((64, 700), (128, 300), (128, 1500)):
         chunks = [(int(c), int(n)) for c, n in zip(rng.integers(0, 60, B), rng.integers(0, 4, B))]
         b = Batch(cuda_device, 4, 2, d, 16, chunks)
         b.check(*b.run(), f"{B} sequences", seqs=set(rng.integers(0, B, 60).tolist()) | {0, B - 1})
+
+
+def test_the_most_sequences(cuda_device):
+    """16384 places of a padded batch, nearly all unused; the used ones among them, the first and the last."""
+    for d, window in ((64, 0), (128, 20)):
+        chunks = [(0, 0)] * 16384
+        used = {0: (5, 3), 1: (0, 1), 700: (100, 40), 8191: (17, 1), 16382: (0, 300), 16383: (33, 2)}
+        for i, c in used.items():
+            chunks[i] = c
+        b = Batch(cuda_device, 4, 2, d, 16, chunks, width=20)
+        b.len_t[[i for i in range(16384) if i not in used]] = -1
+        b.check(*b.run(window=window, sinks=2), "16384 places", seqs=set(used), window=window, sinks=2)
 
 
 def test_a_long_prompt(cuda_device):
