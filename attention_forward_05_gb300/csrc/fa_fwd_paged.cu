@@ -358,8 +358,7 @@ __global__ void __maxnreg__(C::MAXREG)
     __syncthreads();
     // A thread's blocks x0 .. x1 - 1 (of each key/value head), their tiles, and the tiles before them
     const int pb = (blocks + NT - 1) / NT, x0 = min(blocks, tid * pb), x1 = min(blocks, x0 + pb);
-    long long head;  // tiles of all blocks
-    long long tiles = 0;
+    int all_tiles, tiles = 0;  // of a key/value head: fewer than 2^31 (fa_fwd_paged's limit)
     if (x0 < x1) {
       int b = seq_of_block(nblk, p.B, x0);
       Seq s = load_seq(p, b);
@@ -368,62 +367,63 @@ __global__ void __maxnreg__(C::MAXREG)
         tiles += block_tiles<BC>(p, s, x - nblk[b]);
       }
     }
-    const long long before = scan<NT>(tiles, reinterpret_cast<long long*>(plan_tmp), &head);
+    const int before = scan<NT>(tiles, plan_tmp, &all_tiles);
     // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
     // each takes one, and starts and ends do not count.
-    const int extra = head * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
-    long long* const place = plan_place;  // of each thread's first block in its head, and the head's end
+    const int extra = static_cast<long long>(all_tiles) * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
+    long long* const place = plan_place;  // of each thread's first block in its head
     place[tid] = before + static_cast<long long>(extra) * x0;
-    head += static_cast<long long>(extra) * blocks;
-    if (tid == 0) place[NT] = head;
-    const long long total = head * p.Hkv;
+    const long long head = all_tiles + static_cast<long long>(extra) * blocks, total = head * p.Hkv;
     const int ranges = static_cast<int>(min(static_cast<long long>(min(static_cast<int>(gridDim.x), NT - 1)), total));
     __syncthreads();
-    // Thread i looks up where range i begins: the unit that its first place lies in (or, with several blocks a thread, the
-    // first one of that thread's).  Where a thread has one block at most, it also knows how long the ranges are that take
-    // the units beginning in them, whole.
-    const int my_range = tid;
-    const bool whole_known = pb <= 1;
-    long long from = 0, w = 0;
-    int h = 0, lo = 0;
-    if (ranges > 0 && my_range <= ranges) {
-      w = range_begin(total, my_range, ranges);
-      h = static_cast<int>(divide(w, head));
-      const long long rem = w - h * head;
-      int hi = pb > 1 ? (blocks + pb - 1) / pb : blocks;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (place[mid] <= rem) lo = mid;
-        else hi = mid;
+    // Thread i looks up where ranges i and i + 1 begin: the unit that their first place lies in (or, with several blocks a
+    // thread, the first one of that thread's).  Where a thread has one block at most, it also knows how long range i is if it
+    // takes the units that begin in it, whole.
+    long long from[2] = {0, 0}, w[2] = {0, 0}, next[2] = {0, 0};
+    int h[2] = {0, 0}, at_block[2] = {0, 0};
+    const bool mine_too = tid < ranges;
+    if (mine_too) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        w[k] = range_begin(total, tid + k, ranges);
+        h[k] = static_cast<int>(divide(w[k], head));
       }
-      from = h * head + place[lo];
+      const int n = pb > 1 ? (blocks + pb - 1) / pb : blocks;
+      int lo[2] = {0, 0}, hi[2] = {n, n};
+      while (hi[0] - lo[0] > 1 || hi[1] - lo[1] > 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int mid = (lo[k] + hi[k]) >> 1;  // lo itself at the end
+          if (place[mid] <= w[k] - h[k] * head) lo[k] = mid;
+          else hi[k] = mid;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        from[k] = h[k] * head + place[lo[k]];
+        next[k] = lo[k] + 1 < n ? h[k] * head + place[lo[k] + 1] : (h[k] + 1LL) * head;
+        at_block[k] = lo[k] * max(pb, 1);
+      }
     }
-    bool whole = false;
-    if (whole_known) {
-      const long long next = my_range < ranges ? (lo + 1 < blocks ? h * head + place[lo + 1] : (h + 1LL) * head) : 0;
-      const long long begin = w == from ? w : next;  // of the first unit that begins in the range or behind it
-      __syncthreads();
-      if (my_range <= ranges) place[my_range] = my_range == ranges ? total : begin;
-      __syncthreads();
-      const bool fits = my_range >= ranges || place[my_range + 1] - place[my_range] <= divide(total, max(ranges, 1)) + COST_CUT;
-      whole = __syncthreads_and(fits);
+    // the first unit that begins in a range or behind it
+    const long long length = (w[1] == total ? total : w[1] == from[1] ? w[1] : next[1]) - (w[0] == from[0] ? w[0] : next[0]);
+    const bool whole = __syncthreads_and(!mine_too || (pb <= 1 && length <= divide(total, ranges) + COST_CUT));
+    if (tid == static_cast<int>(blockIdx.x) && mine_too) {
+      const int b = seq_of_block(nblk, p.B, at_block[0]);
+      plan_start[0] = h[0];
+      plan_start[1] = at_block[0] - nblk[b];
+      plan_start[5] = b;
+      plan_at[0] = from[0];
+      plan_at[1] = total;
+      plan_at[2] = w[0];
+      plan_at[3] = w[1];
     }
-    if (my_range == static_cast<int>(blockIdx.x) && my_range < ranges) {
-      plan_start[0] = h;
-      plan_start[1] = lo * max(pb, 1);  // block
-      plan_at[0] = from;
-      plan_at[2] = w;
-    }
-    if (my_range == static_cast<int>(blockIdx.x) + 1 && my_range <= ranges) plan_at[3] = w;
     if (tid == 0) {
       plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
       plan_start[3] = extra;
       plan_start[4] = whole;
-      plan_at[1] = total;
       p.shared[blockIdx.x].parts = 0;
     }
-    __syncthreads();
-    if (warp == C::LOAD_WARP && lane == 0) plan_start[1] -= nblk[plan_start[5] = seq_of_block(nblk, p.B, plan_start[1])];
     __syncthreads();
     if (p.G * p.tile_tokens < C::BR) {  // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
       for (int i = tid; i < 2 * C::Q_BYTES / 16; i += NT) *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);

@@ -496,7 +496,8 @@ int fa_paged_slots(const int* ctx_lens, const int* new_lens, int* page_table, lo
  * with a page outside the cache NaN in the tokens that the page reaches (and others near them); offsets that do
  * not ascend make their sequence's tokens stay unwritten.  fa_check_device_error then reports FA_ERR_INVALID_ARG.
  * Accumulation and softmax statistics are fp32.  No atomics on results: repeated calls on one GPU give identical bits.
- * H / Hkv <= 128, B <= 16384 (FA_ERR_UNSUPPORTED otherwise); max_pages * page_size < 2^30, T * (H / Hkv) <= 2^30.
+ * H / Hkv <= 128, B <= 16384 (FA_ERR_UNSUPPORTED otherwise); max_pages * page_size < 2^30, T * (H / Hkv) <= 2^30 and
+ * (T * (H / Hkv) / 128 + B + 1) * (max_pages * page_size / 64 + 3) < 2^31 (FA_ERR_INVALID_ARG otherwise).
  */
 int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, const int* page_table,
                  long long table_stride, const int* cu_seqlens, const int* seq_lens, int T, int B, int H,

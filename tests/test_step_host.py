@@ -107,6 +107,7 @@ def _fwd(**kw):
     (dict(mp=0), INVALID), (dict(stride=3), INVALID), (dict(mp=1 << 20, ps=1 << 10), INVALID), (dict(window=-1), INVALID),
     (dict(sinks=-1), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=3e38), INVALID), (dict(d=96), UNSUPPORTED),
     (dict(H=129, Hkv=1), UNSUPPORTED), (dict(B=16385), UNSUPPORTED), (dict(T=1 << 29, H=64), INVALID),
+    (dict(T=1 << 16, H=8, Hkv=1, B=200, mp=1 << 16, ps=1 << 13), INVALID),
     (dict(qs=[512, 60]), INVALID), (dict(qs=[512, 0]), INVALID), (dict(qs=[0, 64]), INVALID), (dict(qs=[-512, 64]), INVALID),
     (dict(qs=[64, 1024]), INVALID), (dict(cs=[2048, 1024, 60]), INVALID), (dict(cs=[0, 1024, 64]), INVALID),
 ])
