@@ -308,3 +308,46 @@ def test_many_rows_far_offsets(cuda_device):
 def test_finite_scale_default(cuda_device):
     b = Batch(cuda_device, 4, 2, 64, 16, [(33, 5)])
     assert torch.equal(b.run()[0], b.run(scale=1 / math.sqrt(64))[0])
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls of both head dimensions on two streams at the same time, each with the allocator's workspace."""
+    a = Batch(cuda_device, 8, 2, 128, 16, MIXED + [(3000, 40)], seed=2)
+    b = Batch(cuda_device, 8, 2, 64, 16, MIXED + [(2000, 400)], seed=3)
+    want = a.run(), b.run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(25):
+        got.append((a.run(stream=streams[0]), b.run(stream=streams[1])))
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_error() == fa.FA_OK
+    for pair in got:
+        for x, y in zip(pair, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+def test_back_to_back_behind_the_append(cuda_device):
+    """Each launch may start before the one in front of it has ended: new keys, then the attention that reads them, many layers
+    without a pause, against the same with a synchronisation between all calls."""
+    d, ps, Hkv = 128, 16, 2
+    b = Batch(cuda_device, 8, Hkv, d, ps, [(300, 60), (0, 33), (511, 1), (40, 2)])
+    slots = torch.cat([torch.as_tensor(np.asarray(t, dtype=np.int64))[torch.arange(n - m, n) // ps] * ps + torch.arange(n - m, n) % ps
+                       for t, n, m in zip(b.tables, b.lens, b.news)]).to(cuda_device)
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(8)
+    layers = [tuple(torch.randn((b.T, Hkv, d), generator=g, device=cuda_device).to(BF) for _ in range(2)) for _ in range(12)]
+    results = []
+    for pause in (True, False):
+        out = []
+        for k, v in layers:
+            fa.fa_paged_append(k, v, b.kc, b.vc, slots)
+            if pause:
+                torch.cuda.synchronize()
+            out.append(b.run())
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append(out)
+    for x, y in zip(*results):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])

@@ -127,3 +127,38 @@ def test_wide_rows_and_another_stream(cuda_device):
     s.synchronize()
     compare({"table": wide[:, :12]}, out, fa.fa_check_device_error(), want)
     assert (wide[:, 12:] == 5).all()
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+def test_many_tokens_in_place(cuda_device, aligned):
+    """A cluster of many CTAs that counts on in place, outputs on 16-byte boundaries or not, eager and captured."""
+    ps, B = 16, 2500
+    ctx, new, table, free, count, T = make(B, ps, 40, 300, 30, 17, pad=5)
+    assert T > 20000
+    want = ref.slots(ctx, new, table, free, count, ps, T)
+    i = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32, device=cuda_device)  # noqa: E731
+    first = {"ctx": i(ctx), "table": i(table), "count": i([count])}
+    fixed = i(new), i(free)
+    room = torch.empty(T + 4, dtype=torch.int32, device=cuda_device), torch.empty(T + 4, dtype=torch.int64, device=cuda_device)
+    at = 0 if aligned else 1
+    out = dict(positions=room[0][at:at + T], slots=room[1][at:at + T])
+    state = {n: t.clone() for n, t in first.items()}
+
+    def step():
+        return fa.fa_paged_slots(state["ctx"], fixed[0], state["table"], fixed[1], state["count"], ps, T, seq_lens=state["ctx"],
+                                 free_left=state["count"], **out)
+
+    got = step()
+    torch.cuda.synchronize()
+    compare(state, got, fa.fa_check_device_error(), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(20):
+        for n, t in first.items():
+            state[n].copy_(t)
+        for t in out.values():
+            t.fill_(-9)
+        g.replay()
+        torch.cuda.synchronize()
+        compare(state, got, fa.fa_check_device_error(), want)
