@@ -94,15 +94,25 @@ __device__ __forceinline__ void pack(const Head16& h, Unit<float>* u) {
   for (int i = 0; i < 4; ++i) u->v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// The weights of a lane's elements (nullptr: no such heads).
+// Both kinds' weights into shared memory, in fp32 (nullptr: no such heads).  Beside the rotation's table, so that both wait for
+// memory once; the caller synchronises.
+template <int D>
+__device__ __forceinline__ void load_weights(const void* wq, const void* wk, int fp32, float (&w)[2][D]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const void* const p = k ? wk : wq;
+    for (int i = threadIdx.x; i < D; i += ROPE_THREADS)
+      w[k][i] = p == nullptr ? 0.f
+                : fp32       ? static_cast<const float*>(p)[i]
+                             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  }
+}
+
+// Those of a lane's elements.
 template <typename T, bool INTER>
-__device__ __forceinline__ Head16 load_weight(const void* p, int fp32, int e0, int es) {
+__device__ __forceinline__ Head16 lane_weight(const float* w, int e0, int es) {
   constexpr int W = 16 / sizeof(T);
-  const auto at = [&](int i) {
-    const int e = e0 + i / W * es + i % W;
-    if (p == nullptr) return 0.f;
-    return fp32 ? static_cast<const float*>(p)[e] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[e]);
-  };
+  const auto at = [&](int i) { return w[e0 + i / W * es + i % W]; };
   Head16 h;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -226,11 +236,11 @@ constexpr int FWD_SLOTS = 8, FWD_BLOCKS = 3;
 
 // A block's items, forward.
 template <typename T, int D, bool INTER, bool QUAD>
-__device__ __forceinline__ void norm_items(const NormParams& p, const Heads& hs, const PairTurn* pairs) {
+__device__ __forceinline__ void norm_items(const NormParams& p, const Heads& hs, const PairTurn* pairs, const float* weight) {
   constexpr int P = Unit<T>::PIECES, PER = FWD_SLOTS / P, STEP = Lane<D, QUAD>::STEP, UNITS = D / 16;
   int e0, es;
   const bool rotated = unit_pieces<T, D>(p.r.rot, Lane<D, QUAD>().u, &e0, &es);
-  const Head16 w = load_weight<T, INTER>(hs.w, p.w_fp32, e0, es);
+  const Head16 w = lane_weight<T, INTER>(weight, e0, es);
   const unsigned mask = head_mask<UNITS>();
   run_items<T, D, INTER, QUAD, FWD_SLOTS>(
       hs.g, p.r, pairs, rotated, p.tokens, block_of(hs), gridDim.x,
@@ -268,12 +278,12 @@ constexpr int BWD_SLOTS = 16, BWD_BLOCKS = 3;
 
 // A block's items, backward; leaves the block's share of dw in `parts`.
 template <typename T, int D, bool INTER, bool QUAD>
-__device__ __forceinline__ void norm_items_bwd(const NormParams& p, const Heads& hs, const PairTurn* pairs, float (*share)[D],
-                                               float* parts) {
+__device__ __forceinline__ void norm_items_bwd(const NormParams& p, const Heads& hs, const PairTurn* pairs, const float* weight,
+                                               float (*share)[D], float* parts) {
   constexpr int P = Unit<T>::PIECES, PER = BWD_SLOTS / (2 * P), STEP = Lane<D, QUAD>::STEP, UNITS = D / 16;
   int e0, es;
   const bool rotated = unit_pieces<T, D>(p.r.rot, Lane<D, QUAD>().u, &e0, &es);
-  const Head16 w = load_weight<T, INTER>(hs.w, p.w_fp32, e0, es);
+  const Head16 w = lane_weight<T, INTER>(weight, e0, es);
   const unsigned mask = head_mask<UNITS>();
   Head16 sum{};
   run_items<T, D, INTER, QUAD, BWD_SLOTS>(
@@ -353,17 +363,19 @@ __device__ __forceinline__ void norm_items_bwd(const NormParams& p, const Heads&
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS, FWD_BLOCKS) fa_norm_rope_kernel(const __grid_constant__ NormParams p) {
   __shared__ PairTurn pairs[D / 2];
+  __shared__ float weights[2][D];
   griddep_wait();
   load_rotation<D>(p.r, pairs, p.err);
+  load_weights<D>(p.heads[0].w, p.heads[1].w, p.w_fp32, weights);
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const Heads& hs = p.heads[k];
     if (!has_items(hs)) continue;
     if (hs.quad)
-      norm_items<T, D, INTER, true>(p, hs, pairs);
+      norm_items<T, D, INTER, true>(p, hs, pairs, weights[k]);
     else
-      norm_items<T, D, INTER, false>(p, hs, pairs);
+      norm_items<T, D, INTER, false>(p, hs, pairs, weights[k]);
   }
 }
 
@@ -371,10 +383,12 @@ __global__ void __launch_bounds__(ROPE_THREADS, FWD_BLOCKS) fa_norm_rope_kernel(
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS, BWD_BLOCKS) fa_norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ PairTurn pairs[D / 2];
+  __shared__ float weights[2][D];
   __shared__ float share[ROPE_THREADS / 32][D];
   griddep_launch_dependents();
   griddep_wait();
   load_rotation<D>(p.r, pairs, p.err);
+  load_weights<D>(p.heads[0].w, p.heads[1].w, p.w_fp32, weights);
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
@@ -383,9 +397,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, BWD_BLOCKS) fa_norm_rope_bwd_ker
     if (!has_items(hs)) {
       for (int i = threadIdx.x; i < D; i += ROPE_THREADS) parts[i] = 0.f;
     } else if (hs.quad)
-      norm_items_bwd<T, D, INTER, true>(p, hs, pairs, share, parts);
+      norm_items_bwd<T, D, INTER, true>(p, hs, pairs, weights[k], share, parts);
     else
-      norm_items_bwd<T, D, INTER, false>(p, hs, pairs, share, parts);
+      norm_items_bwd<T, D, INTER, false>(p, hs, pairs, weights[k], share, parts);
   }
 }
 
@@ -395,13 +409,15 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_append_kern
   using T = __nv_bfloat16;
   constexpr int P = Unit<T>::PIECES, PER = PIECE_SLOTS / P, STEP = Lane<D, true>::STEP, UNITS = D / 16;
   __shared__ PairTurn pairs[D / 2];
+  __shared__ float weights[2][D];
   griddep_wait();
   load_rotation<D>(a.r, pairs, a.err);
+  load_weights<D>(nm.wq, nm.wk, nm.fp32, weights);
   __syncthreads();
   const int hk = a.H, hv = a.H + a.Hkv, heads = a.H + 2 * a.Hkv;  // q, k and v heads in a row
   int e0, es;
   const bool rotated = unit_pieces<T, D>(a.r.rot, Lane<D, true>().u, &e0, &es);
-  const Head16 wq = load_weight<T, INTER>(nm.wq, nm.fp32, e0, es), wk = load_weight<T, INTER>(nm.wk, nm.fp32, e0, es);
+  const Head16 wq = lane_weight<T, INTER>(weights[0], e0, es), wk = lane_weight<T, INTER>(weights[1], e0, es);
   const unsigned mask = head_mask<UNITS>();
   run_items<T, D, INTER, true>(
       g, a.r, pairs, rotated, a.T, blockIdx.x, gridDim.x,
