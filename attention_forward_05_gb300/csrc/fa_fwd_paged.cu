@@ -334,7 +334,7 @@ __global__ void __maxnreg__(C::MAXREG)
     constexpr int NT = C::NTHREADS;
     int* const nblk = reinterpret_cast<int*>(smem);          // blocks before each sequence, where the tiles will lie
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int blocks, mine = 0;
+    int mine = 0;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(p, b);
       if (blockIdx.x == 0 && s.n == 0 && (p.cu[b] < 0 || p.cu[b] != p.cu[b + 1] || p.cu[b] > p.T))
@@ -344,7 +344,11 @@ __global__ void __maxnreg__(C::MAXREG)
       if (per > 1) nblk[b] = nb;
       mine += nb;
     }
-    int at = scan<NT>(mine, plan_tmp, &blocks);
+    // Offsets that do not ascend can give more blocks than T tokens have, which 32 bits need not hold: then there are none.
+    const unsigned most = static_cast<unsigned>(blocks_of(p, p.T)) + p.B;
+    unsigned sum;
+    int at = static_cast<int>(scan<NT>(min(static_cast<unsigned>(mine), most + 1), reinterpret_cast<unsigned*>(plan_tmp), &sum));
+    const int blocks = sum > most ? 0 : static_cast<int>(sum);
     if (per == 1) {
       if (b0 < b1) nblk[b0] = at;
     } else {
@@ -426,7 +430,8 @@ __global__ void __maxnreg__(C::MAXREG)
     }
     __syncthreads();
     if (p.G * p.tile_tokens < C::BR) {  // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
-      for (int i = tid; i < 2 * C::Q_BYTES / 16; i += NT) *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < 2 * C::Q_BYTES / 16; i += NT)
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async();
   }
@@ -561,7 +566,8 @@ __global__ void __maxnreg__(C::MAXREG)
               };
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (i0 + 32 * k < r1 * PIECES) *at16(i0 + 32 * k) = make_uint4(keep(w[k].x), keep(w[k].y), keep(w[k].z), keep(w[k].w));
+                if (i0 + 32 * k < r1 * PIECES)
+                  *at16(i0 + 32 * k) = make_uint4(keep(w[k].x), keep(w[k].y), keep(w[k].z), keep(w[k].w));
               *reinterpret_cast<volatile int*>(&units[slot].set_aside) = 1;
             }
           };
@@ -723,8 +729,8 @@ __global__ void __maxnreg__(C::MAXREG)
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const int e = kk * 16;
-        mma_ss<0>(tmem + t * BC, qa + ((e / 64 * C::Q_CH_BYTES + e % 64 * 2) >> 4), kb + ((e / 64 * C::KV_CH_BYTES + e % 64 * 2) >> 4),
-                  idesc_qk, kk > 0);
+        mma_ss<0>(tmem + t * BC, qa + ((e / 64 * C::Q_CH_BYTES + e % 64 * 2) >> 4),
+                  kb + ((e / 64 * C::KV_CH_BYTES + e % 64 * 2) >> 4), idesc_qk, kk > 0);
       }
     };
     const auto issue_pv = [&](int t, int s, bool acc, int kk0, int kk1) {
@@ -861,9 +867,9 @@ __global__ void __maxnreg__(C::MAXREG)
         const bool full = __all_sync(0xffffffffu, valid >= BC && (first <= 0 || sink >= BC));
         const bool started = __all_sync(0xffffffffu, m_ref != -INFINITY);
         tc_fence_after();
-        // Once every row of the warp has a reference maximum and sees all columns, P is computed against it with no row maximum in front of it;
-        // row sums of at most 2^tau (and at d = 128 the second half's maximum) show that no score moved past m_ref + tau.
-        // Otherwise nothing has been stored yet, and the general path reads S again (fa_fwd_kernel.cuh, `fast`, PV2).
+        // Once every row of the warp has a reference maximum and sees all columns, P is computed against it with no row maximum
+        // in front of it; row sums of at most 2^tau (and at d = 128 the second half's maximum) show that no score moved past
+        // m_ref + tau.  Otherwise nothing has been stored yet, and the general path reads S again (fa_fwd_kernel.cuh, `fast`, PV2).
         // (A masked copy of it costs more in registers and code than it saves: 375 us on a prompt of 8191 tokens, d = 128, without
         // it 371; a mixed batch, d = 64, 89 and 86.)
         const auto fast = [&]() -> bool {
@@ -1006,7 +1012,9 @@ __global__ void __maxnreg__(C::MAXREG)
         const size_t out = static_cast<size_t>(uv.q0 + tok) * p.H + uv.h * p.G + g;
         uint8_t* const stage = smem + C::OFF_STAGE + warp * C::STAGE_BYTES;
         const int piece = lane % PCS;
-        const auto at16 = [&](int r, int pc) { return reinterpret_cast<uint4*>(stage + r * (PCS * 16) + ((pc ^ (r / (8 / PCS) % PCS)) << 4)); };
+        const auto at16 = [&](int r, int pc) {
+          return reinterpret_cast<uint4*>(stage + r * (PCS * 16) + ((pc ^ (r / (8 / PCS) % PCS)) << 4));
+        };
         __nv_bfloat16* rows[PCS];  // that this lane writes pieces of
 #pragma unroll
         for (int i = 0; i < PCS; ++i) {
@@ -1053,7 +1061,7 @@ __global__ void __maxnreg__(C::MAXREG)
             tmem_ld32(tO + cc * 32, orr);
             tmem_wait_ld();
             reg_fence(orr);
-            } else {
+          } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) orr[e] = 0;
           }

@@ -14,11 +14,11 @@
 // over all its items, a block joins its lanes' shares in a fixed order and leaves them in the workspace, and
 // fa_norm_rope_join_kernel adds the blocks' (no atomics: the same bits every time).
 //
-// Bound by device memory: 336 MB forward (2 x 8192 tokens, 32 + 8 heads of 128, bf16) 58.5 us, 5.7 TB/s with the launch, where
-// the rotation alone takes 53 on as many bytes; 503 MB backward 87 us, 5.8 TB/s.  With all heads of an item in registers at a
+// Bound by device memory: 336 MB forward (2 x 8192 tokens, 32 + 8 heads of 128, bf16) 57 us, 5.9 TB/s with the launch, where
+// the rotation alone takes 53 on as many bytes; 503 MB backward 86 us, 5.8 TB/s.  With all heads of an item in registers at a
 // time (they spill) 78 and 138 us; with query and key heads on blocks of their own 63.5 and 94; forward with 4 and 2 blocks a
 // SM 62.5 and 64, with items of twice as many heads 65.  Small calls are bound by the launch (333 tokens of 20 heads of 64,
-// fp32: 3.9 us in a graph).
+// fp32: 3.3 us in a graph; 3.9 with each lane reading its weights from device memory behind the wait for the rotation's table).
 #include "fa_rope_items.cuh"
 
 namespace fa {
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) fa_norm_append_kern
         for (int i = 0; i < PER; ++i) {  // unused places too: their slots are still on the way
           const int h = h0 + STEP * i;
           if (i < g.per && h < heads)
-            Unit<T>::fetch(dst + i * P * 512, h < hk ? q + h * a.q_head : h < hv ? k + (h - hk) * a.k_head : v + (h - hv) * a.v_head,
-                           e0, es);
+            Unit<T>::fetch(dst + i * P * 512,
+                           h < hk ? q + h * a.q_head : h < hv ? k + (h - hk) * a.k_head : v + (h - hv) * a.v_head, e0, es);
         }
         return a.r.pos + t;
       },

@@ -359,7 +359,8 @@ static cudaError_t tile(long long tokens, int heads, int sms, Tiling* g, unsigne
   using L = Lane<D, QUAD>;
   const int warps = ROPE_THREADS / 32, most = PIECE_SLOTS / Unit<T>::PIECES;
   const long long bytes = tokens * heads * D * static_cast<long long>(2 * sizeof(T));
-  const long long room = (heads + L::STEP * most - 1) / (L::STEP * most) * static_cast<long long>(L::STEP * most);  // heads the stages hold
+  // heads the stages hold
+  const long long room = (heads + L::STEP * most - 1) / (L::STEP * most) * static_cast<long long>(L::STEP * most);
   const int full = static_cast<int>((4 * room + heads) / (2 * heads));  // 2 * room / heads, to the nearest
   const int least = bytes < 165000000 ? ROPE_BLOCKS : bytes < 256000000 ? 3 : 2;
   const int blocks_sm = full > ROPE_BLOCKS ? ROPE_BLOCKS : full > least ? full : least;

@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(THREADS) fa_slots_kernel(const SlotsLaunch a, 
     for (int t = rank * THREADS + tid; t < a.T; t += ctas * THREADS) one(t);
   } else {
     // RUN neighbouring tokens a thread: of one sequence, they lie in two pages at most.
-    const bool wide = ((reinterpret_cast<unsigned long long>(a.positions) | reinterpret_cast<unsigned long long>(a.slots)) & 15) == 0;
+    const bool wide =
+        ((reinterpret_cast<unsigned long long>(a.positions) | reinterpret_cast<unsigned long long>(a.slots)) & 15) == 0;
     for (int t = (rank * THREADS + tid) * RUN; t < a.T; t += ctas * THREADS * RUN) {
       const int b = t < tokens ? sequence_of(t) : 0;
       const int end = t >= tokens ? 0 : b + 1 < a.B ? s_start[b + 1] : tokens;
@@ -194,7 +195,8 @@ template <int RUN>
 static cudaError_t launch_run(const SlotsLaunch& a) {
   const int need = (a.T + RUN * THREADS - 1) / (RUN * THREADS), ctas = need < 1 ? 1 : need > MAX_CTAS ? MAX_CTAS : need;
   cudaError_t e = allow_shared_memory<fa_slots_kernel<RUN>>(12 * SLOTS_MAX_B);
-  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(fa_slots_kernel<RUN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && ctas > 8)
+    e = cudaFuncSetAttribute(fa_slots_kernel<RUN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   return launch_dependent_clusters(fa_slots_kernel<RUN>, static_cast<unsigned>(ctas), ctas, THREADS, 12 * a.B, a.stream, a,
                                    FastDiv(static_cast<unsigned>(a.page_size)), ctas);

@@ -182,6 +182,22 @@ def test_bad_offsets_write_nothing_of_their_sequence(cuda_device, cu, good):
         b.check(o, None, "beside bad ones", seqs=set(good))
 
 
+def test_offsets_of_far_too_many_blocks_write_nothing(cuda_device):
+    # 0, T, 0, T, ...: every other sequence has all tokens, more blocks than T tokens can have in as many sequences
+    T, B = 600, 4000
+    for d in (64, 128):
+        q = torch.zeros(T, 2, d, dtype=BF, device=cuda_device)
+        cache = torch.zeros(4, 1, 16, d, dtype=BF, device=cuda_device)
+        cu = torch.arange(B + 1, dtype=torch.int32, device=cuda_device) % 2 * T
+        table = torch.zeros(B, 50, dtype=torch.int32, device=cuda_device)
+        lens = torch.full((B,), 700, dtype=torch.int32, device=cuda_device)
+        o = torch.full((T, 2, d), 7.0, dtype=BF, device=cuda_device)
+        fa.fa_fwd_paged(q, cache, cache, table, cu, lens, o=o)
+        torch.cuda.synchronize()
+        assert fa.fa_check_device_error() == fa.FA_ERR_INVALID_ARG
+        assert (o == 7).all()
+
+
 def test_no_tokens_and_no_sequences(cuda_device):
     b = Batch(cuda_device, 4, 2, 64, 16, [(40, 0), (0, 0)])
     o, lse = b.run()
