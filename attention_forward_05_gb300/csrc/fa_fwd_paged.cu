@@ -637,7 +637,6 @@ __global__ void __maxnreg__(C::MAXREG)
           const int s = n % STAGES;
           const uint32_t ph = ((n / STAGES) & 1) ^ 1;
           const int key0 = key_tile(u, j) * BC;
-          const int next_page = page_of(j + 1);
           if (do_k) {
             ok = wait_all(bar_ke(s), ph, W_KE);
             if (!ok) break;
@@ -693,7 +692,7 @@ __global__ void __maxnreg__(C::MAXREG)
               nv = n + 1;
             }
           }
-          page = next_page;
+          page = page_of(j + 1);
         }
       }
       if (!do_k && lane == 0) mbar_arrive(bar_ue(slot));
