@@ -131,7 +131,7 @@ __device__ __forceinline__ int range_of(long long total, int ranges, long long w
 }
 
 // A sequence's new tokens, as far as its offsets and length make sense.
-struct Seq {
+struct __align__(16) Seq {
   int q0, n, pos0;  // first row of q, tokens, the first one's position
   bool bad;         // its length does not fit: its tokens become NaN
 };
@@ -200,15 +200,18 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F80
 
 __device__ __forceinline__ int blocks_of(const ChunkParams& p, int n) { return n > 0 ? p.by_block.div(n - 1) + 1 : 0; }
 
+// The last of 0 .. n - 1 that is 0 or below(i), which holds up to some i.  As many steps for every thread.
+template <typename F>
+__device__ __forceinline__ int last_below(int n, F below) {
+  int at = 0;
+  for (int step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; step > 0; step >>= 1)
+    if (at + step < n && below(at + step)) at += step;
+  return at;
+}
+
 // The last sequence that begins at or before block x: those without blocks begin where the next one does.
 __device__ __forceinline__ int seq_of_block(const int* nblk, int B, int x) {
-  int b = 0, hi = B;
-  while (hi - b > 1) {
-    const int mid = (b + hi) >> 1;
-    if (nblk[mid] <= x) b = mid;
-    else hi = mid;
-  }
-  return b;
+  return last_below(B, [&](int b) { return nblk[b] <= x; });
 }
 
 // Exclusive prefix sums of the threads' values, and their total.
@@ -332,7 +335,11 @@ __global__ void __maxnreg__(C::MAXREG)
   // ---------------------------------------------------------------- plan: this CTA's range of all units' tiles
   {
     constexpr int NT = C::NTHREADS;
-    int* const nblk = reinterpret_cast<int*>(smem);          // blocks before each sequence, where the tiles will lie
+    // Where the tiles will lie: blocks before each sequence, then the sequences, if they fit.
+    int* const nblk = reinterpret_cast<int*>(smem);
+    Seq* const seqs = reinterpret_cast<Seq*>(smem + (4 * p.B + 4 + 15) / 16 * 16);
+    const bool kept = p.B <= C::OFF_BAR / 20 - 2;
+    const auto seq_at = [&](int b) { return kept && b < p.B ? seqs[b] : load_seq(p, b); };
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
@@ -340,6 +347,7 @@ __global__ void __maxnreg__(C::MAXREG)
       if (blockIdx.x == 0 && s.n == 0 && (p.cu[b] < 0 || p.cu[b] != p.cu[b + 1] || p.cu[b] > p.T))
         record_bad_index(p.err, W_OFFSETS);
       if (blockIdx.x == 0 && s.bad) record_bad_index(p.err, W_LENGTH);
+      if (kept) seqs[b] = s;
       const int nb = blocks_of(p, s.n);
       if (per > 1) nblk[b] = nb;
       mine += nb;
@@ -365,9 +373,9 @@ __global__ void __maxnreg__(C::MAXREG)
     int all_tiles, tiles = 0;  // of a key/value head: fewer than 2^31 (fa_fwd_paged's limit)
     if (x0 < x1) {
       int b = seq_of_block(nblk, p.B, x0);
-      Seq s = load_seq(p, b);
+      Seq s = seq_at(b);
       for (int x = x0; x < x1; ++x) {
-        while (x >= nblk[b + 1]) s = load_seq(p, ++b);
+        while (x >= nblk[b + 1]) s = seq_at(++b);
         tiles += block_tiles<BC>(p, s, x - nblk[b]);
       }
     }
@@ -387,20 +395,19 @@ __global__ void __maxnreg__(C::MAXREG)
     int h[2] = {0, 0}, at_block[2] = {0, 0};
     const bool mine_too = tid < ranges;
     if (mine_too) {
+      long long in_head[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         w[k] = range_begin(total, tid + k, ranges);
-        h[k] = static_cast<int>(divide(w[k], head));
+        h[k] = static_cast<int>(static_cast<unsigned>(tid + k) * p.Hkv / ranges);  // w[k] / head: total is Hkv heads
+        in_head[k] = w[k] - h[k] * head;
       }
       const int n = pb > 1 ? (blocks + pb - 1) / pb : blocks;
-      int lo[2] = {0, 0}, hi[2] = {n, n};
-      while (hi[0] - lo[0] > 1 || hi[1] - lo[1] > 1) {
+      int lo[2] = {0, 0};
+      for (int step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; step > 0; step >>= 1) {  // last_below, both side by side
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int mid = (lo[k] + hi[k]) >> 1;  // lo itself at the end
-          if (place[mid] <= w[k] - h[k] * head) lo[k] = mid;
-          else hi[k] = mid;
-        }
+        for (int k = 0; k < 2; ++k)
+          if (lo[k] + step < n && place[lo[k] + step] <= in_head[k]) lo[k] += step;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
