@@ -19,8 +19,12 @@
 // evenly to the CTAs, one contiguous range each, whatever the lengths are (they stay in device memory; every CTA sums them
 // itself, 3.5 us).  A range covers whole units, which the CTA finishes, and at most two parts of units at its ends, whose states
 // (m, l, unnormalised O) it leaves in the workspace; fa_fwd_paged_join_kernel joins those in the order of the keys.  Where
-// ranges of whole units are hardly longer, no unit is cut (256 units of 19 tiles, d = 64: 34 us, cut into 304 ranges 44).  No
-// atomics on results: they depend on the lengths and the SM count alone.
+// ranges of whole units are hardly longer, no unit is cut (256 units of 19 tiles, d = 64: 34 us, cut into 304 ranges 44).
+//
+// Small calls are not dealt (CLUSTER, cluster_size): where the units, then of one row tile, are few and short enough, each has a
+// cluster of 1 to 16 CTAs with even shares of its tiles, and the cluster joins its states through its shared memory.
+//
+// No atomics on results: they depend on the lengths, the arguments and the SM count alone.
 //
 // Keys and values come out of the pages by TMA boxes of as many rows as divide the page size (8 at least: a swizzle
 // period), or, where no such box exists, by 16-byte asynchronous copies.  Keys that no row of the block sees are not read
@@ -32,8 +36,11 @@
 // TFLOP/s of the formula's products (the dense causal forward takes about the same).  At d = 64 the exponentials' latency, as in
 // the dense forward: 37 sequences of up to 512 tokens over up to 8192 keys, 32 heads on 4, 78 us, 700 TFLOP/s with start,
 // ends and masked tiles.  Few tokens over long contexts device memory: 24 sequences of 3 to 7 tokens, 1.41 GB, 220 us, 6.4 TB/s.
-// Small calls latency: 23 tokens behind 1000 keys 14.5 us: 3.5 to the plan, 3 to the first scores, 3 to the states, 4 the join.
+// Small calls latency: 23 tokens behind 1000 keys 10.4 us (dealt 13.2 and a call 13.9: 3 for the plan, 3 to the first scores, 3 to
+// the states, 4 for the join).
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "fa_fwd_kernel.cuh"
 
@@ -62,6 +69,7 @@ struct ChunkCfg {
   // tile or two (a step of one is bound by its chain of products and exponentials, or by the tile's bytes).  A prompt of 8191
   // tokens, d = 128, with 2, 3, 4: 371, 357, 362 us; a mixed batch, d = 64: 88, 83, 79.
   static constexpr int COST_UNIT = D == 128 ? 3 : 4;
+  static constexpr int CLUSTER_TILES = D == 128 ? 6 : 8;  // cluster_size
   static constexpr int UNITS = 4;                // units announced at a time
   static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
   static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
@@ -70,6 +78,7 @@ struct ChunkCfg {
   static constexpr int OFF_STAGE = OFF_UNITS + UNITS * 64;
   static constexpr int OFF_MISC = OFF_STAGE + 8 * STAGE_BYTES;
   static constexpr int SMEM_BYTES = OFF_MISC + 160 + (32 * 11 + 2) * 8 + 1024;  // plan's scratch; slack to align the base to 1024
+  static constexpr int OFF_ML = OFF_Q + Q_BYTES;  // CLUSTER: m, l of the rows, where the second tile's queries would lie
   static constexpr int O_COL0 = 2 * BC;          // TMEM: S_t at t * BC, O_t at O_COL0 + t * D
   static constexpr int TMEM_COLS = 2 * (BC + D);
   // The values have a load warp of their own at d = 128 (FwdCfg::SPLIT_LOADS); it comes free of registers there.
@@ -80,12 +89,15 @@ struct ChunkCfg {
   static constexpr int MAXREG = (16384 / (WARPS_PER_SUBPART * 32)) / 8 * 8;
   static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "tensor memory");
   static_assert(SMEM_BYTES * MINB <= 227 * 1024, "shared memory");
+  static_assert(BR * D * 4 <= STAGES * KV_BYTES, "a cluster's states lie where the keys were");
   static_assert((FWD_PAGED_MAX_B + 1) * 4 <= OFF_BAR, "the plan's block counts lie where the tiles will");
 };
 
 // Cutting units costs their states, written and read again, and a start and an end more: so no unit is cut where the
 // longest range of whole units is at most this much longer than an even share.
 constexpr int COST_CUT = 6;
+
+constexpr int MAX_CLUSTER = 16;  // above 8 it has to be asked for
 
 struct ChunkParams {
   __nv_bfloat16* o;
@@ -103,6 +115,7 @@ struct ChunkParams {
   struct Shared* shared;  // [CTA]
   FastDiv by_g, by_page, by_block;
   int T, B, H, Hkv, G, tile_tokens, part_rows, part_tiles;
+  int cl;  // CTAs of a unit, where each unit has a cluster
   int num_pages, page_size, max_pages, box_rows, heads_inner;
   int window, sinks;
   float c, tau, p_lim;
@@ -239,8 +252,9 @@ __device__ __forceinline__ T scan(T v, T* tmp, T* total) {
 }
 
 // Adds the values set aside (infinities, NaN) of the keys that the token at `pos` sees to its row of O, whose element e lies at
-// o + e / run * stride + e % run: rare, so it reads back what the epilogue has just written.
-template <class C, typename T>
+// o + e / run * stride + e % run, or with SWAP, stride the row, in 16-byte pieces swapped by it: rare, so it reads back what the
+// epilogue has just written.
+template <class C, bool SWAP, typename T>
 __device__ __noinline__ void add_aside(const ChunkParams& p, const volatile Unit& u, int pos, T* o, int run, long long stride) {
   const int last_lo = p.window > 0 ? max(0, u.pos0 + u.ntok - p.window) : 0;
   for (int j = u.jb; j < u.je; ++j) {
@@ -255,7 +269,7 @@ __device__ __noinline__ void add_aside(const ChunkParams& p, const volatile Unit
       for (int e = 0; e < C::D; ++e) {
         const float x = __bfloat162float(v[e]);
         if (!(fabsf(x) < INFINITY)) {
-          T& y = o[e / run * stride + e % run];
+          T& y = SWAP ? o[((e / 4) ^ (static_cast<int>(stride) & (C::D / 4 - 1))) * 4 + e % 4] : o[e / run * stride + e % run];
           y = static_cast<T>(static_cast<float>(y) + x);
         }
       }
@@ -263,7 +277,86 @@ __device__ __noinline__ void add_aside(const ChunkParams& p, const volatile Unit
   }
 }
 
+// ---- thread-block clusters
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The shared-memory address `addr` of this CTA in CTA `rank` of its cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 load_peer8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_peer16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Joins a unit's states, which lie in its cluster's shared memory, in the order of the keys; a CTA has every cl-th row, a
+// thread four columns of one.
 template <class C>
+__device__ __forceinline__ void join_cluster(const ChunkParams& p, const Unit& u, uint32_t sbase) {
+  constexpr int PCS = C::D / 4, N = 4;  // states on their way at a time
+  const int rows = u.ntok * p.G, pc = threadIdx.x % PCS;
+  for (int row = threadIdx.x / PCS * p.cl + blockIdx.x % p.cl; row < rows; row += C::NTHREADS / PCS * p.cl) {
+    if (threadIdx.x >= C::NTHREADS / PCS * PCS) break;
+    const uint32_t at_o = sbase + C::OFF_K + row * (C::D * 4) + ((pc ^ (row & (PCS - 1))) << 4);
+    const uint32_t at_ml = sbase + C::OFF_ML + row * 8;
+    float m = -INFINITY, l = 0.f, o[4] = {};
+    for (int c0 = 0; c0 < p.cl; c0 += N) {
+      float2 ml[N];
+      float4 x[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + k < p.cl) {
+          ml[k] = load_peer8(peer_addr(at_ml, c0 + k));
+          x[k] = load_peer16(peer_addr(at_o, c0 + k));
+        }
+      }
+      float m_new = m;
+#pragma unroll
+      for (int k = 0; k < N; ++k) m_new = fmaxf(m_new, ml[k].x);
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;  // no part so far sees a key of this row: weights of 0
+      const float old = ex2_approx(m - m_use);
+      l *= old;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= old;
+      m = m_new;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float w = ex2_approx(ml[k].x - m_use);
+        l = fmaf(w, ml[k].y, l);
+        o[0] = fmaf(w, x[k].x, o[0]);
+        o[1] = fmaf(w, x[k].y, o[1]);
+        o[2] = fmaf(w, x[k].z, o[2]);
+        o[3] = fmaf(w, x[k].w, o[3]);
+      }
+    }
+    const int tok = p.by_g.div(row), g = row - tok * p.G;
+    const float inv = 1.f / l;
+    const size_t out = static_cast<size_t>(u.q0 + tok) * p.H + u.h * p.G + g;
+    *reinterpret_cast<uint2*>(p.o + out * C::D + pc * 4) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (p.lse != nullptr && pc == 0) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// CLUSTER: no dealing, each unit (of one row tile) has a cluster of CTAs, which take even shares of its tiles.
+template <class C, bool CLUSTER>
 __global__ void __maxnreg__(C::MAXREG)
     fa_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
@@ -368,72 +461,83 @@ __global__ void __maxnreg__(C::MAXREG)
     }
     if (tid == 0) nblk[p.B] = blocks;
     __syncthreads();
-    // A thread's blocks x0 .. x1 - 1 (of each key/value head), their tiles, and the tiles before them
-    const int pb = (blocks + NT - 1) / NT, x0 = min(blocks, tid * pb), x1 = min(blocks, x0 + pb);
-    int all_tiles, tiles = 0;  // of a key/value head: fewer than 2^31 (fa_fwd_paged's limit)
-    if (x0 < x1) {
-      int b = seq_of_block(nblk, p.B, x0);
-      Seq s = seq_at(b);
-      for (int x = x0; x < x1; ++x) {
-        while (x >= nblk[b + 1]) s = seq_at(++b);
-        tiles += block_tiles<BC>(p, s, x - nblk[b]);
+    if constexpr (CLUSTER) {
+      if (tid == 0) {
+        const int unit = blockIdx.x / p.cl, x = unit / p.Hkv, b = x < blocks ? seq_of_block(nblk, p.B, x) : 0;
+        plan_start[0] = unit - x * p.Hkv;
+        plan_start[1] = x - nblk[b];
+        plan_start[2] = x < blocks;
+        plan_start[5] = b;
+        units[0].ntok = 0;
       }
-    }
-    const int before = scan<NT>(tiles, plan_tmp, &all_tiles);
-    // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
-    // each takes one, and starts and ends do not count.
-    const int extra = static_cast<long long>(all_tiles) * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
-    long long* const place = plan_place;  // of each thread's first block in its head
-    place[tid] = before + static_cast<long long>(extra) * x0;
-    const long long head = all_tiles + static_cast<long long>(extra) * blocks, total = head * p.Hkv;
-    const int ranges = static_cast<int>(min(static_cast<long long>(min(static_cast<int>(gridDim.x), NT - 1)), total));
-    __syncthreads();
-    // Thread i looks up where ranges i and i + 1 begin: the unit that their first place lies in (or, with several blocks a
-    // thread, the first one of that thread's).  Where a thread has one block at most, it also knows how long range i is if it
-    // takes the units that begin in it, whole.
-    long long from[2] = {0, 0}, w[2] = {0, 0}, next[2] = {0, 0};
-    int h[2] = {0, 0}, at_block[2] = {0, 0};
-    const bool mine_too = tid < ranges;
-    if (mine_too) {
-      long long in_head[2];
+    } else {
+      // A thread's blocks x0 .. x1 - 1 (of each key/value head), their tiles, and the tiles before them
+      const int pb = (blocks + NT - 1) / NT, x0 = min(blocks, tid * pb), x1 = min(blocks, x0 + pb);
+      int all_tiles, tiles = 0;  // of a key/value head: fewer than 2^31 (fa_fwd_paged's limit)
+      if (x0 < x1) {
+        int b = seq_of_block(nblk, p.B, x0);
+        Seq s = seq_at(b);
+        for (int x = x0; x < x1; ++x) {
+          while (x >= nblk[b + 1]) s = seq_at(++b);
+          tiles += block_tiles<BC>(p, s, x - nblk[b]);
+        }
+      }
+      const int before = scan<NT>(tiles, plan_tmp, &all_tiles);
+      // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
+      // each takes one, and starts and ends do not count.
+      const int extra = static_cast<long long>(all_tiles) * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
+      long long* const place = plan_place;  // of each thread's first block in its head
+      place[tid] = before + static_cast<long long>(extra) * x0;
+      const long long head = all_tiles + static_cast<long long>(extra) * blocks, total = head * p.Hkv;
+      const int ranges = static_cast<int>(min(static_cast<long long>(min(static_cast<int>(gridDim.x), NT - 1)), total));
+      __syncthreads();
+      // Thread i looks up where ranges i and i + 1 begin: the unit that their first place lies in (or, with several blocks a
+      // thread, the first one of that thread's).  Where a thread has one block at most, it also knows how long range i is if it
+      // takes the units that begin in it, whole.
+      long long from[2] = {0, 0}, w[2] = {0, 0}, next[2] = {0, 0};
+      int h[2] = {0, 0}, at_block[2] = {0, 0};
+      const bool mine_too = tid < ranges;
+      if (mine_too) {
+        long long in_head[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        w[k] = range_begin(total, tid + k, ranges);
-        h[k] = static_cast<int>(static_cast<unsigned>(tid + k) * p.Hkv / ranges);  // w[k] / head: total is Hkv heads
-        in_head[k] = w[k] - h[k] * head;
-      }
-      const int n = pb > 1 ? (blocks + pb - 1) / pb : blocks;
-      int lo[2] = {0, 0};
-      for (int step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; step > 0; step >>= 1) {  // last_below, both side by side
+        for (int k = 0; k < 2; ++k) {
+          w[k] = range_begin(total, tid + k, ranges);
+          h[k] = static_cast<int>(static_cast<unsigned>(tid + k) * p.Hkv / ranges);  // w[k] / head: total is Hkv heads
+          in_head[k] = w[k] - h[k] * head;
+        }
+        const int n = pb > 1 ? (blocks + pb - 1) / pb : blocks;
+        int lo[2] = {0, 0};
+        for (int step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; step > 0; step >>= 1) {  // last_below, both side by side
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (lo[k] + step < n && place[lo[k] + step] <= in_head[k]) lo[k] += step;
-      }
+          for (int k = 0; k < 2; ++k)
+            if (lo[k] + step < n && place[lo[k] + step] <= in_head[k]) lo[k] += step;
+        }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        from[k] = h[k] * head + place[lo[k]];
-        next[k] = lo[k] + 1 < n ? h[k] * head + place[lo[k] + 1] : (h[k] + 1LL) * head;
-        at_block[k] = lo[k] * max(pb, 1);
+        for (int k = 0; k < 2; ++k) {
+          from[k] = h[k] * head + place[lo[k]];
+          next[k] = lo[k] + 1 < n ? h[k] * head + place[lo[k] + 1] : (h[k] + 1LL) * head;
+          at_block[k] = lo[k] * max(pb, 1);
+        }
       }
-    }
-    // the first unit that begins in a range or behind it
-    const long long length = (w[1] == total ? total : w[1] == from[1] ? w[1] : next[1]) - (w[0] == from[0] ? w[0] : next[0]);
-    const bool whole = __syncthreads_and(!mine_too || (pb <= 1 && length <= divide(total, ranges) + COST_CUT));
-    if (tid == static_cast<int>(blockIdx.x) && mine_too) {
-      const int b = seq_of_block(nblk, p.B, at_block[0]);
-      plan_start[0] = h[0];
-      plan_start[1] = at_block[0] - nblk[b];
-      plan_start[5] = b;
-      plan_at[0] = from[0];
-      plan_at[1] = total;
-      plan_at[2] = w[0];
-      plan_at[3] = w[1];
-    }
-    if (tid == 0) {
-      plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
-      plan_start[3] = extra;
-      plan_start[4] = whole;
-      p.shared[blockIdx.x].parts = 0;
+      // the first unit that begins in a range or behind it
+      const long long length = (w[1] == total ? total : w[1] == from[1] ? w[1] : next[1]) - (w[0] == from[0] ? w[0] : next[0]);
+      const bool whole = __syncthreads_and(!mine_too || (pb <= 1 && length <= divide(total, ranges) + COST_CUT));
+      if (tid == static_cast<int>(blockIdx.x) && mine_too) {
+        const int b = seq_of_block(nblk, p.B, at_block[0]);
+        plan_start[0] = h[0];
+        plan_start[1] = at_block[0] - nblk[b];
+        plan_start[5] = b;
+        plan_at[0] = from[0];
+        plan_at[1] = total;
+        plan_at[2] = w[0];
+        plan_at[3] = w[1];
+      }
+      if (tid == 0) {
+        plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
+        plan_start[3] = extra;
+        plan_start[4] = whole;
+        p.shared[blockIdx.x].parts = 0;
+      }
     }
     __syncthreads();
     if (p.G * p.tile_tokens < C::BR) {  // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
@@ -473,53 +577,75 @@ __global__ void __maxnreg__(C::MAXREG)
     for (int iu = 0; ok; ++iu) {
       const int slot = iu % C::UNITS;
       if (do_k) {
-        // the next unit with work in this range
         u.kind = UNIT_NONE;
-        while (at < w1) {
-          if (base < 0 || b < base || b >= base + 32) {
-            base = b;
-            mine = load_seq(p, base + lane);
+        if constexpr (CLUSTER) {
+          if (iu == 0) {
+            const Seq s = load_seq(p, b);
+            const int first = blk * p.tile_tokens;
+            u.h = h;
+            u.b = b;
+            u.q0 = s.q0 + first;
+            u.ntok = min(p.tile_tokens, s.n - first);
+            u.pos0 = s.pos0 + first;
+            u.bad_page = u.set_aside = 0;
+            const Span sp = span_of<BC>(p, u.pos0, u.ntok);
+            const int rank = blockIdx.x % p.cl;
+            u.jb = s.bad ? 0 : static_cast<long long>(sp.tiles) * rank / p.cl;
+            u.je = s.bad ? 0 : static_cast<long long>(sp.tiles) * (rank + 1) / p.cl;
+            u.ns = sp.ns;
+            u.w0 = sp.w0;
+            u.lo = sp.lo;
+            u.hi = sp.hi;
+            u.kind = s.bad ? UNIT_BAD : p.cl == 1 ? UNIT_WHOLE : UNIT_BEGUN;
           }
-          Seq s;
-          s.q0 = __shfl_sync(0xffffffffu, mine.q0, b - base);
-          s.n = __shfl_sync(0xffffffffu, mine.n, b - base);
-          s.pos0 = __shfl_sync(0xffffffffu, mine.pos0, b - base);
-          s.bad = __shfl_sync(0xffffffffu, static_cast<int>(mine.bad), b - base);
-          const int first = blk * 2 * p.tile_tokens;
-          if (first >= s.n) {  // past the sequence's last block
-            blk = 0;
-            if (++b >= p.B) {
-              b = 0;
-              ++h;
+        } else {
+          // the next unit with work in this range
+          while (at < w1) {
+            if (base < 0 || b < base || b >= base + 32) {
+              base = b;
+              mine = load_seq(p, base + lane);
             }
-            continue;
-          }
-          const long long start = at;
-          at += block_tiles<BC>(p, s, blk) + extra;
-          u.h = h;
-          u.b = b;
-          u.q0 = s.q0 + first;
-          u.ntok = min(2 * p.tile_tokens, s.n - first);
-          u.pos0 = s.pos0 + first;
-          ++blk;
-          u.bad_page = u.set_aside = 0;
-          u.jb = u.je = u.ns = u.w0 = u.lo = u.hi = 0;
-          if ((whole || s.bad) && start < w0) continue;  // the range that it begins in has it
-          if (s.bad) {
-            u.kind = UNIT_BAD;
+            Seq s;
+            s.q0 = __shfl_sync(0xffffffffu, mine.q0, b - base);
+            s.n = __shfl_sync(0xffffffffu, mine.n, b - base);
+            s.pos0 = __shfl_sync(0xffffffffu, mine.pos0, b - base);
+            s.bad = __shfl_sync(0xffffffffu, static_cast<int>(mine.bad), b - base);
+            const int first = blk * 2 * p.tile_tokens;
+            if (first >= s.n) {  // past the sequence's last block
+              blk = 0;
+              if (++b >= p.B) {
+                b = 0;
+                ++h;
+              }
+              continue;
+            }
+            const long long start = at;
+            at += block_tiles<BC>(p, s, blk) + extra;
+            u.h = h;
+            u.b = b;
+            u.q0 = s.q0 + first;
+            u.ntok = min(2 * p.tile_tokens, s.n - first);
+            u.pos0 = s.pos0 + first;
+            ++blk;
+            u.bad_page = u.set_aside = 0;
+            u.jb = u.je = u.ns = u.w0 = u.lo = u.hi = 0;
+            if ((whole || s.bad) && start < w0) continue;  // the range that it begins in has it
+            if (s.bad) {
+              u.kind = UNIT_BAD;
+              break;
+            }
+            const Span sp = span_of<BC>(p, u.pos0, u.ntok);
+            u.jb = whole ? 0 : cut(w0, start, sp.tiles, extra);
+            u.je = whole ? sp.tiles : cut(w1, start, sp.tiles, extra);
+            if (u.jb >= u.je) continue;  // it lies before the range, or its first tile behind it
+            u.ns = sp.ns;
+            u.w0 = sp.w0;
+            u.lo = sp.lo;
+            u.hi = sp.hi;
+            u.kind = u.jb > 0 ? UNIT_CONTINUED : u.je < sp.tiles ? UNIT_BEGUN : UNIT_WHOLE;
+            if (u.kind != UNIT_WHOLE) cut_at = start + extra, cut_tiles = sp.tiles;
             break;
           }
-          const Span sp = span_of<BC>(p, u.pos0, u.ntok);
-          u.jb = whole ? 0 : cut(w0, start, sp.tiles, extra);
-          u.je = whole ? sp.tiles : cut(w1, start, sp.tiles, extra);
-          if (u.jb >= u.je) continue;  // it lies before the range, or its first tile behind it
-          u.ns = sp.ns;
-          u.w0 = sp.w0;
-          u.lo = sp.lo;
-          u.hi = sp.hi;
-          u.kind = u.jb > 0 ? UNIT_CONTINUED : u.je < sp.tiles ? UNIT_BEGUN : UNIT_WHOLE;
-          if (u.kind != UNIT_WHOLE) cut_at = start + extra, cut_tiles = sp.tiles;
-          break;
         }
         if (iu >= C::UNITS) ok = wait_all(bar_ue(slot), (iu / C::UNITS - 1) & 1, W_DESC_FREE);
         if (!ok) break;
@@ -704,7 +830,7 @@ __global__ void __maxnreg__(C::MAXREG)
       }
       if (!do_k && lane == 0) mbar_arrive(bar_ue(slot));
       // A range is a tile long at least: every CTA between the first and the last one has a part.
-      if (do_k && (u.kind == UNIT_BEGUN || u.kind == UNIT_CONTINUED) && lane == 0) {
+      if (!CLUSTER && do_k && (u.kind == UNIT_BEGUN || u.kind == UNIT_CONTINUED) && lane == 0) {
         const int from = range_of(total, ranges, cut_at), to = range_of(total, ranges, cut_at + cut_tiles - 1);
         p.shared[blockIdx.x] = Shared{from, to - from + 1, u.h, u.q0, u.ntok};
       }
@@ -1010,7 +1136,7 @@ __global__ void __maxnreg__(C::MAXREG)
       const bool any_rows = t * p.tile_tokens < ntok;
       if (!any_rows) {
         // a block of one tile
-      } else if (kind == UNIT_WHOLE || kind == UNIT_BAD) {
+      } else if (CLUSTER ? p.cl == 1 : kind == UNIT_WHOLE || kind == UNIT_BAD) {
         // A thread holds a row: written straight from there, a warp's 16 bytes a lane would touch 32 half sectors.  So OUT_COLS
         // columns at a time go through shared memory (16-byte pieces swapped by the row) and out in whole sectors.
         constexpr int PCS = C::OUT_COLS / 8, RPI = 32 / PCS;  // pieces of a row, rows a store
@@ -1055,11 +1181,13 @@ __global__ void __maxnreg__(C::MAXREG)
           }
         }
         if (p.lse != nullptr && real) p.lse[out] = (m_ref + log2f(l)) * 0.6931471805599453f;
-        if (aside && real) add_aside<C>(p, uv, pos, p.o + out * D, D, 0);
+        if (aside && real) add_aside<C, false>(p, uv, pos, p.o + out * D, D, 0);
       } else {
-        // Partial state: 16-byte pieces of the rows side by side, so that a warp's stores are whole lines.
+        // Partial state: 16-byte pieces of the rows side by side, so that a warp's stores are whole lines; in a cluster rows side
+        // by side in shared memory, where the keys were, their pieces swapped by the row.
         const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (kind == UNIT_BEGUN)) * p.part_tiles + t;
-        float4* const po = p.part_o + part * (D / 4) * p.part_rows + row;
+        float4* const po = CLUSTER ? reinterpret_cast<float4*>(smem + C::OFF_K) + row * (D / 4)
+                                   : p.part_o + part * (D / 4) * p.part_rows + row;
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t orr[32];
@@ -1074,13 +1202,14 @@ __global__ void __maxnreg__(C::MAXREG)
           if (real) {
 #pragma unroll
             for (int v4 = 0; v4 < 8; ++v4)
-              po[static_cast<size_t>(cc * 8 + v4) * p.part_rows] =
+              po[CLUSTER ? (cc * 8 + v4) ^ (row & (D / 4 - 1)) : static_cast<size_t>(cc * 8 + v4) * p.part_rows] =
                   make_float4(__uint_as_float(orr[4 * v4]), __uint_as_float(orr[4 * v4 + 1]), __uint_as_float(orr[4 * v4 + 2]),
                               __uint_as_float(orr[4 * v4 + 3]));
           }
         }
-        if (real) p.part_ml[part * p.part_rows + row] = make_float2(m_ref, l);
-        if (aside && real) add_aside<C>(p, uv, pos, reinterpret_cast<float*>(po), 4, 4LL * p.part_rows);
+        float2* const pml = CLUSTER ? reinterpret_cast<float2*>(smem + C::OFF_ML) + row : p.part_ml + part * p.part_rows + row;
+        if (real) *pml = make_float2(m_ref, l);
+        if (aside && real) add_aside<C, CLUSTER>(p, uv, pos, reinterpret_cast<float*>(po), 4, CLUSTER ? row : 4LL * p.part_rows);
       }
       tc_fence_before();  // O has been read: the next unit's first P V comes behind this warp's next hand_over
       __syncwarp();
@@ -1090,10 +1219,16 @@ __global__ void __maxnreg__(C::MAXREG)
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  const bool shared = CLUSTER && p.cl > 1;
+  if (shared) cluster_sync();
+  else __syncthreads();
   if (warp == C::LOAD_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (shared) {
+    join_cluster<C>(p, units[0], sbase);
+    cluster_sync();  // a CTA's shared memory is there while others read it
   }
 }
 
@@ -1216,9 +1351,27 @@ int box_rows_of(int page_size, int bc) {
   return r > bc ? bc : r;
 }
 
+// CTAs of a unit where every unit has a cluster, or 0 for ranges.  `units`: at most; `tiles`: of the longest one that its
+// table, or the window, allows; n_cta: CTAs that may run at once.  As many as there is room for, less the places that clusters
+// of this size leave free in each of the GPU's 8 processor clusters.
+//
+// A cluster saves the dealing, the states in memory and the join, 3 to 6 us, but its CTAs work on no other unit.  So it is taken
+// where its CTAs' tiles are at most C::CLUSTER_TILES more than an even share: that of one longest sequence alone, or of
+// sequences half as long.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 10.4,
+// d = 64 12.5 and 9.4; behind 4000 15.8 and 14.3, 16.2 and 12.7; behind 16000 21.0 and 25.2, 20.8 and 23.5; 16 x 4 tokens behind
+// 1000 21.1 and 17.5, 21.0 and 15.7; behind 1 to 1000 20.9 and 17.5, 17.8 and 14.9; behind 1 to 4000 39 and 46, 29 and 36; a prompt
+// of 500 17.8 and 13.1 both.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
+int cluster_size(long long units, long long tiles, int Hkv, int n_cta, int more) {
+  int cl = 1;
+  while (cl < MAX_CLUSTER && cl < tiles && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
+  const long long share = std::max(tiles * Hkv, units * tiles / 2) / n_cta;
+  return units * cl <= n_cta && (tiles + cl - 1) / cl <= share + more ? cl : 0;
+}
+
 template <class C>
 cudaError_t launch_cfg(const FwdPagedLaunch& a) {
-  cudaError_t e = allow_shared_memory<fa_fwd_paged_kernel<C>>(C::SMEM_BYTES);
+  cudaError_t e = allow_shared_memory<fa_fwd_paged_kernel<C, false>>(C::SMEM_BYTES);
+  if (e == cudaSuccess) e = allow_shared_memory<fa_fwd_paged_kernel<C, true>>(C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const Layout l = layout_of(a.T, a.H, a.Hkv, a.d, a.sms);
   ChunkParams p = {};
@@ -1240,12 +1393,20 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
   p.G = a.H / a.Hkv;
   p.by_g = FastDiv(static_cast<unsigned>(p.G));
   p.by_page = FastDiv(static_cast<unsigned>(a.page_size));
-  p.by_block = FastDiv(static_cast<unsigned>(2 * (C::BR / p.G)));
   p.T = a.T;
   p.B = a.B;
   p.H = a.H;
   p.Hkv = a.Hkv;
   p.tile_tokens = C::BR / p.G;
+  const int n_cta = a.sms * C::MINB;
+  long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + C::BC - 1) / C::BC;
+  if (a.window > 0) {
+    const long long seen = (static_cast<long long>(a.window) + p.tile_tokens) / C::BC + 2 + a.sinks / C::BC + 1;
+    tiles = seen < tiles ? seen : tiles;
+  }
+  const long long units = (static_cast<long long>(a.T) / p.tile_tokens + (a.B < a.T ? a.B : a.T)) * a.Hkv;
+  p.cl = cluster_size(units, tiles, a.Hkv, n_cta, C::CLUSTER_TILES);
+  p.by_block = FastDiv(static_cast<unsigned>(p.cl > 0 ? p.tile_tokens : 2 * p.tile_tokens));
   p.part_rows = l.rows;
   p.part_tiles = l.tiles;
   p.num_pages = a.num_pages;
@@ -1267,8 +1428,15 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
     e = encode_paged_map(&tv, a.v_cache, a.d, a.page_size, a.Hkv, a.num_pages, a.c_row, a.c_head, a.c_page, p.box_rows,
                          p.heads_inner);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(a.sms * C::MINB);
-  e = launch_dependent(fa_fwd_paged_kernel<C>, dim3(grid), C::NTHREADS, C::SMEM_BYTES, a.stream, tq, tk, tv, p);
+  if (p.cl > 8) {
+    e = cudaFuncSetAttribute(fa_fwd_paged_kernel<C, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.cl > 0)
+    return launch_dependent_clusters(fa_fwd_paged_kernel<C, true>, static_cast<unsigned>(units * p.cl), p.cl, C::NTHREADS,
+                                     C::SMEM_BYTES, a.stream, tq, tk, tv, p);
+  const unsigned grid = static_cast<unsigned>(n_cta);
+  e = launch_dependent(fa_fwd_paged_kernel<C, false>, dim3(grid), C::NTHREADS, C::SMEM_BYTES, a.stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(fa_fwd_paged_join_kernel<C::D>, dim3(grid, l.tiles, l.rows / 32), C::D * 4, 0, a.stream, p);
 }

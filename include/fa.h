@@ -496,7 +496,8 @@ int fa_paged_slots(const int* ctx_lens, const int* new_lens, int* page_table, lo
  * with a page outside the cache NaN in the tokens that the page reaches (and others near them); offsets that do
  * not ascend make their sequence's tokens stay unwritten, and give tokens that others then share unspecified values
  * or none.  fa_check_device_error then reports FA_ERR_INVALID_ARG.
- * Accumulation and softmax statistics are fp32.  No atomics on results: repeated calls on one GPU give identical bits.
+ * Accumulation and softmax statistics are fp32.  No atomics on results: repeated calls on one GPU give identical bits
+ * (other sizes of the call, a wider table, say, may change the last one).
  * H / Hkv <= 128, B <= 16384 (FA_ERR_UNSUPPORTED otherwise); max_pages * page_size < 2^30, T * (H / Hkv) <= 2^30 and
  * (T * (H / Hkv) / 128 + B + 1) * (max_pages * page_size / 64 + 3) < 2^31 (FA_ERR_INVALID_ARG otherwise).
  */

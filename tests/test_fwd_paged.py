@@ -59,11 +59,59 @@ def test_chunks(cuda_device, H, Hkv, d, ps, chunks):
     b.check(*b.run(), f"H{H}/{Hkv} d{d} ps{ps}")
 
 
+def many_places(H, Hkv):
+    """Places of q behind the last token with which a call may have more units than can have CTAs of their own."""
+    return 305 * (128 // (H // Hkv)) // Hkv + 1
+
+
+CHUNKS_BY_RANGES = [
+    (1, 1, 64, 16, [(0, 1)]), (4, 1, 128, 16, [(0, 1)]), (8, 2, 64, 16, [(63, 1)]), (8, 2, 128, 64, [(128, 1)]),
+    (4, 4, 64, 16, [(0, 64)]), (2, 2, 128, 32, [(0, 257)]), (8, 2, 64, 16, MIXED), (8, 2, 128, 16, MIXED),
+    (6, 2, 128, 24, MIXED), (5, 1, 64, 64, MIXED), (3, 3, 64, 24, MIXED), (8, 2, 64, 1, MIXED), (4, 2, 128, 20, MIXED),
+    (128, 1, 64, 16, [(77, 3), (0, 2)]), (100, 1, 128, 16, [(40, 5)])]
+
+
+@pytest.mark.parametrize("H,Hkv,d,ps,chunks", CHUNKS_BY_RANGES)
+def test_chunks_by_ranges(cuda_device, H, Hkv, d, ps, chunks):
+    b = Batch(cuda_device, H, Hkv, d, ps, chunks, pad=many_places(H, Hkv))
+    b.check(*b.run(), f"H{H}/{Hkv} d{d} ps{ps} dealt")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_sequence_by_clusters_of_each_size(cuda_device, d):
+    # tables of 1, 2, ... key tiles: as many CTAs a unit, up to 16, and more than that
+    for keys in (1, 64, 65, 129, 257, 385, 600, 1000, 1300, 2000, 2600, 4100):
+        for H, Hkv in ((4, 1), (16, 8)):
+            b = Batch(cuda_device, H, Hkv, d, 16, [(keys - 1, 1)] if keys < 9 else [(keys - 9, 9)])
+            b.check(*b.run(), f"{keys} keys, {Hkv} heads")
+
+
+def test_both_forms_agree(cuda_device):
+    # the same call with more places for tokens: another form, the same result but for the order of its sums
+    for d in (64, 128):
+        a = Batch(cuda_device, 8, 2, d, 16, [(900, 5), (0, 3), (130, 40)])
+        o, lse = a.run()
+        q = torch.zeros(a.T + many_places(8, 2), 8, d, dtype=BF, device=cuda_device)
+        q[:a.T] = a.q
+        o2, lse2 = a.run(q=q)
+        torch.cuda.synchronize()
+        # two results of the formula, each within check_fwd_paged's bound of it: P and o rounded to bf16, 2^-8 each
+        assert (o.float() - o2[:a.T].float()).abs().max() <= 2 * 2 ** -7 * a.vc.float().nan_to_num(0, 0, 0).abs().max()
+        assert (lse - lse2[:a.T]).abs().max() < 1e-4  # sums of 940 fp32 numbers in two orders: 940 * 2^-24, and ex2's 2^-22
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 3), (64, 0), (128, 4), (129, 130), (500, 64), (100000, 0), (200, 100000)])
 @pytest.mark.parametrize("H,Hkv,d,ps", [(8, 2, 64, 16), (4, 1, 128, 32), (3, 1, 128, 1), (2, 2, 64, 24)])
 def test_windows(cuda_device, H, Hkv, d, ps, window, sinks):
     b = Batch(cuda_device, H, Hkv, d, ps, MIXED + [(2000, 1), (1500, 200)], seed=window)
     b.check(*b.run(window=window, sinks=sinks), f"window {window} sinks {sinks}", window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 1), (7, 3), (64, 0), (129, 130), (500, 64)])
+@pytest.mark.parametrize("H,Hkv,d,ps", [(8, 2, 64, 16), (4, 1, 128, 32), (3, 1, 128, 1)])
+def test_windows_by_ranges(cuda_device, H, Hkv, d, ps, window, sinks):
+    b = Batch(cuda_device, H, Hkv, d, ps, MIXED, pad=many_places(H, Hkv))
+    b.check(*b.run(window=window, sinks=sinks), f"w{window} s{sinks} dealt", window=window, sinks=sinks)
 
 
 def test_pages_behind_the_window_may_be_gone(cuda_device):
@@ -146,6 +194,23 @@ def test_values_of_later_tokens_do_not_reach_earlier_ones(cuda_device):
             keep[:90][seen] = False
             assert torch.isfinite(o[keep]).all()
             assert (o[keep].float() - want[keep].float()).abs().max() <= 2 ** -7 * want[keep].float().abs().max()
+
+
+def test_infinite_values_and_bad_sequences_by_ranges(cuda_device):
+    for d, ps in ((64, 16), (128, 16), (128, 1)):
+        b = Batch(cuda_device, 4, 2, d, ps, [(100, 90), (30, 4), (20, 7)], seed=9, pad=many_places(4, 2))
+        want, _ = b.run()
+        for key in (100 + 37, 100 + 70):
+            b.vc[int(b.tables[0][key // ps]), :, key % ps, 5] = float("inf")
+        b.len_t[2] = 3  # fewer keys than new tokens
+        o, lse = b.run()
+        torch.cuda.synchronize()
+        assert fa.fa_check_device_error() == fa.FA_ERR_INVALID_ARG
+        assert (o[37:90, :, 5] == float("inf")).all() and torch.isnan(o[94:101]).all() and torch.isnan(lse[94:101]).all()
+        keep = torch.ones(94, 4, d, dtype=torch.bool, device=cuda_device)
+        keep[37:90, :, 5] = False
+        assert torch.isfinite(o[:94][keep]).all()
+        assert (o[:94][keep].float() - want[:94][keep].float()).abs().max() <= 2 ** -7 * want[:94][keep].float().abs().max()
 
 
 def test_bad_sequences_get_nan_and_others_nothing(cuda_device):
