@@ -36,7 +36,7 @@
 // TFLOP/s of the formula's products (the dense causal forward takes about the same).  At d = 64 the exponentials' latency, as in
 // the dense forward: 37 sequences of up to 512 tokens over up to 8192 keys, 32 heads on 4, 78 us, 700 TFLOP/s with start,
 // ends and masked tiles.  Few tokens over long contexts device memory: 24 sequences of 3 to 7 tokens, 1.41 GB, 220 us, 6.4 TB/s.
-// Small calls latency: 23 tokens behind 1000 keys 10.4 us (dealt 13.2 and a call 13.9: 3 for the plan, 3 to the first scores, 3 to
+// Small calls latency: 23 tokens behind 1000 keys 10.0 us (dealt 13.2: 3 for the plan, 3 to the first scores, 3 to
 // the states, 4 for the join).
 #include <cuda_bf16.h>
 
@@ -305,15 +305,14 @@ __device__ __forceinline__ float4 load_peer16(uint32_t addr) {
 }
 
 // Joins a unit's states, which lie in its cluster's shared memory, in the order of the keys; a CTA has every cl-th row, a
-// thread four columns of one.
+// thread four columns of one, four states on their way.  (Slices of the rows pushed to the CTAs that join them by bulk copies: 23
+// tokens behind 1000 keys 11.3 us instead of 10.0; eight states, or two rows a thread, 10.1 and 10.4.)
 template <class C>
 __device__ __forceinline__ void join_cluster(const ChunkParams& p, const Unit& u, uint32_t sbase) {
-  constexpr int PCS = C::D / 4, N = 4;  // states on their way at a time
+  constexpr int PCS = C::D / 4, PER = C::NTHREADS / PCS, N = 4;
   const int rows = u.ntok * p.G, pc = threadIdx.x % PCS;
-  for (int row = threadIdx.x / PCS * p.cl + blockIdx.x % p.cl; row < rows; row += C::NTHREADS / PCS * p.cl) {
-    if (threadIdx.x >= C::NTHREADS / PCS * PCS) break;
-    const uint32_t at_o = sbase + C::OFF_K + row * (C::D * 4) + ((pc ^ (row & (PCS - 1))) << 4);
-    const uint32_t at_ml = sbase + C::OFF_ML + row * 8;
+  if (threadIdx.x >= PER * PCS) return;
+  for (int row = threadIdx.x / PCS * p.cl + blockIdx.x; row < rows; row += PER * p.cl) {
     float m = -INFINITY, l = 0.f, o[4] = {};
     for (int c0 = 0; c0 < p.cl; c0 += N) {
       float2 ml[N];
@@ -323,8 +322,9 @@ __device__ __forceinline__ void join_cluster(const ChunkParams& p, const Unit& u
         ml[k] = make_float2(-INFINITY, 0.f);
         x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c0 + k < p.cl) {
-          ml[k] = load_peer8(peer_addr(at_ml, c0 + k));
-          x[k] = load_peer16(peer_addr(at_o, c0 + k));
+          const uint32_t peer = peer_addr(sbase, c0 + k);
+          ml[k] = load_peer8(peer + C::OFF_ML + row * 8);
+          x[k] = load_peer16(peer + C::OFF_K + row * (C::D * 4) + ((pc ^ (row & (PCS - 1))) << 4));
         }
       }
       float m_new = m;
@@ -355,7 +355,8 @@ __device__ __forceinline__ void join_cluster(const ChunkParams& p, const Unit& u
   }
 }
 
-// CLUSTER: no dealing, each unit (of one row tile) has a cluster of CTAs, which take even shares of its tiles.
+// CLUSTER: no dealing, each unit (of one row tile) has a cluster of CTAs, which take even shares of its tiles; the grid is the
+// cluster's CTAs, key/value heads, blocks.
 template <class C, bool CLUSTER>
 __global__ void __maxnreg__(C::MAXREG)
     fa_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -463,8 +464,8 @@ __global__ void __maxnreg__(C::MAXREG)
     __syncthreads();
     if constexpr (CLUSTER) {
       if (tid == 0) {
-        const int unit = blockIdx.x / p.cl, x = unit / p.Hkv, b = x < blocks ? seq_of_block(nblk, p.B, x) : 0;
-        plan_start[0] = unit - x * p.Hkv;
+        const int x = blockIdx.z, b = x < blocks ? seq_of_block(nblk, p.B, x) : 0;
+        plan_start[0] = blockIdx.y;
         plan_start[1] = x - nblk[b];
         plan_start[2] = x < blocks;
         plan_start[5] = b;
@@ -589,9 +590,8 @@ __global__ void __maxnreg__(C::MAXREG)
             u.pos0 = s.pos0 + first;
             u.bad_page = u.set_aside = 0;
             const Span sp = span_of<BC>(p, u.pos0, u.ntok);
-            const int rank = blockIdx.x % p.cl;
-            u.jb = s.bad ? 0 : static_cast<long long>(sp.tiles) * rank / p.cl;
-            u.je = s.bad ? 0 : static_cast<long long>(sp.tiles) * (rank + 1) / p.cl;
+            u.jb = s.bad ? 0 : sp.tiles * blockIdx.x / p.cl;  // fewer than 2^25 tiles
+            u.je = s.bad ? 0 : sp.tiles * (blockIdx.x + 1) / p.cl;
             u.ns = sp.ns;
             u.w0 = sp.w0;
             u.lo = sp.lo;
@@ -1357,10 +1357,10 @@ int box_rows_of(int page_size, int bc) {
 //
 // A cluster saves the dealing, the states in memory and the join, 3 to 6 us, but its CTAs work on no other unit.  So it is taken
 // where its CTAs' tiles are at most C::CLUSTER_TILES more than an even share: that of one longest sequence alone, or of
-// sequences half as long.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 10.4,
-// d = 64 12.5 and 9.4; behind 4000 15.8 and 14.3, 16.2 and 12.7; behind 16000 21.0 and 25.2, 20.8 and 23.5; 16 x 4 tokens behind
-// 1000 21.1 and 17.5, 21.0 and 15.7; behind 1 to 1000 20.9 and 17.5, 17.8 and 14.9; behind 1 to 4000 39 and 46, 29 and 36; a prompt
-// of 500 17.8 and 13.1 both.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
+// sequences half as long.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 10.0,
+// d = 64 12.5 and 10.1; behind 4000 15.8 and 14.7, 16.2 and 12.5; behind 16000 21.0 and 25.2, 20.8 and 23.5; 16 x 4 tokens behind
+// 1000 21.1 and 17.2, 21.0 and 15.5; behind 1 to 1000 20.9 and 17.3, 17.8 and 14.6; behind 1 to 4000 39 and 46, 29 and 36; a prompt
+// of 500 17.8 and 12.7, 17.8 and 12.9.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
 int cluster_size(long long units, long long tiles, int Hkv, int n_cta, int more) {
   int cl = 1;
   while (cl < MAX_CLUSTER && cl < tiles && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
@@ -1433,8 +1433,8 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
     if (e != cudaSuccess) return e;
   }
   if (p.cl > 0)
-    return launch_dependent_clusters(fa_fwd_paged_kernel<C, true>, static_cast<unsigned>(units * p.cl), p.cl, C::NTHREADS,
-                                     C::SMEM_BYTES, a.stream, tq, tk, tv, p);
+    return launch_dependent_clusters(fa_fwd_paged_kernel<C, true>, dim3(p.cl, a.Hkv, static_cast<unsigned>(units / a.Hkv)), p.cl,
+                                     C::NTHREADS, C::SMEM_BYTES, a.stream, tq, tk, tv, p);
   const unsigned grid = static_cast<unsigned>(n_cta);
   e = launch_dependent(fa_fwd_paged_kernel<C, false>, dim3(grid), C::NTHREADS, C::SMEM_BYTES, a.stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;

@@ -41,10 +41,10 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, i
 
 // The same in clusters of `cluster` CTAs (a divisor of the grid; above 8 the kernel has to allow it).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), unsigned grid, int cluster, int threads, int smem,
+cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid, int cluster, int threads, int smem,
                                       cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
