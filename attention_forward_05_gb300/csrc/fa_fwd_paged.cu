@@ -36,7 +36,7 @@
 // TFLOP/s of the formula's products (the dense causal forward takes about the same).  At d = 64 the exponentials' latency, as in
 // the dense forward: 37 sequences of up to 512 tokens over up to 8192 keys, 32 heads on 4, 78 us, 700 TFLOP/s with start,
 // ends and masked tiles.  Few tokens over long contexts device memory: 24 sequences of 3 to 7 tokens, 1.41 GB, 220 us, 6.4 TB/s.
-// Small calls latency: 23 tokens behind 1000 keys 10.0 us (dealt 13.2: 3 for the plan, 3 to the first scores, 3 to
+// Small calls latency: 23 tokens behind 1000 keys 9.7 us (dealt 13.2: 3 for the plan, 3 to the first scores, 3 to
 // the states, 4 for the join).
 #include <cuda_bf16.h>
 
@@ -304,9 +304,9 @@ __device__ __forceinline__ float4 load_peer16(uint32_t addr) {
   return v;
 }
 
-// Joins a unit's states, which lie in its cluster's shared memory, in the order of the keys; a CTA has every cl-th row, a
-// thread four columns of one, four states on their way.  (Slices of the rows pushed to the CTAs that join them by bulk copies: 23
-// tokens behind 1000 keys 11.3 us instead of 10.0; eight states, or two rows a thread, 10.1 and 10.4.)
+// Joins a unit's states, which lie in its cluster's shared memory; a CTA has every cl-th row, a thread four columns of one, four
+// states on their way.  (Slices of the rows pushed to the CTAs that join them by bulk copies instead: 23 tokens behind 1000 keys
+// 1.3 us more; eight states at a time, or two rows a thread, 0.1 and 0.4 us.)
 template <class C>
 __device__ __forceinline__ void join_cluster(const ChunkParams& p, const Unit& u, uint32_t sbase) {
   constexpr int PCS = C::D / 4, PER = C::NTHREADS / PCS, N = 4;
@@ -322,7 +322,8 @@ __device__ __forceinline__ void join_cluster(const ChunkParams& p, const Unit& u
         ml[k] = make_float2(-INFINITY, 0.f);
         x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c0 + k < p.cl) {
-          const uint32_t peer = peer_addr(sbase, c0 + k);
+          const int c = c0 + k + blockIdx.x;  // from its own on, so that not all read the same one
+          const uint32_t peer = peer_addr(sbase, c < p.cl ? c : c - p.cl);
           ml[k] = load_peer8(peer + C::OFF_ML + row * 8);
           x[k] = load_peer16(peer + C::OFF_K + row * (C::D * 4) + ((pc ^ (row & (PCS - 1))) << 4));
         }
@@ -386,6 +387,7 @@ __global__ void __maxnreg__(C::MAXREG)
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* const plan_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);             // head, block, ranges, extra, whole, sequence
   long long* const plan_at = reinterpret_cast<long long*>(smem + C::OFF_MISC + 32);   // start, total, range
+  Seq* const plan_seq = reinterpret_cast<Seq*>(plan_at);                              // CLUSTER: the unit's
   int* const plan_tmp = reinterpret_cast<int*>(smem + C::OFF_MISC + 64);              // 12 64-bit numbers
   long long* const plan_place = reinterpret_cast<long long*>(smem + C::OFF_MISC + 160);
 
@@ -429,118 +431,148 @@ __global__ void __maxnreg__(C::MAXREG)
   // ---------------------------------------------------------------- plan: this CTA's range of all units' tiles
   {
     constexpr int NT = C::NTHREADS;
-    // Where the tiles will lie: blocks before each sequence, then the sequences, if they fit.
-    int* const nblk = reinterpret_cast<int*>(smem);
-    Seq* const seqs = reinterpret_cast<Seq*>(smem + (4 * p.B + 4 + 15) / 16 * 16);
-    const bool kept = p.B <= C::OFF_BAR / 20 - 2;
-    const auto seq_at = [&](int b) { return kept && b < p.B ? seqs[b] : load_seq(p, b); };
-    const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(p, b);
-      if (blockIdx.x == 0 && s.n == 0 && (p.cu[b] < 0 || p.cu[b] != p.cu[b + 1] || p.cu[b] > p.T))
-        record_bad_index(p.err, W_OFFSETS);
-      if (blockIdx.x == 0 && s.bad) record_bad_index(p.err, W_LENGTH);
-      if (kept) seqs[b] = s;
-      const int nb = blocks_of(p, s.n);
-      if (per > 1) nblk[b] = nb;
-      mine += nb;
-    }
-    // Offsets that do not ascend can give more blocks than T tokens have, which 32 bits need not hold: then there are none.
-    const unsigned most = static_cast<unsigned>(blocks_of(p, p.T)) + p.B;
-    unsigned sum;
-    int at = static_cast<int>(scan<NT>(min(static_cast<unsigned>(mine), most + 1), reinterpret_cast<unsigned*>(plan_tmp), &sum));
-    const int blocks = sum > most ? 0 : static_cast<int>(sum);
-    if (per == 1) {
-      if (b0 < b1) nblk[b0] = at;
+    const auto report = [&](int b, const Seq& s) {
+      if (blockIdx.x > 0) return;
+      if (s.n == 0 && (p.cu[b] < 0 || p.cu[b] != p.cu[b + 1] || p.cu[b] > p.T)) record_bad_index(p.err, W_OFFSETS);
+      if (s.bad) record_bad_index(p.err, W_LENGTH);
+    };
+    if (CLUSTER && p.B <= 32) {  // one warp finds the unit, a lane a sequence
+      if (warp == C::LOAD_WARP) {
+        const Seq s = load_seq(p, lane);
+        if (lane < p.B) report(lane, s);
+        const int nb = blocks_of(p, s.n), x = blockIdx.z;
+        int upto = nb;
+#pragma unroll
+        for (int i = 1; i < 32; i *= 2) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, i);
+          if (lane >= i) upto += y;
+        }
+        const bool here = x < upto && x >= upto - nb;
+        const bool any = __any_sync(0xffffffffu, here);
+        if (here) {
+          plan_start[0] = blockIdx.y;
+          plan_start[1] = x - (upto - nb);
+          plan_start[5] = lane;
+          *plan_seq = s;
+        }
+        if (lane == 0) {
+          plan_start[2] = any;
+          units[0].ntok = 0;
+        }
+      }
     } else {
+      // Where the tiles will lie: blocks before each sequence, then the sequences, if they fit.
+      int* const nblk = reinterpret_cast<int*>(smem);
+      Seq* const seqs = reinterpret_cast<Seq*>(smem + (4 * p.B + 4 + 15) / 16 * 16);
+      const bool kept = p.B <= C::OFF_BAR / 20 - 2;
+      const auto seq_at = [&](int b) { return kept && b < p.B ? seqs[b] : load_seq(p, b); };
+      const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+      int mine = 0;
       for (int b = b0; b < b1; ++b) {
-        const int nb = nblk[b];
-        nblk[b] = at;
-        at += nb;
+        const Seq s = load_seq(p, b);
+        report(b, s);
+        if (kept) seqs[b] = s;
+        const int nb = blocks_of(p, s.n);
+        if (per > 1) nblk[b] = nb;
+        mine += nb;
       }
-    }
-    if (tid == 0) nblk[p.B] = blocks;
-    __syncthreads();
-    if constexpr (CLUSTER) {
-      if (tid == 0) {
-        const int x = blockIdx.z, b = x < blocks ? seq_of_block(nblk, p.B, x) : 0;
-        plan_start[0] = blockIdx.y;
-        plan_start[1] = x - nblk[b];
-        plan_start[2] = x < blocks;
-        plan_start[5] = b;
-        units[0].ntok = 0;
-      }
-    } else {
-      // A thread's blocks x0 .. x1 - 1 (of each key/value head), their tiles, and the tiles before them
-      const int pb = (blocks + NT - 1) / NT, x0 = min(blocks, tid * pb), x1 = min(blocks, x0 + pb);
-      int all_tiles, tiles = 0;  // of a key/value head: fewer than 2^31 (fa_fwd_paged's limit)
-      if (x0 < x1) {
-        int b = seq_of_block(nblk, p.B, x0);
-        Seq s = seq_at(b);
-        for (int x = x0; x < x1; ++x) {
-          while (x >= nblk[b + 1]) s = seq_at(++b);
-          tiles += block_tiles<BC>(p, s, x - nblk[b]);
+      // Offsets that do not ascend can give more blocks than T tokens have, which 32 bits need not hold: then there are none.
+      const unsigned most = static_cast<unsigned>(blocks_of(p, p.T)) + p.B;
+      unsigned sum;
+      int at = static_cast<int>(scan<NT>(min(static_cast<unsigned>(mine), most + 1), reinterpret_cast<unsigned*>(plan_tmp), &sum));
+      const int blocks = sum > most ? 0 : static_cast<int>(sum);
+      if (per == 1) {
+        if (b0 < b1) nblk[b0] = at;
+      } else {
+        for (int b = b0; b < b1; ++b) {
+          const int nb = nblk[b];
+          nblk[b] = at;
+          at += nb;
         }
       }
-      const int before = scan<NT>(tiles, plan_tmp, &all_tiles);
-      // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
-      // each takes one, and starts and ends do not count.
-      const int extra = static_cast<long long>(all_tiles) * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
-      long long* const place = plan_place;  // of each thread's first block in its head
-      place[tid] = before + static_cast<long long>(extra) * x0;
-      const long long head = all_tiles + static_cast<long long>(extra) * blocks, total = head * p.Hkv;
-      const int ranges = static_cast<int>(min(static_cast<long long>(min(static_cast<int>(gridDim.x), NT - 1)), total));
+      if (tid == 0) nblk[p.B] = blocks;
       __syncthreads();
-      // Thread i looks up where ranges i and i + 1 begin: the unit that their first place lies in (or, with several blocks a
-      // thread, the first one of that thread's).  Where a thread has one block at most, it also knows how long range i is if it
-      // takes the units that begin in it, whole.
-      long long from[2] = {0, 0}, w[2] = {0, 0}, next[2] = {0, 0};
-      int h[2] = {0, 0}, at_block[2] = {0, 0};
-      const bool mine_too = tid < ranges;
-      if (mine_too) {
-        long long in_head[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          w[k] = range_begin(total, tid + k, ranges);
-          h[k] = static_cast<int>(static_cast<unsigned>(tid + k) * p.Hkv / ranges);  // w[k] / head: total is Hkv heads
-          in_head[k] = w[k] - h[k] * head;
+      if constexpr (CLUSTER) {
+        if (tid == 0) {
+          const int x = blockIdx.z, b = x < blocks ? seq_of_block(nblk, p.B, x) : 0;
+          plan_start[0] = blockIdx.y;
+          plan_start[1] = x - nblk[b];
+          plan_start[2] = x < blocks;
+          plan_start[5] = b;
+          *plan_seq = seq_at(b);
+          units[0].ntok = 0;
         }
-        const int n = pb > 1 ? (blocks + pb - 1) / pb : blocks;
-        int lo[2] = {0, 0};
-        for (int step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; step > 0; step >>= 1) {  // last_below, both side by side
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (lo[k] + step < n && place[lo[k] + step] <= in_head[k]) lo[k] += step;
+      } else {
+        // A thread's blocks x0 .. x1 - 1 (of each key/value head), their tiles, and the tiles before them
+        const int pb = (blocks + NT - 1) / NT, x0 = min(blocks, tid * pb), x1 = min(blocks, x0 + pb);
+        int all_tiles, tiles = 0;  // of a key/value head: fewer than 2^31 (fa_fwd_paged's limit)
+        if (x0 < x1) {
+          int b = seq_of_block(nblk, p.B, x0);
+          Seq s = seq_at(b);
+          for (int x = x0; x < x1; ++x) {
+            while (x >= nblk[b + 1]) s = seq_at(++b);
+            tiles += block_tiles<BC>(p, s, x - nblk[b]);
+          }
         }
+        const int before = scan<NT>(tiles, plan_tmp, &all_tiles);
+        // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
+        // each takes one, and starts and ends do not count.
+        const int extra = static_cast<long long>(all_tiles) * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : C::COST_UNIT;
+        long long* const place = plan_place;  // of each thread's first block in its head
+        place[tid] = before + static_cast<long long>(extra) * x0;
+        const long long head = all_tiles + static_cast<long long>(extra) * blocks, total = head * p.Hkv;
+        const int ranges = static_cast<int>(min(static_cast<long long>(min(static_cast<int>(gridDim.x), NT - 1)), total));
+        __syncthreads();
+        // Thread i looks up where ranges i and i + 1 begin: the unit that their first place lies in (or, with several blocks a
+        // thread, the first one of that thread's).  Where a thread has one block at most, it also knows how long range i is if it
+        // takes the units that begin in it, whole.
+        long long from[2] = {0, 0}, w[2] = {0, 0}, next[2] = {0, 0};
+        int h[2] = {0, 0}, at_block[2] = {0, 0};
+        const bool mine_too = tid < ranges;
+        if (mine_too) {
+          long long in_head[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          from[k] = h[k] * head + place[lo[k]];
-          next[k] = lo[k] + 1 < n ? h[k] * head + place[lo[k] + 1] : (h[k] + 1LL) * head;
-          at_block[k] = lo[k] * max(pb, 1);
+          for (int k = 0; k < 2; ++k) {
+            w[k] = range_begin(total, tid + k, ranges);
+            h[k] = static_cast<int>(static_cast<unsigned>(tid + k) * p.Hkv / ranges);  // w[k] / head: total is Hkv heads
+            in_head[k] = w[k] - h[k] * head;
+          }
+          const int n = pb > 1 ? (blocks + pb - 1) / pb : blocks;
+          int lo[2] = {0, 0};
+          for (int step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; step > 0; step >>= 1) {  // last_below, both side by side
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (lo[k] + step < n && place[lo[k] + step] <= in_head[k]) lo[k] += step;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            from[k] = h[k] * head + place[lo[k]];
+            next[k] = lo[k] + 1 < n ? h[k] * head + place[lo[k] + 1] : (h[k] + 1LL) * head;
+            at_block[k] = lo[k] * max(pb, 1);
+          }
+        }
+        // the first unit that begins in a range or behind it
+        const long long length = (w[1] == total ? total : w[1] == from[1] ? w[1] : next[1]) - (w[0] == from[0] ? w[0] : next[0]);
+        const bool whole = __syncthreads_and(!mine_too || (pb <= 1 && length <= divide(total, ranges) + COST_CUT));
+        if (tid == static_cast<int>(blockIdx.x) && mine_too) {
+          const int b = seq_of_block(nblk, p.B, at_block[0]);
+          plan_start[0] = h[0];
+          plan_start[1] = at_block[0] - nblk[b];
+          plan_start[5] = b;
+          plan_at[0] = from[0];
+          plan_at[1] = total;
+          plan_at[2] = w[0];
+          plan_at[3] = w[1];
+        }
+        if (tid == 0) {
+          plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
+          plan_start[3] = extra;
+          plan_start[4] = whole;
+          p.shared[blockIdx.x].parts = 0;
         }
       }
-      // the first unit that begins in a range or behind it
-      const long long length = (w[1] == total ? total : w[1] == from[1] ? w[1] : next[1]) - (w[0] == from[0] ? w[0] : next[0]);
-      const bool whole = __syncthreads_and(!mine_too || (pb <= 1 && length <= divide(total, ranges) + COST_CUT));
-      if (tid == static_cast<int>(blockIdx.x) && mine_too) {
-        const int b = seq_of_block(nblk, p.B, at_block[0]);
-        plan_start[0] = h[0];
-        plan_start[1] = at_block[0] - nblk[b];
-        plan_start[5] = b;
-        plan_at[0] = from[0];
-        plan_at[1] = total;
-        plan_at[2] = w[0];
-        plan_at[3] = w[1];
-      }
-      if (tid == 0) {
-        plan_start[2] = static_cast<int>(blockIdx.x) < ranges ? ranges : 0;
-        plan_start[3] = extra;
-        plan_start[4] = whole;
-        p.shared[blockIdx.x].parts = 0;
-      }
+      __syncthreads();
     }
-    __syncthreads();
     if (p.G * p.tile_tokens < C::BR) {  // rows of Q that no copy reaches (a tile holds whole tokens) are zeros
       for (int i = tid; i < 2 * C::Q_BYTES / 16; i += NT)
         *reinterpret_cast<uint4*>(smem + C::OFF_Q + i * 16) = make_uint4(0, 0, 0, 0);
@@ -581,7 +613,7 @@ __global__ void __maxnreg__(C::MAXREG)
         u.kind = UNIT_NONE;
         if constexpr (CLUSTER) {
           if (iu == 0) {
-            const Seq s = load_seq(p, b);
+            const Seq s = *plan_seq;
             const int first = blk * p.tile_tokens;
             u.h = h;
             u.b = b;
@@ -1355,12 +1387,12 @@ int box_rows_of(int page_size, int bc) {
 // table, or the window, allows; n_cta: CTAs that may run at once.  As many as there is room for, less the places that clusters
 // of this size leave free in each of the GPU's 8 processor clusters.
 //
-// A cluster saves the dealing, the states in memory and the join, 3 to 6 us, but its CTAs work on no other unit.  So it is taken
+// A cluster saves the dealing, the states in memory and the join, 3 to 7 us, but its CTAs work on no other unit.  So it is taken
 // where its CTAs' tiles are at most C::CLUSTER_TILES more than an even share: that of one longest sequence alone, or of
-// sequences half as long.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 10.0,
-// d = 64 12.5 and 10.1; behind 4000 15.8 and 14.7, 16.2 and 12.5; behind 16000 21.0 and 25.2, 20.8 and 23.5; 16 x 4 tokens behind
-// 1000 21.1 and 17.2, 21.0 and 15.5; behind 1 to 1000 20.9 and 17.3, 17.8 and 14.6; behind 1 to 4000 39 and 46, 29 and 36; a prompt
-// of 500 17.8 and 12.7, 17.8 and 12.9.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
+// sequences half as long.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 9.7,
+// d = 64 12.5 and 9.2; behind 4000 15.8 and 14.1, 16.2 and 11.6; behind 16000 21.0 and 25, 20.8 and 23; 16 x 4 tokens behind 1000
+// 21.1 and 16.8, 21.0 and 14.7; behind 1 to 1000 20.9 and 16.8, 17.8 and 13.8; behind 1 to 4000 39 and 46, 29 and 36; a prompt of
+// 500 17.8 and 12.5, 17.8 and 12.7.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
 int cluster_size(long long units, long long tiles, int Hkv, int n_cta, int more) {
   int cl = 1;
   while (cl < MAX_CLUSTER && cl < tiles && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
