@@ -86,6 +86,14 @@ def test_one_sequence_by_clusters_of_each_size(cuda_device, d):
             b.check(*b.run(), f"{keys} keys, {Hkv} heads")
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 90])
+def test_more_sequences_by_clusters(cuda_device, B):
+    # a warp, or the block, finds the unit; some sequences have no new tokens
+    for d in (64, 128):
+        b = Batch(cuda_device, 4, 1, d, 16, [((37 * i) % 300, (0, 1, 3, 2)[i % 4]) for i in range(B)])
+        b.check(*b.run(), f"{B} sequences d{d}")
+
+
 def test_both_forms_agree(cuda_device):
     # the same call with more places for tokens: another form, the same result but for the order of its sums
     for d in (64, 128):
