@@ -69,7 +69,7 @@ struct ChunkCfg {
   // tile or two (a step of one is bound by its chain of products and exponentials, or by the tile's bytes).  A prompt of 8191
   // tokens, d = 128, with 2, 3, 4: 371, 357, 362 us; a mixed batch, d = 64: 88, 83, 79.
   static constexpr int COST_UNIT = D == 128 ? 3 : 4;
-  static constexpr int CLUSTER_TILES = D == 128 ? 6 : 8;  // cluster_size
+  static constexpr int CLUSTER_TILES = D == 128 ? 6 : 8, CLUSTER_HALVES = D == 128 ? 4 : 5;  // cluster_size
   static constexpr int UNITS = 4;                // units announced at a time
   static constexpr int NBAR = 4 * STAGES + 2 * UNITS + 12;
   static constexpr int OFF_UNITS = OFF_BAR + NBAR * 8;
@@ -1393,11 +1393,16 @@ int box_rows_of(int page_size, int bc) {
 // d = 64 12.5 and 9.2; behind 4000 15.8 and 14.1, 16.2 and 11.6; behind 16000 21.0 and 25, 20.8 and 23; 16 x 4 tokens behind 1000
 // 21.1 and 16.8, 21.0 and 14.7; behind 1 to 1000 20.9 and 16.8, 17.8 and 13.8; behind 1 to 4000 39 and 46, 29 and 36; a prompt of
 // 500 17.8 and 12.5, 17.8 and 12.7.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
-int cluster_size(long long units, long long tiles, int Hkv, int n_cta, int more) {
+//
+// More units than CTAs may run at once, if short, come in waves, of a CTA each, as many as `halves` of what may run: 32 single
+// tokens behind 200, d = 128, 20.1 and 18.1, 12 x 100 tokens of 8 heads behind 200 17.5 and 12.8, 55 x 3 behind 100 (440 units)
+// 20.9 and 23.1; d = 64 60 x 18 behind 200 (600 units) 22.5 and 20.9, 128 single tokens behind 300 (1024) 38.4 and 40.8.
+int cluster_size(long long units, long long tiles, int Hkv, int n_cta, int more, int halves) {
   int cl = 1;
   while (cl < MAX_CLUSTER && cl < tiles && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
   const long long share = std::max(tiles * Hkv, units * tiles / 2) / n_cta;
-  return units * cl <= n_cta && (tiles + cl - 1) / cl <= share + more ? cl : 0;
+  if (units > n_cta) return 2 * units <= halves * n_cta && tiles <= more ? 1 : 0;
+  return (tiles + cl - 1) / cl <= share + more ? cl : 0;
 }
 
 template <class C>
@@ -1437,7 +1442,7 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a) {
     tiles = seen < tiles ? seen : tiles;
   }
   const long long units = (static_cast<long long>(a.T) / p.tile_tokens + (a.B < a.T ? a.B : a.T)) * a.Hkv;
-  p.cl = cluster_size(units, tiles, a.Hkv, n_cta, C::CLUSTER_TILES);
+  p.cl = cluster_size(units, tiles, a.Hkv, n_cta, C::CLUSTER_TILES, C::CLUSTER_HALVES);
   p.by_block = FastDiv(static_cast<unsigned>(p.cl > 0 ? p.tile_tokens : 2 * p.tile_tokens));
   p.part_rows = l.rows;
   p.part_tiles = l.tiles;
