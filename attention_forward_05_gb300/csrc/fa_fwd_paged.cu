@@ -22,7 +22,7 @@
 // ranges of whole units are hardly longer, no unit is cut (256 units of 19 tiles, d = 64: 34 us, cut into 304 ranges 44).
 //
 // Small calls are not dealt (CLUSTER, cluster_size): where the units, then of one row tile, are few and short enough, each has a
-// cluster of 1 to 16 CTAs with even shares of its tiles, and the cluster joins its states through its shared memory.
+// cluster of 1 to 16 CTAs, two an SM, with even shares of its tiles, and the cluster joins its states through its shared memory.
 //
 // No atomics on results: they depend on the lengths, the arguments and the SM count alone.
 //
@@ -36,7 +36,7 @@
 // TFLOP/s of the formula's products (the dense causal forward takes about the same).  At d = 64 the exponentials' latency, as in
 // the dense forward: 37 sequences of up to 512 tokens over up to 8192 keys, 32 heads on 4, 78 us, 700 TFLOP/s with start,
 // ends and masked tiles.  Few tokens over long contexts device memory: 24 sequences of 3 to 7 tokens, 1.41 GB, 220 us, 6.4 TB/s.
-// Small calls latency: 23 tokens behind 1000 keys 9.7 us (dealt 13.2: 3 for the plan, 3 to the first scores, 3 to
+// Small calls latency: 23 tokens behind 1000 keys 9.2 us (dealt 13.2: 3 for the plan, 3 to the first scores, 3 to
 // the states, 4 for the join).
 #include <cuda_bf16.h>
 
@@ -1390,34 +1390,48 @@ int box_rows_of(int page_size, int bc) {
   return r > bc ? bc : r;
 }
 
-// CTAs of a unit where every unit has a cluster, or 0 for ranges.  `units`: at most; `tiles`: of the longest one that its
-// table, or the window, allows; n_cta: CTAs that may run at once.  As many as there is room for, less the places that clusters
-// of this size leave free in each of the GPU's 8 processor clusters.
-//
-// A cluster saves the dealing, the states in memory and the join, 3 to 7 us, but its CTAs work on no other unit.  So it is taken
-// where its CTAs' tiles are at most `more` more than an even share: that of one longest sequence alone, or of
-// sequences half as long.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 9.7,
-// d = 64 12.5 and 9.2; behind 4000 15.8 and 14.1, 16.2 and 11.6; behind 16000 21.0 and 25, 20.8 and 23; 16 x 4 tokens behind 1000
-// 21.1 and 16.8, 21.0 and 14.7; behind 1 to 1000 20.9 and 16.8, 17.8 and 13.8; behind 1 to 4000 39 and 46, 29 and 36; a prompt of
-// 500 17.8 and 12.5, 17.8 and 12.7.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 21.5 with 8 CTAs, 16.2 with 16.
-//
-// More units than CTAs may run at once, if short, come in waves, of a CTA each, as many as `halves` of what may run: 32 single
-// tokens behind 200, d = 128, 20.1 and 18.1, 12 x 100 tokens of 8 heads behind 200 17.5 and 12.8, 55 x 3 behind 100 (440 units)
-// 20.9 and 23.1; d = 64 60 x 18 behind 200 (600 units) 22.5 and 20.9, 128 single tokens behind 300 (1024) 38.4 and 40.8.
-int cluster_size(long long units, long long tiles, int Hkv, int n_cta) {
-  constexpr int more = 8, halves = 5;
-  int cl = 1;
-  if (tiles > 2)  // two steps take less than one and the join
-    while (cl < MAX_CLUSTER && cl < tiles && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
-  const long long share = std::max(tiles * Hkv, units * tiles / 2) / n_cta;
-  if (units > n_cta) return 2 * units <= halves * n_cta && tiles <= more ? 1 : 0;
-  return (tiles + cl - 1) / cl <= share + more ? cl : 0;
-}
-
 // As many units as a call of its sizes can have.
 template <class C>
 long long units_of(const FwdPagedLaunch& a) {
   return (static_cast<long long>(a.T) / (C::BR / (a.H / a.Hkv)) + (a.B < a.T ? a.B : a.T)) * a.Hkv;
+}
+
+// Rows of a unit, if the sequences have as many tokens each.
+template <class C>
+int rows_of(const FwdPagedLaunch& a) {
+  const int G = a.H / a.Hkv;
+  return std::min<long long>(C::BR / G, (static_cast<long long>(a.T) + a.B - 1) / a.B) * G;
+}
+
+// CTAs of a unit where every unit has a cluster, or 0 for ranges.  `tiles`: of the longest one that its table, or the window,
+// allows; n_cta: CTAs that may run at once.  As many as there is room for, less the places that clusters of this size leave free
+// in each of the GPU's 8 processor clusters; one for two tiles, which take less than one and the join.
+//
+// A cluster saves the dealing, the states in memory and the join, 3 to 7 us, and two CTAs on an SM work on units of few rows at the
+// same time, where one range has them one behind the other; but its CTAs work on no other unit.  So it is taken where its CTAs'
+// tiles are at most `more` more than an even share: that of one longest sequence alone, or of sequences half as long, or of one's
+// units, three quarters.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 9.2,
+// d = 64 12.5 and 8.4; behind 4000 15.8 and 13.7, 16.2 and 11.1; behind 16000 20.9 and 25.5, 20.5 and 21.1; 16 x 4 tokens behind 1000
+// 21.1 and 15.8, 21.0 and 13.9; behind 1 to 2000 27.2 and 23.0, 21.9 and 19.8; behind 1 to 4000 39 and 46, 29 and 36; a prompt of
+// 500 17.8 and 12.0, 17.8 and 12.5.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 17.7 with 8 CTAs, 14.2 with 16.
+//
+// More units than CTAs may run at once, if short, come in waves, of a CTA each, up to `halves` halves of what may run: 128 single
+// tokens behind 300 (3.5 waves) 59.6 and 48.1, 37.2 and 38.4; 256 behind 100 (7) 70.7 and 60.9, 40.5 and 49.8; 60 x 18 tokens
+// behind 200 (2.4) 31.7 and 21.1, 22.5 and 19.5; 64 x 100 behind 100 (7) 63 and 77, 45 and 67.
+template <class C>
+int cluster_size(const FwdPagedLaunch& a, long long tiles) {
+  const long long units = units_of<C>(a), n_cta = a.sms * C::MINB;
+  const bool few = rows_of<C>(a) <= 64;
+  if (units > n_cta) {
+    const int halves = !few ? 5 : C::D == 128 ? 16 : 7, most = few && C::D == 128 ? 16 : 8;
+    return 2 * units <= halves * n_cta && tiles <= most ? 1 : 0;
+  }
+  int cl = 1;
+  if (tiles > 2)
+    while (cl < MAX_CLUSTER && cl < tiles && units * (cl + 1) <= n_cta - 8 * cl) ++cl;
+  const long long share = std::max(tiles * a.Hkv, units * tiles * (a.B == 1 ? 3 : 2) / 4) / n_cta;
+  const int more = few ? 12 : 8;
+  return (tiles + cl - 1) / cl <= share + more ? cl : 0;
 }
 
 // p.cl by the keys' tiles of C, 0 for ranges, and about how long the call takes after its start, in tenths of a microsecond.
@@ -1427,18 +1441,16 @@ struct Form {
 };
 template <class C>
 Form form_of(const FwdPagedLaunch& a) {
-  const int G = a.H / a.Hkv, tokens = C::BR / G;
+  const int tokens = C::BR / (a.H / a.Hkv);
   long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + C::BC - 1) / C::BC;
   if (a.window > 0) {
     const long long seen = (static_cast<long long>(a.window) + tokens) / C::BC + 2 + a.sinks / C::BC + 1;
     tiles = seen < tiles ? seen : tiles;
   }
-  const long long units = units_of<C>(a);
-  const int cl = cluster_size(units, tiles, a.Hkv, a.sms * C::MINB);
+  const int cl = cluster_size<C>(a, tiles);
   if (cl == 0) return {0, 0};
   // Two CTAs on an SM take their steps at the same time only while their tiles have few rows.
-  const long long rows = static_cast<long long>(std::min(tokens, (a.T + a.B - 1) / a.B)) * G;
-  const int step = C::BC == 128 || (rows > 64 && units * cl > a.sms) ? 19 : 15;
+  const int step = C::BC == 128 || (rows_of<C>(a) > 64 && units_of<C>(a) * cl > a.sms) ? 19 : 15;
   return {cl, (tiles + cl - 1) / cl * step + (cl == 1 ? 0 : cl <= 8 ? 20 : 27)};
 }
 
@@ -1508,16 +1520,14 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a, int cl) {
 }
 
 // At d = 128 a cluster's CTAs have key tiles of 64, or, where units of many rows are few, one CTA an SM with tiles of 128 (a
-// prompt of 500, 32 heads on 8: 12.5 us instead of 15.8, 23 tokens behind 1000 9.7 instead of 10.5; 4 x 4 tokens behind 1000 10.9
+// prompt of 500, 32 heads on 8: 12.0 us instead of 15.8, 23 tokens behind 1000 9.2 instead of 10.5; 4 x 4 tokens behind 1000 10.9
 // instead of 10.1, 32 single tokens behind 200 18.1 instead of 10.5).
 template <int D, bool GATHER>
 cudaError_t launch_form(const FwdPagedLaunch& a) {
   const Form f = form_of<Cluster<D, GATHER>>(a);
   if constexpr (D == 128) {
     const Form g = form_of<Cluster<D, GATHER, 128>>(a);
-    const int G = a.H / a.Hkv;
-    const long long rows = static_cast<long long>(std::min(128 / G, (a.T + a.B - 1) / a.B)) * G;
-    if (f.cl > 0 && g.cl > 0 && rows > 64 && units_of<Cluster<D, GATHER>>(a) <= a.sms && g.cost <= f.cost)
+    if (f.cl > 0 && g.cl > 0 && rows_of<Cluster<D, GATHER>>(a) > 64 && units_of<Cluster<D, GATHER>>(a) <= a.sms && g.cost <= f.cost)
       return launch_cfg<Cluster<D, GATHER, 128>>(a, g.cl);
   }
   return f.cl > 0 ? launch_cfg<Cluster<D, GATHER>>(a, f.cl) : launch_cfg<Ranges<D, GATHER>>(a, 0);

@@ -61,7 +61,7 @@ def test_chunks(cuda_device, H, Hkv, d, ps, chunks):
 
 def many_places(H, Hkv):
     """Places of q behind the last token with which a call may have more units than are given CTAs of their own."""
-    return 800 * (128 // (H // Hkv)) // Hkv + 1
+    return 2600 * (128 // (H // Hkv)) // Hkv + 1
 
 
 CHUNKS_BY_RANGES = [
