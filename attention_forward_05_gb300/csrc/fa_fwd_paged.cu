@@ -1412,8 +1412,9 @@ int rows_of(const FwdPagedLaunch& a) {
 // tiles are at most `more` more than an even share: that of one longest sequence alone, or of sequences half as long, or of one's
 // units, three quarters.  Ranges and clusters, device time, 32 heads on 8, us: 23 tokens behind 1000 keys d = 128 13.2 and 9.2,
 // d = 64 12.5 and 8.4; behind 4000 15.8 and 13.7, 16.2 and 11.1; behind 16000 20.9 and 25.5, 20.5 and 21.1; 16 x 4 tokens behind
-// 1000 21.1 and 15.8, 21.0 and 13.9; behind 1 to 2000 27.2 and 23.0, 21.9 and 19.8; behind 1 to 4000 39 and 46, 29 and 36; a prompt of
-// 500 17.8 and 12.0, 17.8 and 12.5.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 17.7 with 8 CTAs, 14.2 with 16.
+// 1000 21.1 and 15.8, 21.0 and 13.9; behind 1 to 2000 27.2 and 23.0, 21.9 and 19.8; behind 1 to 4000 39 and 46, 29 and 36; a
+// prompt of 500 17.8 and 12.0, 17.8 and 12.5.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 17.7 with 8 CTAs, 14.2
+// with 16.
 //
 // More units than CTAs may run at once, if short, come in waves, of a CTA each, up to `halves` halves of what may run: 128 single
 // tokens behind 300 (3.5 waves) 59.6 and 48.1, 37.2 and 38.4; 256 behind 100 (7) 70.7 and 60.9, 40.5 and 49.8; 60 x 18 tokens

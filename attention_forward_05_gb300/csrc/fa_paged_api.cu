@@ -345,7 +345,8 @@ int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* 
   if (!std::isfinite(c2)) return FA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || H / Hkv > fa::FWD_PAGED_MAX_G || B > fa::FWD_PAGED_MAX_B) return FA_ERR_UNSUPPORTED;
   // a key/value head's blocks of at least 128 rows and their tiles are counted in 32 bits, all heads' in 62
-  if ((static_cast<long long>(T) * (H / Hkv) / 128 + B + 1) * (static_cast<long long>(max_pages) * page_size / 64 + 3) > 0x7FFFFFFFLL)
+  if ((static_cast<long long>(T) * (H / Hkv) / 128 + B + 1) * (static_cast<long long>(max_pages) * page_size / 64 + 3) >
+      0x7FFFFFFFLL)
     return FA_ERR_INVALID_ARG;
   if (H > (1 << 20) || static_cast<long long>(T) * H > (1LL << 36) ||
       static_cast<long long>(T) * (H / Hkv) > (1LL << 30))
