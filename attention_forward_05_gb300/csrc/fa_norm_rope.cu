@@ -185,24 +185,32 @@ __device__ __forceinline__ Head16 read16(const uint4* src) {
   return unpack<INTER>(x);
 }
 
-// The weights times a token's turn: y1 = x1 a - x2 b, y2 = x1 c + x2 d (b with its sign), the same for all of its heads.
+// The weights times a token's turn: y1 = x1 a - x2 b, y2 = x1 c + x2 d (b with its sign), the same for all of its heads.  Elements
+// that are not rotated take their weight alone (a, d): with products of zero beside it an infinite element, NaN once it is normed,
+// would reach another one.
 struct Fold {
   uint64_t a[4], b[4], c[4], d[4];
-  __device__ __forceinline__ Fold(const Head16& w, const Turn& t, bool rotated) {
+  bool rotated;
+  __device__ __forceinline__ Fold(const Head16& w, const Turn& t, bool rotated) : rotated(rotated) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       a[j] = rotated ? f2_mul(w.x1[j], t.c[j]) : w.x1[j];
-      b[j] = rotated ? f2_mul(w.x2[j], t.n[j]) : 0ull;
-      c[j] = rotated ? f2_mul(w.x1[j], t.s[j]) : 0ull;
+      b[j] = f2_mul(w.x2[j], t.n[j]);
+      c[j] = f2_mul(w.x1[j], t.s[j]);
       d[j] = rotated ? f2_mul(w.x2[j], t.c[j]) : w.x2[j];
     }
   }
   __device__ __forceinline__ void apply(Head16& x) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint64_t y = f2_fma(x.x1[j], a[j], f2_mul(x.x2[j], b[j]));
-      x.x2[j] = f2_fma(x.x1[j], c[j], f2_mul(x.x2[j], d[j]));
-      x.x1[j] = y;
+      if (rotated) {
+        const uint64_t y = f2_fma(x.x1[j], a[j], f2_mul(x.x2[j], b[j]));
+        x.x2[j] = f2_fma(x.x1[j], c[j], f2_mul(x.x2[j], d[j]));
+        x.x1[j] = y;
+      } else {
+        x.x1[j] = f2_mul(x.x1[j], a[j]);
+        x.x2[j] = f2_mul(x.x2[j], d[j]);
+      }
     }
   }
 };
