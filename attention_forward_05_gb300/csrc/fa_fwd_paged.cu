@@ -24,7 +24,7 @@
 // Small calls are not dealt (CLUSTER, cluster_size): where the units, then of one row tile, are few and short enough, each has a
 // cluster of 1 to 16 CTAs, two an SM, with even shares of its tiles, and the cluster joins its states through its shared memory.
 //
-// No atomics on results: they depend on the lengths, the arguments and the SM count alone.
+// No atomics on results: a token's depend on its sequence's queries and keys, the lengths, the call's sizes and the SM count alone.
 //
 // Keys and values come out of the pages by TMA boxes of as many rows as divide the page size (8 at least: a swizzle
 // period), or, where no such box exists, by 16-byte asynchronous copies.  Keys that no row of the block sees are not read
@@ -1023,7 +1023,13 @@ __global__ void __maxnreg__(C::MAXREG)
       // What the steps below do not need is read again where it is used: they have no registers to spare.
       const int pos = uv.pos0 + min(t * p.tile_tokens + my_tok, uv.ntok - 1);
       const int steps = steps_of<BC>(uv, t, p.tile_tokens);
-      float m_ref = -INFINITY, l = 0.f;
+      // Rows that are not the unit's hold other sequences' queries, or whatever lies in unused places.  In a warp with rows of the
+      // unit their reference maximum is infinity: their P are zeros or NaN, and they hold up none of the votes below, which NaN
+      // passes.  (A warp without rows of the unit votes for itself; with infinity there too it takes the fast path on a unit's
+      // first tile beside the others' general one: 256 single tokens behind 100 keys, d = 128, 65 us instead of 62.)
+      const bool mine = my_tok < p.tile_tokens && t * p.tile_tokens + my_tok < uv.ntok;
+      const bool any_mine = __any_sync(0xffffffffu, mine);
+      float m_ref = mine || !any_mine ? -INFINITY : INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++done) {
         const bool okw = __all_sync(0xffffffffu, mbar_wait(bar_sf(t), done & 1, abort_flag, p.err, W_SF));
         if (!okw) {
@@ -1041,6 +1047,7 @@ __global__ void __maxnreg__(C::MAXREG)
         // Once every row of the warp has a reference maximum and sees all columns, P is computed against it with no row maximum
         // in front of it; row sums of at most 2^tau (and at d = 128 the second half's maximum) show that no score moved past
         // m_ref + tau.  Otherwise nothing has been stored yet, and the general path reads S again (fa_fwd_kernel.cuh, `fast`, PV2).
+        // (A row with NaN among its scores is NaN by either path.)
         // (A masked copy of it costs more in registers and code than it saves: 375 us on a prompt of 8191 tokens, d = 128, without
         // it 371; a mixed batch, d = 64, 89 and 86.)
         const auto fast = [&]() -> bool {
@@ -1063,7 +1070,7 @@ __global__ void __maxnreg__(C::MAXREG)
             f2_unpack_f(rs[0], r0, r1);
             f2_unpack_f(rs[1], r2, r3);
             const float l_a = (r0 + r1) + (r2 + r3);
-            if (!__all_sync(0xffffffffu, l_a <= p.p_lim && m_b <= m_ref + p.tau)) return false;
+            if (__any_sync(0xffffffffu, l_a > p.p_lim || m_b > m_ref + p.tau)) return false;
 #pragma unroll
             for (int i = 0; i < HP; ++i) tmem_st32(tS + i * 32, pk[i]);
             hand_over(bar_ph(t));
@@ -1101,7 +1108,7 @@ __global__ void __maxnreg__(C::MAXREG)
             f2_unpack_f(rs[0], r0, r1);
             f2_unpack_f(rs[1], r2, r3);
             const float l_tile = (r0 + r1) + (r2 + r3);
-            if (!__all_sync(0xffffffffu, l_tile <= p.p_lim)) return false;
+            if (__any_sync(0xffffffffu, l_tile > p.p_lim)) return false;
             tmem_st32(tS, pk);
             hand_over(bar_pf(t));
             l += l_tile;
