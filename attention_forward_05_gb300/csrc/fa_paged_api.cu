@@ -3,6 +3,7 @@
 // code: argument validation, workspaces, launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -354,8 +355,8 @@ int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* 
   long long qs[2], c[3];
   qs[0] = q_strides ? q_strides[0] : static_cast<long long>(H) * d;
   qs[1] = q_strides ? q_strides[1] : d;
-  if (T <= 1) qs[0] = static_cast<long long>(H) * d;  // never stepped over
-  if (H == 1) qs[1] = d;
+  if (H == 1) qs[1] = d;  // never stepped over
+  if (T <= 1) qs[0] = std::max(qs[1], static_cast<long long>(H) * d);
   if (!good_strides(qs, 2, 8) || qs[1] < d || qs[0] < qs[1]) return FA_ERR_INVALID_ARG;
   c[0] = cache_strides ? cache_strides[0] : static_cast<long long>(Hkv) * page_size * d;
   c[1] = cache_strides ? cache_strides[1] : static_cast<long long>(page_size) * d;
