@@ -1500,7 +1500,7 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a, int cl) {
   p.max_pages = a.max_pages;
   p.box_rows = box_rows_of(a.page_size, C::BC);
   p.heads_inner = a.c_row > a.c_head;
-  p.window = a.window;
+  p.window = std::min(a.window, 1 << 30);  // no more keys than that: `pos - window + 1 - key` stays in 32 bits
   p.sinks = a.window > 0 ? a.sinks : 0;
   p.c = a.c == 0.f ? 1e-30f : a.c;  // a hidden score (an infinity) times zero would be NaN
   p.tau = kTau;
