@@ -35,7 +35,7 @@ Entry points (same names as the C ABI):
       -> (cu_seqlens, positions, slots, seq_lens, free_left)
   fa_fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, scale=None, window=0, sinks=0,
                workspace=None, with_lse=False) -> (o, lse)
-  fa_fwd_paged_workspace_bytes(T, B, H, Hkv, d)
+  fa_fwd_paged_workspace_bytes(T, B, H, Hkv, d), fa_fwd_paged_call_bytes(T, B, H, Hkv, d, page_size, max_pages, window=0, sinks=0)
   fa_decode_paged(q, k_cache, v_cache, page_table, seq_lens, scale=None, workspace=None, with_lse=False)
       -> (o, lse)
   fa_decode_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None,
@@ -136,6 +136,8 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_paged.restype = i
             L.fa_fwd_paged_workspace_bytes.argtypes = [i, i, i, i, i]
             L.fa_fwd_paged_workspace_bytes.restype = sz
+            L.fa_fwd_paged_call_bytes.argtypes = [i] * 9
+            L.fa_fwd_paged_call_bytes.restype = sz
             L.fa_check_device_error.argtypes = []
             L.fa_check_device_error.restype = i
             L.fa_status_string.argtypes = [i]
@@ -605,6 +607,13 @@ def fa_paged_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_table: t
 
 def fa_fwd_paged_workspace_bytes(T: int, B: int, H: int, Hkv: int, d: int) -> int:
     return int(lib().fa_fwd_paged_workspace_bytes(int(T), int(B), int(H), int(Hkv), int(d)))
+
+
+def fa_fwd_paged_call_bytes(T: int, B: int, H: int, Hkv: int, d: int, page_size: int, max_pages: int, window: int = 0,
+                            sinks: int = 0) -> int:
+    """What a call with tables of max_pages pages and this window uses of its workspace: all of it, or nothing."""
+    return int(lib().fa_fwd_paged_call_bytes(int(T), int(B), int(H), int(Hkv), int(d), int(page_size), int(max_pages),
+                                             int(window), int(sinks)))
 
 
 def fa_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,

@@ -724,7 +724,7 @@ PyObject* fwd_paged(PyObject*, PyObject* const* in, Py_ssize_t n_in) {
     size_t ws_bytes = ws ? ws->nbytes() : 0;
     const bool any = T > 0 && B > 0;
     if (!ws && any) {
-      ws_bytes = fa_fwd_paged_workspace_bytes(Ti, Bi, Hi, hk, di);
+      ws_bytes = fa_fwd_paged_call_bytes(Ti, Bi, Hi, hk, di, psi, mp, window, sinks);
       if (ws_bytes > 0) {  // 0: none needed, or arguments that the call below refuses
         own_ws = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
         ws_ptr = own_ws.get();

@@ -1480,9 +1480,11 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a, int cl) {
   p.lens = a.lens;
   p.table_stride = a.table_stride;
   p.err = a.err;
-  p.part_o = reinterpret_cast<float4*>(a.ws);
-  p.part_ml = reinterpret_cast<float2*>(a.ws + l.part_ml);
-  p.shared = reinterpret_cast<Shared*>(a.ws + l.shared);
+  if (!C::CLUSTER) {
+    p.part_o = reinterpret_cast<float4*>(a.ws);
+    p.part_ml = reinterpret_cast<float2*>(a.ws + l.part_ml);
+    p.shared = reinterpret_cast<Shared*>(a.ws + l.shared);
+  }
   p.G = a.H / a.Hkv;
   p.tile_tokens = C::BR / p.G;
   p.by_g = FastDiv(static_cast<unsigned>(p.G));
@@ -1529,26 +1531,37 @@ cudaError_t launch_cfg(const FwdPagedLaunch& a, int cl) {
 
 // At d = 128 a cluster's CTAs have key tiles of 64, or, where units of many rows are few, one CTA an SM with tiles of 128 (a
 // prompt of 500, 32 heads on 8: 12.0 us instead of 15.8, 23 tokens behind 1000 9.2 instead of 10.5; 4 x 4 tokens behind 1000 10.9
-// instead of 10.1, 32 single tokens behind 200 18.1 instead of 10.5).
-template <int D, bool GATHER>
-cudaError_t launch_form(const FwdPagedLaunch& a) {
-  const Form f = form_of<Cluster<D, GATHER>>(a);
+// instead of 10.1, 32 single tokens behind 200 18.1 instead of 10.5).  Copies of single rows change nothing here.
+template <int D>
+FwdPagedForm choose(const FwdPagedLaunch& a) {
+  using C = Cluster<D, false>;
+  const Form f = form_of<C>(a);
   if constexpr (D == 128) {
-    const Form g = form_of<Cluster<D, GATHER, 128>>(a);
-    if (f.cl > 0 && g.cl > 0 && rows_of<Cluster<D, GATHER>>(a) > 64 && units_of<Cluster<D, GATHER>>(a) <= a.sms && g.cost <= f.cost)
-      return launch_cfg<Cluster<D, GATHER, 128>>(a, g.cl);
+    const Form g = form_of<Cluster<D, false, 128>>(a);
+    if (f.cl > 0 && g.cl > 0 && rows_of<C>(a) > 64 && units_of<C>(a) <= a.sms && g.cost <= f.cost) return {g.cl, 1};
   }
-  return f.cl > 0 ? launch_cfg<Cluster<D, GATHER>>(a, f.cl) : launch_cfg<Ranges<D, GATHER>>(a, 0);
+  return {f.cl, 0};
+}
+
+template <int D, bool GATHER>
+cudaError_t launch_form(const FwdPagedLaunch& a, FwdPagedForm form) {
+  if (form.cl == 0) return launch_cfg<Ranges<D, GATHER>>(a, 0);
+  if constexpr (D == 128) {
+    if (form.wide) return launch_cfg<Cluster<D, GATHER, 128>>(a, form.cl);
+  }
+  return launch_cfg<Cluster<D, GATHER>>(a, form.cl);
 }
 
 }  // namespace
 
-size_t fwd_paged_workspace(int T, int, int H, int Hkv, int d, int sms) { return layout_of(T, H, Hkv, d, sms).total; }
+FwdPagedForm fwd_paged_form(const FwdPagedLaunch& a) { return a.d == 64 ? choose<64>(a) : choose<128>(a); }
 
-cudaError_t launch_fwd_paged(const FwdPagedLaunch& a) {
+size_t fwd_paged_workspace(int T, int H, int Hkv, int d, int sms) { return layout_of(T, H, Hkv, d, sms).total; }
+
+cudaError_t launch_fwd_paged(const FwdPagedLaunch& a, FwdPagedForm form) {
   const bool gather = a.page_size % 8 != 0;
-  if (a.d == 64) return gather ? launch_form<64, true>(a) : launch_form<64, false>(a);
-  return gather ? launch_form<128, true>(a) : launch_form<128, false>(a);
+  if (a.d == 64) return gather ? launch_form<64, true>(a, form) : launch_form<64, false>(a, form);
+  return gather ? launch_form<128, true>(a, form) : launch_form<128, false>(a, form);
 }
 
 }  // namespace fa

@@ -210,13 +210,19 @@ struct FwdPagedLaunch {
   long long table_stride;
   int window, sinks;        // window 0: every key up to the token's own
   float c;                  // scale * log2(e)
-  char* ws;                 // fwd_paged_workspace(...) bytes
+  char* ws;                 // fwd_paged_workspace(...) bytes where the call is dealt to ranges
   int* err;
   int sms;
   cudaStream_t stream;
 };
-size_t fwd_paged_workspace(int T, int B, int H, int Hkv, int d, int sms);
-cudaError_t launch_fwd_paged(const FwdPagedLaunch& a);
+// How a call is split, by its sizes (T to max_pages, window, sinks) and the SM count alone.
+struct FwdPagedForm {
+  int cl;    // CTAs of each unit's cluster; 0: dealt to ranges, which take the workspace
+  int wide;  // clusters with key tiles of 128 (d = 128)
+};
+FwdPagedForm fwd_paged_form(const FwdPagedLaunch& a);
+size_t fwd_paged_workspace(int T, int H, int Hkv, int d, int sms);
+cudaError_t launch_fwd_paged(const FwdPagedLaunch& a, FwdPagedForm form);
 
 struct PagedLaunch {
   const void* q;            // [B, H, d] bf16

@@ -318,6 +318,24 @@ int fa_paged_slots(const int* ctx_lens, const int* new_lens, int* page_table, lo
   return e == cudaSuccess ? FA_OK : fa::report_cuda_error(e);
 }
 
+size_t fa_fwd_paged_call_bytes(int T, int B, int H, int Hkv, int d, int page_size, int max_pages, int window, int sinks) {
+  if (page_size < 1 || max_pages < 1 || static_cast<long long>(max_pages) * page_size >= (1LL << 30) || window < 0 || sinks < 0)
+    return 0;
+  const size_t most = fa_fwd_paged_workspace_bytes(T, B, H, Hkv, d);
+  fa::FwdPagedLaunch a = {};
+  if (most == 0 || fa::current_device_info(&a.err, &a.sms) != FA_OK) return 0;
+  a.T = T;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.window = window;
+  a.sinks = sinks;
+  return fa::fwd_paged_form(a).cl == 0 ? most : 0;
+}
+
 size_t fa_fwd_paged_workspace_bytes(int T, int B, int H, int Hkv, int d) {
   if (T < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || H / Hkv > fa::FWD_PAGED_MAX_G || B > fa::FWD_PAGED_MAX_B ||
       (d != 64 && d != 128) || static_cast<long long>(T) * H > kMaxElems / d)
@@ -325,7 +343,7 @@ size_t fa_fwd_paged_workspace_bytes(int T, int B, int H, int Hkv, int d) {
   int* err = nullptr;
   int sms = 0;
   if (fa::current_device_info(&err, &sms) != FA_OK) return 0;
-  return fa::fwd_paged_workspace(T, B, H, Hkv, d, sms);
+  return fa::fwd_paged_workspace(T, H, Hkv, d, sms);
 }
 
 int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, const int* page_table,
@@ -366,15 +384,6 @@ int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* 
   const int rc = fa::current_device_info(&a.err, &a.sms);
   if (rc != FA_OK) return rc;
   if (T == 0 || B == 0) return FA_OK;  // a step without tokens
-  const size_t need = fa::fwd_paged_workspace(T, B, H, Hkv, d, a.sms);
-  if (workspace && workspace_bytes < need) return FA_ERR_INVALID_ARG;
-  a.stream = reinterpret_cast<cudaStream_t>(stream);
-  void* ws = workspace;
-  const bool own_ws = ws == nullptr && need > 0;
-  if (own_ws) {
-    const cudaError_t ea = cudaMallocAsync(&ws, need, a.stream);
-    if (ea != cudaSuccess) return fa::report_cuda_error(ea);
-  }
   a.q = q;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
@@ -400,8 +409,18 @@ int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* 
   a.window = window;
   a.sinks = sinks;
   a.c = c2;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  const fa::FwdPagedForm form = fa::fwd_paged_form(a);
+  const size_t need = form.cl == 0 ? fa::fwd_paged_workspace(T, H, Hkv, d, a.sms) : 0;
+  if (workspace && workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  void* ws = workspace;
+  const bool own_ws = ws == nullptr && need > 0;
+  if (own_ws) {
+    const cudaError_t ea = cudaMallocAsync(&ws, need, a.stream);
+    if (ea != cudaSuccess) return fa::report_cuda_error(ea);
+  }
   a.ws = static_cast<char*>(ws);
-  cudaError_t e = fa::launch_fwd_paged(a);
+  cudaError_t e = fa::launch_fwd_paged(a, form);
   if (own_ws) {
     const cudaError_t e2 = cudaFreeAsync(ws, a.stream);
     if (e == cudaSuccess) e = e2;

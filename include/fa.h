@@ -491,7 +491,8 @@ int fa_paged_slots(const int* ctx_lens, const int* new_lens, int* page_table, lo
  *   scale, lse as in fa_decode_paged; lse [T, H].
  *   workspace  device buffer of at least fa_fwd_paged_workspace_bytes(T, B, H, Hkv, d) bytes, 16-byte aligned, or
  *              NULL to allocate it stream-ordered on `stream`.  It needs no clearing; calls that may overlap on the
- *              GPU must not share one.
+ *              GPU must not share one.  A call that uses none (fa_fwd_paged_call_bytes) allocates none either, and
+ *              takes a buffer of any size.
  * A sequence with seq_lens[b] below its new tokens or above max_pages * page_size gets NaN in o and lse, one
  * with a page outside the cache NaN in the tokens that the page reaches (and others near them); offsets that do
  * not ascend make their sequence's tokens stay unwritten, and give tokens that others then share unspecified values
@@ -507,9 +508,13 @@ int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* 
                  const long long* cache_strides, float scale, int window, int sinks, void* workspace,
                  size_t workspace_bytes, float* lse, fa_stream_t stream);
 
-/* Bytes of workspace fa_fwd_paged needs on the current device; 0 when none is needed, on bad arguments or without an
- * sm_103 GPU. */
+/* Bytes of workspace that fa_fwd_paged needs on the current device at most, whatever its table and window are; 0 on bad
+ * arguments or without an sm_103 GPU. */
 size_t fa_fwd_paged_workspace_bytes(int T, int B, int H, int Hkv, int d);
+
+/* What a call with tables of max_pages pages and this window uses of its workspace: all of it, or nothing (0: small calls,
+ * whose units' states are joined on chip; 0 too on bad arguments or without an sm_103 GPU). */
+size_t fa_fwd_paged_call_bytes(int T, int B, int H, int Hkv, int d, int page_size, int max_pages, int window, int sinks);
 
 /*
  * fa_check_device_error -- reads and clears the library's device error word
