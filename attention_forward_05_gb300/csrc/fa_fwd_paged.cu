@@ -32,12 +32,12 @@
 // and 0 * inf would reach the others: the load warp sets such values aside (zeros in their place), and the epilogue
 // adds them to the rows that see them.
 //
-// What bounds it, measured (one pass among others): prompts the matrix products: 8191 tokens, 32 heads on 8 of 128, 358 us, 1535
-// TFLOP/s of the formula's products (the dense causal forward takes about the same).  At d = 64 the exponentials' latency, as in
-// the dense forward: 37 sequences of up to 512 tokens over up to 8192 keys, 32 heads on 4, 78 us, 700 TFLOP/s with start,
-// ends and masked tiles.  Few tokens over long contexts device memory: 24 sequences of 3 to 7 tokens, 1.41 GB, 220 us, 6.4 TB/s.
-// Small calls latency: 23 tokens behind 1000 keys 9.2 us (dealt 13.2: 3 for the plan, 3 to the first scores, 3 to
-// the states, 4 for the join).
+// What bounds it, measured (one pass among others): prompts the matrix products: 8191 tokens, 32 heads on 8 of 128, 355 us, 1546
+// TFLOP/s of the formula's products (the dense causal forward 348 us, 1580), in rows of its own under the power cap 375 to 385
+// (dense 363).  At d = 64 the exponentials' latency, as in the dense forward: 37 sequences of up to 512 tokens over up to 8192
+// keys, 32 heads on 4, 79 us, 700 TFLOP/s with start, ends and masked tiles.  Few tokens over long contexts device memory: 24
+// sequences of 3 to 7 tokens, 1.41 GB, 220 us, 6.4 TB/s.  Small calls latency: 23 tokens behind 1000 keys 9.2 us (dealt 13.2: 3
+// for the plan, 3 to the first scores, 3 to the states, 4 for the join).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -522,8 +522,8 @@ __global__ void __maxnreg__(C::MAXREG)
           }
         }
         const int before = scan<NT>(tiles, plan_tmp, &all_tiles);
-        // A unit's place in the order is the tiles before it and `extra` for each unit; where there are fewer tiles than CTAs
-        // each takes one, and starts and ends do not count.
+        // A unit's place in the order is the tiles before it and `extra` for each unit.  Up to two tiles a CTA are dealt evenly,
+        // one or two each, and starts and ends do not count.
         const int extra = static_cast<long long>(all_tiles) * p.Hkv <= 2 * static_cast<long long>(gridDim.x) ? 0 : cost_unit(D);
         long long* const place = plan_place;  // of each thread's first block in its head
         place[tid] = before + static_cast<long long>(extra) * x0;
@@ -1421,7 +1421,11 @@ int rows_of(const FwdPagedLaunch& a) {
 // d = 64 12.5 and 8.4; behind 4000 15.8 and 13.7, 16.2 and 11.1; behind 16000 20.9 and 25.5, 20.5 and 21.1; 16 x 4 tokens behind
 // 1000 21.1 and 15.8, 21.0 and 13.9; behind 1 to 2000 27.2 and 23.0, 21.9 and 19.8; behind 1 to 4000 39 and 46, 29 and 36; a
 // prompt of 500 17.8 and 12.0, 17.8 and 12.5.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 17.7 with 8 CTAs, 14.2
-// with 16.
+// with 16.  (A cluster of cl CTAs is taken only where there are 9 cl - 8 places for CTAs at least, and so at least cl, for 8 and
+// more, in one of the 8 processor clusters: it can be placed.)
+//
+// The host has bounds of the tiles and units only: tables much wider than the sequences, or places for many more tokens, are
+// taken for long sequences and many units, and their calls dealt (the first times of the pairs above instead of the second).
 //
 // More units than CTAs may run at once, if short, come in waves, of a CTA each, up to `halves` halves of what may run: 128 single
 // tokens behind 300 (3.5 waves) 59.6 and 48.1, 37.2 and 38.4; 256 behind 100 (7) 70.7 and 60.9, 40.5 and 49.8; 60 x 18 tokens
