@@ -591,9 +591,10 @@ def fa_paged_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_table: t
     Sequence b has ctx_lens[b] tokens in the cache and gets new_lens[b] more (both int32 [B]).  Its new pages come from the
     top of the stack free_pages (int32, its first free_count[0] entries are free) and go into its row of page_table (int32
     [B, max_pages], changed in place).  cu_seqlens [B + 1], positions [tokens], slots [tokens] (int64), seq_lens [B] and
-    free_left [1] are new tensors or the given ones; seq_lens may be ctx_lens and free_left free_count, so that a captured
-    step counts on by itself.  Places behind the last token get slot -1; a sequence that does not fit gets -1 as its length
-    and slots, and makes fa_check_device_error return FA_ERR_INVALID_ARG.
+    free_left [1] are the given tensors, or new ones: views of one allocation, so give those that are to be resized or kept
+    longer than the others.  seq_lens may be ctx_lens and free_left free_count, so that a captured step counts on by itself.
+    Places behind the last token get slot -1; a sequence that does not fit gets -1 as its length and slots, and makes
+    fa_check_device_error return FA_ERR_INVALID_ARG.
     """
     if stream is not None:
         with _on_stream(stream, ctx_lens, new_lens, page_table, free_pages, free_count, cu_seqlens, positions, slots,
@@ -623,9 +624,10 @@ def fa_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     """Causal attention of a ragged batch's new tokens over a paged cache that holds their keys and values already;
     returns (o [T, H, d], lse [T, H] or None).
 
-    q: bf16 [T, H, d], may be a strided view; sequence b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1])
-    and the last of its seq_lens[b] (int32 [B]) keys.  window > 0: a token sees the last `window` keys up to its own and the
-    first `sinks` keys.  page_table as in fa_decode_paged.  Rows behind cu_seqlens[B] stay unwritten.
+    q: bf16 [T, H, d], may be a strided view whose heads lie within a token; sequence b's tokens are cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 (int32 [B + 1]) and the last of its seq_lens[b] (int32 [B]) keys.  window > 0: a token sees the
+    last `window` keys up to its own and the first `sinks` keys.  page_table as in fa_decode_paged.  Rows behind
+    cu_seqlens[B] stay unwritten.
     """
     if stream is not None:
         with _on_stream(stream, q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, workspace, o, lse):

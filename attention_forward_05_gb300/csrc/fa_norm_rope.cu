@@ -17,7 +17,8 @@
 // Bound by device memory: 336 MB forward (2 x 8192 tokens, 32 + 8 heads of 128, bf16) 57 us, 5.9 TB/s with the launch, where
 // the rotation alone takes 53 on as many bytes; 503 MB backward 86 us, 5.9 TB/s.  With all heads of an item in registers at a
 // time (they spill) 78 and 138 us; with query and key heads on blocks of their own 63.5 and 94; forward with 4 and 2 blocks a
-// SM 62.5 and 64, with items of twice as many heads 65.  Small calls are bound by the launch (333 tokens of 20 heads of 64,
+// SM 62.5 and 64, with items of twice as many heads 65.  The same in fp32 118 us, 5.7 TB/s, and 172 backward, 5.8.  Appended, 8191
+// tokens of 32 + 2 x 8 heads of 128 (201 MB): 40 us, 5.0 TB/s.  Small calls are bound by the launch (333 tokens of 20 heads of 64,
 // fp32: 3.3 us in a graph; 3.9 with each lane reading its weights from device memory behind the wait for the rotation's table).
 #include "fa_rope_items.cuh"
 

@@ -18,7 +18,7 @@ namespace fa {
 namespace {
 
 constexpr int THREADS = 1024;
-constexpr int MAX_CTAS = 16;  // of the cluster (above 8 it has to be asked for)
+constexpr int MAX_CTAS = 16;  // of the cluster (above 8 it has to be asked for); one of the 8 processor clusters has 19 SMs at least
 enum : int { W_STEP = 0x40 };  // site recorded with DEV_BAD_INDEX
 
 // Exclusive prefix sums of the threads' values, and the total; `tmp` is shared, [THREADS / 32 + 1].

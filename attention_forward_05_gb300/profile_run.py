@@ -12,17 +12,21 @@ and a device-error check.  --B / --H override the workload's batch and heads
 decode workload as grouped-query decode (fa_decode_splitkv_gqa) with N key/value
 heads shared by its query heads.
 
---op runs a position or paged-cache operator instead of a workload, on inputs larger than L2:
+--op runs a position or paged-cache operator instead of a workload, on inputs larger than L2 where nothing else is said:
   rope                 q and k of 4 x 4096 tokens, 16 + 16 heads of 64, bf16, read out of a projection's layout
   append               8191 tokens, 32 query and 8 key/value heads of 128, into pages of 64 rows
   decode_paged         32 sequences of 8192 keys, 32 query heads on 4 key/value heads of 128, pages of 16 rows
   decode_paged_prefix  the same heads: 16384 shared keys in pages of 64 rows, 256 sequences of 64 own keys
   norm_rope            norms and rotation of q and k of 2 x 8192 tokens, 32 + 8 heads of 128, bf16
   norm_rope_bwd        its gradients, the norms' weights' too
+  norm_rope_fp32, norm_rope_bwd_fp32   the same in fp32
+  append_norm          `append` with norms of the heads, into pages of 16 rows
   slots                page tables, positions and slots of 64 prompts of 1000 tokens behind 500
   fwd_paged            a prompt of 8191 tokens, 32 query heads on 8 key/value heads of 128, pages of 64 rows
   fwd_paged_d64        8 chunks of 512 tokens behind 4096 keys, 32 query heads on 4 of 64, pages of 16 rows
   fwd_paged_window     48 single tokens behind 8192 keys, window of 4096 and 4 sinks, 32 heads on 8 of 128, pages of 16
+  fwd_paged_question   23 tokens behind 1000 keys, 32 heads on 8 of 128, pages of 16: a cluster of CTAs a unit (inputs in L2)
+  fwd_paged_singles    128 single tokens behind 300 keys, the same heads: a CTA a unit, in waves
 """
 from __future__ import annotations
 
@@ -38,7 +42,8 @@ from attention_forward_05_gb300.inputs import WORKLOADS, make_dout, make_qkv, me
 
 
 OPS = ("rope", "append", "decode_paged", "decode_paged_prefix", "norm_rope", "norm_rope_bwd", "slots", "fwd_paged",
-       "fwd_paged_d64", "fwd_paged_window")
+       "fwd_paged_d64", "fwd_paged_window", "norm_rope_fp32", "norm_rope_bwd_fp32", "append_norm", "fwd_paged_question",
+       "fwd_paged_singles")
 
 
 def operator(name: str, dev):
@@ -46,33 +51,36 @@ def operator(name: str, dev):
     gen = torch.Generator(device=dev)
     gen.manual_seed(1900 + OPS.index(name))
 
+    dtype = torch.float32 if name.endswith("_fp32") else torch.bfloat16
+
     def draw(*shape):
-        return torch.randn(shape, generator=gen, device=dev).to(torch.bfloat16)
+        return torch.randn(shape, generator=gen, device=dev).to(dtype)
 
     if name == "rope":
         B, N, H, d = 4, 4096, 16, 64
         q, k = draw(B, N, H, d).transpose(1, 2), draw(B, N, H, d).transpose(1, 2)
         pos, freqs = torch.arange(N, dtype=torch.int32, device=dev), fa.fa_rope_freqs(d, device=dev)
         return (lambda: fa.fa_rope(q, k, pos, freqs)), 2 * 2 * q.numel() * 2, 6 * q.numel()
-    if name == "append":
-        T, H, Hkv, d, ps = 8191, 32, 8, 128, 64
+    if name in ("append", "append_norm"):
+        T, H, Hkv, d, ps = 8191, 32, 8, 128, 64 if name == "append" else 16
         x = draw(T, H + 2 * Hkv, d)
         pages = -(-T // ps)
         kc, vc = draw(pages, Hkv, ps, d), draw(pages, Hkv, ps, d)
         at = torch.arange(T, device=dev)
         slots = torch.randperm(pages, generator=gen, device=dev)[at // ps] * ps + at % ps
         pos, freqs = at.to(torch.int32), fa.fa_rope_freqs(d, device=dev)
+        norms = {} if name == "append" else {"q_weight": draw(d), "k_weight": draw(d)}
         return (lambda: fa.fa_paged_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, slots, q=x[:, :H], positions=pos,
-                                           freqs=freqs)), 4 * x.numel(), 3 * T * (H + Hkv) * d
+                                           freqs=freqs, **norms)), 4 * x.numel(), (8 if norms else 3) * T * (H + Hkv) * d
     if name.startswith("norm_rope"):
         B, N, H, Hkv, d = 2, 8192, 32, 8, 128
         q, k = draw(B, N, H, d).transpose(1, 2), draw(B, N, Hkv, d).transpose(1, 2)
         wq, wk, pos, freqs = draw(d), draw(d), torch.arange(N, dtype=torch.int32, device=dev), fa.fa_rope_freqs(d, device=dev)
-        n = q.numel() + k.numel()
-        if name == "norm_rope":
-            return (lambda: fa.fa_norm_rope(q, k, wq, wk, pos, freqs)), 4 * n, 8 * n
+        n, e = q.numel() + k.numel(), q.element_size()
+        if "bwd" not in name:
+            return (lambda: fa.fa_norm_rope(q, k, wq, wk, pos, freqs)), 2 * e * n, 8 * n
         dq, dk = draw(B, H, N, d), draw(B, Hkv, N, d)
-        return (lambda: fa.fa_norm_rope_bwd(dq, dk, q, k, wq, wk, pos, freqs)), 6 * n, 16 * n
+        return (lambda: fa.fa_norm_rope_bwd(dq, dk, q, k, wq, wk, pos, freqs)), 3 * e * n, 16 * n
     if name == "slots":
         B, n, ctx, ps = 64, 1000, 500, 16
         pages = -(-(ctx + n) // ps)
@@ -84,7 +92,9 @@ def operator(name: str, dev):
     if name.startswith("fwd_paged"):
         B, n, ctx, H, Hkv, d, ps, window, sinks = {"fwd_paged": (1, 8191, 0, 32, 8, 128, 64, 0, 0),
                                                    "fwd_paged_d64": (8, 512, 4096, 32, 4, 64, 16, 0, 0),
-                                                   "fwd_paged_window": (48, 1, 8191, 32, 8, 128, 16, 4096, 4)}[name]
+                                                   "fwd_paged_window": (48, 1, 8191, 32, 8, 128, 16, 4096, 4),
+                                                   "fwd_paged_question": (1, 23, 1000, 32, 8, 128, 16, 0, 0),
+                                                   "fwd_paged_singles": (128, 1, 300, 32, 8, 128, 16, 0, 0)}[name]
         width = -(-(ctx + n) // ps)
         kc, vc = draw(B * width, Hkv, ps, d), draw(B * width, Hkv, ps, d)
         table = torch.randperm(B * width, generator=gen, device=dev).to(torch.int32).view(B, width)
