@@ -1421,8 +1421,8 @@ int rows_of(const FwdPagedLaunch& a) {
 // d = 64 12.5 and 8.4; behind 4000 15.8 and 13.7, 16.2 and 11.1; behind 16000 20.9 and 25.5, 20.5 and 21.1; 16 x 4 tokens behind
 // 1000 21.1 and 15.8, 21.0 and 13.9; behind 1 to 2000 27.2 and 23.0, 21.9 and 19.8; behind 1 to 4000 39 and 46, 29 and 36; a
 // prompt of 500 17.8 and 12.0, 17.8 and 12.5.  Clusters of more than 8: 23 tokens behind 8000, d = 64, 17.7 with 8 CTAs, 14.2
-// with 16.  (A cluster of cl CTAs is taken only where there are 9 cl - 8 places for CTAs at least, and so at least cl, for 8 and
-// more, in one of the 8 processor clusters: it can be placed.)
+// with 16.  (A cluster of cl CTAs is taken only where there are 9 cl - 8 places for CTAs at least, and so at least cl in one of the
+// 8 processor clusters: it can be placed.)
 //
 // The host has bounds of the tiles and units only: tables much wider than the sequences, or places for many more tokens, are
 // taken for long sequences and many units, and their calls dealt (the first times of the pairs above instead of the second).
